@@ -57,6 +57,11 @@ typedef int32_t moe_status;
                                           T*k (a scratch shared by overlapping calls) and
                                           a row could not be placed (its write was
                                           skipped) */
+#define MOE_DEVERR_BAD_SLOT        32  /* a cache slot was neither -1 nor inside the cache */
+#define MOE_DEVERR_BAD_PAGE        64  /* a page of a context was outside the cache (its
+                                          tokens were left out) */
+#define MOE_DEVERR_BAD_LENGTH     128  /* a context length was negative or above max_len
+                                          (taken as 0 or max_len) */
 
 /* One 4-bit groupwise-affine matrix [R][K] ([A] §5-1; [C] glossary):
  *   qw    uint32 [R][K/8]   8 codes per word, code c of a row in word c/8 at bits 4*(c%8)
@@ -278,6 +283,133 @@ moe_status moe_residual_rms(const uint16_t* y, const uint16_t* x, uint16_t* out,
  * with the first megabytes of layer l+1's packed weights: the gate/up weights
  * of the experts that layer's first units read. ptr and bytes 16-byte aligned. */
 moe_status moe_l2_prefetch(const void* ptr, size_t bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention side of a decoder layer: rotary positions, a paged key/value cache
+ * in the weights' number format, and attention over it.
+ * ------------------------------------------------------------------------ */
+
+#define MOE_BF16 0
+#define MOE_F16  1
+#define MOE_F32  2
+
+/* Rotary positions. The first `rot` elements of a head form rot/2 pairs
+ * (a_i, b_i): elements (i, i + rot/2), or (2i, 2i + 1) when interleaved. At
+ * position p pair i is turned by angle 2 pi frac(p * phase[i] / 2^64):
+ *   a' = mscale * (a cos - b sin),  b' = mscale * (b cos + a sin).
+ * phase[i] is the turn per position as a 64-bit binary fraction, so the product
+ * wraps at whole turns and the angle keeps its precision at any int32 position.
+ * Elements from `rot` on pass through unscaled. */
+typedef struct moe_rope_spec {
+  const uint64_t* phase;   /* device, [rot/2]; fill it from moe_rope_phases */
+  int32_t rot;             /* even, 2 <= rot <= head size */
+  int32_t interleaved;     /* 0 or 1 */
+  float   mscale;          /* factor of the turned elements (1 unless scaled for long contexts) */
+} moe_rope_spec;
+
+/* How the frequencies base^(-2i/rot) are changed for contexts beyond the
+ * trained length. */
+#define MOE_ROPE_PLAIN  0  /* as they are */
+#define MOE_ROPE_LINEAR 1  /* all divided by `factor` (positions interpolated) */
+#define MOE_ROPE_BASE   2  /* base * factor^(rot/(rot-2)): the lowest frequency divided by `factor` */
+#define MOE_ROPE_BANDS  3  /* pairs with at least `fast` turns over `trained` positions stay, those
+                              with at most `slow` turns are divided by `factor`, linear in the
+                              pair index between (Peng et al., "YaRN: Efficient Context Window
+                              Extension of Large Language Models", 2023, section 3.2) */
+
+/* Host function: fills phase[rot/2] (host memory). base > 1, factor >= 1; trained
+ * > 0 and fast > slow > 0 for MOE_ROPE_BANDS (ignored otherwise). */
+moe_status moe_rope_phases(uint64_t* phase, int32_t rot, double base, int32_t scaling,
+                           double factor, double trained, double fast, double slow);
+
+/* out[t][h] = x[t][h] turned to position pos[t]; backward = 1: the transposed
+ * rotation, which takes the gradient of out to that of x.
+ *   x, out  device, `dtype` MOE_BF16, MOE_F16 or MOE_F32, T tokens of H heads of D
+ *           elements (D even); token t, head h starts at element t*row + h*head.
+ *           Strides in elements; out's rows may not overlap. out == x with the same
+ *           strides is allowed.
+ *   pos     int32 [T] device (any value)
+ * Angles, sines and products in fp32, one rounding to dtype. 16-byte aligned
+ * pointers and strides take the vector path, anything else a scalar one. */
+moe_status moe_rope(const void* x, int64_t x_row, int64_t x_head, void* out, int64_t out_row,
+                    int64_t out_head, const int32_t* pos, int32_t T, int32_t H, int32_t D,
+                    const moe_rope_spec* rope, int32_t backward, int32_t dtype, void* stream);
+
+/* A paged cache of keys and values in groupwise-affine codes: each run of 64
+ * elements of a head shares one bf16 scale and bias, value = scale * code + bias.
+ * Slot s is token s % page_size of page s / page_size. A page holds, for the Hkv
+ * key heads and then the Hkv value heads, one block each:
+ *   codes  [page_size][D * bits / 8] bytes; 4-bit: element 2i of a row in the low
+ *          nibble of byte i
+ *   words  [page_size][D / 64] uint32, scale | bias << 16
+ * bits 4 or 8, D 64, 128 or 256, page_size a multiple of 16 up to 4096,
+ * pages * page_size < 2^31. Offsets into the cache are 64-bit. */
+typedef struct moe_kv_cache {
+  void*    data;           /* device, moe_kv_cache_size() bytes, 16-byte aligned */
+  int32_t* err;            /* device error word (MOE_DEVERR_* bits are OR-ed into it) */
+  int32_t  pages, page_size, Hkv, D, bits;
+} moe_kv_cache;
+
+/* Bytes of a cache; 0 if the sizes are not allowed. */
+size_t moe_kv_cache_size(int32_t pages, int32_t page_size, int32_t Hkv, int32_t D, int32_t bits);
+
+/* New tokens: bf16 queries, keys and values as they leave the projections
+ * (token t, head h at element t*row + h*head; 16-byte aligned pointers, strides
+ * multiples of 8). */
+typedef struct moe_kv_new {
+  const uint16_t* k;  int64_t k_row, k_head;          /* [T][Hkv][D] */
+  const uint16_t* v;  int64_t v_row, v_head;          /* [T][Hkv][D] */
+  const uint16_t* q;  int64_t q_row, q_head;          /* [T][Hq][D], or NULL: no queries */
+  uint16_t* q_out;    int64_t qo_row, qo_head;        /* turned queries; may be q */
+  const int32_t* slots;                               /* [T] distinct slots, -1: skip the token's row */
+  const int32_t* pos;                                 /* [T]; NULL without rope */
+  const moe_rope_spec* rope;                          /* NULL: keys are kept as given, q must be NULL */
+  int32_t T, Hq;
+} moe_kv_new;
+
+/* Turns queries and keys to their positions, quantises keys and values and
+ * writes them into the cache, in one launch. Turned queries and keys are rounded
+ * to bf16; per group of 64: bias = min, scale = bf16((max - min) / (2^bits - 1)),
+ * code = round((x - bias) / scale), ties to even, 0 when the group is constant.
+ * A group that holds a NaN or an infinity reads back as NaN. Slots outside the
+ * cache are skipped and set MOE_DEVERR_BAD_SLOT. T = 0 launches nothing. */
+moe_status moe_kv_append(const moe_kv_new* a, const moe_kv_cache* c, void* stream);
+
+/* Cache rows back as bf16(scale * code + bias): k_out, v_out [n][Hkv][D] dense,
+ * 16-byte aligned, either may be NULL. A slot of -1 gives a row of zeros; one
+ * outside the cache too, and sets MOE_DEVERR_BAD_SLOT. */
+moe_status moe_kv_read(const moe_kv_cache* c, const int32_t* slots, int32_t n, uint16_t* k_out,
+                       uint16_t* v_out, void* stream);
+
+/* Attention of B requests with nq query tokens each over their cached contexts.
+ * Request b attends first to the prefix that all requests share (prefix_len
+ * tokens in the pages of prefix_table; read and multiplied once for the whole
+ * batch), then to its own lens[b] tokens in the pages table[b][...], of which the
+ * last nq are its query tokens: query i sees own tokens 0 .. lens[b] - nq + i.
+ *   o = sum_t softmax_t(scale * q . k_t) v_t,  0 where nothing is seen.
+ * Query head h reads key/value head h / (Hq / Hkv). Memory of slots that are not
+ * seen is never used in arithmetic, whatever it holds. */
+typedef struct moe_kv_attn {
+  const uint16_t* q;  int64_t q_row, q_head;          /* bf16 [B*nq][Hq][D], row b*nq + i */
+  uint16_t* out;      int64_t out_row, out_head;      /* bf16 [B*nq][Hq][D]; rows may not overlap */
+  const int32_t* table;                               /* [B][table_stride] page numbers */
+  const int32_t* lens;                                /* [B] */
+  const int32_t* prefix_table;                        /* [ceil(prefix_len / page_size)], or NULL */
+  int32_t B, nq, Hq, table_stride;
+  int32_t max_len;                                    /* no lens[b] is above it */
+  int32_t prefix_len;
+  float scale;
+} moe_kv_attn;
+
+/* Bytes of scratch for moe_kv_attention (partial results of split contexts). It
+ * needs no zero-filling; calls that overlap on the GPU must not share it. */
+size_t moe_kv_attention_workspace_size(int32_t B, int32_t nq, int32_t Hq, int32_t Hkv, int32_t D,
+                                       int32_t max_len, int32_t prefix_len);
+
+/* B = 0 launches nothing. Page numbers are read only as far as lens and
+ * prefix_len reach. q and out: 16-byte aligned, strides multiples of 8. */
+moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache* c, void* ws,
+                            size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, copies the device error word `err` to *code and
  * returns MOE_ERR_DEVICE if it is non-zero, MOE_OK otherwise. */

@@ -1,0 +1,579 @@
+// kv.cu — rotary positions and the quantised key/value cache: moe_rope,
+// moe_kv_append (turn, quantise, write) and moe_kv_read (read back).
+//
+// All three move each byte once and do little arithmetic per byte, so they are
+// bound by memory bandwidth at many tokens and by launch latency at few. One
+// launch each, no shared memory, no scratch.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "kv.cuh"
+#include "ptx.cuh"
+
+namespace moeq4 {
+
+moe_status check_kv_cache(const moe_kv_cache* c) {
+  if (!c || !c->data || !c->err) return MOE_ERR_ARG;
+  if (moe_kv_cache_size(c->pages, c->page_size, c->Hkv, c->D, c->bits) == 0) return MOE_ERR_SHAPE;
+  if ((reinterpret_cast<uintptr_t>(c->data) & 15u) || (reinterpret_cast<uintptr_t>(c->err) & 3u))
+    return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+KvCache kv_cache_args(const moe_kv_cache& c) {
+  KvCache k{};
+  k.data = static_cast<uint8_t*>(c.data);
+  k.err = c.err;
+  k.pages = c.pages;
+  k.page_size = c.page_size;
+  k.Hkv = c.Hkv;
+  k.D = c.D;
+  k.bits = c.bits;
+  k.row_bytes = c.D * c.bits / 8;
+  k.code_bytes = c.page_size * k.row_bytes;
+  k.head_bytes = k.code_bytes + c.page_size * (c.D / kKvGroup) * 4;
+  k.page_bytes = 2ll * c.Hkv * k.head_bytes;
+  return k;
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+
+bool bad_align(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// Rows of n heads of D elements may not overlap, in either order of the strides.
+bool rows_disjoint(int64_t row, int64_t head, int64_t T, int64_t H, int64_t D) {
+  if (row < 0 || head < 0) return false;
+  const bool head_in = (H == 1 || head >= D) && (T == 1 || row >= (H - 1) * head + D);
+  const bool row_in = (T == 1 || row >= D) && (H == 1 || head >= (T - 1) * row + D);
+  return head_in || row_in;
+}
+
+// ------------------------------------------------------------------- rotary
+
+struct RopeArgs {
+  const void* x;
+  void* out;
+  const int32_t* pos;
+  const uint64_t* phase;
+  int64_t x_row, x_head, o_row, o_head;
+  int T, H, D, rot;
+  int units;                 // units of 2V elements per head: rot / 2V turned, the rest copied
+  int head_blocks;           // heads per thread: ceil(H / head_blocks)
+  float mscale;
+  int interleaved, backward, copy_tail;
+};
+
+template <typename E>
+__device__ __forceinline__ float to_f(E v);
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <typename E>
+__device__ __forceinline__ E from_f(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ float from_f(float v) { return v; }
+
+template <typename E, int V>
+struct alignas(V * sizeof(E) > 16 ? 16 : V * sizeof(E)) Vec {
+  E e[V];
+};
+
+// Thread = (token, block of heads, unit of V pairs): the V angles are computed
+// once and used for every head of the block.
+template <typename E, int V>
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int u = static_cast<int>(id % a.units);
+  const int64_t th = id / a.units;
+  const int hb = static_cast<int>(th % a.head_blocks);
+  const int64_t t = th / a.head_blocks;
+  if (t >= a.T) return;
+  const int per = (a.H + a.head_blocks - 1) / a.head_blocks;
+  const int h0 = hb * per, h1 = min(a.H, h0 + per);
+  const int turned = a.rot / (2 * V);
+  const bool tail = u >= turned;
+  if (tail && !a.copy_tail) return;
+  int first, second;                       // start of the unit's two runs of V elements
+  if (tail) {
+    first = a.rot + (u - turned) * 2 * V;
+    second = first + V;
+  } else if (a.interleaved) {
+    first = u * 2 * V;
+    second = first + V;
+  } else {
+    first = u * V;
+    second = first + a.rot / 2;
+  }
+  const E* x = static_cast<const E*>(a.x) + t * a.x_row;
+  E* o = static_cast<E*>(a.out) + t * a.o_row;
+  using Vt = Vec<E, V>;
+  if (tail) {
+    for (int h = h0; h < h1; ++h) {
+      const Vt p = *reinterpret_cast<const Vt*>(x + h * a.x_head + first);
+      const Vt q = *reinterpret_cast<const Vt*>(x + h * a.x_head + second);
+      *reinterpret_cast<Vt*>(o + h * a.o_head + first) = p;
+      *reinterpret_cast<Vt*>(o + h * a.o_head + second) = q;
+    }
+    return;
+  }
+  float c[V], s[V];
+  const int32_t pos = a.pos[t];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    rope_sincos(pos, a.phase[u * V + i], c[i], s[i]);
+    c[i] *= a.mscale;
+    s[i] *= a.backward ? -a.mscale : a.mscale;
+  }
+  for (int h = h0; h < h1; ++h) {
+    Vt p = *reinterpret_cast<const Vt*>(x + h * a.x_head + first);
+    Vt q = *reinterpret_cast<const Vt*>(x + h * a.x_head + second);
+    if (a.interleaved) {
+      E* e[2] = {p.e, q.e};
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        E& ea = V == 1 ? p.e[0] : e[2 * i / V][2 * i % V];
+        E& eb = V == 1 ? q.e[0] : e[(2 * i + 1) / V][(2 * i + 1) % V];
+        const float fa = to_f(ea), fb = to_f(eb);
+        ea = from_f<E>(rope_first(fa, fb, c[i], s[i]));
+        eb = from_f<E>(rope_second(fa, fb, c[i], s[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float fa = to_f(p.e[i]), fb = to_f(q.e[i]);
+        p.e[i] = from_f<E>(rope_first(fa, fb, c[i], s[i]));
+        q.e[i] = from_f<E>(rope_second(fa, fb, c[i], s[i]));
+      }
+    }
+    *reinterpret_cast<Vt*>(o + h * a.o_head + first) = p;
+    *reinterpret_cast<Vt*>(o + h * a.o_head + second) = q;
+  }
+}
+
+template <typename E, int V>
+cudaError_t launch_rope_v(RopeArgs a, cudaStream_t s) {
+  a.units = a.D / (2 * V);
+  // few tokens: one head per thread (latency); many: up to 8 heads share their angles
+  int per = 1;
+  while (per < 8 && static_cast<int64_t>(a.T) * a.units * a.H / (2 * per) >= 152 * 1024) per *= 2;
+  a.head_blocks = (a.H + per - 1) / per;
+  const int64_t n = static_cast<int64_t>(a.T) * a.units * a.head_blocks;
+  const int64_t blocks = (n + kThreads - 1) / kThreads;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  rope_kernel<E, V><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename E>
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
+  const uint64_t all = static_cast<uint64_t>(a.x_row | a.x_head | a.o_row | a.o_head);
+  const uint64_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out);
+  const int half = a.interleaved ? 0 : a.rot / 2;
+  const auto fits = [&](unsigned v) {
+    const unsigned bytes = std::min<unsigned>(16, v * sizeof(E));
+    return a.rot % (2 * v) == 0 && a.D % (2 * v) == 0 && half % v == 0 && all % v == 0 &&
+           p % bytes == 0;
+  };
+  if (fits(8)) return launch_rope_v<E, 8>(a, s);
+  if (fits(4)) return launch_rope_v<E, 4>(a, s);
+  return launch_rope_v<E, 1>(a, s);
+}
+
+// ------------------------------------------------------------------- append
+
+struct AppendArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* q_out;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head, qo_row, qo_head;
+  const int32_t *slots, *pos;
+  const uint64_t* phase;     // nullptr: no rotation
+  int T, Hq, rot, interleaved;
+  float mscale;
+  KvCache c;
+};
+
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(r[i]);
+    v[2 * i + 1] = bf16_hi(r[i]);
+  }
+}
+
+__device__ __forceinline__ float ld_bf16(const uint16_t* p) {
+  return __uint_as_float(static_cast<uint32_t>(*p) << 16);
+}
+
+// Elements e0 .. e0+7 of one head turned to their position, rounded to bf16.
+__device__ __forceinline__ void turned8(const AppendArgs& a, const uint16_t* head, int e0,
+                                        int32_t pos, float (&v)[8]) {
+  load8(head + e0, v);
+  if (!a.phase) return;
+  const int half = a.rot / 2;
+  if (a.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      if (e0 + i < a.rot) {
+        float c, s;
+        rope_sincos(pos, a.phase[(e0 + i) / 2], c, s);
+        c *= a.mscale;
+        s *= a.mscale;
+        const float x = v[i], y = v[i + 1];
+        v[i] = rope_first(x, y, c, s);
+        v[i + 1] = rope_second(x, y, c, s);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = e0 + i;
+      if (e < a.rot) {
+        const bool lower = e < half;
+        const int pair = lower ? e : e - half;
+        float c, s;
+        rope_sincos(pos, a.phase[pair], c, s);
+        c *= a.mscale;
+        s *= a.mscale;
+        const float other = ld_bf16(head + (lower ? e + half : pair));
+        v[i] = lower ? rope_first(v[i], other, c, s) : rope_second(other, v[i], c, s);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t w = pack_bf16(v[i], v[i + 1]);
+    v[i] = bf16_lo(w);
+    v[i + 1] = bf16_hi(w);
+  }
+}
+
+// Thread = (token, head, run of 8 elements); heads are the query heads, the key
+// heads, then the value heads. The 8 lanes of a group find its range by shuffles.
+// (q_out may be q only if no thread reads what another wrote: a turned run reads
+// its partner run of the same head, so in place the whole head must be read
+// before any of it is written: the D/8 <= 32 threads of a head are lanes of one
+// warp, and __syncwarp separates the two.)
+template <int BITS>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+  const int runs = a.c.D / 8;
+  const int heads = a.Hq + 2 * a.c.Hkv;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int run = static_cast<int>(id % runs);
+  const int64_t th = id / runs;
+  const int h = static_cast<int>(th % heads);
+  const int64_t t = th / heads;
+  const bool live = t < a.T;               // whole groups of 8 lanes: D / 8 is a multiple of 8
+  const int e0 = run * 8;
+  float v[8] = {};
+  if (live) {
+    const int32_t pos = a.phase ? a.pos[t] : 0;
+    if (h < a.Hq)
+      turned8(a, a.q + t * a.q_row + h * a.q_head, e0, pos, v);
+    else if (h < a.Hq + a.c.Hkv)
+      turned8(a, a.k + t * a.k_row + (h - a.Hq) * a.k_head, e0, pos, v);
+    else
+      load8(a.v + t * a.v_row + (h - a.Hq - a.c.Hkv) * a.v_head + e0, v);
+  }
+  __syncwarp();
+  if (live && h < a.Hq)
+    *reinterpret_cast<uint4*>(a.q_out + t * a.qo_row + h * a.qo_head + e0) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                   pack_bf16(v[6], v[7]));
+  float lo = v[0], hi = v[0];
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo = fminf(lo, v[i]);
+    hi = fmaxf(hi, v[i]);
+    finite &= fabsf(v[i]) < INFINITY;
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+  }
+  finite = ((__ballot_sync(0xFFFFFFFFu, finite) >> (threadIdx.x & 24u)) & 0xFFu) == 0xFFu;
+  if (!live || h < a.Hq) return;
+  const int slot = a.slots[t];
+  if (slot < 0 || slot >= a.c.pages * a.c.page_size) {
+    if (slot != -1 && run == 0 && h == a.Hq) atomicOr(a.c.err, MOE_DEVERR_BAD_SLOT);
+    return;
+  }
+  constexpr float kLevels = (1 << BITS) - 1;
+  uint32_t words = 0x7FC00000u;            // scale 0, bias NaN
+  uint32_t code[8] = {};
+  if (finite) {
+    // halves: max - min may pass the largest float; the constant is one rounding of 2 / levels
+    const float range = __fsub_rn(0.5f * hi, 0.5f * lo);
+    const uint32_t sw = pack_bf16(__fmul_rn(range, 1.0f / (0.5f * kLevels)), lo);
+    const float scale = bf16_lo(sw);
+    const float per = scale > 0.f ? __fdiv_rn(1.0f, scale) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      code[i] = static_cast<uint32_t>(
+          fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(v[i], lo), per)), 0.f), kLevels));
+    words = sw;
+  }
+  const int page = slot / a.c.page_size, row = slot % a.c.page_size;
+  uint8_t* blk = kv_block(a.c, page, h - a.Hq);
+  uint8_t* dst = blk + row * a.c.row_bytes + run * BITS;
+  if (BITS == 8)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
+                   code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = code[0] | code[1] << 4 | code[2] << 8 | code[3] << 12 |
+                                        code[4] << 16 | code[5] << 20 | code[6] << 24 |
+                                        code[7] << 28;
+  if ((run & 7) == 0)
+    *reinterpret_cast<uint32_t*>(blk + a.c.code_bytes +
+                                 (row * (a.c.D / kKvGroup) + run / 8) * 4) = words;
+}
+
+// --------------------------------------------------------------------- read
+
+// Thread = (row, key or value head, run of 16 codes) -> 32 bytes of bf16.
+template <int BITS>
+__global__ void __launch_bounds__(kThreads) read_kernel(KvCache c, const int32_t* slots, int n,
+                                                        uint16_t* k_out, uint16_t* v_out) {
+  const int runs = c.D / 16;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int run = static_cast<int>(id % runs);
+  const int64_t th = id / runs;
+  const int h = static_cast<int>(th % (2 * c.Hkv));
+  const int64_t t = th / (2 * c.Hkv);
+  if (t >= n) return;
+  uint16_t* out = h < c.Hkv ? k_out : v_out;
+  if (!out) return;
+  out += (t * c.Hkv + h % c.Hkv) * c.D + run * 16;
+  const int slot = slots[t];
+  uint32_t r[8] = {};
+  if (slot >= 0 && slot < c.pages * c.page_size) {
+    const int page = slot / c.page_size, row = slot % c.page_size;
+    const uint8_t* blk = kv_block(c, page, h);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(
+        blk + c.code_bytes + (row * (c.D / kKvGroup) + run / 4) * 4);
+    const float scale = bf16_lo(w), bias = bf16_hi(w);
+    const uint8_t* src = blk + row * c.row_bytes + run * 2 * BITS;
+    uint32_t q[4];
+    if (BITS == 8) {
+      const uint4 x = *reinterpret_cast<const uint4*>(src);
+      q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(src);
+      q[0] = x.x, q[1] = x.y;
+    }
+    constexpr int kPer = 32 / BITS;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t two = q[2 * i / kPer] >> (2 * i % kPer * BITS);
+      constexpr uint32_t kMask = (1u << BITS) - 1;
+      r[i] = pack_bf16(fmaf(scale, static_cast<float>(two & kMask), bias),
+                       fmaf(scale, static_cast<float>((two >> BITS) & kMask), bias));
+    }
+  } else if (slot != -1 && run == 0 && h % c.Hkv == 0) {
+    atomicOr(c.err, MOE_DEVERR_BAD_SLOT);
+  }
+  reinterpret_cast<uint4*>(out)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+  reinterpret_cast<uint4*>(out)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+moe_status check_rope(const moe_rope_spec* r, int D) {
+  if (!r || !r->phase) return MOE_ERR_ARG;
+  if (r->interleaved < 0 || r->interleaved > 1 || !std::isfinite(r->mscale)) return MOE_ERR_ARG;
+  if (r->rot < 2 || r->rot % 2 || r->rot > D) return MOE_ERR_SHAPE;
+  if (bad_align(r->phase, 8)) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+// Strided bf16 rows that the vector path reads 16 bytes at a time.
+moe_status check_rows(const void* p, int64_t row, int64_t head) {
+  if (!p) return MOE_ERR_ARG;
+  if (row < 0 || head < 0) return MOE_ERR_SHAPE;
+  if (bad_align(p, 16) || row % 8 || head % 8) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moeq4
+
+extern "C" size_t moe_kv_cache_size(int32_t pages, int32_t page_size, int32_t Hkv, int32_t D,
+                                    int32_t bits) {
+  if (pages < 1 || page_size < 16 || page_size % 16 || page_size > 4096 || Hkv < 1 ||
+      Hkv > 1024 || (D != 64 && D != 128 && D != 256) || (bits != 4 && bits != 8) ||
+      static_cast<int64_t>(pages) * page_size > 0x7FFFFFFF)
+    return 0;
+  return static_cast<size_t>(pages) * 2 * Hkv * page_size * (D * bits / 8 + D / moeq4::kKvGroup * 4);
+}
+
+extern "C" moe_status moe_rope_phases(uint64_t* phase, int32_t rot, double base, int32_t scaling,
+                                      double factor, double trained, double fast, double slow) {
+  if (!phase || !(base > 1.0) || !std::isfinite(base) || !(factor >= 1.0) ||
+      !std::isfinite(factor) || scaling < MOE_ROPE_PLAIN || scaling > MOE_ROPE_BANDS)
+    return MOE_ERR_ARG;
+  if (rot < 2 || rot % 2) return MOE_ERR_SHAPE;
+  if (scaling == MOE_ROPE_BANDS &&
+      (!(trained > 0.0) || !(slow > 0.0) || !(fast > slow) || !std::isfinite(trained) ||
+       !std::isfinite(fast)))
+    return MOE_ERR_ARG;
+  if (scaling == MOE_ROPE_BASE && rot == 2) return MOE_ERR_SHAPE;   // the exponent rot / (rot - 2)
+  constexpr double kTurn = 6.283185307179586476925;
+  if (scaling == MOE_ROPE_BASE) base *= std::pow(factor, rot / (rot - 2.0));
+  // pair index whose frequency makes `turns` turns over the trained length
+  const auto pair_of = [&](double turns) {
+    return rot * std::log(trained / (turns * kTurn)) / (2.0 * std::log(base));
+  };
+  double lo = 0.0, hi = 0.0;
+  if (scaling == MOE_ROPE_BANDS) {
+    lo = std::max(0.0, std::floor(pair_of(fast)));
+    hi = std::min(rot - 1.0, std::ceil(pair_of(slow)));
+    if (hi <= lo) hi = lo + 0.001;
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot);
+    if (scaling == MOE_ROPE_LINEAR) f /= factor;
+    if (scaling == MOE_ROPE_BANDS) {
+      const double slowed = std::min(1.0, std::max(0.0, (i - lo) / (hi - lo)));
+      f = f * (1.0 - slowed) + f / factor * slowed;
+    }
+    phase[i] = static_cast<uint64_t>(std::rint(std::ldexp(f / kTurn, 64)));
+  }
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_rope(const void* x, int64_t x_row, int64_t x_head, void* out,
+                               int64_t out_row, int64_t out_head, const int32_t* pos, int32_t T,
+                               int32_t H, int32_t D, const moe_rope_spec* rope, int32_t backward,
+                               int32_t dtype, void* stream) {
+  using namespace moeq4;
+  if (T < 0 || H < 1 || D < 2 || backward < 0 || backward > 1 || dtype < MOE_BF16 ||
+      dtype > MOE_F32)
+    return MOE_ERR_ARG;
+  if (D % 2 || D > 65536 || H > 65536) return MOE_ERR_SHAPE;
+  moe_status st = check_rope(rope, D);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!x || !out || !pos) return MOE_ERR_ARG;
+  if (x_row < 0 || x_head < 0 || !rows_disjoint(out_row, out_head, T, H, D)) return MOE_ERR_SHAPE;
+  if (x == out && (x_row != out_row || x_head != out_head)) return MOE_ERR_ARG;
+  const unsigned es = dtype == MOE_F32 ? 4 : 2;
+  if (bad_align(x, es) || bad_align(out, es) || bad_align(pos, 4)) return MOE_ERR_ALIGN;
+  RopeArgs a{};
+  a.x = x;
+  a.out = out;
+  a.pos = pos;
+  a.phase = rope->phase;
+  a.x_row = x_row;
+  a.x_head = x_head;
+  a.o_row = out_row;
+  a.o_head = out_head;
+  a.T = T;
+  a.H = H;
+  a.D = D;
+  a.rot = rope->rot;
+  a.mscale = rope->mscale;
+  a.interleaved = rope->interleaved;
+  a.backward = backward;
+  a.copy_tail = x != out;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = dtype == MOE_F32   ? launch_rope<float>(a, s)
+                  : dtype == MOE_F16 ? launch_rope<__half>(a, s)
+                                     : launch_rope<__nv_bfloat16>(a, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status moe_kv_append(const moe_kv_new* n, const moe_kv_cache* c, void* stream) {
+  using namespace moeq4;
+  if (!n || n->T < 0 || n->Hq < 0) return MOE_ERR_ARG;
+  moe_status st = check_kv_cache(c);
+  if (st != MOE_OK) return st;
+  if (n->rope && (st = check_rope(n->rope, c->D)) != MOE_OK) return st;
+  if (!n->rope && n->q) return MOE_ERR_ARG;
+  if (n->T == 0) return MOE_OK;
+  if ((st = check_rows(n->k, n->k_row, n->k_head)) != MOE_OK ||
+      (st = check_rows(n->v, n->v_row, n->v_head)) != MOE_OK)
+    return st;
+  if (!n->slots || (n->rope && !n->pos)) return MOE_ERR_ARG;
+  if (bad_align(n->slots, 4) || bad_align(n->pos, 4)) return MOE_ERR_ALIGN;
+  const int Hq = n->q ? n->Hq : 0;
+  if (n->q) {
+    if (n->Hq < 1) return MOE_ERR_ARG;
+    if (n->Hq > 65536) return MOE_ERR_SHAPE;
+    if ((st = check_rows(n->q, n->q_row, n->q_head)) != MOE_OK ||
+        (st = check_rows(n->q_out, n->qo_row, n->qo_head)) != MOE_OK)
+      return st;
+    if (!rows_disjoint(n->qo_row, n->qo_head, n->T, Hq, c->D)) return MOE_ERR_SHAPE;
+    if (n->q == n->q_out && (n->q_row != n->qo_row || n->q_head != n->qo_head)) return MOE_ERR_ARG;
+  }
+  AppendArgs a{};
+  a.q = n->q;
+  a.k = n->k;
+  a.v = n->v;
+  a.q_out = n->q_out;
+  a.q_row = n->q_row;
+  a.q_head = n->q_head;
+  a.k_row = n->k_row;
+  a.k_head = n->k_head;
+  a.v_row = n->v_row;
+  a.v_head = n->v_head;
+  a.qo_row = n->qo_row;
+  a.qo_head = n->qo_head;
+  a.slots = n->slots;
+  a.pos = n->pos;
+  a.T = n->T;
+  a.Hq = Hq;
+  if (n->rope) {
+    a.phase = n->rope->phase;
+    a.rot = n->rope->rot;
+    a.interleaved = n->rope->interleaved;
+    a.mscale = n->rope->mscale;
+  }
+  a.c = kv_cache_args(*c);
+  const int64_t threads = static_cast<int64_t>(n->T) * (Hq + 2 * c->Hkv) * (c->D / 8);
+  const int64_t blocks = (threads + kThreads - 1) / kThreads;
+  if (blocks > 0x7FFFFFFF) return MOE_ERR_SHAPE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c->bits == 8)
+    append_kernel<8><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
+  else
+    append_kernel<4><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status moe_kv_read(const moe_kv_cache* c, const int32_t* slots, int32_t n,
+                                  uint16_t* k_out, uint16_t* v_out, void* stream) {
+  using namespace moeq4;
+  if (n < 0) return MOE_ERR_ARG;
+  moe_status st = check_kv_cache(c);
+  if (st != MOE_OK) return st;
+  if (n == 0) return MOE_OK;
+  if (!slots || (!k_out && !v_out)) return MOE_ERR_ARG;
+  if (bad_align(slots, 4) || bad_align(k_out, 16) || bad_align(v_out, 16)) return MOE_ERR_ALIGN;
+  const int64_t threads = static_cast<int64_t>(n) * 2 * c->Hkv * (c->D / 16);
+  const int64_t blocks = (threads + kThreads - 1) / kThreads;
+  if (blocks > 0x7FFFFFFF) return MOE_ERR_SHAPE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const KvCache k = kv_cache_args(*c);
+  if (c->bits == 8)
+    read_kernel<8><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(k, slots, n, k_out, v_out);
+  else
+    read_kernel<4><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(k, slots, n, k_out, v_out);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

@@ -23,9 +23,17 @@ MOE_DEVERR_SCAN_TIMEOUT = 2
 MOE_DEVERR_PIPE_TIMEOUT = 4
 MOE_DEVERR_BAD_TILE = 8
 MOE_DEVERR_BAD_WORKSPACE = 16
+MOE_DEVERR_BAD_SLOT = 32
+MOE_DEVERR_BAD_PAGE = 64
+MOE_DEVERR_BAD_LENGTH = 128
 MOE_ERR_TOO_LARGE = -8
+MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_BASE, MOE_ROPE_BANDS = 0, 1, 2, 3
 
 _c_i32 = ctypes.c_int32
+_c_i64 = ctypes.c_int64
+_c_f32 = ctypes.c_float
+_c_f64 = ctypes.c_double
 _c_ptr = ctypes.c_void_p
 _c_size = ctypes.c_size_t
 
@@ -48,6 +56,32 @@ class RouteOutC(ctypes.Structure):
                 ("perm", _c_ptr), ("inv", _c_ptr), ("tiles", _c_ptr), ("n_tiles", _c_ptr),
                 ("err", _c_ptr), ("T", _c_i32), ("E", _c_i32), ("k", _c_i32),
                 ("block_m", _c_i32)]
+
+
+class RopeSpecC(ctypes.Structure):
+    _fields_ = [("phase", _c_ptr), ("rot", _c_i32), ("interleaved", _c_i32), ("mscale", _c_f32)]
+
+
+class KVCacheC(ctypes.Structure):
+    _fields_ = [("data", _c_ptr), ("err", _c_ptr), ("pages", _c_i32), ("page_size", _c_i32),
+                ("Hkv", _c_i32), ("D", _c_i32), ("bits", _c_i32)]
+
+
+class KVNewC(ctypes.Structure):
+    _fields_ = [("k", _c_ptr), ("k_row", _c_i64), ("k_head", _c_i64),
+                ("v", _c_ptr), ("v_row", _c_i64), ("v_head", _c_i64),
+                ("q", _c_ptr), ("q_row", _c_i64), ("q_head", _c_i64),
+                ("q_out", _c_ptr), ("qo_row", _c_i64), ("qo_head", _c_i64),
+                ("slots", _c_ptr), ("pos", _c_ptr), ("rope", ctypes.POINTER(RopeSpecC)),
+                ("T", _c_i32), ("Hq", _c_i32)]
+
+
+class KVAttnC(ctypes.Structure):
+    _fields_ = [("q", _c_ptr), ("q_row", _c_i64), ("q_head", _c_i64),
+                ("out", _c_ptr), ("out_row", _c_i64), ("out_head", _c_i64),
+                ("table", _c_ptr), ("lens", _c_ptr), ("prefix_table", _c_ptr),
+                ("B", _c_i32), ("nq", _c_i32), ("Hq", _c_i32), ("table_stride", _c_i32),
+                ("max_len", _c_i32), ("prefix_len", _c_i32), ("scale", _c_f32)]
 
 
 class MoeError(RuntimeError):
@@ -84,6 +118,15 @@ _SIGS = {
     "moe_get_device_error": (_c_i32, [_c_ptr, ctypes.POINTER(_c_i32), _c_ptr]),
     "moe_status_string": (ctypes.c_char_p, [_c_i32]),
     "moe_residual_rms": (_c_i32, [_c_ptr, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr]),
+    "moe_rope_phases": (_c_i32, [_c_ptr, _c_i32, _c_f64, _c_i32, _c_f64, _c_f64, _c_f64, _c_f64]),
+    "moe_rope": (_c_i32, [_c_ptr, _c_i64, _c_i64, _c_ptr, _c_i64, _c_i64, _c_ptr, _c_i32, _c_i32,
+                          _c_i32, ctypes.POINTER(RopeSpecC), _c_i32, _c_i32, _c_ptr]),
+    "moe_kv_cache_size": (_c_size, [_c_i32] * 5),
+    "moe_kv_append": (_c_i32, [ctypes.POINTER(KVNewC), ctypes.POINTER(KVCacheC), _c_ptr]),
+    "moe_kv_read": (_c_i32, [ctypes.POINTER(KVCacheC), _c_ptr, _c_i32, _c_ptr, _c_ptr, _c_ptr]),
+    "moe_kv_attention_workspace_size": (_c_size, [_c_i32] * 7),
+    "moe_kv_attention": (_c_i32, [ctypes.POINTER(KVAttnC), ctypes.POINTER(KVCacheC), _c_ptr,
+                                  _c_size, _c_ptr]),
     "moe_debug_dequant": (_c_i32, [_c_ptr, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr, _c_ptr]),
     "moe_debug_mma": (_c_i32, [_c_i32, _c_ptr, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr]),
     "moe_debug_set_stage_events": (_c_i32, [ctypes.POINTER(_c_ptr), _c_i32]),
@@ -365,8 +408,180 @@ def moe_l2_prefetch(t: torch.Tensor, nbytes: int = None, stream=None) -> None:
     _check("moe_l2_prefetch", lib().moe_l2_prefetch(_ptr(t), n, _stream(stream)))
 
 
-def moe_get_device_error(r: RouteBuffers, stream=None) -> int:
-    """Synchronises the stream and returns the device error word (0 = none)."""
+# ------------------------------------------------- attention side of a decoder layer
+
+def moe_rope_phases(rot, base, scaling=MOE_ROPE_PLAIN, factor=1.0, trained=0.0, fast=32.0,
+                    slow=1.0) -> torch.Tensor:
+    """Turns per position of rot/2 pairs as 64-bit fractions (int64 bit patterns, on the host)."""
+    phase = torch.empty(max(1, rot // 2), dtype=torch.int64)
+    _check("moe_rope_phases", lib().moe_rope_phases(_ptr(phase), rot, base, scaling, factor,
+                                                    trained, fast, slow))
+    return phase
+
+
+class RopeSpec:
+    """Rotary positions of the first ``rot`` elements of a head (moe_rope_spec); ``phase`` is
+    the device copy of :func:`moe_rope_phases`."""
+
+    def __init__(self, phase: torch.Tensor, rot: int, interleaved=False, mscale=1.0):
+        _need("RopeSpec", phase, torch.int64, "phase")
+        if phase.numel() != rot // 2:
+            raise ValueError(f"RopeSpec: phase must hold rot/2 = {rot // 2} values, got {phase.numel()}")
+        self.phase, self.rot, self.interleaved, self.mscale = phase, rot, interleaved, mscale
+        self._c = RopeSpecC(_ptr(phase), rot, int(interleaved), mscale)
+
+
+def moe_kv_cache_size(pages, page_size, Hkv, D, bits) -> int:
+    """Bytes of a cache (0 if the sizes are not allowed)."""
+    return lib().moe_kv_cache_size(pages, page_size, Hkv, D, bits)
+
+
+class KVCache:
+    """A paged key/value cache in 64-element groups of 8- or 4-bit codes (moe_kv_cache).
+
+    ``data`` is a dense uint8 CUDA tensor of whole pages (its layout is described in
+    moeq4.h); ``err`` the int32 device error word of the calls on this cache."""
+
+    def __init__(self, data: torch.Tensor, page_size: int, Hkv: int, D: int, bits: int,
+                 err: torch.Tensor = None):
+        _need("KVCache", data, torch.uint8, "data")
+        page = moe_kv_cache_size(1, page_size, Hkv, D, bits)
+        if page == 0 or data.numel() == 0 or data.numel() % page:
+            raise ValueError(f"KVCache: data must be whole pages of page_size={page_size}, Hkv={Hkv}, "
+                             f"D={D}, bits={bits} ({page} bytes each), got {data.numel()} bytes")
+        self.data, self.page_size, self.Hkv, self.D, self.bits = data, page_size, Hkv, D, bits
+        self.pages = data.numel() // page
+        self.err = torch.zeros(4, dtype=torch.int32, device=data.device) if err is None else err
+        _need("KVCache", self.err, torch.int32, "err")
+        self._c = KVCacheC(_ptr(data), _ptr(self.err), self.pages, page_size, Hkv, D, bits)
+
+    @classmethod
+    def alloc(cls, pages, page_size, Hkv, D, bits, device="cuda"):
+        n = moe_kv_cache_size(pages, page_size, Hkv, D, bits)
+        if n == 0:
+            raise ValueError(f"KVCache: sizes not allowed: pages={pages}, page_size={page_size}, "
+                             f"Hkv={Hkv}, D={D}, bits={bits}")
+        return cls(torch.empty(n, dtype=torch.uint8, device=device), page_size, Hkv, D, bits)
+
+
+def _need_rows(fn, t, name, D=None, dtype=torch.bfloat16):
+    """[rows][heads][elements] with dense elements; rows and heads may be strided."""
+    if (t is None or not t.is_cuda or t.dtype != dtype or t.dim() != 3 or t.stride(2) != 1
+            or (D is not None and t.shape[2] != D)):
+        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
+        raise ValueError(f"{fn}: {name} must be a {dtype} CUDA tensor [rows][heads]"
+                         f"[{'D' if D is None else D}] with dense elements, got {got}")
+
+
+def _need_ints(fn, t, n, name):
+    if t is None or not t.is_cuda or t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
+        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"
+        raise ValueError(f"{fn}: {name} must be a contiguous int32 CUDA tensor of at least {n} "
+                         f"values, got {got}")
+
+
+_ROPE_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+
+
+def moe_rope(x: torch.Tensor, out: torch.Tensor, pos: torch.Tensor, rope: RopeSpec,
+             backward=False, stream=None) -> None:
+    """Turns x [T, H, D] (bf16, fp16 or fp32, strided rows and heads) to positions pos [T];
+    ``backward`` takes the gradient of the output to that of x. out may be x."""
+    dtype = _ROPE_DTYPES.get(x.dtype)
+    if dtype is None:
+        raise ValueError(f"moe_rope: x must be bfloat16, float16 or float32, got {x.dtype}")
+    _need_rows("moe_rope", x, "x", dtype=x.dtype)
+    T, H, D = x.shape
+    _need_rows("moe_rope", out, "out", D, x.dtype)
+    if out.shape != x.shape:
+        raise ValueError(f"moe_rope: out must have x's shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    _need_ints("moe_rope", pos, T, "pos")
+    _check("moe_rope", lib().moe_rope(_ptr(x), x.stride(0), x.stride(1), _ptr(out), out.stride(0),
+                                      out.stride(1), _ptr(pos), T, H, D, ctypes.byref(rope._c),
+                                      int(backward), dtype, _stream(stream)))
+
+
+def moe_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                  pos: torch.Tensor = None, rope: RopeSpec = None, q: torch.Tensor = None,
+                  q_out: torch.Tensor = None, stream=None) -> None:
+    """Turns k [T, Hkv, D] (and q [T, Hq, D] into q_out), quantises k and v and writes them to
+    ``slots`` [T] (-1: skip). Without ``rope`` the keys are stored as given and q must be None."""
+    fn = "moe_kv_append"
+    D = cache.D
+    _need_rows(fn, k, "k", D)
+    _need_rows(fn, v, "v", D)
+    T = k.shape[0]
+    if k.shape[1] != cache.Hkv or v.shape != k.shape:
+        raise ValueError(f"{fn}: k and v must be [T][{cache.Hkv}][{D}], got {tuple(k.shape)} and "
+                         f"{tuple(v.shape)}")
+    _need_ints(fn, slots, T, "slots")
+    a = KVNewC(_ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1))
+    a.slots, a.T = _ptr(slots), T
+    if rope is not None:
+        _need_ints(fn, pos, T, "pos")
+        a.pos, a.rope = _ptr(pos), ctypes.pointer(rope._c)
+    if q is not None:
+        _need_rows(fn, q, "q", D)
+        _need_rows(fn, q_out, "q_out", D)
+        if q.shape[0] != T or q_out.shape != q.shape:
+            raise ValueError(f"{fn}: q and q_out must be [{T}][Hq][{D}], got {tuple(q.shape)} and "
+                             f"{tuple(q_out.shape)}")
+        a.q, a.q_row, a.q_head, a.Hq = _ptr(q), q.stride(0), q.stride(1), q.shape[1]
+        a.q_out, a.qo_row, a.qo_head = _ptr(q_out), q_out.stride(0), q_out.stride(1)
+    _check(fn, lib().moe_kv_append(ctypes.byref(a), ctypes.byref(cache._c), _stream(stream)))
+
+
+def moe_kv_read(cache: KVCache, slots: torch.Tensor, k_out: torch.Tensor = None,
+                v_out: torch.Tensor = None, stream=None) -> None:
+    """Cache rows of ``slots`` [n] as bf16 [n, Hkv, D]; k_out or v_out may be None."""
+    fn, n = "moe_kv_read", slots.numel()
+    _need_ints(fn, slots, 0, "slots")
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _need(fn, t, torch.bfloat16, name, optional=True)
+        if t is not None and t.shape != (n, cache.Hkv, cache.D):
+            raise ValueError(f"{fn}: {name} must be [{n}][{cache.Hkv}][{cache.D}], got {tuple(t.shape)}")
+    _check(fn, lib().moe_kv_read(ctypes.byref(cache._c), _ptr(slots), n, _ptr(k_out), _ptr(v_out),
+                                 _stream(stream)))
+
+
+def moe_kv_attention_workspace_size(B, nq, Hq, Hkv, D, max_len, prefix_len=0) -> int:
+    return lib().moe_kv_attention_workspace_size(B, nq, Hq, Hkv, D, max_len, prefix_len)
+
+
+def moe_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
+                     max_len: int, out: torch.Tensor, ws: torch.Tensor, nq=1,
+                     prefix_table: torch.Tensor = None, prefix_len=0, scale=None,
+                     stream=None) -> None:
+    """Attention of q [B*nq, Hq, D] over each request's cached context into out.
+
+    Request b sees the first ``prefix_len`` tokens of ``prefix_table``'s pages (shared by the
+    batch), then its own ``lens[b]`` tokens in the pages ``table[b]``, the last nq of which are
+    its query tokens (causal among themselves). ``scale`` defaults to 1/sqrt(D)."""
+    fn, D = "moe_kv_attention", cache.D
+    _need_rows(fn, q, "q", D)
+    _need_rows(fn, out, "out", D)
+    rows, Hq, _ = q.shape
+    if nq < 1 or rows % nq or out.shape != q.shape:
+        raise ValueError(f"{fn}: q and out must be [B*nq][Hq][{D}] with nq={nq}, got "
+                         f"{tuple(q.shape)} and {tuple(out.shape)}")
+    B = rows // nq
+    _need_ints(fn, lens, B, "lens")
+    if table is None or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"{fn}: table must be an int32 tensor of {B} rows of pages")
+    _need_ints(fn, table, 0, "table")
+    if prefix_len:
+        _need_ints(fn, prefix_table, -(-prefix_len // cache.page_size), "prefix_table")
+    _need(fn, ws, torch.uint8, "ws")
+    a = KVAttnC(_ptr(q), q.stride(0), q.stride(1), _ptr(out), out.stride(0), out.stride(1),
+                _ptr(table), _ptr(lens), _ptr(prefix_table), B, nq, Hq, table.shape[1], max_len,
+                prefix_len, D ** -0.5 if scale is None else scale)
+    _check(fn, lib().moe_kv_attention(ctypes.byref(a), ctypes.byref(cache._c), _ptr(ws), ws.numel(),
+                                      _stream(stream)))
+
+
+def moe_get_device_error(r: "RouteBuffers | KVCache", stream=None) -> int:
+    """Synchronises the stream and returns the device error word of a routing result or a
+    cache (0 = none)."""
     code = _c_i32(0)
     s = lib().moe_get_device_error(_ptr(r.err), ctypes.byref(code), _stream(stream))
     if s not in (MOE_OK, -5):
