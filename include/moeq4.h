@@ -406,7 +406,8 @@ typedef struct moe_kv_attn {
 size_t moe_kv_attention_workspace_size(int32_t B, int32_t nq, int32_t Hq, int32_t Hkv, int32_t D,
                                        int32_t max_len, int32_t prefix_len);
 
-/* B = 0 launches nothing. Page numbers are read only as far as lens and
+/* Limits: B * nq <= 2^24, Hq % Hkv == 0, Hq <= 65535, max_len and prefix_len <= 2^30.
+ * B = 0 launches nothing. Page numbers are read only as far as lens and
  * prefix_len reach. q and out: 16-byte aligned, strides multiples of 8. */
 moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache* c, void* ws,
                             size_t ws_bytes, void* stream);

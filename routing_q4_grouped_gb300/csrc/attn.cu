@@ -1,8 +1,37 @@
 // attn.cu — attention over the paged, quantised key/value cache, with an
 // optional prefix that every request of the batch shares (moe_kv_attention).
+//
+// Contexts are cut into splits; a block takes one split for a tile of query rows
+// that share a key/value head (the heads of a group, a request's query tokens
+// and, for the prefix, all requests of the batch), and writes a partial result:
+// the largest logit m, the sum l of exp2(x - m) and the weighted sum of values.
+// A second kernel joins the splits of a row.
+//
+// Few rows read many codes, so the work is bound by memory bandwidth as long as
+// turning codes into tensor-core operands costs less than the bytes. Two choices
+// keep it cheap:
+//  * Codes go into the products as integers. A byte c under the byte 0x64 is the
+//    fp16 number 1024 + c, so one byte permutation makes an operand pair. With
+//    value = s c + b and q' the query in fp16,
+//      q . k = sum over groups of  s (sum (1024 + c) q' - 1024 sum q') + b sum q',
+//    where the first difference is the accumulator's initial value. Values are
+//    centred ((1024 + c) - 1152, exact) and their scale is taken into the weights:
+//      sum_t p_t v_t = sum_t (p_t s_t)(c_t - 128) + sum_t p_t (b_t + 128 s_t).
+//  * Tokens are the rows (M) of the products and queries the columns (N = 8), so
+//    that 8 rows fill the tensor core: X^T = K Q^T, then O^T = V^T P^T. The
+//    products' own register layouts let a thread read 16 (keys) or 8 (values)
+//    neighbouring codes of a token at once; P is transposed between the two
+//    products by one 8x8 register transpose per 8 tokens and group.
+// q' and p s are fp16: q' is the query divided by the power of two under its
+// row's largest element, p s is divided by a running power of two not far from
+// the largest scale seen, so neither leaves fp16's range and both keep 11 bits
+// (one rounding of 2^-11 for the weights; bf16 queries are exact above 2^-16 of
+// their row's largest element). Logits, maxima, sums and outputs are fp32.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -13,6 +42,8 @@ namespace moeq4 {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 struct AttnArgs {
   const uint16_t* q;
@@ -20,98 +51,753 @@ struct AttnArgs {
   int64_t q_row, q_head, o_row, o_head;
   const int32_t *table, *lens, *prefix_table;
   int B, nq, Hq, table_stride, max_len, prefix_len, G;
-  float scale;
+  float scale2;              // scale * log2(e)
   KvCache c;
+  uint32_t page_blocks;      // 16-token blocks per page
+  uint64_t page_magic;       // floor(2^40 / page_blocks) + 1
+  // work: blocks [0, pre_blocks) take the prefix, the rest the requests' own tokens
+  int pre_chunk, pre_splits, pre_tiles, pre_blocks;
+  int own_chunk, own_splits, own_tiles;
+  float* part;               // [split][row][head][D]; prefix splits first
+  float2* ml;                // [split][row][head]: (m, l)
 };
 
 // A context length as the kernels use it.
-__device__ __forceinline__ int context_len(const AttnArgs& a, int b) {
+__device__ __forceinline__ int context_len(const AttnArgs& a, int b, bool report) {
   const int n = a.lens[b];
   if (n >= 0 && n <= a.max_len) return n;
-  atomicOr(a.c.err, MOE_DEVERR_BAD_LENGTH);
+  if (report) atomicOr(a.c.err, MOE_DEVERR_BAD_LENGTH);
   return n < 0 ? 0 : a.max_len;
 }
 
-// Block = one query row of one head; its warps share the tokens, each with its
-// own running maximum and sum, joined through shared memory. Lane l holds
-// elements l*E .. l*E+E-1 of the head.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D += A B: A 16x16 fp16 (row), B 16x8 fp16 (col), D 16x8 fp32.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ float max_over_rows8(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+__device__ __forceinline__ float sum_over_rows8(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// Geometry of the split kernel for head size D and code width BITS.
 template <int D, int BITS>
-__global__ void __launch_bounds__(kWarps * 32) attn_row_kernel(AttnArgs a) {
-  constexpr int E = D / 32;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int row = blockIdx.x, hq = blockIdx.y;
-  const int b = row / a.nq, i = row % a.nq, hk = hq / a.G;
-  const int len = context_len(a, b);
-  const int seen = max(0, len - a.nq + 1 + i);
-  float q[E], o[E] = {};
-  const uint16_t* qp = a.q + row * a.q_row + hq * a.q_head + lane * E;
+struct Geo {
+  static constexpr int J = D / kKvGroup;          // groups of a head
+  static constexpr int RB = D * BITS / 8;         // code bytes of a token
+  static constexpr int TB = D == 256 ? 1 : 2;     // 16-token blocks per step
+  static constexpr int kCodes = 16 * RB;          // one block's codes (keys or values)
+  static constexpr int kWords = 16 * J * 4;
+  static constexpr int kBlock = 2 * (kCodes + kWords);   // K codes, V codes, K words, V words
+  static constexpr int kStage = TB * kBlock;
+  static constexpr int kStages = 3;
+  static constexpr int kWarpBytes = kStages * kStage;
+  static constexpr int kRing = kWarps * kWarpBytes;
+  // Shared memory is laid out in rows of RB bytes whose 32-byte units are
+  // exchanged by the token's low bits, so that the lanes of one shared-memory
+  // access (which read the same unit of several tokens) meet no bank twice.
+  static constexpr int kUnits = RB / 32;
+  __device__ static int key_unit(int row, int u) {
+    if (BITS == 8) return kUnits >= 4 ? u ^ ((row & 1) << 1) : u;
+    return kUnits >= 4 ? u ^ (row & 3) : kUnits == 2 ? u ^ ((row >> 1) & 1) : u;
+  }
+  __device__ static int value_unit(int row, int u) {
+    return kUnits >= 4 ? u ^ ((row >> 1) & 3) : kUnits == 2 ? u ^ ((row >> 1) & 1) : u;
+  }
+};
+
+template <int D, int BITS, int NT>
+struct SplitSmem {
+  static constexpr size_t kMerge = size_t(kWarps) * 8 * NT * (D + 4) * 4;   // rows padded by 4
+  static constexpr size_t kBytes =
+      (Geo<D, BITS>::kRing > kMerge ? size_t(Geo<D, BITS>::kRing) : kMerge) + kWarps * 8 * NT * 8;
+};
+
+// One step's operands and state of a warp.
+template <int D, int BITS, int NT>
+struct Warp {
+  using G = Geo<D, BITS>;
+  uint32_t q[NT][G::J][8];        // queries: B operand of X^T = K Q^T
+  float init[NT][G::J][2];        // -1024 * sum of the operand's elements, by group
+  float qsum[NT][G::J][2];        // sum of q' by group
+  float row_scale[NT][2];         // scale2 * 2^(row exponent)
+  int lim[NT][2];                 // tokens seen by the row
+  float m[NT][2], l[NT][2];
+  float o[NT][G::J][4][4];        // O^T: group, tile of 16 elements
+  float ob[NT][G::J][2];          // sum of p * centred bias
+  float f;                        // 2^-e: p s f is near or below 1
+
+  // Columns 2t, 2t+1 of this thread (queries); rows lane/4 and lane/4 + 8 (tokens).
+  template <bool MASK>
+  __device__ __forceinline__ void step(const uint8_t* st, int tok0, const int (&top)[G::TB],
+                                       int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float x[G::TB][NT][4];
+    uint32_t vw[G::TB][2][G::J];            // value words of tokens g, g + 8
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    q[e] = __uint_as_float(static_cast<uint32_t>(qp[e]) << 16) * a.scale;
-  float m = -INFINITY, l = 0.f;
-  for (int part = 0; part < 2; ++part) {
-    const int32_t* pages =
-        part == 0 ? a.prefix_table : a.table + static_cast<int64_t>(b) * a.table_stride;
-    const int n = part == 0 ? a.prefix_len : seen;
-    for (int t = warp; t < n; t += kWarps) {
-      const int page = pages[t / a.c.page_size], r = t % a.c.page_size;
-      if (page < 0 || page >= a.c.pages) {
-        if (lane == 0) atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
-        continue;
-      }
-      float kv[2][E];
+    for (int b = 0; b < G::TB; ++b) {
+      const uint8_t* kc = st + b * G::kBlock;
+      const uint8_t* words = kc + 2 * G::kCodes;
+      uint32_t kw[2][G::J];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const uint8_t* blk = kv_block(a.c, page, hk + w * a.c.Hkv);
-        const uint32_t sb = *reinterpret_cast<const uint32_t*>(
-            blk + a.c.code_bytes + (r * (D / kKvGroup) + lane * E / kKvGroup) * 4);
+      for (int r = 0; r < 2; ++r) {
+        const int row = g + 8 * r;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int d = lane * E + e;
-          const uint32_t byte = blk[static_cast<int64_t>(r) * a.c.row_bytes + d * BITS / 8];
-          const uint32_t code = BITS == 8 ? byte : (byte >> (d % 2 * 4)) & 15u;
-          kv[w][e] = fmaf(bf16_lo(sb), static_cast<float>(code), bf16_hi(sb));
+        for (int j = 0; j < G::J; ++j) {
+          kw[r][j] = *reinterpret_cast<const uint32_t*>(words + (row * G::J + j) * 4);
+          vw[b][r][j] =
+              *reinterpret_cast<const uint32_t*>(words + G::kWords + (row * G::J + j) * 4);
         }
       }
-      float x = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x = fmaf(q[e], kv[0][e], x);
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, s);
-      const float top = fmaxf(m, x);
-      const float base = top == -INFINITY ? 0.f : top;
-      const float keep = __expf(m - base), p = __expf(x - base);
-      m = top;
-      l = fmaf(l, keep, p);
+        for (int i = 0; i < 4; ++i) x[b][n][i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], keep, p * kv[1][e]);
+      for (int j = 0; j < G::J; ++j) {
+        // 16 codes of tokens g and g + 8: elements 64 j + 16 t ..
+        uint32_t w[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = g + 8 * r;
+          if (BITS == 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                kc + row * G::RB + G::key_unit(row, 2 * j + (t >> 1)) * 32 + (t & 1) * 16);
+            w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(
+                kc + row * G::RB + G::key_unit(row, j) * 32 + t * 8);
+            w[r][0] = v.x, w[r][1] = v.x >> 8, w[r][2] = v.y, w[r][3] = v.y >> 8;
+          }
+        }
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] = init[n][j][i & 1];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint32_t a[4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (BITS == 8) {
+              a[r] = prmt(w[r][s], 0x64646464u, 0x4140);
+              a[2 + r] = prmt(w[r][s], 0x64646464u, 0x4342);
+            } else {
+              a[r] = lop3_and_or(w[r][s], 0x000F000Fu, 0x64006400u);
+              a[2 + r] = lop3_and_or(w[r][s], 0x00F000F0u, 0x64006400u);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(acc[n], a, q[n][j][2 * s], q[n][j][2 * s + 1]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t sb = kw[i >> 1][j];
+            x[b][n][i] = fmaf(bf16_lo(sb), acc[n][i],
+                              fmaf(bf16_hi(sb), qsum[n][j][i & 1], x[b][n][i]));
+          }
+      }
+    }
+    bool grow = false;
+#pragma unroll
+    for (int b = 0; b < G::TB; ++b) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int tok = tok0 + 16 * b + 8 * r + g;
+        const bool any = !MASK || tok < top[b];
+#pragma unroll
+        for (int j = 0; j < G::J; ++j) {
+          if (MASK && !any) vw[b][r][j] = 0;
+          grow |= fabsf(bf16_lo(vw[b][r][j])) * f >= 2.f;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float& v = x[b][n][2 * r + c];
+            v *= row_scale[n][c];
+            if (MASK && !(any && tok < lim[n][c])) v = -INFINITY;
+            // weights may pass 1 by 2^8 before the reference is moved
+            grow |= v > m[n][c] + 8.f;
+          }
+      }
+    }
+    if (__any_sync(kAll, grow)) rescale(x, vw);
+    // weights
+#pragma unroll
+    for (int b = 0; b < G::TB; ++b)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float ref = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1];
+          const float p = exp2_approx(x[b][n][i] - ref);
+          x[b][n][i] = p;
+          l[n][i & 1] += p;
+        }
+    // O^T += V^T P^T
+#pragma unroll
+    for (int b = 0; b < G::TB; ++b) {
+      const uint8_t* vc = st + b * G::kBlock + G::kCodes;
+#pragma unroll
+      for (int j = 0; j < G::J; ++j) {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float s = bf16_lo(vw[b][r][j]);
+          const float sf = s * f;
+          const float bias = fmaf(BITS == 8 ? 128.f : 8.f, s, bf16_hi(vw[b][r][j]));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float p0 = x[b][n][2 * r], p1 = x[b][n][2 * r + 1];
+            pb[n][r] = transpose8x8(pack_f16(p0 * sf, p1 * sf));
+            if (MASK) {            // a bias may be NaN: no product with rows that do not see it
+              if (p0 != 0.f) ob[n][j][0] = fmaf(p0, bias, ob[n][j][0]);
+              if (p1 != 0.f) ob[n][j][1] = fmaf(p1, bias, ob[n][j][1]);
+            } else {
+              ob[n][j][0] = fmaf(p0, bias, ob[n][j][0]);
+              ob[n][j][1] = fmaf(p1, bias, ob[n][j][1]);
+            }
+          }
+        }
+        // 8 codes of tokens 2t, 2t+1, 2t+8, 2t+9: elements 64 j + 8 g ..
+        uint32_t w[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = 2 * t + (k & 1) + 8 * (k >> 1);
+          if (BITS == 8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(
+                vc + row * G::RB + G::value_unit(row, 2 * j + (g >> 2)) * 32 + (g & 3) * 8);
+            w[k][0] = v.x, w[k][1] = v.y;
+          } else {
+            w[k][0] = *reinterpret_cast<const uint32_t*>(
+                vc + row * G::RB + G::value_unit(row, j) * 32 + g * 4);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {        // tiles 2h, 2h + 1: elements 4h .. 4h + 3 of the 8
+          uint32_t a[2][4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {      // token pairs (2t, 2t+1) and (2t+8, 2t+9)
+            if (BITS == 8) {
+              const uint32_t lo = prmt(w[2 * k][h], w[2 * k + 1][h], 0x5140);
+              const uint32_t hi = prmt(w[2 * k][h], w[2 * k + 1][h], 0x7362);
+              constexpr uint32_t kC = 0x64806480u;     // 1024 + 128
+              a[0][2 * k] = sub_f16x2(prmt(lo, 0x64646464u, 0x4140), kC);
+              a[0][2 * k + 1] = sub_f16x2(prmt(lo, 0x64646464u, 0x4342), kC);
+              a[1][2 * k] = sub_f16x2(prmt(hi, 0x64646464u, 0x4140), kC);
+              a[1][2 * k + 1] = sub_f16x2(prmt(hi, 0x64646464u, 0x4342), kC);
+            } else {
+              // odd elements stay multiplied by 16 until the end
+              const uint32_t v = prmt(w[2 * k][0], w[2 * k + 1][0], h ? 0x7632 : 0x5410);
+              constexpr uint32_t kC = 0x64086408u, kC16 = 0x64806480u;   // 1024 + 8, 1024 + 128
+              a[0][2 * k] = sub_f16x2(lop3_and_or(v, 0x000F000Fu, 0x64006400u), kC);
+              a[0][2 * k + 1] = sub_f16x2(lop3_and_or(v, 0x00F000F0u, 0x64006400u), kC16);
+              a[1][2 * k] = sub_f16x2(lop3_and_or(v >> 8, 0x000F000Fu, 0x64006400u), kC);
+              a[1][2 * k + 1] = sub_f16x2(lop3_and_or(v >> 8, 0x00F000F0u, 0x64006400u), kC16);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(o[n][j][2 * h], a[0], pb[n][0], pb[n][1]);
+            mma16816(o[n][j][2 * h + 1], a[1], pb[n][0], pb[n][1]);
+          }
+        }
+      }
     }
   }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
+
+  // Moves the rows' reference m to their largest logit and the weights' power of
+  // two to the largest scale, and what has been summed up along with them.
+  __device__ __forceinline__ void rescale(const float (&x)[G::TB][NT][4],
+                                          const uint32_t (&vw)[G::TB][2][G::J]) {
+    uint32_t big = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+    for (int b = 0; b < G::TB; ++b)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < G::J; ++j) big = max(big, vw[b][r][j] & 0x7FFFu);
+    const uint32_t e_new = min(max(__reduce_max_sync(kAll, big) >> 7, 1u), 252u);
+    const uint32_t e_old = 254u - (__float_as_uint(f) >> 23);
+    const uint32_t e = max(e_old, e_new);
+    const float fn = __uint_as_float((254u - e) << 23);
+    const float down = exp2_approx(static_cast<float>(e_old) - static_cast<float>(e));
+    f = fn;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float keep[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = m[n][c];
+#pragma unroll
+        for (int b = 0; b < G::TB; ++b) mx = fmaxf(mx, fmaxf(x[b][n][c], x[b][n][2 + c]));
+        mx = max_over_rows8(mx);
+        keep[c] = mx == m[n][c] ? 1.f : exp2_approx(m[n][c] - mx);
+        m[n][c] = mx;
+        l[n][c] *= keep[c];
+      }
+#pragma unroll
+      for (int j = 0; j < G::J; ++j) {
+        ob[n][j][0] *= keep[0];
+        ob[n][j][1] *= keep[1];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[n][j][u][i] *= keep[i & 1] * down;
+      }
+    }
+  }
+};
+
+// One block: one split of one context (a request's own tokens, or the prefix) for
+// a tile of 8 NT query rows of one key/value head. Its warps take every fourth
+// step of 16 TB tokens, each through a ring of asynchronous copies of its own (no
+// block barrier until the join).
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) {
+  using G = Geo<D, BITS>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = lane >> 2, t = lane & 3;
+  // ---- which work
+  int id = blockIdx.x;
+  const bool pre = id < a.pre_blocks;
+  int b = 0, split, tile, hk, n_rows, ctx, t0, chunk;
+  const int32_t* pages;
+  if (pre) {
+    tile = id % a.pre_tiles;
+    id /= a.pre_tiles;
+    hk = id % a.c.Hkv;
+    split = id / a.c.Hkv;
+    n_rows = a.B * a.nq * a.G;
+    ctx = a.prefix_len;
+    chunk = a.pre_chunk;
+    pages = a.prefix_table;
+  } else {
+    id -= a.pre_blocks;
+    tile = id % a.own_tiles;
+    id /= a.own_tiles;
+    hk = id % a.c.Hkv;
+    id /= a.c.Hkv;
+    split = id % a.own_splits;
+    b = id / a.own_splits;
+    n_rows = a.nq * a.G;
+    ctx = context_len(a, b, split == 0 && tile == 0 && hk == 0 && threadIdx.x == 0);
+    chunk = a.own_chunk;
+    pages = a.table + static_cast<int64_t>(b) * a.table_stride;
+  }
+  t0 = split * chunk;
+  const int row0 = tile * 8 * NT;
+  // the tile's last row sees most
+  const auto limit = [&](int r) {
+    return pre ? ctx : max(0, ctx - a.nq + 1 + r / a.G);
+  };
+  if (t0 >= ctx && !(split == 0 && a.pre_splits == 0)) return;   // split 0 of a lone context writes zeros
+  const int t1 = min(min(t0 + chunk, ctx), limit(min(row0 + 8 * NT, n_rows) - 1));
+
+  // ---- queries
+  Warp<D, BITS, NT> w;
+  w.f = __uint_as_float(253u << 23);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = row0 + 8 * n + g;
+    float mx = 0.f;
+    float qv[G::J][16];
+    if (r < n_rows) {
+      const int qrow = pre ? r / a.G : b * a.nq + r / a.G;
+      const uint16_t* qp = a.q + qrow * a.q_row + (hk * a.G + r % a.G) * a.q_head;
+#pragma unroll
+      for (int j = 0; j < G::J; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 v = *reinterpret_cast<const uint4*>(qp + 64 * j + 16 * t + 8 * h);
+          const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            qv[j][8 * h + 2 * i] = bf16_lo(wd[i]);
+            qv[j][8 * h + 2 * i + 1] = bf16_hi(wd[i]);
+          }
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < G::J; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) qv[j][i] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < G::J; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(qv[j][i]));
+    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
+    const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
+    const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
+#pragma unroll
+    for (int j = 0; j < G::J; ++j) {
+      float all = 0.f, in = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // operand pairs in the order the codes come out of a word: neighbours of a
+        // byte pair, or nibbles 4 apart, the odd ones times 16 and so q' over 16
+        const int e0 = BITS == 8 ? 2 * i : 8 * (i / 4) + i % 4;
+        const int e1 = BITS == 8 ? e0 + 1 : e0 + 4;
+        const float z = BITS == 4 && (i & 1) ? down * 0.0625f : down;
+        const uint32_t p = pack_f16(qv[j][e0] * z, qv[j][e1] * z);
+        w.q[n][j][i] = p;
+        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&p));
+        in += back.x + back.y;
+        all += (back.x + back.y) * (BITS == 4 && (i & 1) ? 16.f : 1.f);
+      }
+      in += __shfl_xor_sync(kAll, in, 1);
+      in += __shfl_xor_sync(kAll, in, 2);
+      all += __shfl_xor_sync(kAll, all, 1);
+      all += __shfl_xor_sync(kAll, all, 2);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {            // of the columns this thread accumulates
+        w.init[n][j][c] = -1024.f * __shfl_sync(kAll, in, (2 * t + c) * 4);
+        w.qsum[n][j][c] = __shfl_sync(kAll, all, (2 * t + c) * 4);
+        w.ob[n][j][c] = 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.o[n][j][u][i] = 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      w.row_scale[n][c] = a.scale2 * __shfl_sync(kAll, up, (2 * t + c) * 4);
+      const int rc = row0 + 8 * n + 2 * t + c;
+      w.lim[n][c] = rc < n_rows ? limit(rc) : t1;
+      w.m[n][c] = -INFINITY;
+      w.l[n][c] = 0.f;
+    }
+  }
+  int low = t1;                                // tokens that every row of the tile sees
+#pragma unroll
+  for (int n = 0; n < NT; ++n) low = min(low, min(w.lim[n][0], w.lim[n][1]));
+  low = __reduce_min_sync(kAll, low);
+
+  // ---- tokens
+  uint8_t* ring = smem + warp * G::kWarpBytes;
+  constexpr int kStep = 16 * G::TB;
+  const int steps = t1 > t0 ? (t1 - t0 + kStep - 1) / kStep : 0;
+  const int64_t head_k = static_cast<int64_t>(hk) * a.c.head_bytes;
+  const int64_t head_v = static_cast<int64_t>(hk + a.c.Hkv) * a.c.head_bytes;
+  const auto page_of = [&](int tok) {          // page number of a block's tokens, -1 past the end
+    if (tok >= t1) return -1;
+    const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
+    return __ldg(pages + static_cast<uint32_t>((blk * a.page_magic) >> 40));
+  };
+  int next[G::TB];                             // pages of the step after the one last requested
+  const auto look = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < G::TB; ++i)
+      next[i] = s < steps ? page_of(t0 + s * kStep + 16 * i) : -1;
+  };
+  uint32_t absent = 0;                         // bit (stage, block): nothing was requested
+  const auto request = [&](int s, int stage) {
+#pragma unroll
+    for (int i = 0; i < G::TB; ++i) {
+      const int tok = t0 + s * kStep + 16 * i;
+      const int page = next[i];
+      const bool in = s < steps && tok < t1;
+      const bool ok = in && page >= 0 && page < a.c.pages;
+      const uint32_t bit = 1u << (stage * G::TB + i);
+      absent = ok ? absent & ~bit : absent | bit;
+      if (in && !ok && lane == 0) atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
+      if (ok) {
+        const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
+        const uint32_t in_page =
+            blk - static_cast<uint32_t>((blk * a.page_magic) >> 40) * a.page_blocks;
+        const uint8_t* base = a.c.data + page * a.c.page_bytes;
+        uint8_t* dst = ring + stage * G::kStage + i * G::kBlock;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint8_t* src = base + (kv ? head_v : head_k);
+          const uint8_t* codes = src + in_page * G::kCodes;
+#pragma unroll
+          for (int c = 0; c < G::RB / 32; ++c) {
+            const int chunk16 = c * 32 + lane;
+            const int row = chunk16 / (G::RB / 16), at = chunk16 % (G::RB / 16);
+            const int u = kv ? G::value_unit(row, at >> 1) : G::key_unit(row, at >> 1);
+            cp_async16(dst + kv * G::kCodes + row * G::RB + u * 32 + (at & 1) * 16,
+                       codes + chunk16 * 16);
+          }
+          if (lane < G::kWords / 16)
+            cp_async16(dst + 2 * G::kCodes + kv * G::kWords + lane * 16,
+                       src + a.c.code_bytes + in_page * G::kWords + lane * 16);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  look(warp);
+#pragma unroll
+  for (int s = 0; s < G::kStages - 1; ++s) {
+    request(warp + s * kWarps, s);
+    look(warp + (s + 1) * kWarps);
+  }
+  int stage = 0;
+  for (int s = warp; s < steps; s += kWarps) {
+    {
+      const int free = stage == 0 ? G::kStages - 1 : stage - 1;
+      request(s + (G::kStages - 1) * kWarps, free);
+      look(s + G::kStages * kWarps);
+    }
+    cp_async_wait<G::kStages - 1>();
+    __syncwarp();
+    const int tok0 = t0 + s * kStep;
+    const uint32_t gone = absent >> (stage * G::TB) & ((1u << G::TB) - 1);
+    int top[G::TB];
+#pragma unroll
+    for (int i = 0; i < G::TB; ++i) top[i] = gone >> i & 1 ? 0 : t1;
+    const uint8_t* st = ring + stage * G::kStage;
+    if (tok0 + kStep <= low && gone == 0)
+      w.template step<false>(st, tok0, top, lane);
+    else
+      w.template step<true>(st, tok0, top, lane);
+    __syncwarp();                              // the stage may be overwritten
+    stage = stage == G::kStages - 1 ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+  __syncthreads();                             // the ring becomes the join's buffer
+
+  // ---- join the warps
+  constexpr int kRow = D + 4;
+  float* so = reinterpret_cast<float*>(smem);
+  float2* sml = reinterpret_cast<float2*>(smem + SplitSmem<D, BITS, NT>::kBytes - kWarps * 8 * NT * 8);
+  const float grow = 1.f / w.f;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = 8 * n + 2 * t + c;
+      const float l = sum_over_rows8(w.l[n][c]);
+      if (g == 0) sml[warp * 8 * NT + r] = make_float2(w.m[n][c], l);
+#pragma unroll
+      for (int j = 0; j < G::J; ++j) {
+        const float ob = sum_over_rows8(w.ob[n][j][c]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float odd = BITS == 4 ? grow * 0.0625f : grow;
+          *reinterpret_cast<float2*>(so + (warp * 8 * NT + r) * kRow + 64 * j + 8 * g + 2 * u) =
+              make_float2(fmaf(w.o[n][j][u][c], grow, ob), fmaf(w.o[n][j][u][2 + c], odd, ob));
+        }
+      }
+    }
+  }
   __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  if (top == -INFINITY) top = 0.f;
-  for (int w = 0; w < kWarps; ++w) sum += sl[w] * __expf(sm[w] - top);
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float y = 0.f;
-    for (int w = 0; w < kWarps; ++w) y += so[w][d] * __expf(sm[w] - top);
-    a.out[row * a.o_row + hq * a.o_head + d] =
-        static_cast<uint16_t>(pack_bf16(sum == 0.f ? 0.f : y / sum, 0.f));
+  const bool lone = a.pre_splits + a.own_splits == 1;
+  const int64_t heads = static_cast<int64_t>(a.B) * a.nq * a.Hq;
+  for (int i = threadIdx.x; i < 8 * NT * D / 4; i += kThreads) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    const int row = row0 + r;
+    if (row >= n_rows) break;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sml[k * 8 * NT + r].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const float2 ml = sml[k * 8 * NT + r];
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;
+      const float keep = exp2_approx(ml.x - ref);
+      const float4 v = *reinterpret_cast<const float4*>(so + (k * 8 * NT + r) * kRow + d);
+      l = fmaf(ml.y, keep, l);
+      y.x = fmaf(v.x, keep, y.x);
+      y.y = fmaf(v.y, keep, y.y);
+      y.z = fmaf(v.z, keep, y.z);
+      y.w = fmaf(v.w, keep, y.w);
+    }
+    const int qrow = pre ? row / a.G : b * a.nq + row / a.G;
+    const int head = hk * a.G + row % a.G;
+    if (lone) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      *reinterpret_cast<uint2*>(a.out + qrow * a.o_row + head * a.o_head + d) =
+          make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+    } else {
+      const int64_t at = (pre ? split : a.pre_splits + split) * heads +
+                         static_cast<int64_t>(qrow) * a.Hq + head;
+      *reinterpret_cast<float4*>(a.part + at * D + d) = y;
+      if (d == 0) a.ml[at] = make_float2(top, l);
+    }
   }
 }
 
+// Joins the splits of one query row and head: one block each, its warps share the
+// splits, then the block adds up.
 template <int D>
-cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
-  const dim3 grid(a.B * a.nq, a.Hq);
-  if (a.c.bits == 8)
-    attn_row_kernel<D, 8><<<grid, kWarps * 32, 0, s>>>(a);
-  else
-    attn_row_kernel<D, 4><<<grid, kWarps * 32, 0, s>>>(a);
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
+  griddep_wait();
+  constexpr int E = D / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t heads = static_cast<int64_t>(a.B) * a.nq * a.Hq;
+  const int64_t at = blockIdx.x;
+  const int row = static_cast<int>(at / a.Hq), head = static_cast<int>(at % a.Hq);
+  const int len = context_len(a, row / a.nq, false);
+  const int splits = a.pre_splits + (a.own_splits ? (len + a.own_chunk - 1) / a.own_chunk : 0);
+  float m = -INFINITY, l = 0.f, o[E] = {};
+  for (int s = warp; s < splits; s += kWarps) {
+    const float2 ml = a.ml[s * heads + at];
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;
+    const float* p = a.part + (s * heads + at) * D + lane * E;
+    const float top = fmaxf(m, ml.x);
+    const float keep = m == top ? 1.f : exp2_approx(m - top);
+    const float add = exp2_approx(ml.x - top);
+    m = top;
+    l = fmaf(l, keep, ml.y * add);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], keep, p[e] * add);
+  }
+  __shared__ float2 sml[kWarps];
+  __shared__ float so[kWarps][D];
+  if (lane == 0) sml[warp] = make_float2(m, l);
+#pragma unroll
+  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+  __syncthreads();
+  float top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sml[k].x);
+  const float ref = top == -INFINITY ? 0.f : top;
+  for (int d = 2 * threadIdx.x; d < D; d += 2 * kThreads) {
+    float sum = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      if (sml[k].x == -INFINITY && sml[k].y == 0.f) continue;
+      const float keep = exp2_approx(sml[k].x - ref);
+      sum = fmaf(sml[k].y, keep, sum);
+      y0 = fmaf(so[k][d], keep, y0);
+      y1 = fmaf(so[k][d + 1], keep, y1);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint32_t*>(a.out + row * a.o_row + head * a.o_head + d) =
+        pack_bf16(y0 * inv, y1 * inv);
+  }
+}
+
+// How a call is cut into blocks.
+struct Plan {
+  int nt;                    // row tiles of 8 nt
+  int pre_chunk, pre_splits, pre_tiles;
+  int own_chunk, own_splits, own_tiles;
+  size_t part, ml, total;    // workspace offsets and size
+};
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// Splits of a context of `len` tokens that `units` blocks share out: enough for
+// several blocks per multiprocessor, each of at least 256 tokens.
+int chunk_of(int64_t len, int64_t units) {
+  constexpr int64_t kBlocks = 152 * 8;
+  const int64_t splits = std::max<int64_t>(1, kBlocks / std::max<int64_t>(1, units));
+  const int64_t c = std::max<int64_t>(256, (len + splits - 1) / splits);
+  return static_cast<int>((std::min<int64_t>(c, std::max<int64_t>(len, 1)) + 127) / 128 * 128);
+}
+
+Plan make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_len, int prefix_len) {
+  Plan p{};
+  const int64_t G = Hq / Hkv;
+  // two column tiles share the conversion of the codes; at D = 256 their state
+  // would not fit the registers
+  p.nt = D <= 128 && (nq * G > 8 || (prefix_len > 0 && B * nq * G > 8)) ? 2 : 1;
+  p.own_tiles = ceil_div(nq * G, 8 * p.nt);
+  p.pre_tiles = ceil_div(B * nq * G, 8 * p.nt);
+  if (max_len > 0 || prefix_len == 0) {
+    p.own_chunk = chunk_of(max_len, B * Hkv * p.own_tiles);
+    p.own_splits = std::max(1, ceil_div(max_len, p.own_chunk));
+  }
+  if (prefix_len > 0) {
+    p.pre_chunk = chunk_of(prefix_len, Hkv * p.pre_tiles);
+    p.pre_splits = ceil_div(prefix_len, p.pre_chunk);
+  }
+  const size_t splits = p.pre_splits + p.own_splits;
+  const size_t heads = static_cast<size_t>(B * nq * Hq);
+  if (splits > 1) {
+    p.ml = (splits * heads * D * 4 + 255) / 256 * 256;
+    p.total = p.ml + splits * heads * 8;
+  }
+  p.total = std::max<size_t>(256, (p.total + 255) / 256 * 256);
+  return p;
+}
+
+template <int D, int BITS, int NT>
+cudaError_t launch_split(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
+  constexpr size_t smem = SplitSmem<D, BITS, NT>::kBytes;
+  const auto kernel = attn_split_kernel<D, BITS, NT>;
+  // (a per-device attribute; setting it again costs well under a microsecond)
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kernel<<<blocks, kThreads, smem, s>>>(a);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, int nt, unsigned blocks, cudaStream_t s) {
+  cudaError_t e;
+  if constexpr (D <= 128) {
+    if (nt == 2)
+      e = a.c.bits == 8 ? launch_split<D, 8, 2>(a, blocks, s) : launch_split<D, 4, 2>(a, blocks, s);
+    else
+      e = a.c.bits == 8 ? launch_split<D, 8, 1>(a, blocks, s) : launch_split<D, 4, 1>(a, blocks, s);
+  } else {
+    e = a.c.bits == 8 ? launch_split<D, 8, 1>(a, blocks, s) : launch_split<D, 4, 1>(a, blocks, s);
+  }
+  if (e != cudaSuccess || a.pre_splits + a.own_splits == 1) return e;
+  return launch_pdl(attn_join_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.nq * a.Hq),
+                    dim3(kThreads), 0, s, a);
 }
 
 bool rows_disjoint(int64_t row, int64_t head, int64_t T, int64_t H, int64_t D) {
@@ -128,8 +814,10 @@ bool bad4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 extern "C" size_t moe_kv_attention_workspace_size(int32_t B, int32_t nq, int32_t Hq, int32_t Hkv,
                                                   int32_t D, int32_t max_len, int32_t prefix_len) {
-  (void)B, (void)nq, (void)Hq, (void)Hkv, (void)D, (void)max_len, (void)prefix_len;
-  return 256;
+  if (B < 0 || nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256) ||
+      max_len < 0 || prefix_len < 0)
+    return 0;
+  return moeq4::make_plan(B, nq, Hq, Hkv, D, max_len, prefix_len).total;
 }
 
 extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache* c, void* ws,
@@ -140,7 +828,7 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
     return MOE_ERR_ARG;
   moe_status st = check_kv_cache(c);
   if (st != MOE_OK) return st;
-  if (a->Hq % c->Hkv || a->Hq > 65535 || static_cast<int64_t>(a->B) * a->nq > (1 << 24))
+  if (a->Hq % c->Hkv || a->Hq > 65535 || a->max_len > (1 << 30) || a->prefix_len > (1 << 30) || static_cast<int64_t>(a->B) * a->nq > (1 << 24))
     return MOE_ERR_SHAPE;
   if (a->B == 0) return MOE_OK;
   const int64_t pages = (static_cast<int64_t>(a->max_len) + c->page_size - 1) / c->page_size;
@@ -154,9 +842,12 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
   if (bad16(a->q) || bad16(a->out) || bad16(ws) || bad4(a->lens) || bad4(a->table) ||
       bad4(a->prefix_table) || a->q_row % 8 || a->q_head % 8 || a->out_row % 8 || a->out_head % 8)
     return MOE_ERR_ALIGN;
-  if (ws_bytes < moe_kv_attention_workspace_size(a->B, a->nq, a->Hq, c->Hkv, c->D, a->max_len,
-                                                 a->prefix_len))
-    return MOE_ERR_WORKSPACE;
+  const Plan p = make_plan(a->B, a->nq, a->Hq, c->Hkv, c->D, a->max_len, a->prefix_len);
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+  const int64_t blocks = static_cast<int64_t>(p.pre_splits) * c->Hkv * p.pre_tiles +
+                         static_cast<int64_t>(p.own_splits) * a->B * c->Hkv * p.own_tiles;
+  if (blocks > 0x7FFFFFFF || static_cast<int64_t>(a->B) * a->nq * a->Hq > 0x7FFFFFFF)
+    return MOE_ERR_SHAPE;
   AttnArgs k{};
   k.q = a->q;
   k.out = a->out;
@@ -174,11 +865,23 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
   k.max_len = a->max_len;
   k.prefix_len = a->prefix_len;
   k.G = a->Hq / c->Hkv;
-  k.scale = a->scale;
+  k.scale2 = a->scale * 1.44269504088896340736f;
   k.c = kv_cache_args(*c);
+  k.page_blocks = static_cast<uint32_t>(c->page_size / 16);
+  k.page_magic = (1ull << 40) / k.page_blocks + 1;
+  k.pre_chunk = p.pre_chunk;
+  k.pre_splits = p.pre_splits;
+  k.pre_tiles = p.pre_tiles;
+  k.pre_blocks = p.pre_splits * c->Hkv * p.pre_tiles;
+  k.own_chunk = p.own_chunk;
+  k.own_splits = p.own_splits;
+  k.own_tiles = p.own_tiles;
+  k.part = static_cast<float*>(ws);
+  k.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = c->D == 64    ? launch_rows<64>(k, s)
-                        : c->D == 128 ? launch_rows<128>(k, s)
-                                      : launch_rows<256>(k, s);
+  const unsigned n = static_cast<unsigned>(blocks);
+  const cudaError_t e = c->D == 64    ? launch<64>(k, p.nt, n, s)
+                        : c->D == 128 ? launch<128>(k, p.nt, n, s)
+                                      : launch<256>(k, p.nt, n, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

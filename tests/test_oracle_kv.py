@@ -209,7 +209,8 @@ def test_attention_arguments_rejected_on_host(L):
                dict(prefix_len=-1), dict(scale=float("inf")), dict(table_stride=-1)):
         assert call(**kw) == -1, kw
     for kw in (dict(Hq=3), dict(table_stride=6), dict(q_row=-512), dict(out_row=128),
-               dict(out_head=64), dict(B=1 << 30)):
+               dict(out_head=64), dict(B=1 << 30), dict(prefix_len=(1 << 30) + 1),
+               dict(max_len=(1 << 30) + 1, table_stride=1 << 30)):
         assert call(**kw) == -2, kw
     for kw in (dict(q=FAKE + 8), dict(out=FAKE + 2), dict(ws=FAKE + 4), dict(lens=FAKE + 1),
                dict(table=FAKE + 2), dict(prefix_table=FAKE + 2), dict(q_row=513), dict(out_head=129,
