@@ -387,6 +387,8 @@ std::atomic<int> g_nevents{0};
 
 }  // namespace
 
+uint64_t wait_timeout_ns() { return timeout_ns(); }
+
 void stage_mark(int i, cudaStream_t s) {
   if (g_nevents.load(std::memory_order_relaxed) == 0) return;   // the common case: no timing requested
   std::lock_guard<std::mutex> g(g_ev_mu);

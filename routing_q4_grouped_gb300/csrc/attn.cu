@@ -23,10 +23,10 @@
 //    neighbouring codes of a token at once; P is transposed between the two
 //    products by one 8x8 register transpose per 8 tokens and group.
 // q' and p s are fp16: q' is the query divided by the power of two under its
-// row's largest element, p s is divided by a running power of two not far from
-// the largest scale seen, so neither leaves fp16's range and both keep 11 bits
-// (one rounding of 2^-11 for the weights; bf16 queries are exact above 2^-16 of
-// their row's largest element). Logits, maxima, sums and outputs are fp32.
+// row's largest element, p s is multiplied by a factor f of the row that keeps its
+// largest p s near 1, so neither leaves fp16's range and both keep 11 bits (one
+// rounding of 2^-11 for the weights; bf16 queries are exact above 2^-16 of their
+// row's largest element). Logits, maxima, sums and outputs are fp32.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -34,9 +34,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "attn.cuh"
 #include "internal.h"
-#include "kv.cuh"
-#include "ptx.cuh"
 
 namespace moeq4 {
 namespace {
@@ -44,31 +43,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-
-struct AttnArgs {
-  const uint16_t* q;
-  uint16_t* out;
-  int64_t q_row, q_head, o_row, o_head;
-  const int32_t *table, *lens, *prefix_table;
-  int B, nq, Hq, table_stride, max_len, prefix_len, G;
-  float scale2;              // scale * log2(e)
-  KvCache c;
-  uint32_t page_blocks;      // 16-token blocks per page
-  uint64_t page_magic;       // floor(2^40 / page_blocks) + 1
-  // work: blocks [0, pre_blocks) take the prefix, the rest the requests' own tokens
-  int pre_chunk, pre_splits, pre_tiles, pre_blocks;
-  int own_chunk, own_splits, own_tiles;
-  float* part;               // [split][row][head][D]; prefix splits first
-  float2* ml;                // [split][row][head]: (m, l)
-};
-
-// A context length as the kernels use it.
-__device__ __forceinline__ int context_len(const AttnArgs& a, int b, bool report) {
-  const int n = a.lens[b];
-  if (n >= 0 && n <= a.max_len) return n;
-  if (report) atomicOr(a.c.err, MOE_DEVERR_BAD_LENGTH);
-  return n < 0 ? 0 : a.max_len;
-}
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
@@ -95,23 +69,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
-  return d;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
@@ -171,7 +128,8 @@ struct Warp {
   float m[NT][2], l[NT][2];
   float o[NT][G::J][4][4];        // O^T: group, tile of 16 elements
   float ob[NT][G::J][2];          // sum of p * centred bias
-  float f;                        // 2^-e: p s f is near or below 1
+  float e[NT][2], f[NT][2];       // f = 2^-e: p s f stays below 2^15
+  float top_x[NT][2], top_ps[NT][2];   // m + 8, m + e + 14: the bounds of a logit and of log2(p s) + m
 
   // Columns 2t, 2t+1 of this thread (queries); rows lane/4 and lane/4 + 8 (tokens).
   template <bool MASK>
@@ -247,18 +205,24 @@ struct Warp {
           }
       }
     }
+    // A row's reference m is any value near its largest logit, so that weights may
+    // pass 1 by 2^8, and e any value near its largest log2(p s); both move only when
+    // a logit leaves these bounds.
     bool grow = false;
+    float es[G::TB][2];                       // exponent of a token's largest scale
 #pragma unroll
     for (int b = 0; b < G::TB; ++b) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int tok = tok0 + 16 * b + 8 * r + g;
         const bool any = !MASK || tok < top[b];
+        uint32_t big = 0;
 #pragma unroll
         for (int j = 0; j < G::J; ++j) {
           if (MASK && !any) vw[b][r][j] = 0;
-          grow |= fabsf(bf16_lo(vw[b][r][j])) * f >= 2.f;
+          big = max(big, vw[b][r][j] & 0x7FFFu);
         }
+        es[b][r] = static_cast<float>(static_cast<int>(big >> 7) - 127);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -266,12 +230,11 @@ struct Warp {
             float& v = x[b][n][2 * r + c];
             v *= row_scale[n][c];
             if (MASK && !(any && tok < lim[n][c])) v = -INFINITY;
-            // weights may pass 1 by 2^8 before the reference is moved
-            grow |= v > m[n][c] + 8.f;
+            grow |= v > top_x[n][c] || v + es[b][r] > top_ps[n][c];
           }
       }
     }
-    if (__any_sync(kAll, grow)) rescale(x, vw);
+    if (__any_sync(kAll, grow)) rescale(x, es);
     // weights
 #pragma unroll
     for (int b = 0; b < G::TB; ++b)
@@ -294,12 +257,11 @@ struct Warp {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float s = bf16_lo(vw[b][r][j]);
-          const float sf = s * f;
           const float bias = fmaf(BITS == 8 ? 128.f : 8.f, s, bf16_hi(vw[b][r][j]));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const float p0 = x[b][n][2 * r], p1 = x[b][n][2 * r + 1];
-            pb[n][r] = transpose8x8(pack_f16(p0 * sf, p1 * sf));
+            pb[n][r] = transpose8x8(pack_f16(p0 * (s * f[n][0]), p1 * (s * f[n][1])));
             if (MASK) {            // a bias may be NaN: no product with rows that do not see it
               if (p0 != 0.f) ob[n][j][0] = fmaf(p0, bias, ob[n][j][0]);
               if (p1 != 0.f) ob[n][j][1] = fmaf(p1, bias, ob[n][j][1]);
@@ -356,34 +318,38 @@ struct Warp {
     }
   }
 
-  // Moves the rows' reference m to their largest logit and the weights' power of
-  // two to the largest scale, and what has been summed up along with them.
+  // Moves the rows' m to their largest logit and e to their largest log2(p s), and
+  // what has been summed up along with them.
   __device__ __forceinline__ void rescale(const float (&x)[G::TB][NT][4],
-                                          const uint32_t (&vw)[G::TB][2][G::J]) {
-    uint32_t big = 0;
-#pragma unroll
-    for (int b = 0; b < G::TB; ++b)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int j = 0; j < G::J; ++j) big = max(big, vw[b][r][j] & 0x7FFFu);
-    const uint32_t e_new = min(max(__reduce_max_sync(kAll, big) >> 7, 1u), 252u);
-    const uint32_t e_old = 254u - (__float_as_uint(f) >> 23);
-    const uint32_t e = max(e_old, e_new);
-    const float fn = __uint_as_float((254u - e) << 23);
-    const float down = exp2_approx(static_cast<float>(e_old) - static_cast<float>(e));
-    f = fn;
+                                          const float (&es)[G::TB][2]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float keep[2];
+      float keep[2], down[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float mx = m[n][c];
+        float mx = -INFINITY, ux = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < G::TB; ++b) mx = fmaxf(mx, fmaxf(x[b][n][c], x[b][n][2 + c]));
+        for (int b = 0; b < G::TB; ++b)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            mx = fmaxf(mx, x[b][n][2 * r + c]);
+            ux = fmaxf(ux, x[b][n][2 * r + c] + es[b][r]);
+          }
         mx = max_over_rows8(mx);
-        keep[c] = mx == m[n][c] ? 1.f : exp2_approx(m[n][c] - mx);
-        m[n][c] = mx;
+        ux = max_over_rows8(ux);
+        keep[c] = down[c] = 1.f;
+        if (mx == -INFINITY) continue;          // nothing seen yet
+        const bool first = m[n][c] == -INFINITY;
+        const float mn = fmaxf(m[n][c], mx);
+        const float en = first ? ux - mn : fmaxf(e[n][c], ux - mn);
+        keep[c] = mn == m[n][c] ? 1.f : exp2_approx(m[n][c] - mn);
+        const float fn = exp2_approx(-en);
+        down[c] = first ? 0.f : keep[c] * (fn / f[n][c]);
+        m[n][c] = mn;
+        e[n][c] = en;
+        f[n][c] = fn;
+        top_x[n][c] = mn + 8.f;
+        top_ps[n][c] = mn + en + 14.f;
         l[n][c] *= keep[c];
       }
 #pragma unroll
@@ -393,7 +359,7 @@ struct Warp {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[n][j][u][i] *= keep[i & 1] * down;
+          for (int i = 0; i < 4; ++i) o[n][j][u][i] *= down[i & 1];
       }
     }
   }
@@ -440,14 +406,14 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
   const int row0 = tile * 8 * NT;
   // the tile's last row sees most
   const auto limit = [&](int r) {
-    return pre ? ctx : max(0, ctx - a.nq + 1 + r / a.G);
+    return pre ? ctx : own_limit(a, ctx, r);
   };
-  if (t0 >= ctx && !(split == 0 && a.pre_splits == 0)) return;   // split 0 of a lone context writes zeros
+  const bool lone = a.pre_parts + a.own_parts == 1;
+  if (t0 >= ctx && !lone) return;              // (a lone split of nothing writes zeros)
   const int t1 = min(min(t0 + chunk, ctx), limit(min(row0 + 8 * NT, n_rows) - 1));
 
   // ---- queries
   Warp<D, BITS, NT> w;
-  w.f = __uint_as_float(253u << 23);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = row0 + 8 * n + g;
@@ -520,6 +486,9 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
       w.lim[n][c] = rc < n_rows ? limit(rc) : t1;
       w.m[n][c] = -INFINITY;
       w.l[n][c] = 0.f;
+      w.e[n][c] = 0.f;
+      w.f[n][c] = 1.f;
+      w.top_x[n][c] = w.top_ps[n][c] = -INFINITY;
     }
   }
   int low = t1;                                // tokens that every row of the tile sees
@@ -616,28 +585,27 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
   constexpr int kRow = D + 4;
   float* so = reinterpret_cast<float*>(smem);
   float2* sml = reinterpret_cast<float2*>(smem + SplitSmem<D, BITS, NT>::kBytes - kWarps * 8 * NT * 8);
-  const float grow = 1.f / w.f;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int r = 8 * n + 2 * t + c;
       const float l = sum_over_rows8(w.l[n][c]);
+      const float up = 1.f / w.f[n][c];
       if (g == 0) sml[warp * 8 * NT + r] = make_float2(w.m[n][c], l);
 #pragma unroll
       for (int j = 0; j < G::J; ++j) {
         const float ob = sum_over_rows8(w.ob[n][j][c]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float odd = BITS == 4 ? grow * 0.0625f : grow;
+          const float odd = BITS == 4 ? up * 0.0625f : up;
           *reinterpret_cast<float2*>(so + (warp * 8 * NT + r) * kRow + 64 * j + 8 * g + 2 * u) =
-              make_float2(fmaf(w.o[n][j][u][c], grow, ob), fmaf(w.o[n][j][u][2 + c], odd, ob));
+              make_float2(fmaf(w.o[n][j][u][c], up, ob), fmaf(w.o[n][j][u][2 + c], odd, ob));
         }
       }
     }
   }
   __syncthreads();
-  const bool lone = a.pre_splits + a.own_splits == 1;
   const int64_t heads = static_cast<int64_t>(a.B) * a.nq * a.Hq;
   for (int i = threadIdx.x; i < 8 * NT * D / 4; i += kThreads) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -668,7 +636,7 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
       *reinterpret_cast<uint2*>(a.out + qrow * a.o_row + head * a.o_head + d) =
           make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
     } else {
-      const int64_t at = (pre ? split : a.pre_splits + split) * heads +
+      const int64_t at = (pre ? split : a.pre_parts + split) * heads +
                          static_cast<int64_t>(qrow) * a.Hq + head;
       *reinterpret_cast<float4*>(a.part + at * D + d) = y;
       if (d == 0) a.ml[at] = make_float2(top, l);
@@ -676,100 +644,182 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
   }
 }
 
-// Joins the splits of one query row and head: one block each, its warps share the
-// splits, then the block adds up.
-template <int D>
+// Parts that the row kernel made of a unit of T tiles, the first of which is tile
+// g of all: one per block that has a share of it.
+__device__ __forceinline__ int unit_parts(const AttnArgs& a, int64_t g, int T) {
+  return T > 0 ? static_cast<int>((g + T - 1) / a.share - g / a.share) + 1 : 0;
+}
+
+// Joins the parts of a query row and head: W warps each, which share the parts.
+template <int D, int W>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
   griddep_wait();
   constexpr int E = D / 32;
+  constexpr int kRows = kWarps / W;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t heads = static_cast<int64_t>(a.B) * a.nq * a.Hq;
-  const int64_t at = blockIdx.x;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * kRows + warp / W;
+  if (at >= heads) return;                       // (W == kWarps: at is the block's)
   const int row = static_cast<int>(at / a.Hq), head = static_cast<int>(at % a.Hq);
-  const int len = context_len(a, row / a.nq, false);
-  const int splits = a.pre_splits + (a.own_splits ? (len + a.own_chunk - 1) / a.own_chunk : 0);
+  const int hk = head / a.G, b = row / a.nq;
+  int n_pre = a.pre_parts, n_own = 0;
+  if (a.pre_units) {
+    const int u = hk * a.pre_row_tiles + (row * a.G + head % a.G) / a.unit_rows;
+    n_pre = unit_parts(a, static_cast<int64_t>(u) * a.pre_T, a.pre_T);
+  }
+  if (a.own_parts) {
+    const int len = context_len(a, b, false);
+    if (a.own_units) {
+      const int n_rows = a.nq * a.G;
+      const int rt = (row % a.nq * a.G + head % a.G) / a.unit_rows;
+      const int u = (b * a.c.Hkv + hk) * a.own_row_tiles + unit_place(rt, a.own_row_tiles);
+      const int seen = own_limit(a, len, min((rt + 1) * a.unit_rows, n_rows) - 1);
+      n_own = unit_parts(a, static_cast<int64_t>(a.pre_units) * a.pre_T +
+                                static_cast<int64_t>(u) * a.own_T,
+                         (seen + kRowTile - 1) / kRowTile);
+      if (a.pre_parts == 0 && n_own == 1) return;   // the row kernel wrote the output
+    } else {
+      n_own = (len + a.own_chunk - 1) / a.own_chunk;
+    }
+  } else if (a.pre_units && n_pre == 1) {
+    return;
+  }
   float m = -INFINITY, l = 0.f, o[E] = {};
-  for (int s = warp; s < splits; s += kWarps) {
-    const float2 ml = a.ml[s * heads + at];
+#pragma unroll 4
+  for (int s = warp % W; s < n_pre + n_own; s += W) {
+    const int64_t i = (s < n_pre ? s : a.pre_parts + s - n_pre) * heads + at;
+    const float2 ml = a.ml[i];
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(a.part + i * D + lane * E + e);
+      v[e] = x.x, v[e + 1] = x.y;
+    }
     if (ml.x == -INFINITY && ml.y == 0.f) continue;
-    const float* p = a.part + (s * heads + at) * D + lane * E;
     const float top = fmaxf(m, ml.x);
     const float keep = m == top ? 1.f : exp2_approx(m - top);
-    const float add = exp2_approx(ml.x - top);
+    const float add = exp2_approx(ml.x - (top == -INFINITY ? 0.f : top));
     m = top;
     l = fmaf(l, keep, ml.y * add);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], keep, p[e] * add);
+    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], keep, v[e] * add);
   }
-  __shared__ float2 sml[kWarps];
-  __shared__ float so[kWarps][D];
-  if (lane == 0) sml[warp] = make_float2(m, l);
+  if constexpr (W > 1) {
+    __shared__ float2 sml[kWarps];
+    __shared__ float so[kWarps][D];
+    if (lane == 0) sml[warp] = make_float2(m, l);
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-  __syncthreads();
-  float top = -INFINITY;
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+    __syncthreads();
+    if (warp) return;
+    float top = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sml[k].x);
-  const float ref = top == -INFINITY ? 0.f : top;
-  for (int d = 2 * threadIdx.x; d < D; d += 2 * kThreads) {
-    float sum = 0.f, y0 = 0.f, y1 = 0.f;
+    for (int k = 0; k < W; ++k) top = fmaxf(top, sml[k].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    l = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
       if (sml[k].x == -INFINITY && sml[k].y == 0.f) continue;
       const float keep = exp2_approx(sml[k].x - ref);
-      sum = fmaf(sml[k].y, keep, sum);
-      y0 = fmaf(so[k][d], keep, y0);
-      y1 = fmaf(so[k][d + 1], keep, y1);
+      l = fmaf(sml[k].y, keep, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(so[k][lane * E + e], keep, o[e]);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint32_t*>(a.out + row * a.o_row + head * a.o_head + d) =
-        pack_bf16(y0 * inv, y1 * inv);
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(a.out + row * a.o_row + head * a.o_head + lane * E + e) =
+        pack_bf16(o[e] * inv, o[e + 1] * inv);
 }
 
 // How a call is cut into blocks.
 struct Plan {
-  int nt;                    // row tiles of 8 nt
-  int pre_chunk, pre_splits, pre_tiles;
-  int own_chunk, own_splits, own_tiles;
-  size_t part, ml, total;    // workspace offsets and size
+  int nt;                    // split kernel: row tiles of 8 nt
+  AttnArgs a;                // chunks, splits, units, shares and parts
+  unsigned split_blocks, row_blocks;
+  size_t ml, total;          // workspace: offset of the (m, l) pairs, size
 };
 
-int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+constexpr int kSMs = 152;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Splits of a context of `len` tokens that `units` blocks share out: enough for
 // several blocks per multiprocessor, each of at least 256 tokens.
 int chunk_of(int64_t len, int64_t units) {
-  constexpr int64_t kBlocks = 152 * 8;
+  constexpr int64_t kBlocks = kSMs * 8;
   const int64_t splits = std::max<int64_t>(1, kBlocks / std::max<int64_t>(1, units));
   const int64_t c = std::max<int64_t>(256, (len + splits - 1) / splits);
   return static_cast<int>((std::min<int64_t>(c, std::max<int64_t>(len, 1)) + 127) / 128 * 128);
 }
 
-Plan make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_len, int prefix_len) {
+// Query rows of a key/value head from which the row kernel is taken.
+constexpr int64_t kRowKernelRows = 64;
+
+bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_len, int prefix_len,
+               Plan* out) {
   Plan p{};
+  AttnArgs& a = p.a;
   const int64_t G = Hq / Hkv;
+  const int64_t own_rows = nq * G, pre_rows = B * nq * G;
+  const bool pre = prefix_len > 0, own = max_len > 0 || !pre;
+  const bool pre_tc = pre && pre_rows >= kRowKernelRows;
+  const bool own_tc = max_len > 0 && own_rows >= kRowKernelRows;
   // two column tiles share the conversion of the codes; at D = 256 their state
   // would not fit the registers
-  p.nt = D <= 128 && (nq * G > 8 || (prefix_len > 0 && B * nq * G > 8)) ? 2 : 1;
-  p.own_tiles = ceil_div(nq * G, 8 * p.nt);
-  p.pre_tiles = ceil_div(B * nq * G, 8 * p.nt);
-  if (max_len > 0 || prefix_len == 0) {
-    p.own_chunk = chunk_of(max_len, B * Hkv * p.own_tiles);
-    p.own_splits = std::max(1, ceil_div(max_len, p.own_chunk));
+  p.nt = D <= 128 && ((own && !own_tc && own_rows > 8) || (pre && !pre_tc && pre_rows > 8)) ? 2 : 1;
+  int64_t split_blocks = 0, tiles = 0;
+  a.unit_rows = attn_unit_rows(D);
+  if (pre_tc) {
+    a.pre_row_tiles = static_cast<int>(ceil_div(pre_rows, a.unit_rows));
+    a.pre_T = static_cast<int>(ceil_div(prefix_len, kRowTile));
+    const int64_t units = Hkv * a.pre_row_tiles;
+    tiles += units * a.pre_T;
+    if (units > 0x7FFFFFFF) return false;
+    a.pre_units = static_cast<int>(units);
+  } else if (pre) {
+    a.pre_tiles = static_cast<int>(ceil_div(pre_rows, 8 * p.nt));
+    a.pre_chunk = chunk_of(prefix_len, Hkv * a.pre_tiles);
+    a.pre_splits = a.pre_parts = static_cast<int>(ceil_div(prefix_len, a.pre_chunk));
+    split_blocks += Hkv * a.pre_tiles * a.pre_splits;
+    if (split_blocks > 0x7FFFFFFF) return false;
+    a.pre_blocks = static_cast<int>(split_blocks);
   }
-  if (prefix_len > 0) {
-    p.pre_chunk = chunk_of(prefix_len, Hkv * p.pre_tiles);
-    p.pre_splits = ceil_div(prefix_len, p.pre_chunk);
+  if (own_tc) {
+    a.own_row_tiles = static_cast<int>(ceil_div(own_rows, a.unit_rows));
+    a.own_T = static_cast<int>(ceil_div(max_len, kRowTile));
+    const int64_t units = B * Hkv * a.own_row_tiles;
+    tiles += units * a.own_T;
+    if (units > 0x7FFFFFFF) return false;
+    a.own_units = static_cast<int>(units);
+  } else if (own) {
+    a.own_tiles = static_cast<int>(ceil_div(own_rows, 8 * p.nt));
+    a.own_chunk = chunk_of(max_len, B * Hkv * a.own_tiles);
+    a.own_splits = a.own_parts = static_cast<int>(std::max<int64_t>(1, ceil_div(max_len, a.own_chunk)));
+    split_blocks += B * Hkv * a.own_tiles * a.own_splits;
   }
-  const size_t splits = p.pre_splits + p.own_splits;
+  if (split_blocks > 0x7FFFFFFF) return false;
+  p.split_blocks = static_cast<unsigned>(split_blocks);
+  if (tiles > 0) {
+    const int64_t share = std::max<int64_t>(2, ceil_div(tiles, kSMs));
+    if (share > 0x7FFFFFFF) return false;
+    a.share = static_cast<int>(share);
+    p.row_blocks = static_cast<unsigned>(ceil_div(tiles, share));
+    if (a.pre_units) a.pre_parts = static_cast<int>((a.pre_T - 1) / share + 2);
+    if (a.own_units) a.own_parts = static_cast<int>((a.own_T - 1) / share + 2);
+  }
+  const size_t parts = static_cast<size_t>(a.pre_parts) + a.own_parts;
   const size_t heads = static_cast<size_t>(B * nq * Hq);
-  if (splits > 1) {
-    p.ml = (splits * heads * D * 4 + 255) / 256 * 256;
-    p.total = p.ml + splits * heads * 8;
+  if (parts > 1) {
+    p.ml = (parts * heads * D * 4 + 255) / 256 * 256;
+    p.total = p.ml + parts * heads * 8;
   }
   p.total = std::max<size_t>(256, (p.total + 255) / 256 * 256);
-  return p;
+  *out = p;
+  return true;
 }
 
 template <int D, int BITS, int NT>
@@ -785,18 +835,28 @@ cudaError_t launch_split(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t launch(const AttnArgs& a, int nt, unsigned blocks, cudaStream_t s) {
-  cudaError_t e;
-  if constexpr (D <= 128) {
-    if (nt == 2)
-      e = a.c.bits == 8 ? launch_split<D, 8, 2>(a, blocks, s) : launch_split<D, 4, 2>(a, blocks, s);
-    else
-      e = a.c.bits == 8 ? launch_split<D, 8, 1>(a, blocks, s) : launch_split<D, 4, 1>(a, blocks, s);
-  } else {
-    e = a.c.bits == 8 ? launch_split<D, 8, 1>(a, blocks, s) : launch_split<D, 4, 1>(a, blocks, s);
+cudaError_t launch(const AttnArgs& a, const Plan& p, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (p.row_blocks) e = launch_attn_rows(a, p.row_blocks, s);
+  if (e != cudaSuccess) return e;
+  if (p.split_blocks) {
+    if constexpr (D <= 128) {
+      if (p.nt == 2)
+        e = a.c.bits == 8 ? launch_split<D, 8, 2>(a, p.split_blocks, s)
+                          : launch_split<D, 4, 2>(a, p.split_blocks, s);
+    }
+    if (p.nt == 1)
+      e = a.c.bits == 8 ? launch_split<D, 8, 1>(a, p.split_blocks, s)
+                        : launch_split<D, 4, 1>(a, p.split_blocks, s);
   }
-  if (e != cudaSuccess || a.pre_splits + a.own_splits == 1) return e;
-  return launch_pdl(attn_join_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.nq * a.Hq),
+  const int parts = a.pre_parts + a.own_parts;
+  if (e != cudaSuccess || parts == 1) return e;
+  const int64_t heads = static_cast<int64_t>(a.B) * a.nq * a.Hq;
+  // many parts: a block's warps share a row's; few: a warp per row
+  if (parts > 8)
+    return launch_pdl(attn_join_kernel<D, kWarps>, dim3(static_cast<unsigned>(heads)),
+                      dim3(kThreads), 0, s, a);
+  return launch_pdl(attn_join_kernel<D, 1>, dim3(static_cast<unsigned>(ceil_div(heads, kWarps))),
                     dim3(kThreads), 0, s, a);
 }
 
@@ -817,7 +877,8 @@ extern "C" size_t moe_kv_attention_workspace_size(int32_t B, int32_t nq, int32_t
   if (B < 0 || nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256) ||
       max_len < 0 || prefix_len < 0)
     return 0;
-  return moeq4::make_plan(B, nq, Hq, Hkv, D, max_len, prefix_len).total;
+  moeq4::Plan p;
+  return moeq4::make_plan(B, nq, Hq, Hkv, D, max_len, prefix_len, &p) ? p.total : 0;
 }
 
 extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache* c, void* ws,
@@ -842,13 +903,12 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
   if (bad16(a->q) || bad16(a->out) || bad16(ws) || bad4(a->lens) || bad4(a->table) ||
       bad4(a->prefix_table) || a->q_row % 8 || a->q_head % 8 || a->out_row % 8 || a->out_head % 8)
     return MOE_ERR_ALIGN;
-  const Plan p = make_plan(a->B, a->nq, a->Hq, c->Hkv, c->D, a->max_len, a->prefix_len);
-  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
-  const int64_t blocks = static_cast<int64_t>(p.pre_splits) * c->Hkv * p.pre_tiles +
-                         static_cast<int64_t>(p.own_splits) * a->B * c->Hkv * p.own_tiles;
-  if (blocks > 0x7FFFFFFF || static_cast<int64_t>(a->B) * a->nq * a->Hq > 0x7FFFFFFF)
+  Plan p;
+  if (static_cast<int64_t>(a->B) * a->nq * a->Hq > 0x7FFFFFFF ||
+      !make_plan(a->B, a->nq, a->Hq, c->Hkv, c->D, a->max_len, a->prefix_len, &p))
     return MOE_ERR_SHAPE;
-  AttnArgs k{};
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+  AttnArgs& k = p.a;
   k.q = a->q;
   k.out = a->out;
   k.q_row = a->q_row;
@@ -869,19 +929,12 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
   k.c = kv_cache_args(*c);
   k.page_blocks = static_cast<uint32_t>(c->page_size / 16);
   k.page_magic = (1ull << 40) / k.page_blocks + 1;
-  k.pre_chunk = p.pre_chunk;
-  k.pre_splits = p.pre_splits;
-  k.pre_tiles = p.pre_tiles;
-  k.pre_blocks = p.pre_splits * c->Hkv * p.pre_tiles;
-  k.own_chunk = p.own_chunk;
-  k.own_splits = p.own_splits;
-  k.own_tiles = p.own_tiles;
   k.part = static_cast<float*>(ws);
   k.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml);
+  k.timeout_ns = wait_timeout_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned n = static_cast<unsigned>(blocks);
-  const cudaError_t e = c->D == 64    ? launch<64>(k, p.nt, n, s)
-                        : c->D == 128 ? launch<128>(k, p.nt, n, s)
-                                      : launch<256>(k, p.nt, n, s);
+  const cudaError_t e = c->D == 64    ? launch<64>(k, p, s)
+                        : c->D == 128 ? launch<128>(k, p, s)
+                                      : launch<256>(k, p, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -1,0 +1,948 @@
+// attn_rows.cu — attention for many query rows of one key/value head (a chunk of a
+// prompt, or a batch behind a shared prefix) on the 5th-generation tensor cores.
+//
+// With R rows a cached byte feeds 4 R operations, so from about a hundred rows on
+// the products bound the work, not the bytes. A unit is 256 query rows (128 for
+// D = 256) of one key/value head against a run of 128-token tiles:
+//   X[rows, tokens] = Q K^T     tcgen05.mma, M = 128 rows, N = 128 tokens, both in
+//                               shared memory (K-major, 128-byte swizzle)
+//   P = exp2(X - m)             tensor memory -> registers -> tensor memory, one
+//                               thread per row, fp16, in place of X
+//   O[rows, D] += P V           A = P from tensor memory, B = V^T in shared memory
+// Codes are turned into fp16 operands once per tile, for all rows of the unit: with
+// c exact from a byte (1024 + c) - 1024, value = s c + b is one fp16 fma, one
+// rounding of 2^-11.
+//
+// fp16's range. Queries are divided by the power of two under their row's largest
+// element. A tile's keys and values are divided by powers of two 2^eK and 2^eV near
+// their largest magnitude; eK goes into the logits' factor, and 2^eV into the
+// weights' exponent: P' = exp2(x - m + eV - E) with a running E per row, so P' stays
+// near 1 whatever the values' size. A tile whose tokens differ by more than 2^6 in
+// magnitude takes one exponent per token (the same formulas with a factor per
+// column), as does one with a NaN group or a page outside the cache.
+//
+// The row maximum is not looked for tile by tile: m is only a reference, any value
+// near the largest logit does. All P' are positive, so a row whose tile sums to less
+// than 2^15 held no weight near fp16's end and m stands; otherwise (and at a row's
+// first tile) the tile's logits are read again for their maximum, m moves there and
+// O and l follow. That leaves one fma, one exp2, one addition and half a conversion
+// per element.
+//
+// Warps (544 threads, one block per SM, persistent over its share of tiles):
+//   0-3, 4-7  softmax of query tile 0 and 1 (warp % 4 = tensor-memory lane quarter),
+//             their queries' load and their outputs' store
+//   8-15      codes to operands
+//   16        issues the products
+// D <= 128: two query tiles share each token tile and take turns, one in the tensor
+// cores while the other is in its softmax. D = 256: one query tile, whose logits
+// alternate between two slots. Every wait on an mbarrier has a time limit; after one
+// ran out, no thread waits again and the kernel ends with MOE_DEVERR_PIPE_TIMEOUT.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "attn.cuh"
+#include "internal.h"
+
+namespace moeq4 {
+namespace {
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kSoftWarps = 8;
+constexpr int kConvWarps = 8;
+constexpr int kConvThreads = kConvWarps * 32;
+constexpr int kMmaWarp = kSoftWarps + kConvWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kMetaRing = 4;
+constexpr int kMaxSpread = 6;          // exponents of a tile's tokens that share one power of two
+constexpr uint32_t kTmemCols = 512;
+constexpr uint8_t kDead = 0x80;        // token flag: its page is outside the cache
+
+template <int D>
+struct RowGeo {
+  static constexpr int J = D / kKvGroup;
+  static constexpr int QT = D == 256 ? 1 : 2;         // query tiles of a unit
+  static constexpr int KS = D == 256 ? 1 : 2;         // operand tiles in flight, keys and values each
+  static constexpr uint32_t kTileBytes = 128 * D * 2; // a query, key or value tile
+  static constexpr uint32_t kOffK = QT * kTileBytes;
+  static constexpr uint32_t kOffV = kOffK + KS * kTileBytes;
+  static constexpr uint32_t kOffMeta = kOffV + KS * kTileBytes;
+  static constexpr uint32_t kColO = 0;                // tensor memory: O of tile q at D q,
+  static constexpr uint32_t kColS = QT * D;           // then two logit slots of 128 columns
+  static_assert(kColS + 256 <= kTmemCols, "tensor memory");
+};
+
+// Scales, biases and exponents of one tile, ready for use.
+template <int D>
+struct alignas(16) Meta {
+  static constexpr int J = RowGeo<D>::J;
+  uint16_t vs[J][128], vb[J][128];     // values: scale, bias (fp16, divided by 2^e)
+  uint32_t ksb[J][128];                // keys: scale | bias << 16
+  float kf[128];                       // 2^eK of each token (slow tiles)
+  float ve[128];                       // eV of each token (slow tiles)
+  uint8_t flag[128];                   // bit j: value group j is NaN; kDead
+  float tile_kf, tile_ve;              // of all tokens (other tiles)
+  int slow;
+};
+
+struct Ctl {
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], pv_done[2], meta_full[kMetaRing], drain;
+  int64_t base[kMetaRing][8];          // byte offset of a 16-token block's key codes, -1: none
+  int32_t words[kMetaRing][8];         // from there to its words
+  int red_max[2][4], red_min[2][4], red_bad[2][4];
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+constexpr size_t row_smem() {
+  return 1024 + RowGeo<D>::kOffMeta + kMetaRing * sizeof(Meta<D>) + sizeof(Ctl);
+}
+
+// One block's piece of a unit: token tiles [kt0, kt1) for query rows row0 ...
+struct Seg {
+  bool pre;
+  int b, hk, row0, n_rows, ctx, kt0, kt1, tiles, part;
+  const int32_t* pages;
+};
+
+// Walks a block's share [g, end) of the tiles of all units.
+struct Walk {
+  int64_t g, end;
+  __device__ explicit Walk(const AttnArgs& a) {
+    const int64_t total = static_cast<int64_t>(a.pre_units) * a.pre_T +
+                          static_cast<int64_t>(a.own_units) * a.own_T;
+    g = static_cast<int64_t>(blockIdx.x) * a.share;
+    end = min(g + a.share, total);
+  }
+  // The next piece with any work; false at the end.
+  __device__ bool next(const AttnArgs& a, Seg& s, bool report) {
+    const int64_t pre_total = static_cast<int64_t>(a.pre_units) * a.pre_T;
+    while (g < end) {
+      int64_t base;
+      int T;
+      if (g < pre_total) {
+        const int u = static_cast<int>(g / a.pre_T);
+        s.pre = true;
+        T = a.pre_T;
+        base = static_cast<int64_t>(u) * T;
+        s.hk = u / a.pre_row_tiles;
+        s.b = 0;
+        s.row0 = u % a.pre_row_tiles * a.unit_rows;
+        s.n_rows = a.B * a.nq * a.G;
+        s.ctx = a.prefix_len;
+        s.pages = a.prefix_table;
+      } else {
+        const int u = static_cast<int>((g - pre_total) / a.own_T);
+        s.pre = false;
+        T = a.own_T;
+        base = pre_total + static_cast<int64_t>(u) * T;
+        const int place = u % a.own_row_tiles, bh = u / a.own_row_tiles;
+        s.hk = bh % a.c.Hkv;
+        s.b = bh / a.c.Hkv;
+        s.row0 = unit_tile(place, a.own_row_tiles) * a.unit_rows;
+        s.n_rows = a.nq * a.G;
+        s.ctx = context_len(a, s.b, report && s.hk == 0 && place == 0);
+        s.pages = a.table + static_cast<int64_t>(s.b) * a.table_stride;
+      }
+      const int last = min(s.row0 + a.unit_rows, s.n_rows) - 1;
+      const int seen = s.pre ? s.ctx : own_limit(a, s.ctx, last);
+      s.tiles = (seen + kRowTile - 1) / kRowTile;
+      s.kt0 = static_cast<int>(g - base);
+      const int64_t stop = min(end, base + T);
+      s.kt1 = min(static_cast<int>(stop - base), s.tiles);
+      s.part = static_cast<int>(blockIdx.x - base / a.share);
+      g = stop;
+      if (s.kt1 > s.kt0) return true;
+    }
+    return false;
+  }
+  __device__ static int seen(const AttnArgs& a, const Seg& s) {
+    const int last = min(s.row0 + a.unit_rows, s.n_rows) - 1;
+    return s.pre ? s.ctx : own_limit(a, s.ctx, last);
+  }
+};
+
+// A bounded wait: after the first that runs out, none waits again.
+struct Waiter {
+  Ctl* ctl;
+  int32_t* err;
+  uint64_t limit;
+  bool ok;
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+    if (!ok) return;
+    if (mbar_wait(bar, parity, &ctl->abort, limit)) return;
+    ok = false;
+    if (atomicExch(&ctl->abort, 1) == 0) atomicOr(err, MOE_DEVERR_PIPE_TIMEOUT);
+  }
+};
+
+// Instruction descriptor, kind::f16: fp16 A and B, fp32 D, both K-major, M = 128.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// 64 of the reduction (4 steps of 16), issued by one elected lane: A and B in shared memory.
+__device__ __forceinline__ void mma_ss_chunk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      ".reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+      "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// tcgen05.st: 32 lanes x 32-bit, 8 consecutive columns per thread.
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+
+__device__ __forceinline__ void conv_bar() { named_bar_sync(1, kConvThreads); }
+
+__device__ __forceinline__ uint32_t exp_field(uint32_t bf16_bits) { return (bf16_bits >> 7) & 255u; }
+__device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
+
+// -------------------------------------------------------- codes to operands
+
+template <int D, int BITS>
+struct Converter {
+  using G = RowGeo<D>;
+  static constexpr int J = G::J;
+  static constexpr int RB = D * BITS / 8;
+  static constexpr int PR = D / 16;                  // 16-code pieces of a row
+  static constexpr int KU = PR / 2;                  // key pieces per thread and tile
+  static constexpr int VU = D >= 128 ? D / 128 : 1;  // value pieces (8 tokens x 8 elements)
+  static constexpr int KW = BITS / 2;                // words of a key piece (16 codes)
+
+  const AttnArgs& a;
+  Ctl& ctl;
+  Meta<D>* metas;
+  uint8_t* smem;
+  int ct, cw, lane;
+  uint32_t kr[KU][KW];
+  uint32_t vr[VU][8][BITS / 4];
+
+  // Block offsets of the tile at token tok0 into ring slot `slot` (8 threads).
+  __device__ void put_base(int slot, int page, int tok, int end, int hk) {
+    int64_t off = -1;
+    int wd = 0;
+    if (tok < end && page >= 0 && page < a.c.pages) {
+      const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
+      const uint32_t in_page =
+          blk - static_cast<uint32_t>((blk * a.page_magic) >> 40) * a.page_blocks;
+      off = page * a.c.page_bytes + static_cast<int64_t>(hk) * a.c.head_bytes + in_page * (16 * RB);
+      wd = a.c.code_bytes + static_cast<int>(in_page) * (16 * J * 4 - 16 * RB);
+    } else if (tok < end) {
+      atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
+    }
+    ctl.base[slot][ct] = off;
+    ctl.words[slot][ct] = wd;
+  }
+  __device__ int page_at(const int32_t* pages, int tok, int end) const {
+    if (tok >= end) return -1;
+    const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
+    return __ldg(pages + static_cast<uint32_t>((blk * a.page_magic) >> 40));
+  }
+
+  // This thread's scale and bias words: token ct % 128 of the keys (ct < 128) or values.
+  __device__ void load_words(int slot, uint32_t (&w)[J]) const {
+    const int tk = ct & 127;
+    const int64_t off = ctl.base[slot][tk >> 4];
+#pragma unroll
+    for (int j = 0; j < J; ++j) w[j] = 0;
+    if (off < 0) return;
+    const uint8_t* p = a.c.data + off + ctl.words[slot][tk >> 4] + (tk & 15) * (J * 4);
+    if (ct >= 128) p += static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes;
+    if constexpr (J == 1) {
+      w[0] = ld_nc_u32(p);
+    } else if constexpr (J == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      const uint4 v = ld_nc_v4(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+  }
+
+  __device__ void load_keys(int slot) {
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      const int row = (cw * KU + u) * (32 / PR) + lane / PR, piece = lane % PR;
+      const int64_t off = ctl.base[slot][row >> 4];
+#pragma unroll
+      for (int i = 0; i < KW; ++i) kr[u][i] = 0;
+      if (off < 0) continue;
+      const uint8_t* p = a.c.data + off + (row & 15) * RB + piece * (2 * BITS);
+      if constexpr (BITS == 8) {
+        const uint4 v = ld_nc_v4(p);
+        kr[u][0] = v.x, kr[u][1] = v.y, kr[u][2] = v.z, kr[u][3] = v.w;
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        kr[u][0] = v.x, kr[u][1] = v.y;
+      }
+    }
+  }
+
+  // Value piece u: tokens 64 th + 8 tg .. of elements 32 db + 8 dq ..
+  __device__ bool value_piece(int u, int& th, int& d0) const {
+    const int unit = cw + 8 * u;
+    th = unit & 1;
+    d0 = (unit >> 1) * 32 + (lane >> 3) * 8;
+    return D >= 128 || unit < 4;
+  }
+  __device__ void load_values(int slot) {
+#pragma unroll
+    for (int u = 0; u < VU; ++u) {
+      int th, d0;
+      if (!value_piece(u, th, d0)) continue;
+      const int t0 = th * 64 + (lane & 7) * 8;
+      const int64_t off = ctl.base[slot][t0 >> 4];
+      const uint8_t* p = a.c.data + off + static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes +
+                         (t0 & 15) * RB + d0 * BITS / 8;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (BITS == 8) {
+          uint2 v = make_uint2(0, 0);
+          if (off >= 0) v = __ldg(reinterpret_cast<const uint2*>(p + k * RB));
+          vr[u][k][0] = v.x, vr[u][k][1] = v.y;
+        } else {
+          vr[u][k][0] = off >= 0 ? ld_nc_u32(p + k * RB) : 0;
+        }
+      }
+    }
+  }
+
+  // Exponents, scales and biases of a tile of `n` seen tokens from this thread's words.
+  __device__ void put_meta(Meta<D>& m, int slot, const uint32_t (&w)[J], int n) {
+    const int kv = ct >> 7, tk = ct & 127;
+    const bool valid = tk < n && ctl.base[slot][tk >> 4] >= 0;
+    uint32_t e = 0, bad = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint32_t se = exp_field(w[j]), be = exp_field(w[j] >> 16);
+      if (se == 255u || be == 255u)
+        bad |= 1u << j;
+      else
+        e = max(e, max(se ? se + BITS : 0u, be));
+    }
+    if (!valid) e = bad = 0;
+    const uint32_t top = __reduce_max_sync(kAll, e);
+    const uint32_t low = __reduce_min_sync(kAll, e ? e : 255u);
+    // NaN values, and tokens that a page outside the cache would hold
+    const bool odd = (kv == 1 && bad) || (tk < n && !valid);
+    const bool any_odd = __any_sync(kAll, odd);
+    if (lane == 0) {
+      ctl.red_max[kv][cw & 3] = static_cast<int>(top);
+      ctl.red_min[kv][cw & 3] = static_cast<int>(low);
+      ctl.red_bad[kv][cw & 3] = any_odd;
+    }
+    conv_bar();
+    int E[2], slow = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int hi = 0, lo = 255;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        hi = max(hi, ctl.red_max[i][k]);
+        lo = min(lo, ctl.red_min[i][k]);
+        slow |= ctl.red_bad[i][k];
+      }
+      slow |= hi - lo > kMaxSpread;
+      E[i] = hi == 0 ? 127 : min(hi, 253);
+    }
+    const uint32_t eu = slow && valid && e ? min(e, 253u) : static_cast<uint32_t>(E[kv]);
+    const float down = pow2_field(254u - eu);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const bool nan = bad >> j & 1;
+      const float s = valid && !nan ? bf16_lo(w[j]) * down : 0.f;
+      const float b = valid && !nan ? bf16_hi(w[j]) * down : 0.f;
+      uint32_t sb = pack_f16(s, b);
+      if (kv == 0) {
+        if (nan && valid) sb = 0x7E000000u;            // a NaN key: NaN logits
+        m.ksb[j][tk] = sb;
+      } else {
+        m.vs[j][tk] = static_cast<uint16_t>(sb);
+        m.vb[j][tk] = static_cast<uint16_t>(sb >> 16);
+      }
+    }
+    if (kv == 0) {
+      m.kf[tk] = pow2_field(eu);
+    } else {
+      m.ve[tk] = static_cast<float>(static_cast<int>(eu) - 127);
+      m.flag[tk] = static_cast<uint8_t>(bad | (tk < n && !valid ? kDead : 0));
+    }
+    if (ct == 0) {
+      m.tile_kf = pow2_field(static_cast<uint32_t>(E[0]));
+      m.tile_ve = static_cast<float>(E[1] - 127);
+      m.slow = slow;
+    }
+    conv_bar();
+  }
+
+  // Keys: 16 codes of a token -> two 16-byte chunks of its row. 4-bit chunks hold
+  // elements 0 4 1 5 2 6 3 7 (as they come out of a word); the queries' do too.
+  __device__ void put_keys(const Meta<D>& m, uint32_t off) const {
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      const int row = (cw * KU + u) * (32 / PR) + lane / PR, piece = lane % PR;
+      const int j = piece >> 2;
+      const uint32_t sb = m.ksb[j][row];
+      const uint32_t s2 = prmt(sb, sb, 0x1010), b2 = prmt(sb, sb, 0x3232);
+      uint32_t r[8];
+      constexpr uint32_t k1024 = 0x64006400u;
+      if constexpr (BITS == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          r[2 * i] = fma_f16x2(s2, sub_f16x2(prmt(kr[u][i], k1024 >> 8, 0x4140), k1024), b2);
+          r[2 * i + 1] = fma_f16x2(s2, sub_f16x2(prmt(kr[u][i], k1024 >> 8, 0x4342), k1024), b2);
+        }
+      } else {
+        const uint32_t s16 = fma_f16x2(s2, 0x2C002C00u, 0u);      // scale / 16
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = i & 1 ? kr[u][i >> 1] >> 8 : kr[u][i >> 1];
+          r[2 * i] = fma_f16x2(s2, sub_f16x2(lop3_and_or(w, 0x000F000Fu, k1024), k1024), b2);
+          r[2 * i + 1] = fma_f16x2(s16, sub_f16x2(lop3_and_or(w, 0x00F000F0u, k1024), k1024), b2);
+        }
+      }
+      uint8_t* dst = smem + off + j * 16384 + row * 128;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // odd groups store their second chunk first: the lanes of a store meet all banks once
+        const bool second = (h ^ (j & 1)) != 0;
+        const int chunk = (piece & 3) * 2 + (second ? 1 : 0);
+        *reinterpret_cast<uint4*>(dst + ((chunk ^ (row & 7)) << 4)) =
+            second ? make_uint4(r[4], r[5], r[6], r[7]) : make_uint4(r[0], r[1], r[2], r[3]);
+      }
+    }
+  }
+
+  // Values, transposed: 8 tokens x 8 elements -> one 16-byte chunk in each of 8 rows.
+  __device__ void put_values(const Meta<D>& m, uint32_t off) const {
+#pragma unroll
+    for (int u = 0; u < VU; ++u) {
+      int th, d0;
+      if (!value_piece(u, th, d0)) continue;
+      const int tg = lane & 7, j = d0 / kKvGroup;
+      const uint4 sv = *reinterpret_cast<const uint4*>(&m.vs[j][th * 64 + tg * 8]);
+      const uint4 bv = *reinterpret_cast<const uint4*>(&m.vb[j][th * 64 + tg * 8]);
+      const uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
+      uint8_t* dst = smem + off + th * (D * 128) + d0 * 128;
+      constexpr uint32_t k1024 = 0x64006400u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {                 // elements 4h .. 4h + 3
+        uint32_t r[4][4];                           // [element][token pair]
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          if constexpr (BITS == 8) {
+            const uint32_t x = vr[u][2 * p][h], y = vr[u][2 * p + 1][h];
+            const uint32_t lo = prmt(x, y, 0x5140), hi = prmt(x, y, 0x7362);
+            r[0][p] = fma_f16x2(s[p], sub_f16x2(prmt(lo, k1024 >> 8, 0x4140), k1024), b[p]);
+            r[1][p] = fma_f16x2(s[p], sub_f16x2(prmt(lo, k1024 >> 8, 0x4342), k1024), b[p]);
+            r[2][p] = fma_f16x2(s[p], sub_f16x2(prmt(hi, k1024 >> 8, 0x4140), k1024), b[p]);
+            r[3][p] = fma_f16x2(s[p], sub_f16x2(prmt(hi, k1024 >> 8, 0x4342), k1024), b[p]);
+          } else {
+            const uint32_t v = prmt(vr[u][2 * p][0], vr[u][2 * p + 1][0], h ? 0x7632 : 0x5410);
+            const uint32_t s16 = fma_f16x2(s[p], 0x2C002C00u, 0u);
+            r[0][p] = fma_f16x2(s[p], sub_f16x2(lop3_and_or(v, 0x000F000Fu, k1024), k1024), b[p]);
+            r[1][p] = fma_f16x2(s16, sub_f16x2(lop3_and_or(v, 0x00F000F0u, k1024), k1024), b[p]);
+            r[2][p] = fma_f16x2(s[p], sub_f16x2(lop3_and_or(v >> 8, 0x000F000Fu, k1024), k1024), b[p]);
+            r[3][p] = fma_f16x2(s16, sub_f16x2(lop3_and_or(v >> 8, 0x00F000F0u, k1024), k1024), b[p]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 4 * h + i;
+          *reinterpret_cast<uint4*>(dst + row * 128 + ((tg ^ row) << 4)) =
+              make_uint4(r[i][0], r[i][1], r[i][2], r[i][3]);
+        }
+      }
+    }
+  }
+
+  // All tiles of one piece; `tc` counts this block's tiles.
+  __device__ void run(const Seg& sg, int seen, uint32_t& tc, Waiter& w) {
+    const int nt = sg.kt1 - sg.kt0;
+    const int tok0 = sg.kt0 * kRowTile;
+    uint32_t words[J];
+    int page = -1;
+    // no reader of the ring slots written here is left: the softmax of the piece before is
+    // at most a tile behind the products, whose last use of a slot freed it
+    if (ct < 8) {
+      put_base(tc & 3, page_at(sg.pages, tok0 + 16 * ct, seen), tok0 + 16 * ct, seen, sg.hk);
+      page = page_at(sg.pages, tok0 + kRowTile + 16 * ct, seen);
+    }
+    conv_bar();
+    load_words(tc & 3, words);
+    load_keys(tc & 3);
+    for (int it = 0; it < nt; ++it, ++tc) {
+      const int slot = tc & 3, st = tc % G::KS;
+      const int tok = tok0 + it * kRowTile;
+      if (ct < 8) {
+        const int nx = tok + kRowTile + 16 * ct;
+        put_base((tc + 1) & 3, page, nx, it + 1 < nt ? seen : 0, sg.hk);
+        page = page_at(sg.pages, nx + kRowTile, seen);
+      }
+      Meta<D>& m = metas[slot];
+      put_meta(m, slot, words, min(seen - tok, kRowTile));
+      if (lane == 0) mbar_arrive(&ctl.meta_full[slot]);
+      load_values(slot);
+      const uint32_t parity = ((tc / G::KS) & 1) ^ 1;
+      w.wait(&ctl.k_empty[st], parity);
+      put_keys(m, G::kOffK + st * G::kTileBytes);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.k_full[st]);
+      if (it + 1 < nt) {
+        load_words((tc + 1) & 3, words);
+        load_keys((tc + 1) & 3);
+      }
+      w.wait(&ctl.v_empty[st], parity);
+      put_values(m, G::kOffV + st * G::kTileBytes);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.v_full[st]);
+    }
+  }
+};
+
+// ------------------------------------------------------------------ softmax
+
+template <int D, int BITS>
+struct Softmax {
+  using G = RowGeo<D>;
+  const AttnArgs& a;
+  Ctl& ctl;
+  Meta<D>* metas;
+  uint8_t* smem;
+  uint32_t tmem;             // + lane quarter
+  int wg, warp, lane;
+  float m, l, E;             // reference of the logits (log2), sum, exponent of O
+  float c;                   // scale2 * 2^(row exponent)
+  uint32_t nan;              // value groups that are NaN for this row
+
+  // The row's query, divided by the power of two under its largest element, as fp16
+  // in the key tiles' element order.
+  __device__ void load_query(const uint16_t* qp, bool live) {
+    const int r = (warp & 3) * 32 + lane;
+    float mx = 0.f;
+    if (live)
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(qp) + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+      }
+    const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
+    const float down = pow2_field(254u - e);
+    c = a.scale2 * pow2_field(e);
+    uint8_t* dst = smem + wg * G::kTileBytes + r * 128;
+    for (int i = 0; i < D / 8; ++i) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (live) v = __ldg(reinterpret_cast<const uint4*>(qp) + i);
+      const float x[8] = {bf16_lo(v.x) * down, bf16_hi(v.x) * down, bf16_lo(v.y) * down,
+                          bf16_hi(v.y) * down, bf16_lo(v.z) * down, bf16_hi(v.z) * down,
+                          bf16_lo(v.w) * down, bf16_hi(v.w) * down};
+      const uint4 o = BITS == 8 ? make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
+                                             pack_f16(x[4], x[5]), pack_f16(x[6], x[7]))
+                                : make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]),
+                                             pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
+      *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4)) = o;
+    }
+  }
+
+  // Logit (log2 units) of column k of a tile; -inf where the row does not see it.
+  template <bool SLOW, bool MASK>
+  __device__ __forceinline__ float logit(float s, float ck, const Meta<D>& t, int k, int lim) const {
+    float x = SLOW ? s * (c * t.kf[k]) : s * ck;
+    if (MASK && k >= lim) x = -INFINITY;
+    if (SLOW && (t.flag[k] & kDead)) x = -INFINITY;
+    return x;
+  }
+
+  // Weights of columns 64 H .. 64 H + 63 into registers, and their sum.
+  template <bool MASK, int H>
+  __device__ __forceinline__ float weights(uint32_t s_col, float ck, float off, int lim,
+                                           uint32_t (&p)[32]) {
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(tmem + s_col + 64 * H + 16 * h, v);
+      tmem_ld_wait();
+      tmem_regs_ready(v);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const int col = 64 * H + 16 * h + i;
+        float x0 = fmaf(__uint_as_float(v[i]), ck, off);
+        float x1 = fmaf(__uint_as_float(v[i + 1]), ck, off);
+        if (MASK && col >= lim) x0 = -INFINITY;
+        if (MASK && col + 1 >= lim) x1 = -INFINITY;
+        const float w0 = exp2_approx(x0), w1 = exp2_approx(x1);
+        part[(i >> 1) & 3] += w0 + w1;
+        p[8 * h + i / 2] = pack_f16(w0, w1);
+      }
+    }
+    return (part[0] + part[1]) + (part[2] + part[3]);
+  }
+
+  // Moves m to the largest logit of columns 16 H0 .. 127 and E so that none of their
+  // weights passes 1 (in the lanes that `need` it), and l, O and the tile's weights
+  // already written (columns below 16 H0) along with them.
+  template <bool SLOW, bool MASK, int H0>
+  __device__ __forceinline__ void move(uint32_t s_col, const Meta<D>& t, int lim, bool need, bool first,
+                                       uint64_t* pv, uint32_t pv_parity, Waiter& w) {
+    float mx = -INFINITY, ux = -INFINITY;
+    const float ck = c * t.tile_kf;
+#pragma unroll 1
+    for (int h = H0; h < 8; ++h) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(tmem + s_col + 16 * h, v);
+      tmem_ld_wait();
+      tmem_regs_ready(v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float x = logit<SLOW, MASK>(__uint_as_float(v[i]), ck, t, 16 * h + i, lim);
+        mx = fmaxf(mx, x);
+        ux = fmaxf(ux, x + (SLOW ? t.ve[16 * h + i] : t.tile_ve));
+      }
+    }
+    float fo = 1.f;
+    if (need && mx > -INFINITY) {
+      const float mn = fmaxf(m, mx);
+      const float u = ux - mn;                      // exponent of the largest contribution
+      const float En = m == -INFINITY ? u : fmaxf(E, u);
+      l *= exp2_approx(m - mn);
+      fo = exp2_approx(m - mn + (E - En));
+      m = mn;
+      E = En;
+    }
+    if (!__any_sync(kAll, fo != 1.f)) return;
+    if (H0 > 0) {
+      const uint32_t f2 = pack_f16(fo, fo);
+#pragma unroll 1
+      for (int h = 0; h < H0 / 2; ++h) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tmem + s_col + 16 * h, v);
+        tmem_ld_wait();
+        tmem_regs_ready(v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = fma_f16x2(v[i], f2, 0u);
+        tmem_st_32x32b_x16(tmem + s_col + 16 * h, v);
+      }
+      tmem_st_wait();
+    }
+    if (first) return;
+    w.wait(pv, pv_parity);                          // the last product into O is done
+    tc_fence_after();
+    const uint32_t o_col = tmem + G::kColO + wg * D;
+#pragma unroll 1
+    for (int h = 0; h < D / 16; ++h) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(o_col + 16 * h, v);
+      tmem_ld_wait();
+      tmem_regs_ready(v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fo);
+      tmem_st_32x32b_x16(o_col + 16 * h, v);
+    }
+    tmem_st_wait();
+  }
+
+  // Half H of a tile. Its 64 weights are packed into 32 columns that hold logits of
+  // half 0, so a tile takes no tensor memory beside its logits.
+  template <bool MASK, int H>
+  __device__ __forceinline__ void half_tile(uint32_t s_col, const Meta<D>& t, int lim, bool first,
+                                            uint64_t* pv, uint32_t pv_parity, Waiter& w) {
+    uint32_t p[32];
+    float size, d;
+    bool need = m == -INFINITY && lim > 64 * H;
+#pragma unroll 1
+    for (int round = 0;; ++round) {
+      if (__any_sync(kAll, need)) move<false, MASK, 4 * H>(s_col, t, lim, need, first, pv, pv_parity, w);
+      d = fmaxf(t.tile_ve - E, -60.f);
+      size = weights<MASK, H>(s_col, c * t.tile_kf, d - (m == -INFINITY ? 0.f : m), lim, p);
+      need = size >= 32768.f;
+      if (round || !__any_sync(kAll, need)) break;
+    }
+    l = fmaf(size, exp2_approx(-d), l);
+    tmem_st_32x32b_x16(tmem + s_col + 32 * H, reinterpret_cast<uint32_t(&)[16]>(p[0]));
+    tmem_st_32x32b_x16(tmem + s_col + 32 * H + 16, reinterpret_cast<uint32_t(&)[16]>(p[16]));
+    tmem_st_wait();
+  }
+  template <bool MASK>
+  __device__ __forceinline__ void tile(uint32_t s_col, const Meta<D>& t, int lim, bool first,
+                                       uint64_t* pv, uint32_t pv_parity, Waiter& w) {
+    half_tile<MASK, 0>(s_col, t, lim, first, pv, pv_parity, w);
+    half_tile<MASK, 1>(s_col, t, lim, first, pv, pv_parity, w);
+  }
+
+  // A tile with an exponent per token, NaN groups or missing pages: m always moves to
+  // the maximum, so no weight passes 1 and the weights may overwrite the logits that
+  // have been read.
+  __device__ __forceinline__ void slow_tile(uint32_t s_col, const Meta<D>& t, int lim, bool first,
+                                            uint64_t* pv, uint32_t pv_parity, Waiter& w) {
+    move<true, true, 0>(s_col, t, lim, true, first, pv, pv_parity, w);
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+    for (int h = 0; h < 8; ++h) {
+      uint32_t v[16], p[8];
+      tmem_ld_32x32b_x16(tmem + s_col + 16 * h, v);
+      tmem_ld_wait();
+      tmem_regs_ready(v);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float wt[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int col = 16 * h + i + k;
+          const float d = fmaxf(t.ve[col] - E, -60.f);
+          const float x = logit<true, true>(__uint_as_float(v[i + k]), 0.f, t, col, lim);
+          wt[k] = exp2_approx(x - ref + d);
+          l = fmaf(wt[k], exp2_approx(-d), l);
+          if (x != -INFINITY) nan |= t.flag[col];
+        }
+        p[i / 2] = pack_f16(wt[0], wt[1]);
+      }
+      tmem_st_32x32b_x8(tmem + s_col + 8 * h, p);
+    }
+    tmem_st_wait();
+  }
+
+  __device__ void run(const Seg& sg, int nqt, uint32_t tc, const uint32_t (&sc)[2], uint32_t pc,
+                      Waiter& w) {
+    const int r = sg.row0 + wg * 128 + (warp & 3) * 32 + lane;
+    const bool live = r < sg.n_rows;
+    const int qrow = live ? (sg.pre ? r / a.G : sg.b * a.nq + r / a.G) : 0;
+    const int head = sg.hk * a.G + (live ? r % a.G : 0);
+    load_query(a.q + qrow * a.q_row + head * a.q_head, live);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.q_full[wg]);
+    m = -INFINITY;
+    l = 0.f;
+    E = 0.f;
+    nan = 0;
+    const int lim = !live ? 0 : sg.pre ? sg.ctx : own_limit(a, sg.ctx, r);
+    const int nt = sg.kt1 - sg.kt0;
+    for (int it = 0; it < nt; ++it) {
+      const int slot = nqt == 2 ? wg : it & 1;
+      const uint32_t use = sc[slot] + (nqt == 2 ? it : it >> 1);
+      const Meta<D>& t = metas[(tc + it) & 3];
+      w.wait(&ctl.meta_full[(tc + it) & 3], ((tc + it) >> 2) & 1);
+      w.wait(&ctl.s_full[slot], use & 1);
+      tc_fence_after();
+      const int rel = lim - (sg.kt0 + it) * kRowTile;
+      const uint32_t s_col = G::kColS + 128 * slot;
+      const uint32_t pv_parity = (pc + it - 1) & 1;
+      uint64_t* pv = &ctl.pv_done[wg];
+      if (t.slow)
+        slow_tile(s_col, t, rel, it == 0, pv, pv_parity, w);
+      else if (__all_sync(kAll, rel >= kRowTile))
+        tile<false>(s_col, t, rel, it == 0, pv, pv_parity, w);
+      else
+        tile<true>(s_col, t, rel, it == 0, pv, pv_parity, w);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.p_full[slot]);
+    }
+    // ---- outputs. With one query tile the last but one product may still run too (the last
+    // logits were issued before it), and a parity tells only neighbouring phases apart.
+    if (nt > 1) w.wait(&ctl.pv_done[wg], (pc + nt - 2) & 1);
+    w.wait(&ctl.pv_done[wg], (pc + nt - 1) & 1);
+    tc_fence_after();
+    const bool lone = (a.pre_parts == 0 || a.own_parts == 0) && sg.kt0 == 0 && sg.kt1 == sg.tiles;
+    const float up = exp2_approx(E) * (lone ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+    const int64_t at = (static_cast<int64_t>(sg.pre ? 0 : a.pre_parts) + sg.part) * a.B * a.nq * a.Hq +
+                       static_cast<int64_t>(qrow) * a.Hq + head;
+    if (live && !lone) a.ml[at] = make_float2(m, l);
+    uint16_t* out = a.out + qrow * a.o_row + head * a.o_head;
+    float* part = a.part + at * D;
+    for (int h = 0; h < D / 16; ++h) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(tmem + G::kColO + wg * D + 16 * h, v);
+      tmem_ld_wait();
+      tmem_regs_ready(v);
+      if (!live) continue;
+      const bool is_nan = nan >> (h * 16 / kKvGroup) & 1;
+      float y[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = is_nan ? NAN : __uint_as_float(v[i]) * up;
+      if (lone) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<uint4*>(out + 16 * h + 8 * k) =
+              make_uint4(pack_bf16(y[8 * k], y[8 * k + 1]), pack_bf16(y[8 * k + 2], y[8 * k + 3]),
+                         pack_bf16(y[8 * k + 4], y[8 * k + 5]), pack_bf16(y[8 * k + 6], y[8 * k + 7]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<float4*>(part + 16 * h + 4 * k) =
+              make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+      }
+    }
+    tc_fence_before();
+  }
+};
+
+// ------------------------------------------------------------------- kernel
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a) {
+  using G = RowGeo<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Meta<D>* metas = reinterpret_cast<Meta<D>*>(smem + G::kOffMeta);
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem + G::kOffMeta + kMetaRing * sizeof(Meta<D>));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.q_full[i], 4);
+      mbar_init(&ctl.k_full[i], kConvWarps);
+      mbar_init(&ctl.k_empty[i], 1);
+      mbar_init(&ctl.v_full[i], kConvWarps);
+      mbar_init(&ctl.v_empty[i], 1);
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.p_full[i], 4);
+      mbar_init(&ctl.pv_done[i], 1);
+    }
+    for (int i = 0; i < kMetaRing; ++i) mbar_init(&ctl.meta_full[i], kConvWarps);
+    mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ctl.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+  Waiter w{&ctl, a.c.err, a.timeout_ns, true};
+
+  // counts of tiles, uses of the logit slots and products into each O so far
+  uint32_t tc = 0, sc[2] = {0, 0}, pc[2] = {0, 0};
+  Walk walk(a);
+  Seg sg;
+  if (warp < kSoftWarps) {
+    Softmax<D, BITS> sm{a, ctl, metas, smem, tmem + ((warp & 3) << 21), warp >> 2, warp, lane};
+    while (walk.next(a, sg, threadIdx.x == 0)) {
+      const int nt = sg.kt1 - sg.kt0;
+      const int nqt = G::QT == 2 && sg.row0 + 128 < sg.n_rows ? 2 : 1;
+      if (sm.wg < nqt) sm.run(sg, nqt, tc, sc, pc[sm.wg], w);
+      // a warpgroup without a query tile may not run ahead: a wait tells only
+      // neighbouring phases of its barrier apart
+      named_bar_sync(2, kSoftWarps * 32);
+      tc += nt;
+      sc[0] += nqt == 2 ? nt : (nt + 1) / 2;
+      sc[1] += nqt == 2 ? nt : nt / 2;
+      pc[0] += nt;
+      pc[1] += nqt == 2 ? nt : 0;
+    }
+  } else if (warp < kMmaWarp) {
+    Converter<D, BITS> cv{a, ctl, metas, smem, static_cast<int>(threadIdx.x) - kSoftWarps * 32,
+                          warp - kSoftWarps, lane};
+    while (walk.next(a, sg, false)) cv.run(sg, Walk::seen(a, sg), tc, w);
+  } else {
+    const uint32_t idesc_x = idesc_f16(128), idesc_o = idesc_f16(D);
+    const uint32_t base = smem_u32(smem);
+    uint32_t q_uses[2] = {0, 0};
+    while (walk.next(a, sg, false)) {
+      const int nt = sg.kt1 - sg.kt0;
+      const int nqt = G::QT == 2 && sg.row0 + 128 < sg.n_rows ? 2 : 1;
+      for (int i = 0; i < nqt; ++i) w.wait(&ctl.q_full[i], q_uses[i]++ & 1);
+      const int items = nt * nqt;
+      // item n: query tile q, token tile it; its weights' product follows the next item's logits
+      const auto weigh = [&](int n) {
+        const int q = nqt == 2 ? n & 1 : 0, it = nqt == 2 ? n >> 1 : n, slot = n & 1;
+        const uint32_t t = tc + it, st = t % G::KS;
+        if (q == 0) w.wait(&ctl.v_full[st], (t / G::KS) & 1);
+        w.wait(&ctl.p_full[slot], (sc[slot] + (nqt == 2 ? it : it >> 1)) & 1);
+        tc_fence_after();
+        __syncwarp();
+        const uint32_t p = tmem + G::kColS + 128 * slot, o = tmem + G::kColO + q * D;
+        const uint64_t v = sdesc_k_sw128(base + G::kOffV + st * G::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          mma_ts_tile_chunk_elect(o, p + 32 * k, v + k * (D * 128 / 16), idesc_o, it > 0 || k > 0);
+        mma_commit_elect(&ctl.pv_done[q]);
+        if (q == nqt - 1) mma_commit_elect(&ctl.v_empty[st]);
+      };
+      for (int n = 0; n < items; ++n) {
+        const int q = nqt == 2 ? n & 1 : 0, it = nqt == 2 ? n >> 1 : n, slot = n & 1;
+        const uint32_t t = tc + it, st = t % G::KS;
+        if (q == 0) {
+          w.wait(&ctl.k_full[st], (t / G::KS) & 1);
+          tc_fence_after();
+        }
+        __syncwarp();
+        const uint64_t qd = sdesc_k_sw128(base + q * G::kTileBytes);
+        const uint64_t kd = sdesc_k_sw128(base + G::kOffK + st * G::kTileBytes);
+#pragma unroll
+        for (int j = 0; j < G::J; ++j)
+          mma_ss_chunk(tmem + G::kColS + 128 * slot, qd + j * 1024, kd + j * 1024, idesc_x, j > 0);
+        mma_commit_elect(&ctl.s_full[slot]);
+        if (q == nqt - 1) mma_commit_elect(&ctl.k_empty[st]);
+        if (n > 0) weigh(n - 1);
+      }
+      weigh(items - 1);
+      tc += nt;
+      sc[0] += nqt == 2 ? nt : (nt + 1) / 2;
+      sc[1] += nqt == 2 ? nt : nt / 2;
+    }
+    // nothing issued may outlive the tensor memory
+    mma_commit_elect(&ctl.drain);
+    w.ok = true;
+    w.wait(&ctl.drain, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, int BITS>
+cudaError_t launch_rows(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
+  constexpr size_t smem = row_smem<D>();
+  static_assert(smem <= 227 * 1024, "shared memory");
+  const auto kernel = attn_rows_kernel<D, BITS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kernel<<<blocks, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int attn_unit_rows(int D) { return D == 256 ? 128 : 256; }
+
+cudaError_t launch_attn_rows(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
+  if (a.c.bits == 8)
+    return a.c.D == 64    ? launch_rows<64, 8>(a, blocks, s)
+           : a.c.D == 128 ? launch_rows<128, 8>(a, blocks, s)
+                          : launch_rows<256, 8>(a, blocks, s);
+  return a.c.D == 64    ? launch_rows<64, 4>(a, blocks, s)
+         : a.c.D == 128 ? launch_rows<128, 4>(a, blocks, s)
+                        : launch_rows<256, 4>(a, blocks, s);
+}
+
+}  // namespace moeq4

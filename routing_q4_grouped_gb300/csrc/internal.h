@@ -75,6 +75,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// Time limit of a wait inside a kernel (MOEQ4_WAIT_TIMEOUT_MS, 2 s by default).
+uint64_t wait_timeout_ns();
+
 // Optional stage events (bench/test timing): mark(i) records event i on `s`.
 void stage_mark(int i, cudaStream_t s);
 
