@@ -44,8 +44,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src)
                : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
@@ -88,26 +88,53 @@ template <int D, int BITS>
 struct Geo {
   static constexpr int J = D / kKvGroup;          // groups of a head
   static constexpr int RB = D * BITS / 8;         // code bytes of a token
-  static constexpr int TB = D == 256 ? 1 : 2;     // 16-token blocks per step
+  static constexpr int TB = D * BITS > 1024 ? 1 : 2;   // 16-token blocks per step
   static constexpr int kCodes = 16 * RB;          // one block's codes (keys or values)
   static constexpr int kWords = 16 * J * 4;
   static constexpr int kBlock = 2 * (kCodes + kWords);   // K codes, V codes, K words, V words
   static constexpr int kStage = TB * kBlock;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = TB == 1 ? 3 : 2;
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kRing = kWarps * kWarpBytes;
-  // Shared memory is laid out in rows of RB bytes whose 32-byte units are
-  // exchanged by the token's low bits, so that the lanes of one shared-memory
-  // access (which read the same unit of several tokens) meet no bank twice.
+  // Shared memory is laid out in rows of RB bytes (a token) whose 32-byte units are
+  // exchanged by the token's low bits, so that the lanes of one shared-memory access,
+  // which read the same unit of several tokens, meet no bank twice (twice at most for
+  // rows of one or two units). Keys are read for 4 or 2 neighbouring tokens at once,
+  // values for tokens 0 2 4 6.
   static constexpr int kUnits = RB / 32;
-  __device__ static int key_unit(int row, int u) {
-    if (BITS == 8) return kUnits >= 4 ? u ^ ((row & 1) << 1) : u;
-    return kUnits >= 4 ? u ^ (row & 3) : kUnits == 2 ? u ^ ((row >> 1) & 1) : u;
+  __device__ static int key_unit(int row) {
+    return kUnits < 2 ? 0 : BITS == 8 ? (kUnits >= 4 ? (row & 1) << 1 : 0)
+                                      : (kUnits >= 4 ? row & 3 : (row >> 1) & 1);
   }
-  __device__ static int value_unit(int row, int u) {
-    return kUnits >= 4 ? u ^ ((row >> 1) & 3) : kUnits == 2 ? u ^ ((row >> 1) & 1) : u;
+  __device__ static int value_unit(int row) {
+    return kUnits >= 4 ? (row >> 1) & 3 : kUnits == 2 ? (row >> 1) & 1 : 0;
+  }
+  // A lane's byte offset for its reads of group 0 (group j: key_at / value_at).
+  __device__ static uint32_t key_lane(int g, int t) {
+    return BITS == 8 ? g * RB + ((t >> 1) ^ key_unit(g)) * 32 + (t & 1) * 16
+                     : g * RB + key_unit(g) * 32 + t * 8;
+  }
+  __device__ static uint32_t value_lane(int g, int t) {
+    return BITS == 8 ? 2 * t * RB + ((g >> 2) ^ value_unit(2 * t)) * 32 + (g & 3) * 8
+                     : 2 * t * RB + value_unit(2 * t) * 32 + g * 4;
+  }
+  __device__ static constexpr uint32_t group_bits(int j) { return j * (BITS == 8 ? 64u : 32u); }
+  // A lane's destination of 16-byte chunk `lane` of a block; chunk 32 c + lane goes to
+  // (it ^ copy_bits(c)) + 512 c: a copy instruction covers whole rows.
+  static constexpr int kChunks = RB / 16;            // per row
+  __device__ static uint32_t copy_lane(int lane, bool value) {
+    const int row = lane / kChunks, at = lane % kChunks;
+    return row * RB + ((at >> 1) ^ (value ? value_unit(row) : key_unit(row))) * 32 + (at & 1) * 16;
+  }
+  __device__ static constexpr uint32_t copy_bits(int c, bool value) {
+    return !value ? 0u : RB == 128 ? (c & 1) * 64u : RB == 256 ? (c & 3) * 32u : 0u;
   }
 };
+
+// Blocks of the split kernel that share a multiprocessor, by registers and shared memory.
+constexpr int split_blocks_per_sm(int D, int BITS, int NT) {
+  return D == 256 ? 2 : D == 128 ? (NT == 2 ? 2 : BITS == 8 ? 3 : 4) : (NT == 2 ? 3 : 5);
+}
 
 template <int D, int BITS, int NT>
 struct SplitSmem {
@@ -131,27 +158,33 @@ struct Warp {
   float e[NT][2], f[NT][2];       // f = 2^-e: p s f stays below 2^15
   float top_x[NT][2], top_ps[NT][2];   // m + 8, m + e + 14: the bounds of a logit and of log2(p s) + m
 
+  __device__ __forceinline__ static void load_words(const uint8_t* p, uint32_t (&w)[G::J]) {
+    if constexpr (G::J == 1) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (G::J == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+  }
+
   // Columns 2t, 2t+1 of this thread (queries); rows lane/4 and lane/4 + 8 (tokens).
   template <bool MASK>
-  __device__ __forceinline__ void step(const uint8_t* st, int tok0, const int (&top)[G::TB],
-                                       int lane) {
-    const int g = lane >> 2, t = lane & 3;
+  __device__ __forceinline__ void step(const uint8_t* st, int tok0, const int (&top)[G::TB], int g,
+                                       uint32_t key_off, uint32_t value_off) {
     float x[G::TB][NT][4];
     uint32_t vw[G::TB][2][G::J];            // value words of tokens g, g + 8
 #pragma unroll
     for (int b = 0; b < G::TB; ++b) {
       const uint8_t* kc = st + b * G::kBlock;
-      const uint8_t* words = kc + 2 * G::kCodes;
+      const uint8_t* words = kc + 2 * G::kCodes + g * (G::J * 4);
       uint32_t kw[2][G::J];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = g + 8 * r;
-#pragma unroll
-        for (int j = 0; j < G::J; ++j) {
-          kw[r][j] = *reinterpret_cast<const uint32_t*>(words + (row * G::J + j) * 4);
-          vw[b][r][j] =
-              *reinterpret_cast<const uint32_t*>(words + G::kWords + (row * G::J + j) * 4);
-        }
+        load_words(words + r * (8 * G::J * 4), kw[r]);
+        load_words(words + G::kWords + r * (8 * G::J * 4), vw[b][r]);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -163,14 +196,12 @@ struct Warp {
         uint32_t w[2][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = g + 8 * r;
+          const uint8_t* kp = kc + (key_off ^ G::group_bits(j)) + r * 8 * G::RB;
           if (BITS == 8) {
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                kc + row * G::RB + G::key_unit(row, 2 * j + (t >> 1)) * 32 + (t & 1) * 16);
+            const uint4 v = *reinterpret_cast<const uint4*>(kp);
             w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
           } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(
-                kc + row * G::RB + G::key_unit(row, j) * 32 + t * 8);
+            const uint2 v = *reinterpret_cast<const uint2*>(kp);
             w[r][0] = v.x, w[r][1] = v.x >> 8, w[r][2] = v.y, w[r][3] = v.y >> 8;
           }
         }
@@ -250,6 +281,11 @@ struct Warp {
     // O^T += V^T P^T
 #pragma unroll
     for (int b = 0; b < G::TB; ++b) {
+      float pf[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf[n][i] = x[b][n][i] * f[n][i & 1];
       const uint8_t* vc = st + b * G::kBlock + G::kCodes;
 #pragma unroll
       for (int j = 0; j < G::J; ++j) {
@@ -261,7 +297,7 @@ struct Warp {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const float p0 = x[b][n][2 * r], p1 = x[b][n][2 * r + 1];
-            pb[n][r] = transpose8x8(pack_f16(p0 * (s * f[n][0]), p1 * (s * f[n][1])));
+            pb[n][r] = transpose8x8(pack_f16(pf[n][2 * r] * s, pf[n][2 * r + 1] * s));
             if (MASK) {            // a bias may be NaN: no product with rows that do not see it
               if (p0 != 0.f) ob[n][j][0] = fmaf(p0, bias, ob[n][j][0]);
               if (p1 != 0.f) ob[n][j][1] = fmaf(p1, bias, ob[n][j][1]);
@@ -275,14 +311,13 @@ struct Warp {
         uint32_t w[4][2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int row = 2 * t + (k & 1) + 8 * (k >> 1);
+          const uint8_t* vp =
+              vc + (value_off ^ G::group_bits(j)) + ((k & 1) + 8 * (k >> 1)) * G::RB;
           if (BITS == 8) {
-            const uint2 v = *reinterpret_cast<const uint2*>(
-                vc + row * G::RB + G::value_unit(row, 2 * j + (g >> 2)) * 32 + (g & 3) * 8);
+            const uint2 v = *reinterpret_cast<const uint2*>(vp);
             w[k][0] = v.x, w[k][1] = v.y;
           } else {
-            w[k][0] = *reinterpret_cast<const uint32_t*>(
-                vc + row * G::RB + G::value_unit(row, j) * 32 + g * 4);
+            w[k][0] = *reinterpret_cast<const uint32_t*>(vp);
           }
         }
 #pragma unroll
@@ -365,52 +400,134 @@ struct Warp {
   }
 };
 
-// One block: one split of one context (a request's own tokens, or the prefix) for
-// a tile of 8 NT query rows of one key/value head. Its warps take every fourth
-// step of 16 TB tokens, each through a ring of asynchronous copies of its own (no
-// block barrier until the join).
+constexpr int kSplitTile = kWarps * 32;          // tokens; shares are counted in these tiles
+
+// Where a block's share of the split kernel's tiles begins. The tiles of all units
+// are lined up (the prefix's units first, then request by request) and cut into
+// equal shares, whatever the requests' lengths.
+struct Share {
+  int64_t g, end;                                // tiles [g, end) of all
+  int64_t share;                                 // tiles per block
+  int64_t first;                                 // tiles per unit of the requests before b
+  int b;
+};
+
+__device__ __forceinline__ int split_tiles(int tokens) {
+  return (tokens + kSplitTile - 1) / kSplitTile;
+}
+
+// Sums up the requests' tiles (each thread a run of requests) and finds the request
+// at which this block's share begins. Block 0 keeps the sums for the join.
+__device__ __forceinline__ Share find_share(const AttnArgs& a) {
+  __shared__ int64_t sums[kWarps];
+  __shared__ int64_t found_first;
+  __shared__ int found_b;
+  const int64_t pre_total = static_cast<int64_t>(a.pre_blocks) * a.pre_T;
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int lo = min(a.B, static_cast<int>(threadIdx.x) * per), hi = min(a.B, lo + per);
+  int64_t mine = 0;
+  if (a.own_tiles)
+    for (int r = lo; r < hi; ++r) mine += split_tiles(context_len(a, r, blockIdx.x == 0));
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(kAll, upto, o);
+    if ((threadIdx.x & 31) >= o) upto += x;
+  }
+  if ((threadIdx.x & 31) == 31) sums[threadIdx.x / 32] = upto;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < threadIdx.x / 32) upto += sums[w];
+    total += sums[w];
+  }
+  const int64_t units = static_cast<int64_t>(a.c.Hkv) * a.own_tiles;   // per request
+  Share s;
+  s.share = max(int64_t{1}, (pre_total + total * units + gridDim.x - 1) / gridDim.x);
+  s.g = blockIdx.x * s.share;
+  s.end = min(s.g + s.share, pre_total + total * units);
+  int64_t first = upto - mine;
+  const int64_t want = max(int64_t{0}, s.g - pre_total);
+  if (blockIdx.x == 0 || (want >= first * units && want < upto * units)) {
+    for (int r = lo; r < hi; ++r) {
+      const int n = split_tiles(context_len(a, r, false));
+      if (blockIdx.x == 0) a.first[r] = first;
+      if (want >= first * units && want < (first + n) * units) {
+        found_first = first;
+        found_b = r;
+      }
+      first += n;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.share_out = s.share;
+  __syncthreads();
+  s.first = found_first;                         // (read only if the share has own tiles)
+  s.b = found_b;
+  return s;
+}
+
+// One block takes its share piece by piece: a run of tiles of one unit, i.e. of one
+// context (a request's own tokens, or the prefix) for a tile of 8 NT query rows of one
+// key/value head. Its warps take every fourth step of 16 TB tokens, each through a ring
+// of asynchronous copies of its own (no block barrier until the join of the warps). A
+// unit in one piece gives the output itself, or the row's one partial result of that
+// context; the pieces of a cut unit go to the block's two slots.
 template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
+    attn_split_kernel(const AttnArgs a) {
   using G = Geo<D, BITS>;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(kAll, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int g = lane >> 2, t = lane & 3;
+  Share sh = find_share(a);
+  const int64_t first_g = sh.g;
+  const int64_t pre_total = static_cast<int64_t>(a.pre_blocks) * a.pre_T;
+  const int64_t units = static_cast<int64_t>(a.c.Hkv) * a.own_tiles;
+  while (sh.g < sh.end) {
   // ---- which work
-  int id = blockIdx.x;
-  const bool pre = id < a.pre_blocks;
-  int b = 0, split, tile, hk, n_rows, ctx, t0, chunk;
+  const bool pre = sh.g < pre_total;
+  int b = 0, tile, hk, n_rows, ctx, T;
+  int64_t unit_g;
   const int32_t* pages;
   if (pre) {
-    tile = id % a.pre_tiles;
-    id /= a.pre_tiles;
-    hk = id % a.c.Hkv;
-    split = id / a.c.Hkv;
+    const int u = static_cast<int>(sh.g / a.pre_T);
+    T = a.pre_T;
+    unit_g = static_cast<int64_t>(u) * T;
+    tile = u % a.pre_tiles;
+    hk = u / a.pre_tiles;
     n_rows = a.B * a.nq * a.G;
     ctx = a.prefix_len;
-    chunk = a.pre_chunk;
     pages = a.prefix_table;
   } else {
-    id -= a.pre_blocks;
-    tile = id % a.own_tiles;
-    id /= a.own_tiles;
-    hk = id % a.c.Hkv;
-    id /= a.c.Hkv;
-    split = id % a.own_splits;
-    b = id / a.own_splits;
+    const int64_t at = sh.g - pre_total;
+    ctx = context_len(a, sh.b, false);
+    T = split_tiles(ctx);
+    while (at >= (sh.first + T) * units) {       // the next request with any tokens
+      sh.first += T;
+      ctx = context_len(a, ++sh.b, false);
+      T = split_tiles(ctx);
+    }
+    b = sh.b;
+    const int u = static_cast<int>((at - sh.first * units) / T);
+    unit_g = pre_total + sh.first * units + static_cast<int64_t>(u) * T;
+    tile = u % a.own_tiles;
+    hk = u / a.own_tiles;
     n_rows = a.nq * a.G;
-    ctx = context_len(a, b, split == 0 && tile == 0 && hk == 0 && threadIdx.x == 0);
-    chunk = a.own_chunk;
     pages = a.table + static_cast<int64_t>(b) * a.table_stride;
   }
-  t0 = split * chunk;
+  const int64_t stop = min(sh.end, unit_g + T);
+  const bool whole = sh.g == unit_g && stop == unit_g + T;
+  const int slot = 2 * blockIdx.x + (sh.g != first_g);
   const int row0 = tile * 8 * NT;
   // the tile's last row sees most
   const auto limit = [&](int r) {
     return pre ? ctx : own_limit(a, ctx, r);
   };
-  const bool lone = a.pre_parts + a.own_parts == 1;
-  if (t0 >= ctx && !lone) return;              // (a lone split of nothing writes zeros)
-  const int t1 = min(min(t0 + chunk, ctx), limit(min(row0 + 8 * NT, n_rows) - 1));
+  const int t0 = static_cast<int>(sh.g - unit_g) * kSplitTile;
+  const int t1 = min(min(static_cast<int>(stop - unit_g) * kSplitTile, ctx),
+                     limit(min(row0 + 8 * NT, n_rows) - 1));
+  sh.g = stop;
 
   // ---- queries
   Warp<D, BITS, NT> w;
@@ -500,52 +617,45 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
   uint8_t* ring = smem + warp * G::kWarpBytes;
   constexpr int kStep = 16 * G::TB;
   const int steps = t1 > t0 ? (t1 - t0 + kStep - 1) / kStep : 0;
-  const int64_t head_k = static_cast<int64_t>(hk) * a.c.head_bytes;
-  const int64_t head_v = static_cast<int64_t>(hk + a.c.Hkv) * a.c.head_bytes;
-  const auto page_of = [&](int tok) {          // page number of a block's tokens, -1 past the end
-    if (tok >= t1) return -1;
-    const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
-    return __ldg(pages + static_cast<uint32_t>((blk * a.page_magic) >> 40));
-  };
-  int next[G::TB];                             // pages of the step after the one last requested
+  const uint8_t* lane_src = a.c.data + static_cast<int64_t>(hk) * a.c.head_bytes + lane * 16;
+  const int64_t to_values = static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes;
+  const uint32_t copy_k = smem_u32(ring) + G::copy_lane(lane, false);
+  const uint32_t copy_v = smem_u32(ring) + G::kCodes + G::copy_lane(lane, true);
+  const uint32_t copy_w = smem_u32(ring) + 2 * G::kCodes + lane * 16;
+  int page[G::TB], in_page[G::TB];             // of the step after the one last requested
   const auto look = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < G::TB; ++i)
-      next[i] = s < steps ? page_of(t0 + s * kStep + 16 * i) : -1;
+    for (int i = 0; i < G::TB; ++i) {
+      const int tok = t0 + s * kStep + 16 * i;
+      const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
+      const uint32_t at = static_cast<uint32_t>((blk * a.page_magic) >> 40);
+      in_page[i] = static_cast<int>(blk - at * a.page_blocks);
+      page[i] = tok < t1 ? __ldg(pages + at) : -1;
+    }
   };
   uint32_t absent = 0;                         // bit (stage, block): nothing was requested
   const auto request = [&](int s, int stage) {
 #pragma unroll
     for (int i = 0; i < G::TB; ++i) {
-      const int tok = t0 + s * kStep + 16 * i;
-      const int page = next[i];
-      const bool in = s < steps && tok < t1;
-      const bool ok = in && page >= 0 && page < a.c.pages;
+      const bool ok = static_cast<uint32_t>(page[i]) < static_cast<uint32_t>(a.c.pages);
       const uint32_t bit = 1u << (stage * G::TB + i);
       absent = ok ? absent & ~bit : absent | bit;
-      if (in && !ok && lane == 0) atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
       if (ok) {
-        const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
-        const uint32_t in_page =
-            blk - static_cast<uint32_t>((blk * a.page_magic) >> 40) * a.page_blocks;
-        const uint8_t* base = a.c.data + page * a.c.page_bytes;
-        uint8_t* dst = ring + stage * G::kStage + i * G::kBlock;
+        const uint8_t* src = lane_src + page[i] * a.c.page_bytes;
+        const uint8_t* codes = src + in_page[i] * G::kCodes;
+        const uint8_t* words = src + (a.c.code_bytes + in_page[i] * G::kWords);
+        const uint32_t at = stage * G::kStage + i * G::kBlock;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint8_t* src = base + (kv ? head_v : head_k);
-          const uint8_t* codes = src + in_page * G::kCodes;
-#pragma unroll
-          for (int c = 0; c < G::RB / 32; ++c) {
-            const int chunk16 = c * 32 + lane;
-            const int row = chunk16 / (G::RB / 16), at = chunk16 % (G::RB / 16);
-            const int u = kv ? G::value_unit(row, at >> 1) : G::key_unit(row, at >> 1);
-            cp_async16(dst + kv * G::kCodes + row * G::RB + u * 32 + (at & 1) * 16,
-                       codes + chunk16 * 16);
-          }
-          if (lane < G::kWords / 16)
-            cp_async16(dst + 2 * G::kCodes + kv * G::kWords + lane * 16,
-                       src + a.c.code_bytes + in_page * G::kWords + lane * 16);
+        for (int c = 0; c < G::RB / 32; ++c) {
+          cp_async16(copy_k + at + 512 * c, codes + 512 * c);
+          cp_async16((copy_v ^ G::copy_bits(c, true)) + at + 512 * c, codes + to_values + 512 * c);
         }
+        if (lane < G::kWords / 16) {
+          cp_async16(copy_w + at, words);
+          cp_async16(copy_w + G::kWords + at, words + to_values);
+        }
+      } else if (t0 + s * kStep + 16 * i < t1) {
+        if (lane == 0) atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
       }
     }
     cp_async_commit();
@@ -556,6 +666,7 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
     request(warp + s * kWarps, s);
     look(warp + (s + 1) * kWarps);
   }
+  const uint32_t key_off = G::key_lane(g, t), value_off = G::value_lane(g, t);
   int stage = 0;
   for (int s = warp; s < steps; s += kWarps) {
     {
@@ -572,9 +683,9 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
     for (int i = 0; i < G::TB; ++i) top[i] = gone >> i & 1 ? 0 : t1;
     const uint8_t* st = ring + stage * G::kStage;
     if (tok0 + kStep <= low && gone == 0)
-      w.template step<false>(st, tok0, top, lane);
+      w.template step<false>(st, tok0, top, g, key_off, value_off);
     else
-      w.template step<true>(st, tok0, top, lane);
+      w.template step<true>(st, tok0, top, g, key_off, value_off);
     __syncwarp();                              // the stage may be overwritten
     stage = stage == G::kStages - 1 ? 0 : stage + 1;
   }
@@ -606,7 +717,6 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
     }
   }
   __syncthreads();
-  const int64_t heads = static_cast<int64_t>(a.B) * a.nq * a.Hq;
   for (int i = threadIdx.x; i < 8 * NT * D / 4; i += kThreads) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     const int row = row0 + r;
@@ -631,23 +741,19 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnArgs a) 
     }
     const int qrow = pre ? row / a.G : b * a.nq + row / a.G;
     const int head = hk * a.G + row % a.G;
-    if (lone) {
+    if (whole && a.lone) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
       *reinterpret_cast<uint2*>(a.out + qrow * a.o_row + head * a.o_head + d) =
           make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
     } else {
-      const int64_t at = (pre ? split : a.pre_parts + split) * heads +
-                         static_cast<int64_t>(qrow) * a.Hq + head;
+      const int64_t at = whole ? (pre ? 0 : a.own_whole) + static_cast<int64_t>(qrow) * a.Hq + head
+                               : a.slots + static_cast<int64_t>(slot) * (8 * NT) + r;
       *reinterpret_cast<float4*>(a.part + at * D + d) = y;
       if (d == 0) a.ml[at] = make_float2(top, l);
     }
   }
-}
-
-// Parts that the row kernel made of a unit of T tiles, the first of which is tile
-// g of all: one per block that has a share of it.
-__device__ __forceinline__ int unit_parts(const AttnArgs& a, int64_t g, int T) {
-  return T > 0 ? static_cast<int>((g + T - 1) / a.share - g / a.share) + 1 : 0;
+  __syncthreads();                             // the join's buffer becomes the ring again
+  }
 }
 
 // Joins the parts of a query row and head: W warps each, which share the parts.
@@ -662,32 +768,63 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
   if (at >= heads) return;                       // (W == kWarps: at is the block's)
   const int row = static_cast<int>(at / a.Hq), head = static_cast<int>(at % a.Hq);
   const int hk = head / a.G, b = row / a.nq;
-  int n_pre = a.pre_parts, n_own = 0;
+  // Parts of each context: `n` of them; the first at p0, the second at p1, then p1 + step, ...
+  struct Parts {
+    int n = 0;
+    int64_t p0 = 0, p1 = 0, step = 0;
+    __device__ int64_t at(int i) const { return i == 0 ? p0 : p1 + (i - 1) * step; }
+  } parts[2];
+  // row kernel: part k of the row at (k * heads + row); split kernel: tiles [g, g + T)
+  const auto of_rows = [&](Parts& p, int64_t base, int64_t g, int T) {
+    p.n = T > 0 ? static_cast<int>((g + T - 1) / a.share - g / a.share) + 1 : 0;
+    p.p0 = base + at;
+    p.p1 = base + heads + at;
+    p.step = heads;
+  };
+  const auto of_split = [&](Parts& p, int64_t whole, int64_t g, int T, int r) {
+    if (T == 0) return;
+    const int64_t share = *a.share_out;
+    const int64_t k0 = g / share, k1 = (g + T - 1) / share;
+    const int rows = 8 * a.nt;
+    p.n = static_cast<int>(k1 - k0) + 1;
+    // a unit that begins inside a block's share is that block's second kind of piece
+    p.p0 = p.n == 1 ? whole + at : a.slots + (2 * k0 + (g != k0 * share)) * rows + r % rows;
+    p.p1 = a.slots + 2 * (k0 + 1) * rows + r % rows;
+    p.step = 2 * rows;
+  };
   if (a.pre_units) {
     const int u = hk * a.pre_row_tiles + (row * a.G + head % a.G) / a.unit_rows;
-    n_pre = unit_parts(a, static_cast<int64_t>(u) * a.pre_T, a.pre_T);
+    of_rows(parts[0], 0, static_cast<int64_t>(u) * a.pre_T, a.pre_T);
+  } else if (a.pre_blocks) {
+    const int r = row * a.G + head % a.G;
+    const int u = hk * a.pre_tiles + r / (8 * a.nt);
+    of_split(parts[0], 0, static_cast<int64_t>(u) * a.pre_T, a.pre_T, r);
   }
-  if (a.own_parts) {
+  if (a.own_units || a.own_tiles) {
     const int len = context_len(a, b, false);
+    const int r = row % a.nq * a.G + head % a.G;
     if (a.own_units) {
-      const int n_rows = a.nq * a.G;
-      const int rt = (row % a.nq * a.G + head % a.G) / a.unit_rows;
+      const int rt = r / a.unit_rows;
       const int u = (b * a.c.Hkv + hk) * a.own_row_tiles + unit_place(rt, a.own_row_tiles);
-      const int seen = own_limit(a, len, min((rt + 1) * a.unit_rows, n_rows) - 1);
-      n_own = unit_parts(a, static_cast<int64_t>(a.pre_units) * a.pre_T +
-                                static_cast<int64_t>(u) * a.own_T,
-                         (seen + kRowTile - 1) / kRowTile);
-      if (a.pre_parts == 0 && n_own == 1) return;   // the row kernel wrote the output
+      const int seen = own_limit(a, len, min((rt + 1) * a.unit_rows, a.nq * a.G) - 1);
+      of_rows(parts[1], a.own_whole, static_cast<int64_t>(a.pre_units) * a.pre_T +
+                                         static_cast<int64_t>(u) * a.own_T,
+              (seen + kRowTile - 1) / kRowTile);
     } else {
-      n_own = (len + a.own_chunk - 1) / a.own_chunk;
+      const int T = split_tiles(len);
+      const int64_t units = static_cast<int64_t>(a.c.Hkv) * a.own_tiles;
+      of_split(parts[1], a.own_whole,
+               static_cast<int64_t>(a.pre_blocks) * a.pre_T + a.first[b] * units +
+                   static_cast<int64_t>(hk * a.own_tiles + r / (8 * a.nt)) * T,
+               T, r);
     }
-  } else if (a.pre_units && n_pre == 1) {
-    return;
   }
+  if (a.lone && parts[0].n + parts[1].n == 1) return;   // its kernel wrote the output
+  const int n = parts[0].n + parts[1].n;
   float m = -INFINITY, l = 0.f, o[E] = {};
 #pragma unroll 4
-  for (int s = warp % W; s < n_pre + n_own; s += W) {
-    const int64_t i = (s < n_pre ? s : a.pre_parts + s - n_pre) * heads + at;
+  for (int s = warp % W; s < n; s += W) {
+    const int64_t i = s < parts[0].n ? parts[0].at(s) : parts[1].at(s - parts[0].n);
     const float2 ml = a.ml[i];
     float v[E];
 #pragma unroll
@@ -737,24 +874,15 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
 
 // How a call is cut into blocks.
 struct Plan {
-  int nt;                    // split kernel: row tiles of 8 nt
-  AttnArgs a;                // chunks, splits, units, shares and parts
-  unsigned split_blocks, row_blocks;
-  size_t ml, total;          // workspace: offset of the (m, l) pairs, size
+  AttnArgs a;                // units, shares and partial results
+  int64_t split_tiles;       // most tiles of the split kernel
+  unsigned row_blocks;
+  size_t ml, first, total;   // workspace: offsets of the (m, l) pairs and the tile sums, size
 };
 
 constexpr int kSMs = 152;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Splits of a context of `len` tokens that `units` blocks share out: enough for
-// several blocks per multiprocessor, each of at least 256 tokens.
-int chunk_of(int64_t len, int64_t units) {
-  constexpr int64_t kBlocks = kSMs * 8;
-  const int64_t splits = std::max<int64_t>(1, kBlocks / std::max<int64_t>(1, units));
-  const int64_t c = std::max<int64_t>(256, (len + splits - 1) / splits);
-  return static_cast<int>((std::min<int64_t>(c, std::max<int64_t>(len, 1)) + 127) / 128 * 128);
-}
 
 // Query rows of a key/value head from which the row kernel is taken.
 constexpr int64_t kRowKernelRows = 64;
@@ -765,13 +893,13 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
   AttnArgs& a = p.a;
   const int64_t G = Hq / Hkv;
   const int64_t own_rows = nq * G, pre_rows = B * nq * G;
-  const bool pre = prefix_len > 0, own = max_len > 0 || !pre;
+  const bool pre = prefix_len > 0, own = max_len > 0;
   const bool pre_tc = pre && pre_rows >= kRowKernelRows;
-  const bool own_tc = max_len > 0 && own_rows >= kRowKernelRows;
+  const bool own_tc = own && own_rows >= kRowKernelRows;
   // two column tiles share the conversion of the codes; at D = 256 their state
   // would not fit the registers
-  p.nt = D <= 128 && ((own && !own_tc && own_rows > 8) || (pre && !pre_tc && pre_rows > 8)) ? 2 : 1;
-  int64_t split_blocks = 0, tiles = 0;
+  a.nt = D <= 128 && ((own && !own_tc && own_rows > 8) || (pre && !pre_tc && pre_rows > 8)) ? 2 : 1;
+  int64_t split_tiles = 0, tiles = 0;
   a.unit_rows = attn_unit_rows(D);
   if (pre_tc) {
     a.pre_row_tiles = static_cast<int>(ceil_div(pre_rows, a.unit_rows));
@@ -781,12 +909,10 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
     if (units > 0x7FFFFFFF) return false;
     a.pre_units = static_cast<int>(units);
   } else if (pre) {
-    a.pre_tiles = static_cast<int>(ceil_div(pre_rows, 8 * p.nt));
-    a.pre_chunk = chunk_of(prefix_len, Hkv * a.pre_tiles);
-    a.pre_splits = a.pre_parts = static_cast<int>(ceil_div(prefix_len, a.pre_chunk));
-    split_blocks += Hkv * a.pre_tiles * a.pre_splits;
-    if (split_blocks > 0x7FFFFFFF) return false;
-    a.pre_blocks = static_cast<int>(split_blocks);
+    a.pre_tiles = static_cast<int>(ceil_div(pre_rows, 8 * a.nt));
+    a.pre_T = static_cast<int>(ceil_div(prefix_len, kSplitTile));
+    a.pre_blocks = static_cast<int>(Hkv) * a.pre_tiles;
+    split_tiles += static_cast<int64_t>(a.pre_blocks) * a.pre_T;
   }
   if (own_tc) {
     a.own_row_tiles = static_cast<int>(ceil_div(own_rows, a.unit_rows));
@@ -796,34 +922,41 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
     if (units > 0x7FFFFFFF) return false;
     a.own_units = static_cast<int>(units);
   } else if (own) {
-    a.own_tiles = static_cast<int>(ceil_div(own_rows, 8 * p.nt));
-    a.own_chunk = chunk_of(max_len, B * Hkv * a.own_tiles);
-    a.own_splits = a.own_parts = static_cast<int>(std::max<int64_t>(1, ceil_div(max_len, a.own_chunk)));
-    split_blocks += B * Hkv * a.own_tiles * a.own_splits;
+    a.own_tiles = static_cast<int>(ceil_div(own_rows, 8 * a.nt));
+    split_tiles += B * Hkv * a.own_tiles * ceil_div(max_len, kSplitTile);
   }
-  if (split_blocks > 0x7FFFFFFF) return false;
-  p.split_blocks = static_cast<unsigned>(split_blocks);
+  // one wave of blocks, or fewer with a tile each
+  int wave = 0;
+  for (int bits : {4, 8}) wave = std::max(wave, kSMs * split_blocks_per_sm(D, bits, a.nt));
+  p.split_tiles = split_tiles;
+  const int64_t slots = 2 * std::min<int64_t>(wave, split_tiles);
   if (tiles > 0) {
     const int64_t share = std::max<int64_t>(2, ceil_div(tiles, kSMs));
     if (share > 0x7FFFFFFF) return false;
     a.share = static_cast<int>(share);
     p.row_blocks = static_cast<unsigned>(ceil_div(tiles, share));
-    if (a.pre_units) a.pre_parts = static_cast<int>((a.pre_T - 1) / share + 2);
-    if (a.own_units) a.own_parts = static_cast<int>((a.own_T - 1) / share + 2);
   }
-  const size_t parts = static_cast<size_t>(a.pre_parts) + a.own_parts;
-  const size_t heads = static_cast<size_t>(B * nq * Hq);
-  if (parts > 1) {
-    p.ml = (parts * heads * D * 4 + 255) / 256 * 256;
-    p.total = p.ml + parts * heads * 8;
-  }
-  p.total = std::max<size_t>(256, (p.total + 255) / 256 * 256);
+  // partial results: the prefix's per row, the own tokens' per row, the split kernel's slots
+  const int64_t heads = B * nq * Hq;
+  const int64_t pre_parts = a.pre_units ? (a.pre_T - 1) / a.share + 2 : pre ? 1 : 0;
+  const int64_t own_parts = a.own_units ? (a.own_T - 1) / a.share + 2 : own && pre ? 1 : 0;
+  a.lone = !(pre && own);
+  a.own_whole = (a.lone && !a.pre_units ? 0 : pre_parts) * heads;
+  a.slots = a.own_whole + own_parts * heads;
+  if (a.lone && !a.pre_units && !a.own_units) a.slots = 0;   // whole pieces write the output
+  const int64_t n = a.slots + slots * 8 * a.nt;
+  p.ml = (static_cast<size_t>(n) * D * 4 + 255) / 256 * 256;
+  p.first = (p.ml + static_cast<size_t>(n) * 8 + 255) / 256 * 256;
+  p.total = p.first + (static_cast<size_t>(B) + 1) * 8;
+  p.total = (p.total + 255) / 256 * 256;
   *out = p;
   return true;
 }
 
 template <int D, int BITS, int NT>
-cudaError_t launch_split(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
+cudaError_t launch_split(const AttnArgs& a, int64_t tiles, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(
+      std::min<int64_t>(tiles, kSMs * split_blocks_per_sm(D, BITS, NT)));
   constexpr size_t smem = SplitSmem<D, BITS, NT>::kBytes;
   const auto kernel = attn_split_kernel<D, BITS, NT>;
   // (a per-device attribute; setting it again costs well under a microsecond)
@@ -839,21 +972,20 @@ cudaError_t launch(const AttnArgs& a, const Plan& p, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (p.row_blocks) e = launch_attn_rows(a, p.row_blocks, s);
   if (e != cudaSuccess) return e;
-  if (p.split_blocks) {
+  if (p.split_tiles) {
     if constexpr (D <= 128) {
-      if (p.nt == 2)
-        e = a.c.bits == 8 ? launch_split<D, 8, 2>(a, p.split_blocks, s)
-                          : launch_split<D, 4, 2>(a, p.split_blocks, s);
+      if (a.nt == 2)
+        e = a.c.bits == 8 ? launch_split<D, 8, 2>(a, p.split_tiles, s)
+                          : launch_split<D, 4, 2>(a, p.split_tiles, s);
     }
-    if (p.nt == 1)
-      e = a.c.bits == 8 ? launch_split<D, 8, 1>(a, p.split_blocks, s)
-                        : launch_split<D, 4, 1>(a, p.split_blocks, s);
+    if (a.nt == 1)
+      e = a.c.bits == 8 ? launch_split<D, 8, 1>(a, p.split_tiles, s)
+                        : launch_split<D, 4, 1>(a, p.split_tiles, s);
   }
-  const int parts = a.pre_parts + a.own_parts;
-  if (e != cudaSuccess || parts == 1) return e;
+  if (e != cudaSuccess) return e;
   const int64_t heads = static_cast<int64_t>(a.B) * a.nq * a.Hq;
-  // many parts: a block's warps share a row's; few: a warp per row
-  if (parts > 8)
+  // few rows of many parts: a block's warps share a row's; else a warp per row
+  if (heads <= kSMs * 16)
     return launch_pdl(attn_join_kernel<D, kWarps>, dim3(static_cast<unsigned>(heads)),
                       dim3(kThreads), 0, s, a);
   return launch_pdl(attn_join_kernel<D, 1>, dim3(static_cast<unsigned>(ceil_div(heads, kWarps))),
@@ -931,6 +1063,8 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
   k.page_magic = (1ull << 40) / k.page_blocks + 1;
   k.part = static_cast<float*>(ws);
   k.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml);
+  k.share_out = reinterpret_cast<int64_t*>(static_cast<char*>(ws) + p.first);
+  k.first = k.share_out + 1;
   k.timeout_ns = wait_timeout_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = c->D == 64    ? launch<64>(k, p, s)

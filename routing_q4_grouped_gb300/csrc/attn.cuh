@@ -11,9 +11,9 @@
 namespace moeq4 {
 
 // A call's contexts: the prefix (all query rows of the batch see it whole) and the
-// requests' own tokens. Each is worked on by the split kernel (fixed chunks of
-// tokens, few query rows per block) or by the row kernel (128 or 256 query rows
-// per unit, a unit's tiles of 128 tokens cut where a block's share ends).
+// requests' own tokens. Each is worked on by the split kernel (few query rows per unit)
+// or by the row kernel (128 or 256 query rows per unit). Both line up the tiles of 128
+// tokens of all their units and give every block an equal share of them.
 struct AttnArgs {
   const uint16_t* q;
   uint16_t* out;
@@ -24,18 +24,24 @@ struct AttnArgs {
   KvCache c;
   uint32_t page_blocks;      // 16-token blocks per page
   uint64_t page_magic;       // floor(2^40 / page_blocks) + 1
-  // split kernel: blocks [0, pre_blocks) take the prefix, the rest the requests' own tokens
-  int pre_chunk, pre_splits, pre_tiles, pre_blocks;
-  int own_chunk, own_splits, own_tiles;
-  // row kernel: units of unit_rows query rows; nominal tiles of 128 tokens per unit
+  // split kernel: units of 8 nt query rows
+  int nt;
+  int pre_blocks, pre_tiles;             // units of the prefix, and per key/value head (0: not here)
+  int own_tiles;                         // units per request and key/value head (0: not here)
+  int64_t* share_out;                    // tiles per block, found on the device
+  int64_t* first;                        // [B] tiles per unit of the requests before b
+  // row kernel: units of unit_rows query rows, by the largest length
   int unit_rows;
-  int pre_units, pre_T, own_units, own_T;
+  int pre_units, own_units;              // (0: not here)
   int pre_row_tiles, own_row_tiles;      // units per key/value head (and request)
-  int share;                             // tiles per block
-  // partial results; parts of the prefix first
-  int pre_parts, own_parts;              // most parts of a row (0: no such context)
-  float* part;               // [part][row][head][D]
-  float2* ml;                // [part][row][head]: (m, l)
+  int own_T, share;                      // tiles per unit and per block
+  int pre_T;                             // tiles of the prefix, either kernel
+  // partial results, D values and (m, l) each: the prefix's at [part][row][head], the own
+  // tokens' from own_whole on, the split kernel's slots [block][2][8 nt] from slots on
+  int lone;                              // one context only: a unit in one piece gives the output
+  int64_t own_whole, slots;
+  float* part;
+  float2* ml;
   uint64_t timeout_ns;
 };
 

@@ -765,9 +765,10 @@ struct Softmax {
     if (nt > 1) w.wait(&ctl.pv_done[wg], (pc + nt - 2) & 1);
     w.wait(&ctl.pv_done[wg], (pc + nt - 1) & 1);
     tc_fence_after();
-    const bool lone = (a.pre_parts == 0 || a.own_parts == 0) && sg.kt0 == 0 && sg.kt1 == sg.tiles;
+    const bool lone = a.lone && sg.kt0 == 0 && sg.kt1 == sg.tiles;
     const float up = exp2_approx(E) * (lone ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
-    const int64_t at = (static_cast<int64_t>(sg.pre ? 0 : a.pre_parts) + sg.part) * a.B * a.nq * a.Hq +
+    const int64_t at = (sg.pre ? 0 : a.own_whole) +
+                       static_cast<int64_t>(sg.part) * a.B * a.nq * a.Hq +
                        static_cast<int64_t>(qrow) * a.Hq + head;
     if (live && !lone) a.ml[at] = make_float2(m, l);
     uint16_t* out = a.out + qrow * a.o_row + head * a.o_head;
