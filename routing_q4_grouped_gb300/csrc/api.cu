@@ -387,6 +387,11 @@ std::atomic<int> g_nevents{0};
 
 }  // namespace
 
+int32_t check_device() {
+  DevInfo di;
+  return device_info(&di);
+}
+
 uint64_t wait_timeout_ns() { return timeout_ns(); }
 
 void stage_mark(int i, cudaStream_t s) {

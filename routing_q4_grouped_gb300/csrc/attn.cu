@@ -480,6 +480,11 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = __shfl_sync(kAll, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int g = lane >> 2, t = lane & 3;
+  // After the row kernel this one depends on nothing that kernel writes, only on what it
+  // waited for itself before it let this one start; it takes over multiprocessors as
+  // they come free and waits at its end, for the join.
+  if (!a.pre_units) griddep_wait();
+  griddep_launch_dependents();
   Share sh = find_share(a);
   const int64_t first_g = sh.g;
   const int64_t pre_total = static_cast<int64_t>(a.pre_blocks) * a.pre_T;
@@ -528,6 +533,60 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
   const int t1 = min(min(static_cast<int>(stop - unit_g) * kSplitTile, ctx),
                      limit(min(row0 + 8 * NT, n_rows) - 1));
   sh.g = stop;
+
+  // ---- tokens: the first copies are on their way while the queries are prepared
+  uint8_t* ring = smem + warp * G::kWarpBytes;
+  constexpr int kStep = 16 * G::TB;
+  const int steps = t1 > t0 ? (t1 - t0 + kStep - 1) / kStep : 0;
+  const uint8_t* lane_src = a.c.data + static_cast<int64_t>(hk) * a.c.head_bytes + lane * 16;
+  const int64_t to_values = static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes;
+  const uint32_t copy_k = smem_u32(ring) + G::copy_lane(lane, false);
+  const uint32_t copy_v = smem_u32(ring) + G::kCodes + G::copy_lane(lane, true);
+  const uint32_t copy_w = smem_u32(ring) + 2 * G::kCodes + lane * 16;
+  int page[G::TB], in_page[G::TB];             // of the step after the one last requested
+  const auto look = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < G::TB; ++i) {
+      const int tok = t0 + s * kStep + 16 * i;
+      const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
+      const uint32_t at = static_cast<uint32_t>((blk * a.page_magic) >> 40);
+      in_page[i] = static_cast<int>(blk - at * a.page_blocks);
+      page[i] = tok < t1 ? __ldg(pages + at) : -1;
+    }
+  };
+  uint32_t absent = 0;                         // bit (stage, block): nothing was requested
+  const auto request = [&](int s, int stage) {
+#pragma unroll
+    for (int i = 0; i < G::TB; ++i) {
+      const bool ok = static_cast<uint32_t>(page[i]) < static_cast<uint32_t>(a.c.pages);
+      const uint32_t bit = 1u << (stage * G::TB + i);
+      absent = ok ? absent & ~bit : absent | bit;
+      if (ok) {
+        const uint8_t* src = lane_src + page[i] * a.c.page_bytes;
+        const uint8_t* codes = src + in_page[i] * G::kCodes;
+        const uint8_t* words = src + (a.c.code_bytes + in_page[i] * G::kWords);
+        const uint32_t at = stage * G::kStage + i * G::kBlock;
+#pragma unroll
+        for (int c = 0; c < G::RB / 32; ++c) {
+          cp_async16(copy_k + at + 512 * c, codes + 512 * c);
+          cp_async16((copy_v ^ G::copy_bits(c, true)) + at + 512 * c, codes + to_values + 512 * c);
+        }
+        if (lane < G::kWords / 16) {
+          cp_async16(copy_w + at, words);
+          cp_async16(copy_w + G::kWords + at, words + to_values);
+        }
+      } else if (t0 + s * kStep + 16 * i < t1) {
+        if (lane == 0) atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
+      }
+    }
+    cp_async_commit();
+  };
+  look(warp);
+#pragma unroll
+  for (int s = 0; s < G::kStages - 1; ++s) {
+    request(warp + s * kWarps, s);
+    look(warp + (s + 1) * kWarps);
+  }
 
   // ---- queries
   Warp<D, BITS, NT> w;
@@ -613,59 +672,7 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
   for (int n = 0; n < NT; ++n) low = min(low, min(w.lim[n][0], w.lim[n][1]));
   low = __reduce_min_sync(kAll, low);
 
-  // ---- tokens
-  uint8_t* ring = smem + warp * G::kWarpBytes;
-  constexpr int kStep = 16 * G::TB;
-  const int steps = t1 > t0 ? (t1 - t0 + kStep - 1) / kStep : 0;
-  const uint8_t* lane_src = a.c.data + static_cast<int64_t>(hk) * a.c.head_bytes + lane * 16;
-  const int64_t to_values = static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes;
-  const uint32_t copy_k = smem_u32(ring) + G::copy_lane(lane, false);
-  const uint32_t copy_v = smem_u32(ring) + G::kCodes + G::copy_lane(lane, true);
-  const uint32_t copy_w = smem_u32(ring) + 2 * G::kCodes + lane * 16;
-  int page[G::TB], in_page[G::TB];             // of the step after the one last requested
-  const auto look = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < G::TB; ++i) {
-      const int tok = t0 + s * kStep + 16 * i;
-      const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
-      const uint32_t at = static_cast<uint32_t>((blk * a.page_magic) >> 40);
-      in_page[i] = static_cast<int>(blk - at * a.page_blocks);
-      page[i] = tok < t1 ? __ldg(pages + at) : -1;
-    }
-  };
-  uint32_t absent = 0;                         // bit (stage, block): nothing was requested
-  const auto request = [&](int s, int stage) {
-#pragma unroll
-    for (int i = 0; i < G::TB; ++i) {
-      const bool ok = static_cast<uint32_t>(page[i]) < static_cast<uint32_t>(a.c.pages);
-      const uint32_t bit = 1u << (stage * G::TB + i);
-      absent = ok ? absent & ~bit : absent | bit;
-      if (ok) {
-        const uint8_t* src = lane_src + page[i] * a.c.page_bytes;
-        const uint8_t* codes = src + in_page[i] * G::kCodes;
-        const uint8_t* words = src + (a.c.code_bytes + in_page[i] * G::kWords);
-        const uint32_t at = stage * G::kStage + i * G::kBlock;
-#pragma unroll
-        for (int c = 0; c < G::RB / 32; ++c) {
-          cp_async16(copy_k + at + 512 * c, codes + 512 * c);
-          cp_async16((copy_v ^ G::copy_bits(c, true)) + at + 512 * c, codes + to_values + 512 * c);
-        }
-        if (lane < G::kWords / 16) {
-          cp_async16(copy_w + at, words);
-          cp_async16(copy_w + G::kWords + at, words + to_values);
-        }
-      } else if (t0 + s * kStep + 16 * i < t1) {
-        if (lane == 0) atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
-      }
-    }
-    cp_async_commit();
-  };
-  look(warp);
-#pragma unroll
-  for (int s = 0; s < G::kStages - 1; ++s) {
-    request(warp + s * kWarps, s);
-    look(warp + (s + 1) * kWarps);
-  }
+
   const uint32_t key_off = G::key_lane(g, t), value_off = G::value_lane(g, t);
   int stage = 0;
   for (int s = warp; s < steps; s += kWarps) {
@@ -754,6 +761,7 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
   }
   __syncthreads();                             // the join's buffer becomes the ring again
   }
+  if (a.pre_units) griddep_wait();
 }
 
 // Joins the parts of a query row and head: W warps each, which share the parts.
@@ -959,12 +967,10 @@ cudaError_t launch_split(const AttnArgs& a, int64_t tiles, cudaStream_t s) {
       std::min<int64_t>(tiles, kSMs * split_blocks_per_sm(D, BITS, NT)));
   constexpr size_t smem = SplitSmem<D, BITS, NT>::kBytes;
   const auto kernel = attn_split_kernel<D, BITS, NT>;
-  // (a per-device attribute; setting it again costs well under a microsecond)
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  kernel<<<blocks, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, s, a);
 }
 
 template <int D>
@@ -1040,6 +1046,7 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
       !make_plan(a->B, a->nq, a->Hq, c->Hkv, c->D, a->max_len, a->prefix_len, &p))
     return MOE_ERR_SHAPE;
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+  if ((st = check_device()) != MOE_OK) return st;
   AttnArgs& k = p.a;
   k.q = a->q;
   k.out = a->out;

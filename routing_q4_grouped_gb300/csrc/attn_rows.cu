@@ -835,6 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
+  griddep_wait();
+  griddep_launch_dependents();
   Waiter w{&ctl, a.c.err, a.timeout_ns, true};
 
   // counts of tiles, uses of the logit slots and products into each O so far
@@ -925,11 +927,10 @@ cudaError_t launch_rows(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
   constexpr size_t smem = row_smem<D>();
   static_assert(smem <= 227 * 1024, "shared memory");
   const auto kernel = attn_rows_kernel<D, BITS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  kernel<<<blocks, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, s, a);
 }
 
 }  // namespace

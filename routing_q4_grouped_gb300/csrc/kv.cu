@@ -97,6 +97,8 @@ struct alignas(V * sizeof(E) > 16 ? 16 : V * sizeof(E)) Vec {
 // once and used for every head of the block.
 template <typename E, int V>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int u = static_cast<int>(id % a.units);
   const int64_t th = id / a.units;
@@ -175,8 +177,7 @@ cudaError_t launch_rope_v(RopeArgs a, cudaStream_t s) {
   const int64_t n = static_cast<int64_t>(a.T) * a.units * a.head_blocks;
   const int64_t blocks = (n + kThreads - 1) / kThreads;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  rope_kernel<E, V><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(rope_kernel<E, V>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, a);
 }
 
 template <typename E>
@@ -274,6 +275,8 @@ template <int BITS>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   const int runs = a.c.D / 8;
   const int heads = a.Hq + 2 * a.c.Hkv;
+  griddep_wait();
+  griddep_launch_dependents();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int run = static_cast<int>(id % runs);
   const int64_t th = id / runs;
@@ -354,6 +357,8 @@ template <int BITS>
 __global__ void __launch_bounds__(kThreads) read_kernel(KvCache c, const int32_t* slots, int n,
                                                         uint16_t* k_out, uint16_t* v_out) {
   const int runs = c.D / 16;
+  griddep_wait();
+  griddep_launch_dependents();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int run = static_cast<int>(id % runs);
   const int64_t th = id / runs;
@@ -475,6 +480,7 @@ extern "C" moe_status moe_rope(const void* x, int64_t x_row, int64_t x_head, voi
   if (x == out && (x_row != out_row || x_head != out_head)) return MOE_ERR_ARG;
   const unsigned es = dtype == MOE_F32 ? 4 : 2;
   if (bad_align(x, es) || bad_align(out, es) || bad_align(pos, 4)) return MOE_ERR_ALIGN;
+  if ((st = check_device()) != MOE_OK) return st;
   RopeArgs a{};
   a.x = x;
   a.out = out;
@@ -550,11 +556,10 @@ extern "C" moe_status moe_kv_append(const moe_kv_new* n, const moe_kv_cache* c, 
   const int64_t blocks = (threads + kThreads - 1) / kThreads;
   if (blocks > 0x7FFFFFFF) return MOE_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (c->bits == 8)
-    append_kernel<8><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
-  else
-    append_kernel<4><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if ((st = check_device()) != MOE_OK) return st;
+  const cudaError_t e = launch_pdl(c->bits == 8 ? append_kernel<8> : append_kernel<4>,
+                                   dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, a);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" moe_status moe_kv_read(const moe_kv_cache* c, const int32_t* slots, int32_t n,
@@ -571,9 +576,9 @@ extern "C" moe_status moe_kv_read(const moe_kv_cache* c, const int32_t* slots, i
   if (blocks > 0x7FFFFFFF) return MOE_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const KvCache k = kv_cache_args(*c);
-  if (c->bits == 8)
-    read_kernel<8><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(k, slots, n, k_out, v_out);
-  else
-    read_kernel<4><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(k, slots, n, k_out, v_out);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if ((st = check_device()) != MOE_OK) return st;
+  const cudaError_t e =
+      launch_pdl(c->bits == 8 ? read_kernel<8> : read_kernel<4>,
+                 dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, k, slots, n, k_out, v_out);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

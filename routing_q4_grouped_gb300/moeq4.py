@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct
 
 import torch
 
@@ -120,13 +121,12 @@ _SIGS = {
     "moe_residual_rms": (_c_i32, [_c_ptr, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr]),
     "moe_rope_phases": (_c_i32, [_c_ptr, _c_i32, _c_f64, _c_i32, _c_f64, _c_f64, _c_f64, _c_f64]),
     "moe_rope": (_c_i32, [_c_ptr, _c_i64, _c_i64, _c_ptr, _c_i64, _c_i64, _c_ptr, _c_i32, _c_i32,
-                          _c_i32, ctypes.POINTER(RopeSpecC), _c_i32, _c_i32, _c_ptr]),
+                          _c_i32, _c_ptr, _c_i32, _c_i32, _c_ptr]),
     "moe_kv_cache_size": (_c_size, [_c_i32] * 5),
-    "moe_kv_append": (_c_i32, [ctypes.POINTER(KVNewC), ctypes.POINTER(KVCacheC), _c_ptr]),
-    "moe_kv_read": (_c_i32, [ctypes.POINTER(KVCacheC), _c_ptr, _c_i32, _c_ptr, _c_ptr, _c_ptr]),
+    "moe_kv_append": (_c_i32, [_c_ptr, _c_ptr, _c_ptr]),
+    "moe_kv_read": (_c_i32, [_c_ptr, _c_ptr, _c_i32, _c_ptr, _c_ptr, _c_ptr]),
     "moe_kv_attention_workspace_size": (_c_size, [_c_i32] * 7),
-    "moe_kv_attention": (_c_i32, [ctypes.POINTER(KVAttnC), ctypes.POINTER(KVCacheC), _c_ptr,
-                                  _c_size, _c_ptr]),
+    "moe_kv_attention": (_c_i32, [_c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "moe_debug_dequant": (_c_i32, [_c_ptr, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr, _c_ptr]),
     "moe_debug_mma": (_c_i32, [_c_i32, _c_ptr, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr]),
     "moe_debug_set_stage_events": (_c_i32, [ctypes.POINTER(_c_ptr), _c_i32]),
@@ -172,9 +172,21 @@ def _need(fn, t, dtype, name, optional=False):
         raise ValueError(f"{fn}: {name} must be a contiguous {dtype} CUDA tensor, got {got}")
 
 
+def _current_stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+try:   # the same handle without building a Stream object (saves about a microsecond per call)
+    from torch._C import _cuda_getCurrentRawStream, _cuda_getDevice
+
+    def _current_stream() -> int:                                          # noqa: F811
+        return _cuda_getCurrentRawStream(_cuda_getDevice())
+except ImportError:
+    pass
+
+
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    return _current_stream() if stream is None else stream.cuda_stream
 
 
 # ----------------------------------------------------------------- host-side sizes
@@ -429,6 +441,7 @@ class RopeSpec:
             raise ValueError(f"RopeSpec: phase must hold rot/2 = {rot // 2} values, got {phase.numel()}")
         self.phase, self.rot, self.interleaved, self.mscale = phase, rot, interleaved, mscale
         self._c = RopeSpecC(_ptr(phase), rot, int(interleaved), mscale)
+        self._addr = ctypes.addressof(self._c)
 
 
 def moe_kv_cache_size(pages, page_size, Hkv, D, bits) -> int:
@@ -454,6 +467,7 @@ class KVCache:
         self.err = torch.zeros(4, dtype=torch.int32, device=data.device) if err is None else err
         _need("KVCache", self.err, torch.int32, "err")
         self._c = KVCacheC(_ptr(data), _ptr(self.err), self.pages, page_size, Hkv, D, bits)
+        self._addr = ctypes.addressof(self._c)
 
     @classmethod
     def alloc(cls, pages, page_size, Hkv, D, bits, device="cuda"):
@@ -464,20 +478,31 @@ class KVCache:
         return cls(torch.empty(n, dtype=torch.uint8, device=device), page_size, Hkv, D, bits)
 
 
-def _need_rows(fn, t, name, D=None, dtype=torch.bfloat16):
-    """[rows][heads][elements] with dense elements; rows and heads may be strided."""
-    if (t is None or not t.is_cuda or t.dtype != dtype or t.dim() != 3 or t.stride(2) != 1
-            or (D is not None and t.shape[2] != D)):
-        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
-        raise ValueError(f"{fn}: {name} must be a {dtype} CUDA tensor [rows][heads]"
-                         f"[{'D' if D is None else D}] with dense elements, got {got}")
+# moe_kv_new and moe_kv_attn as packed bytes (native alignment, as the C compiler lays
+# them out): a fraction of the time that filling a ctypes structure takes.
+_KV_NEW = struct.Struct("@PqqPqqPqqPqqPPPii")
+_KV_ATTN = struct.Struct("@PqqPqqPPPiiiiiif4x")
 
 
-def _need_ints(fn, t, n, name):
-    if t is None or not t.is_cuda or t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
-        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"
-        raise ValueError(f"{fn}: {name} must be a contiguous int32 CUDA tensor of at least {n} "
-                         f"values, got {got}")
+def _rows(fn, t, name, D=None, dtype=torch.bfloat16):
+    """(shape, pointer, row stride, head stride) of [rows][heads][elements] with dense
+    elements; rows and heads may be strided."""
+    if t is not None and t.is_cuda and t.dtype is dtype:
+        shape, st = t.shape, t.stride()
+        if len(shape) == 3 and st[2] == 1 and (D is None or shape[2] == D):
+            return shape, t.data_ptr(), st[0], st[1]
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
+    raise ValueError(f"{fn}: {name} must be a {dtype} CUDA tensor [rows][heads]"
+                     f"[{'D' if D is None else D}] with dense elements, got {got}")
+
+
+def _ints(fn, t, n, name):
+    """Pointer of a dense int32 array of at least n values."""
+    if t is not None and t.is_cuda and t.dtype is torch.int32 and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"
+    raise ValueError(f"{fn}: {name} must be a contiguous int32 CUDA tensor of at least {n} "
+                     f"values, got {got}")
 
 
 _ROPE_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
@@ -490,15 +515,15 @@ def moe_rope(x: torch.Tensor, out: torch.Tensor, pos: torch.Tensor, rope: RopeSp
     dtype = _ROPE_DTYPES.get(x.dtype)
     if dtype is None:
         raise ValueError(f"moe_rope: x must be bfloat16, float16 or float32, got {x.dtype}")
-    _need_rows("moe_rope", x, "x", dtype=x.dtype)
-    T, H, D = x.shape
-    _need_rows("moe_rope", out, "out", D, x.dtype)
-    if out.shape != x.shape:
-        raise ValueError(f"moe_rope: out must have x's shape {tuple(x.shape)}, got {tuple(out.shape)}")
-    _need_ints("moe_rope", pos, T, "pos")
-    _check("moe_rope", lib().moe_rope(_ptr(x), x.stride(0), x.stride(1), _ptr(out), out.stride(0),
-                                      out.stride(1), _ptr(pos), T, H, D, ctypes.byref(rope._c),
-                                      int(backward), dtype, _stream(stream)))
+    shape, xp, xr, xh = _rows("moe_rope", x, "x", None, x.dtype)
+    T, H, D = shape
+    oshape, op, orow, oh = _rows("moe_rope", out, "out", D, x.dtype)
+    if oshape != shape:
+        raise ValueError(f"moe_rope: out must have x's shape {tuple(shape)}, got {tuple(oshape)}")
+    st = lib().moe_rope(xp, xr, xh, op, orow, oh, _ints("moe_rope", pos, T, "pos"), T, H, D,
+                        rope._addr, backward, dtype, _stream(stream))
+    if st:
+        _check("moe_rope", st)
 
 
 def moe_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -508,40 +533,41 @@ def moe_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
     ``slots`` [T] (-1: skip). Without ``rope`` the keys are stored as given and q must be None."""
     fn = "moe_kv_append"
     D = cache.D
-    _need_rows(fn, k, "k", D)
-    _need_rows(fn, v, "v", D)
-    T = k.shape[0]
-    if k.shape[1] != cache.Hkv or v.shape != k.shape:
-        raise ValueError(f"{fn}: k and v must be [T][{cache.Hkv}][{D}], got {tuple(k.shape)} and "
-                         f"{tuple(v.shape)}")
-    _need_ints(fn, slots, T, "slots")
-    a = KVNewC(_ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1))
-    a.slots, a.T = _ptr(slots), T
-    if rope is not None:
-        _need_ints(fn, pos, T, "pos")
-        a.pos, a.rope = _ptr(pos), ctypes.pointer(rope._c)
+    shape, kp, kr, kh = _rows(fn, k, "k", D)
+    vshape, vp, vr, vh = _rows(fn, v, "v", D)
+    T = shape[0]
+    if shape[1] != cache.Hkv or vshape != shape:
+        raise ValueError(f"{fn}: k and v must be [T][{cache.Hkv}][{D}], got {tuple(shape)} and "
+                         f"{tuple(vshape)}")
+    qp = qr = qh = op = orow = oh = Hq = 0
     if q is not None:
-        _need_rows(fn, q, "q", D)
-        _need_rows(fn, q_out, "q_out", D)
-        if q.shape[0] != T or q_out.shape != q.shape:
-            raise ValueError(f"{fn}: q and q_out must be [{T}][Hq][{D}], got {tuple(q.shape)} and "
-                             f"{tuple(q_out.shape)}")
-        a.q, a.q_row, a.q_head, a.Hq = _ptr(q), q.stride(0), q.stride(1), q.shape[1]
-        a.q_out, a.qo_row, a.qo_head = _ptr(q_out), q_out.stride(0), q_out.stride(1)
-    _check(fn, lib().moe_kv_append(ctypes.byref(a), ctypes.byref(cache._c), _stream(stream)))
+        qshape, qp, qr, qh = _rows(fn, q, "q", D)
+        oshape, op, orow, oh = _rows(fn, q_out, "q_out", D)
+        if qshape[0] != T or oshape != qshape:
+            raise ValueError(f"{fn}: q and q_out must be [{T}][Hq][{D}], got {tuple(qshape)} and "
+                             f"{tuple(oshape)}")
+        Hq = qshape[1]
+    a = _KV_NEW.pack(kp, kr, kh, vp, vr, vh, qp, qr, qh, op, orow, oh, _ints(fn, slots, T, "slots"),
+                     0 if rope is None else _ints(fn, pos, T, "pos"),
+                     0 if rope is None else rope._addr, T, Hq)
+    st = lib().moe_kv_append(a, cache._addr, _stream(stream))
+    if st:
+        _check(fn, st)
 
 
 def moe_kv_read(cache: KVCache, slots: torch.Tensor, k_out: torch.Tensor = None,
                 v_out: torch.Tensor = None, stream=None) -> None:
     """Cache rows of ``slots`` [n] as bf16 [n, Hkv, D]; k_out or v_out may be None."""
     fn, n = "moe_kv_read", slots.numel()
-    _need_ints(fn, slots, 0, "slots")
+    sp = _ints(fn, slots, 0, "slots")
+    shape = (n, cache.Hkv, cache.D)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         _need(fn, t, torch.bfloat16, name, optional=True)
-        if t is not None and t.shape != (n, cache.Hkv, cache.D):
+        if t is not None and t.shape != shape:
             raise ValueError(f"{fn}: {name} must be [{n}][{cache.Hkv}][{cache.D}], got {tuple(t.shape)}")
-    _check(fn, lib().moe_kv_read(ctypes.byref(cache._c), _ptr(slots), n, _ptr(k_out), _ptr(v_out),
-                                 _stream(stream)))
+    st = lib().moe_kv_read(cache._addr, sp, n, _ptr(k_out), _ptr(v_out), _stream(stream))
+    if st:
+        _check(fn, st)
 
 
 def moe_kv_attention_workspace_size(B, nq, Hq, Hkv, D, max_len, prefix_len=0) -> int:
@@ -558,25 +584,25 @@ def moe_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens:
     batch), then its own ``lens[b]`` tokens in the pages ``table[b]``, the last nq of which are
     its query tokens (causal among themselves). ``scale`` defaults to 1/sqrt(D)."""
     fn, D = "moe_kv_attention", cache.D
-    _need_rows(fn, q, "q", D)
-    _need_rows(fn, out, "out", D)
-    rows, Hq, _ = q.shape
-    if nq < 1 or rows % nq or out.shape != q.shape:
+    shape, qp, qr, qh = _rows(fn, q, "q", D)
+    oshape, op, orow, oh = _rows(fn, out, "out", D)
+    rows, Hq = shape[0], shape[1]
+    if nq < 1 or rows % nq or oshape != shape:
         raise ValueError(f"{fn}: q and out must be [B*nq][Hq][{D}] with nq={nq}, got "
-                         f"{tuple(q.shape)} and {tuple(out.shape)}")
+                         f"{tuple(shape)} and {tuple(oshape)}")
     B = rows // nq
-    _need_ints(fn, lens, B, "lens")
     if table is None or table.dim() != 2 or table.shape[0] != B:
         raise ValueError(f"{fn}: table must be an int32 tensor of {B} rows of pages")
-    _need_ints(fn, table, 0, "table")
-    if prefix_len:
-        _need_ints(fn, prefix_table, -(-prefix_len // cache.page_size), "prefix_table")
     _need(fn, ws, torch.uint8, "ws")
-    a = KVAttnC(_ptr(q), q.stride(0), q.stride(1), _ptr(out), out.stride(0), out.stride(1),
-                _ptr(table), _ptr(lens), _ptr(prefix_table), B, nq, Hq, table.shape[1], max_len,
-                prefix_len, D ** -0.5 if scale is None else scale)
-    _check(fn, lib().moe_kv_attention(ctypes.byref(a), ctypes.byref(cache._c), _ptr(ws), ws.numel(),
-                                      _stream(stream)))
+    pp = 0
+    if prefix_len:
+        pp = _ints(fn, prefix_table, -(-prefix_len // cache.page_size), "prefix_table")
+    a = _KV_ATTN.pack(qp, qr, qh, op, orow, oh, _ints(fn, table, 0, "table"),
+                      _ints(fn, lens, B, "lens"), pp, B, nq, Hq, table.shape[1], max_len, prefix_len,
+                      D ** -0.5 if scale is None else scale)
+    st = lib().moe_kv_attention(a, cache._addr, ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _check(fn, st)
 
 
 def moe_get_device_error(r: "RouteBuffers | KVCache", stream=None) -> int:
