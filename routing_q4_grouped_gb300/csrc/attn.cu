@@ -10,22 +10,21 @@
 // Few rows read many codes, so the work is bound by memory bandwidth as long as
 // turning codes into tensor-core operands costs less than the bytes. Two choices
 // keep it cheap:
-//  * Codes go into the products as integers. A byte c under the byte 0x64 is the
-//    fp16 number 1024 + c, so one byte permutation makes an operand pair. With
-//    value = s c + b and q' the query in fp16,
-//      q . k = sum over groups of  s (sum (1024 + c) q' - 1024 sum q') + b sum q',
-//    where the first difference is the accumulator's initial value. Values are
-//    centred ((1024 + c) - 1152, exact) and their scale is taken into the weights:
-//      sum_t p_t v_t = sum_t (p_t s_t)(c_t - 128) + sum_t p_t (b_t + 128 s_t).
+//  * Codes go into the products as integers. A code c alone in the low bits of an fp16
+//    is the subnormal number c 2^-24, which the tensor cores take at full rate, so
+//    one byte permutation or mask makes an operand pair. With value = s c + b,
+//      q . k = sum over groups of  s sum c q + b sum q,
+//    and the values' scale is taken into the weights:
+//      sum_t p_t v_t = sum_t (p_t s_t) c_t + sum_t p_t b_t.
 //  * Tokens are the rows (M) of the products and queries the columns (N = 8), so
 //    that 8 rows fill the tensor core: X^T = K Q^T, then O^T = V^T P^T. The
 //    products' own register layouts let a thread read 16 (keys) or 8 (values)
 //    neighbouring codes of a token at once; P is transposed between the two
 //    products by one 8x8 register transpose per 8 tokens and group.
-// q' and p s are fp16: q' is the query divided by the power of two under its
-// row's largest element, p s is multiplied by a factor f of the row that keeps its
-// largest p s near 1, so neither leaves fp16's range and both keep 11 bits (one
-// rounding of 2^-11 for the weights; bf16 queries are exact above 2^-16 of their
+// q' and p s are fp16: q' is the query scaled by a power of two so that its row's
+// largest element is near 2^12, p s is multiplied by a factor f of the row that keeps
+// its largest p s near 1, so neither leaves fp16's range and both keep 11 bits (one
+// rounding of 2^-11 for the weights; bf16 queries are exact above 2^-26 of their
 // row's largest element). Logits, maxima, sums and outputs are fp32.
 #include <algorithm>
 #include <cmath>
@@ -148,13 +147,12 @@ template <int D, int BITS, int NT>
 struct Warp {
   using G = Geo<D, BITS>;
   uint32_t q[NT][G::J][8];        // queries: B operand of X^T = K Q^T
-  float init[NT][G::J][2];        // -1024 * sum of the operand's elements, by group
-  float qsum[NT][G::J][2];        // sum of q' by group
-  float row_scale[NT][2];         // scale2 * 2^(row exponent)
+  float qsum[NT][G::J][2];        // 2^-24 * sum of q' by group
+  float row_scale[NT][2];         // scale2 * 2^(24 + row exponent)
   int lim[NT][2];                 // tokens seen by the row
   float m[NT][2], l[NT][2];
   float o[NT][G::J][4][4];        // O^T: group, tile of 16 elements
-  float ob[NT][G::J][2];          // sum of p * centred bias
+  float ob[NT][G::J][2];          // sum of p * bias
   float e[NT][2], f[NT][2];       // f = 2^-e: p s f stays below 2^15
   float top_x[NT][2], top_ps[NT][2];   // m + 8, m + e + 14: the bounds of a logit and of log2(p s) + m
 
@@ -209,18 +207,18 @@ struct Warp {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][i] = init[n][j][i & 1];
+          for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           uint32_t a[4];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             if (BITS == 8) {
-              a[r] = prmt(w[r][s], 0x64646464u, 0x4140);
-              a[2 + r] = prmt(w[r][s], 0x64646464u, 0x4342);
+              a[r] = prmt(w[r][s], 0u, 0x4140);
+              a[2 + r] = prmt(w[r][s], 0u, 0x4342);
             } else {
-              a[r] = lop3_and_or(w[r][s], 0x000F000Fu, 0x64006400u);
-              a[2 + r] = lop3_and_or(w[r][s], 0x00F000F0u, 0x64006400u);
+              a[r] = w[r][s] & 0x000F000Fu;
+              a[2 + r] = w[r][s] & 0x00F000F0u;        // 16 c
             }
           }
 #pragma unroll
@@ -293,7 +291,7 @@ struct Warp {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float s = bf16_lo(vw[b][r][j]);
-          const float bias = fmaf(BITS == 8 ? 128.f : 8.f, s, bf16_hi(vw[b][r][j]));
+          const float bias = bf16_hi(vw[b][r][j]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const float p0 = x[b][n][2 * r], p1 = x[b][n][2 * r + 1];
@@ -328,19 +326,17 @@ struct Warp {
             if (BITS == 8) {
               const uint32_t lo = prmt(w[2 * k][h], w[2 * k + 1][h], 0x5140);
               const uint32_t hi = prmt(w[2 * k][h], w[2 * k + 1][h], 0x7362);
-              constexpr uint32_t kC = 0x64806480u;     // 1024 + 128
-              a[0][2 * k] = sub_f16x2(prmt(lo, 0x64646464u, 0x4140), kC);
-              a[0][2 * k + 1] = sub_f16x2(prmt(lo, 0x64646464u, 0x4342), kC);
-              a[1][2 * k] = sub_f16x2(prmt(hi, 0x64646464u, 0x4140), kC);
-              a[1][2 * k + 1] = sub_f16x2(prmt(hi, 0x64646464u, 0x4342), kC);
+              a[0][2 * k] = prmt(lo, 0u, 0x4140);
+              a[0][2 * k + 1] = prmt(lo, 0u, 0x4342);
+              a[1][2 * k] = prmt(hi, 0u, 0x4140);
+              a[1][2 * k + 1] = prmt(hi, 0u, 0x4342);
             } else {
               // odd elements stay multiplied by 16 until the end
               const uint32_t v = prmt(w[2 * k][0], w[2 * k + 1][0], h ? 0x7632 : 0x5410);
-              constexpr uint32_t kC = 0x64086408u, kC16 = 0x64806480u;   // 1024 + 8, 1024 + 128
-              a[0][2 * k] = sub_f16x2(lop3_and_or(v, 0x000F000Fu, 0x64006400u), kC);
-              a[0][2 * k + 1] = sub_f16x2(lop3_and_or(v, 0x00F000F0u, 0x64006400u), kC16);
-              a[1][2 * k] = sub_f16x2(lop3_and_or(v >> 8, 0x000F000Fu, 0x64006400u), kC);
-              a[1][2 * k + 1] = sub_f16x2(lop3_and_or(v >> 8, 0x00F000F0u, 0x64006400u), kC16);
+              a[0][2 * k] = v & 0x000F000Fu;
+              a[0][2 * k + 1] = v & 0x00F000F0u;
+              a[1][2 * k] = v >> 8 & 0x000F000Fu;
+              a[1][2 * k + 1] = v >> 8 & 0x00F000F0u;
             }
           }
 #pragma unroll
@@ -543,19 +539,28 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
   const uint32_t copy_k = smem_u32(ring) + G::copy_lane(lane, false);
   const uint32_t copy_v = smem_u32(ring) + G::kCodes + G::copy_lane(lane, true);
   const uint32_t copy_w = smem_u32(ring) + 2 * G::kCodes + lane * 16;
-  int page[G::TB], in_page[G::TB];             // of the step after the one last requested
-  const auto look = [&](int s) {
+  // page and 16-token block within it of the step after the one last requested; a
+  // warp's next step is kWarps TB blocks further
+  int page[G::TB], in_page[G::TB], at_page[G::TB], tok_next = t0 + warp * kStep;
+#pragma unroll
+  for (int i = 0; i < G::TB; ++i) {
+    const uint32_t blk = static_cast<uint32_t>(tok_next >> 4) + i;
+    at_page[i] = static_cast<int>((blk * a.page_magic) >> 40);
+    in_page[i] = static_cast<int>(blk - at_page[i] * a.page_blocks);
+    page[i] = tok_next + 16 * i < t1 ? __ldg(pages + at_page[i]) : -1;
+  }
+  const auto look = [&]() {
+    tok_next += kWarps * kStep;
 #pragma unroll
     for (int i = 0; i < G::TB; ++i) {
-      const int tok = t0 + s * kStep + 16 * i;
-      const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
-      const uint32_t at = static_cast<uint32_t>((blk * a.page_magic) >> 40);
-      in_page[i] = static_cast<int>(blk - at * a.page_blocks);
-      page[i] = tok < t1 ? __ldg(pages + at) : -1;
+      at_page[i] += a.skip_pages[G::TB - 1];
+      in_page[i] += a.skip_blocks[G::TB - 1];
+      if (in_page[i] >= static_cast<int>(a.page_blocks)) in_page[i] -= a.page_blocks, ++at_page[i];
+      page[i] = tok_next + 16 * i < t1 ? __ldg(pages + at_page[i]) : -1;
     }
   };
   uint32_t absent = 0;                         // bit (stage, block): nothing was requested
-  const auto request = [&](int s, int stage) {
+  const auto request = [&](int stage) {
 #pragma unroll
     for (int i = 0; i < G::TB; ++i) {
       const bool ok = static_cast<uint32_t>(page[i]) < static_cast<uint32_t>(a.c.pages);
@@ -575,17 +580,16 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
           cp_async16(copy_w + at, words);
           cp_async16(copy_w + G::kWords + at, words + to_values);
         }
-      } else if (t0 + s * kStep + 16 * i < t1) {
+      } else if (tok_next + 16 * i < t1) {
         if (lane == 0) atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
       }
     }
     cp_async_commit();
   };
-  look(warp);
 #pragma unroll
   for (int s = 0; s < G::kStages - 1; ++s) {
-    request(warp + s * kWarps, s);
-    look(warp + (s + 1) * kWarps);
+    request(s);
+    look();
   }
 
   // ---- queries
@@ -623,10 +627,12 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
     mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
     const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
-    const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
+    // q' reaches 2^12 .. 2^13: subnormals only below 2^-26 of the row's largest element
+    const float down = __uint_as_float((254u - e) << 23) * 4096.f;
+    const float up = __uint_as_float(e << 23) * 4096.f;         // 2^-12 * 2^24
 #pragma unroll
     for (int j = 0; j < G::J; ++j) {
-      float all = 0.f, in = 0.f;
+      float all = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         // operand pairs in the order the codes come out of a word: neighbours of a
@@ -637,17 +643,13 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
         const uint32_t p = pack_f16(qv[j][e0] * z, qv[j][e1] * z);
         w.q[n][j][i] = p;
         const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&p));
-        in += back.x + back.y;
         all += (back.x + back.y) * (BITS == 4 && (i & 1) ? 16.f : 1.f);
       }
-      in += __shfl_xor_sync(kAll, in, 1);
-      in += __shfl_xor_sync(kAll, in, 2);
       all += __shfl_xor_sync(kAll, all, 1);
       all += __shfl_xor_sync(kAll, all, 2);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {            // of the columns this thread accumulates
-        w.init[n][j][c] = -1024.f * __shfl_sync(kAll, in, (2 * t + c) * 4);
-        w.qsum[n][j][c] = __shfl_sync(kAll, all, (2 * t + c) * 4);
+        w.qsum[n][j][c] = __shfl_sync(kAll, all, (2 * t + c) * 4) * 0x1p-24f;
         w.ob[n][j][c] = 0.f;
       }
 #pragma unroll
@@ -678,8 +680,8 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
   for (int s = warp; s < steps; s += kWarps) {
     {
       const int free = stage == 0 ? G::kStages - 1 : stage - 1;
-      request(s + (G::kStages - 1) * kWarps, free);
-      look(s + G::kStages * kWarps);
+      request(free);
+      look();
     }
     cp_async_wait<G::kStages - 1>();
     __syncwarp();
@@ -709,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
     for (int c = 0; c < 2; ++c) {
       const int r = 8 * n + 2 * t + c;
       const float l = sum_over_rows8(w.l[n][c]);
-      const float up = 1.f / w.f[n][c];
+      const float up = 0x1p24f / w.f[n][c];
       if (g == 0) sml[warp * 8 * NT + r] = make_float2(w.m[n][c], l);
 #pragma unroll
       for (int j = 0; j < G::J; ++j) {
@@ -1068,6 +1070,10 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
   k.c = kv_cache_args(*c);
   k.page_blocks = static_cast<uint32_t>(c->page_size / 16);
   k.page_magic = (1ull << 40) / k.page_blocks + 1;
+  for (int tb = 1; tb <= 2; ++tb) {
+    k.skip_pages[tb - 1] = kWarps * tb / static_cast<int>(k.page_blocks);
+    k.skip_blocks[tb - 1] = kWarps * tb % static_cast<int>(k.page_blocks);
+  }
   k.part = static_cast<float*>(ws);
   k.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml);
   k.share_out = reinterpret_cast<int64_t*>(static_cast<char*>(ws) + p.first);

@@ -24,6 +24,7 @@ struct AttnArgs {
   KvCache c;
   uint32_t page_blocks;      // 16-token blocks per page
   uint64_t page_magic;       // floor(2^40 / page_blocks) + 1
+  int skip_pages[2], skip_blocks[2];     // four blocks further, and eight
   // split kernel: units of 8 nt query rows
   int nt;
   int pre_blocks, pre_tiles;             // units of the prefix, and per key/value head (0: not here)

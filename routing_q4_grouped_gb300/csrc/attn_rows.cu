@@ -9,13 +9,14 @@
 //   P = exp2(X - m)             tensor memory -> registers -> tensor memory, one
 //                               thread per row, fp16, in place of X
 //   O[rows, D] += P V           A = P from tensor memory, B = V^T in shared memory
-// Codes are turned into fp16 operands once per tile, for all rows of the unit: with
-// c exact from a byte (1024 + c) - 1024, value = s c + b is one fp16 fma, one
-// rounding of 2^-11.
+// Codes are turned into fp16 operands once per tile, for all rows of the unit. A code
+// c alone in the low bits of an fp16 is the subnormal c 2^-24, so value = s c + b is
+// one fp16 fma with 2^24 s, with one rounding of 2^-11.
 //
 // fp16's range. Queries are divided by the power of two under their row's largest
-// element. A tile's keys and values are divided by powers of two 2^eK and 2^eV near
-// their largest magnitude; eK goes into the logits' factor, and 2^eV into the
+// element. A tile's keys and values are divided by powers of two 2^eK and 2^eV 2^8 above
+// their largest magnitude (so 2^24 s fits, and what is 2^-8 of the largest is still a
+// normal number); eK goes into the logits' factor, and 2^eV into the
 // weights' exponent: P' = exp2(x - m + eV - E) with a running E per row, so P' stays
 // near 1 whatever the values' size. A tile whose tokens differ by more than 2^6 in
 // magnitude takes one exponent per token (the same formulas with a factor per
@@ -77,8 +78,8 @@ struct RowGeo {
 template <int D>
 struct alignas(16) Meta {
   static constexpr int J = RowGeo<D>::J;
-  uint16_t vs[J][128], vb[J][128];     // values: scale, bias (fp16, divided by 2^e)
-  uint32_t ksb[J][128];                // keys: scale | bias << 16
+  uint16_t vs[J][128], vb[J][128];     // values: scale * 2^24, bias (fp16, divided by 2^e)
+  uint32_t ksb[J][128];                // keys: the same, bias in the high half
   float kf[128];                       // 2^eK of each token (slow tiles)
   float ve[128];                       // eV of each token (slow tiles)
   uint8_t flag[128];                   // bit j: value group j is NaN; kDead
@@ -364,11 +365,11 @@ struct Converter {
       E[i] = hi == 0 ? 127 : min(hi, 253);
     }
     const uint32_t eu = slow && valid && e ? min(e, 253u) : static_cast<uint32_t>(E[kv]);
-    const float down = pow2_field(254u - eu);
+    const float down = pow2_field(254u - eu) * 0x1p-8f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const bool nan = bad >> j & 1;
-      const float s = valid && !nan ? bf16_lo(w[j]) * down : 0.f;
+      const float s = valid && !nan ? bf16_lo(w[j]) * down * 0x1p24f : 0.f;
       const float b = valid && !nan ? bf16_hi(w[j]) * down : 0.f;
       uint32_t sb = pack_f16(s, b);
       if (kv == 0) {
@@ -380,14 +381,14 @@ struct Converter {
       }
     }
     if (kv == 0) {
-      m.kf[tk] = pow2_field(eu);
+      m.kf[tk] = pow2_field(eu) * 0x1p8f;
     } else {
-      m.ve[tk] = static_cast<float>(static_cast<int>(eu) - 127);
+      m.ve[tk] = static_cast<float>(static_cast<int>(eu) - 119);
       m.flag[tk] = static_cast<uint8_t>(bad | (tk < n && !valid ? kDead : 0));
     }
     if (ct == 0) {
-      m.tile_kf = pow2_field(static_cast<uint32_t>(E[0]));
-      m.tile_ve = static_cast<float>(E[1] - 127);
+      m.tile_kf = pow2_field(static_cast<uint32_t>(E[0])) * 0x1p8f;
+      m.tile_ve = static_cast<float>(E[1] - 119);
       m.slow = slow;
     }
     conv_bar();
@@ -403,20 +404,19 @@ struct Converter {
       const uint32_t sb = m.ksb[j][row];
       const uint32_t s2 = prmt(sb, sb, 0x1010), b2 = prmt(sb, sb, 0x3232);
       uint32_t r[8];
-      constexpr uint32_t k1024 = 0x64006400u;
       if constexpr (BITS == 8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          r[2 * i] = fma_f16x2(s2, sub_f16x2(prmt(kr[u][i], k1024 >> 8, 0x4140), k1024), b2);
-          r[2 * i + 1] = fma_f16x2(s2, sub_f16x2(prmt(kr[u][i], k1024 >> 8, 0x4342), k1024), b2);
+          r[2 * i] = fma_f16x2(s2, prmt(kr[u][i], 0u, 0x4140), b2);
+          r[2 * i + 1] = fma_f16x2(s2, prmt(kr[u][i], 0u, 0x4342), b2);
         }
       } else {
         const uint32_t s16 = fma_f16x2(s2, 0x2C002C00u, 0u);      // scale / 16
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = i & 1 ? kr[u][i >> 1] >> 8 : kr[u][i >> 1];
-          r[2 * i] = fma_f16x2(s2, sub_f16x2(lop3_and_or(w, 0x000F000Fu, k1024), k1024), b2);
-          r[2 * i + 1] = fma_f16x2(s16, sub_f16x2(lop3_and_or(w, 0x00F000F0u, k1024), k1024), b2);
+          r[2 * i] = fma_f16x2(s2, w & 0x000F000Fu, b2);
+          r[2 * i + 1] = fma_f16x2(s16, w & 0x00F000F0u, b2);
         }
       }
       uint8_t* dst = smem + off + j * 16384 + row * 128;
@@ -442,7 +442,6 @@ struct Converter {
       const uint4 bv = *reinterpret_cast<const uint4*>(&m.vb[j][th * 64 + tg * 8]);
       const uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
       uint8_t* dst = smem + off + th * (D * 128) + d0 * 128;
-      constexpr uint32_t k1024 = 0x64006400u;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {                 // elements 4h .. 4h + 3
         uint32_t r[4][4];                           // [element][token pair]
@@ -451,17 +450,17 @@ struct Converter {
           if constexpr (BITS == 8) {
             const uint32_t x = vr[u][2 * p][h], y = vr[u][2 * p + 1][h];
             const uint32_t lo = prmt(x, y, 0x5140), hi = prmt(x, y, 0x7362);
-            r[0][p] = fma_f16x2(s[p], sub_f16x2(prmt(lo, k1024 >> 8, 0x4140), k1024), b[p]);
-            r[1][p] = fma_f16x2(s[p], sub_f16x2(prmt(lo, k1024 >> 8, 0x4342), k1024), b[p]);
-            r[2][p] = fma_f16x2(s[p], sub_f16x2(prmt(hi, k1024 >> 8, 0x4140), k1024), b[p]);
-            r[3][p] = fma_f16x2(s[p], sub_f16x2(prmt(hi, k1024 >> 8, 0x4342), k1024), b[p]);
+            r[0][p] = fma_f16x2(s[p], prmt(lo, 0u, 0x4140), b[p]);
+            r[1][p] = fma_f16x2(s[p], prmt(lo, 0u, 0x4342), b[p]);
+            r[2][p] = fma_f16x2(s[p], prmt(hi, 0u, 0x4140), b[p]);
+            r[3][p] = fma_f16x2(s[p], prmt(hi, 0u, 0x4342), b[p]);
           } else {
             const uint32_t v = prmt(vr[u][2 * p][0], vr[u][2 * p + 1][0], h ? 0x7632 : 0x5410);
             const uint32_t s16 = fma_f16x2(s[p], 0x2C002C00u, 0u);
-            r[0][p] = fma_f16x2(s[p], sub_f16x2(lop3_and_or(v, 0x000F000Fu, k1024), k1024), b[p]);
-            r[1][p] = fma_f16x2(s16, sub_f16x2(lop3_and_or(v, 0x00F000F0u, k1024), k1024), b[p]);
-            r[2][p] = fma_f16x2(s[p], sub_f16x2(lop3_and_or(v >> 8, 0x000F000Fu, k1024), k1024), b[p]);
-            r[3][p] = fma_f16x2(s16, sub_f16x2(lop3_and_or(v >> 8, 0x00F000F0u, k1024), k1024), b[p]);
+            r[0][p] = fma_f16x2(s[p], v & 0x000F000Fu, b[p]);
+            r[1][p] = fma_f16x2(s16, v & 0x00F000F0u, b[p]);
+            r[2][p] = fma_f16x2(s[p], v >> 8 & 0x000F000Fu, b[p]);
+            r[3][p] = fma_f16x2(s16, v >> 8 & 0x00F000F0u, b[p]);
           }
         }
 #pragma unroll
