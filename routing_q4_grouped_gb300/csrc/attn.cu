@@ -402,9 +402,9 @@ constexpr int kSplitTile = kWarps * 32;          // tokens; shares are counted i
 // are lined up (the prefix's units first, then request by request) and cut into
 // equal shares, whatever the requests' lengths.
 struct Share {
-  int64_t g, end;                                // tiles [g, end) of all
-  int64_t share;                                 // tiles per block
-  int64_t first;                                 // tiles per unit of the requests before b
+  int g, end;                                // tiles [g, end) of all
+  int share;                                 // tiles per block
+  int first;                                 // tiles per unit of the requests before b
   int b;
 };
 
@@ -415,36 +415,36 @@ __device__ __forceinline__ int split_tiles(int tokens) {
 // Sums up the requests' tiles (each thread a run of requests) and finds the request
 // at which this block's share begins. Block 0 keeps the sums for the join.
 __device__ __forceinline__ Share find_share(const AttnArgs& a) {
-  __shared__ int64_t sums[kWarps];
-  __shared__ int64_t found_first;
+  __shared__ int sums[kWarps];
+  __shared__ int found_first;
   __shared__ int found_b;
-  const int64_t pre_total = static_cast<int64_t>(a.pre_blocks) * a.pre_T;
+  const int pre_total = a.pre_blocks * a.pre_T;
   const int per = (a.B + kThreads - 1) / kThreads;
   const int lo = min(a.B, static_cast<int>(threadIdx.x) * per), hi = min(a.B, lo + per);
-  int64_t mine = 0;
+  int mine = 0;
   if (a.own_tiles)
     for (int r = lo; r < hi; ++r) mine += split_tiles(context_len(a, r, blockIdx.x == 0));
-  int64_t upto = mine;
+  int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(kAll, upto, o);
+    const int x = __shfl_up_sync(kAll, upto, o);
     if ((threadIdx.x & 31) >= o) upto += x;
   }
   if ((threadIdx.x & 31) == 31) sums[threadIdx.x / 32] = upto;
   __syncthreads();
-  int64_t total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < threadIdx.x / 32) upto += sums[w];
     total += sums[w];
   }
-  const int64_t units = static_cast<int64_t>(a.c.Hkv) * a.own_tiles;   // per request
+  const int units = a.c.Hkv * a.own_tiles;   // per request
   Share s;
-  s.share = max(int64_t{1}, (pre_total + total * units + gridDim.x - 1) / gridDim.x);
+  s.share = max(1, static_cast<int>((pre_total + total * units + gridDim.x - 1) / gridDim.x));
   s.g = blockIdx.x * s.share;
   s.end = min(s.g + s.share, pre_total + total * units);
-  int64_t first = upto - mine;
-  const int64_t want = max(int64_t{0}, s.g - pre_total);
+  int first = upto - mine;
+  const int want = max(0, s.g - pre_total);
   if (blockIdx.x == 0 || (want >= first * units && want < upto * units)) {
     for (int r = lo; r < hi; ++r) {
       const int n = split_tiles(context_len(a, r, false));
@@ -482,26 +482,26 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
   if (!a.pre_units) griddep_wait();
   griddep_launch_dependents();
   Share sh = find_share(a);
-  const int64_t first_g = sh.g;
-  const int64_t pre_total = static_cast<int64_t>(a.pre_blocks) * a.pre_T;
-  const int64_t units = static_cast<int64_t>(a.c.Hkv) * a.own_tiles;
+  const int first_g = sh.g;
+  const int pre_total = a.pre_blocks * a.pre_T;
+  const int units = a.c.Hkv * a.own_tiles;
   while (sh.g < sh.end) {
   // ---- which work
   const bool pre = sh.g < pre_total;
   int b = 0, tile, hk, n_rows, ctx, T;
-  int64_t unit_g;
+  int unit_g;
   const int32_t* pages;
   if (pre) {
-    const int u = static_cast<int>(sh.g / a.pre_T);
+    const int u = sh.g / a.pre_T;
     T = a.pre_T;
-    unit_g = static_cast<int64_t>(u) * T;
+    unit_g = u * T;
     tile = u % a.pre_tiles;
     hk = u / a.pre_tiles;
     n_rows = a.B * a.nq * a.G;
     ctx = a.prefix_len;
     pages = a.prefix_table;
   } else {
-    const int64_t at = sh.g - pre_total;
+    const int at = sh.g - pre_total;
     ctx = context_len(a, sh.b, false);
     T = split_tiles(ctx);
     while (at >= (sh.first + T) * units) {       // the next request with any tokens
@@ -510,14 +510,14 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
       T = split_tiles(ctx);
     }
     b = sh.b;
-    const int u = static_cast<int>((at - sh.first * units) / T);
-    unit_g = pre_total + sh.first * units + static_cast<int64_t>(u) * T;
+    const int u = (at - sh.first * units) / T;
+    unit_g = pre_total + sh.first * units + u * T;
     tile = u % a.own_tiles;
     hk = u / a.own_tiles;
     n_rows = a.nq * a.G;
     pages = a.table + static_cast<int64_t>(b) * a.table_stride;
   }
-  const int64_t stop = min(sh.end, unit_g + T);
+  const int stop = min(sh.end, unit_g + T);
   const bool whole = sh.g == unit_g && stop == unit_g + T;
   const int slot = 2 * blockIdx.x + (sh.g != first_g);
   const int row0 = tile * 8 * NT;
@@ -525,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
   const auto limit = [&](int r) {
     return pre ? ctx : own_limit(a, ctx, r);
   };
-  const int t0 = static_cast<int>(sh.g - unit_g) * kSplitTile;
-  const int t1 = min(min(static_cast<int>(stop - unit_g) * kSplitTile, ctx),
+  const int t0 = (sh.g - unit_g) * kSplitTile;
+  const int t1 = min(min((stop - unit_g) * kSplitTile, ctx),
                      limit(min(row0 + 8 * NT, n_rows) - 1));
   sh.g = stop;
 
@@ -778,6 +778,10 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
   if (at >= heads) return;                       // (W == kWarps: at is the block's)
   const int row = static_cast<int>(at / a.Hq), head = static_cast<int>(at % a.Hq);
   const int hk = head / a.G, b = row / a.nq;
+  // (loads that do not wait for each other)
+  const int len = a.own_units || a.own_tiles ? context_len(a, b, false) : 0;
+  const int first = a.own_tiles ? a.first[b] : 0;
+  const int share = a.pre_blocks || a.own_tiles ? *a.share_out : 1;
   // Parts of each context: `n` of them; the first at p0, the second at p1, then p1 + step, ...
   struct Parts {
     int n = 0;
@@ -785,48 +789,43 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
     __device__ int64_t at(int i) const { return i == 0 ? p0 : p1 + (i - 1) * step; }
   } parts[2];
   // row kernel: part k of the row at (k * heads + row); split kernel: tiles [g, g + T)
-  const auto of_rows = [&](Parts& p, int64_t base, int64_t g, int T) {
-    p.n = T > 0 ? static_cast<int>((g + T - 1) / a.share - g / a.share) + 1 : 0;
+  const auto of_rows = [&](Parts& p, int64_t base, int g, int T) {
+    p.n = T > 0 ? (g + T - 1) / a.share - g / a.share + 1 : 0;
     p.p0 = base + at;
     p.p1 = base + heads + at;
     p.step = heads;
   };
-  const auto of_split = [&](Parts& p, int64_t whole, int64_t g, int T, int r) {
+  const auto of_split = [&](Parts& p, int64_t whole, int g, int T, int r) {
     if (T == 0) return;
-    const int64_t share = *a.share_out;
-    const int64_t k0 = g / share, k1 = (g + T - 1) / share;
+    const int k0 = g / share, k1 = (g + T - 1) / share;
     const int rows = 8 * a.nt;
-    p.n = static_cast<int>(k1 - k0) + 1;
+    p.n = k1 - k0 + 1;
     // a unit that begins inside a block's share is that block's second kind of piece
-    p.p0 = p.n == 1 ? whole + at : a.slots + (2 * k0 + (g != k0 * share)) * rows + r % rows;
-    p.p1 = a.slots + 2 * (k0 + 1) * rows + r % rows;
+    p.p0 = p.n == 1 ? whole + at : a.slots + static_cast<int64_t>(2 * k0 + (g != k0 * share)) * rows + r % rows;
+    p.p1 = a.slots + static_cast<int64_t>(2 * (k0 + 1)) * rows + r % rows;
     p.step = 2 * rows;
   };
   if (a.pre_units) {
     const int u = hk * a.pre_row_tiles + (row * a.G + head % a.G) / a.unit_rows;
-    of_rows(parts[0], 0, static_cast<int64_t>(u) * a.pre_T, a.pre_T);
+    of_rows(parts[0], 0, u * a.pre_T, a.pre_T);
   } else if (a.pre_blocks) {
     const int r = row * a.G + head % a.G;
     const int u = hk * a.pre_tiles + r / (8 * a.nt);
-    of_split(parts[0], 0, static_cast<int64_t>(u) * a.pre_T, a.pre_T, r);
+    of_split(parts[0], 0, u * a.pre_T, a.pre_T, r);
   }
   if (a.own_units || a.own_tiles) {
-    const int len = context_len(a, b, false);
     const int r = row % a.nq * a.G + head % a.G;
     if (a.own_units) {
       const int rt = r / a.unit_rows;
       const int u = (b * a.c.Hkv + hk) * a.own_row_tiles + unit_place(rt, a.own_row_tiles);
       const int seen = own_limit(a, len, min((rt + 1) * a.unit_rows, a.nq * a.G) - 1);
-      of_rows(parts[1], a.own_whole, static_cast<int64_t>(a.pre_units) * a.pre_T +
-                                         static_cast<int64_t>(u) * a.own_T,
+      of_rows(parts[1], a.own_whole, a.pre_units * a.pre_T + u * a.own_T,
               (seen + kRowTile - 1) / kRowTile);
     } else {
       const int T = split_tiles(len);
-      const int64_t units = static_cast<int64_t>(a.c.Hkv) * a.own_tiles;
+      const int units = a.c.Hkv * a.own_tiles;
       of_split(parts[1], a.own_whole,
-               static_cast<int64_t>(a.pre_blocks) * a.pre_T + a.first[b] * units +
-                   static_cast<int64_t>(hk * a.own_tiles + r / (8 * a.nt)) * T,
-               T, r);
+               a.pre_blocks * a.pre_T + first * units + (hk * a.own_tiles + r / (8 * a.nt)) * T, T, r);
     }
   }
   if (a.lone && parts[0].n + parts[1].n == 1) return;   // its kernel wrote the output
@@ -939,6 +938,7 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
   int wave = 0;
   for (int bits : {4, 8}) wave = std::max(wave, kSMs * split_blocks_per_sm(D, bits, a.nt));
   p.split_tiles = split_tiles;
+  if (split_tiles > (1 << 30) || tiles > (1 << 30)) return false;   // the kernels count them in 32 bits
   const int64_t slots = 2 * std::min<int64_t>(wave, split_tiles);
   if (tiles > 0) {
     const int64_t share = std::max<int64_t>(2, ceil_div(tiles, kSMs));
@@ -957,7 +957,7 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
   const int64_t n = a.slots + slots * 8 * a.nt;
   p.ml = (static_cast<size_t>(n) * D * 4 + 255) / 256 * 256;
   p.first = (p.ml + static_cast<size_t>(n) * 8 + 255) / 256 * 256;
-  p.total = p.first + (static_cast<size_t>(B) + 1) * 8;
+  p.total = p.first + (static_cast<size_t>(B) + 1) * 4;
   p.total = (p.total + 255) / 256 * 256;
   *out = p;
   return true;
@@ -1076,7 +1076,7 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
   }
   k.part = static_cast<float*>(ws);
   k.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml);
-  k.share_out = reinterpret_cast<int64_t*>(static_cast<char*>(ws) + p.first);
+  k.share_out = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + p.first);
   k.first = k.share_out + 1;
   k.timeout_ns = wait_timeout_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);

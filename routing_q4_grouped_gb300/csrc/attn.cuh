@@ -29,8 +29,8 @@ struct AttnArgs {
   int nt;
   int pre_blocks, pre_tiles;             // units of the prefix, and per key/value head (0: not here)
   int own_tiles;                         // units per request and key/value head (0: not here)
-  int64_t* share_out;                    // tiles per block, found on the device
-  int64_t* first;                        // [B] tiles per unit of the requests before b
+  int32_t* share_out;                    // tiles per block, found on the device
+  int32_t* first;                        // [B] tiles per unit of the requests before b
   // row kernel: units of unit_rows query rows, by the largest length
   int unit_rows;
   int pre_units, own_units;              // (0: not here)
@@ -79,11 +79,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {

@@ -111,24 +111,22 @@ struct Seg {
 
 // Walks a block's share [g, end) of the tiles of all units.
 struct Walk {
-  int64_t g, end;
+  int g, end;
   __device__ explicit Walk(const AttnArgs& a) {
-    const int64_t total = static_cast<int64_t>(a.pre_units) * a.pre_T +
-                          static_cast<int64_t>(a.own_units) * a.own_T;
-    g = static_cast<int64_t>(blockIdx.x) * a.share;
+    const int total = a.pre_units * a.pre_T + a.own_units * a.own_T;
+    g = blockIdx.x * a.share;
     end = min(g + a.share, total);
   }
   // The next piece with any work; false at the end.
   __device__ bool next(const AttnArgs& a, Seg& s, bool report) {
-    const int64_t pre_total = static_cast<int64_t>(a.pre_units) * a.pre_T;
+    const int pre_total = a.pre_units * a.pre_T;
     while (g < end) {
-      int64_t base;
-      int T;
+      int base, T;
       if (g < pre_total) {
-        const int u = static_cast<int>(g / a.pre_T);
+        const int u = g / a.pre_T;
         s.pre = true;
         T = a.pre_T;
-        base = static_cast<int64_t>(u) * T;
+        base = u * T;
         s.hk = u / a.pre_row_tiles;
         s.b = 0;
         s.row0 = u % a.pre_row_tiles * a.unit_rows;
@@ -136,10 +134,10 @@ struct Walk {
         s.ctx = a.prefix_len;
         s.pages = a.prefix_table;
       } else {
-        const int u = static_cast<int>((g - pre_total) / a.own_T);
+        const int u = (g - pre_total) / a.own_T;
         s.pre = false;
         T = a.own_T;
-        base = pre_total + static_cast<int64_t>(u) * T;
+        base = pre_total + u * T;
         const int place = u % a.own_row_tiles, bh = u / a.own_row_tiles;
         s.hk = bh % a.c.Hkv;
         s.b = bh / a.c.Hkv;
@@ -151,10 +149,10 @@ struct Walk {
       const int last = min(s.row0 + a.unit_rows, s.n_rows) - 1;
       const int seen = s.pre ? s.ctx : own_limit(a, s.ctx, last);
       s.tiles = (seen + kRowTile - 1) / kRowTile;
-      s.kt0 = static_cast<int>(g - base);
-      const int64_t stop = min(end, base + T);
-      s.kt1 = min(static_cast<int>(stop - base), s.tiles);
-      s.part = static_cast<int>(blockIdx.x - base / a.share);
+      s.kt0 = g - base;
+      const int stop = min(end, base + T);
+      s.kt1 = min(stop - base, s.tiles);
+      s.part = static_cast<int>(blockIdx.x) - base / a.share;
       g = stop;
       if (s.kt1 > s.kt0) return true;
     }
