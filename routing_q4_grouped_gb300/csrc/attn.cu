@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
       const int u = (b * a.c.Hkv + hk) * a.own_row_tiles + unit_place(rt, a.own_row_tiles);
       const int seen = own_limit(a, len, min((rt + 1) * a.unit_rows, a.nq * a.G) - 1);
       of_rows(parts[1], a.own_whole, a.pre_units * a.pre_T + u * a.own_T,
-              (seen + kRowTile - 1) / kRowTile);
+              (seen + a.row_tile - 1) / a.row_tile);
     } else {
       const int T = split_tiles(len);
       const int units = a.c.Hkv * a.own_tiles;
@@ -910,9 +910,10 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
   a.nt = D <= 128 && ((own && !own_tc && own_rows > 8) || (pre && !pre_tc && pre_rows > 8)) ? 2 : 1;
   int64_t split_tiles = 0, tiles = 0;
   a.unit_rows = attn_unit_rows(D);
+  a.row_tile = attn_row_tile(D);
   if (pre_tc) {
     a.pre_row_tiles = static_cast<int>(ceil_div(pre_rows, a.unit_rows));
-    a.pre_T = static_cast<int>(ceil_div(prefix_len, kRowTile));
+    a.pre_T = static_cast<int>(ceil_div(prefix_len, a.row_tile));
     const int64_t units = Hkv * a.pre_row_tiles;
     tiles += units * a.pre_T;
     if (units > 0x7FFFFFFF) return false;
@@ -925,7 +926,7 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
   }
   if (own_tc) {
     a.own_row_tiles = static_cast<int>(ceil_div(own_rows, a.unit_rows));
-    a.own_T = static_cast<int>(ceil_div(max_len, kRowTile));
+    a.own_T = static_cast<int>(ceil_div(max_len, a.row_tile));
     const int64_t units = B * Hkv * a.own_row_tiles;
     tiles += units * a.own_T;
     if (units > 0x7FFFFFFF) return false;

@@ -12,8 +12,8 @@ namespace moeq4 {
 
 // A call's contexts: the prefix (all query rows of the batch see it whole) and the
 // requests' own tokens. Each is worked on by the split kernel (few query rows per unit)
-// or by the row kernel (128 or 256 query rows per unit). Both line up the tiles of 128
-// tokens of all their units and give every block an equal share of them.
+// or by the row kernel (128 or 256 query rows per unit). Both line up the token
+// tiles of all their units and give every block an equal share of them.
 struct AttnArgs {
   const uint16_t* q;
   uint16_t* out;
@@ -31,8 +31,8 @@ struct AttnArgs {
   int own_tiles;                         // units per request and key/value head (0: not here)
   int32_t* share_out;                    // tiles per block, found on the device
   int32_t* first;                        // [B] tiles per unit of the requests before b
-  // row kernel: units of unit_rows query rows, by the largest length
-  int unit_rows;
+  // row kernel: units of unit_rows query rows, tiles of row_tile tokens, by the largest length
+  int unit_rows, row_tile;
   int pre_units, own_units;              // (0: not here)
   int pre_row_tiles, own_row_tiles;      // units per key/value head (and request)
   int own_T, share;                      // tiles per unit and per block
@@ -45,8 +45,6 @@ struct AttnArgs {
   float2* ml;
   uint64_t timeout_ns;
 };
-
-constexpr int kRowTile = 128;          // tokens of a row-kernel tile
 
 // A context length as the kernels use it.
 __device__ __forceinline__ int context_len(const AttnArgs& a, int b, bool report) {
@@ -89,6 +87,7 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
 
 // Row kernel (tcgen05): launches it over a.pre_units / a.own_units.
 cudaError_t launch_attn_rows(const AttnArgs& a, unsigned blocks, cudaStream_t s);
-int attn_unit_rows(int D);
+int attn_unit_rows(int D);             // query rows of a unit
+int attn_row_tile(int D);              // tokens of a tile
 
 }  // namespace moeq4

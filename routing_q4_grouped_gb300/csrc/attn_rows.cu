@@ -3,9 +3,9 @@
 //
 // With R rows a cached byte feeds 4 R operations, so from about a hundred rows on
 // the products bound the work, not the bytes. A unit is 256 query rows (128 for
-// D = 256) of one key/value head against a run of 128-token tiles:
-//   X[rows, tokens] = Q K^T     tcgen05.mma, M = 128 rows, N = 128 tokens, both in
-//                               shared memory (K-major, 128-byte swizzle)
+// D = 256) of one key/value head against a run of token tiles:
+//   X[rows, tokens] = Q K^T     tcgen05.mma, M = 128 rows, N = 128 tokens (64 for
+//                               D = 256), keys in shared memory (128-byte swizzle)
 //   P = exp2(X - m)             tensor memory -> registers -> tensor memory, one
 //                               thread per row, fp16, in place of X
 //   O[rows, D] += P V           A = P from tensor memory, B = V^T in shared memory
@@ -29,14 +29,14 @@
 // O and l follow. That leaves one fma, one exp2, one addition and half a conversion
 // per element.
 //
-// Warps (544 threads, one block per SM, persistent over its share of tiles):
+// Warps (416 threads, one block per SM, persistent over its share of tiles):
 //   0-3, 4-7  softmax of query tile 0 and 1 (warp % 4 = tensor-memory lane quarter),
 //             their queries' load and their outputs' store
-//   8-15      codes to operands
-//   16        issues the products
+//   8-11      codes to operands
+//   12        issues the products
 // D <= 128: two query tiles share each token tile and take turns, one in the tensor
-// cores while the other is in its softmax. D = 256: one query tile, whose logits
-// alternate between two slots. Every wait on an mbarrier has a time limit; after one
+// cores while the other is in its softmax. D = 256: one query tile, held in tensor
+// memory, tiles of 64 tokens, and logits that alternate between two slots. Every wait on an mbarrier has a time limit; after one
 // ran out, no thread waits again and the kernel ends with MOE_DEVERR_PIPE_TIMEOUT.
 #include <cstdint>
 
@@ -51,10 +51,6 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kSoftWarps = 8;
-constexpr int kConvWarps = 8;
-constexpr int kConvThreads = kConvWarps * 32;
-constexpr int kMmaWarp = kSoftWarps + kConvWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kMetaRing = 4;
 constexpr int kMaxSpread = 6;          // exponents of a tile's tokens that share one power of two
 constexpr uint32_t kTmemCols = 512;
@@ -64,31 +60,40 @@ template <int D>
 struct RowGeo {
   static constexpr int J = D / kKvGroup;
   static constexpr int QT = D == 256 ? 1 : 2;         // query tiles of a unit
-  static constexpr int KS = D == 256 ? 1 : 2;         // operand tiles in flight, keys and values each
-  static constexpr uint32_t kTileBytes = 128 * D * 2; // a query, key or value tile
-  static constexpr uint32_t kOffK = QT * kTileBytes;
+  static constexpr int TT = D == 256 ? 64 : 128;      // tokens of a tile
+  static constexpr int kConvWarps = D == 128 ? 8 : 4;
+  static constexpr int kConvThreads = kConvWarps * 32;
+  static constexpr int kMmaWarp = kSoftWarps + kConvWarps;
+  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  static constexpr int KS = D == 256 ? 3 : 2;         // operand tiles in flight, keys and values each
+  static constexpr bool kQTmem = D == 256;            // queries in tensor memory, not shared memory
+  static constexpr uint32_t kQBytes = kQTmem ? 0 : 128 * D * 2;   // a query tile
+  static constexpr uint32_t kTileBytes = TT * D * 2;  // a key or value tile
+  static constexpr uint32_t kOffK = QT * kQBytes;
   static constexpr uint32_t kOffV = kOffK + KS * kTileBytes;
   static constexpr uint32_t kOffMeta = kOffV + KS * kTileBytes;
-  static constexpr uint32_t kColO = 0;                // tensor memory: O of tile q at D q,
-  static constexpr uint32_t kColS = QT * D;           // then two logit slots of 128 columns
-  static_assert(kColS + 256 <= kTmemCols, "tensor memory");
+  static constexpr uint32_t kColO = 0;                // tensor memory: O of query tile q at D q,
+  static constexpr uint32_t kColS = QT * D;           // then two logit slots of TT columns,
+  static constexpr uint32_t kColQ = kColS + 2 * TT;   // then the queries
+  static_assert(kColQ + (kQTmem ? D / 2 : 0) <= kTmemCols, "tensor memory");
+  static_assert(KS + 1 <= kMetaRing, "a tile's scales outlive its operands by one tile");
 };
 
 // Scales, biases and exponents of one tile, ready for use.
 template <int D>
 struct alignas(16) Meta {
-  static constexpr int J = RowGeo<D>::J;
-  uint16_t vs[J][128], vb[J][128];     // values: scale * 2^24, bias (fp16, divided by 2^e)
-  uint32_t ksb[J][128];                // keys: the same, bias in the high half
-  float kf[128];                       // 2^eK of each token (slow tiles)
-  float ve[128];                       // eV of each token (slow tiles)
-  uint8_t flag[128];                   // bit j: value group j is NaN; kDead
+  static constexpr int J = RowGeo<D>::J, TT = RowGeo<D>::TT;
+  uint16_t vs[J][TT], vb[J][TT];       // values: scale * 2^24, bias (fp16, divided by 2^e)
+  uint32_t ksb[J][TT];                 // keys: the same, bias in the high half
+  float kf[TT];                        // 2^eK of each token (slow tiles)
+  float ve[TT];                        // eV of each token (slow tiles)
+  uint8_t flag[TT];                    // bit j: value group j is NaN; kDead
   float tile_kf, tile_ve;              // of all tokens (other tiles)
   int slow;
 };
 
 struct Ctl {
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t s_full[2], p_full[2], pv_done[2], meta_full[kMetaRing], drain;
   int64_t base[kMetaRing][8];          // byte offset of a 16-token block's key codes, -1: none
   int32_t words[kMetaRing][8];         // from there to its words
@@ -148,7 +153,7 @@ struct Walk {
       }
       const int last = min(s.row0 + a.unit_rows, s.n_rows) - 1;
       const int seen = s.pre ? s.ctx : own_limit(a, s.ctx, last);
-      s.tiles = (seen + kRowTile - 1) / kRowTile;
+      s.tiles = (seen + a.row_tile - 1) / a.row_tile;
       s.kt0 = g - base;
       const int stop = min(end, base + T);
       s.kt1 = min(stop - base, s.tiles);
@@ -209,8 +214,6 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
       : "memory");
 }
 
-__device__ __forceinline__ void conv_bar() { named_bar_sync(1, kConvThreads); }
-
 __device__ __forceinline__ uint32_t exp_field(uint32_t bf16_bits) { return (bf16_bits >> 7) & 255u; }
 __device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
 
@@ -221,9 +224,11 @@ struct Converter {
   using G = RowGeo<D>;
   static constexpr int J = G::J;
   static constexpr int RB = D * BITS / 8;
+  static constexpr int TT = G::TT;
   static constexpr int PR = D / 16;                  // 16-code pieces of a row
-  static constexpr int KU = PR / 2;                  // key pieces per thread and tile
-  static constexpr int VU = D >= 128 ? D / 128 : 1;  // value pieces (8 tokens x 8 elements)
+  static constexpr int KU = TT * PR / G::kConvThreads;  // key pieces per thread and tile
+  static constexpr int VU = TT * D / 64 / G::kConvThreads;   // value pieces (8 tokens x 8 elements)
+  static constexpr int WU = 2 * TT / G::kConvThreads;   // tokens (keys, then values) per thread and tile
   static constexpr int KW = BITS / 2;                // words of a key piece (16 codes)
 
   const AttnArgs& a;
@@ -256,23 +261,33 @@ struct Converter {
     return __ldg(pages + static_cast<uint32_t>((blk * a.page_magic) >> 40));
   }
 
-  // This thread's scale and bias words: token ct % 128 of the keys (ct < 128) or values.
-  __device__ void load_words(int slot, uint32_t (&w)[J]) const {
-    const int tk = ct & 127;
-    const int64_t off = ctl.base[slot][tk >> 4];
+  // Item i of this thread: token tk of the keys (kv = 0) or of the values.
+  __device__ __forceinline__ void word_item(int i, int& kv, int& tk) const {
+    const int id = ct + G::kConvThreads * i;
+    kv = id / TT;
+    tk = id % TT;
+  }
+  // This thread's scale and bias words.
+  __device__ void load_words(int slot, uint32_t (&w)[WU][J]) const {
 #pragma unroll
-    for (int j = 0; j < J; ++j) w[j] = 0;
-    if (off < 0) return;
-    const uint8_t* p = a.c.data + off + ctl.words[slot][tk >> 4] + (tk & 15) * (J * 4);
-    if (ct >= 128) p += static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes;
-    if constexpr (J == 1) {
-      w[0] = ld_nc_u32(p);
-    } else if constexpr (J == 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = v.x, w[1] = v.y;
-    } else {
-      const uint4 v = ld_nc_v4(p);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    for (int i = 0; i < WU; ++i) {
+      int kv, tk;
+      word_item(i, kv, tk);
+      const int64_t off = ctl.base[slot][tk >> 4];
+#pragma unroll
+      for (int j = 0; j < J; ++j) w[i][j] = 0;
+      if (off < 0) continue;
+      const uint8_t* p = a.c.data + off + ctl.words[slot][tk >> 4] + (tk & 15) * (J * 4);
+      if (kv) p += static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes;
+      if constexpr (J == 1) {
+        w[i][0] = ld_nc_u32(p);
+      } else if constexpr (J == 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        w[i][0] = v.x, w[i][1] = v.y;
+      } else {
+        const uint4 v = ld_nc_v4(p);
+        w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+      }
     }
   }
 
@@ -295,18 +310,17 @@ struct Converter {
     }
   }
 
-  // Value piece u: tokens 64 th + 8 tg .. of elements 32 db + 8 dq ..
-  __device__ bool value_piece(int u, int& th, int& d0) const {
-    const int unit = cw + 8 * u;
-    th = unit & 1;
-    d0 = (unit >> 1) * 32 + (lane >> 3) * 8;
-    return D >= 128 || unit < 4;
+  // Value piece u: tokens 64 th + 8 (lane % 8) .. of elements d0 ..
+  __device__ __forceinline__ void value_piece(int u, int& th, int& d0) const {
+    const int unit = cw + G::kConvWarps * u;
+    th = unit % (TT / 64);
+    d0 = unit / (TT / 64) * 32 + (lane >> 3) * 8;
   }
   __device__ void load_values(int slot) {
 #pragma unroll
     for (int u = 0; u < VU; ++u) {
       int th, d0;
-      if (!value_piece(u, th, d0)) continue;
+      value_piece(u, th, d0);
       const int t0 = th * 64 + (lane & 7) * 8;
       const int64_t off = ctl.base[slot][t0 >> 4];
       const uint8_t* p = a.c.data + off + static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes +
@@ -325,71 +339,81 @@ struct Converter {
   }
 
   // Exponents, scales and biases of a tile of `n` seen tokens from this thread's words.
-  __device__ void put_meta(Meta<D>& m, int slot, const uint32_t (&w)[J], int n) {
-    const int kv = ct >> 7, tk = ct & 127;
-    const bool valid = tk < n && ctl.base[slot][tk >> 4] >= 0;
-    uint32_t e = 0, bad = 0;
+  __device__ void put_meta(Meta<D>& m, int slot, const uint32_t (&w)[WU][J], int n) {
+    uint32_t e[WU], bad[WU];
+    bool valid[WU];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint32_t se = exp_field(w[j]), be = exp_field(w[j] >> 16);
-      if (se == 255u || be == 255u)
-        bad |= 1u << j;
-      else
-        e = max(e, max(se ? se + BITS : 0u, be));
+    for (int i = 0; i < WU; ++i) {
+      int kv, tk;
+      word_item(i, kv, tk);
+      valid[i] = tk < n && ctl.base[slot][tk >> 4] >= 0;
+      e[i] = bad[i] = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const uint32_t se = exp_field(w[i][j]), be = exp_field(w[i][j] >> 16);
+        if (se == 255u || be == 255u)
+          bad[i] |= 1u << j;
+        else
+          e[i] = max(e[i], max(se ? se + BITS : 0u, be));
+      }
+      if (!valid[i]) e[i] = bad[i] = 0;
+      const uint32_t top = __reduce_max_sync(kAll, e[i]);
+      const uint32_t low = __reduce_min_sync(kAll, e[i] ? e[i] : 255u);
+      // NaN values, and tokens that a page outside the cache would hold
+      const bool odd = __any_sync(kAll, (kv == 1 && bad[i]) || (tk < n && !valid[i]));
+      if (lane == 0) {                               // a warp's tokens are all keys or all values
+        ctl.red_max[kv][tk / 32] = static_cast<int>(top);
+        ctl.red_min[kv][tk / 32] = static_cast<int>(low);
+        ctl.red_bad[kv][tk / 32] = odd;
+      }
     }
-    if (!valid) e = bad = 0;
-    const uint32_t top = __reduce_max_sync(kAll, e);
-    const uint32_t low = __reduce_min_sync(kAll, e ? e : 255u);
-    // NaN values, and tokens that a page outside the cache would hold
-    const bool odd = (kv == 1 && bad) || (tk < n && !valid);
-    const bool any_odd = __any_sync(kAll, odd);
-    if (lane == 0) {
-      ctl.red_max[kv][cw & 3] = static_cast<int>(top);
-      ctl.red_min[kv][cw & 3] = static_cast<int>(low);
-      ctl.red_bad[kv][cw & 3] = any_odd;
-    }
-    conv_bar();
+    named_bar_sync(1, G::kConvThreads);
     int E[2], slow = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int v = 0; v < 2; ++v) {
       int hi = 0, lo = 255;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        hi = max(hi, ctl.red_max[i][k]);
-        lo = min(lo, ctl.red_min[i][k]);
-        slow |= ctl.red_bad[i][k];
+      for (int k = 0; k < TT / 32; ++k) {
+        hi = max(hi, ctl.red_max[v][k]);
+        lo = min(lo, ctl.red_min[v][k]);
+        slow |= ctl.red_bad[v][k];
       }
       slow |= hi - lo > kMaxSpread;
-      E[i] = hi == 0 ? 127 : min(hi, 253);
+      E[v] = hi == 0 ? 127 : min(hi, 253);
     }
-    const uint32_t eu = slow && valid && e ? min(e, 253u) : static_cast<uint32_t>(E[kv]);
-    const float down = pow2_field(254u - eu) * 0x1p-8f;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const bool nan = bad >> j & 1;
-      const float s = valid && !nan ? bf16_lo(w[j]) * down * 0x1p24f : 0.f;
-      const float b = valid && !nan ? bf16_hi(w[j]) * down : 0.f;
-      uint32_t sb = pack_f16(s, b);
-      if (kv == 0) {
-        if (nan && valid) sb = 0x7E000000u;            // a NaN key: NaN logits
-        m.ksb[j][tk] = sb;
-      } else {
-        m.vs[j][tk] = static_cast<uint16_t>(sb);
-        m.vb[j][tk] = static_cast<uint16_t>(sb >> 16);
+    for (int i = 0; i < WU; ++i) {
+      int kv, tk;
+      word_item(i, kv, tk);
+      const uint32_t eu = slow && e[i] ? min(e[i], 253u) : static_cast<uint32_t>(kv ? E[1] : E[0]);
+      const float down = pow2_field(254u - eu) * 0x1p-8f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const bool nan = bad[i] >> j & 1;
+        const float s = valid[i] && !nan ? bf16_lo(w[i][j]) * down * 0x1p24f : 0.f;
+        const float b = valid[i] && !nan ? bf16_hi(w[i][j]) * down : 0.f;
+        uint32_t sb = pack_f16(s, b);
+        if (kv == 0) {
+          if (nan) sb = 0x7E000000u;                 // a NaN key: NaN logits
+          m.ksb[j][tk] = sb;
+        } else {
+          m.vs[j][tk] = static_cast<uint16_t>(sb);
+          m.vb[j][tk] = static_cast<uint16_t>(sb >> 16);
+        }
       }
-    }
-    if (kv == 0) {
-      m.kf[tk] = pow2_field(eu) * 0x1p8f;
-    } else {
-      m.ve[tk] = static_cast<float>(static_cast<int>(eu) - 119);
-      m.flag[tk] = static_cast<uint8_t>(bad | (tk < n && !valid ? kDead : 0));
+      if (kv == 0) {
+        m.kf[tk] = pow2_field(eu) * 0x1p8f;
+      } else {
+        m.ve[tk] = static_cast<float>(static_cast<int>(eu) - 119);
+        m.flag[tk] = static_cast<uint8_t>(bad[i] | (tk < n && !valid[i] ? kDead : 0));
+      }
     }
     if (ct == 0) {
       m.tile_kf = pow2_field(static_cast<uint32_t>(E[0])) * 0x1p8f;
       m.tile_ve = static_cast<float>(E[1] - 119);
       m.slow = slow;
     }
-    conv_bar();
+    named_bar_sync(1, G::kConvThreads);
   }
 
   // Keys: 16 codes of a token -> two 16-byte chunks of its row. 4-bit chunks hold
@@ -417,7 +441,7 @@ struct Converter {
           r[2 * i + 1] = fma_f16x2(s16, w & 0x00F000F0u, b2);
         }
       }
-      uint8_t* dst = smem + off + j * 16384 + row * 128;
+      uint8_t* dst = smem + off + j * (TT * 128) + row * 128;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // odd groups store their second chunk first: the lanes of a store meet all banks once
@@ -434,7 +458,7 @@ struct Converter {
 #pragma unroll
     for (int u = 0; u < VU; ++u) {
       int th, d0;
-      if (!value_piece(u, th, d0)) continue;
+      value_piece(u, th, d0);
       const int tg = lane & 7, j = d0 / kKvGroup;
       const uint4 sv = *reinterpret_cast<const uint4*>(&m.vs[j][th * 64 + tg * 8]);
       const uint4 bv = *reinterpret_cast<const uint4*>(&m.vb[j][th * 64 + tg * 8]);
@@ -474,28 +498,28 @@ struct Converter {
   // All tiles of one piece; `tc` counts this block's tiles.
   __device__ void run(const Seg& sg, int seen, uint32_t& tc, Waiter& w) {
     const int nt = sg.kt1 - sg.kt0;
-    const int tok0 = sg.kt0 * kRowTile;
-    uint32_t words[J];
+    const int tok0 = sg.kt0 * TT;
+    uint32_t words[WU][J];
     int page = -1;
     // no reader of the ring slots written here is left: the softmax of the piece before is
     // at most a tile behind the products, whose last use of a slot freed it
-    if (ct < 8) {
+    if (ct < TT / 16) {
       put_base(tc & 3, page_at(sg.pages, tok0 + 16 * ct, seen), tok0 + 16 * ct, seen, sg.hk);
-      page = page_at(sg.pages, tok0 + kRowTile + 16 * ct, seen);
+      page = page_at(sg.pages, tok0 + TT + 16 * ct, seen);
     }
-    conv_bar();
+    named_bar_sync(1, G::kConvThreads);
     load_words(tc & 3, words);
     load_keys(tc & 3);
     for (int it = 0; it < nt; ++it, ++tc) {
       const int slot = tc & 3, st = tc % G::KS;
-      const int tok = tok0 + it * kRowTile;
-      if (ct < 8) {
-        const int nx = tok + kRowTile + 16 * ct;
+      const int tok = tok0 + it * TT;
+      if (ct < TT / 16) {
+        const int nx = tok + TT + 16 * ct;
         put_base((tc + 1) & 3, page, nx, it + 1 < nt ? seen : 0, sg.hk);
-        page = page_at(sg.pages, nx + kRowTile, seen);
+        page = page_at(sg.pages, nx + TT, seen);
       }
       Meta<D>& m = metas[slot];
-      put_meta(m, slot, words, min(seen - tok, kRowTile));
+      put_meta(m, slot, words, min(seen - tok, TT));
       if (lane == 0) mbar_arrive(&ctl.meta_full[slot]);
       load_values(slot);
       const uint32_t parity = ((tc / G::KS) & 1) ^ 1;
@@ -522,6 +546,7 @@ struct Converter {
 template <int D, int BITS>
 struct Softmax {
   using G = RowGeo<D>;
+  static constexpr int kLoad = D == 128 ? 16 : 32;   // logits loaded at a time
   const AttnArgs& a;
   Ctl& ctl;
   Meta<D>* metas;
@@ -536,29 +561,54 @@ struct Softmax {
   // in the key tiles' element order.
   __device__ void load_query(const uint16_t* qp, bool live) {
     const int r = (warp & 3) * 32 + lane;
+    constexpr int kHalf = D / 16;                 // 16-byte pieces kept at a time
+    uint4 v[kHalf];
     float mx = 0.f;
-    if (live)
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(qp) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i)
+        v[i] = live ? __ldg(reinterpret_cast<const uint4*>(qp) + h * kHalf + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
       }
+    }
     const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
     const float down = pow2_field(254u - e);
     c = a.scale2 * pow2_field(e);
-    uint8_t* dst = smem + wg * G::kTileBytes + r * 128;
-    for (int i = 0; i < D / 8; ++i) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (live) v = __ldg(reinterpret_cast<const uint4*>(qp) + i);
-      const float x[8] = {bf16_lo(v.x) * down, bf16_hi(v.x) * down, bf16_lo(v.y) * down,
-                          bf16_hi(v.y) * down, bf16_lo(v.z) * down, bf16_hi(v.z) * down,
-                          bf16_lo(v.w) * down, bf16_hi(v.w) * down};
-      const uint4 o = BITS == 8 ? make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
-                                             pack_f16(x[4], x[5]), pack_f16(x[6], x[7]))
-                                : make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]),
-                                             pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
-      *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4)) = o;
+    uint8_t* dst = smem + wg * G::kQBytes + r * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i)             // (read twice: the second time from the L1 cache)
+        v[i] = live ? __ldg(reinterpret_cast<const uint4*>(qp) + h * kHalf + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) {
+        const int k = h * kHalf + i;
+        const float x[8] = {bf16_lo(v[i].x) * down, bf16_hi(v[i].x) * down, bf16_lo(v[i].y) * down,
+                            bf16_hi(v[i].y) * down, bf16_lo(v[i].z) * down, bf16_hi(v[i].z) * down,
+                            bf16_lo(v[i].w) * down, bf16_hi(v[i].w) * down};
+        v[i] = BITS == 8 ? make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
+                                      pack_f16(x[4], x[5]), pack_f16(x[6], x[7]))
+                         : make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]),
+                                      pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
+        if (!G::kQTmem)
+          *reinterpret_cast<uint4*>(dst + (k >> 3) * 16384 + (((k & 7) ^ (r & 7)) << 4)) = v[i];
+      }
+      if (G::kQTmem) {
+#pragma unroll
+        for (int i = 0; i + 4 <= kHalf; i += 4) {
+          const uint32_t q[16] = {v[i].x,     v[i].y,     v[i].z,     v[i].w,
+                                  v[i + 1].x, v[i + 1].y, v[i + 1].z, v[i + 1].w,
+                                  v[i + 2].x, v[i + 2].y, v[i + 2].z, v[i + 2].w,
+                                  v[i + 3].x, v[i + 3].y, v[i + 3].z, v[i + 3].w};
+          tmem_st_32x32b_x16(tmem + G::kColQ + (h * kHalf + i) * 4, q);
+        }
+        tmem_st_wait();
+      }
     }
   }
 
@@ -577,27 +627,35 @@ struct Softmax {
                                            uint32_t (&p)[32]) {
     float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint32_t v[16];
-      tmem_ld_32x32b_x16(tmem + s_col + 64 * H + 16 * h, v);
-      tmem_ld_wait();
-      tmem_regs_ready(v);
+    for (int h = 0; h < 64 / kLoad; ++h) {
+      // (a tensor-memory load is waited for at once: its registers arrive late, and the
+      // compiler may only be kept from moving them while nothing else happens)
+      uint32_t v[kLoad];
+      if constexpr (kLoad == 32) {
+        tmem_ld_32x32b_x32(tmem + s_col + 64 * H + 32 * h, v);
+        tmem_ld_wait();
+        tmem_regs_ready(reinterpret_cast<uint32_t(&)[16]>(v[16]));
+      } else {
+        tmem_ld_32x32b_x16(tmem + s_col + 64 * H + 16 * h, v);
+        tmem_ld_wait();
+      }
+      tmem_regs_ready(reinterpret_cast<uint32_t(&)[16]>(v[0]));
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const int col = 64 * H + 16 * h + i;
+      for (int i = 0; i < kLoad; i += 2) {
+        const int col = 64 * H + kLoad * h + i;
         float x0 = fmaf(__uint_as_float(v[i]), ck, off);
         float x1 = fmaf(__uint_as_float(v[i + 1]), ck, off);
         if (MASK && col >= lim) x0 = -INFINITY;
         if (MASK && col + 1 >= lim) x1 = -INFINITY;
         const float w0 = exp2_approx(x0), w1 = exp2_approx(x1);
         part[(i >> 1) & 3] += w0 + w1;
-        p[8 * h + i / 2] = pack_f16(w0, w1);
+        p[kLoad / 2 * h + i / 2] = pack_f16(w0, w1);
       }
     }
     return (part[0] + part[1]) + (part[2] + part[3]);
   }
 
-  // Moves m to the largest logit of columns 16 H0 .. 127 and E so that none of their
+  // Moves m to the largest logit of columns 16 H0 .. and E so that none of their
   // weights passes 1 (in the lanes that `need` it), and l, O and the tile's weights
   // already written (columns below 16 H0) along with them.
   template <bool SLOW, bool MASK, int H0>
@@ -606,7 +664,7 @@ struct Softmax {
     float mx = -INFINITY, ux = -INFINITY;
     const float ck = c * t.tile_kf;
 #pragma unroll 1
-    for (int h = H0; h < 8; ++h) {
+    for (int h = H0; h < G::TT / 16; ++h) {
       uint32_t v[16];
       tmem_ld_32x32b_x16(tmem + s_col + 16 * h, v);
       tmem_ld_wait();
@@ -685,7 +743,7 @@ struct Softmax {
   __device__ __forceinline__ void tile(uint32_t s_col, const Meta<D>& t, int lim, bool first,
                                        uint64_t* pv, uint32_t pv_parity, Waiter& w) {
     half_tile<MASK, 0>(s_col, t, lim, first, pv, pv_parity, w);
-    half_tile<MASK, 1>(s_col, t, lim, first, pv, pv_parity, w);
+    if constexpr (G::TT == 128) half_tile<MASK, 1>(s_col, t, lim, first, pv, pv_parity, w);
   }
 
   // A tile with an exponent per token, NaN groups or missing pages: m always moves to
@@ -696,7 +754,7 @@ struct Softmax {
     move<true, true, 0>(s_col, t, lim, true, first, pv, pv_parity, w);
     const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
-    for (int h = 0; h < 8; ++h) {
+    for (int h = 0; h < G::TT / 16; ++h) {
       uint32_t v[16], p[8];
       tmem_ld_32x32b_x16(tmem + s_col + 16 * h, v);
       tmem_ld_wait();
@@ -727,7 +785,10 @@ struct Softmax {
     const int qrow = live ? (sg.pre ? r / a.G : sg.b * a.nq + r / a.G) : 0;
     const int head = sg.hk * a.G + (live ? r % a.G : 0);
     load_query(a.q + qrow * a.q_row + head * a.q_head, live);
-    fence_proxy_async_smem();
+    if (G::kQTmem)
+      tc_fence_before();
+    else
+      fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl.q_full[wg]);
     m = -INFINITY;
@@ -743,23 +804,25 @@ struct Softmax {
       w.wait(&ctl.meta_full[(tc + it) & 3], ((tc + it) >> 2) & 1);
       w.wait(&ctl.s_full[slot], use & 1);
       tc_fence_after();
-      const int rel = lim - (sg.kt0 + it) * kRowTile;
-      const uint32_t s_col = G::kColS + 128 * slot;
+      const int rel = lim - (sg.kt0 + it) * G::TT;
+      const uint32_t s_col = G::kColS + G::TT * slot;
       const uint32_t pv_parity = (pc + it - 1) & 1;
       uint64_t* pv = &ctl.pv_done[wg];
       if (t.slow)
         slow_tile(s_col, t, rel, it == 0, pv, pv_parity, w);
-      else if (__all_sync(kAll, rel >= kRowTile))
+      else if (__all_sync(kAll, rel >= G::TT))
         tile<false>(s_col, t, rel, it == 0, pv, pv_parity, w);
       else
         tile<true>(s_col, t, rel, it == 0, pv, pv_parity, w);
+      // The end waits for the last product; with one query tile the last but one may still
+      // run now (these logits were issued before it). A parity tells only neighbouring
+      // phases apart, so that one is waited for while the last cannot have been issued.
+      if (it > 0 && it == nt - 1) w.wait(pv, pv_parity);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.p_full[slot]);
     }
-    // ---- outputs. With one query tile the last but one product may still run too (the last
-    // logits were issued before it), and a parity tells only neighbouring phases apart.
-    if (nt > 1) w.wait(&ctl.pv_done[wg], (pc + nt - 2) & 1);
+    // ---- outputs
     w.wait(&ctl.pv_done[wg], (pc + nt - 1) & 1);
     tc_fence_after();
     const bool lone = a.lone && sg.kt0 == 0 && sg.kt1 == sg.tiles;
@@ -800,7 +863,7 @@ struct Softmax {
 // ------------------------------------------------------------------- kernel
 
 template <int D, int BITS>
-__global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const AttnArgs a) {
   using G = RowGeo<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -809,22 +872,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + G::kOffMeta + kMetaRing * sizeof(Meta<D>));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&ctl.k_full[i], G::kConvWarps);
+      mbar_init(&ctl.k_empty[i], 1);
+      mbar_init(&ctl.v_full[i], G::kConvWarps);
+      mbar_init(&ctl.v_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.q_full[i], 4);
-      mbar_init(&ctl.k_full[i], kConvWarps);
-      mbar_init(&ctl.k_empty[i], 1);
-      mbar_init(&ctl.v_full[i], kConvWarps);
-      mbar_init(&ctl.v_empty[i], 1);
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_full[i], 4);
       mbar_init(&ctl.pv_done[i], 1);
     }
-    for (int i = 0; i < kMetaRing; ++i) mbar_init(&ctl.meta_full[i], kConvWarps);
+    for (int i = 0; i < kMetaRing; ++i) mbar_init(&ctl.meta_full[i], G::kConvWarps);
     mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == G::kMmaWarp) {
     tmem_alloc(&ctl.tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -855,18 +920,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       pc[0] += nt;
       pc[1] += nqt == 2 ? nt : 0;
     }
-  } else if (warp < kMmaWarp) {
+  } else if (warp < G::kMmaWarp) {
     Converter<D, BITS> cv{a, ctl, metas, smem, static_cast<int>(threadIdx.x) - kSoftWarps * 32,
                           warp - kSoftWarps, lane};
     while (walk.next(a, sg, false)) cv.run(sg, Walk::seen(a, sg), tc, w);
   } else {
-    const uint32_t idesc_x = idesc_f16(128), idesc_o = idesc_f16(D);
+    const uint32_t idesc_x = idesc_f16(G::TT), idesc_o = idesc_f16(D);
     const uint32_t base = smem_u32(smem);
     uint32_t q_uses[2] = {0, 0};
     while (walk.next(a, sg, false)) {
       const int nt = sg.kt1 - sg.kt0;
       const int nqt = G::QT == 2 && sg.row0 + 128 < sg.n_rows ? 2 : 1;
       for (int i = 0; i < nqt; ++i) w.wait(&ctl.q_full[i], q_uses[i]++ & 1);
+      tc_fence_after();
       const int items = nt * nqt;
       // item n: query tile q, token tile it; its weights' product follows the next item's logits
       const auto weigh = [&](int n) {
@@ -876,10 +942,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         w.wait(&ctl.p_full[slot], (sc[slot] + (nqt == 2 ? it : it >> 1)) & 1);
         tc_fence_after();
         __syncwarp();
-        const uint32_t p = tmem + G::kColS + 128 * slot, o = tmem + G::kColO + q * D;
+        const uint32_t p = tmem + G::kColS + G::TT * slot, o = tmem + G::kColO + q * D;
         const uint64_t v = sdesc_k_sw128(base + G::kOffV + st * G::kTileBytes);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < G::TT / 64; ++k)
           mma_ts_tile_chunk_elect(o, p + 32 * k, v + k * (D * 128 / 16), idesc_o, it > 0 || k > 0);
         mma_commit_elect(&ctl.pv_done[q]);
         if (q == nqt - 1) mma_commit_elect(&ctl.v_empty[st]);
@@ -892,11 +958,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           tc_fence_after();
         }
         __syncwarp();
-        const uint64_t qd = sdesc_k_sw128(base + q * G::kTileBytes);
+        const uint32_t x = tmem + G::kColS + G::TT * slot;
         const uint64_t kd = sdesc_k_sw128(base + G::kOffK + st * G::kTileBytes);
+        if constexpr (G::kQTmem) {
 #pragma unroll
-        for (int j = 0; j < G::J; ++j)
-          mma_ss_chunk(tmem + G::kColS + 128 * slot, qd + j * 1024, kd + j * 1024, idesc_x, j > 0);
+          for (int j = 0; j < G::J; ++j)
+            mma_ts_tile_chunk_elect(x, tmem + G::kColQ + 32 * j, kd + j * (G::TT * 8), idesc_x, j > 0);
+        } else {
+          const uint64_t qd = sdesc_k_sw128(base + q * G::kQBytes);
+#pragma unroll
+          for (int j = 0; j < G::J; ++j)
+            mma_ss_chunk(x, qd + j * 1024, kd + j * (G::TT * 8), idesc_x, j > 0);
+        }
         mma_commit_elect(&ctl.s_full[slot]);
         if (q == nqt - 1) mma_commit_elect(&ctl.k_empty[st]);
         if (n > 0) weigh(n - 1);
@@ -913,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == G::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -927,12 +1000,13 @@ cudaError_t launch_rows(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, s, a);
+  return launch_pdl(kernel, dim3(blocks), dim3(RowGeo<D>::kThreads), smem, s, a);
 }
 
 }  // namespace
 
 int attn_unit_rows(int D) { return D == 256 ? 128 : 256; }
+int attn_row_tile(int D) { return D == 256 ? RowGeo<256>::TT : RowGeo<128>::TT; }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
   if (a.c.bits == 8)
