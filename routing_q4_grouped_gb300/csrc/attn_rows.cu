@@ -95,8 +95,9 @@ struct alignas(16) Meta {
 struct Ctl {
   uint64_t q_full[2], k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t s_full[2], p_full[2], pv_done[2], meta_full[kMetaRing], drain;
-  int64_t base[kMetaRing][8];          // byte offset of a 16-token block's key codes, -1: none
-  int32_t words[kMetaRing][8];         // from there to its words
+  int64_t base[kMetaRing][8];          // byte offset of a 16-token block's key codes
+  int32_t words[kMetaRing][8];         // from there to its words; -1: no such block (its codes
+                                       // are read from the cache's start and multiplied by 0)
   int red_max[2][4], red_min[2][4], red_bad[2][4];
   uint32_t tmem_base;
   int abort;
@@ -217,6 +218,32 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
 __device__ __forceinline__ uint32_t exp_field(uint32_t bf16_bits) { return (bf16_bits >> 7) & 255u; }
 __device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z,
+                                             uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // -------------------------------------------------------- codes to operands
 
 template <int D, int BITS>
@@ -241,8 +268,8 @@ struct Converter {
 
   // Block offsets of the tile at token tok0 into ring slot `slot` (8 threads).
   __device__ void put_base(int slot, int page, int tok, int end, int hk) {
-    int64_t off = -1;
-    int wd = 0;
+    int64_t off = 0;
+    int wd = -1;
     if (tok < end && page >= 0 && page < a.c.pages) {
       const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
       const uint32_t in_page =
@@ -273,11 +300,8 @@ struct Converter {
     for (int i = 0; i < WU; ++i) {
       int kv, tk;
       word_item(i, kv, tk);
-      const int64_t off = ctl.base[slot][tk >> 4];
-#pragma unroll
-      for (int j = 0; j < J; ++j) w[i][j] = 0;
-      if (off < 0) continue;
-      const uint8_t* p = a.c.data + off + ctl.words[slot][tk >> 4] + (tk & 15) * (J * 4);
+      const uint8_t* p = a.c.data + ctl.base[slot][tk >> 4] + max(ctl.words[slot][tk >> 4], 0) +
+                         (tk & 15) * (J * 4);
       if (kv) p += static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes;
       if constexpr (J == 1) {
         w[i][0] = ld_nc_u32(p);
@@ -291,48 +315,55 @@ struct Converter {
     }
   }
 
+  // Key piece u of a lane: 16 codes (group j, quarter of it) of token row. The rows of a
+  // piece are RU, of a warp KU * RU (16 or 32); lanes are laid out so that the eight
+  // lanes of a shared-memory store hit every bank once.
+  static constexpr int RU = 32 / PR;
+  __device__ __forceinline__ int key_row() const {       // of piece 0, within the warp's rows
+    return D == 64 ? lane >> 2 : D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2 & 1;
+  }
+  __device__ __forceinline__ int key_group() const {
+    return D == 64 ? 0 : D == 128 ? lane >> 3 & 1 : lane >> 3;
+  }
   __device__ void load_keys(int slot) {
+    const int in_row = key_group() * (4 * 2 * BITS) + (lane & 3) * (2 * BITS);
 #pragma unroll
-    for (int u = 0; u < KU; ++u) {
-      const int row = (cw * KU + u) * (32 / PR) + lane / PR, piece = lane % PR;
-      const int64_t off = ctl.base[slot][row >> 4];
+    for (int b = 0; b < KU * RU / 16; ++b) {
+      const uint8_t* p = a.c.data + ctl.base[slot][cw * (KU * RU / 16) + b] + key_row() * RB + in_row;
 #pragma unroll
-      for (int i = 0; i < KW; ++i) kr[u][i] = 0;
-      if (off < 0) continue;
-      const uint8_t* p = a.c.data + off + (row & 15) * RB + piece * (2 * BITS);
-      if constexpr (BITS == 8) {
-        const uint4 v = ld_nc_v4(p);
-        kr[u][0] = v.x, kr[u][1] = v.y, kr[u][2] = v.z, kr[u][3] = v.w;
-      } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-        kr[u][0] = v.x, kr[u][1] = v.y;
+      for (int i = 0; i < 16 / RU; ++i) {
+        uint32_t(&k)[KW] = kr[b * (16 / RU) + i];
+        if constexpr (BITS == 8) {
+          const uint4 v = ld_nc_v4(p + i * RU * RB);
+          k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + i * RU * RB));
+          k[0] = v.x, k[1] = v.y;
+        }
       }
     }
   }
 
-  // Value piece u: tokens 64 th + 8 (lane % 8) .. of elements d0 ..
-  __device__ __forceinline__ void value_piece(int u, int& th, int& d0) const {
-    const int unit = cw + G::kConvWarps * u;
-    th = unit % (TT / 64);
-    d0 = unit / (TT / 64) * 32 + (lane >> 3) * 8;
-  }
+  // Value piece u: tokens 64 th + 8 (lane % 8) .. of elements d0 + u * kPieceD ..; th is the
+  // same for all pieces of a warp.
+  static constexpr int TH = TT / 64;
+  static constexpr int kPieceD = G::kConvWarps / TH * 32;
+  __device__ __forceinline__ int value_half() const { return cw % TH; }
+  __device__ __forceinline__ int value_d0() const { return cw / TH * 32 + (lane >> 3) * 8; }
   __device__ void load_values(int slot) {
+    const int t0 = value_half() * 64 + (lane & 7) * 8;
+    const uint8_t* p = a.c.data + ctl.base[slot][t0 >> 4] +
+                       static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes + (t0 & 15) * RB +
+                       value_d0() * BITS / 8;
 #pragma unroll
     for (int u = 0; u < VU; ++u) {
-      int th, d0;
-      value_piece(u, th, d0);
-      const int t0 = th * 64 + (lane & 7) * 8;
-      const int64_t off = ctl.base[slot][t0 >> 4];
-      const uint8_t* p = a.c.data + off + static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes +
-                         (t0 & 15) * RB + d0 * BITS / 8;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         if constexpr (BITS == 8) {
-          uint2 v = make_uint2(0, 0);
-          if (off >= 0) v = __ldg(reinterpret_cast<const uint2*>(p + k * RB));
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + k * RB + u * kPieceD));
           vr[u][k][0] = v.x, vr[u][k][1] = v.y;
         } else {
-          vr[u][k][0] = off >= 0 ? ld_nc_u32(p + k * RB) : 0;
+          vr[u][k][0] = ld_nc_u32(p + k * RB + u * (kPieceD / 2));
         }
       }
     }
@@ -346,7 +377,7 @@ struct Converter {
     for (int i = 0; i < WU; ++i) {
       int kv, tk;
       word_item(i, kv, tk);
-      valid[i] = tk < n && ctl.base[slot][tk >> 4] >= 0;
+      valid[i] = tk < n && ctl.words[slot][tk >> 4] >= 0;
       e[i] = bad[i] = 0;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -419,11 +450,12 @@ struct Converter {
   // Keys: 16 codes of a token -> two 16-byte chunks of its row. 4-bit chunks hold
   // elements 0 4 1 5 2 6 3 7 (as they come out of a word); the queries' do too.
   __device__ void put_keys(const Meta<D>& m, uint32_t off) const {
+    const int j = key_group(), row = cw * (KU * RU) + key_row();
+    const uint32_t dst = smem_u32(smem) + off + j * (TT * 128) + row * 128 +
+                         (((lane & 3) * 2 ^ (row & 7)) << 4);
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
-      const int row = (cw * KU + u) * (32 / PR) + lane / PR, piece = lane % PR;
-      const int j = piece >> 2;
-      const uint32_t sb = m.ksb[j][row];
+      const uint32_t sb = m.ksb[j][row + u * RU];
       const uint32_t s2 = prmt(sb, sb, 0x1010), b2 = prmt(sb, sb, 0x3232);
       uint32_t r[8];
       if constexpr (BITS == 8) {
@@ -441,29 +473,23 @@ struct Converter {
           r[2 * i + 1] = fma_f16x2(s16, w & 0x00F000F0u, b2);
         }
       }
-      uint8_t* dst = smem + off + j * (TT * 128) + row * 128;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // odd groups store their second chunk first: the lanes of a store meet all banks once
-        const bool second = (h ^ (j & 1)) != 0;
-        const int chunk = (piece & 3) * 2 + (second ? 1 : 0);
-        *reinterpret_cast<uint4*>(dst + ((chunk ^ (row & 7)) << 4)) =
-            second ? make_uint4(r[4], r[5], r[6], r[7]) : make_uint4(r[0], r[1], r[2], r[3]);
-      }
+      const uint32_t at = (dst ^ ((u * RU & 7) << 4)) + u * RU * 128;
+      st_shared_v4(at, r[0], r[1], r[2], r[3]);
+      st_shared_v4(at ^ 16u, r[4], r[5], r[6], r[7]);
     }
   }
 
   // Values, transposed: 8 tokens x 8 elements -> one 16-byte chunk in each of 8 rows.
   __device__ void put_values(const Meta<D>& m, uint32_t off) const {
+    const int th = value_half(), tg = lane & 7;
+    const uint32_t dst0 = smem_u32(smem) + off + th * (D * 128) + value_d0() * 128 + (tg << 4);
 #pragma unroll
     for (int u = 0; u < VU; ++u) {
-      int th, d0;
-      value_piece(u, th, d0);
-      const int tg = lane & 7, j = d0 / kKvGroup;
+      const int j = (value_d0() + u * kPieceD) / kKvGroup;
       const uint4 sv = *reinterpret_cast<const uint4*>(&m.vs[j][th * 64 + tg * 8]);
       const uint4 bv = *reinterpret_cast<const uint4*>(&m.vb[j][th * 64 + tg * 8]);
       const uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
-      uint8_t* dst = smem + off + th * (D * 128) + d0 * 128;
+      const uint32_t dst = dst0 + u * (kPieceD * 128);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {                 // elements 4h .. 4h + 3
         uint32_t r[4][4];                           // [element][token pair]
@@ -488,8 +514,7 @@ struct Converter {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = 4 * h + i;
-          *reinterpret_cast<uint4*>(dst + row * 128 + ((tg ^ row) << 4)) =
-              make_uint4(r[i][0], r[i][1], r[i][2], r[i][3]);
+          st_shared_v4((dst ^ (row << 4)) + row * 128, r[i][0], r[i][1], r[i][2], r[i][3]);
         }
       }
     }
@@ -625,11 +650,12 @@ struct Softmax {
   template <bool MASK, int H>
   __device__ __forceinline__ float weights(uint32_t s_col, float ck, float off, int lim,
                                            uint32_t (&p)[32]) {
-    float part[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint64_t ck2 = pack_f32x2(ck, ck), off2 = pack_f32x2(off, off);
+    uint64_t part[2] = {0, 0};
 #pragma unroll
     for (int h = 0; h < 64 / kLoad; ++h) {
       // (a tensor-memory load is waited for at once: its registers arrive late, and the
-      // compiler may only be kept from moving them while nothing else happens)
+      // compiler must not move them in between)
       uint32_t v[kLoad];
       if constexpr (kLoad == 32) {
         tmem_ld_32x32b_x32(tmem + s_col + 64 * H + 32 * h, v);
@@ -643,16 +669,19 @@ struct Softmax {
 #pragma unroll
       for (int i = 0; i < kLoad; i += 2) {
         const int col = 64 * H + kLoad * h + i;
-        float x0 = fmaf(__uint_as_float(v[i]), ck, off);
-        float x1 = fmaf(__uint_as_float(v[i + 1]), ck, off);
+        float x0, x1;
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), ck2, off2),
+                     x0, x1);
         if (MASK && col >= lim) x0 = -INFINITY;
         if (MASK && col + 1 >= lim) x1 = -INFINITY;
         const float w0 = exp2_approx(x0), w1 = exp2_approx(x1);
-        part[(i >> 1) & 3] += w0 + w1;
+        part[(i >> 1) & 1] = add_f32x2(part[(i >> 1) & 1], pack_f32x2(w0, w1));
         p[kLoad / 2 * h + i / 2] = pack_f16(w0, w1);
       }
     }
-    return (part[0] + part[1]) + (part[2] + part[3]);
+    float s0, s1;
+    unpack_f32x2(add_f32x2(part[0], part[1]), s0, s1);
+    return s0 + s1;
   }
 
   // Moves m to the largest logit of columns 16 H0 .. and E so that none of their
@@ -866,8 +895,8 @@ template <int D, int BITS>
 __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const AttnArgs a) {
   using G = RowGeo<D>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  // (an offset, not a rounded pointer: the compiler keeps seeing shared memory)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   Meta<D>* metas = reinterpret_cast<Meta<D>*>(smem + G::kOffMeta);
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + G::kOffMeta + kMetaRing * sizeof(Meta<D>));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
