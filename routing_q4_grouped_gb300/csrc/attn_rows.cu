@@ -29,11 +29,11 @@
 // O and l follow. That leaves one fma, one exp2, one addition and half a conversion
 // per element.
 //
-// Warps (416 threads, one block per SM, persistent over its share of tiles):
+// Warps (one block per SM, persistent over its share of tiles):
 //   0-3, 4-7  softmax of query tile 0 and 1 (warp % 4 = tensor-memory lane quarter),
 //             their queries' load and their outputs' store
-//   8-11      codes to operands
-//   12        issues the products
+//   11        issues the products
+//   8 9 10 12 13 14 16 17 (D = 64: the first four)  codes to operands
 // D <= 128: two query tiles share each token tile and take turns, one in the tensor
 // cores while the other is in its softmax. D = 256: one query tile, held in tensor
 // memory, tiles of 64 tokens, and logits that alternate between two slots. Every wait on an mbarrier has a time limit; after one
@@ -51,6 +51,13 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = 11;
+// Conversion warps: 8 9 10, 12 13 14, 16 17, i.e. none with warp % 4 == 3. A warp issues
+// from sub-partition warp % 4, and the products' warp must not wait for busy neighbours
+// there: alone on the multiprocessor it issues one product per 64 cycles (their full rate),
+// beside four warps of fp32 arithmetic one per 128.
+__host__ __device__ constexpr bool is_conv_warp(int warp) { return warp >= kSoftWarps && warp % 4 != 3; }
+__host__ __device__ constexpr int conv_index(int warp) { return warp - 8 - (warp > 11) - (warp > 15); }
 constexpr int kMetaRing = 4;
 constexpr int kMaxSpread = 6;          // exponents of a tile's tokens that share one power of two
 constexpr uint32_t kTmemCols = 512;
@@ -61,10 +68,9 @@ struct RowGeo {
   static constexpr int J = D / kKvGroup;
   static constexpr int QT = D == 256 ? 1 : 2;         // query tiles of a unit
   static constexpr int TT = D == 256 ? 64 : 128;      // tokens of a tile
-  static constexpr int kConvWarps = D == 128 ? 8 : 4;
+  static constexpr int kConvWarps = D == 64 ? 4 : 8;
   static constexpr int kConvThreads = kConvWarps * 32;
-  static constexpr int kMmaWarp = kSoftWarps + kConvWarps;
-  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  static constexpr int kThreads = (kConvWarps == 4 ? 13 : 18) * 32;
   static constexpr int KS = D == 256 ? 3 : 2;         // operand tiles in flight, keys and values each
   static constexpr bool kQTmem = D == 256;            // queries in tensor memory, not shared memory
   static constexpr uint32_t kQBytes = kQTmem ? 0 : 128 * D * 2;   // a query tile
@@ -215,6 +221,31 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
       : "memory");
 }
 
+// The same for 128 of the reduction: second operands at a + a_step and b + b_step.
+__device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint64_t a_step,
+                                            uint64_t b_step, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      ".reg .b64 a1, a2, a3, b1, b2, b3, c0, c1, c2, c3, f0, f1, f2, f3;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+      "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+      "add.u64 c0, %1, %3;\n\tadd.u64 f0, %2, %4;\n\t"
+      "add.u64 c1, c0, 2;\n\tadd.u64 c2, c0, 4;\n\tadd.u64 c3, c0, 6;\n\t"
+      "add.u64 f1, f0, 2;\n\tadd.u64 f2, f0, 4;\n\tadd.u64 f3, f0, 6;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %5, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c0, f0, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c1, f1, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c2, f2, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c3, f3, %5, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "l"(a_step), "l"(b_step), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 __device__ __forceinline__ uint32_t exp_field(uint32_t bf16_bits) { return (bf16_bits >> 7) & 255u; }
 __device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
 
@@ -255,7 +286,9 @@ struct Converter {
   static constexpr int PR = D / 16;                  // 16-code pieces of a row
   static constexpr int KU = TT * PR / G::kConvThreads;  // key pieces per thread and tile
   static constexpr int VU = TT * D / 64 / G::kConvThreads;   // value pieces (8 tokens x 8 elements)
-  static constexpr int WU = 2 * TT / G::kConvThreads;   // tokens (keys, then values) per thread and tile
+  // tokens (keys, then values) per thread and tile; with more threads than tokens the
+  // last warps have none
+  static constexpr int WU = 2 * TT > G::kConvThreads ? 2 * TT / G::kConvThreads : 1;
   static constexpr int KW = BITS / 2;                // words of a key piece (16 codes)
 
   const AttnArgs& a;
@@ -295,7 +328,9 @@ struct Converter {
     tk = id % TT;
   }
   // This thread's scale and bias words.
+  __device__ __forceinline__ bool has_words() const { return ct < 2 * TT; }
   __device__ void load_words(int slot, uint32_t (&w)[WU][J]) const {
+    if (!has_words()) return;
 #pragma unroll
     for (int i = 0; i < WU; ++i) {
       int kv, tk;
@@ -316,9 +351,10 @@ struct Converter {
   }
 
   // Key piece u of a lane: 16 codes (group j, quarter of it) of token row. The rows of a
-  // piece are RU, of a warp KU * RU (16 or 32); lanes are laid out so that the eight
+  // piece are RU, of a warp RW = KU * RU (8, 16 or 32); lanes are laid out so that the eight
   // lanes of a shared-memory store hit every bank once.
-  static constexpr int RU = 32 / PR;
+  static constexpr int RU = 32 / PR, RW = KU * RU;
+  static constexpr int RB16 = RW < 16 ? RW : 16;         // of one 16-token block
   __device__ __forceinline__ int key_row() const {       // of piece 0, within the warp's rows
     return D == 64 ? lane >> 2 : D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2 & 1;
   }
@@ -328,11 +364,12 @@ struct Converter {
   __device__ void load_keys(int slot) {
     const int in_row = key_group() * (4 * 2 * BITS) + (lane & 3) * (2 * BITS);
 #pragma unroll
-    for (int b = 0; b < KU * RU / 16; ++b) {
-      const uint8_t* p = a.c.data + ctl.base[slot][cw * (KU * RU / 16) + b] + key_row() * RB + in_row;
+    for (int b = 0; b < RW / RB16; ++b) {
+      const uint8_t* p = a.c.data + ctl.base[slot][(cw * RW >> 4) + b] +
+                         ((cw * RW & 15) + key_row()) * RB + in_row;
 #pragma unroll
-      for (int i = 0; i < 16 / RU; ++i) {
-        uint32_t(&k)[KW] = kr[b * (16 / RU) + i];
+      for (int i = 0; i < RB16 / RU; ++i) {
+        uint32_t(&k)[KW] = kr[b * (RB16 / RU) + i];
         if constexpr (BITS == 8) {
           const uint4 v = ld_nc_v4(p + i * RU * RB);
           k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
@@ -374,7 +411,7 @@ struct Converter {
     uint32_t e[WU], bad[WU];
     bool valid[WU];
 #pragma unroll
-    for (int i = 0; i < WU; ++i) {
+    for (int i = 0; i < WU && has_words(); ++i) {
       int kv, tk;
       word_item(i, kv, tk);
       valid[i] = tk < n && ctl.words[slot][tk >> 4] >= 0;
@@ -413,7 +450,7 @@ struct Converter {
       E[v] = hi == 0 ? 127 : min(hi, 253);
     }
 #pragma unroll
-    for (int i = 0; i < WU; ++i) {
+    for (int i = 0; i < WU && has_words(); ++i) {
       int kv, tk;
       word_item(i, kv, tk);
       const uint32_t eu = slow && e[i] ? min(e[i], 253u) : static_cast<uint32_t>(kv ? E[1] : E[0]);
@@ -450,7 +487,7 @@ struct Converter {
   // Keys: 16 codes of a token -> two 16-byte chunks of its row. 4-bit chunks hold
   // elements 0 4 1 5 2 6 3 7 (as they come out of a word); the queries' do too.
   __device__ void put_keys(const Meta<D>& m, uint32_t off) const {
-    const int j = key_group(), row = cw * (KU * RU) + key_row();
+    const int j = key_group(), row = cw * RW + key_row();
     const uint32_t dst = smem_u32(smem) + off + j * (TT * 128) + row * 128 +
                          (((lane & 3) * 2 ^ (row & 7)) << 4);
 #pragma unroll
@@ -918,7 +955,7 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
     ctl.abort = 0;
     fence_mbar_init();
   }
-  if (warp == G::kMmaWarp) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&ctl.tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -949,18 +986,24 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
       pc[0] += nt;
       pc[1] += nqt == 2 ? nt : 0;
     }
-  } else if (warp < G::kMmaWarp) {
-    Converter<D, BITS> cv{a, ctl, metas, smem, static_cast<int>(threadIdx.x) - kSoftWarps * 32,
-                          warp - kSoftWarps, lane};
+  } else if (is_conv_warp(warp)) {
+    Converter<D, BITS> cv{a, ctl, metas, smem, conv_index(warp) * 32 + lane, conv_index(warp), lane};
     while (walk.next(a, sg, false)) cv.run(sg, Walk::seen(a, sg), tc, w);
-  } else {
+  } else if (warp == kMmaWarp) {
     const uint32_t idesc_x = idesc_f16(G::TT), idesc_o = idesc_f16(D);
+    // Counts and addresses are broadcast from lane 0, which tells the compiler that they are
+    // the same in all lanes: operands of the products then live in uniform registers,
+    // and the products issue without being moved there one by one (the issuing warp
+    // set the pace before).
     const uint32_t base = smem_u32(smem);
+    const uint32_t tmem = __shfl_sync(kAll, ctl.tmem_base, 0);
     uint32_t q_uses[2] = {0, 0};
     while (walk.next(a, sg, false)) {
-      const int nt = sg.kt1 - sg.kt0;
-      const int nqt = G::QT == 2 && sg.row0 + 128 < sg.n_rows ? 2 : 1;
-      for (int i = 0; i < nqt; ++i) w.wait(&ctl.q_full[i], q_uses[i]++ & 1);
+      const int nt = __shfl_sync(kAll, sg.kt1 - sg.kt0, 0);
+      const int nqt =
+          __shfl_sync(kAll, G::QT == 2 && sg.row0 + 128 < sg.n_rows ? 2 : 1, 0);
+      w.wait(&ctl.q_full[0], q_uses[0]++ & 1);
+      if (nqt == 2) w.wait(&ctl.q_full[1], q_uses[1]++ & 1);
       tc_fence_after();
       const int items = nt * nqt;
       // item n: query tile q, token tile it; its weights' product follows the next item's logits
@@ -973,9 +1016,10 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
         __syncwarp();
         const uint32_t p = tmem + G::kColS + G::TT * slot, o = tmem + G::kColO + q * D;
         const uint64_t v = sdesc_k_sw128(base + G::kOffV + st * G::kTileBytes);
-#pragma unroll
-        for (int k = 0; k < G::TT / 64; ++k)
-          mma_ts_tile_chunk_elect(o, p + 32 * k, v + k * (D * 128 / 16), idesc_o, it > 0 || k > 0);
+        if constexpr (G::TT == 128)
+          mma_ts_tile_pair_elect(o, p, p + 32, v, v + D * 128 / 16, idesc_o, it > 0);
+        else
+          mma_ts_tile_chunk_elect(o, p, v, idesc_o, it > 0);
         mma_commit_elect(&ctl.pv_done[q]);
         if (q == nqt - 1) mma_commit_elect(&ctl.v_empty[st]);
       };
@@ -991,13 +1035,15 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
         const uint64_t kd = sdesc_k_sw128(base + G::kOffK + st * G::kTileBytes);
         if constexpr (G::kQTmem) {
 #pragma unroll
-          for (int j = 0; j < G::J; ++j)
-            mma_ts_tile_chunk_elect(x, tmem + G::kColQ + 32 * j, kd + j * (G::TT * 8), idesc_x, j > 0);
+          for (int j = 0; j < G::J; j += 2)
+            mma_ts_tile_pair_elect(x, tmem + G::kColQ + 32 * j, tmem + G::kColQ + 32 * (j + 1),
+                                   kd + j * (G::TT * 8), kd + (j + 1) * (G::TT * 8), idesc_x, j > 0);
         } else {
           const uint64_t qd = sdesc_k_sw128(base + q * G::kQBytes);
-#pragma unroll
-          for (int j = 0; j < G::J; ++j)
-            mma_ss_chunk(x, qd + j * 1024, kd + j * (G::TT * 8), idesc_x, j > 0);
+          if constexpr (G::J == 2)
+            mma_ss_pair(x, qd, kd, 1024, G::TT * 8, idesc_x, 0);
+          else
+            mma_ss_chunk(x, qd, kd, idesc_x, 0);
         }
         mma_commit_elect(&ctl.s_full[slot]);
         if (q == nqt - 1) mma_commit_elect(&ctl.k_empty[st]);
@@ -1015,7 +1061,7 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == G::kMmaWarp) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
