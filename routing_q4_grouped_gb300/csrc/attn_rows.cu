@@ -14,12 +14,12 @@
 // one fp16 fma with 2^24 s, with one rounding of 2^-11.
 //
 // fp16's range. Queries are divided by the power of two under their row's largest
-// element. A tile's keys and values are divided by powers of two 2^eK and 2^eV 2^8 above
+// element. The keys and the values of each 32 tokens are divided by powers of two 2^eK and 2^eV 2^8 above
 // their largest magnitude (so 2^24 s fits, and what is 2^-8 of the largest is still a
 // normal number); eK goes into the logits' factor, and 2^eV into the
 // weights' exponent: P' = exp2(x - m + eV - E) with a running E per row, so P' stays
-// near 1 whatever the values' size. A tile whose tokens differ by more than 2^6 in
-// magnitude takes one exponent per token (the same formulas with a factor per
+// near 1 whatever the values' size. A tile with tokens that differ by more than 2^6
+// within 32 takes one exponent per token (the same formulas with a factor per
 // column), as does one with a NaN group or a page outside the cache.
 //
 // The row maximum is not looked for tile by tile: m is only a reference, any value
@@ -33,7 +33,8 @@
 //   0-3, 4-7  softmax of query tile 0 and 1 (warp % 4 = tensor-memory lane quarter),
 //             their queries' load and their outputs' store
 //   11        issues the products
-//   8 9 10 12 13 14 16 17 (D = 64: the first four)  codes to operands
+//   15        finds the pages of the tiles ahead
+//   8 9 10 12 13 14 16 17 (D = 64: the first four)  scales, and codes to operands
 // D <= 128: two query tiles share each token tile and take turns, one in the tensor
 // cores while the other is in its softmax. D = 256: one query tile, held in tensor
 // memory, tiles of 64 tokens, and logits that alternate between two slots. Every wait on an mbarrier has a time limit; after one
@@ -51,7 +52,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 11;
+constexpr int kMmaWarp = 11, kPageWarp = 15;
 // Conversion warps: 8 9 10, 12 13 14, 16 17, i.e. none with warp % 4 == 3. A warp issues
 // from sub-partition warp % 4, and the products' warp must not wait for busy neighbours
 // there: alone on the multiprocessor it issues one product per 64 cycles (their full rate),
@@ -70,7 +71,7 @@ struct RowGeo {
   static constexpr int TT = D == 256 ? 64 : 128;      // tokens of a tile
   static constexpr int kConvWarps = D == 64 ? 4 : 8;
   static constexpr int kConvThreads = kConvWarps * 32;
-  static constexpr int kThreads = (kConvWarps == 4 ? 13 : 18) * 32;
+  static constexpr int kThreads = (kConvWarps == 4 ? 16 : 18) * 32;
   static constexpr int KS = D == 256 ? 3 : 2;         // operand tiles in flight, keys and values each
   static constexpr bool kQTmem = D == 256;            // queries in tensor memory, not shared memory
   static constexpr uint32_t kQBytes = kQTmem ? 0 : 128 * D * 2;   // a query tile
@@ -82,7 +83,7 @@ struct RowGeo {
   static constexpr uint32_t kColS = QT * D;           // then two logit slots of TT columns,
   static constexpr uint32_t kColQ = kColS + 2 * TT;   // then the queries
   static_assert(kColQ + (kQTmem ? D / 2 : 0) <= kTmemCols, "tensor memory");
-  static_assert(KS + 1 <= kMetaRing, "a tile's scales outlive its operands by one tile");
+  static_assert(KS < kMetaRing, "rings");
 };
 
 // Scales, biases and exponents of one tile, ready for use.
@@ -94,17 +95,19 @@ struct alignas(16) Meta {
   float kf[TT];                        // 2^eK of each token (slow tiles)
   float ve[TT];                        // eV of each token (slow tiles)
   uint8_t flag[TT];                    // bit j: value group j is NaN; kDead
-  float tile_kf, tile_ve;              // of all tokens (other tiles)
-  int slow;
+  // of each run of 32 tokens (other tiles), and whether its keys or values need more
+  float run_kf[4], run_ve[4];
+  int slow[2][4];
 };
 
 struct Ctl {
-  uint64_t q_full[2], k_full[3], k_empty[3], v_full[3], v_empty[3];
-  uint64_t s_full[2], p_full[2], pv_done[2], meta_full[kMetaRing], drain;
+  uint64_t q_full[2], k_full[3], k_empty[3], v_full[3];
+  uint64_t s_full[2], p_full[2], pv_done[2], drain;
+  // of tile t at t % 4: pages found; scales written; products done
+  uint64_t base_full[kMetaRing], meta_full[kMetaRing], done[kMetaRing];
   int64_t base[kMetaRing][8];          // byte offset of a 16-token block's key codes
   int32_t words[kMetaRing][8];         // from there to its words; -1: no such block (its codes
                                        // are read from the cache's start and multiplied by 0)
-  int red_max[2][4], red_min[2][4], red_bad[2][4];
   uint32_t tmem_base;
   int abort;
 };
@@ -275,78 +278,157 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// -------------------------------------------------- pages of the tiles ahead
+
+// One warp turns page numbers into the offsets of each tile's 16-token blocks, up to
+// three tiles ahead of the products.
+template <int D, int BITS>
+struct Pages {
+  using G = RowGeo<D>;
+  static constexpr int J = G::J, TT = G::TT;
+  static constexpr int RB = D * BITS / 8;
+  const AttnArgs& a;
+  Ctl& ctl;
+  int lane;
+
+  __device__ void run(const Seg& sg, int seen, uint32_t& tc, Waiter& w) {
+    int tok = sg.kt0 * TT + 16 * lane;               // lane i has block i of a tile
+    const auto look = [&](int t, int& page, uint32_t& in_page) {
+      const uint32_t blk = static_cast<uint32_t>(t) >> 4;
+      const uint32_t at = static_cast<uint32_t>((blk * a.page_magic) >> 40);
+      in_page = blk - at * a.page_blocks;
+      page = lane < TT / 16 && t < seen ? __ldg(sg.pages + at) : -1;
+    };
+    int page, next;
+    uint32_t in_page, next_in;
+    look(tok, page, in_page);
+    for (int it = sg.kt0; it < sg.kt1; ++it, ++tc, tok += TT) {
+      const int slot = tc % kMetaRing;
+      look(tok + TT, next, next_in);
+      if (tc >= kMetaRing) w.wait(&ctl.done[slot], (tc / kMetaRing - 1) & 1);
+      if (lane < TT / 16) {
+        int64_t off = 0;
+        int wd = -1;
+        if (page >= 0 && page < a.c.pages) {
+          off = page * a.c.page_bytes + static_cast<int64_t>(sg.hk) * a.c.head_bytes +
+                in_page * (16 * RB);
+          wd = a.c.code_bytes + static_cast<int>(in_page) * (16 * J * 4 - 16 * RB);
+        } else if (tok < seen) {
+          atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
+        }
+        ctl.base[slot][lane] = off;
+        ctl.words[slot][lane] = wd;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.base_full[slot]);
+      page = next;
+      in_page = next_in;
+    }
+  }
+};
+
 // -------------------------------------------------------- codes to operands
 
 template <int D, int BITS>
 struct Converter {
   using G = RowGeo<D>;
-  static constexpr int J = G::J;
   static constexpr int RB = D * BITS / 8;
   static constexpr int TT = G::TT;
   static constexpr int PR = D / 16;                  // 16-code pieces of a row
-  static constexpr int KU = TT * PR / G::kConvThreads;  // key pieces per thread and tile
+  static constexpr int KU = TT * PR / G::kConvThreads;    // key pieces per thread and tile
   static constexpr int VU = TT * D / 64 / G::kConvThreads;   // value pieces (8 tokens x 8 elements)
-  // tokens (keys, then values) per thread and tile; with more threads than tokens the
-  // last warps have none
-  static constexpr int WU = 2 * TT > G::kConvThreads ? 2 * TT / G::kConvThreads : 1;
   static constexpr int KW = BITS / 2;                // words of a key piece (16 codes)
+  static constexpr int J = G::J;
+  // runs of 32 tokens, keys and values, per warp and tile (with fewer runs than warps the
+  // last warps have none)
+  static constexpr int kRuns = 2 * TT / 32;
+  static constexpr int WU = kRuns > G::kConvWarps ? kRuns / G::kConvWarps : 1;
 
   const AttnArgs& a;
   Ctl& ctl;
   Meta<D>* metas;
   uint8_t* smem;
-  int ct, cw, lane;
+  int cw, lane;
+  uint32_t words[WU][J];
   uint32_t kr[KU][KW];
   uint32_t vr[VU][8][BITS / 4];
 
-  // Block offsets of the tile at token tok0 into ring slot `slot` (8 threads).
-  __device__ void put_base(int slot, int page, int tok, int end, int hk) {
-    int64_t off = 0;
-    int wd = -1;
-    if (tok < end && page >= 0 && page < a.c.pages) {
-      const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
-      const uint32_t in_page =
-          blk - static_cast<uint32_t>((blk * a.page_magic) >> 40) * a.page_blocks;
-      off = page * a.c.page_bytes + static_cast<int64_t>(hk) * a.c.head_bytes + in_page * (16 * RB);
-      wd = a.c.code_bytes + static_cast<int>(in_page) * (16 * J * 4 - 16 * RB);
-    } else if (tok < end) {
-      atomicOr(a.c.err, MOE_DEVERR_BAD_PAGE);
-    }
-    ctl.base[slot][ct] = off;
-    ctl.words[slot][ct] = wd;
+  // Run i of this warp: tokens 32 r + lane of the keys (kv = 0) or of the values.
+  __device__ __forceinline__ bool run_of(int i, int& kv, int& r) const {
+    const int id = cw + G::kConvWarps * i;
+    kv = id / (TT / 32);
+    r = id % (TT / 32);
+    return id < kRuns;
   }
-  __device__ int page_at(const int32_t* pages, int tok, int end) const {
-    if (tok >= end) return -1;
-    const uint32_t blk = static_cast<uint32_t>(tok) >> 4;
-    return __ldg(pages + static_cast<uint32_t>((blk * a.page_magic) >> 40));
-  }
-
-  // Item i of this thread: token tk of the keys (kv = 0) or of the values.
-  __device__ __forceinline__ void word_item(int i, int& kv, int& tk) const {
-    const int id = ct + G::kConvThreads * i;
-    kv = id / TT;
-    tk = id % TT;
-  }
-  // This thread's scale and bias words.
-  __device__ __forceinline__ bool has_words() const { return ct < 2 * TT; }
-  __device__ void load_words(int slot, uint32_t (&w)[WU][J]) const {
-    if (!has_words()) return;
+  __device__ void load_words(int slot) {
 #pragma unroll
     for (int i = 0; i < WU; ++i) {
-      int kv, tk;
-      word_item(i, kv, tk);
+      int kv, r;
+      if (!run_of(i, kv, r)) return;
+      const int tk = 32 * r + lane;
       const uint8_t* p = a.c.data + ctl.base[slot][tk >> 4] + max(ctl.words[slot][tk >> 4], 0) +
                          (tk & 15) * (J * 4);
       if (kv) p += static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes;
       if constexpr (J == 1) {
-        w[i][0] = ld_nc_u32(p);
+        words[i][0] = ld_nc_u32(p);
       } else if constexpr (J == 2) {
         const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-        w[i][0] = v.x, w[i][1] = v.y;
+        words[i][0] = v.x, words[i][1] = v.y;
       } else {
         const uint4 v = ld_nc_v4(p);
-        w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+        words[i][0] = v.x, words[i][1] = v.y, words[i][2] = v.z, words[i][3] = v.w;
       }
+    }
+  }
+  // Exponents, scales and biases of a tile of `n` seen tokens from the loaded words.
+  __device__ void put_meta(Meta<D>& m, int slot, int n) const {
+#pragma unroll
+    for (int i = 0; i < WU; ++i) {
+      int kv, r;
+      if (!run_of(i, kv, r)) return;
+      const int tk = 32 * r + lane;
+      const bool ok = tk < n && ctl.words[slot][tk >> 4] >= 0;
+      uint32_t e = 0, bad = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const uint32_t se = exp_field(words[i][j]), be = exp_field(words[i][j] >> 16);
+        if (se == 255u || be == 255u)
+          bad |= 1u << j;
+        else
+          e = max(e, max(se ? se + BITS : 0u, be));
+      }
+      if (!ok) e = bad = 0;
+      const uint32_t top = __reduce_max_sync(kAll, e);
+      const uint32_t low = __reduce_min_sync(kAll, e ? e : 255u);
+      // NaN values, and tokens that a page outside the cache would hold
+      const bool odd = __any_sync(kAll, (kv == 1 && bad) || (tk < n && !ok));
+      const bool slow = odd || top > low + kMaxSpread;
+      const uint32_t E = top == 0 ? 127u : min(top, 253u);
+      const uint32_t eu = slow && e ? min(e, 253u) : E;
+      const float down = pow2_field(254u - eu) * 0x1p-8f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const bool nan = bad >> j & 1;
+        const float s = ok && !nan ? bf16_lo(words[i][j]) * (down * 0x1p24f) : 0.f;
+        const float b = ok && !nan ? bf16_hi(words[i][j]) * down : 0.f;
+        uint32_t sb = pack_f16(s, b);
+        if (kv == 0) {
+          if (nan) sb = 0x7E000000u;                 // a NaN key: NaN logits
+          m.ksb[j][tk] = sb;
+        } else {
+          m.vs[j][tk] = static_cast<uint16_t>(sb);
+          m.vb[j][tk] = static_cast<uint16_t>(sb >> 16);
+        }
+      }
+      if (kv == 0) {
+        m.kf[tk] = pow2_field(eu) * 0x1p8f;
+        if (lane == 0) m.run_kf[r] = pow2_field(E) * 0x1p8f;
+      } else {
+        m.ve[tk] = static_cast<float>(static_cast<int>(eu) - 119);
+        m.flag[tk] = static_cast<uint8_t>(bad | (tk < n && !ok ? kDead : 0));
+        if (lane == 0) m.run_ve[r] = static_cast<float>(static_cast<int>(E) - 119);
+      }
+      if (lane == 0) m.slow[kv][r] = slow;
     }
   }
 
@@ -404,84 +486,6 @@ struct Converter {
         }
       }
     }
-  }
-
-  // Exponents, scales and biases of a tile of `n` seen tokens from this thread's words.
-  __device__ void put_meta(Meta<D>& m, int slot, const uint32_t (&w)[WU][J], int n) {
-    uint32_t e[WU], bad[WU];
-    bool valid[WU];
-#pragma unroll
-    for (int i = 0; i < WU && has_words(); ++i) {
-      int kv, tk;
-      word_item(i, kv, tk);
-      valid[i] = tk < n && ctl.words[slot][tk >> 4] >= 0;
-      e[i] = bad[i] = 0;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const uint32_t se = exp_field(w[i][j]), be = exp_field(w[i][j] >> 16);
-        if (se == 255u || be == 255u)
-          bad[i] |= 1u << j;
-        else
-          e[i] = max(e[i], max(se ? se + BITS : 0u, be));
-      }
-      if (!valid[i]) e[i] = bad[i] = 0;
-      const uint32_t top = __reduce_max_sync(kAll, e[i]);
-      const uint32_t low = __reduce_min_sync(kAll, e[i] ? e[i] : 255u);
-      // NaN values, and tokens that a page outside the cache would hold
-      const bool odd = __any_sync(kAll, (kv == 1 && bad[i]) || (tk < n && !valid[i]));
-      if (lane == 0) {                               // a warp's tokens are all keys or all values
-        ctl.red_max[kv][tk / 32] = static_cast<int>(top);
-        ctl.red_min[kv][tk / 32] = static_cast<int>(low);
-        ctl.red_bad[kv][tk / 32] = odd;
-      }
-    }
-    named_bar_sync(1, G::kConvThreads);
-    int E[2], slow = 0;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      int hi = 0, lo = 255;
-#pragma unroll
-      for (int k = 0; k < TT / 32; ++k) {
-        hi = max(hi, ctl.red_max[v][k]);
-        lo = min(lo, ctl.red_min[v][k]);
-        slow |= ctl.red_bad[v][k];
-      }
-      slow |= hi - lo > kMaxSpread;
-      E[v] = hi == 0 ? 127 : min(hi, 253);
-    }
-#pragma unroll
-    for (int i = 0; i < WU && has_words(); ++i) {
-      int kv, tk;
-      word_item(i, kv, tk);
-      const uint32_t eu = slow && e[i] ? min(e[i], 253u) : static_cast<uint32_t>(kv ? E[1] : E[0]);
-      const float down = pow2_field(254u - eu) * 0x1p-8f;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const bool nan = bad[i] >> j & 1;
-        const float s = valid[i] && !nan ? bf16_lo(w[i][j]) * down * 0x1p24f : 0.f;
-        const float b = valid[i] && !nan ? bf16_hi(w[i][j]) * down : 0.f;
-        uint32_t sb = pack_f16(s, b);
-        if (kv == 0) {
-          if (nan) sb = 0x7E000000u;                 // a NaN key: NaN logits
-          m.ksb[j][tk] = sb;
-        } else {
-          m.vs[j][tk] = static_cast<uint16_t>(sb);
-          m.vb[j][tk] = static_cast<uint16_t>(sb >> 16);
-        }
-      }
-      if (kv == 0) {
-        m.kf[tk] = pow2_field(eu) * 0x1p8f;
-      } else {
-        m.ve[tk] = static_cast<float>(static_cast<int>(eu) - 119);
-        m.flag[tk] = static_cast<uint8_t>(bad[i] | (tk < n && !valid[i] ? kDead : 0));
-      }
-    }
-    if (ct == 0) {
-      m.tile_kf = pow2_field(static_cast<uint32_t>(E[0])) * 0x1p8f;
-      m.tile_ve = static_cast<float>(E[1] - 119);
-      m.slow = slow;
-    }
-    named_bar_sync(1, G::kConvThreads);
   }
 
   // Keys: 16 codes of a token -> two 16-byte chunks of its row. 4-bit chunks hold
@@ -557,48 +561,51 @@ struct Converter {
     }
   }
 
-  // All tiles of one piece; `tc` counts this block's tiles.
+  // All tiles of one piece; `tc` counts this block's tiles. What a tile needs from memory
+  // is requested as soon as its registers are free, half a tile and more ahead, and its
+  // scales are ready before its keys are: no warp waits for another inside a tile.
   __device__ void run(const Seg& sg, int seen, uint32_t& tc, Waiter& w) {
-    const int nt = sg.kt1 - sg.kt0;
-    const int tok0 = sg.kt0 * TT;
-    uint32_t words[WU][J];
-    int page = -1;
-    // no reader of the ring slots written here is left: the softmax of the piece before is
-    // at most a tile behind the products, whose last use of a slot freed it
-    if (ct < TT / 16) {
-      put_base(tc & 3, page_at(sg.pages, tok0 + 16 * ct, seen), tok0 + 16 * ct, seen, sg.hk);
-      page = page_at(sg.pages, tok0 + TT + 16 * ct, seen);
+    const auto pages_of = [&](uint32_t t) {
+      w.wait(&ctl.base_full[t % kMetaRing], (t / kMetaRing) & 1);
+    };
+    const auto scales_for = [&](uint32_t t, int it) {   // (the ring slot was tile t - 4's)
+      if (t >= kMetaRing) w.wait(&ctl.done[t % kMetaRing], (t / kMetaRing - 1) & 1);
+      put_meta(metas[t % kMetaRing], t % kMetaRing, min(seen - it * TT, TT));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.meta_full[t % kMetaRing]);
+    };
+    pages_of(tc);
+    load_words(tc % kMetaRing);
+    load_keys(tc % kMetaRing);
+    load_values(tc % kMetaRing);
+    scales_for(tc, sg.kt0);
+    if (sg.kt0 + 1 < sg.kt1) {
+      pages_of(tc + 1);
+      load_words((tc + 1) % kMetaRing);
     }
-    named_bar_sync(1, G::kConvThreads);
-    load_words(tc & 3, words);
-    load_keys(tc & 3);
-    for (int it = 0; it < nt; ++it, ++tc) {
-      const int slot = tc & 3, st = tc % G::KS;
-      const int tok = tok0 + it * TT;
-      if (ct < TT / 16) {
-        const int nx = tok + TT + 16 * ct;
-        put_base((tc + 1) & 3, page, nx, it + 1 < nt ? seen : 0, sg.hk);
-        page = page_at(sg.pages, nx + TT, seen);
-      }
-      Meta<D>& m = metas[slot];
-      put_meta(m, slot, words, min(seen - tok, TT));
-      if (lane == 0) mbar_arrive(&ctl.meta_full[slot]);
-      load_values(slot);
-      const uint32_t parity = ((tc / G::KS) & 1) ^ 1;
-      w.wait(&ctl.k_empty[st], parity);
+    for (int it = sg.kt0; it < sg.kt1; ++it, ++tc) {
+      const int st = tc % G::KS;
+      const Meta<D>& m = metas[tc % kMetaRing];
+      w.wait(&ctl.meta_full[tc % kMetaRing], (tc / kMetaRing) & 1);
+      if (tc >= G::KS) w.wait(&ctl.k_empty[st], (tc / G::KS - 1) & 1);
       put_keys(m, G::kOffK + st * G::kTileBytes);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.k_full[st]);
-      if (it + 1 < nt) {
-        load_words((tc + 1) & 3, words);
-        load_keys((tc + 1) & 3);
+      if (it + 1 < sg.kt1) {
+        load_keys((tc + 1) % kMetaRing);
+        scales_for(tc + 1, it + 1);
       }
-      w.wait(&ctl.v_empty[st], parity);
+      if (tc >= G::KS) w.wait(&ctl.done[(tc - G::KS) % kMetaRing], ((tc - G::KS) / kMetaRing) & 1);
       put_values(m, G::kOffV + st * G::kTileBytes);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.v_full[st]);
+      if (it + 1 < sg.kt1) load_values((tc + 1) % kMetaRing);
+      if (it + 2 < sg.kt1) {
+        pages_of(tc + 2);
+        load_words((tc + 2) % kMetaRing);
+      }
     }
   }
 };
@@ -683,29 +690,28 @@ struct Softmax {
     return x;
   }
 
-  // Weights of columns 64 H .. 64 H + 63 into registers, and their sum.
-  template <bool MASK, int H>
-  __device__ __forceinline__ float weights(uint32_t s_col, float ck, float off, int lim,
-                                           uint32_t (&p)[32]) {
+  // Weights of the 32 tokens of run R into registers p[0 .. 15], and their sum.
+  template <bool MASK, int R>
+  __device__ __forceinline__ float weights(uint32_t s_col, float ck, float off, int lim, uint32_t* p) {
     const uint64_t ck2 = pack_f32x2(ck, ck), off2 = pack_f32x2(off, off);
     uint64_t part[2] = {0, 0};
 #pragma unroll
-    for (int h = 0; h < 64 / kLoad; ++h) {
+    for (int h = 0; h < 32 / kLoad; ++h) {
       // (a tensor-memory load is waited for at once: its registers arrive late, and the
       // compiler must not move them in between)
       uint32_t v[kLoad];
       if constexpr (kLoad == 32) {
-        tmem_ld_32x32b_x32(tmem + s_col + 64 * H + 32 * h, v);
+        tmem_ld_32x32b_x32(tmem + s_col + 32 * R, v);
         tmem_ld_wait();
         tmem_regs_ready(reinterpret_cast<uint32_t(&)[16]>(v[16]));
       } else {
-        tmem_ld_32x32b_x16(tmem + s_col + 64 * H + 16 * h, v);
+        tmem_ld_32x32b_x16(tmem + s_col + 32 * R + 16 * h, v);
         tmem_ld_wait();
       }
       tmem_regs_ready(reinterpret_cast<uint32_t(&)[16]>(v[0]));
 #pragma unroll
       for (int i = 0; i < kLoad; i += 2) {
-        const int col = 64 * H + kLoad * h + i;
+        const int col = 32 * R + kLoad * h + i;
         float x0, x1;
         unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), ck2, off2),
                      x0, x1);
@@ -728,18 +734,18 @@ struct Softmax {
   __device__ __forceinline__ void move(uint32_t s_col, const Meta<D>& t, int lim, bool need, bool first,
                                        uint64_t* pv, uint32_t pv_parity, Waiter& w) {
     float mx = -INFINITY, ux = -INFINITY;
-    const float ck = c * t.tile_kf;
 #pragma unroll 1
     for (int h = H0; h < G::TT / 16; ++h) {
       uint32_t v[16];
       tmem_ld_32x32b_x16(tmem + s_col + 16 * h, v);
       tmem_ld_wait();
       tmem_regs_ready(v);
+      const float ck = c * t.run_kf[h >> 1], ve = t.run_ve[h >> 1];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float x = logit<SLOW, MASK>(__uint_as_float(v[i]), ck, t, 16 * h + i, lim);
         mx = fmaxf(mx, x);
-        ux = fmaxf(ux, x + (SLOW ? t.ve[16 * h + i] : t.tile_ve));
+        ux = fmaxf(ux, x + (SLOW ? t.ve[16 * h + i] : ve));
       }
     }
     float fo = 1.f;
@@ -790,17 +796,22 @@ struct Softmax {
   __device__ __forceinline__ void half_tile(uint32_t s_col, const Meta<D>& t, int lim, bool first,
                                             uint64_t* pv, uint32_t pv_parity, Waiter& w) {
     uint32_t p[32];
-    float size, d;
+    const float2 kf = *reinterpret_cast<const float2*>(&t.run_kf[2 * H]);
+    const float2 ve = *reinterpret_cast<const float2*>(&t.run_ve[2 * H]);
+    float s0, s1, d0, d1;
     bool need = m == -INFINITY && lim > 64 * H;
 #pragma unroll 1
     for (int round = 0;; ++round) {
       if (__any_sync(kAll, need)) move<false, MASK, 4 * H>(s_col, t, lim, need, first, pv, pv_parity, w);
-      d = fmaxf(t.tile_ve - E, -60.f);
-      size = weights<MASK, H>(s_col, c * t.tile_kf, d - (m == -INFINITY ? 0.f : m), lim, p);
-      need = size >= 32768.f;
+      const float ref = m == -INFINITY ? 0.f : m;
+      d0 = fmaxf(ve.x - E, -60.f);
+      d1 = fmaxf(ve.y - E, -60.f);
+      s0 = weights<MASK, 2 * H>(s_col, c * kf.x, d0 - ref, lim, p);
+      s1 = weights<MASK, 2 * H + 1>(s_col, c * kf.y, d1 - ref, lim, p + 16);
+      need = fmaxf(s0, s1) >= 32768.f;
       if (round || !__any_sync(kAll, need)) break;
     }
-    l = fmaf(size, exp2_approx(-d), l);
+    l = fmaf(s0, exp2_approx(-d0), fmaf(s1, exp2_approx(-d1), l));
     tmem_st_32x32b_x16(tmem + s_col + 32 * H, reinterpret_cast<uint32_t(&)[16]>(p[0]));
     tmem_st_32x32b_x16(tmem + s_col + 32 * H + 16, reinterpret_cast<uint32_t(&)[16]>(p[16]));
     tmem_st_wait();
@@ -844,8 +855,8 @@ struct Softmax {
     tmem_st_wait();
   }
 
-  __device__ void run(const Seg& sg, int nqt, uint32_t tc, const uint32_t (&sc)[2], uint32_t pc,
-                      Waiter& w) {
+  // sp: parity of each logit slot's next phase (bit = slot); pc: products into O so far.
+  __device__ void run(const Seg& sg, int nqt, uint32_t tc, uint32_t sp, uint32_t pc, Waiter& w) {
     const int r = sg.row0 + wg * 128 + (warp & 3) * 32 + lane;
     const bool live = r < sg.n_rows;
     const int qrow = live ? (sg.pre ? r / a.G : sg.b * a.nq + r / a.G) : 0;
@@ -865,16 +876,18 @@ struct Softmax {
     const int nt = sg.kt1 - sg.kt0;
     for (int it = 0; it < nt; ++it) {
       const int slot = nqt == 2 ? wg : it & 1;
-      const uint32_t use = sc[slot] + (nqt == 2 ? it : it >> 1);
       const Meta<D>& t = metas[(tc + it) & 3];
       w.wait(&ctl.meta_full[(tc + it) & 3], ((tc + it) >> 2) & 1);
-      w.wait(&ctl.s_full[slot], use & 1);
+      w.wait(&ctl.s_full[slot], sp >> slot & 1);
+      sp ^= 1u << slot;
       tc_fence_after();
       const int rel = lim - (sg.kt0 + it) * G::TT;
       const uint32_t s_col = G::kColS + G::TT * slot;
       const uint32_t pv_parity = (pc + it - 1) & 1;
       uint64_t* pv = &ctl.pv_done[wg];
-      if (t.slow)
+      int slow = t.slow[0][0] | t.slow[0][1] | t.slow[1][0] | t.slow[1][1];
+      if (G::TT == 128) slow |= t.slow[0][2] | t.slow[0][3] | t.slow[1][2] | t.slow[1][3];
+      if (slow)
         slow_tile(s_col, t, rel, it == 0, pv, pv_parity, w);
       else if (__all_sync(kAll, rel >= G::TT))
         tile<false>(s_col, t, rel, it == 0, pv, pv_parity, w);
@@ -942,7 +955,6 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
       mbar_init(&ctl.k_full[i], G::kConvWarps);
       mbar_init(&ctl.k_empty[i], 1);
       mbar_init(&ctl.v_full[i], G::kConvWarps);
-      mbar_init(&ctl.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.q_full[i], 4);
@@ -950,7 +962,11 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
       mbar_init(&ctl.p_full[i], 4);
       mbar_init(&ctl.pv_done[i], 1);
     }
-    for (int i = 0; i < kMetaRing; ++i) mbar_init(&ctl.meta_full[i], G::kConvWarps);
+    for (int i = 0; i < kMetaRing; ++i) {
+      mbar_init(&ctl.base_full[i], 1);
+      mbar_init(&ctl.meta_full[i], G::kConvWarps);
+      mbar_init(&ctl.done[i], 1);
+    }
     mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     fence_mbar_init();
@@ -967,92 +983,121 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
   griddep_launch_dependents();
   Waiter w{&ctl, a.c.err, a.timeout_ns, true};
 
-  // counts of tiles, uses of the logit slots and products into each O so far
-  uint32_t tc = 0, sc[2] = {0, 0}, pc[2] = {0, 0};
+  uint32_t tc = 0;                               // this block's tiles so far
   Walk walk(a);
   Seg sg;
+  const auto query_tiles = [](const Seg& g) { return G::QT == 2 && g.row0 + 128 < g.n_rows ? 2 : 1; };
   if (warp < kSoftWarps) {
     Softmax<D, BITS> sm{a, ctl, metas, smem, tmem + ((warp & 3) << 21), warp >> 2, warp, lane};
+    uint32_t sp = 0, pc[2] = {0, 0};
     while (walk.next(a, sg, threadIdx.x == 0)) {
-      const int nt = sg.kt1 - sg.kt0;
-      const int nqt = G::QT == 2 && sg.row0 + 128 < sg.n_rows ? 2 : 1;
-      if (sm.wg < nqt) sm.run(sg, nqt, tc, sc, pc[sm.wg], w);
+      const int nt = sg.kt1 - sg.kt0, nqt = query_tiles(sg);
+      if (sm.wg < nqt) sm.run(sg, nqt, tc, sp, sm.wg ? pc[1] : pc[0], w);
       // a warpgroup without a query tile may not run ahead: a wait tells only
       // neighbouring phases of its barrier apart
       named_bar_sync(2, kSoftWarps * 32);
       tc += nt;
-      sc[0] += nqt == 2 ? nt : (nt + 1) / 2;
-      sc[1] += nqt == 2 ? nt : nt / 2;
+      sp ^= nqt == 2 ? (nt & 1) * 3 : ((nt + 1) / 2 & 1) | (nt / 2 & 1) << 1;
       pc[0] += nt;
       pc[1] += nqt == 2 ? nt : 0;
     }
-  } else if (is_conv_warp(warp)) {
-    Converter<D, BITS> cv{a, ctl, metas, smem, conv_index(warp) * 32 + lane, conv_index(warp), lane};
+  } else if (is_conv_warp(warp) && conv_index(warp) < G::kConvWarps) {
+    Converter<D, BITS> cv{a, ctl, metas, smem, conv_index(warp), lane};
     while (walk.next(a, sg, false)) cv.run(sg, Walk::seen(a, sg), tc, w);
+  } else if (warp == kPageWarp) {
+    Pages<D, BITS> pg{a, ctl, lane};
+    while (walk.next(a, sg, false)) pg.run(sg, Walk::seen(a, sg), tc, w);
   } else if (warp == kMmaWarp) {
+    // This warp's own instructions set the pace of the products if there are many between
+    // them: the two orders of a piece are written out, ring positions and parities are
+    // counters of their own, and what comes from memory is broadcast from lane 0, which
+    // tells the compiler that it is the same in all lanes (uniform registers).
     const uint32_t idesc_x = idesc_f16(G::TT), idesc_o = idesc_f16(D);
-    // Counts and addresses are broadcast from lane 0, which tells the compiler that they are
-    // the same in all lanes: operands of the products then live in uniform registers,
-    // and the products issue without being moved there one by one (the issuing warp
-    // set the pace before).
     const uint32_t base = smem_u32(smem);
     const uint32_t tmem = __shfl_sync(kAll, ctl.tmem_base, 0);
-    uint32_t q_uses[2] = {0, 0};
+    uint32_t ks = 0, kp = 0, vs = 0, vp = 0;       // next key and value tile: ring place, parity
+    uint32_t dn = 0, qp[2] = {0, 0}, pp[2] = {0, 0};
+    const auto logits = [&](int q, int slot) {       // X of query tile q with key tile ks
+      __syncwarp();
+      const uint32_t x = tmem + G::kColS + G::TT * slot;
+      const uint64_t kd = sdesc_k_sw128(base + G::kOffK + ks * G::kTileBytes);
+      if constexpr (G::kQTmem) {
+#pragma unroll
+        for (int j = 0; j < G::J; j += 2)
+          mma_ts_tile_pair_elect(x, tmem + G::kColQ + 32 * j, tmem + G::kColQ + 32 * (j + 1),
+                                 kd + j * (G::TT * 8), kd + (j + 1) * (G::TT * 8), idesc_x, j > 0);
+      } else {
+        const uint64_t qd = sdesc_k_sw128(base + q * G::kQBytes);
+        if constexpr (G::J == 2)
+          mma_ss_pair(x, qd, kd, 1024, G::TT * 8, idesc_x, 0);
+        else
+          mma_ss_chunk(x, qd, kd, idesc_x, 0);
+      }
+      mma_commit_elect(&ctl.s_full[slot]);
+    };
+    const auto keys_done = [&]() {
+      mma_commit_elect(&ctl.k_empty[ks]);
+      if (++ks == G::KS) ks = 0, kp ^= 1;
+    };
+    const auto outputs = [&](int q, int slot, bool first) {   // O of query tile q with value tile vs
+      w.wait(&ctl.p_full[slot], slot ? pp[1] : pp[0]);
+      (slot ? pp[1] : pp[0]) ^= 1;
+      tc_fence_after();
+      __syncwarp();
+      const uint32_t p = tmem + G::kColS + G::TT * slot, o = tmem + G::kColO + q * D;
+      const uint64_t v = sdesc_k_sw128(base + G::kOffV + vs * G::kTileBytes);
+      if constexpr (G::TT == 128)
+        mma_ts_tile_pair_elect(o, p, p + 32, v, v + D * 128 / 16, idesc_o, !first);
+      else
+        mma_ts_tile_chunk_elect(o, p, v, idesc_o, !first);
+      mma_commit_elect(&ctl.pv_done[q]);
+    };
+    const auto values_done = [&]() {
+      mma_commit_elect(&ctl.done[dn]);
+      dn = (dn + 1) % kMetaRing;
+      if (++vs == G::KS) vs = 0, vp ^= 1;
+    };
     while (walk.next(a, sg, false)) {
       const int nt = __shfl_sync(kAll, sg.kt1 - sg.kt0, 0);
-      const int nqt =
-          __shfl_sync(kAll, G::QT == 2 && sg.row0 + 128 < sg.n_rows ? 2 : 1, 0);
-      w.wait(&ctl.q_full[0], q_uses[0]++ & 1);
-      if (nqt == 2) w.wait(&ctl.q_full[1], q_uses[1]++ & 1);
-      tc_fence_after();
-      const int items = nt * nqt;
-      // item n: query tile q, token tile it; its weights' product follows the next item's logits
-      const auto weigh = [&](int n) {
-        const int q = nqt == 2 ? n & 1 : 0, it = nqt == 2 ? n >> 1 : n, slot = n & 1;
-        const uint32_t t = tc + it, st = t % G::KS;
-        if (q == 0) w.wait(&ctl.v_full[st], (t / G::KS) & 1);
-        w.wait(&ctl.p_full[slot], (sc[slot] + (nqt == 2 ? it : it >> 1)) & 1);
+      const int nqt = __shfl_sync(kAll, query_tiles(sg), 0);
+      w.wait(&ctl.q_full[0], qp[0]);
+      qp[0] ^= 1;
+      if (nqt == 2) {
+        w.wait(&ctl.q_full[1], qp[1]);
+        qp[1] ^= 1;
         tc_fence_after();
-        __syncwarp();
-        const uint32_t p = tmem + G::kColS + G::TT * slot, o = tmem + G::kColO + q * D;
-        const uint64_t v = sdesc_k_sw128(base + G::kOffV + st * G::kTileBytes);
-        if constexpr (G::TT == 128)
-          mma_ts_tile_pair_elect(o, p, p + 32, v, v + D * 128 / 16, idesc_o, it > 0);
-        else
-          mma_ts_tile_chunk_elect(o, p, v, idesc_o, it > 0);
-        mma_commit_elect(&ctl.pv_done[q]);
-        if (q == nqt - 1) mma_commit_elect(&ctl.v_empty[st]);
-      };
-      for (int n = 0; n < items; ++n) {
-        const int q = nqt == 2 ? n & 1 : 0, it = nqt == 2 ? n >> 1 : n, slot = n & 1;
-        const uint32_t t = tc + it, st = t % G::KS;
-        if (q == 0) {
-          w.wait(&ctl.k_full[st], (t / G::KS) & 1);
+        for (int it = 0; it < nt; ++it) {
+          w.wait(&ctl.k_full[ks], kp);
           tc_fence_after();
+          logits(0, 0);
+          if (it > 0) {
+            outputs(1, 1, it == 1);
+            values_done();
+          }
+          logits(1, 1);
+          keys_done();
+          w.wait(&ctl.v_full[vs], vp);
+          outputs(0, 0, it == 0);
         }
-        __syncwarp();
-        const uint32_t x = tmem + G::kColS + G::TT * slot;
-        const uint64_t kd = sdesc_k_sw128(base + G::kOffK + st * G::kTileBytes);
-        if constexpr (G::kQTmem) {
-#pragma unroll
-          for (int j = 0; j < G::J; j += 2)
-            mma_ts_tile_pair_elect(x, tmem + G::kColQ + 32 * j, tmem + G::kColQ + 32 * (j + 1),
-                                   kd + j * (G::TT * 8), kd + (j + 1) * (G::TT * 8), idesc_x, j > 0);
-        } else {
-          const uint64_t qd = sdesc_k_sw128(base + q * G::kQBytes);
-          if constexpr (G::J == 2)
-            mma_ss_pair(x, qd, kd, 1024, G::TT * 8, idesc_x, 0);
-          else
-            mma_ss_chunk(x, qd, kd, idesc_x, 0);
+        outputs(1, 1, nt == 1);
+        values_done();
+      } else {
+        tc_fence_after();
+        for (int it = 0; it < nt; ++it) {
+          w.wait(&ctl.k_full[ks], kp);
+          tc_fence_after();
+          logits(0, it & 1);
+          keys_done();
+          if (it > 0) {
+            w.wait(&ctl.v_full[vs], vp);
+            outputs(0, (it - 1) & 1, it == 1);
+            values_done();
+          }
         }
-        mma_commit_elect(&ctl.s_full[slot]);
-        if (q == nqt - 1) mma_commit_elect(&ctl.k_empty[st]);
-        if (n > 0) weigh(n - 1);
+        w.wait(&ctl.v_full[vs], vp);
+        outputs(0, (nt - 1) & 1, nt == 1);
+        values_done();
       }
-      weigh(items - 1);
-      tc += nt;
-      sc[0] += nqt == 2 ? nt : (nt + 1) / 2;
-      sc[1] += nqt == 2 ? nt : nt / 2;
     }
     // nothing issued may outlive the tensor memory
     mma_commit_elect(&ctl.drain);
