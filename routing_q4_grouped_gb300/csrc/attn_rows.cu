@@ -615,7 +615,6 @@ struct Converter {
 template <int D, int BITS>
 struct Softmax {
   using G = RowGeo<D>;
-  static constexpr int kLoad = D == 128 ? 16 : 32;   // logits loaded at a time
   const AttnArgs& a;
   Ctl& ctl;
   Meta<D>* metas;
@@ -690,41 +689,41 @@ struct Softmax {
     return x;
   }
 
-  // Weights of the 32 tokens of run R into registers p[0 .. 15], and their sum.
-  template <bool MASK, int R>
-  __device__ __forceinline__ float weights(uint32_t s_col, float ck, float off, int lim, uint32_t* p) {
-    const uint64_t ck2 = pack_f32x2(ck, ck), off2 = pack_f32x2(off, off);
-    uint64_t part[2] = {0, 0};
+  // Weights of columns 64 H .. 64 H + 63 (runs 2H and 2H + 1, each with its factor and
+  // offset) into registers, and the runs' sums. The next 16 logits are on their way out of
+  // tensor memory while these are worked on.
+  template <bool MASK, int H>
+  __device__ __forceinline__ void weights(uint32_t s_col, const float (&ck)[2], const float (&off)[2],
+                                          int lim, uint32_t (&p)[32], float (&sum)[2]) {
+    uint32_t v[2][16];
+    tmem_ld_32x32b_x16(tmem + s_col + 64 * H, v[0]);
 #pragma unroll
-    for (int h = 0; h < 32 / kLoad; ++h) {
-      // (a tensor-memory load is waited for at once: its registers arrive late, and the
-      // compiler must not move them in between)
-      uint32_t v[kLoad];
-      if constexpr (kLoad == 32) {
-        tmem_ld_32x32b_x32(tmem + s_col + 32 * R, v);
-        tmem_ld_wait();
-        tmem_regs_ready(reinterpret_cast<uint32_t(&)[16]>(v[16]));
-      } else {
-        tmem_ld_32x32b_x16(tmem + s_col + 32 * R + 16 * h, v);
-        tmem_ld_wait();
-      }
-      tmem_regs_ready(reinterpret_cast<uint32_t(&)[16]>(v[0]));
+    for (int r = 0; r < 2; ++r) {
+      const uint64_t ck2 = pack_f32x2(ck[r], ck[r]), off2 = pack_f32x2(off[r], off[r]);
+      uint64_t part[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < kLoad; i += 2) {
-        const int col = 32 * R + kLoad * h + i;
-        float x0, x1;
-        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), ck2, off2),
-                     x0, x1);
-        if (MASK && col >= lim) x0 = -INFINITY;
-        if (MASK && col + 1 >= lim) x1 = -INFINITY;
-        const float w0 = exp2_approx(x0), w1 = exp2_approx(x1);
-        part[(i >> 1) & 1] = add_f32x2(part[(i >> 1) & 1], pack_f32x2(w0, w1));
-        p[kLoad / 2 * h + i / 2] = pack_f16(w0, w1);
+      for (int h = 2 * r; h < 2 * r + 2; ++h) {
+        uint32_t(&u)[16] = v[h & 1];
+        tmem_ld_wait();
+        tmem_regs_ready(u);
+        if (h < 3) tmem_ld_32x32b_x16(tmem + s_col + 64 * H + 16 * (h + 1), v[(h + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const int col = 64 * H + 16 * h + i;
+          float x0, x1;
+          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), ck2, off2),
+                       x0, x1);
+          if (MASK && col >= lim) x0 = -INFINITY;
+          if (MASK && col + 1 >= lim) x1 = -INFINITY;
+          const float w0 = exp2_approx(x0), w1 = exp2_approx(x1);
+          part[(i >> 1) & 1] = add_f32x2(part[(i >> 1) & 1], pack_f32x2(w0, w1));
+          p[8 * h + i / 2] = pack_f16(w0, w1);
+        }
       }
+      float s0, s1;
+      unpack_f32x2(add_f32x2(part[0], part[1]), s0, s1);
+      sum[r] = s0 + s1;
     }
-    float s0, s1;
-    unpack_f32x2(add_f32x2(part[0], part[1]), s0, s1);
-    return s0 + s1;
   }
 
   // Moves m to the largest logit of columns 16 H0 .. and E so that none of their
@@ -798,20 +797,21 @@ struct Softmax {
     uint32_t p[32];
     const float2 kf = *reinterpret_cast<const float2*>(&t.run_kf[2 * H]);
     const float2 ve = *reinterpret_cast<const float2*>(&t.run_ve[2 * H]);
-    float s0, s1, d0, d1;
+    float sum[2], d[2];
+    const float ck[2] = {c * kf.x, c * kf.y};
     bool need = m == -INFINITY && lim > 64 * H;
 #pragma unroll 1
     for (int round = 0;; ++round) {
       if (__any_sync(kAll, need)) move<false, MASK, 4 * H>(s_col, t, lim, need, first, pv, pv_parity, w);
       const float ref = m == -INFINITY ? 0.f : m;
-      d0 = fmaxf(ve.x - E, -60.f);
-      d1 = fmaxf(ve.y - E, -60.f);
-      s0 = weights<MASK, 2 * H>(s_col, c * kf.x, d0 - ref, lim, p);
-      s1 = weights<MASK, 2 * H + 1>(s_col, c * kf.y, d1 - ref, lim, p + 16);
-      need = fmaxf(s0, s1) >= 32768.f;
+      d[0] = fmaxf(ve.x - E, -60.f);
+      d[1] = fmaxf(ve.y - E, -60.f);
+      const float off[2] = {d[0] - ref, d[1] - ref};
+      weights<MASK, H>(s_col, ck, off, lim, p, sum);
+      need = fmaxf(sum[0], sum[1]) >= 32768.f;
       if (round || !__any_sync(kAll, need)) break;
     }
-    l = fmaf(s0, exp2_approx(-d0), fmaf(s1, exp2_approx(-d1), l));
+    l = fmaf(sum[0], exp2_approx(-d[0]), fmaf(sum[1], exp2_approx(-d[1]), l));
     tmem_st_32x32b_x16(tmem + s_col + 32 * H, reinterpret_cast<uint32_t(&)[16]>(p[0]));
     tmem_st_32x32b_x16(tmem + s_col + 32 * H + 16, reinterpret_cast<uint32_t(&)[16]>(p[16]));
     tmem_st_wait();
