@@ -65,7 +65,7 @@ struct RopeArgs {
   const uint64_t* phase;
   int64_t x_row, x_head, o_row, o_head;
   int T, H, D, rot;
-  int units;                 // units of 2V elements per head: rot / 2V turned, the rest copied
+  int units;                 // units of 2V elements per head, D / 2V
   int head_blocks;           // heads per thread: ceil(H / head_blocks)
   float mscale;
   int interleaved, backward, copy_tail;
@@ -89,12 +89,15 @@ template <>
 __device__ __forceinline__ float from_f(float v) { return v; }
 
 template <typename E, int V>
-struct alignas(V * sizeof(E) > 16 ? 16 : V * sizeof(E)) Vec {
+struct alignas(V * sizeof(E)) Vec {
   E e[V];
 };
 
-// Thread = (token, block of heads, unit of V pairs): the V angles are computed
-// once and used for every head of the block.
+// Thread = (token, block of heads, unit): a unit is two vectors of V elements rot/2 apart,
+// which hold V whole pairs in either layout (elements i and i + rot/2 meet across the two,
+// elements 2i and 2i + 1 within one), so that neighbouring lanes always touch
+// neighbouring vectors. The V angles are computed once and used for every head of the
+// block; heads go two at a time, to keep more loads in flight. Units past rot / 2V copy.
 template <typename E, int V>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
   griddep_wait();
@@ -110,49 +113,38 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
   const int turned = a.rot / (2 * V);
   const bool tail = u >= turned;
   if (tail && !a.copy_tail) return;
-  int first, second;                       // start of the unit's two runs of V elements
-  if (tail) {
-    first = a.rot + (u - turned) * 2 * V;
-    second = first + V;
-  } else if (a.interleaved) {
-    first = u * 2 * V;
-    second = first + V;
-  } else {
-    first = u * V;
-    second = first + a.rot / 2;
-  }
+  const int first = tail ? a.rot + (u - turned) * 2 * V : u * V;
+  const int second = tail ? first + V : first + a.rot / 2;
   const E* x = static_cast<const E*>(a.x) + t * a.x_row;
   E* o = static_cast<E*>(a.out) + t * a.o_row;
   using Vt = Vec<E, V>;
-  if (tail) {
-    for (int h = h0; h < h1; ++h) {
-      const Vt p = *reinterpret_cast<const Vt*>(x + h * a.x_head + first);
-      const Vt q = *reinterpret_cast<const Vt*>(x + h * a.x_head + second);
-      *reinterpret_cast<Vt*>(o + h * a.o_head + first) = p;
-      *reinterpret_cast<Vt*>(o + h * a.o_head + second) = q;
-    }
-    return;
-  }
   float c[V], s[V];
-  const int32_t pos = a.pos[t];
+  if (!tail) {
+    const int32_t pos = a.pos[t];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    rope_sincos(pos, a.phase[u * V + i], c[i], s[i]);
-    c[i] *= a.mscale;
-    s[i] *= a.backward ? -a.mscale : a.mscale;
+    for (int i = 0; i < V; ++i) {
+      // pairs of the first vector, then (interleaved) those of the second
+      const int pair = !a.interleaved ? first + i
+                       : i < V / 2    ? first / 2 + i
+                                      : second / 2 + i - V / 2;
+      rope_sincos(pos, a.phase[pair], c[i], s[i]);
+      c[i] *= a.mscale;
+      s[i] *= a.backward ? -a.mscale : a.mscale;
+    }
   }
-  for (int h = h0; h < h1; ++h) {
-    Vt p = *reinterpret_cast<const Vt*>(x + h * a.x_head + first);
-    Vt q = *reinterpret_cast<const Vt*>(x + h * a.x_head + second);
+  const auto turn = [&](Vt& p, Vt& q) {
+    if (tail) return;
     if (a.interleaved) {
-      E* e[2] = {p.e, q.e};
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        E& ea = V == 1 ? p.e[0] : e[2 * i / V][2 * i % V];
-        E& eb = V == 1 ? q.e[0] : e[(2 * i + 1) / V][(2 * i + 1) % V];
-        const float fa = to_f(ea), fb = to_f(eb);
-        ea = from_f<E>(rope_first(fa, fb, c[i], s[i]));
-        eb = from_f<E>(rope_second(fa, fb, c[i], s[i]));
+      for (int i = 0; i + 1 < V; i += 2) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          Vt& v = k ? q : p;
+          const int at = i / 2 + k * (V / 2);
+          const float fa = to_f(v.e[i]), fb = to_f(v.e[i + 1]);
+          v.e[i] = from_f<E>(rope_first(fa, fb, c[at], s[at]));
+          v.e[i + 1] = from_f<E>(rope_second(fa, fb, c[at], s[at]));
+        }
       }
     } else {
 #pragma unroll
@@ -162,20 +154,69 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
         q.e[i] = from_f<E>(rope_second(fa, fb, c[i], s[i]));
       }
     }
-    *reinterpret_cast<Vt*>(o + h * a.o_head + first) = p;
-    *reinterpret_cast<Vt*>(o + h * a.o_head + second) = q;
+  };
+  for (int h = h0; h < h1; h += 2) {
+    Vt p[2], q[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (h + k >= h1) break;
+      p[k] = *reinterpret_cast<const Vt*>(x + (h + k) * a.x_head + first);
+      q[k] = *reinterpret_cast<const Vt*>(x + (h + k) * a.x_head + second);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (h + k >= h1) break;
+      turn(p[k], q[k]);
+      *reinterpret_cast<Vt*>(o + (h + k) * a.o_head + first) = p[k];
+      *reinterpret_cast<Vt*>(o + (h + k) * a.o_head + second) = q[k];
+    }
   }
+}
+
+// One pair, or two elements to copy, per thread: any sizes, strides and alignment.
+template <typename E>
+__global__ void __launch_bounds__(kThreads) rope_pair_kernel(RopeArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int u = static_cast<int>(id % (a.D / 2));
+  const int64_t th = id / (a.D / 2);
+  const int64_t t = th / a.H, h = th % a.H;
+  if (t >= a.T) return;
+  const E* x = static_cast<const E*>(a.x) + t * a.x_row + h * a.x_head;
+  E* o = static_cast<E*>(a.out) + t * a.o_row + h * a.o_head;
+  if (2 * u >= a.rot) {
+    if (a.copy_tail) {
+      o[2 * u] = x[2 * u];
+      o[2 * u + 1] = x[2 * u + 1];
+    }
+    return;
+  }
+  const int first = a.interleaved ? 2 * u : u, second = a.interleaved ? 2 * u + 1 : u + a.rot / 2;
+  float c, s;
+  rope_sincos(a.pos[t], a.phase[u], c, s);
+  c *= a.mscale;
+  s *= a.backward ? -a.mscale : a.mscale;
+  const float fa = to_f(x[first]), fb = to_f(x[second]);
+  o[first] = from_f<E>(rope_first(fa, fb, c, s));
+  o[second] = from_f<E>(rope_second(fa, fb, c, s));
+}
+
+// Heads per thread: one while the call is small (latency), up to 8 that share their
+// angles once there are threads enough to fill the multiprocessors several times.
+int heads_per_thread(int64_t T, int64_t units, int64_t H) {
+  int per = 1;
+  while (per < 8 && T * units * H / (2 * per) >= 152 * 1024) per *= 2;
+  return per;
 }
 
 template <typename E, int V>
 cudaError_t launch_rope_v(RopeArgs a, cudaStream_t s) {
   a.units = a.D / (2 * V);
-  // few tokens: one head per thread (latency); many: up to 8 heads share their angles
-  int per = 1;
-  while (per < 8 && static_cast<int64_t>(a.T) * a.units * a.H / (2 * per) >= 152 * 1024) per *= 2;
+  const int per = heads_per_thread(a.T, a.units, a.H);
   a.head_blocks = (a.H + per - 1) / per;
-  const int64_t n = static_cast<int64_t>(a.T) * a.units * a.head_blocks;
-  const int64_t blocks = (n + kThreads - 1) / kThreads;
+  const int64_t blocks =
+      (static_cast<int64_t>(a.T) * a.units * a.head_blocks + kThreads - 1) / kThreads;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_pdl(rope_kernel<E, V>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, a);
 }
@@ -184,15 +225,15 @@ template <typename E>
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   const uint64_t all = static_cast<uint64_t>(a.x_row | a.x_head | a.o_row | a.o_head);
   const uint64_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out);
-  const int half = a.interleaved ? 0 : a.rot / 2;
-  const auto fits = [&](unsigned v) {
-    const unsigned bytes = std::min<unsigned>(16, v * sizeof(E));
-    return a.rot % (2 * v) == 0 && a.D % (2 * v) == 0 && half % v == 0 && all % v == 0 &&
-           p % bytes == 0;
+  const auto fits = [&](int v) {
+    return a.rot % (2 * v) == 0 && a.D % (2 * v) == 0 && all % v == 0 && p % (v * sizeof(E)) == 0;
   };
-  if (fits(8)) return launch_rope_v<E, 8>(a, s);
-  if (fits(4)) return launch_rope_v<E, 4>(a, s);
-  return launch_rope_v<E, 1>(a, s);
+  constexpr int kWide = 16 / sizeof(E);
+  if (fits(kWide)) return launch_rope_v<E, kWide>(a, s);
+  if (fits(kWide / 2)) return launch_rope_v<E, kWide / 2>(a, s);
+  const int64_t blocks = (static_cast<int64_t>(a.T) * a.H * (a.D / 2) + kThreads - 1) / kThreads;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl(rope_pair_kernel<E>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, a);
 }
 
 // ------------------------------------------------------------------- append
@@ -205,6 +246,7 @@ struct AppendArgs {
   const uint64_t* phase;     // nullptr: no rotation
   int T, Hq, rot, interleaved;
   float mscale;
+  int per, turn_blocks, head_blocks;   // heads per thread; blocks of query and key heads; all blocks
   KvCache c;
 };
 
@@ -222,83 +264,69 @@ __device__ __forceinline__ float ld_bf16(const uint16_t* p) {
   return __uint_as_float(static_cast<uint32_t>(*p) << 16);
 }
 
-// Elements e0 .. e0+7 of one head turned to their position, rounded to bf16.
-__device__ __forceinline__ void turned8(const AppendArgs& a, const uint16_t* head, int e0,
-                                        int32_t pos, float (&v)[8]) {
-  load8(head + e0, v);
-  if (!a.phase) return;
-  const int half = a.rot / 2;
-  if (a.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      if (e0 + i < a.rot) {
-        float c, s;
-        rope_sincos(pos, a.phase[(e0 + i) / 2], c, s);
-        c *= a.mscale;
-        s *= a.mscale;
-        const float x = v[i], y = v[i + 1];
-        v[i] = rope_first(x, y, c, s);
-        v[i + 1] = rope_second(x, y, c, s);
-      }
-    }
-  } else {
+// Turns the 8 elements from e0 on of one head after another to one position. Element e
+// becomes x cos -+ partner sin (- in the first of a pair), rounded to bf16.
+struct Turner {
+  float c[8], s[8];          // cos, and sin with its sign, of each element's pair
+  int n;                     // elements below rot
+  int mode;                  // 0: none of them; 1: partners are neighbours; 2: a run at `shift`;
+  int shift;                 // 3: one by one, element i's at shift or (upper half) -shift
+  int upper;
+
+  __device__ __forceinline__ void prepare(const AppendArgs& a, int e0, int32_t pos) {
+    n = a.phase ? min(max(a.rot - e0, 0), 8) : 0;
+    mode = 0;
+    shift = upper = 0;
+    if (n == 0) return;
+    const int half = a.rot / 2;
+    mode = a.interleaved ? 1 : half % 8 == 0 ? 2 : 3;
+    shift = mode == 2 && e0 >= half ? -half : half;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = e0 + i;
-      if (e < a.rot) {
-        const bool lower = e < half;
-        const int pair = lower ? e : e - half;
-        float c, s;
-        rope_sincos(pos, a.phase[pair], c, s);
-        c *= a.mscale;
-        s *= a.mscale;
-        const float other = ld_bf16(head + (lower ? e + half : pair));
-        v[i] = lower ? rope_first(v[i], other, c, s) : rope_second(other, v[i], c, s);
+      const bool first = a.interleaved ? (e & 1) == 0 : e < half;
+      const int pair = a.interleaved ? e >> 1 : first ? e : e - half;
+      if (!first) upper |= 1 << i;
+      c[i] = 1.f;
+      s[i] = 0.f;
+      if (i < n) {
+        rope_sincos(pos, a.phase[pair], c[i], s[i]);
+        c[i] *= a.mscale;
+        s[i] *= first ? -a.mscale : a.mscale;
       }
     }
   }
+  __device__ __forceinline__ void turn(const uint16_t* head, int e0, float (&v)[8]) const {
+    if (mode == 0) return;
+    float p[8];
+    if (mode == 1) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const uint32_t w = pack_bf16(v[i], v[i + 1]);
-    v[i] = bf16_lo(w);
-    v[i + 1] = bf16_hi(w);
+      for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
+    } else if (mode == 2) {
+      load8(head + e0 + shift, p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        p[i] = i < n ? ld_bf16(head + e0 + i + (upper >> i & 1 ? -shift : shift)) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      float y[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        y[k] = i + k < n ? __fadd_rn(__fmul_rn(v[i + k], c[i + k]), __fmul_rn(p[i + k], s[i + k]))
+                         : v[i + k];
+      const uint32_t w = pack_bf16(y[0], y[1]);
+      v[i] = bf16_lo(w);
+      v[i + 1] = bf16_hi(w);
+    }
   }
-}
+};
 
-// Thread = (token, head, run of 8 elements); heads are the query heads, the key
-// heads, then the value heads. The 8 lanes of a group find its range by shuffles.
-// (q_out may be q only if no thread reads what another wrote: a turned run reads
-// its partner run of the same head, so in place the whole head must be read
-// before any of it is written: the D/8 <= 32 threads of a head are lanes of one
-// warp, and __syncwarp separates the two.)
+// Quantises the 8 elements of each lane in groups of 8 lanes and writes codes and word.
 template <int BITS>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
-  const int runs = a.c.D / 8;
-  const int heads = a.Hq + 2 * a.c.Hkv;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int run = static_cast<int>(id % runs);
-  const int64_t th = id / runs;
-  const int h = static_cast<int>(th % heads);
-  const int64_t t = th / heads;
-  const bool live = t < a.T;               // whole groups of 8 lanes: D / 8 is a multiple of 8
-  const int e0 = run * 8;
-  float v[8] = {};
-  if (live) {
-    const int32_t pos = a.phase ? a.pos[t] : 0;
-    if (h < a.Hq)
-      turned8(a, a.q + t * a.q_row + h * a.q_head, e0, pos, v);
-    else if (h < a.Hq + a.c.Hkv)
-      turned8(a, a.k + t * a.k_row + (h - a.Hq) * a.k_head, e0, pos, v);
-    else
-      load8(a.v + t * a.v_row + (h - a.Hq - a.c.Hkv) * a.v_head + e0, v);
-  }
-  __syncwarp();
-  if (live && h < a.Hq)
-    *reinterpret_cast<uint4*>(a.q_out + t * a.qo_row + h * a.qo_head + e0) =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                   pack_bf16(v[6], v[7]));
+__device__ __forceinline__ void store_codes(const AppendArgs& a, const float (&v)[8], int slot,
+                                            int head, int run, bool write) {
   float lo = v[0], hi = v[0];
   bool finite = true;
 #pragma unroll
@@ -313,29 +341,23 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
   }
   finite = ((__ballot_sync(0xFFFFFFFFu, finite) >> (threadIdx.x & 24u)) & 0xFFu) == 0xFFu;
-  if (!live || h < a.Hq) return;
-  const int slot = a.slots[t];
-  if (slot < 0 || slot >= a.c.pages * a.c.page_size) {
-    if (slot != -1 && run == 0 && h == a.Hq) atomicOr(a.c.err, MOE_DEVERR_BAD_SLOT);
-    return;
-  }
+  if (!write) return;
   constexpr float kLevels = (1 << BITS) - 1;
   uint32_t words = 0x7FC00000u;            // scale 0, bias NaN
   uint32_t code[8] = {};
   if (finite) {
     // halves: max - min may pass the largest float; the constant is one rounding of 2 / levels
     const float range = __fsub_rn(0.5f * hi, 0.5f * lo);
-    const uint32_t sw = pack_bf16(__fmul_rn(range, 1.0f / (0.5f * kLevels)), lo);
-    const float scale = bf16_lo(sw);
+    words = pack_bf16(__fmul_rn(range, 1.0f / (0.5f * kLevels)), lo);
+    const float scale = bf16_lo(words);
     const float per = scale > 0.f ? __fdiv_rn(1.0f, scale) : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       code[i] = static_cast<uint32_t>(
           fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(v[i], lo), per)), 0.f), kLevels));
-    words = sw;
   }
   const int page = slot / a.c.page_size, row = slot % a.c.page_size;
-  uint8_t* blk = kv_block(a.c, page, h - a.Hq);
+  uint8_t* blk = kv_block(a.c, page, head);
   uint8_t* dst = blk + row * a.c.row_bytes + run * BITS;
   if (BITS == 8)
     *reinterpret_cast<uint2*>(dst) =
@@ -348,6 +370,60 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   if ((run & 7) == 0)
     *reinterpret_cast<uint32_t*>(blk + a.c.code_bytes +
                                  (row * (a.c.D / kKvGroup) + run / 8) * 4) = words;
+}
+
+// Thread = (token, block of heads, run of 8 elements). The blocks cover the query and key
+// heads, whose angles a thread computes once for all of its heads, then the value heads.
+// (q_out may be q only if no thread reads what another wrote: a turned run reads its
+// partner run of the same head, whose D / 8 <= 32 threads are lanes of one warp;
+// __syncwarp separates a head's reads from its writes. Lanes of one warp may be at
+// different blocks of heads, so all go through `per` rounds.)
+template <int BITS>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int runs = a.c.D / 8;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int run = static_cast<int>(id % runs);
+  const int64_t th = id / runs;
+  const int hb = static_cast<int>(th % a.head_blocks);
+  const int64_t t = th / a.head_blocks;
+  const bool live = t < a.T;               // whole groups of 8 lanes: D / 8 is a multiple of 8
+  const int turned = a.Hq + a.c.Hkv;       // heads that turn
+  const bool values = hb >= a.turn_blocks;
+  const int h0 = (values ? hb - a.turn_blocks : hb) * a.per;
+  const int h1 = min(values ? a.c.Hkv : turned, h0 + a.per);
+  const int e0 = run * 8;
+  int slot = -1;
+  Turner turner;
+  turner.mode = 0;
+  if (live) {
+    if (values || h1 > a.Hq) slot = a.slots[t];
+    if (!values) turner.prepare(a, e0, a.phase ? a.pos[t] : 0);
+  }
+  const bool inside = slot >= 0 && slot < a.c.pages * a.c.page_size;
+  if (slot != -1 && !inside && run == 0 && values && h0 == 0) atomicOr(a.c.err, MOE_DEVERR_BAD_SLOT);
+  for (int k = 0; k < a.per; ++k) {
+    const int h = h0 + k;
+    const bool here = live && h < h1;
+    const bool query = here && !values && h < a.Hq;
+    float v[8] = {};
+    if (here) {
+      const uint16_t* head = values  ? a.v + t * a.v_row + h * a.v_head
+                             : query ? a.q + t * a.q_row + h * a.q_head
+                                     : a.k + t * a.k_row + (h - a.Hq) * a.k_head;
+      load8(head + e0, v);
+      turner.turn(head, e0, v);
+    }
+    __syncwarp();
+    if (query)
+      *reinterpret_cast<uint4*>(a.q_out + t * a.qo_row + h * a.qo_head + e0) =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                     pack_bf16(v[6], v[7]));
+    const bool code = here && !query;
+    if (__any_sync(0xFFFFFFFFu, code))
+      store_codes<BITS>(a, v, slot, values ? a.c.Hkv + h : h - a.Hq, run, code && inside);
+  }
 }
 
 // --------------------------------------------------------------------- read
@@ -552,7 +628,10 @@ extern "C" moe_status moe_kv_append(const moe_kv_new* n, const moe_kv_cache* c, 
     a.mscale = n->rope->mscale;
   }
   a.c = kv_cache_args(*c);
-  const int64_t threads = static_cast<int64_t>(n->T) * (Hq + 2 * c->Hkv) * (c->D / 8);
+  a.per = heads_per_thread(n->T, c->D / 8, Hq + 2 * c->Hkv);
+  a.turn_blocks = (Hq + c->Hkv + a.per - 1) / a.per;
+  a.head_blocks = a.turn_blocks + (c->Hkv + a.per - 1) / a.per;
+  const int64_t threads = static_cast<int64_t>(n->T) * a.head_blocks * (c->D / 8);
   const int64_t blocks = (threads + kThreads - 1) / kThreads;
   if (blocks > 0x7FFFFFFF) return MOE_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
