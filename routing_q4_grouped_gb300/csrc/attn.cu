@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
 #pragma unroll
   for (int i = 0; i < G::TB; ++i) {
     const uint32_t blk = static_cast<uint32_t>(tok_next >> 4) + i;
-    at_page[i] = static_cast<int>((blk * a.page_magic) >> 40);
-    in_page[i] = static_cast<int>(blk - at_page[i] * a.page_blocks);
+    at_page[i] = page_of_block(a.c, blk);
+    in_page[i] = static_cast<int>(blk - at_page[i] * a.c.page_blocks);
     page[i] = tok_next + 16 * i < t1 ? __ldg(pages + at_page[i]) : -1;
   }
   const auto look = [&]() {
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
     for (int i = 0; i < G::TB; ++i) {
       at_page[i] += a.skip_pages[G::TB - 1];
       in_page[i] += a.skip_blocks[G::TB - 1];
-      if (in_page[i] >= static_cast<int>(a.page_blocks)) in_page[i] -= a.page_blocks, ++at_page[i];
+      if (in_page[i] >= static_cast<int>(a.c.page_blocks)) in_page[i] -= a.c.page_blocks, ++at_page[i];
       page[i] = tok_next + 16 * i < t1 ? __ldg(pages + at_page[i]) : -1;
     }
   };
@@ -1069,11 +1069,9 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
   k.G = a->Hq / c->Hkv;
   k.scale2 = a->scale * 1.44269504088896340736f;
   k.c = kv_cache_args(*c);
-  k.page_blocks = static_cast<uint32_t>(c->page_size / 16);
-  k.page_magic = (1ull << 40) / k.page_blocks + 1;
   for (int tb = 1; tb <= 2; ++tb) {
-    k.skip_pages[tb - 1] = kWarps * tb / static_cast<int>(k.page_blocks);
-    k.skip_blocks[tb - 1] = kWarps * tb % static_cast<int>(k.page_blocks);
+    k.skip_pages[tb - 1] = kWarps * tb / static_cast<int>(k.c.page_blocks);
+    k.skip_blocks[tb - 1] = kWarps * tb % static_cast<int>(k.c.page_blocks);
   }
   k.part = static_cast<float*>(ws);
   k.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml);

@@ -22,8 +22,6 @@ struct AttnArgs {
   int B, nq, Hq, table_stride, max_len, prefix_len, G;
   float scale2;              // scale * log2(e)
   KvCache c;
-  uint32_t page_blocks;      // 16-token blocks per page
-  uint64_t page_magic;       // floor(2^40 / page_blocks) + 1
   int skip_pages[2], skip_blocks[2];     // four blocks further, and eight
   // split kernel: units of 8 nt query rows
   int nt;

@@ -295,8 +295,8 @@ struct Pages {
     int tok = sg.kt0 * TT + 16 * lane;               // lane i has block i of a tile
     const auto look = [&](int t, int& page, uint32_t& in_page) {
       const uint32_t blk = static_cast<uint32_t>(t) >> 4;
-      const uint32_t at = static_cast<uint32_t>((blk * a.page_magic) >> 40);
-      in_page = blk - at * a.page_blocks;
+      const uint32_t at = page_of_block(a.c, blk);
+      in_page = blk - at * a.c.page_blocks;
       page = lane < TT / 16 && t < seen ? __ldg(sg.pages + at) : -1;
     };
     int page, next;

@@ -39,6 +39,8 @@ KvCache kv_cache_args(const moe_kv_cache& c) {
   k.code_bytes = c.page_size * k.row_bytes;
   k.head_bytes = k.code_bytes + c.page_size * (c.D / kKvGroup) * 4;
   k.page_bytes = 2ll * c.Hkv * k.head_bytes;
+  k.page_blocks = static_cast<uint32_t>(c.page_size / 16);
+  k.page_magic = (1ull << 40) / k.page_blocks + 1;
   return k;
 }
 
@@ -66,7 +68,7 @@ struct RopeArgs {
   int64_t x_row, x_head, o_row, o_head;
   int T, H, D, rot;
   int units;                 // units of 2V elements per head, D / 2V
-  int head_blocks;           // heads per thread: ceil(H / head_blocks)
+  int per;                   // heads per thread
   float mscale;
   int interleaved, backward, copy_tail;
 };
@@ -102,14 +104,11 @@ template <typename E, int V>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int u = static_cast<int>(id % a.units);
-  const int64_t th = id / a.units;
-  const int hb = static_cast<int>(th % a.head_blocks);
-  const int64_t t = th / a.head_blocks;
-  if (t >= a.T) return;
-  const int per = (a.H + a.head_blocks - 1) / a.head_blocks;
-  const int h0 = hb * per, h1 = min(a.H, h0 + per);
+  const int tokens = max(1, kThreads / a.units);       // per block; (units above the block: several)
+  const int u = threadIdx.x % a.units + blockIdx.z * kThreads;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * tokens + threadIdx.x / a.units;
+  if (t >= a.T || u >= a.units || threadIdx.x >= tokens * a.units) return;
+  const int h0 = blockIdx.y * a.per, h1 = min(a.H, h0 + a.per);
   const int turned = a.rot / (2 * V);
   const bool tail = u >= turned;
   if (tail && !a.copy_tail) return;
@@ -202,23 +201,22 @@ __global__ void __launch_bounds__(kThreads) rope_pair_kernel(RopeArgs a) {
   o[second] = from_f<E>(rope_second(fa, fb, c, s));
 }
 
-// Heads per thread: one while the call is small (latency), up to 8 that share their
+// Heads per thread: one while the call is small (latency), up to 16 that share their
 // angles once there are threads enough to fill the multiprocessors several times.
 int heads_per_thread(int64_t T, int64_t units, int64_t H) {
   int per = 1;
-  while (per < 8 && T * units * H / (2 * per) >= 152 * 1024) per *= 2;
+  while (per < 16 && T * units * H / (2 * per) >= 152 * 1024) per *= 2;
   return per;
 }
 
 template <typename E, int V>
 cudaError_t launch_rope_v(RopeArgs a, cudaStream_t s) {
   a.units = a.D / (2 * V);
-  const int per = heads_per_thread(a.T, a.units, a.H);
-  a.head_blocks = (a.H + per - 1) / per;
-  const int64_t blocks =
-      (static_cast<int64_t>(a.T) * a.units * a.head_blocks + kThreads - 1) / kThreads;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return launch_pdl(rope_kernel<E, V>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, a);
+  a.per = heads_per_thread(a.T, a.units, a.H);
+  const int tokens = std::max(1, kThreads / a.units);
+  const dim3 grid((a.T - 1) / tokens + 1, (a.H + a.per - 1) / a.per,
+                  (a.units + kThreads - 1) / kThreads);
+  return launch_pdl(rope_kernel<E, V>, grid, dim3(kThreads), 0, s, a);
 }
 
 template <typename E>
@@ -246,12 +244,11 @@ struct AppendArgs {
   const uint64_t* phase;     // nullptr: no rotation
   int T, Hq, rot, interleaved;
   float mscale;
-  int per, turn_blocks, head_blocks;   // heads per thread; blocks of query and key heads; all blocks
+  int per, turn_blocks;      // heads per thread; blocks of query and key heads
   KvCache c;
 };
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
   const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -296,19 +293,25 @@ struct Turner {
       }
     }
   }
-  __device__ __forceinline__ void turn(const uint16_t* head, int e0, float (&v)[8]) const {
-    if (mode == 0) return;
-    float p[8];
+  // The partner run, where it is one (mode 2).
+  __device__ __forceinline__ uint4 partner(const uint16_t* head, int e0) const {
+    return mode == 2 ? *reinterpret_cast<const uint4*>(head + e0 + shift) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ uint4 turn(const uint16_t* head, int e0, uint4 own, uint4 other) const {
+    if (mode == 0) return own;
+    float v[8], p[8];
+    unpack8(own, v);
     if (mode == 1) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
     } else if (mode == 2) {
-      load8(head + e0 + shift, p);
+      unpack8(other, p);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         p[i] = i < n ? ld_bf16(head + e0 + i + (upper >> i & 1 ? -shift : shift)) : 0.f;
     }
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       float y[2];
@@ -316,17 +319,18 @@ struct Turner {
       for (int k = 0; k < 2; ++k)
         y[k] = i + k < n ? __fadd_rn(__fmul_rn(v[i + k], c[i + k]), __fmul_rn(p[i + k], s[i + k]))
                          : v[i + k];
-      const uint32_t w = pack_bf16(y[0], y[1]);
-      v[i] = bf16_lo(w);
-      v[i + 1] = bf16_hi(w);
+      w[i / 2] = pack_bf16(y[0], y[1]);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
 // Quantises the 8 elements of each lane in groups of 8 lanes and writes codes and word.
 template <int BITS>
-__device__ __forceinline__ void store_codes(const AppendArgs& a, const float (&v)[8], int slot,
-                                            int head, int run, bool write) {
+__device__ __forceinline__ void store_codes(const AppendArgs& a, uint4 raw, int slot, int head,
+                                            int run, bool write) {
+  float v[8];
+  unpack8(raw, v);
   float lo = v[0], hi = v[0];
   bool finite = true;
 #pragma unroll
@@ -356,7 +360,8 @@ __device__ __forceinline__ void store_codes(const AppendArgs& a, const float (&v
       code[i] = static_cast<uint32_t>(
           fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(v[i], lo), per)), 0.f), kLevels));
   }
-  const int page = slot / a.c.page_size, row = slot % a.c.page_size;
+  const int page = page_of_block(a.c, static_cast<uint32_t>(slot) >> 4);
+  const int row = slot - page * a.c.page_size;
   uint8_t* blk = kv_block(a.c, page, head);
   uint8_t* dst = blk + row * a.c.row_bytes + run * BITS;
   if (BITS == 8)
@@ -376,18 +381,15 @@ __device__ __forceinline__ void store_codes(const AppendArgs& a, const float (&v
 // heads, whose angles a thread computes once for all of its heads, then the value heads.
 // (q_out may be q only if no thread reads what another wrote: a turned run reads its
 // partner run of the same head, whose D / 8 <= 32 threads are lanes of one warp;
-// __syncwarp separates a head's reads from its writes. Lanes of one warp may be at
-// different blocks of heads, so all go through `per` rounds.)
+// __syncwarp separates a head's reads from its writes.)
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int runs = a.c.D / 8;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int run = static_cast<int>(id % runs);
-  const int64_t th = id / runs;
-  const int hb = static_cast<int>(th % a.head_blocks);
-  const int64_t t = th / a.head_blocks;
+  const int runs = a.c.D / 8;              // 8, 16 or 32
+  const int run = threadIdx.x & (runs - 1);
+  const int hb = blockIdx.y;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / runs) + threadIdx.x / runs;
   const bool live = t < a.T;               // whole groups of 8 lanes: D / 8 is a multiple of 8
   const int turned = a.Hq + a.c.Hkv;       // heads that turn
   const bool values = hb >= a.turn_blocks;
@@ -403,77 +405,94 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   }
   const bool inside = slot >= 0 && slot < a.c.pages * a.c.page_size;
   if (slot != -1 && !inside && run == 0 && values && h0 == 0) atomicOr(a.c.err, MOE_DEVERR_BAD_SLOT);
-  for (int k = 0; k < a.per; ++k) {
-    const int h = h0 + k;
+  const auto head_at = [&](int h) {
+    return values     ? a.v + t * a.v_row + h * a.v_head
+           : h < a.Hq ? a.q + t * a.q_row + h * a.q_head
+                      : a.k + t * a.k_row + (h - a.Hq) * a.k_head;
+  };
+  // the next head's loads are on their way while this one is worked on
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  uint4 own = none, other = none;
+  if (live && h0 < h1) {
+    const uint16_t* head = head_at(h0);
+    own = *reinterpret_cast<const uint4*>(head + e0);
+    other = turner.partner(head, e0);
+  }
+  for (int h = h0; h < h0 + a.per; ++h) {
     const bool here = live && h < h1;
     const bool query = here && !values && h < a.Hq;
-    float v[8] = {};
-    if (here) {
-      const uint16_t* head = values  ? a.v + t * a.v_row + h * a.v_head
-                             : query ? a.q + t * a.q_row + h * a.q_head
-                                     : a.k + t * a.k_row + (h - a.Hq) * a.k_head;
-      load8(head + e0, v);
-      turner.turn(head, e0, v);
+    const uint4 now = here ? turner.turn(head_at(h), e0, own, other) : none;
+    if (live && h + 1 < h1) {
+      const uint16_t* head = head_at(h + 1);
+      own = *reinterpret_cast<const uint4*>(head + e0);
+      other = turner.partner(head, e0);
     }
     __syncwarp();
-    if (query)
-      *reinterpret_cast<uint4*>(a.q_out + t * a.qo_row + h * a.qo_head + e0) =
-          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                     pack_bf16(v[6], v[7]));
+    if (query) *reinterpret_cast<uint4*>(a.q_out + t * a.qo_row + h * a.qo_head + e0) = now;
     const bool code = here && !query;
     if (__any_sync(0xFFFFFFFFu, code))
-      store_codes<BITS>(a, v, slot, values ? a.c.Hkv + h : h - a.Hq, run, code && inside);
+      store_codes<BITS>(a, now, slot, values ? a.c.Hkv + h : h - a.Hq, run, code && inside);
   }
 }
 
 // --------------------------------------------------------------------- read
 
-// Thread = (row, key or value head, run of 16 codes) -> 32 bytes of bf16.
+// Thread = (run of 8 codes of a key or value head, four rows): lanes read neighbouring
+// codes and write neighbouring 16 bytes of bf16, and a thread's four rows keep their
+// loads in flight together. (Block = rows x one head; no division but by page.)
+constexpr int kReadRows = 4;
+
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) read_kernel(KvCache c, const int32_t* slots, int n,
                                                         uint16_t* k_out, uint16_t* v_out) {
-  const int runs = c.D / 16;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int run = static_cast<int>(id % runs);
-  const int64_t th = id / runs;
-  const int h = static_cast<int>(th % (2 * c.Hkv));
-  const int64_t t = th / (2 * c.Hkv);
-  if (t >= n) return;
+  const int runs = c.D / 8, step = kThreads / runs;     // rows apart
+  const int run = threadIdx.x & (runs - 1), h = blockIdx.y;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * step * kReadRows + threadIdx.x / runs;
   uint16_t* out = h < c.Hkv ? k_out : v_out;
-  if (!out) return;
-  out += (t * c.Hkv + h % c.Hkv) * c.D + run * 16;
-  const int slot = slots[t];
-  uint32_t r[8] = {};
-  if (slot >= 0 && slot < c.pages * c.page_size) {
-    const int page = slot / c.page_size, row = slot % c.page_size;
-    const uint8_t* blk = kv_block(c, page, h);
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(
-        blk + c.code_bytes + (row * (c.D / kKvGroup) + run / 4) * 4);
-    const float scale = bf16_lo(w), bias = bf16_hi(w);
-    const uint8_t* src = blk + row * c.row_bytes + run * 2 * BITS;
-    uint32_t q[4];
-    if (BITS == 8) {
-      const uint4 x = *reinterpret_cast<const uint4*>(src);
-      q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w;
-    } else {
-      const uint2 x = *reinterpret_cast<const uint2*>(src);
-      q[0] = x.x, q[1] = x.y;
-    }
-    constexpr int kPer = 32 / BITS;
+  if (t0 >= n || !out) return;
+  uint32_t q[kReadRows][2], w[kReadRows];
+  bool in[kReadRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t two = q[2 * i / kPer] >> (2 * i % kPer * BITS);
-      constexpr uint32_t kMask = (1u << BITS) - 1;
-      r[i] = pack_bf16(fmaf(scale, static_cast<float>(two & kMask), bias),
-                       fmaf(scale, static_cast<float>((two >> BITS) & kMask), bias));
+  for (int i = 0; i < kReadRows; ++i) {
+    const int slot = t0 + i * step < n ? slots[t0 + i * step] : -1;
+    in[i] = slot >= 0 && slot < c.pages * c.page_size;
+    if (!in[i]) {
+      if (slot != -1 && run == 0 && h % c.Hkv == 0) atomicOr(c.err, MOE_DEVERR_BAD_SLOT);
+      continue;
     }
-  } else if (slot != -1 && run == 0 && h % c.Hkv == 0) {
-    atomicOr(c.err, MOE_DEVERR_BAD_SLOT);
+    const int page = page_of_block(c, static_cast<uint32_t>(slot) >> 4);
+    const int row = slot - page * c.page_size;
+    const uint8_t* blk = kv_block(c, page, h);
+    w[i] = *reinterpret_cast<const uint32_t*>(blk + c.code_bytes +
+                                              (row * (c.D / kKvGroup) + run / 8) * 4);
+    const uint8_t* src = blk + row * c.row_bytes + run * BITS;
+    if (BITS == 8) {
+      const uint2 x = *reinterpret_cast<const uint2*>(src);
+      q[i][0] = x.x, q[i][1] = x.y;
+    } else {
+      q[i][0] = *reinterpret_cast<const uint32_t*>(src);
+    }
   }
-  reinterpret_cast<uint4*>(out)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-  reinterpret_cast<uint4*>(out)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+#pragma unroll
+  for (int i = 0; i < kReadRows; ++i) {
+    if (t0 + i * step >= n) break;
+    uint32_t r[4] = {};
+    if (in[i]) {
+      const float scale = bf16_lo(w[i]), bias = bf16_hi(w[i]);
+      constexpr int kPer = 32 / BITS;
+      constexpr uint32_t kMask = (1u << BITS) - 1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t two = q[i][2 * k / kPer] >> (2 * k % kPer * BITS);
+        r[k] = pack_bf16(fmaf(scale, static_cast<float>(two & kMask), bias),
+                         fmaf(scale, static_cast<float>((two >> BITS) & kMask), bias));
+      }
+    }
+    reinterpret_cast<uint4*>(out + ((t0 + i * step) * c.Hkv + h % c.Hkv) * c.D)[run] =
+        make_uint4(r[0], r[1], r[2], r[3]);
+  }
 }
 
 moe_status check_rope(const moe_rope_spec* r, int D) {
@@ -547,7 +566,7 @@ extern "C" moe_status moe_rope(const void* x, int64_t x_row, int64_t x_head, voi
   if (T < 0 || H < 1 || D < 2 || backward < 0 || backward > 1 || dtype < MOE_BF16 ||
       dtype > MOE_F32)
     return MOE_ERR_ARG;
-  if (D % 2 || D > 65536 || H > 65536) return MOE_ERR_SHAPE;
+  if (D % 2 || D > 65536 || H > 65535) return MOE_ERR_SHAPE;
   moe_status st = check_rope(rope, D);
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
@@ -597,7 +616,7 @@ extern "C" moe_status moe_kv_append(const moe_kv_new* n, const moe_kv_cache* c, 
   const int Hq = n->q ? n->Hq : 0;
   if (n->q) {
     if (n->Hq < 1) return MOE_ERR_ARG;
-    if (n->Hq > 65536) return MOE_ERR_SHAPE;
+    if (n->Hq > 32768) return MOE_ERR_SHAPE;
     if ((st = check_rows(n->q, n->q_row, n->q_head)) != MOE_OK ||
         (st = check_rows(n->q_out, n->qo_row, n->qo_head)) != MOE_OK)
       return st;
@@ -630,14 +649,12 @@ extern "C" moe_status moe_kv_append(const moe_kv_new* n, const moe_kv_cache* c, 
   a.c = kv_cache_args(*c);
   a.per = heads_per_thread(n->T, c->D / 8, Hq + 2 * c->Hkv);
   a.turn_blocks = (Hq + c->Hkv + a.per - 1) / a.per;
-  a.head_blocks = a.turn_blocks + (c->Hkv + a.per - 1) / a.per;
-  const int64_t threads = static_cast<int64_t>(n->T) * a.head_blocks * (c->D / 8);
-  const int64_t blocks = (threads + kThreads - 1) / kThreads;
-  if (blocks > 0x7FFFFFFF) return MOE_ERR_SHAPE;
+  const int tokens = kThreads / (c->D / 8);      // per block
+  const dim3 grid((n->T - 1) / tokens + 1, a.turn_blocks + (c->Hkv + a.per - 1) / a.per);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = check_device()) != MOE_OK) return st;
-  const cudaError_t e = launch_pdl(c->bits == 8 ? append_kernel<8> : append_kernel<4>,
-                                   dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, a);
+  const cudaError_t e = launch_pdl(c->bits == 8 ? append_kernel<8> : append_kernel<4>, grid,
+                                   dim3(kThreads), 0, s, a);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -650,14 +667,13 @@ extern "C" moe_status moe_kv_read(const moe_kv_cache* c, const int32_t* slots, i
   if (n == 0) return MOE_OK;
   if (!slots || (!k_out && !v_out)) return MOE_ERR_ARG;
   if (bad_align(slots, 4) || bad_align(k_out, 16) || bad_align(v_out, 16)) return MOE_ERR_ALIGN;
-  const int64_t threads = static_cast<int64_t>(n) * 2 * c->Hkv * (c->D / 16);
-  const int64_t blocks = (threads + kThreads - 1) / kThreads;
-  if (blocks > 0x7FFFFFFF) return MOE_ERR_SHAPE;
+  const int rows = kThreads / (c->D / 8) * kReadRows;   // per block
+  const dim3 grid((n - 1) / rows + 1, 2 * c->Hkv);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const KvCache k = kv_cache_args(*c);
   if ((st = check_device()) != MOE_OK) return st;
   const cudaError_t e =
       launch_pdl(c->bits == 8 ? read_kernel<8> : read_kernel<4>,
-                 dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, k, slots, n, k_out, v_out);
+                 grid, dim3(kThreads), 0, s, k, slots, n, k_out, v_out);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -21,10 +21,18 @@ struct KvCache {
   int code_bytes;                    // codes of one head of a page (words follow)
   int head_bytes;                    // one head of a page
   int64_t page_bytes;
+  uint32_t page_blocks;              // 16-token blocks per page
+  uint64_t page_magic;               // floor(2^40 / page_blocks) + 1
 };
 
 moe_status check_kv_cache(const moe_kv_cache* c);
 KvCache kv_cache_args(const moe_kv_cache& c);
+
+// Page of 16-token block blk < 2^27: blk / page_blocks, exact because the magic number's
+// excess, below 2^-40 * page_blocks * blk < 2^-5, stays below 1 / page_blocks.
+__device__ __forceinline__ int page_of_block(const KvCache& c, uint32_t blk) {
+  return static_cast<int>((blk * c.page_magic) >> 40);
+}
 
 // The block of head h (key heads 0 .. Hkv-1, then value heads) of a page.
 __device__ __forceinline__ uint8_t* kv_block(const KvCache& c, int page, int h) {
@@ -47,8 +55,7 @@ __device__ __forceinline__ void rope_sincos(int32_t pos, uint64_t phase, float& 
   const uint64_t w = static_cast<uint64_t>(static_cast<int64_t>(pos)) * phase;
   const float a = __fmul_rn(static_cast<float>(static_cast<int32_t>(w >> 32)),
                             3.14159265358979323846f / 2147483648.0f);
-  c = cosf(a);
-  s = sinf(a);
+  sincosf(a, &s, &c);
 }
 
 // (a, b) turned; products and sums rounded one by one so that every path that
