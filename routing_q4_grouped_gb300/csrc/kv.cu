@@ -46,7 +46,7 @@ KvCache kv_cache_args(const moe_kv_cache& c) {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 bool bad_align(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
@@ -201,18 +201,18 @@ __global__ void __launch_bounds__(kThreads) rope_pair_kernel(RopeArgs a) {
   o[second] = from_f<E>(rope_second(fa, fb, c, s));
 }
 
-// Heads per thread: one while the call is small (latency), up to 16 that share their
+// Heads per thread: one while the call is small (latency), up to `most` that share their
 // angles once there are threads enough to fill the multiprocessors several times.
-int heads_per_thread(int64_t T, int64_t units, int64_t H) {
+int heads_per_thread(int64_t T, int64_t units, int64_t H, int most) {
   int per = 1;
-  while (per < 16 && T * units * H / (2 * per) >= 152 * 1024) per *= 2;
+  while (per < most && T * units * H / (2 * per) >= 152 * 1024) per *= 2;
   return per;
 }
 
 template <typename E, int V>
 cudaError_t launch_rope_v(RopeArgs a, cudaStream_t s) {
   a.units = a.D / (2 * V);
-  a.per = heads_per_thread(a.T, a.units, a.H);
+  a.per = heads_per_thread(a.T, a.units, a.H, 4);
   const int tokens = std::max(1, kThreads / a.units);
   const dim3 grid((a.T - 1) / tokens + 1, (a.H + a.per - 1) / a.per,
                   (a.units + kThreads - 1) / kThreads);
@@ -410,28 +410,34 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
            : h < a.Hq ? a.q + t * a.q_row + h * a.q_head
                       : a.k + t * a.k_row + (h - a.Hq) * a.k_head;
   };
-  // the next head's loads are on their way while this one is worked on
+  // Four heads' loads are in flight at a time: with one, the loop waits for memory.
   const uint4 none = make_uint4(0, 0, 0, 0);
-  uint4 own = none, other = none;
-  if (live && h0 < h1) {
-    const uint16_t* head = head_at(h0);
-    own = *reinterpret_cast<const uint4*>(head + e0);
-    other = turner.partner(head, e0);
-  }
-  for (int h = h0; h < h0 + a.per; ++h) {
-    const bool here = live && h < h1;
-    const bool query = here && !values && h < a.Hq;
-    const uint4 now = here ? turner.turn(head_at(h), e0, own, other) : none;
-    if (live && h + 1 < h1) {
-      const uint16_t* head = head_at(h + 1);
-      own = *reinterpret_cast<const uint4*>(head + e0);
-      other = turner.partner(head, e0);
+  constexpr int kBatch = 4;
+  for (int hh = h0; hh < h0 + a.per; hh += kBatch) {
+    uint4 own[kBatch], other[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      own[k] = other[k] = none;
+      if (live && hh + k < h1) {
+        const uint16_t* head = head_at(hh + k);
+        own[k] = *reinterpret_cast<const uint4*>(head + e0);
+        other[k] = turner.partner(head, e0);
+      }
     }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (live && hh + k < h1) own[k] = turner.turn(head_at(hh + k), e0, own[k], other[k]);
     __syncwarp();
-    if (query) *reinterpret_cast<uint4*>(a.q_out + t * a.qo_row + h * a.qo_head + e0) = now;
-    const bool code = here && !query;
-    if (__any_sync(0xFFFFFFFFu, code))
-      store_codes<BITS>(a, now, slot, values ? a.c.Hkv + h : h - a.Hq, run, code && inside);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = hh + k;
+      const bool here = live && h < h1;
+      const bool query = here && !values && h < a.Hq;
+      if (query) *reinterpret_cast<uint4*>(a.q_out + t * a.qo_row + h * a.qo_head + e0) = own[k];
+      const bool code = here && !query;
+      if (__any_sync(0xFFFFFFFFu, code))
+        store_codes<BITS>(a, own[k], slot, values ? a.c.Hkv + h : h - a.Hq, run, code && inside);
+    }
   }
 }
 
@@ -647,7 +653,7 @@ extern "C" moe_status moe_kv_append(const moe_kv_new* n, const moe_kv_cache* c, 
     a.mscale = n->rope->mscale;
   }
   a.c = kv_cache_args(*c);
-  a.per = heads_per_thread(n->T, c->D / 8, Hq + 2 * c->Hkv);
+  a.per = heads_per_thread(n->T, c->D / 8, Hq + 2 * c->Hkv, 16);
   a.turn_blocks = (Hq + c->Hkv + a.per - 1) / a.per;
   const int tokens = kThreads / (c->D / 8);      // per block
   const dim3 grid((n->T - 1) / tokens + 1, a.turn_blocks + (c->Hkv + a.per - 1) / a.per);
