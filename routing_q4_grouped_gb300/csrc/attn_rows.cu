@@ -595,6 +595,10 @@ struct Converter {
       if (it + 1 < sg.kt1) {
         load_keys((tc + 1) % kMetaRing);
         scales_for(tc + 1, it + 1);
+        if (it + 2 < sg.kt1) {
+          pages_of(tc + 2);
+          load_words((tc + 2) % kMetaRing);
+        }
       }
       if (tc >= G::KS) w.wait(&ctl.done[(tc - G::KS) % kMetaRing], ((tc - G::KS) / kMetaRing) & 1);
       put_values(m, G::kOffV + st * G::kTileBytes);
@@ -602,10 +606,6 @@ struct Converter {
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.v_full[st]);
       if (it + 1 < sg.kt1) load_values((tc + 1) % kMetaRing);
-      if (it + 2 < sg.kt1) {
-        pages_of(tc + 2);
-        load_words((tc + 2) % kMetaRing);
-      }
     }
   }
 };
