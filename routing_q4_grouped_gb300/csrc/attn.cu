@@ -14,8 +14,10 @@
 //    is the subnormal number c 2^-24, which the tensor cores take at full rate, so
 //    one byte permutation or mask makes an operand pair. With value = s c + b,
 //      q . k = sum over groups of  s sum c q + b sum q,
-//    and the values' scale is taken into the weights:
-//      sum_t p_t v_t = sum_t (p_t s_t) c_t + sum_t p_t b_t.
+//    and the values' scale is taken into the weights, which are rounded to fp16 once,
+//    w = fp16(p s), and used for codes and biases alike, so that the rounding stays
+//    relative to the value:
+//      sum_t p_t v_t = sum_t w_t c_t + sum_t w_t (b_t / s_t).
 //  * Tokens are the rows (M) of the products and queries the columns (N = 8), so
 //    that 8 rows fill the tensor core: X^T = K Q^T, then O^T = V^T P^T. The
 //    products' own register layouts let a thread read 16 (keys) or 8 (values)
@@ -152,9 +154,16 @@ struct Warp {
   int lim[NT][2];                 // tokens seen by the row
   float m[NT][2], l[NT][2];
   float o[NT][G::J][4][4];        // O^T: group, tile of 16 elements
-  float ob[NT][G::J][2];          // sum of p * bias
+  float ob[NT][G::J][2];          // sum of w * bias / scale
   float e[NT][2], f[NT][2];       // f = 2^-e: p s f stays below 2^15
   float top_x[NT][2], top_ps[NT][2];   // m + 8, m + e + 14: the bounds of a logit and of log2(p s) + m
+
+  // The scale that a group's weights take: a constant group (scale 0, codes 0) may have
+  // any, and takes one near its bias.
+  __device__ __forceinline__ static float value_scale(uint32_t word) {
+    const float s = bf16_lo(word);
+    return s != 0.f ? s : fmaxf(fabsf(bf16_hi(word)), 0x1p-60f);
+  }
 
   __device__ __forceinline__ static void load_words(const uint8_t* p, uint32_t (&w)[G::J]) {
     if constexpr (G::J == 1) {
@@ -245,13 +254,13 @@ struct Warp {
       for (int r = 0; r < 2; ++r) {
         const int tok = tok0 + 16 * b + 8 * r + g;
         const bool any = !MASK || tok < top[b];
-        uint32_t big = 0;
+        float big = 0.f;
 #pragma unroll
         for (int j = 0; j < G::J; ++j) {
           if (MASK && !any) vw[b][r][j] = 0;
-          big = max(big, vw[b][r][j] & 0x7FFFu);
+          big = fmaxf(big, fabsf(value_scale(vw[b][r][j])));
         }
-        es[b][r] = static_cast<float>(static_cast<int>(big >> 7) - 127);
+        es[b][r] = static_cast<float>(static_cast<int>(__float_as_uint(big) >> 23) - 127);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -290,19 +299,20 @@ struct Warp {
         uint32_t pb[NT][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float s = bf16_lo(vw[b][r][j]);
-          const float bias = bf16_hi(vw[b][r][j]);
+          const float s = value_scale(vw[b][r][j]), bias = bf16_hi(vw[b][r][j]);
+          // bias / s with one correction step: exact where the quotient is a float
+          float inv;
+          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+          float ratio = bias * inv;
+          ratio = fmaf(fmaf(-ratio, s, bias), inv, ratio);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const float p0 = x[b][n][2 * r], p1 = x[b][n][2 * r + 1];
-            pb[n][r] = transpose8x8(pack_f16(pf[n][2 * r] * s, pf[n][2 * r + 1] * s));
-            if (MASK) {            // a bias may be NaN: no product with rows that do not see it
-              if (p0 != 0.f) ob[n][j][0] = fmaf(p0, bias, ob[n][j][0]);
-              if (p1 != 0.f) ob[n][j][1] = fmaf(p1, bias, ob[n][j][1]);
-            } else {
-              ob[n][j][0] = fmaf(p0, bias, ob[n][j][0]);
-              ob[n][j][1] = fmaf(p1, bias, ob[n][j][1]);
-            }
+            const uint32_t w2 = pack_f16(pf[n][2 * r] * s, pf[n][2 * r + 1] * s);
+            pb[n][r] = transpose8x8(w2);
+            const float2 wf = __half22float2(*reinterpret_cast<const __half2*>(&w2));
+            // (a bias may be NaN: no product with rows that do not see it)
+            if (!MASK || x[b][n][2 * r] != 0.f) ob[n][j][0] = fmaf(wf.x, ratio, ob[n][j][0]);
+            if (!MASK || x[b][n][2 * r + 1] != 0.f) ob[n][j][1] = fmaf(wf.y, ratio, ob[n][j][1]);
           }
         }
         // 8 codes of tokens 2t, 2t+1, 2t+8, 2t+9: elements 64 j + 8 g ..
@@ -372,9 +382,11 @@ struct Warp {
         if (mx == -INFINITY) continue;          // nothing seen yet
         const bool first = m[n][c] == -INFINITY;
         const float mn = fmaxf(m[n][c], mx);
-        const float en = first ? ux - mn : fmaxf(e[n][c], ux - mn);
+        // (a whole exponent, so that f is a power of two and 1/f undoes it exactly)
+        const float eu = fminf(fmaxf(ceilf(ux - mn), -126.f), 126.f);
+        const float en = first ? eu : fmaxf(e[n][c], eu);
         keep[c] = mn == m[n][c] ? 1.f : exp2_approx(m[n][c] - mn);
-        const float fn = exp2_approx(-en);
+        const float fn = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(en)) << 23);
         down[c] = first ? 0.f : keep[c] * (fn / f[n][c]);
         m[n][c] = mn;
         e[n][c] = en;
@@ -385,8 +397,8 @@ struct Warp {
       }
 #pragma unroll
       for (int j = 0; j < G::J; ++j) {
-        ob[n][j][0] *= keep[0];
-        ob[n][j][1] *= keep[1];
+        ob[n][j][0] *= down[0];
+        ob[n][j][1] *= down[1];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -711,16 +723,17 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
     for (int c = 0; c < 2; ++c) {
       const int r = 8 * n + 2 * t + c;
       const float l = sum_over_rows8(w.l[n][c]);
-      const float up = 0x1p24f / w.f[n][c];
+      const float up = 1.f / w.f[n][c];
       if (g == 0) sml[warp * 8 * NT + r] = make_float2(w.m[n][c], l);
 #pragma unroll
       for (int j = 0; j < G::J; ++j) {
         const float ob = sum_over_rows8(w.ob[n][j][c]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float odd = BITS == 4 ? up * 0.0625f : up;
+          constexpr float kOdd = BITS == 4 ? 0x1p20f : 0x1p24f;
           *reinterpret_cast<float2*>(so + (warp * 8 * NT + r) * kRow + 64 * j + 8 * g + 2 * u) =
-              make_float2(fmaf(w.o[n][j][u][c], up, ob), fmaf(w.o[n][j][u][2 + c], odd, ob));
+              make_float2(fmaf(w.o[n][j][u][c], 0x1p24f, ob) * up,
+                          fmaf(w.o[n][j][u][2 + c], kOdd, ob) * up);
         }
       }
     }
@@ -807,7 +820,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
   };
   if (a.pre_units) {
     const int u = hk * a.pre_row_tiles + (row * a.G + head % a.G) / a.unit_rows;
-    of_rows(parts[0], 0, u * a.pre_T, a.pre_T);
+    of_rows(parts[0], 0, u * a.pre_T, (a.prefix_len + a.row_tile - 1) / a.row_tile);
   } else if (a.pre_blocks) {
     const int r = row * a.G + head % a.G;
     const int u = hk * a.pre_tiles + r / (8 * a.nt);
@@ -893,8 +906,34 @@ constexpr int kSMs = 152;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Query rows of a key/value head from which the row kernel is taken.
+// The row kernel is taken from 64 query rows of a key/value head on, if there is enough to
+// multiply: it does 700 to 1050 TFLOP/s where the split kernel does 40 to 180, but takes
+// about 20 us longer to get going. Measured, split and row kernel: 512 rows, D = 256, 64
+// tokens (0.07 GFLOP) 14 and 36 us, 1024 tokens (1.1) 33 and 26 us; 4096 rows, D = 128, 1024
+// tokens (4.3) 97 and 45 us.
 constexpr int64_t kRowKernelRows = 64;
+constexpr double kRowKernelFlops = 1e9;
+bool row_kernel_pays(int64_t rows, int64_t heads, int D, int64_t len) {
+  return rows >= kRowKernelRows && 4.0 * D * rows * heads * len >= kRowKernelFlops;
+}
+
+// Tiles per block for `units` units of T tiles on `sms` blocks, and the tiles that a unit
+// is taken to have. Equal shares of the lined-up tiles leave some blocks two pieces, and a
+// piece costs about as much as 5 tiles to start and end; with fewer units than blocks a
+// unit may instead be cut into equal parts of its own (T rounded up to whole shares).
+void share_out(int64_t units, int64_t* T, int64_t* share) {
+  constexpr int64_t kPieceTiles = 5;
+  const int64_t lined = std::max<int64_t>(1, ceil_div(units * *T, kSMs));
+  if (units <= kSMs) {
+    const int64_t own = std::max<int64_t>(2, ceil_div(*T, kSMs / units));   // (each part costs a partial result)
+    if (own + kPieceTiles <= lined + (lined < *T ? 2 * kPieceTiles : kPieceTiles)) {
+      *share = own;
+      *T = ceil_div(*T, own) * own;
+      return;
+    }
+  }
+  *share = lined;
+}
 
 bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_len, int prefix_len,
                Plan* out) {
@@ -903,21 +942,18 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
   const int64_t G = Hq / Hkv;
   const int64_t own_rows = nq * G, pre_rows = B * nq * G;
   const bool pre = prefix_len > 0, own = max_len > 0;
-  const bool pre_tc = pre && pre_rows >= kRowKernelRows;
-  const bool own_tc = own && own_rows >= kRowKernelRows;
+  const bool pre_tc = pre && row_kernel_pays(pre_rows, Hkv, D, prefix_len);
+  const bool own_tc = own && row_kernel_pays(own_rows, B * Hkv, D, max_len);
   // two column tiles share the conversion of the codes; at D = 256 their state
   // would not fit the registers
   a.nt = D <= 128 && ((own && !own_tc && own_rows > 8) || (pre && !pre_tc && pre_rows > 8)) ? 2 : 1;
-  int64_t split_tiles = 0, tiles = 0;
+  int64_t split_tiles = 0, pre_T = 0, own_T = 0, pre_units = 0, own_units = 0;
   a.unit_rows = attn_unit_rows(D);
   a.row_tile = attn_row_tile(D);
   if (pre_tc) {
     a.pre_row_tiles = static_cast<int>(ceil_div(pre_rows, a.unit_rows));
-    a.pre_T = static_cast<int>(ceil_div(prefix_len, a.row_tile));
-    const int64_t units = Hkv * a.pre_row_tiles;
-    tiles += units * a.pre_T;
-    if (units > 0x7FFFFFFF) return false;
-    a.pre_units = static_cast<int>(units);
+    pre_T = ceil_div(prefix_len, a.row_tile);
+    pre_units = Hkv * a.pre_row_tiles;
   } else if (pre) {
     a.pre_tiles = static_cast<int>(ceil_div(pre_rows, 8 * a.nt));
     a.pre_T = static_cast<int>(ceil_div(prefix_len, kSplitTile));
@@ -926,11 +962,8 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
   }
   if (own_tc) {
     a.own_row_tiles = static_cast<int>(ceil_div(own_rows, a.unit_rows));
-    a.own_T = static_cast<int>(ceil_div(max_len, a.row_tile));
-    const int64_t units = B * Hkv * a.own_row_tiles;
-    tiles += units * a.own_T;
-    if (units > 0x7FFFFFFF) return false;
-    a.own_units = static_cast<int>(units);
+    own_T = ceil_div(max_len, a.row_tile);
+    own_units = B * Hkv * a.own_row_tiles;
   } else if (own) {
     a.own_tiles = static_cast<int>(ceil_div(own_rows, 8 * a.nt));
     split_tiles += B * Hkv * a.own_tiles * ceil_div(max_len, kSplitTile);
@@ -939,13 +972,23 @@ bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_le
   int wave = 0;
   for (int bits : {4, 8}) wave = std::max(wave, kSMs * split_blocks_per_sm(D, bits, a.nt));
   p.split_tiles = split_tiles;
+  int64_t share = 0;
+  if (pre_units && own_units)
+    share = std::max<int64_t>(1, ceil_div(pre_units * pre_T + own_units * own_T, kSMs));
+  else if (pre_units)
+    share_out(pre_units, &pre_T, &share);
+  else if (own_units)
+    share_out(own_units, &own_T, &share);
+  const int64_t tiles = pre_units * pre_T + own_units * own_T;
   if (split_tiles > (1 << 30) || tiles > (1 << 30)) return false;   // the kernels count them in 32 bits
   const int64_t slots = 2 * std::min<int64_t>(wave, split_tiles);
   if (tiles > 0) {
-    const int64_t share = std::max<int64_t>(2, ceil_div(tiles, kSMs));
-    if (share > 0x7FFFFFFF) return false;
     a.share = static_cast<int>(share);
     p.row_blocks = static_cast<unsigned>(ceil_div(tiles, share));
+    a.pre_units = static_cast<int>(pre_units);
+    a.own_units = static_cast<int>(own_units);
+    if (pre_units) a.pre_T = static_cast<int>(pre_T);
+    if (own_units) a.own_T = static_cast<int>(own_T);
   }
   // partial results: the prefix's per row, the own tokens' per row, the split kernel's slots
   const int64_t heads = B * nq * Hq;
