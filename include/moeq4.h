@@ -327,7 +327,8 @@ moe_status moe_rope_phases(uint64_t* phase, int32_t rot, double base, int32_t sc
  *   x, out  device, `dtype` MOE_BF16, MOE_F16 or MOE_F32, T tokens of H heads of D
  *           elements (D even); token t, head h starts at element t*row + h*head.
  *           Strides in elements; out's rows may not overlap. out == x with the same
- *           strides is allowed.
+ *           strides is allowed, any other overlap of the two is not. H <= 65535,
+ *           D <= 65536.
  *   pos     int32 [T] device (any value)
  * Angles, sines and products in fp32, one rounding to dtype. 16-byte aligned
  * pointers and strides take the vector path, anything else a scalar one. */
@@ -372,7 +373,8 @@ typedef struct moe_kv_new {
  * to bf16; per group of 64: bias = min, scale = bf16((max - min) / (2^bits - 1)),
  * code = round((x - bias) / scale), ties to even, 0 when the group is constant.
  * A group that holds a NaN or an infinity reads back as NaN. Slots outside the
- * cache are skipped and set MOE_DEVERR_BAD_SLOT. T = 0 launches nothing. */
+ * cache are skipped and set MOE_DEVERR_BAD_SLOT. q_out may be q with the same strides;
+ * otherwise it overlaps no input. Hq <= 32768. T = 0 launches nothing. */
 moe_status moe_kv_append(const moe_kv_new* a, const moe_kv_cache* c, void* stream);
 
 /* Cache rows back as bf16(scale * code + bias): k_out, v_out [n][Hkv][D] dense,
@@ -402,13 +404,18 @@ typedef struct moe_kv_attn {
 } moe_kv_attn;
 
 /* Bytes of scratch for moe_kv_attention (partial results of split contexts). It
- * needs no zero-filling; calls that overlap on the GPU must not share it. */
+ * needs no zero-filling; calls that overlap on the GPU must not share it. 0 if the
+ * sizes are not allowed. */
 size_t moe_kv_attention_workspace_size(int32_t B, int32_t nq, int32_t Hq, int32_t Hkv, int32_t D,
                                        int32_t max_len, int32_t prefix_len);
 
 /* Limits: B * nq <= 2^24, Hq % Hkv == 0, Hq <= 65535, max_len and prefix_len <= 2^30.
- * B = 0 launches nothing. Page numbers are read only as far as lens and
- * prefix_len reach. q and out: 16-byte aligned, strides multiples of 8. */
+ * Sizes whose work passes 2^30 tiles (8 query rows x 64 tokens at the least) are
+ * MOE_ERR_SHAPE. B = 0 launches nothing. Page numbers are read only as far as lens and
+ * prefix_len reach; a page outside the cache gives no tokens and sets
+ * MOE_DEVERR_BAD_PAGE, a length outside 0 .. max_len is clamped and sets
+ * MOE_DEVERR_BAD_LENGTH. q and out: 16-byte aligned, strides multiples of 8, no
+ * overlap. */
 moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache* c, void* ws,
                             size_t ws_bytes, void* stream);
 

@@ -3,7 +3,9 @@
 //
 // All three move each byte once and do little arithmetic per byte, so they are
 // bound by memory bandwidth at many tokens and by launch latency at few. One
-// launch each, no shared memory, no scratch.
+// launch each, no shared memory, no scratch. Bandwidths below are of a copy of 6.8 TB/s
+// as measured on the same card, where a plain fill of memory reaches 4.0 TB/s: what
+// writes more than it reads cannot come near the copy.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -100,6 +102,8 @@ struct alignas(V * sizeof(E)) Vec {
 // elements 2i and 2i + 1 within one), so that neighbouring lanes always touch
 // neighbouring vectors. The V angles are computed once and used for every head of the
 // block; heads go two at a time, to keep more loads in flight. Units past rot / 2V copy.
+// Measured: 2047 tokens of 40 fp32 heads of 128 elements (83.9 MB), 15.7 us, 79 % of the
+// copy's bandwidth. One token: 2.4 us on the device, which is the launch.
 template <typename E, int V>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
   griddep_wait();
@@ -202,7 +206,10 @@ __global__ void __launch_bounds__(kThreads) rope_pair_kernel(RopeArgs a) {
 }
 
 // Heads per thread: one while the call is small (latency), up to `most` that share their
-// angles once there are threads enough to fill the multiprocessors several times.
+// angles once there are threads enough to fill the multiprocessors several times. Measured
+// back to back: an append of 4096 tokens of 32 + 8 + 8 heads with at most 16, 4 and 1 heads
+// 29.9, 37.3 and 98.1 us; rope on 2047 tokens of 40 heads with 4, 2 and 1 heads 10.6, 10.8
+// and 16.3 us (inputs partly in L2).
 int heads_per_thread(int64_t T, int64_t units, int64_t H, int most) {
   int per = 1;
   while (per < most && T * units * H / (2 * per) >= 152 * 1024) per *= 2;
@@ -381,7 +388,12 @@ __device__ __forceinline__ void store_codes(const AppendArgs& a, uint4 raw, int 
 // heads, whose angles a thread computes once for all of its heads, then the value heads.
 // (q_out may be q only if no thread reads what another wrote: a turned run reads its
 // partner run of the same head, whose D / 8 <= 32 threads are lanes of one warp;
-// __syncwarp separates a head's reads from its writes.)
+// __syncwarp separates a head's reads from its writes.) Eight lanes hold a group of 64: its
+// least and largest element take three exchanges each.
+// Measured: 4096 tokens of 32 + 8 + 8 heads, D = 128, 4 bits (50 MB read, 38 MB written),
+// 29.9 us, 43 % of the copy's bandwidth; issue slots are 53 % busy with turning, rounding
+// and quantising, and the loads of a thread's few heads in flight bind beside them. 64
+// tokens: 3.7 us on the device.
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   griddep_wait();
@@ -446,6 +458,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
 // Thread = (run of 8 codes of a key or value head, four rows): lanes read neighbouring
 // codes and write neighbouring 16 bytes of bf16, and a thread's four rows keep their
 // loads in flight together. (Block = rows x one head; no division but by page.)
+// Measured: 32768 rows of 8 heads, D = 128, 4 bits (38 MB read, 134 MB written), 42.0 us,
+// 60 % of the copy's bandwidth; a plain fill of the 134 MB takes 34 us.
 constexpr int kReadRows = 4;
 
 template <int BITS>
