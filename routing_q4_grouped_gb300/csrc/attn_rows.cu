@@ -14,9 +14,9 @@
 // one fp16 fma with 2^24 s, with one rounding of 2^-11.
 //
 // fp16's range. Queries are divided by the power of two under their row's largest
-// element. The keys and the values of each 32 tokens are divided by powers of two 2^eK and 2^eV 2^8 above
-// their largest magnitude (so 2^24 s fits, and what is 2^-8 of the largest is still a
-// normal number); eK goes into the logits' factor, and 2^eV into the
+// element. The keys and the values of each 32 tokens are divided by powers of two, 2^eK
+// and 2^eV, 2^8 above their largest magnitude (so 2^24 s fits, and what is 2^-8 of the
+// largest is still a normal number); eK goes into the logits' factor, and 2^eV into the
 // weights' exponent: P' = exp2(x - m + eV - E) with a running E per row, so P' stays
 // near 1 whatever the values' size. A tile with tokens that differ by more than 2^6
 // within 32 takes one exponent per token (the same formulas with a factor per
@@ -31,14 +31,25 @@
 //
 // Warps (one block per SM, persistent over its share of tiles):
 //   0-3, 4-7  softmax of query tile 0 and 1 (warp % 4 = tensor-memory lane quarter),
-//             their queries' load and their outputs' store
+//             their queries' load and their outputs' store (D = 256: 4-7 do half of both
+//             for tile 0)
 //   11        issues the products
 //   15        finds the pages of the tiles ahead
 //   8 9 10 12 13 14 16 17 (D = 64: the first four)  scales, and codes to operands
 // D <= 128: two query tiles share each token tile and take turns, one in the tensor
 // cores while the other is in its softmax. D = 256: one query tile, held in tensor
-// memory, tiles of 64 tokens, and logits that alternate between two slots. Every wait on an mbarrier has a time limit; after one
-// ran out, no thread waits again and the kernel ends with MOE_DEVERR_PIPE_TIMEOUT.
+// memory, tiles of 64 tokens, and logits that alternate between two slots. Every wait on an
+// mbarrier has a time limit; after one ran out, no thread waits again and the kernel ends
+// with MOE_DEVERR_PIPE_TIMEOUT.
+//
+// Measured: the last 4096 query tokens of 32768 (16 query heads on 2, D = 128, 8 bits),
+// 977 us, 1055 TFLOP/s, 54 % of the bf16 peak as measured. A tile of 128 tokens for 256
+// rows takes about 4450 cycles, its products alone 2200. What binds is latency: the
+// conversion of the next tile (codes from L2, fp16 arithmetic, shared memory) and the
+// softmax (about 3400 cycles) leave each other hardly any slack. 512 rows behind a prefix
+// of 16000 tokens (D = 256, 14 tiles a block) take 14 % of the peak: to load the queries
+// (7 us, several dependent rounds of loads that queue behind the codes'), to come to the
+// first weights (2 us) and to write partial results (4 us) costs as much as 8 tiles.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -74,6 +85,7 @@ struct RowGeo {
   static constexpr int kThreads = (kConvWarps == 4 ? 16 : 18) * 32;
   static constexpr int KS = D == 256 ? 3 : 2;         // operand tiles in flight, keys and values each
   static constexpr bool kQTmem = D == 256;            // queries in tensor memory, not shared memory
+  static constexpr int kStageRow = kQTmem ? 64 : 128;             // bytes of a row in a softmax warp's staging
   static constexpr uint32_t kQBytes = kQTmem ? 0 : 128 * D * 2;   // a query tile
   static constexpr uint32_t kTileBytes = TT * D * 2;  // a key or value tile
   static constexpr uint32_t kOffK = QT * kQBytes;
@@ -112,9 +124,16 @@ struct Ctl {
   int abort;
 };
 
+// Where the queries are in tensor memory, the softmax warps' staging has its own place,
+// and after it 128 rows' ends.
+template <int D>
+constexpr uint32_t kOffStage =
+    (RowGeo<D>::kOffMeta + kMetaRing * sizeof(Meta<D>) + sizeof(Ctl) + 127) / 128 * 128;
+
 template <int D>
 constexpr size_t row_smem() {
-  return 1024 + RowGeo<D>::kOffMeta + kMetaRing * sizeof(Meta<D>) + sizeof(Ctl);
+  return 1024 + kOffStage<D> +
+         (RowGeo<D>::kQTmem ? kSoftWarps * 32 * RowGeo<D>::kStageRow + 128 * sizeof(float2) : 0);
 }
 
 // One block's piece of a unit: token tiles [kt0, kt1) for query rows row0 ...
@@ -252,6 +271,11 @@ __device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, 
 __device__ __forceinline__ uint32_t exp_field(uint32_t bf16_bits) { return (bf16_bits >> 7) & 255u; }
 __device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z,
                                              uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w)
@@ -625,58 +649,142 @@ struct Softmax {
   float c;                   // scale2 * 2^(row exponent)
   uint32_t nan;              // value groups that are NaN for this row
 
-  // The row's query, divided by the power of two under its largest element, as fp16
-  // in the key tiles' element order.
+  // This warp's staging: 32 rows of SB bytes, 16-byte pieces permuted by their row, for
+  // turning between a thread's own row and neighbouring lanes on one row (which memory
+  // wants). Queries in shared memory lend it after their last product.
+  static constexpr int SB = G::kStageRow;
+  static constexpr int PC = SB / 16;              // pieces of a row,
+  static constexpr int RL = 32 / PC;              // rows of a warp's access
+  __device__ __forceinline__ uint8_t* stage() const {
+    return smem + (G::kQTmem ? kOffStage<D> + warp * (32 * SB) : wg * G::kQBytes + (warp & 3) * (32 * SB));
+  }
+  static __device__ __forceinline__ int piece(int row, int k) {
+    return row * SB + ((k ^ (SB == 128 ? row & 7 : row >> 1 & 3)) << 4);
+  }
+
+  // The rows' queries, each divided by the power of two under its largest element, as
+  // fp16 in the key tiles' element order. `qp` is the thread's own row; lanes read
+  // neighbouring pieces of a row. (D = 256: each warpgroup prepares half of the elements.)
   __device__ void load_query(const uint16_t* qp, bool live) {
-    const int r = (warp & 3) * 32 + lane;
-    constexpr int kHalf = D / 16;                 // 16-byte pieces kept at a time
-    uint4 v[kHalf];
-    float mx = 0.f;
+    const uint32_t lives = __ballot_sync(kAll, live);
+    const uint64_t base = reinterpret_cast<uint64_t>(qp);
+    const auto at = [&](int row) { return reinterpret_cast<const uint8_t*>(__shfl_sync(kAll, base, row)); };
+    // largest magnitude: bf16 bits without their sign order like the numbers
+    constexpr int LW = D / 64;                    // words of a row per lane
+    uint32_t mx = 0;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 8) {
+      uint32_t w[8][LW];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+      for (int u = 0; u < 8; ++u) {
+        const uint8_t* q = at(r0 + u) + lane * (4 * LW);
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i)
-        v[i] = live ? __ldg(reinterpret_cast<const uint4*>(qp) + h * kHalf + i) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < LW; ++k) w[u][k] = 0;
+        if (lives >> (r0 + u) & 1) {
+          if constexpr (LW == 1) {
+            w[u][0] = ld_nc_u32(q);
+          } else if constexpr (LW == 2) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
+            w[u][0] = v.x, w[u][1] = v.y;
+          } else {
+            const uint4 v = ld_nc_v4(q);
+            w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
+          }
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      for (int u = 0; u < 8; ++u) {
+        uint32_t x = w[u][0] & 0x7FFF7FFFu;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+        for (int k = 1; k < LW; ++k) x = max_u16x2(x, w[u][k] & 0x7FFF7FFFu);
+        x = __reduce_max_sync(kAll, max(x >> 16, x & 0xFFFFu));
+        if (lane == r0 + u) mx = x;
       }
     }
-    const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
+    const uint32_t e = min(max(mx >> 7, 1u), 253u);
     const float down = pow2_field(254u - e);
     c = a.scale2 * pow2_field(e);
-    uint8_t* dst = smem + wg * G::kQBytes + r * 128;
+    constexpr int kChunks = D / 8 / PC, kMine = G::kQTmem ? kChunks / 2 : kChunks;
+    constexpr int kBatch = 8 / PC;                // chunks of PC pieces loaded together
+    const int first = G::kQTmem ? wg * kMine : 0;
+#pragma unroll 1
+    for (int j0 = first; j0 < first + kMine; j0 += kBatch) {
+      uint4 v[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i)             // (read twice: the second time from the L1 cache)
-        v[i] = live ? __ldg(reinterpret_cast<const uint4*>(qp) + h * kHalf + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i) {
-        const int k = h * kHalf + i;
-        const float x[8] = {bf16_lo(v[i].x) * down, bf16_hi(v[i].x) * down, bf16_lo(v[i].y) * down,
-                            bf16_hi(v[i].y) * down, bf16_lo(v[i].z) * down, bf16_hi(v[i].z) * down,
-                            bf16_lo(v[i].w) * down, bf16_hi(v[i].w) * down};
-        v[i] = BITS == 8 ? make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
-                                      pack_f16(x[4], x[5]), pack_f16(x[6], x[7]))
-                         : make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]),
-                                      pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
-        if (!G::kQTmem)
-          *reinterpret_cast<uint4*>(dst + (k >> 3) * 16384 + (((k & 7) ^ (r & 7)) << 4)) = v[i];
+      for (int u = 0; u < 8; ++u) {
+        const int row = u % PC * RL + lane / PC;
+        const uint4* q = reinterpret_cast<const uint4*>(at(row)) + (j0 + u / PC) * PC + lane % PC;
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (lives >> row & 1) v[u] = __ldg(q);
       }
-      if (G::kQTmem) {
 #pragma unroll
-        for (int i = 0; i + 4 <= kHalf; i += 4) {
-          const uint32_t q[16] = {v[i].x,     v[i].y,     v[i].z,     v[i].w,
-                                  v[i + 1].x, v[i + 1].y, v[i + 1].z, v[i + 1].w,
-                                  v[i + 2].x, v[i + 2].y, v[i + 2].z, v[i + 2].w,
-                                  v[i + 3].x, v[i + 3].y, v[i + 3].z, v[i + 3].w};
-          tmem_st_32x32b_x16(tmem + G::kColQ + (h * kHalf + i) * 4, q);
+      for (int b = 0; b < kBatch; ++b) {
+        uint8_t* dst = stage() + (G::kQTmem ? 0 : j0 * 16384);
+#pragma unroll
+        for (int u = 0; u < PC; ++u) {
+          const uint4 x4 = v[b * PC + u];
+          const int row = u * RL + lane / PC;
+          const float f = __shfl_sync(kAll, down, row);
+          const float x[8] = {bf16_lo(x4.x) * f, bf16_hi(x4.x) * f, bf16_lo(x4.y) * f, bf16_hi(x4.y) * f,
+                              bf16_lo(x4.z) * f, bf16_hi(x4.z) * f, bf16_lo(x4.w) * f, bf16_hi(x4.w) * f};
+          *reinterpret_cast<uint4*>(dst + piece(row, lane % PC)) =
+              BITS == 8 ? make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]),
+                                     pack_f16(x[6], x[7]))
+                        : make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]), pack_f16(x[2], x[6]),
+                                     pack_f16(x[3], x[7]));
         }
-        tmem_st_wait();
+        if constexpr (G::kQTmem) {
+          __syncwarp();
+          uint32_t q[4 * PC];
+#pragma unroll
+          for (int k = 0; k < PC; ++k) {
+            const uint4 x4 = *reinterpret_cast<const uint4*>(dst + piece(lane, k));
+            q[4 * k] = x4.x, q[4 * k + 1] = x4.y, q[4 * k + 2] = x4.z, q[4 * k + 3] = x4.w;
+          }
+          tmem_st_32x32b_x16(tmem + G::kColQ + 16 * (j0 + b), q);
+          __syncwarp();
+        }
       }
+    }
+    if (G::kQTmem) tmem_st_wait();
+  }
+
+  // This thread's row of O times `up` (NaN for the value groups in `nan`) to memory at
+  // element `dst`, as the output or as a partial result. (D = 256: each warpgroup half of it.)
+  __device__ void store(int64_t dst, bool live, bool output, float up, uint32_t nan_groups) {
+    constexpr int kCols = SB / 4, kChunks = D / kCols, kMine = G::kQTmem ? kChunks / 2 : kChunks;
+    const int first = G::kQTmem ? wg * kMine : 0;
+    const uint32_t lives = __ballot_sync(kAll, live);
+    uint8_t* st = stage();
+#pragma unroll 1
+    for (int h = first; h < first + kMine; ++h) {
+      const float f = nan_groups >> (h * kCols / kKvGroup) & 1 ? NAN : up;
+#pragma unroll
+      for (int k = 0; k < PC / 4; ++k) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tmem + G::kColO + (G::kQTmem ? 0 : wg * D) + kCols * h + 16 * k, v);
+        tmem_ld_wait();
+        tmem_regs_ready(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(st + piece(lane, 4 * k + i)) =
+              make_float4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f,
+                          __uint_as_float(v[4 * i + 2]) * f, __uint_as_float(v[4 * i + 3]) * f);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < PC; ++i) {
+        const int row = RL * i + lane / PC;
+        const int64_t to = __shfl_sync(kAll, dst, row) + kCols * h + lane % PC * 4;
+        const float4 y = *reinterpret_cast<const float4*>(st + piece(row, lane % PC));
+        if (lives >> row & 1) {
+          if (output)
+            *reinterpret_cast<uint2*>(a.out + to) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+          else
+            *reinterpret_cast<float4*>(a.part + to) = y;
+        }
+      }
+      __syncwarp();
     }
   }
 
@@ -857,7 +965,7 @@ struct Softmax {
 
   // sp: parity of each logit slot's next phase (bit = slot); pc: products into O so far.
   __device__ void run(const Seg& sg, int nqt, uint32_t tc, uint32_t sp, uint32_t pc, Waiter& w) {
-    const int r = sg.row0 + wg * 128 + (warp & 3) * 32 + lane;
+    const int r = sg.row0 + (G::kQTmem ? 0 : wg * 128) + (warp & 3) * 32 + lane;
     const bool live = r < sg.n_rows;
     const int qrow = live ? (sg.pre ? r / a.G : sg.b * a.nq + r / a.G) : 0;
     const int head = sg.hk * a.G + (live ? r % a.G : 0);
@@ -867,13 +975,28 @@ struct Softmax {
     else
       fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl.q_full[wg]);
+    if (lane == 0) mbar_arrive(&ctl.q_full[G::kQTmem ? 0 : wg]);
+    const int nt = sg.kt1 - sg.kt0;
+    const bool lone = a.lone && sg.kt0 == 0 && sg.kt1 == sg.tiles;
+    const int64_t at = (sg.pre ? 0 : a.own_whole) +
+                       static_cast<int64_t>(sg.part) * a.B * a.nq * a.Hq +
+                       static_cast<int64_t>(qrow) * a.Hq + head;
+    const int64_t dst = lone ? qrow * a.o_row + head * a.o_head : at * D;
+    float2* ends = reinterpret_cast<float2*>(smem + kOffStage<D> + kSoftWarps * 32 * SB);
+    if (G::kQTmem && wg == 1) {                    // helps with the row's ends only
+      named_bar_sync(3, kSoftWarps * 32);
+      w.wait(&ctl.pv_done[0], (pc + nt - 1) & 1);
+      tc_fence_after();
+      const float2 end = ends[(warp & 3) * 32 + lane];
+      store(dst, live, lone, end.x, __float_as_uint(end.y));
+      tc_fence_before();
+      return;
+    }
     m = -INFINITY;
     l = 0.f;
     E = 0.f;
     nan = 0;
     const int lim = !live ? 0 : sg.pre ? sg.ctx : own_limit(a, sg.ctx, r);
-    const int nt = sg.kt1 - sg.kt0;
     for (int it = 0; it < nt; ++it) {
       const int slot = nqt == 2 ? wg : it & 1;
       const Meta<D>& t = metas[(tc + it) & 3];
@@ -904,37 +1027,13 @@ struct Softmax {
     // ---- outputs
     w.wait(&ctl.pv_done[wg], (pc + nt - 1) & 1);
     tc_fence_after();
-    const bool lone = a.lone && sg.kt0 == 0 && sg.kt1 == sg.tiles;
     const float up = exp2_approx(E) * (lone ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
-    const int64_t at = (sg.pre ? 0 : a.own_whole) +
-                       static_cast<int64_t>(sg.part) * a.B * a.nq * a.Hq +
-                       static_cast<int64_t>(qrow) * a.Hq + head;
     if (live && !lone) a.ml[at] = make_float2(m, l);
-    uint16_t* out = a.out + qrow * a.o_row + head * a.o_head;
-    float* part = a.part + at * D;
-    for (int h = 0; h < D / 16; ++h) {
-      uint32_t v[16];
-      tmem_ld_32x32b_x16(tmem + G::kColO + wg * D + 16 * h, v);
-      tmem_ld_wait();
-      tmem_regs_ready(v);
-      if (!live) continue;
-      const bool is_nan = nan >> (h * 16 / kKvGroup) & 1;
-      float y[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = is_nan ? NAN : __uint_as_float(v[i]) * up;
-      if (lone) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          *reinterpret_cast<uint4*>(out + 16 * h + 8 * k) =
-              make_uint4(pack_bf16(y[8 * k], y[8 * k + 1]), pack_bf16(y[8 * k + 2], y[8 * k + 3]),
-                         pack_bf16(y[8 * k + 4], y[8 * k + 5]), pack_bf16(y[8 * k + 6], y[8 * k + 7]));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<float4*>(part + 16 * h + 4 * k) =
-              make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-      }
+    if (G::kQTmem) {
+      ends[(warp & 3) * 32 + lane] = make_float2(up, __uint_as_float(nan));
+      named_bar_sync(3, kSoftWarps * 32);
     }
+    store(dst, live, lone, up, nan);
     tc_fence_before();
   }
 };
@@ -957,7 +1056,7 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
       mbar_init(&ctl.v_full[i], G::kConvWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.q_full[i], 4);
+      mbar_init(&ctl.q_full[i], G::kQTmem ? 8 : 4);
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_full[i], 4);
       mbar_init(&ctl.pv_done[i], 1);
@@ -992,7 +1091,7 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
     uint32_t sp = 0, pc[2] = {0, 0};
     while (walk.next(a, sg, threadIdx.x == 0)) {
       const int nt = sg.kt1 - sg.kt0, nqt = query_tiles(sg);
-      if (sm.wg < nqt) sm.run(sg, nqt, tc, sp, sm.wg ? pc[1] : pc[0], w);
+      if (G::kQTmem || sm.wg < nqt) sm.run(sg, nqt, tc, sp, !G::kQTmem && sm.wg ? pc[1] : pc[0], w);
       // a warpgroup without a query tile may not run ahead: a wait tells only
       // neighbouring phases of its barrier apart
       named_bar_sync(2, kSoftWarps * 32);
@@ -1115,6 +1214,7 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
 template <int D, int BITS>
 cudaError_t launch_rows(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
   constexpr size_t smem = row_smem<D>();
+  static_assert(smem <= 232448, "shared memory");
   static_assert(smem <= 227 * 1024, "shared memory");
   const auto kernel = attn_rows_kernel<D, BITS>;
   static std::atomic<uint64_t> done{0};
