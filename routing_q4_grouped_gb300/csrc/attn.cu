@@ -34,7 +34,7 @@
 //
 // Measured (D = 128, 32 query heads on 8 key/value heads, join included): one request of
 // 131071 tokens, 8 bits, 54 us, 5.3 TB/s, 78 % of the copy's bandwidth; 64 requests of
-// mixed lengths, 4 bits, 98 us, 3.1 TB/s. There a byte holds twice the codes and the
+// mixed lengths, 4 bits, 99 us, 3.1 TB/s. There a byte holds twice the codes and the
 // issue slots bind (62 % of them used in the kernel's middle, 46 % at 8 bits, tensor
 // cores at 16 to 19 %), not the memory.
 #include <algorithm>

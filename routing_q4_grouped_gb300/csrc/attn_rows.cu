@@ -43,7 +43,7 @@
 // with MOE_DEVERR_PIPE_TIMEOUT.
 //
 // Measured: the last 4096 query tokens of 32768 (16 query heads on 2, D = 128, 8 bits),
-// 977 us, 1055 TFLOP/s, 54 % of the bf16 peak as measured. A tile of 128 tokens for 256
+// 983 us, 1050 TFLOP/s, 54 % of the bf16 peak as measured. A tile of 128 tokens for 256
 // rows takes about 4450 cycles, its products alone 2200. What binds is latency: the
 // conversion of the next tile (codes from L2, fp16 arithmetic, shared memory) and the
 // softmax (about 3400 cycles) leave each other hardly any slack. 512 rows behind a prefix
