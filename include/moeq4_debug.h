@@ -59,6 +59,11 @@ moe_status moe_debug_set_decode_max_t(int32_t t);
  * test can plant stale contents in it. */
 moe_status moe_debug_noalloc_scratch(void** addr, size_t* bytes);
 
+/* Page of a cache slot as the kernels that write, read and attend over a cache
+ * compute it (the same function, on the host). page_size a multiple of 16 up to
+ * 4096, slot >= 0; -1 otherwise. */
+int32_t moe_debug_kv_page(int32_t page_size, int32_t slot);
+
 #ifdef __cplusplus
 }
 #endif

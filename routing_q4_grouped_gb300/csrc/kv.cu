@@ -14,6 +14,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "../../include/moeq4_debug.h"
 #include "internal.h"
 #include "kv.cuh"
 #include "ptx.cuh"
@@ -42,7 +43,7 @@ KvCache kv_cache_args(const moe_kv_cache& c) {
   k.head_bytes = k.code_bytes + c.page_size * (c.D / kKvGroup) * 4;
   k.page_bytes = 2ll * c.Hkv * k.head_bytes;
   k.page_blocks = static_cast<uint32_t>(c.page_size / 16);
-  k.page_magic = (1ull << 40) / k.page_blocks + 1;
+  k.page_magic = (1ull << 37) / k.page_blocks + 1;
   return k;
 }
 
@@ -696,4 +697,10 @@ extern "C" moe_status moe_kv_read(const moe_kv_cache* c, const int32_t* slots, i
       launch_pdl(c->bits == 8 ? read_kernel<8> : read_kernel<4>,
                  grid, dim3(kThreads), 0, s, k, slots, n, k_out, v_out);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" int32_t moe_debug_kv_page(int32_t page_size, int32_t slot) {
+  if (slot < 0 || moe_kv_cache_size(1, page_size, 1, 64, 8) == 0) return -1;
+  const moe_kv_cache c = {nullptr, nullptr, 1, page_size, 1, 64, 8};
+  return moeq4::page_of_block(moeq4::kv_cache_args(c), static_cast<uint32_t>(slot) >> 4);
 }

@@ -22,16 +22,18 @@ struct KvCache {
   int head_bytes;                    // one head of a page
   int64_t page_bytes;
   uint32_t page_blocks;              // 16-token blocks per page
-  uint64_t page_magic;               // floor(2^40 / page_blocks) + 1
+  uint64_t page_magic;               // floor(2^37 / page_blocks) + 1
 };
 
 moe_status check_kv_cache(const moe_kv_cache* c);
 KvCache kv_cache_args(const moe_kv_cache& c);
 
-// Page of 16-token block blk < 2^27: blk / page_blocks, exact because the magic number's
-// excess, below 2^-40 * page_blocks * blk < 2^-5, stays below 1 / page_blocks.
-__device__ __forceinline__ int page_of_block(const KvCache& c, uint32_t blk) {
-  return static_cast<int>((blk * c.page_magic) >> 40);
+// Page of 16-token block blk < 2^27: blk / page_blocks by multiplication. The magic number is
+// at most 2^37 + 1, so the product stays below 2^64, and its excess over 2^37 / page_blocks is
+// at most 1, so the quotient is too large by at most blk * 2^-37 < 2^-10, less than the
+// 1 / page_blocks >= 2^-8 that the next whole page needs.
+__host__ __device__ inline int page_of_block(const KvCache& c, uint32_t blk) {
+  return static_cast<int>((blk * c.page_magic) >> 37);
 }
 
 // The block of head h (key heads 0 .. Hkv-1, then value heads) of a page.

@@ -131,6 +131,7 @@ _SIGS = {
     "moe_debug_mma": (_c_i32, [_c_i32, _c_ptr, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr]),
     "moe_debug_set_stage_events": (_c_i32, [ctypes.POINTER(_c_ptr), _c_i32]),
     "moe_debug_tmem_layout": (_c_i32, [_c_ptr, _c_ptr]),
+    "moe_debug_kv_page": (_c_i32, [_c_i32, _c_i32]),
     "moe_debug_noalloc_scratch": (_c_i32, [ctypes.POINTER(_c_ptr), ctypes.POINTER(_c_size)]),
 }
 
@@ -631,6 +632,11 @@ def moe_debug_mma(a_from_tmem: bool, A, B, D, stream=None) -> None:
 
 def moe_debug_tmem_layout(out, stream=None) -> None:
     _check("moe_debug_tmem_layout", lib().moe_debug_tmem_layout(_ptr(out), _stream(stream)))
+
+
+def moe_debug_kv_page(page_size: int, slot: int) -> int:
+    """Page of a cache slot as the kernels compute it (-1: not allowed). Host only."""
+    return lib().moe_debug_kv_page(page_size, slot)
 
 
 def moe_debug_noalloc_scratch() -> tuple[int, int]:
