@@ -64,6 +64,12 @@ moe_status moe_debug_noalloc_scratch(void** addr, size_t* bytes);
  * 4096, slot >= 0; -1 otherwise. */
 int32_t moe_debug_kv_page(int32_t page_size, int32_t slot);
 
+/* Which kernel moe_kv_attention takes for a call of these sizes: bit 0 set if
+ * the prefix, bit 1 if the requests' own tokens go to the kernel for many query
+ * rows; -1 if the sizes are not allowed. Host function. */
+int32_t moe_debug_kv_attention_rows(int32_t B, int32_t nq, int32_t Hq, int32_t Hkv, int32_t D,
+                                    int32_t max_len, int32_t prefix_len);
+
 #ifdef __cplusplus
 }
 #endif

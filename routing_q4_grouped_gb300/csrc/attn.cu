@@ -44,6 +44,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "../../include/moeq4_debug.h"
 #include "attn.cuh"
 #include "internal.h"
 
@@ -1108,6 +1109,14 @@ extern "C" size_t moe_kv_attention_workspace_size(int32_t B, int32_t nq, int32_t
     return 0;
   moeq4::Plan p;
   return moeq4::make_plan(B, nq, Hq, Hkv, D, max_len, prefix_len, &p) ? p.total : 0;
+}
+
+extern "C" int32_t moe_debug_kv_attention_rows(int32_t B, int32_t nq, int32_t Hq, int32_t Hkv,
+                                               int32_t D, int32_t max_len, int32_t prefix_len) {
+  if (moe_kv_attention_workspace_size(B, nq, Hq, Hkv, D, max_len, prefix_len) == 0) return -1;
+  moeq4::Plan p;
+  moeq4::make_plan(B, nq, Hq, Hkv, D, max_len, prefix_len, &p);
+  return (p.a.pre_units > 0 ? 1 : 0) | (p.a.own_units > 0 ? 2 : 0);
 }
 
 extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache* c, void* ws,

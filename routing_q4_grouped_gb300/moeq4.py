@@ -132,6 +132,7 @@ _SIGS = {
     "moe_debug_set_stage_events": (_c_i32, [ctypes.POINTER(_c_ptr), _c_i32]),
     "moe_debug_tmem_layout": (_c_i32, [_c_ptr, _c_ptr]),
     "moe_debug_kv_page": (_c_i32, [_c_i32, _c_i32]),
+    "moe_debug_kv_attention_rows": (_c_i32, [_c_i32] * 7),
     "moe_debug_noalloc_scratch": (_c_i32, [ctypes.POINTER(_c_ptr), ctypes.POINTER(_c_size)]),
 }
 
@@ -637,6 +638,11 @@ def moe_debug_tmem_layout(out, stream=None) -> None:
 def moe_debug_kv_page(page_size: int, slot: int) -> int:
     """Page of a cache slot as the kernels compute it (-1: not allowed). Host only."""
     return lib().moe_debug_kv_page(page_size, slot)
+
+
+def moe_debug_kv_attention_rows(B, nq, Hq, Hkv, D, max_len, prefix_len=0) -> int:
+    """1: the prefix, 2: the requests' own tokens go to the kernel for many query rows. Host only."""
+    return lib().moe_debug_kv_attention_rows(B, nq, Hq, Hkv, D, max_len, prefix_len)
 
 
 def moe_debug_noalloc_scratch() -> tuple[int, int]:
