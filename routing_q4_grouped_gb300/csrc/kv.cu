@@ -362,11 +362,14 @@ __device__ __forceinline__ void store_codes(const AppendArgs& a, uint4 raw, int 
     const float range = __fsub_rn(0.5f * hi, 0.5f * lo);
     words = pack_bf16(__fmul_rn(range, 1.0f / (0.5f * kLevels)), lo);
     const float scale = bf16_lo(words);
-    const float per = scale > 0.f ? __fdiv_rn(1.0f, scale) : 0.f;
+    // (the reciprocal of a scale below 2^-126 may pass the largest float: differences and
+    // scale are taken 2^64 times as large there, which is exact)
+    const float up = scale < 0x1p-126f ? 0x1p64f : 1.f;
+    const float per = scale > 0.f ? __fdiv_rn(1.0f, scale * up) : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       code[i] = static_cast<uint32_t>(
-          fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(v[i], lo), per)), 0.f), kLevels));
+          fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(v[i], lo) * up, per)), 0.f), kLevels));
   }
   const int page = page_of_block(a.c, static_cast<uint32_t>(slot) >> 4);
   const int row = slot - page * a.c.page_size;
