@@ -310,11 +310,15 @@ struct Warp {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float s = value_scale(vw[b][r][j]), bias = bf16_hi(vw[b][r][j]);
-          // bias / s with one correction step: exact where the quotient is a float
+          // bias / s with one correction step: exact where the quotient is a float. (The
+          // approximate reciprocal takes numbers below 2^-126 as 0: tiny scales are divided
+          // 2^100 times as large, and their biases are no larger than 2^17 scales.)
+          const float up = fabsf(s) < 0x1p-100f ? 0x1p100f : 1.f;
+          const float su = s * up, bu = bias * up;
           float inv;
-          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-          float ratio = bias * inv;
-          ratio = fmaf(fmaf(-ratio, s, bias), inv, ratio) + (BITS == 8 ? 128.f : 8.f);
+          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(su));
+          float ratio = bu * inv;
+          ratio = fmaf(fmaf(-ratio, su, bu), inv, ratio) + (BITS == 8 ? 128.f : 8.f);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint32_t w2 = pack_f16(pf[n][2 * r] * s, pf[n][2 * r + 1] * s);
@@ -394,8 +398,9 @@ struct Warp {
         if (mx == -INFINITY) continue;          // nothing seen yet
         const bool first = m[n][c] == -INFINITY;
         const float mn = fmaxf(m[n][c], mx);
-        // (a whole exponent, so that f is a power of two and 1/f undoes it exactly)
-        const float eu = fminf(fmaxf(ceilf(ux - mn), -126.f), 126.f);
+        // (a whole exponent, so that f is a power of two and 1/f undoes it exactly; f times
+        // a weight of 2^8 is still a float)
+        const float eu = fminf(fmaxf(ceilf(ux - mn), -118.f), 126.f);
         const float en = first ? eu : fmaxf(e[n][c], eu);
         keep[c] = mn == m[n][c] ? 1.f : exp2_approx(m[n][c] - mn);
         const float fn = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(en)) << 23);

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import oracle as O
+from kv_case import Case
 from routing_q4_grouped_gb300 import moeq4
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +32,15 @@ def test_write_keeps_tiny_groups(bits):
         bound = step * 0.5 * (1 + 2.0 ** -8) + (span + np.abs(x[r])) * 2.0 ** -8 \
             + (2 ** bits - 1) * 2.0 ** -134 + 2.0 ** -134
         assert np.all(np.abs(got[r] - x[r]) <= bound), (r, got[r], x[r])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("size", [2.0 ** -116, 2.0 ** -122])
+@pytest.mark.parametrize("lens,nq,G", [([17, 40, 1], 1, 4), ([900, 65, 300], 9, 3)])
+def test_attention_over_tiny_values(lens, nq, G, size, D, bits):
+    # scales around and below 2^-126; outputs stay above it but for a few
+    def shape(x, what, b):
+        x[:, 1] *= size
+    c = Case(D + bits, lens, 2 * G, 2, D, bits, 16, nq=nq, shape=shape)
+    c.check(c.run(), norm=4e-3)
