@@ -433,7 +433,8 @@ struct Converter {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const bool nan = bad >> j & 1;
-        const float s = ok && !nan ? bf16_lo(words[i][j]) * (down * 0x1p24f) : 0.f;
+        // (down may be 2^118: its product with 2^24 is no float)
+        const float s = ok && !nan ? bf16_lo(words[i][j]) * down * 0x1p24f : 0.f;
         const float b = ok && !nan ? bf16_hi(words[i][j]) * down : 0.f;
         uint32_t sb = pack_f16(s, b);
         if (kv == 0) {

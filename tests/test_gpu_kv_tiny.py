@@ -44,3 +44,15 @@ def test_attention_over_tiny_values(lens, nq, G, size, D, bits):
         x[:, 1] *= size
     c = Case(D + bits, lens, 2 * G, 2, D, bits, 16, nq=nq, shape=shape)
     c.check(c.run(), norm=4e-3)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("size", [2.0 ** -112, 2.0 ** -116])
+def test_many_rows_over_tiny_values(size, D, bits):
+    # 560 rows a request: the kernel for many rows
+    def shape(x, what, b):
+        x[:, 1] *= size
+    c = Case(D + bits, [2000, 65], 16, 2, D, bits, 16, nq=70, shape=shape)
+    assert c.rows_kernel() == 2
+    c.check(c.run(), norm=4e-3)
