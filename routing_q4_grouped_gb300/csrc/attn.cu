@@ -18,19 +18,25 @@
 //    z = 128 or 8. (Uncentred, the sum of w c and the sum of w b / s nearly cancel over a
 //    long context, and the tensor cores' truncating sums show: at 131071 tokens the
 //    output's error against 64 bits was 0.0019 instead of 0.0017.) The values' scale is
-//    taken into the weights, rounded to fp16 once, w = fp16(p s), and used for codes and
+//    taken into the weights, rounded to fp16 once, w = fp16(p s / u), and used for codes and
 //    biases alike, so that the rounding stays relative to the value:
-//      sum_t p_t v_t = sum_t w_t (c_t - z) + sum_t w_t (b_t / s_t + z).
+//      sum_t p_t v_t = u (sum_t w_t (c_t - z) + sum_t w_t (b_t / s_t + z)).
+//    u is a power of two near the scales, one per group of the head, since a group has
+//    its own sums: a small group beside a large one keeps its bits. It moves with the
+//    scales (the sums are fp32 and move along). A step in which one group's scales differ
+//    by more than 2^12, or that holds a scale that is 0, subnormal or not finite, takes
+//    the same sums with w as two bf16 (16 bits and fp32's range) and biases in fp32, so
+//    large values of little weight cost the others nothing.
 //  * Tokens are the rows (M) of the products and queries the columns (N = 8), so
 //    that 8 rows fill the tensor core: X^T = K Q^T, then O^T = V^T P^T. The
 //    products' own register layouts let a thread read 16 (keys) or 8 (values)
 //    neighbouring codes of a token at once; P is transposed between the two
 //    products by one 8x8 register transpose per 8 tokens and group.
-// q' and p s are fp16: q' is the query scaled by a power of two so that its row's
-// largest element is near 2^12, p s is multiplied by a factor f of the row that keeps
-// its largest p s near 1, so neither leaves fp16's range and both keep 11 bits (one
-// rounding of 2^-11 for the weights; bf16 queries are exact above 2^-26 of their
-// row's largest element). Logits, maxima, sums and outputs are fp32.
+// q' and w are fp16: q' is the query scaled by a power of two so that its row's largest
+// element is near 2^12; p <= 2^8 and s / u < 2^7, so neither leaves fp16's range (one
+// rounding of 2^-11 for weights above 2^-14 units, less for smaller ones; bf16 queries
+// are exact above 2^-26 of their row's largest element). Logits, maxima, sums and outputs
+// are fp32.
 //
 // Measured (D = 128, 32 query heads on 8 key/value heads, join included): one request of
 // 131071 tokens, 8 bits, 54 us, 5.3 TB/s, 78 % of the copy's bandwidth; 64 requests of
@@ -75,6 +81,22 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same with bf16 operands.
+__device__ __forceinline__ void mma16816_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two small whole numbers, exact in both types.
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t v) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return pack_bf16(f.x, f.y);
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -165,14 +187,98 @@ struct Warp {
   float m[NT][2], l[NT][2];
   float o[NT][G::J][4][4];        // O^T: group, tile of 16 elements
   float ob[NT][G::J][2];          // sum of w * (bias / scale + z)
-  float e[NT][2], f[NT][2];       // f = 2^-e: p s f stays below 2^15
-  float top_x[NT][2], top_ps[NT][2];   // m + 8, m + e + 14: the bounds of a logit and of log2(p s) + m
+  float top_x[NT][2];             // m + 8: the bound of a logit
+  // o and ob of group j are in units of a power of two near the values' scales. Its bounds
+  // as packed words (as of a value word: scale in the low half, bias in the high half, their
+  // exponents alone), and the largest exponent so far. The same in all lanes.
+  uint32_t low[G::J], high[G::J], seen[G::J];
 
-  // The scale that a group's weights take: a constant group (scale 0, codes 0) may have
-  // any, and takes one near its bias.
-  __device__ __forceinline__ static float value_scale(uint32_t word) {
-    const float s = bf16_lo(word);
-    return s != 0.f ? s : fmaxf(fabsf(bf16_hi(word)), 0x1p-60f);
+  static constexpr uint32_t kWindow = 6;          // scales within 2^-6 .. 2^6 of the unit,
+  static constexpr uint32_t kBias = 24;           // biases below 2^24 units (bf16 groups have 2^23)
+  __device__ __forceinline__ void set_unit(int j, uint32_t field) {
+    low[j] = (field - kWindow) << 7;
+    high[j] = (field + kWindow) << 7 | min(field + kBias, 254u) << 23;
+    seen[j] = max(seen[j], field + kBias);
+  }
+  __device__ __forceinline__ uint32_t unit_field(int j) const { return (low[j] >> 7) + kWindow; }
+  __device__ __forceinline__ float unit(int j) const {
+    return __uint_as_float((low[j] << 16) + (kWindow << 23));
+  }
+  __device__ __forceinline__ float per_unit(int j) const {
+    return __uint_as_float(((254u - kWindow) << 23) - (low[j] << 16));
+  }
+
+  // Whether a value word of a token is not what the plain step takes: a normal scale and a
+  // bias in the window of its group's unit.
+  template <bool MASK>
+  __device__ __forceinline__ bool outside(const uint32_t (&vw)[G::TB][2][G::J], int tok0,
+                                          const int (&top)[G::TB], int g) const {
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < G::J; ++j) {
+      uint32_t lo = low[j], hi = high[j];
+#pragma unroll
+      for (int b = 0; b < G::TB; ++b)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (MASK && tok0 + 16 * b + 8 * r + g >= top[b]) continue;
+          const uint32_t e = vw[b][r][j] & 0x7F807F80u;
+          lo = min_u16x2(lo, e);
+          hi = max_u16x2(hi, e);
+        }
+      odd |= lo != low[j] || hi != high[j];
+    }
+    return odd;
+  }
+
+  // Moves the units of the groups whose scales left the window, and what has been summed up
+  // along with them. True if no units suit this step: a group's scales span more than the
+  // window, or are 0, subnormal or not finite, or a bias is far above them.
+  __device__ __forceinline__ bool refer(const uint32_t (&vw)[G::TB][2][G::J], int tok0,
+                                        const int (&top)[G::TB], int g) {
+    bool wide = false;
+#pragma unroll
+    for (int j = 0; j < G::J; ++j) {
+      uint32_t hi = 0, lo = 255, bias = 0;
+      bool odd = false;
+#pragma unroll
+      for (int b = 0; b < G::TB; ++b)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (tok0 + 16 * b + 8 * r + g >= top[b]) continue;
+          uint32_t s = vw[b][r][j] >> 7 & 255u, z = vw[b][r][j] >> 23 & 255u;
+          odd |= s == 0 || s == 255u || z == 255u;
+          if (vw[b][r][j] & 0x7Fu) s = max(s, 1u);            // (subnormal: below 2^-126)
+          if (s < 255u) hi = max(hi, s);
+          if (s > 0) lo = min(lo, s);
+          if (z < 255u) bias = max(bias, z);
+        }
+      hi = __reduce_max_sync(kAll, hi);
+      lo = __reduce_min_sync(kAll, lo);
+      bias = __reduce_max_sync(kAll, bias);
+      // what is summed up stays finite with a unit at most 2^60 below all it was made of
+      seen[j] = max(seen[j], max(hi, bias));
+      const uint32_t old = unit_field(j);
+      uint32_t to = old;
+      if (hi > 0 && (hi > to + kWindow || lo + kWindow < to)) to = min(hi, lo + kWindow);
+      to = min(max(max(to, seen[j] > 61u ? seen[j] - 60u : 1u), 7u), 247u);
+      odd |= lo + kWindow < to || hi > to + kWindow || bias > to + kBias;
+      wide |= __any_sync(kAll, odd);
+      if (to == old) continue;
+      const int by = min(max(static_cast<int>(old) - static_cast<int>(to), -126), 127);
+      const float f = __uint_as_float(static_cast<uint32_t>(127 + by) << 23);
+      set_unit(j, to);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) ob[n][j][c] *= f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[n][j][u][i] *= f;
+      }
+    }
+    return wide;
   }
 
   __device__ __forceinline__ static void load_words(const uint8_t* p, uint32_t (&w)[G::J]) {
@@ -187,22 +293,31 @@ struct Warp {
     }
   }
 
+  // The value words of tokens g and g + 8 of each block.
+  __device__ __forceinline__ static void load_value_words(const uint8_t* st, int g,
+                                                          uint32_t (&vw)[G::TB][2][G::J]) {
+#pragma unroll
+    for (int b = 0; b < G::TB; ++b)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        load_words(st + b * G::kBlock + 2 * G::kCodes + G::kWords + (8 * r + g) * (G::J * 4), vw[b][r]);
+  }
+
   // Columns 2t, 2t+1 of this thread (queries); rows lane/4 and lane/4 + 8 (tokens).
+  // `fresh`: the piece's first step of this warp.
   template <bool MASK>
   __device__ __forceinline__ void step(const uint8_t* st, int tok0, const int (&top)[G::TB], int g,
-                                       uint32_t key_off, uint32_t value_off) {
+                                       uint32_t key_off, uint32_t value_off, bool fresh) {
     float x[G::TB][NT][4];
-    uint32_t vw[G::TB][2][G::J];            // value words of tokens g, g + 8
+    uint32_t vw[G::TB][2][G::J];
+    load_value_words(st, g, vw);
 #pragma unroll
     for (int b = 0; b < G::TB; ++b) {
       const uint8_t* kc = st + b * G::kBlock;
       const uint8_t* words = kc + 2 * G::kCodes + g * (G::J * 4);
       uint32_t kw[2][G::J];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        load_words(words + r * (8 * G::J * 4), kw[r]);
-        load_words(words + G::kWords + r * (8 * G::J * 4), vw[b][r]);
-      }
+      for (int r = 0; r < 2; ++r) load_words(words + r * (8 * G::J * 4), kw[r]);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -254,23 +369,14 @@ struct Warp {
       }
     }
     // A row's reference m is any value near its largest logit, so that weights may
-    // pass 1 by 2^8, and e any value near its largest log2(p s); both move only when
-    // a logit leaves these bounds.
+    // pass 1 by 2^8; it moves only when a logit leaves that bound.
     bool grow = false;
-    float es[G::TB][2];                       // exponent of a token's largest scale
 #pragma unroll
     for (int b = 0; b < G::TB; ++b) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int tok = tok0 + 16 * b + 8 * r + g;
         const bool any = !MASK || tok < top[b];
-        float big = 0.f;
-#pragma unroll
-        for (int j = 0; j < G::J; ++j) {
-          if (MASK && !any) vw[b][r][j] = 0;
-          big = fmaxf(big, fabsf(value_scale(vw[b][r][j])));
-        }
-        es[b][r] = static_cast<float>(static_cast<int>(__float_as_uint(big) >> 23) - 127);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -278,11 +384,24 @@ struct Warp {
             float& v = x[b][n][2 * r + c];
             v *= row_scale[n][c];
             if (MASK && !(any && tok < lim[n][c])) v = -INFINITY;
-            grow |= v > top_x[n][c] || v + es[b][r] > top_ps[n][c];
+            grow |= v > top_x[n][c];
           }
       }
     }
-    if (__any_sync(kAll, grow)) rescale(x, es);
+    if (fresh) {
+      // units from one token's scales, so that the search is seldom needed
+#pragma unroll
+      for (int j = 0; j < G::J; ++j) {
+        const uint32_t s = __shfl_sync(kAll, vw[0][0][j], 0) >> 7 & 255u;
+        if (tok0 < top[0] && s > 0 && s < 255u) set_unit(j, min(max(s, 7u), 247u));
+      }
+    }
+    bool wide = false;
+    const bool odd = outside<MASK>(vw, tok0, top, g);
+    if (__any_sync(kAll, grow || odd)) {
+      if (__any_sync(kAll, odd)) wide = refer(vw, tok0, top, g);
+      rescale(x);
+    }
     // weights
 #pragma unroll
     for (int b = 0; b < G::TB; ++b)
@@ -295,38 +414,70 @@ struct Warp {
           x[b][n][i] = p;
           l[n][i & 1] += p;
         }
-    // O^T += V^T P^T
+    if (wide) {
+      values<true>(st, vw, x, value_off);
+      return;
+    }
+    if (MASK) {                                  // a scale of one unit for what is not there
+#pragma unroll
+      for (int b = 0; b < G::TB; ++b)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < G::J; ++j)
+            if (tok0 + 16 * b + 8 * r + g >= top[b]) vw[b][r][j] = unit_field(j) << 7;
+    }
+    values<false>(st, vw, x, value_off);
+  }
+
+  // O^T += V^T P^T
+  template <bool WIDE>
+  __device__ __forceinline__ void values(const uint8_t* st, const uint32_t (&vw)[G::TB][2][G::J],
+                                         const float (&x)[G::TB][NT][4], uint32_t value_off) {
 #pragma unroll
     for (int b = 0; b < G::TB; ++b) {
-      float pf[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pf[n][i] = x[b][n][i] * f[n][i & 1];
       const uint8_t* vc = st + b * G::kBlock + G::kCodes;
 #pragma unroll
       for (int j = 0; j < G::J; ++j) {
-        uint32_t pb[NT][2];
+        uint32_t pb[NT][2], pl[NT][2];
+        const float inverse = per_unit(j);
+        constexpr float kZ = BITS == 8 ? 128.f : 8.f;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float s = value_scale(vw[b][r][j]), bias = bf16_hi(vw[b][r][j]);
-          // bias / s with one correction step: exact where the quotient is a float. (The
-          // approximate reciprocal takes numbers below 2^-126 as 0: tiny scales are divided
-          // 2^100 times as large, and their biases are no larger than 2^17 scales.)
-          const float up = fabsf(s) < 0x1p-100f ? 0x1p100f : 1.f;
-          const float su = s * up, bu = bias * up;
-          float inv;
-          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(su));
-          float ratio = bu * inv;
-          ratio = fmaf(fmaf(-ratio, su, bu), inv, ratio) + (BITS == 8 ? 128.f : 8.f);
+          const float s = bf16_lo(vw[b][r][j]), bias = bf16_hi(vw[b][r][j]);
+          const float su = s * inverse;
+          if (!WIDE) {
+            // bias / s with one correction step: exact where the quotient is a float
+            float inv;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+            float ratio = bias * inv;
+            ratio = fmaf(fmaf(-ratio, s, bias), inv, ratio) + kZ;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint32_t w2 = pack_f16(pf[n][2 * r] * s, pf[n][2 * r + 1] * s);
-            pb[n][r] = transpose8x8(w2);
-            const float2 wf = __half22float2(*reinterpret_cast<const __half2*>(&w2));
-            // (a bias may be NaN: no product with rows that do not see it)
-            if (!MASK || x[b][n][2 * r] != 0.f) ob[n][j][0] = fmaf(wf.x, ratio, ob[n][j][0]);
-            if (!MASK || x[b][n][2 * r + 1] != 0.f) ob[n][j][1] = fmaf(wf.y, ratio, ob[n][j][1]);
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t w2 = pack_f16(x[b][n][2 * r] * su, x[b][n][2 * r + 1] * su);
+              pb[n][r] = transpose8x8(w2);
+              const float2 wf = __half22float2(*reinterpret_cast<const __half2*>(&w2));
+              ob[n][j][0] = fmaf(wf.x, ratio, ob[n][j][0]);
+              ob[n][j][1] = fmaf(wf.y, ratio, ob[n][j][1]);
+            }
+          } else {
+            // any scale: weights as two bf16 each (16 bits, fp32's range), the rest in fp32;
+            // nothing of a token reaches a row that gives it no weight
+            const float rest = fmaf(s, kZ, bias) * inverse;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float w[2], low[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float p = x[b][n][2 * r + c];
+                const bool none = p == 0.f;
+                w[c] = none ? 0.f : p * su;
+                low[c] = w[c] - __bfloat162float(__float2bfloat16_rn(w[c]));
+                if (!none) ob[n][j][c] = fmaf(p, rest, ob[n][j][c]);
+              }
+              pb[n][r] = transpose8x8(pack_bf16(w[0], w[1]));
+              pl[n][r] = transpose8x8(pack_bf16(low[0], low[1]));
+            }
           }
         }
         // 8 codes of tokens 2t, 2t+1, 2t+8, 2t+9: elements 64 j + 8 g ..
@@ -367,59 +518,53 @@ struct Warp {
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma16816(o[n][j][2 * h], a[0], pb[n][0], pb[n][1]);
-            mma16816(o[n][j][2 * h + 1], a[1], pb[n][0], pb[n][1]);
+            if (!WIDE) {
+              mma16816(o[n][j][2 * h], a[0], pb[n][0], pb[n][1]);
+              mma16816(o[n][j][2 * h + 1], a[1], pb[n][0], pb[n][1]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t c[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[i] = f16x2_to_bf16x2(a[k][i]);
+                mma16816_bf16(o[n][j][2 * h + k], c, pb[n][0], pb[n][1]);
+                mma16816_bf16(o[n][j][2 * h + k], c, pl[n][0], pl[n][1]);
+              }
+            }
           }
         }
       }
     }
   }
 
-  // Moves the rows' m to their largest logit and e to their largest log2(p s), and
-  // what has been summed up along with them.
-  __device__ __forceinline__ void rescale(const float (&x)[G::TB][NT][4],
-                                          const float (&es)[G::TB][2]) {
+  // Moves the rows' m to their largest logit, and what has been summed up along with it.
+  __device__ __forceinline__ void rescale(const float (&x)[G::TB][NT][4]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float keep[2], down[2];
+      float keep[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float mx = -INFINITY, ux = -INFINITY;
+        float mx = -INFINITY;
 #pragma unroll
         for (int b = 0; b < G::TB; ++b)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            mx = fmaxf(mx, x[b][n][2 * r + c]);
-            ux = fmaxf(ux, x[b][n][2 * r + c] + es[b][r]);
-          }
+          for (int r = 0; r < 2; ++r) mx = fmaxf(mx, x[b][n][2 * r + c]);
         mx = max_over_rows8(mx);
-        ux = max_over_rows8(ux);
-        keep[c] = down[c] = 1.f;
-        if (mx == -INFINITY) continue;          // nothing seen yet
-        const bool first = m[n][c] == -INFINITY;
-        const float mn = fmaxf(m[n][c], mx);
-        // (a whole exponent, so that f is a power of two and 1/f undoes it exactly; f times
-        // a weight of 2^8 is still a float)
-        const float eu = fminf(fmaxf(ceilf(ux - mn), -118.f), 126.f);
-        const float en = first ? eu : fmaxf(e[n][c], eu);
-        keep[c] = mn == m[n][c] ? 1.f : exp2_approx(m[n][c] - mn);
-        const float fn = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(en)) << 23);
-        down[c] = first ? 0.f : keep[c] * (fn / f[n][c]);
-        m[n][c] = mn;
-        e[n][c] = en;
-        f[n][c] = fn;
-        top_x[n][c] = mn + 8.f;
-        top_ps[n][c] = mn + en + 14.f;
+        keep[c] = 1.f;
+        if (!(mx > m[n][c])) continue;
+        keep[c] = exp2_approx(m[n][c] - mx);    // (0 from -inf on, where nothing is summed up)
+        m[n][c] = mx;
+        top_x[n][c] = mx + 8.f;
         l[n][c] *= keep[c];
       }
 #pragma unroll
       for (int j = 0; j < G::J; ++j) {
-        ob[n][j][0] *= down[0];
-        ob[n][j][1] *= down[1];
+        ob[n][j][0] *= keep[0];
+        ob[n][j][1] *= keep[1];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[n][j][u][i] *= down[i & 1];
+          for (int i = 0; i < 4; ++i) o[n][j][u][i] *= keep[i & 1];
       }
     }
   }
@@ -693,16 +838,15 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
       w.lim[n][c] = rc < n_rows ? limit(rc) : t1;
       w.m[n][c] = -INFINITY;
       w.l[n][c] = 0.f;
-      w.e[n][c] = 0.f;
-      w.f[n][c] = 1.f;
-      w.top_x[n][c] = w.top_ps[n][c] = -INFINITY;
+      w.top_x[n][c] = -INFINITY;
     }
   }
+#pragma unroll
+  for (int j = 0; j < G::J; ++j) w.seen[j] = 0, w.set_unit(j, 127), w.seen[j] = 0;
   int low = t1;                                // tokens that every row of the tile sees
 #pragma unroll
   for (int n = 0; n < NT; ++n) low = min(low, min(w.lim[n][0], w.lim[n][1]));
   low = __reduce_min_sync(kAll, low);
-
 
   const uint32_t key_off = G::key_lane(g, t), value_off = G::value_lane(g, t);
   int stage = 0;
@@ -721,9 +865,9 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
     for (int i = 0; i < G::TB; ++i) top[i] = gone >> i & 1 ? 0 : t1;
     const uint8_t* st = ring + stage * G::kStage;
     if (tok0 + kStep <= low && gone == 0)
-      w.template step<false>(st, tok0, top, g, key_off, value_off);
+      w.template step<false>(st, tok0, top, g, key_off, value_off, s == warp);
     else
-      w.template step<true>(st, tok0, top, g, key_off, value_off);
+      w.template step<true>(st, tok0, top, g, key_off, value_off, s == warp);
     __syncwarp();                              // the stage may be overwritten
     stage = stage == G::kStages - 1 ? 0 : stage + 1;
   }
@@ -740,11 +884,11 @@ __global__ void __launch_bounds__(kThreads, split_blocks_per_sm(D, BITS, NT))
     for (int c = 0; c < 2; ++c) {
       const int r = 8 * n + 2 * t + c;
       const float l = sum_over_rows8(w.l[n][c]);
-      const float up = 1.f / w.f[n][c];
       if (g == 0) sml[warp * 8 * NT + r] = make_float2(w.m[n][c], l);
 #pragma unroll
       for (int j = 0; j < G::J; ++j) {
         const float ob = sum_over_rows8(w.ob[n][j][c]);
+        const float up = w.unit(j);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           constexpr float kOdd = BITS == 4 ? 0.0625f : 1.f;
