@@ -14,16 +14,17 @@
 // one fp16 fma with 2^24 s, with one rounding of 2^-11.
 //
 // fp16's range. Queries are divided by the power of two under their row's largest
-// element. The keys and the values of each 32 tokens are divided by powers of two, 2^eK
-// and 2^eV, 2^8 above their largest magnitude (so 2^24 s fits, and what is 2^-8 of the
-// largest is still a normal number); eK goes into the logits' factor, and 2^eV into the
-// weights' exponent: P' = exp2(x - m + eV - E) with a running E per row, so P' stays
-// near 1 whatever the values' size. A tile with tokens that differ by more than 2^6
-// within 32 takes one exponent per token (the same formulas with a factor per
-// column), as does one with a NaN group or a page outside the cache.
+// element, the keys of each 32 tokens by one over their largest magnitude, which goes into
+// the logits' factor. A tile with keys that differ by more than 2^6 within 32 tokens takes
+// one exponent per key (the same formulas with a factor per column).
+// Values are divided by a power of two per group of the head and piece, since a group has
+// its own columns of O: it is found from the piece's first tile and undone when the
+// outputs are written, so groups of any ratio keep their bits. A tile in which a group of a
+// token is outside the window in which fp16 rounds it by 2^-12 of its size or better is
+// multiplied as bf16, weights and values (2^-9 each, fp32's range).
 //
 // The row maximum is not looked for tile by tile: m is only a reference, any value
-// near the largest logit does. All P' are positive, so a row whose tile sums to less
+// near the largest logit does. All weights are positive, so a row whose 32 columns sum to less
 // than 2^15 held no weight near fp16's end and m stands; otherwise (and at a row's
 // first tile) the tile's logits are read again for their maximum, m moves there and
 // O and l follow. That leaves one fma, one exp2, one addition and half a conversion
@@ -71,9 +72,23 @@ constexpr int kMmaWarp = 11, kPageWarp = 15;
 __host__ __device__ constexpr bool is_conv_warp(int warp) { return warp >= kSoftWarps && warp % 4 != 3; }
 __host__ __device__ constexpr int conv_index(int warp) { return warp - 8 - (warp > 11) - (warp > 15); }
 constexpr int kMetaRing = 4;
-constexpr int kMaxSpread = 6;          // exponents of a tile's tokens that share one power of two
+constexpr int kMaxSpread = 6;          // exponents of a tile's keys that share one power of two
 constexpr uint32_t kTmemCols = 512;
 constexpr uint8_t kDead = 0x80;        // token flag: its page is outside the cache
+
+// Operands are divided so that the largest 2^24 scale is a finite fp16 (scale <= largest
+// magnitude / 2^(BITS - 1)): keys by 2^kKeyRoom above the power of two under their largest,
+// values by 2^kValueRoom above their group's.
+template <int BITS>
+constexpr int kKeyRoom = BITS == 8 ? 2 : 6;
+template <int BITS>
+constexpr uint32_t kValueRoom = BITS == 8 ? 1 : 5;
+// A group's values may be up to 2^kAbove larger than the piece's first tokens suggested, and
+// 2^kWindow smaller than that: there fp16's subnormals round them by 2^-12 of the group's size.
+template <int BITS>
+constexpr uint32_t kAbove = BITS == 8 ? 3 : 2;
+template <int BITS>
+constexpr uint32_t kWindow = BITS == 8 ? 11 : 7;
 
 template <int D>
 struct RowGeo {
@@ -102,15 +117,22 @@ struct RowGeo {
 template <int D>
 struct alignas(16) Meta {
   static constexpr int J = RowGeo<D>::J, TT = RowGeo<D>::TT;
-  uint16_t vs[J][TT], vb[J][TT];       // values: scale * 2^24, bias (fp16, divided by 2^e)
-  uint32_t ksb[J][TT];                 // keys: the same, bias in the high half
-  float kf[TT];                        // 2^eK of each token (slow tiles)
-  float ve[TT];                        // eV of each token (slow tiles)
+  uint16_t vs[J][TT], vb[J][TT];       // values: scale * 2^24, bias (fp16, divided)
+  uint32_t ksb[J][TT];                 // keys: as vs and vb, bias in the high half
+  float kf[TT];                        // divisor of each token's key (slow tiles)
   uint8_t flag[TT];                    // bit j: value group j is NaN; kDead
-  // of each run of 32 tokens (other tiles), and whether its keys or values need more
-  float run_kf[4], run_ve[4];
-  int slow[2][4];
+  float run_kf[4];                     // of each run of 32 tokens (other tiles)
+  // of each run: keys, values need the slow path; values outside the window of fp16
+  alignas(8) uint8_t slow[2][4];
+  alignas(4) uint8_t wide[4];
+  uint32_t units;                      // exponent fields of the value groups' divisors
 };
+
+// Whether a tile's values are multiplied as bf16.
+template <int D>
+__device__ __forceinline__ bool is_wide(const Meta<D>& m) {
+  return *reinterpret_cast<const uint32_t*>(m.wide) != 0;
+}
 
 struct Ctl {
   uint64_t q_full[2], k_full[3], k_empty[3], v_full[3];
@@ -118,8 +140,11 @@ struct Ctl {
   // of tile t at t % 4: pages found; scales written; products done
   uint64_t base_full[kMetaRing], meta_full[kMetaRing], done[kMetaRing];
   int64_t base[kMetaRing][8];          // byte offset of a 16-token block's key codes
+  const uint8_t* values;               // the cache's first value block
   int32_t words[kMetaRing][8];         // from there to its words; -1: no such block (its codes
                                        // are read from the cache's start and multiplied by 0)
+  uint32_t run_top[2][4];              // of a piece's first tile: largest exponents of each run
+  uint32_t units;                      // D = 256: the piece's, for the second warpgroup
   uint32_t tmem_base;
   int abort;
 };
@@ -216,6 +241,7 @@ struct Waiter {
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((128u >> 4) << 24);
 }
+constexpr uint32_t kBothBf16 = 1u << 7 | 1u << 10;     // added: bf16 A and B
 
 // 64 of the reduction (4 steps of 16), issued by one elected lane: A and B in shared memory.
 __device__ __forceinline__ void mma_ss_chunk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -268,7 +294,17 @@ __device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, 
       : "memory");
 }
 
-__device__ __forceinline__ uint32_t exp_field(uint32_t bf16_bits) { return (bf16_bits >> 7) & 255u; }
+// Of a word (scale and bias): whether both are finite; an exponent field above all magnitudes
+// of its group, times 128 (that of 2^(BITS - 126) for zeros and subnormal scales).
+__device__ __forceinline__ bool finite_word(uint32_t word) {
+  return (((word & 0x7F807F80u) + 0x00800080u) & 0x80008000u) == 0;
+}
+__device__ __forceinline__ bool zero_word(uint32_t word) { return (word & 0x7FFF7FFFu) == 0; }
+template <int BITS>
+__device__ __forceinline__ uint32_t group_field(uint32_t word) {
+  const uint32_t u = word & 0x7F807F80u;
+  return max((u & 0xFFFFu) + (BITS << 7), u >> 16);
+}
 __device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z,
@@ -368,6 +404,7 @@ struct Converter {
   Meta<D>* metas;
   uint8_t* smem;
   int cw, lane;
+  uint32_t units;                                    // of the piece's value groups, 8 bits each
   uint32_t words[WU][J];
   uint32_t kr[KU][KW];
   uint32_t vr[VU][8][BITS / 4];
@@ -399,6 +436,39 @@ struct Converter {
       }
     }
   }
+  // The divisors of a piece's value groups from its first tile (`n` seen tokens): the least of
+  // the runs' largest values, so that neither a few large nor a few small tokens decide.
+  __device__ void find_units(int slot, int n, uint32_t parity) {
+#pragma unroll
+    for (int i = 0; i < WU; ++i) {
+      int kv, r;
+      if (!run_of(i, kv, r) || kv == 0) continue;
+      const int tk = 32 * r + lane;
+      const bool ok = tk < n && ctl.words[slot][tk >> 4] >= 0;
+      uint32_t all = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const bool use = ok && finite_word(words[i][j]) && !zero_word(words[i][j]);
+        const uint32_t e = use ? group_field<BITS>(words[i][j]) >> 7 : 0u;
+        all |= min(__reduce_max_sync(kAll, e), 255u) << (8 * j);
+      }
+      if (lane == 0) ctl.run_top[parity][r] = all;
+    }
+    named_bar_sync(4, G::kConvThreads);
+    units = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      uint32_t low = 255u;
+#pragma unroll
+      for (int r = 0; r < TT / 32; ++r) {
+        const uint32_t e = ctl.run_top[parity][r] >> (8 * j) & 255u;
+        if (e) low = min(low, e);
+      }
+      if (low == 255u) low = 127u;                   // (no values but 0)
+      units |= min(low + kAbove<BITS>, 248u) << (8 * j);
+    }
+  }
+
   // Exponents, scales and biases of a tile of `n` seen tokens from the loaded words.
   __device__ void put_meta(Meta<D>& m, int slot, int n) const {
 #pragma unroll
@@ -407,48 +477,58 @@ struct Converter {
       if (!run_of(i, kv, r)) return;
       const int tk = 32 * r + lane;
       const bool ok = tk < n && ctl.words[slot][tk >> 4] >= 0;
-      uint32_t e = 0, bad = 0;
+      const bool dead = tk < n && !ok;               // a page outside the cache would hold it
+      uint32_t bad = 0;
+      if (kv == 0) {
+        uint32_t big = 0;
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const uint32_t se = exp_field(words[i][j]), be = exp_field(words[i][j] >> 16);
-        if (se == 255u || be == 255u)
-          bad |= 1u << j;
-        else
-          e = max(e, max(se ? se + BITS : 0u, be));
-      }
-      if (!ok) e = bad = 0;
-      const uint32_t top = __reduce_max_sync(kAll, e);
-      const uint32_t low = __reduce_min_sync(kAll, e ? e : 255u);
-      // NaN values, and tokens that a page outside the cache would hold
-      const bool odd = __any_sync(kAll, (kv == 1 && bad) || (tk < n && !ok));
-      const bool slow = odd || top > low + kMaxSpread;
-      const uint32_t E = top == 0 ? 127u : min(top, 253u);
-      const uint32_t eu = slow && e ? min(e, 253u) : E;
-      const float down = pow2_field(254u - eu) * 0x1p-8f;
+        for (int j = 0; j < J; ++j) {
+          if (ok && !finite_word(words[i][j]))
+            bad |= 1u << j;
+          else if (ok && !zero_word(words[i][j]))
+            big = max(big, group_field<BITS>(words[i][j]) >> 7);
+        }
+        const uint32_t top = __reduce_max_sync(kAll, big);
+        const uint32_t low = __reduce_min_sync(kAll, big ? big : 255u);
+        const bool slow = __any_sync(kAll, dead) || top > low + kMaxSpread;
+        const uint32_t E = top == 0 ? 127u : min(top, 253u);
+        const uint32_t eu = slow && big ? min(big, 253u) : E;
+        constexpr float kRoom = 1 << kKeyRoom<BITS>;
+        const float down = pow2_field(254u - eu) * (1.f / kRoom);
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const bool nan = bad >> j & 1;
-        // (down may be 2^118: its product with 2^24 is no float)
-        const float s = ok && !nan ? bf16_lo(words[i][j]) * down * 0x1p24f : 0.f;
-        const float b = ok && !nan ? bf16_hi(words[i][j]) * down : 0.f;
-        uint32_t sb = pack_f16(s, b);
-        if (kv == 0) {
-          if (nan) sb = 0x7E000000u;                 // a NaN key: NaN logits
-          m.ksb[j][tk] = sb;
-        } else {
+        for (int j = 0; j < J; ++j) {
+          const bool nan = bad >> j & 1;
+          // (down may be 2^124: its product with 2^24 is no float)
+          const float s = ok && !nan ? bf16_lo(words[i][j]) * down * 0x1p24f : 0.f;
+          const float b = ok && !nan ? bf16_hi(words[i][j]) * down : 0.f;
+          m.ksb[j][tk] = nan ? 0x7E000000u : pack_f16(s, b);      // a NaN key: NaN logits
+        }
+        m.kf[tk] = pow2_field(eu) * kRoom;
+        if (lane == 0) m.run_kf[r] = pow2_field(E) * kRoom;
+        if (lane == 0) m.slow[0][r] = slow;
+      } else {
+        bool out = false;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const uint32_t unit = units >> (8 * j) & 255u;
+          uint32_t word = ok ? words[i][j] : 0u;
+          if (!finite_word(word)) bad |= 1u << j, word = 0u;
+          // (unsigned: too small, or above the unit)
+          out |= !zero_word(word) && (unit << 7) - group_field<BITS>(word) > kWindow<BITS> << 7;
+          const float down = pow2_field(254u - kValueRoom<BITS> - unit);
+          const uint32_t sb = pack_f16(bf16_lo(word) * down * 0x1p24f, bf16_hi(word) * down);
           m.vs[j][tk] = static_cast<uint16_t>(sb);
           m.vb[j][tk] = static_cast<uint16_t>(sb >> 16);
         }
+        m.flag[tk] = static_cast<uint8_t>(bad | (dead ? kDead : 0));
+        const bool slow = __any_sync(kAll, bad != 0 || dead);
+        const bool wide = __any_sync(kAll, out);
+        if (lane == 0) {
+          m.slow[1][r] = slow;
+          m.wide[r] = wide;
+          m.units = units;
+        }
       }
-      if (kv == 0) {
-        m.kf[tk] = pow2_field(eu) * 0x1p8f;
-        if (lane == 0) m.run_kf[r] = pow2_field(E) * 0x1p8f;
-      } else {
-        m.ve[tk] = static_cast<float>(static_cast<int>(eu) - 119);
-        m.flag[tk] = static_cast<uint8_t>(bad | (tk < n && !ok ? kDead : 0));
-        if (lane == 0) m.run_ve[r] = static_cast<float>(static_cast<int>(E) - 119);
-      }
-      if (lane == 0) m.slow[kv][r] = slow;
     }
   }
 
@@ -581,10 +661,49 @@ struct Converter {
     }
   }
 
+  // The same as bf16 from the cache, of a tile of `n` seen tokens. Seldom: not inlined, and
+  // nothing is taken from the caller's registers, so that it costs the loop few of them.
+  static __device__ __noinline__ void put_wide_values(uint8_t* smem, uint32_t tile, int slot, int n) {
+    const Ctl& ctl = *reinterpret_cast<const Ctl*>(smem + G::kOffMeta + kMetaRing * sizeof(Meta<D>));
+    const uint32_t units = reinterpret_cast<const Meta<D>*>(smem + G::kOffMeta)[slot].units;
+    const int cw = conv_index(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int th = cw % TH, tg = lane & 7, d0 = cw / TH * 32 + (lane >> 3) * 8;
+    const int t0 = th * 64 + tg * 8;
+    const int to_words = ctl.words[slot][t0 >> 4];
+    const uint8_t* block = ctl.values + ctl.base[slot][t0 >> 4];
+#pragma unroll 1
+    for (int u = 0; u < VU; ++u) {
+      const int d = d0 + u * kPieceD, j = d / kKvGroup;
+      const float down = pow2_field(254u - kValueRoom<BITS> - (units >> (8 * j) & 255u));
+      const uint32_t dst = smem_u32(smem) + tile + th * (D * 128) + d * 128 + (tg << 4);
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        uint32_t r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float v[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int t = (t0 & 15) + 2 * k + x;
+            uint32_t word = 0;
+            if (to_words >= 0 && t0 + 2 * k + x < n)
+              word = __ldg(reinterpret_cast<const uint32_t*>(block + to_words + t * (J * 4)) + j);
+            if (!finite_word(word)) word = 0;
+            const uint32_t byte = __ldg(block + t * RB + (d + i) * BITS / 8);
+            const uint32_t code = BITS == 8 ? byte : byte >> (i & 1) * 4 & 15u;
+            v[x] = fmaf(bf16_lo(word), static_cast<float>(code), bf16_hi(word)) * down;
+          }
+          r[k] = pack_bf16(v[0], v[1]);
+        }
+        st_shared_v4((dst ^ (i << 4)) + i * 128, r[0], r[1], r[2], r[3]);
+      }
+    }
+  }
+
   // All tiles of one piece; `tc` counts this block's tiles. What a tile needs from memory
   // is requested as soon as its registers are free, half a tile and more ahead, and its
   // scales are ready before its keys are: no warp waits for another inside a tile.
-  __device__ void run(const Seg& sg, int seen, uint32_t& tc, Waiter& w) {
+  __device__ void run(const Seg& sg, int seen, uint32_t& tc, uint32_t piece, Waiter& w) {
     const auto pages_of = [&](uint32_t t) {
       w.wait(&ctl.base_full[t % kMetaRing], (t / kMetaRing) & 1);
     };
@@ -598,6 +717,7 @@ struct Converter {
     load_words(tc % kMetaRing);
     load_keys(tc % kMetaRing);
     load_values(tc % kMetaRing);
+    find_units(tc % kMetaRing, min(seen - sg.kt0 * TT, TT), piece & 1);
     scales_for(tc, sg.kt0);
     if (sg.kt0 + 1 < sg.kt1) {
       pages_of(tc + 1);
@@ -621,7 +741,10 @@ struct Converter {
         }
       }
       if (tc >= G::KS) w.wait(&ctl.done[(tc - G::KS) % kMetaRing], ((tc - G::KS) / kMetaRing) & 1);
-      put_values(m, G::kOffV + st * G::kTileBytes);
+      if (is_wide(m))
+        put_wide_values(smem, G::kOffV + st * G::kTileBytes, tc % kMetaRing, min(seen - it * TT, TT));
+      else
+        put_values(m, G::kOffV + st * G::kTileBytes);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.v_full[st]);
@@ -641,9 +764,10 @@ struct Softmax {
   uint8_t* smem;
   uint32_t tmem;             // + lane quarter
   int wg, warp, lane;
-  float m, l, E;             // reference of the logits (log2), sum, exponent of O
+  float m, l;                // reference of the logits (log2), sum
   float c;                   // scale2 * 2^(row exponent)
   uint32_t nan;              // value groups that are NaN for this row
+  uint32_t units;            // divisors of the value groups
 
   // This warp's staging: 32 rows of SB bytes, 16-byte pieces permuted by their row, for
   // turning between a thread's own row and neighbouring lanes on one row (which memory
@@ -745,16 +869,19 @@ struct Softmax {
     if (G::kQTmem) tmem_st_wait();
   }
 
-  // This thread's row of O times `up` (NaN for the value groups in `nan`) to memory at
-  // element `dst`, as the output or as a partial result. (D = 256: each warpgroup half of it.)
-  __device__ void store(int64_t dst, bool live, bool output, float up, uint32_t nan_groups) {
+  // This thread's row of O times `up` and the groups' units (NaN for the groups in
+  // `nan_groups`) to memory at element `dst`, as the output or as a partial result. (D = 256: each warpgroup half of it.)
+  __device__ void store(int64_t dst, bool live, bool output, float up, uint32_t nan_groups,
+                        uint32_t group_units) {
     constexpr int kCols = SB / 4, kChunks = D / kCols, kMine = G::kQTmem ? kChunks / 2 : kChunks;
     const int first = G::kQTmem ? wg * kMine : 0;
     const uint32_t lives = __ballot_sync(kAll, live);
     uint8_t* st = stage();
 #pragma unroll 1
     for (int h = first; h < first + kMine; ++h) {
-      const float f = nan_groups >> (h * kCols / kKvGroup) & 1 ? NAN : up;
+      const int j = h * kCols / kKvGroup;
+      const float unit = pow2_field((group_units >> (8 * j) & 255u) + kValueRoom<BITS>);
+      const float f = nan_groups >> j & 1 ? NAN : up * unit;
 #pragma unroll
       for (int k = 0; k < PC / 4; ++k) {
         uint32_t v[16];
@@ -793,17 +920,17 @@ struct Softmax {
     return x;
   }
 
-  // Weights of columns 64 H .. 64 H + 63 (runs 2H and 2H + 1, each with its factor and
-  // offset) into registers, and the runs' sums. The next 16 logits are on their way out of
+  // Weights of columns 64 H .. 64 H + 63 (runs 2H and 2H + 1, each with its factor) into
+  // registers, and the runs' sums. The next 16 logits are on their way out of
   // tensor memory while these are worked on.
   template <bool MASK, int H>
-  __device__ __forceinline__ void weights(uint32_t s_col, const float (&ck)[2], const float (&off)[2],
+  __device__ __forceinline__ void weights(uint32_t s_col, const float (&ck)[2], float off,
                                           int lim, uint32_t (&p)[32], float (&sum)[2]) {
     uint32_t v[2][16];
     tmem_ld_32x32b_x16(tmem + s_col + 64 * H, v[0]);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint64_t ck2 = pack_f32x2(ck[r], ck[r]), off2 = pack_f32x2(off[r], off[r]);
+      const uint64_t ck2 = pack_f32x2(ck[r], ck[r]), off2 = pack_f32x2(off, off);
       uint64_t part[2] = {0, 0};
 #pragma unroll
       for (int h = 2 * r; h < 2 * r + 2; ++h) {
@@ -830,36 +957,28 @@ struct Softmax {
     }
   }
 
-  // Moves m to the largest logit of columns 16 H0 .. and E so that none of their
-  // weights passes 1 (in the lanes that `need` it), and l, O and the tile's weights
-  // already written (columns below 16 H0) along with them.
+  // Moves m to the largest logit of columns 16 H0 .. (in the lanes that `need` it), and l, O
+  // and the tile's weights already written (columns below 16 H0) along with it.
   template <bool SLOW, bool MASK, int H0>
   __device__ __forceinline__ void move(uint32_t s_col, const Meta<D>& t, int lim, bool need, bool first,
                                        uint64_t* pv, uint32_t pv_parity, Waiter& w) {
-    float mx = -INFINITY, ux = -INFINITY;
+    float mx = -INFINITY;
 #pragma unroll 1
     for (int h = H0; h < G::TT / 16; ++h) {
       uint32_t v[16];
       tmem_ld_32x32b_x16(tmem + s_col + 16 * h, v);
       tmem_ld_wait();
       tmem_regs_ready(v);
-      const float ck = c * t.run_kf[h >> 1], ve = t.run_ve[h >> 1];
+      const float ck = c * t.run_kf[h >> 1];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float x = logit<SLOW, MASK>(__uint_as_float(v[i]), ck, t, 16 * h + i, lim);
-        mx = fmaxf(mx, x);
-        ux = fmaxf(ux, x + (SLOW ? t.ve[16 * h + i] : ve));
-      }
+      for (int i = 0; i < 16; ++i)
+        mx = fmaxf(mx, logit<SLOW, MASK>(__uint_as_float(v[i]), ck, t, 16 * h + i, lim));
     }
     float fo = 1.f;
-    if (need && mx > -INFINITY) {
-      const float mn = fmaxf(m, mx);
-      const float u = ux - mn;                      // exponent of the largest contribution
-      const float En = m == -INFINITY ? u : fmaxf(E, u);
-      l *= exp2_approx(m - mn);
-      fo = exp2_approx(m - mn + (E - En));
-      m = mn;
-      E = En;
+    if (need && mx > m) {
+      fo = exp2_approx(m - mx);                     // (0 from -inf on)
+      l *= fo;
+      m = mx;
     }
     if (!__any_sync(kAll, fo != 1.f)) return;
     if (H0 > 0) {
@@ -900,22 +1019,17 @@ struct Softmax {
                                             uint64_t* pv, uint32_t pv_parity, Waiter& w) {
     uint32_t p[32];
     const float2 kf = *reinterpret_cast<const float2*>(&t.run_kf[2 * H]);
-    const float2 ve = *reinterpret_cast<const float2*>(&t.run_ve[2 * H]);
-    float sum[2], d[2];
+    float sum[2];
     const float ck[2] = {c * kf.x, c * kf.y};
     bool need = m == -INFINITY && lim > 64 * H;
 #pragma unroll 1
     for (int round = 0;; ++round) {
       if (__any_sync(kAll, need)) move<false, MASK, 4 * H>(s_col, t, lim, need, first, pv, pv_parity, w);
-      const float ref = m == -INFINITY ? 0.f : m;
-      d[0] = fmaxf(ve.x - E, -60.f);
-      d[1] = fmaxf(ve.y - E, -60.f);
-      const float off[2] = {d[0] - ref, d[1] - ref};
-      weights<MASK, H>(s_col, ck, off, lim, p, sum);
+      weights<MASK, H>(s_col, ck, m == -INFINITY ? 0.f : -m, lim, p, sum);
       need = fmaxf(sum[0], sum[1]) >= 32768.f;
       if (round || !__any_sync(kAll, need)) break;
     }
-    l = fmaf(sum[0], exp2_approx(-d[0]), fmaf(sum[1], exp2_approx(-d[1]), l));
+    l += sum[0] + sum[1];
     tmem_st_32x32b_x16(tmem + s_col + 32 * H, reinterpret_cast<uint32_t(&)[16]>(p[0]));
     tmem_st_32x32b_x16(tmem + s_col + 32 * H + 16, reinterpret_cast<uint32_t(&)[16]>(p[16]));
     tmem_st_wait();
@@ -927,10 +1041,10 @@ struct Softmax {
     if constexpr (G::TT == 128) half_tile<MASK, 1>(s_col, t, lim, first, pv, pv_parity, w);
   }
 
-  // A tile with an exponent per token, NaN groups or missing pages: m always moves to
-  // the maximum, so no weight passes 1 and the weights may overwrite the logits that
-  // have been read.
-  __device__ __forceinline__ void slow_tile(uint32_t s_col, const Meta<D>& t, int lim, bool first,
+  // A tile with an exponent per key, NaN groups, missing pages or values outside the window
+  // (`wide`: weights as bf16): m always moves to the maximum, so no weight passes 1 and the
+  // weights may overwrite the logits that have been read.
+  __device__ __forceinline__ void slow_tile(uint32_t s_col, const Meta<D>& t, int lim, bool wide, bool first,
                                             uint64_t* pv, uint32_t pv_parity, Waiter& w) {
     move<true, true, 0>(s_col, t, lim, true, first, pv, pv_parity, w);
     const float ref = m == -INFINITY ? 0.f : m;
@@ -946,13 +1060,12 @@ struct Softmax {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int col = 16 * h + i + k;
-          const float d = fmaxf(t.ve[col] - E, -60.f);
           const float x = logit<true, true>(__uint_as_float(v[i + k]), 0.f, t, col, lim);
-          wt[k] = exp2_approx(x - ref + d);
-          l = fmaf(wt[k], exp2_approx(-d), l);
+          wt[k] = exp2_approx(x - ref);
+          l += wt[k];
           if (x != -INFINITY) nan |= t.flag[col];
         }
-        p[i / 2] = pack_f16(wt[0], wt[1]);
+        p[i / 2] = wide ? pack_bf16(wt[0], wt[1]) : pack_f16(wt[0], wt[1]);
       }
       tmem_st_32x32b_x8(tmem + s_col + 8 * h, p);
     }
@@ -984,14 +1097,14 @@ struct Softmax {
       w.wait(&ctl.pv_done[0], (pc + nt - 1) & 1);
       tc_fence_after();
       const float2 end = ends[(warp & 3) * 32 + lane];
-      store(dst, live, lone, end.x, __float_as_uint(end.y));
+      store(dst, live, lone, end.x, __float_as_uint(end.y), ctl.units);
       tc_fence_before();
       return;
     }
     m = -INFINITY;
     l = 0.f;
-    E = 0.f;
     nan = 0;
+    units = 0;
     const int lim = !live ? 0 : sg.pre ? sg.ctx : own_limit(a, sg.ctx, r);
     for (int it = 0; it < nt; ++it) {
       const int slot = nqt == 2 ? wg : it & 1;
@@ -1004,10 +1117,10 @@ struct Softmax {
       const uint32_t s_col = G::kColS + G::TT * slot;
       const uint32_t pv_parity = (pc + it - 1) & 1;
       uint64_t* pv = &ctl.pv_done[wg];
-      int slow = t.slow[0][0] | t.slow[0][1] | t.slow[1][0] | t.slow[1][1];
-      if (G::TT == 128) slow |= t.slow[0][2] | t.slow[0][3] | t.slow[1][2] | t.slow[1][3];
-      if (slow)
-        slow_tile(s_col, t, rel, it == 0, pv, pv_parity, w);
+      if (it == 0) units = t.units;
+      const bool wide = is_wide(t);
+      if (*reinterpret_cast<const uint64_t*>(t.slow) != 0 || wide)
+        slow_tile(s_col, t, rel, wide, it == 0, pv, pv_parity, w);
       else if (__all_sync(kAll, rel >= G::TT))
         tile<false>(s_col, t, rel, it == 0, pv, pv_parity, w);
       else
@@ -1023,13 +1136,14 @@ struct Softmax {
     // ---- outputs
     w.wait(&ctl.pv_done[wg], (pc + nt - 1) & 1);
     tc_fence_after();
-    const float up = exp2_approx(E) * (lone ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+    const float up = !lone ? 1.f : l == 0.f ? 0.f : 1.f / l;
     if (live && !lone) a.ml[at] = make_float2(m, l);
     if (G::kQTmem) {
       ends[(warp & 3) * 32 + lane] = make_float2(up, __uint_as_float(nan));
+      if (lane == 0) ctl.units = units;
       named_bar_sync(3, kSoftWarps * 32);
     }
-    store(dst, live, lone, up, nan);
+    store(dst, live, lone, up, nan, units);
     tc_fence_before();
   }
 };
@@ -1063,6 +1177,9 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
       mbar_init(&ctl.done[i], 1);
     }
     mbar_init(&ctl.drain, 1);
+    for (int i = 0; i < kMetaRing; ++i)              // (D = 256 has two runs a tile)
+      for (int r = 0; r < 4; ++r) metas[i].slow[0][r] = metas[i].slow[1][r] = metas[i].wide[r] = 0;
+    ctl.values = a.c.data + static_cast<int64_t>(a.c.Hkv) * a.c.head_bytes;
     ctl.abort = 0;
     fence_mbar_init();
   }
@@ -1098,7 +1215,8 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
     }
   } else if (is_conv_warp(warp) && conv_index(warp) < G::kConvWarps) {
     Converter<D, BITS> cv{a, ctl, metas, smem, conv_index(warp), lane};
-    while (walk.next(a, sg, false)) cv.run(sg, Walk::seen(a, sg), tc, w);
+    for (uint32_t piece = 0; walk.next(a, sg, false); ++piece)
+      cv.run(sg, Walk::seen(a, sg), tc, piece, w);
   } else if (warp == kPageWarp) {
     Pages<D, BITS> pg{a, ctl, lane};
     while (walk.next(a, sg, false)) pg.run(sg, Walk::seen(a, sg), tc, w);
@@ -1111,7 +1229,13 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
     const uint32_t base = smem_u32(smem);
     const uint32_t tmem = __shfl_sync(kAll, ctl.tmem_base, 0);
     uint32_t ks = 0, kp = 0, vs = 0, vp = 0;       // next key and value tile: ring place, parity
-    uint32_t dn = 0, qp[2] = {0, 0}, pp[2] = {0, 0};
+    uint32_t dn = 0, mt = 0, qp[2] = {0, 0}, pp[2] = {0, 0};
+    // whether the next tile's values are bf16 (known with its keys, used with its values)
+    const auto look = [&]() {
+      const bool wide = is_wide(metas[mt]);
+      mt = (mt + 1) % kMetaRing;
+      return wide;
+    };
     const auto logits = [&](int q, int slot) {       // X of query tile q with key tile ks
       __syncwarp();
       const uint32_t x = tmem + G::kColS + G::TT * slot;
@@ -1134,17 +1258,18 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
       mma_commit_elect(&ctl.k_empty[ks]);
       if (++ks == G::KS) ks = 0, kp ^= 1;
     };
-    const auto outputs = [&](int q, int slot, bool first) {   // O of query tile q with value tile vs
+    const auto outputs = [&](int q, int slot, bool first, bool wide) {   // O of query tile q with value tile vs
       w.wait(&ctl.p_full[slot], slot ? pp[1] : pp[0]);
       (slot ? pp[1] : pp[0]) ^= 1;
       tc_fence_after();
       __syncwarp();
       const uint32_t p = tmem + G::kColS + G::TT * slot, o = tmem + G::kColO + q * D;
       const uint64_t v = sdesc_k_sw128(base + G::kOffV + vs * G::kTileBytes);
+      const uint32_t idesc = __any_sync(kAll, wide) ? idesc_o | kBothBf16 : idesc_o;
       if constexpr (G::TT == 128)
-        mma_ts_tile_pair_elect(o, p, p + 32, v, v + D * 128 / 16, idesc_o, !first);
+        mma_ts_tile_pair_elect(o, p, p + 32, v, v + D * 128 / 16, idesc, !first);
       else
-        mma_ts_tile_chunk_elect(o, p, v, idesc_o, !first);
+        mma_ts_tile_chunk_elect(o, p, v, idesc, !first);
       mma_commit_elect(&ctl.pv_done[q]);
     };
     const auto values_done = [&]() {
@@ -1161,36 +1286,42 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
         w.wait(&ctl.q_full[1], qp[1]);
         qp[1] ^= 1;
         tc_fence_after();
+        bool wide = false;
         for (int it = 0; it < nt; ++it) {
           w.wait(&ctl.k_full[ks], kp);
           tc_fence_after();
           logits(0, 0);
+          const bool next = look();
           if (it > 0) {
-            outputs(1, 1, it == 1);
+            outputs(1, 1, it == 1, wide);
             values_done();
           }
+          wide = next;
           logits(1, 1);
           keys_done();
           w.wait(&ctl.v_full[vs], vp);
-          outputs(0, 0, it == 0);
+          outputs(0, 0, it == 0, wide);
         }
-        outputs(1, 1, nt == 1);
+        outputs(1, 1, nt == 1, wide);
         values_done();
       } else {
         tc_fence_after();
+        bool wide = false;
         for (int it = 0; it < nt; ++it) {
           w.wait(&ctl.k_full[ks], kp);
           tc_fence_after();
           logits(0, it & 1);
           keys_done();
+          const bool next = look();
           if (it > 0) {
             w.wait(&ctl.v_full[vs], vp);
-            outputs(0, (it - 1) & 1, it == 1);
+            outputs(0, (it - 1) & 1, it == 1, wide);
             values_done();
           }
+          wide = next;
         }
         w.wait(&ctl.v_full[vs], vp);
-        outputs(0, (nt - 1) & 1, nt == 1);
+        outputs(0, (nt - 1) & 1, nt == 1, wide);
         values_done();
       }
     }
