@@ -1183,6 +1183,13 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
     ctl.abort = 0;
     fence_mbar_init();
   }
+  if (warp == 1) {
+    // After a wait that ran out, conversion goes on with what the ring holds: offsets inside
+    // the cache, whether or not a tile's pages were found.
+    static_assert(kMetaRing * 8 == 32, "a lane each");
+    ctl.base[lane / 8][lane % 8] = 0;
+    ctl.words[lane / 8][lane % 8] = -1;
+  }
   if (warp == kMmaWarp) {
     tmem_alloc(&ctl.tmem_base, kTmemCols);
     tmem_relinquish();
