@@ -960,7 +960,10 @@ __global__ void __launch_bounds__(kJoinThreads<W>) attn_join_kernel(const AttnAr
   const int row = static_cast<int>(at / a.Hq), head = static_cast<int>(at % a.Hq);
   const int hk = head / a.G, b = row / a.nq;
   // (loads that do not wait for each other)
-  const int len = a.own_units || a.own_tiles ? context_len(a, b, false) : 0;
+  // (with max_len = 0 no other kernel looks at the lengths)
+  const bool own = a.own_units || a.own_tiles;
+  const bool report = !own && row % a.nq == 0 && head == 0 && warp % W == 0 && lane == 0;
+  const int len = own || report ? context_len(a, b, report) : 0;
   const int first = a.own_tiles ? a.first[b] : 0;
   const int share = a.pre_blocks || a.own_tiles ? *a.share_out : 1;
   // Parts of each context: `n` of them; the first at p0, the second at p1, then p1 + step, ...
@@ -994,7 +997,7 @@ __global__ void __launch_bounds__(kJoinThreads<W>) attn_join_kernel(const AttnAr
     const int u = hk * a.pre_tiles + r / (8 * a.nt);
     of_split(parts[0], 0, u * a.pre_T, a.pre_T, r);
   }
-  if (a.own_units || a.own_tiles) {
+  if (own) {
     const int r = row % a.nq * a.G + head % a.G;
     if (a.own_units) {
       const int rt = r / a.unit_rows;
