@@ -1130,8 +1130,19 @@ void share_out(int64_t units, int64_t* T, int64_t* share) {
   *share = lined;
 }
 
+// The sizes that a call takes; products of them stay below 2^63.
+bool sizes_allowed(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int64_t max_len,
+                   int64_t prefix_len) {
+  return B >= 0 && nq >= 1 && Hq >= 1 && Hq <= 65535 && Hkv >= 1 && Hkv <= 1024 && Hq % Hkv == 0 &&
+         (D == 64 || D == 128 || D == 256) && max_len >= 0 && max_len <= (1 << 30) &&
+         prefix_len >= 0 && prefix_len <= (1 << 30) && B * nq <= (1 << 24) &&
+         B * nq * Hq <= 0x7FFFFFFF;
+}
+
+// False if the sizes are not allowed or ask for too much work.
 bool make_plan(int64_t B, int64_t nq, int64_t Hq, int64_t Hkv, int D, int max_len, int prefix_len,
                Plan* out) {
+  if (!sizes_allowed(B, nq, Hq, Hkv, D, max_len, prefix_len)) return false;
   Plan p{};
   AttnArgs& a = p.a;
   const int64_t G = Hq / Hkv;
@@ -1256,18 +1267,14 @@ bool bad4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 extern "C" size_t moe_kv_attention_workspace_size(int32_t B, int32_t nq, int32_t Hq, int32_t Hkv,
                                                   int32_t D, int32_t max_len, int32_t prefix_len) {
-  if (B < 0 || nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256) ||
-      max_len < 0 || prefix_len < 0)
-    return 0;
   moeq4::Plan p;
   return moeq4::make_plan(B, nq, Hq, Hkv, D, max_len, prefix_len, &p) ? p.total : 0;
 }
 
 extern "C" int32_t moe_debug_kv_attention_rows(int32_t B, int32_t nq, int32_t Hq, int32_t Hkv,
                                                int32_t D, int32_t max_len, int32_t prefix_len) {
-  if (moe_kv_attention_workspace_size(B, nq, Hq, Hkv, D, max_len, prefix_len) == 0) return -1;
   moeq4::Plan p;
-  moeq4::make_plan(B, nq, Hq, Hkv, D, max_len, prefix_len, &p);
+  if (!moeq4::make_plan(B, nq, Hq, Hkv, D, max_len, prefix_len, &p)) return -1;
   return (p.a.pre_units > 0 ? 1 : 0) | (p.a.own_units > 0 ? 2 : 0);
 }
 
@@ -1279,8 +1286,7 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
     return MOE_ERR_ARG;
   moe_status st = check_kv_cache(c);
   if (st != MOE_OK) return st;
-  if (a->Hq % c->Hkv || a->Hq > 65535 || a->max_len > (1 << 30) || a->prefix_len > (1 << 30) || static_cast<int64_t>(a->B) * a->nq > (1 << 24))
-    return MOE_ERR_SHAPE;
+  if (!sizes_allowed(a->B, a->nq, a->Hq, c->Hkv, c->D, a->max_len, a->prefix_len)) return MOE_ERR_SHAPE;
   if (a->B == 0) return MOE_OK;
   const int64_t pages = (static_cast<int64_t>(a->max_len) + c->page_size - 1) / c->page_size;
   if (!a->q || !a->out || !a->lens || (a->max_len > 0 && !a->table) ||
@@ -1294,9 +1300,7 @@ extern "C" moe_status moe_kv_attention(const moe_kv_attn* a, const moe_kv_cache*
       bad4(a->prefix_table) || a->q_row % 8 || a->q_head % 8 || a->out_row % 8 || a->out_head % 8)
     return MOE_ERR_ALIGN;
   Plan p;
-  if (static_cast<int64_t>(a->B) * a->nq * a->Hq > 0x7FFFFFFF ||
-      !make_plan(a->B, a->nq, a->Hq, c->Hkv, c->D, a->max_len, a->prefix_len, &p))
-    return MOE_ERR_SHAPE;
+  if (!make_plan(a->B, a->nq, a->Hq, c->Hkv, c->D, a->max_len, a->prefix_len, &p)) return MOE_ERR_SHAPE;
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
   if ((st = check_device()) != MOE_OK) return st;
   AttnArgs& k = p.a;
