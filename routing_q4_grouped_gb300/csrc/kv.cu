@@ -567,14 +567,13 @@ extern "C" moe_status moe_rope_phases(uint64_t* phase, int32_t rot, double base,
   double lo = 0.0, hi = 0.0;
   if (scaling == MOE_ROPE_BANDS) {
     lo = std::max(0.0, std::floor(pair_of(fast)));
-    hi = std::min(rot - 1.0, std::ceil(pair_of(slow)));
-    if (hi <= lo) hi = lo + 0.001;
+    hi = std::min(rot - 1.0, std::ceil(pair_of(slow)));   // (0 or less: every pair is slow)
   }
   for (int i = 0; i < rot / 2; ++i) {
     double f = std::pow(base, -2.0 * i / rot);
     if (scaling == MOE_ROPE_LINEAR) f /= factor;
     if (scaling == MOE_ROPE_BANDS) {
-      const double slowed = std::min(1.0, std::max(0.0, (i - lo) / (hi - lo)));
+      const double slowed = i >= hi ? 1.0 : i <= lo ? 0.0 : (i - lo) / (hi - lo);
       f = f * (1.0 - slowed) + f / factor * slowed;
     }
     phase[i] = static_cast<uint64_t>(std::rint(std::ldexp(f / kTurn, 64)));
