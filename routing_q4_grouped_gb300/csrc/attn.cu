@@ -1097,15 +1097,23 @@ struct Plan {
   size_t ml, first, total;   // workspace: offsets of the (m, l) pairs and the tile sums, size
 };
 
+// Sizes shares and grids only: no block waits for another, so a device with fewer
+// multiprocessors gives the same results.
 constexpr int kSMs = 152;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The row kernel is taken from 64 query rows of a key/value head on, if there is enough to
-// multiply: it does 700 to 1050 TFLOP/s where the split kernel does 40 to 180, but takes
-// about 20 us longer to get going. Measured, split and row kernel: 512 rows, D = 256, 64
-// tokens (0.07 GFLOP) 14 and 36 us, 1024 tokens (1.1) 33 and 26 us; 4096 rows, D = 128, 1024
-// tokens (4.3) 97 and 45 us.
+// multiply: it takes longer to get going and then multiplies faster. Measured, one request, 8
+// bits, 2 key/value heads (4 bits alike), split and row kernel, us:
+//   GFLOP              0.25         0.5          1            2            4
+//   D 64,   64 rows    11.6  14.6   13.9  16.8   20.4  21.0   23.1  29.9   36.2  48.8
+//   D 64,  256 rows    15.6  15.1   14.4  15.6   17.6  16.4   25.4  18.9   36.3  21.9
+//   D 128,  64 rows    13.3  17.0   14.8  17.5   18.0  19.4   27.2  24.1   36.9  34.0
+//   D 128, 256 rows    13.5  19.8   20.4  19.9   23.0  20.3   27.5  20.7   36.7  24.1
+//   D 256,  64 rows    13.8  18.8   16.2  19.2   21.1  20.8   29.9  23.3   42.8  30.9
+//   D 256, 1024 rows                13.8  20.3   18.3  21.0   31.2  22.4   44.0  24.7
+// At D = 64 a unit of 64 rows is a quarter full, and the split kernel stays ahead of it.
 constexpr int64_t kRowKernelRows = 64;
 constexpr double kRowKernelFlops = 1e9;
 bool row_kernel_pays(int64_t rows, int64_t heads, int D, int64_t len) {
@@ -1251,12 +1259,6 @@ cudaError_t launch(const AttnArgs& a, const Plan& p, cudaStream_t s) {
   if (heads <= kSMs) return join(attn_join_kernel<D, 8>, 8, heads);
   if (heads <= kSMs * 8) return join(attn_join_kernel<D, 4>, 4, heads);
   return join(attn_join_kernel<D, 1>, kWarps, ceil_div(heads, kWarps));
-}
-
-bool rows_disjoint(int64_t row, int64_t head, int64_t T, int64_t H, int64_t D) {
-  const bool head_in = (H == 1 || head >= D) && (T == 1 || row >= (H - 1) * head + D);
-  const bool row_in = (T == 1 || row >= D) && (H == 1 || head >= (T - 1) * row + D);
-  return head_in || row_in;
 }
 
 bool bad16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }

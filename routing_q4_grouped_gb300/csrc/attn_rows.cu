@@ -261,14 +261,6 @@ __device__ __forceinline__ void mma_ss_chunk(uint32_t d, uint64_t a, uint64_t b,
       : "memory");
 }
 
-// tcgen05.st: 32 lanes x 32-bit, 8 consecutive columns per thread.
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-      : "memory");
-}
-
 // The same for 128 of the reduction: second operands at a + a_step and b + b_step.
 __device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint64_t a_step,
                                             uint64_t b_step, uint32_t idesc, uint32_t accumulate) {
@@ -291,6 +283,14 @@ __device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, 
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c2, f2, %5, 1;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c3, f3, %5, 1;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "l"(a_step), "l"(b_step), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// tcgen05.st: 32 lanes x 32-bit, 8 consecutive columns per thread.
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
 }
 
@@ -1348,7 +1348,6 @@ __global__ void __launch_bounds__(RowGeo<D>::kThreads, 1) attn_rows_kernel(const
 template <int D, int BITS>
 cudaError_t launch_rows(const AttnArgs& a, unsigned blocks, cudaStream_t s) {
   constexpr size_t smem = row_smem<D>();
-  static_assert(smem <= 232448, "shared memory");
   static_assert(smem <= 227 * 1024, "shared memory");
   const auto kernel = attn_rows_kernel<D, BITS>;
   static std::atomic<uint64_t> done{0};

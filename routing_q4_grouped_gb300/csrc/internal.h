@@ -94,6 +94,14 @@ cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done)
   return e;
 }
 
+// T rows of H heads of D elements do not overlap, in either order of the strides.
+inline bool rows_disjoint(int64_t row, int64_t head, int64_t T, int64_t H, int64_t D) {
+  if (row < 0 || head < 0) return false;
+  const bool head_in = (H == 1 || head >= D) && (T == 1 || row >= (H - 1) * head + D);
+  const bool row_in = (T == 1 || row >= D) && (H == 1 || head >= (T - 1) * row + D);
+  return head_in || row_in;
+}
+
 // Time limit of a wait inside a kernel (MOEQ4_WAIT_TIMEOUT_MS, 2 s by default).
 uint64_t wait_timeout_ns();
 

@@ -53,14 +53,6 @@ constexpr int kThreads = 128;
 
 bool bad_align(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
-// Rows of n heads of D elements may not overlap, in either order of the strides.
-bool rows_disjoint(int64_t row, int64_t head, int64_t T, int64_t H, int64_t D) {
-  if (row < 0 || head < 0) return false;
-  const bool head_in = (H == 1 || head >= D) && (T == 1 || row >= (H - 1) * head + D);
-  const bool row_in = (T == 1 || row >= D) && (H == 1 || head >= (T - 1) * row + D);
-  return head_in || row_in;
-}
-
 // ------------------------------------------------------------------- rotary
 
 struct RopeArgs {
