@@ -371,7 +371,9 @@ typedef struct moe_kv_new {
 /* Turns queries and keys to their positions, quantises keys and values and
  * writes them into the cache, in one launch. Turned queries and keys are rounded
  * to bf16; per group of 64: bias = min, scale = bf16((max - min) / (2^bits - 1)),
- * code = round((x - bias) / scale), ties to even, 0 when the group is constant.
+ * code = round((x - bias) * (1 / scale)), difference, reciprocal and product rounded to
+ * fp32, ties to even; 0 where scale is 0 (the group is constant, or its range is below
+ * bf16's smallest numbers).
  * A group that holds a NaN or an infinity reads back as NaN. Slots outside the
  * cache are skipped and set MOE_DEVERR_BAD_SLOT. q_out may be q with the same strides;
  * otherwise it overlaps no input. Hq <= 32768. T = 0 launches nothing. */
@@ -390,7 +392,8 @@ moe_status moe_kv_read(const moe_kv_cache* c, const int32_t* slots, int32_t n, u
  * last nq are its query tokens: query i sees own tokens 0 .. lens[b] - nq + i.
  *   o = sum_t softmax_t(scale * q . k_t) v_t,  0 where nothing is seen.
  * Query head h reads key/value head h / (Hq / Hkv). Memory of slots that are not
- * seen is never used in arithmetic, whatever it holds. */
+ * seen is never used in arithmetic, whatever it holds. Results do not depend on max_len,
+ * but many query tokens take longer with one far above the lengths. */
 typedef struct moe_kv_attn {
   const uint16_t* q;  int64_t q_row, q_head;          /* bf16 [B*nq][Hq][D], row b*nq + i */
   uint16_t* out;      int64_t out_row, out_head;      /* bf16 [B*nq][Hq][D]; rows may not overlap */

@@ -39,9 +39,9 @@
 // are fp32.
 //
 // Measured (D = 128, 32 query heads on 8 key/value heads, join included): one request of
-// 131071 tokens, 8 bits, 54 us, 5.3 TB/s, 78 % of the copy's bandwidth; 64 requests of
-// mixed lengths, 4 bits, 99 us, 3.1 TB/s. There a byte holds twice the codes and the
-// issue slots bind (62 % of them used in the kernel's middle, 46 % at 8 bits, tensor
+// 131071 tokens, 8 bits, 55 us, 5.2 TB/s, 76 % of the copy's bandwidth; 64 requests of
+// mixed lengths, 4 bits, 95 us, 3.2 TB/s. There a byte holds twice the codes and the
+// issue slots bind (54 % of them used over the whole kernel, 42 % at 8 bits, tensor
 // cores at 16 to 19 %), not the memory.
 #include <algorithm>
 #include <cmath>

@@ -44,11 +44,11 @@
 // with MOE_DEVERR_PIPE_TIMEOUT.
 //
 // Measured: the last 4096 query tokens of 32768 (16 query heads on 2, D = 128, 8 bits),
-// 983 us, 1050 TFLOP/s, 54 % of the bf16 peak as measured. A tile of 128 tokens for 256
-// rows takes about 4450 cycles, its products alone 2200. What binds is latency: the
+// 995 us, 1040 TFLOP/s, 53 % of the bf16 peak as measured. A tile of 128 tokens for 256
+// rows takes about 4500 cycles, its products alone 2200. What binds is latency: the
 // conversion of the next tile (codes from L2, fp16 arithmetic, shared memory) and the
 // softmax (about 3400 cycles) leave each other hardly any slack. 512 rows behind a prefix
-// of 16000 tokens (D = 256, 14 tiles a block) take 14 % of the peak: to load the queries
+// of 16000 tokens (D = 256, 14 tiles a block) take 13 % of the peak: to load the queries
 // (7 us, several dependent rounds of loads that queue behind the codes'), to come to the
 // first weights (2 us) and to write partial results (4 us) costs as much as 8 tiles.
 #include <cstdint>
