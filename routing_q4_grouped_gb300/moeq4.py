@@ -514,9 +514,10 @@ def moe_rope(x: torch.Tensor, out: torch.Tensor, pos: torch.Tensor, rope: RopeSp
              backward=False, stream=None) -> None:
     """Turns x [T, H, D] (bf16, fp16 or fp32, strided rows and heads) to positions pos [T];
     ``backward`` takes the gradient of the output to that of x. out may be x."""
-    dtype = _ROPE_DTYPES.get(x.dtype)
+    dtype = None if x is None else _ROPE_DTYPES.get(x.dtype)
     if dtype is None:
-        raise ValueError(f"moe_rope: x must be bfloat16, float16 or float32, got {x.dtype}")
+        raise ValueError("moe_rope: x must be bfloat16, float16 or float32, got "
+                         f"{None if x is None else x.dtype}")
     shape, xp, xr, xh = _rows("moe_rope", x, "x", None, x.dtype)
     T, H, D = shape
     oshape, op, orow, oh = _rows("moe_rope", out, "out", D, x.dtype)
@@ -560,8 +561,9 @@ def moe_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
 def moe_kv_read(cache: KVCache, slots: torch.Tensor, k_out: torch.Tensor = None,
                 v_out: torch.Tensor = None, stream=None) -> None:
     """Cache rows of ``slots`` [n] as bf16 [n, Hkv, D]; k_out or v_out may be None."""
-    fn, n = "moe_kv_read", slots.numel()
+    fn = "moe_kv_read"
     sp = _ints(fn, slots, 0, "slots")
+    n = slots.numel()
     shape = (n, cache.Hkv, cache.D)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         _need(fn, t, torch.bfloat16, name, optional=True)
