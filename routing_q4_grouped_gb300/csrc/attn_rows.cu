@@ -21,7 +21,7 @@
 // its own columns of O: it is found from the piece's first tile and undone when the
 // outputs are written, so groups of any ratio keep their bits. A tile in which a group of a
 // token is outside the window in which fp16 rounds it by 2^-12 of its size or better is
-// multiplied as bf16, weights and values (2^-9 each, fp32's range).
+// multiplied as bf16, weights and values (2^-8 each, fp32's range).
 //
 // The row maximum is not looked for tile by tile: m is only a reference, any value
 // near the largest logit does. All weights are positive, so a row whose 32 columns sum to less
