@@ -182,6 +182,34 @@ size_t moe_layer_workspace_size(int32_t T, int32_t E, int32_t k, int32_t d, int3
 moe_status moe_route(const float* logits, const moe_route_out* out, void* ws, size_t ws_bytes,
                      void* stream);
 
+/* How moe_route_scored chooses. Score of an expert: softmax over all E logits, or the
+ * sigmoid of its own. key = score + bias; the bias (a balance term) takes part in the
+ * choice only. The E experts form `groups` runs of E / groups; a group ranks by the sum
+ * of its group_best largest keys, the top_groups best groups stay, and the k largest
+ * keys among their experts are chosen, descending; equal ranks and equal keys go to the
+ * lower index. Weight of a choice: factor * score, divided by the sum of the chosen
+ * scores if renorm (0 where that sum is 0). */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
+typedef struct moe_route_score {
+  const float* bias;       /* device fp32 [E], or NULL: none. -inf: only where fewer than k
+                              other experts are left; NaN counts as -inf */
+  int32_t score;           /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+  int32_t groups;          /* divides E, at most 32; 1: no groups */
+  int32_t top_groups;      /* 1 <= top_groups <= groups, k <= top_groups * E / groups */
+  int32_t group_best;      /* 1 or 2 (at most E / groups); not used without groups */
+  int32_t renorm;          /* 0 or 1 */
+  float   factor;
+} moe_route_score;
+
+/* moe_route with another choice: the same arrays, limits, scratch and launches. Keys are
+ * compared as in 64-bit arithmetic; weights are fp32 within a few units in the last
+ * place. A NaN or -inf logit counts as the least finite number, +inf as the largest, and
+ * either sets MOE_DEVERR_NONFINITE_LOGIT. */
+moe_status moe_route_scored(const float* logits, const moe_route_score* score,
+                            const moe_route_out* out, void* ws, size_t ws_bytes, void* stream);
+
 /* moe_route for callers that cannot allocate device memory. The pages have no
  * counterpart; this entry exists for code that may not call cudaMalloc at all,
  * such as a serving process that reserves all device memory up front and hands
@@ -269,6 +297,13 @@ moe_status moe_layer(const uint16_t* x, const float* logits, int32_t T, const mo
                      const moe_route_out* r, uint16_t* y, void* ws, size_t ws_bytes,
                      void* stream);
 
+/* moe_layer with the routing of moe_route_scored. Every host-side check of both steps
+ * runs before the first launch. */
+moe_status moe_layer_scored(const uint16_t* x, const float* logits, int32_t T,
+                            const moe_q4_packed* W, const moe_route_score* score,
+                            const moe_route_out* r, uint16_t* y, void* ws, size_t ws_bytes,
+                            void* stream);
+
 /* Input of the next stacked layer in the bounded-chunk prefill run ([A] §5-2:
  * long prompts run in bounded chunks; [C] "GPU 상주와 메모리 절감"):
  *   out[t] = bf16( v / sqrt(mean(v^2)) ),  v = y[t] + x[t]   (fp32, no epsilon)
@@ -292,6 +327,34 @@ moe_status moe_l2_prefetch(const void* ptr, size_t bytes, void* stream);
 #define MOE_BF16 0
 #define MOE_F16  1
 #define MOE_F32  2
+
+/* Residual addition and root-mean-square norm of T tokens of H rows of D elements (H = 1:
+ * hidden rows; H heads: per head):
+ *   h = x + add,  y = h / sqrt(mean(h^2) + eps) * (weight + offset)
+ * in fp32 (sums whose squares leave fp32's range are taken again on scaled elements).
+ * Any of three results, each rounded once: sum = h, out = y, and y in 8 bits:
+ *   scales = max(max|y| / 448, 2^-126) of a row, codes = e4m3(y / scale), ties to even.
+ * A row whose y holds a NaN or an infinity has the scale NaN. */
+typedef struct moe_norm {
+  const void* x;   int64_t x_row, x_head;             /* dtype; token t, row h at t*row + h*head */
+  const void* add; int64_t add_row, add_head;         /* dtype, or NULL: h = x */
+  void* sum;       int64_t sum_row, sum_head;         /* dtype, or NULL */
+  void* out;       int64_t out_row, out_head;         /* dtype, or NULL */
+  uint8_t* codes;  int64_t codes_row, codes_head;     /* e4m3, or NULL */
+  float* scales;                                      /* [T][H], with codes */
+  const void* weight;                                 /* dtype [D], or NULL: 1 */
+  int32_t T, H, D;
+  int32_t dtype;                                      /* MOE_BF16, MOE_F16 or MOE_F32 */
+  float eps;                                          /* > 0 */
+  float offset;                                       /* added to the weight */
+} moe_norm;
+
+/* One launch. At least one of out and codes. sum or out may be x or add with the same
+ * strides; any other overlap of arrays is not allowed, and rows of a result may not
+ * overlap. D <= 16384, H <= 65535, T * H < 2^31. Elements aligned to their type; 16-byte
+ * aligned pointers and strides (codes: 8 bytes, or 4 for MOE_F32) take the vector path,
+ * anything else one element per load. T = 0 launches nothing. */
+moe_status moe_rms_norm(const moe_norm* a, void* stream);
 
 /* Rotary positions. The first `rot` elements of a head form rot/2 pairs
  * (a_i, b_i): elements (i, i + rot/2), or (2i, 2i + 1) when interleaved. At

@@ -1,6 +1,7 @@
 // api.cu — the extern "C" boundary of libmoeq4: argument validation,
 // workspace layout, TMA descriptor encoding and the launch sequence.
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -162,10 +163,24 @@ RouteArgs make_route_args(const float* logits, const moe_route_out* r, void* ws)
   return a;
 }
 
+moe_status check_score(const moe_route_score* c, const moe_route_out* r) {
+  if (!c) return MOE_ERR_ARG;
+  if (c->score < MOE_SCORE_SOFTMAX || c->score > MOE_SCORE_SIGMOID || c->renorm < 0 ||
+      c->renorm > 1 || c->group_best < 1 || c->group_best > 2 || c->groups < 1 ||
+      c->top_groups < 1 || c->top_groups > c->groups || !std::isfinite(c->factor))
+    return MOE_ERR_ARG;
+  if (c->groups > kRouteMaxGroups || r->E % c->groups) return MOE_ERR_SHAPE;
+  const int per = r->E / c->groups;
+  if ((c->groups > 1 && c->group_best > per) || r->k > c->top_groups * per) return MOE_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(c->bias) & 3u) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
 // ids_given: the chosen experts and weights are already in r->ids / r->w (the
-// fused router wrote them); logits are then not read.
+// fused router wrote them); logits are then not read. score: the choice of
+// moe_route_scored (nullptr: moe_route's).
 moe_status route_impl(const float* logits, const moe_route_out* r, void* ws, size_t ws_bytes,
-                      cudaStream_t s, int ids_given = 0) {
+                      cudaStream_t s, int ids_given = 0, const moe_route_score* score = nullptr) {
   moe_status st = check_route_out(r);
   if (st != MOE_OK) return st;
   if ((!ids_given && !logits && r->T > 0) || !ws) return MOE_ERR_ARG;
@@ -175,8 +190,17 @@ moe_status route_impl(const float* logits, const moe_route_out* r, void* ws, siz
   if ((st = device_info(&di)) != MOE_OK) return st;
   RouteArgs a = make_route_args(logits, r, ws);
   a.ids_given = ids_given;
+  if (score) {
+    a.bias = score->bias;
+    a.score = score->score;
+    a.groups = score->groups;
+    a.top_groups = score->top_groups;
+    a.group_best = score->group_best;
+    a.renorm = score->renorm;
+    a.factor = score->factor;
+  }
   stage_mark(0, s);
-  if (launch_route(a, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((score ? launch_route_scored(a, s) : launch_route(a, s)) != cudaSuccess) return MOE_ERR_CUDA;
   stage_mark(1, s);
   stage_mark(2, s);   // (routing is one step: stages 1 and 2 coincide)
   return MOE_OK;
@@ -468,15 +492,23 @@ moe_status moe_route(const float* logits, const moe_route_out* out, void* ws, si
   return route_impl(logits, out, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
+moe_status moe_route_scored(const float* logits, const moe_route_score* score,
+                            const moe_route_out* out, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_route_out(out);
+  if (st != MOE_OK || (st = check_score(score, out)) != MOE_OK) return st;
+  return route_impl(logits, out, ws, ws_bytes, static_cast<cudaStream_t>(stream), 0, score);
+}
+
 moe_status moe_expert_ffn(const uint16_t* x, int32_t T, int32_t d, const moe_q4_packed* W,
                           const moe_route_out* r, uint16_t* y, void* ws, size_t ws_bytes,
                           void* stream) {
   return ffn_impl(x, T, d, W, r, y, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
-moe_status moe_layer(const uint16_t* x, const float* logits, int32_t T, const moe_q4_packed* W,
-                     const moe_route_out* r, uint16_t* y, void* ws, size_t ws_bytes,
-                     void* stream) {
+static moe_status layer_impl(const uint16_t* x, const float* logits, int32_t T,
+                             const moe_q4_packed* W, const moe_route_score* score,
+                             const moe_route_out* r, uint16_t* y, void* ws, size_t ws_bytes,
+                             void* stream) {
   if (!W || !r) return MOE_ERR_ARG;
   if (r->T != T) return MOE_ERR_SHAPE;
   const size_t need = moe_layer_workspace_size(T, r->E, r->k, W->d, W->f, W->f_s, r->block_m);
@@ -489,8 +521,23 @@ moe_status moe_layer(const uint16_t* x, const float* logits, int32_t T, const mo
   if (!aligned16(x) || !aligned16(y)) return MOE_ERR_ALIGN;
   if (W->E != r->E) return MOE_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((st = route_impl(logits, r, ws, rsz, s)) != MOE_OK) return st;
+  if ((st = route_impl(logits, r, ws, rsz, s, 0, score)) != MOE_OK) return st;
   return ffn_impl(x, T, W->d, W, r, y, static_cast<char*>(ws) + rsz, ws_bytes - rsz, s);
+}
+
+moe_status moe_layer(const uint16_t* x, const float* logits, int32_t T, const moe_q4_packed* W,
+                     const moe_route_out* r, uint16_t* y, void* ws, size_t ws_bytes,
+                     void* stream) {
+  return layer_impl(x, logits, T, W, nullptr, r, y, ws, ws_bytes, stream);
+}
+
+moe_status moe_layer_scored(const uint16_t* x, const float* logits, int32_t T,
+                            const moe_q4_packed* W, const moe_route_score* score,
+                            const moe_route_out* r, uint16_t* y, void* ws, size_t ws_bytes,
+                            void* stream) {
+  moe_status st = check_route_out(r);
+  if (st != MOE_OK || (st = check_score(score, r)) != MOE_OK) return st;
+  return layer_impl(x, logits, T, W, score, r, y, ws, ws_bytes, stream);
 }
 
 moe_status moe_expert_ffn_decode(const uint16_t* x, int32_t T, int32_t d,

@@ -38,6 +38,10 @@ struct RouteArgs {
   // scratch
   uint32_t* rows;           // [nblk][round_up(E, 4)] per-block expert counts
   uint64_t timeout_ns;
+  // moe_route_scored: how the choice and the weights come from the logits
+  const float* bias;        // [E], or nullptr
+  int score, groups, top_groups, group_best, renorm;
+  float factor;
   int ids_given;            // 0: select from logits; 1: ids and w already hold the choice and
                             // its weights; 2: ids hold the choice and w its logits (descending),
                             // from which the weights are computed
@@ -56,6 +60,9 @@ RouteWs route_ws_layout(int T, int E, int k);
 // The whole routing step: one launch for a batch that one block covers, else
 // two (choose and count, then place), each with programmatic serialization.
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
+// The same with the choice and the weights of moe_route_scored (ids_given = 0).
+cudaError_t launch_route_scored(const RouteArgs& a, cudaStream_t s);
+constexpr int kRouteMaxGroups = 32;
 
 // Launch with programmatic stream serialization: the kernel may be scheduled
 // while the previous kernel on `s` finishes (it calls griddep_wait before

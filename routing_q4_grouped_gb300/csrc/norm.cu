@@ -1,0 +1,352 @@
+// norm.cu — residual addition and root-mean-square norm (moe_rms_norm), with the
+// result in the input's type, in 8 bits with one scale per row, or both.
+//
+//   h = x + add,  r = 1 / sqrt(mean(h^2) + eps),  y = h r (weight + offset)
+//   scale = max(max|y| / 448, 2^-126),  code = e4m3(y / scale)
+//
+// Each byte moves once and each element takes a few instructions, so many rows are
+// bound by memory bandwidth and few rows by launch latency. A row is held in registers
+// between its reductions (nothing is read twice): by 8, 16 or 32 lanes where it has up
+// to 128 vectors of 16 bytes, by a block of up to 512 threads where it has more.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "../../include/moeq4.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moeq4 {
+namespace {
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kMaxD = 16384;
+constexpr float kCodeMax = 448.f;                    // largest e4m3 value
+constexpr float kScaleMin = 1.17549435e-38f;         // 2^-126: its reciprocal is finite
+
+struct NormArgs {
+  const void *x, *add, *weight;
+  void *sum, *out;
+  uint8_t* codes;
+  float* scales;
+  int64_t x_row, x_head, add_row, add_head, sum_row, sum_head, out_row, out_head, c_row, c_head;
+  int rows, H, D;            // rows = T * H
+  int n;                     // vectors per row, D / V
+  float eps, offset, inv_d;
+};
+
+template <typename E, int V>
+struct alignas(V * sizeof(E)) Vec {
+  E e[V];
+};
+template <int V>
+struct alignas(V) Bytes {
+  uint8_t e[V];
+};
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <typename E>
+__device__ __forceinline__ E from_f(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ float from_f(float v) { return v; }
+
+// Sum, and unsigned maximum, over the lanes of a row: LANES neighbouring lanes of a warp
+// (LANES <= 32), or the whole block (LANES = 0; `sh` holds a word per warp; the order of
+// the additions is fixed).
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, float* sh) {
+  constexpr int kFirst = (LANES == 0 ? 32 : LANES) / 2;
+#pragma unroll
+  for (int off = kFirst; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  if constexpr (LANES == 0) {
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) sh[warp] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int i = 0; i < warps; ++i) v += sh[i];
+    __syncthreads();
+  }
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, float* sh) {
+  constexpr int kFirst = (LANES == 0 ? 32 : LANES) / 2;
+#pragma unroll
+  for (int off = kFirst; off > 0; off >>= 1) v = max(v, __shfl_xor_sync(kFull, v, off));
+  if constexpr (LANES == 0) {
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) sh[warp] = __uint_as_float(v);
+    __syncthreads();
+    v = 0;
+    for (int i = 0; i < warps; ++i) v = max(v, __float_as_uint(sh[i]));
+    __syncthreads();
+  }
+  return v;
+}
+
+// One row per LANES lanes (LANES = 0: per block), NV vectors of V elements per thread:
+// vector u of the row in thread u % lanes.
+template <typename E, int V, int NV, int LANES>
+__global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
+  __shared__ float sh[16];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lanes = LANES == 0 ? static_cast<int>(blockDim.x) : LANES;
+  const int tid = LANES == 0 ? static_cast<int>(threadIdx.x)
+                             : static_cast<int>(threadIdx.x) % lanes;
+  const int64_t row = LANES == 0 ? static_cast<int64_t>(blockIdx.x)
+                                 : static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) +
+                                       threadIdx.x / lanes;
+  const bool live = row < a.rows;        // (lanes of a dead row take part in the reductions)
+  const int64_t t = live ? row / a.H : 0, h = live ? row % a.H : 0;
+  using Vt = Vec<E, V>;
+  const Vt* x = reinterpret_cast<const Vt*>(static_cast<const E*>(a.x) + t * a.x_row + h * a.x_head);
+  const Vt* add =
+      reinterpret_cast<const Vt*>(static_cast<const E*>(a.add) + t * a.add_row + h * a.add_head);
+  float v[NV][V];
+  {
+    Vt p[NV], q[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int u = tid + j * lanes;
+      if (live && u < a.n) {
+        p[j] = x[u];
+        if (a.add) q[j] = add[u];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = live && tid + j * lanes < a.n;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[j][i] = in ? to_f(p[j].e[i]) : 0.f;
+        if (in && a.add) v[j][i] += to_f(q[j].e[i]);
+      }
+    }
+  }
+  if (a.sum && live) {
+    Vt* o = reinterpret_cast<Vt*>(static_cast<E*>(a.sum) + t * a.sum_row + h * a.sum_head);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Vt w;
+#pragma unroll
+      for (int i = 0; i < V; ++i) w.e[i] = from_f<E>(v[j][i]);
+      if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+  ss = row_sum<LANES>(ss, sh);
+  float r = __frsqrt_rn(fmaf(ss, a.inv_d, a.eps));
+  // Squares that left fp32's range, above or (beside a small eps) below: again, on elements
+  // scaled by a power of two. All lanes of a warp, or of the block, take part.
+  const bool odd = !(ss < 1e37f) || ss < 1e-24f;
+  if (LANES == 0 ? odd : __any_sync(kFull, odd)) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+    m = row_max<LANES>(m, sh);
+    const float top = __uint_as_float(m);
+    const int e = m != 0 && m < 0x7F800000u ? ilogbf(top) : 0;
+    float s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float z = ldexpf(v[j][i], -e);
+        s2 = fmaf(z, z, s2);
+      }
+    s2 = row_sum<LANES>(s2, sh);
+    if (odd)
+      r = static_cast<float>(
+          1.0 / sqrt(ldexp(static_cast<double>(s2) / a.D, 2 * e) + static_cast<double>(a.eps)));
+  }
+  const Vt* weight = static_cast<const Vt*>(a.weight);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int u = tid + j * lanes;
+    Vt w;
+    if (a.weight && u < a.n) w = weight[u];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float g = a.weight && u < a.n ? to_f(w.e[i]) + a.offset : 1.f + a.offset;
+      v[j][i] = v[j][i] * r * g;
+    }
+  }
+  if (a.out && live) {
+    Vt* o = reinterpret_cast<Vt*>(static_cast<E*>(a.out) + t * a.out_row + h * a.out_head);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Vt w;
+#pragma unroll
+      for (int i = 0; i < V; ++i) w.e[i] = from_f<E>(v[j][i]);
+      if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
+    }
+  }
+  if (a.codes) {
+    // the largest magnitude by its bits, above which lie infinity and NaN
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (tid + j * lanes < a.n) m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+    m = row_max<LANES>(m, sh);
+    const float scale = m < 0x7F800000u
+                            ? fmaxf(__fdiv_rn(__uint_as_float(m), kCodeMax), kScaleMin)
+                            : __uint_as_float(0x7FC00000u);
+    const float inv = __frcp_rn(scale);
+    if (live) {
+      if (tid == 0) a.scales[row] = scale;
+      Bytes<V>* o = reinterpret_cast<Bytes<V>*>(a.codes + t * a.c_row + h * a.c_head);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        Bytes<V> w;
+        if constexpr (V % 2 == 0) {
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
+                make_float2(v[j][i] * inv, v[j][i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+            w.e[i] = static_cast<uint8_t>(two & 0xFF);
+            w.e[i + 1] = static_cast<uint8_t>(two >> 8);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            w.e[i] = __nv_cvt_float_to_fp8(v[j][i] * inv, __NV_SATFINITE, __NV_E4M3);
+        }
+        if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
+      }
+    }
+  }
+}
+
+template <typename E, int V, int NV, int LANES>
+cudaError_t launch_rows(const NormArgs& a, int threads, cudaStream_t s) {
+  const int per = LANES == 0 ? 1 : threads / LANES;
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.rows) + per - 1) / per);
+  return launch_pdl(norm_kernel<E, V, NV, LANES>, dim3(blocks), dim3(threads), 0, s, a);
+}
+
+int round32(int n) { return (n + 31) / 32 * 32; }
+
+template <typename E, int V>
+cudaError_t launch_norm_v(NormArgs a, cudaStream_t s) {
+  a.n = a.D / V;
+  constexpr int kWarpRows = 128;         // threads of a block of several rows
+  if (a.n <= 8) return launch_rows<E, V, 1, 8>(a, kWarpRows, s);
+  if (a.n <= 16) return launch_rows<E, V, 1, 16>(a, kWarpRows, s);
+  if (a.n <= 32) return launch_rows<E, V, 1, 32>(a, kWarpRows, s);
+  if (a.n <= 64) return launch_rows<E, V, 2, 32>(a, kWarpRows, s);
+  if (a.n <= 128) return launch_rows<E, V, 4, 32>(a, kWarpRows, s);
+  if (a.n <= 1024) return launch_rows<E, V, 2, 0>(a, round32((a.n + 1) / 2), s);
+  if (a.n <= 2048) return launch_rows<E, V, 4, 0>(a, round32((a.n + 3) / 4), s);
+  if constexpr (V * sizeof(E) < 16 || sizeof(E) == 4) {
+    if (a.n <= 4096) return launch_rows<E, V, 8, 0>(a, round32((a.n + 7) / 8), s);
+  }
+  if constexpr (V == 1) return launch_rows<E, V, 32, 0>(a, round32((a.n + 31) / 32), s);
+  return cudaErrorInvalidValue;
+}
+
+template <typename E>
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(E);
+  const uint64_t strides =
+      static_cast<uint64_t>(a.x_row | a.x_head | (a.add ? a.add_row | a.add_head : 0) |
+                            (a.sum ? a.sum_row | a.sum_head : 0) |
+                            (a.out ? a.out_row | a.out_head : 0) |
+                            (a.codes ? a.c_row | a.c_head : 0));
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.add) |
+                      reinterpret_cast<uintptr_t>(a.sum) | reinterpret_cast<uintptr_t>(a.out) |
+                      reinterpret_cast<uintptr_t>(a.weight);
+  if (a.D % V == 0 && strides % V == 0 && p % 16 == 0 &&
+      reinterpret_cast<uintptr_t>(a.codes) % V == 0)
+    return launch_norm_v<E, V>(a, s);
+  return launch_norm_v<E, 1>(a, s);
+}
+
+bool bad_align(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+}  // namespace
+}  // namespace moeq4
+
+extern "C" moe_status moe_rms_norm(const moe_norm* n, void* stream) {
+  using namespace moeq4;
+  if (!n || n->T < 0 || n->H < 1 || n->D < 1 || n->dtype < MOE_BF16 || n->dtype > MOE_F32)
+    return MOE_ERR_ARG;
+  if (!(n->eps > 0.f) || !std::isfinite(n->eps) || !std::isfinite(n->offset)) return MOE_ERR_ARG;
+  if (n->D > kMaxD || n->H > 65535 || static_cast<int64_t>(n->T) * n->H > 0x7FFFFFFF)
+    return MOE_ERR_SHAPE;
+  if (n->T == 0) return MOE_OK;
+  if (!n->x || (!n->out && !n->codes) || (n->codes && !n->scales)) return MOE_ERR_ARG;
+  if (n->x_row < 0 || n->x_head < 0 || (n->add && (n->add_row < 0 || n->add_head < 0)))
+    return MOE_ERR_SHAPE;
+  const struct {
+    const void* p;
+    int64_t row, head;
+  } outs[3] = {{n->sum, n->sum_row, n->sum_head},
+               {n->out, n->out_row, n->out_head},
+               {n->codes, n->codes_row, n->codes_head}};
+  for (int i = 0; i < 3; ++i) {
+    if (!outs[i].p) continue;
+    if (!rows_disjoint(outs[i].row, outs[i].head, n->T, n->H, n->D)) return MOE_ERR_SHAPE;
+    for (int j = 0; j < i; ++j)
+      if (outs[i].p == outs[j].p) return MOE_ERR_ARG;
+    // in place: each thread overwrites the elements that it has read
+    const bool as_x = outs[i].row == n->x_row && outs[i].head == n->x_head && i < 2;
+    const bool as_add = outs[i].row == n->add_row && outs[i].head == n->add_head && i < 2;
+    if ((outs[i].p == n->x && !as_x) || (n->add && outs[i].p == n->add && !as_add))
+      return MOE_ERR_ARG;
+  }
+  const unsigned es = n->dtype == MOE_F32 ? 4 : 2;
+  if (bad_align(n->x, es) || bad_align(n->add, es) || bad_align(n->sum, es) ||
+      bad_align(n->out, es) || bad_align(n->weight, es) || (n->codes && bad_align(n->scales, 4)))
+    return MOE_ERR_ALIGN;
+  const moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  NormArgs a{};
+  a.x = n->x;
+  a.add = n->add;
+  a.weight = n->weight;
+  a.sum = n->sum;
+  a.out = n->out;
+  a.codes = n->codes;
+  a.scales = n->scales;
+  a.x_row = n->x_row;
+  a.x_head = n->x_head;
+  a.add_row = n->add_row;
+  a.add_head = n->add_head;
+  a.sum_row = n->sum_row;
+  a.sum_head = n->sum_head;
+  a.out_row = n->out_row;
+  a.out_head = n->out_head;
+  a.c_row = n->codes_row;
+  a.c_head = n->codes_head;
+  a.rows = n->T * n->H;
+  a.H = n->H;
+  a.D = n->D;
+  a.eps = n->eps;
+  a.offset = n->offset;
+  a.inv_d = static_cast<float>(1.0 / n->D);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = n->dtype == MOE_F32   ? launch_norm<float>(a, s)
+                        : n->dtype == MOE_F16 ? launch_norm<__half>(a, s)
+                                              : launch_norm<__nv_bfloat16>(a, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

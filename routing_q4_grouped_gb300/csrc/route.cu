@@ -166,6 +166,8 @@ __device__ __forceinline__ void select_block_rows(const RouteArgs& a, int t0, co
   }
 }
 
+#include "route_scored.cuh"
+
 // Block-wide exclusive scan of two counts per thread (kRouteThreads threads), in
 // unsigned arithmetic (wraps rather than overflows on a corrupt workspace).
 // Gives this thread's exclusive prefixes of (x, y) and the block totals.
@@ -245,15 +247,20 @@ __device__ __forceinline__ RouteSmem route_smem(int* smem, const RouteArgs& a) {
 }
 
 // The choice of each of the block's nt tokens (experts into sE, logits into
-// sV), then the block's counts (sCnt) and each row's stable rank among the
+// sV; SCORED: the final weights into sV), then the block's counts (sCnt) and each row's stable rank among the
 // block's rows of its expert (sRank, rows in ascending (t, j) order).
-template <int S>
+template <int S, bool SCORED>
 __device__ __forceinline__ void choose_and_rank(const RouteArgs& a, const RouteSmem& m, int t0,
                                                 int nt) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int E = a.E, k = a.k;
   for (int e = tid; e < route_ep(E); e += kRouteThreads) m.sCnt[e] = 0;
-  if (a.ids_given != 0) {
+  if constexpr (SCORED) {
+    bool bad = false;
+    for (int i = warp; i < nt; i += kRouteWarps)
+      select_scored<S>(a, t0 + i, lane, m.sE + i * k, m.sV + i * k, bad);
+    if (__any_sync(kFull, bad) && lane == 0) atomicOr(a.err, MOE_DEVERR_NONFINITE_LOGIT);
+  } else if (a.ids_given != 0) {
     // the fused router chose the experts (mode 1: with their weights in w;
     // mode 2: with their logits in w, the weights are computed later). An id
     // out of range is reported and counted as expert 0 so that the permutation
@@ -409,15 +416,22 @@ __device__ __forceinline__ void place_rows(const RouteArgs& a, const RouteSmem& 
 // block, no other block to wait for. Launched with programmatic serialization:
 // the previous kernel on the stream may still read the arrays this call
 // rewrites until griddep_wait returns.
-template <int S>
+template <int S, bool SCORED>
 __global__ void __launch_bounds__(kRouteThreads) route_single_kernel(const RouteArgs a) {
   extern __shared__ int smem[];
   const RouteSmem m = route_smem(smem, a);
   griddep_launch_dependents();   // the GEMM that follows may start its prologue
   griddep_wait();
   const int nt = max(0, a.T);
-  choose_and_rank<S>(a, m, 0, nt);
-  block_weights(a, m, 0, nt, a.ids_given == 0);
+  choose_and_rank<S, SCORED>(a, m, 0, nt);
+  if constexpr (SCORED) {
+    for (int i = threadIdx.x; i < nt * a.k; i += kRouteThreads) {
+      a.ids[i] = m.sE[i];
+      a.w[i] = m.sV[i];
+    }
+  } else {
+    block_weights(a, m, 0, nt, a.ids_given == 0);
+  }
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
     m.sBase[e] = 0;
     m.sOff[e] = m.sCnt[e];
@@ -428,9 +442,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_single_kernel(const Route
 
 // Routing of a larger batch, first of two launches: block b chooses the
 // experts of its a.tpb tokens, counts them and ranks its rows; it publishes its
-// counts as row b of the count rows, the experts in ids, their logits in w
-// (mode 0; mode 2 arrives with them there) and each row's rank in inv.
-template <int S>
+// counts as row b of the count rows, the experts in ids, their logits (SCORED:
+// their weights) in w (mode 0; mode 2 arrives with them there) and each row's rank in inv.
+template <int S, bool SCORED>
 __global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const RouteArgs a) {
   extern __shared__ int smem[];
   const RouteSmem m = route_smem(smem, a);
@@ -438,7 +452,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const RouteA
   griddep_wait();
   const int t0 = b * a.tpb;
   const int nt = max(0, min(a.tpb, a.T - t0));
-  choose_and_rank<S>(a, m, t0, nt);
+  choose_and_rank<S, SCORED>(a, m, t0, nt);
   const int ep = route_ep(a.E);
   uint4* row = reinterpret_cast<uint4*>(a.rows + static_cast<size_t>(b) * ep);
   for (int g = tid; g < ep / 4; g += kRouteThreads)
@@ -553,7 +567,7 @@ static size_t route_smem_bytes(int E, int k, int tpb) {
   return sizeof(int) * route_smem_words(E, k, tpb);
 }
 
-template <int S>
+template <int S, bool SCORED>
 static cudaError_t launch_s(RouteArgs a, cudaStream_t s) {
   // Tokens per block: the multiple of kRouteTokensMin that keeps the grid near
   // kRouteBlocksTarget blocks (every placing block reads every count row; small
@@ -569,22 +583,30 @@ static cudaError_t launch_s(RouteArgs a, cudaStream_t s) {
   a.nblk = a.T > 0 ? (a.T + tpb - 1) / tpb : 1;
   if (a.nblk == 1) {
     a.tpb = max(a.T, 1);
-    return launch_pdl(route_single_kernel<S>, dim3(1), dim3(kRouteThreads),
+    return launch_pdl(route_single_kernel<S, SCORED>, dim3(1), dim3(kRouteThreads),
                       route_smem_bytes(a.E, a.k, a.tpb), s, a);
   }
-  cudaError_t e = launch_pdl(route_count_kernel<S>, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
+  cudaError_t e =
+      launch_pdl(route_count_kernel<S, SCORED>, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
   if (e != cudaSuccess) return e;
+  if (SCORED) a.ids_given = 1;   // the weights are in w
   return launch_pdl(route_place_kernel, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
 }
 
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
+template <bool SCORED>
+static cudaError_t launch_all(const RouteArgs& a, cudaStream_t s) {
   const int S = (a.E + 31) / 32;
-  if (S <= 1) return launch_s<1>(a, s);
-  if (S <= 2) return launch_s<2>(a, s);
-  if (S <= 4) return launch_s<4>(a, s);
-  if (S <= 8) return launch_s<8>(a, s);
-  if (S <= 16) return launch_s<16>(a, s);
-  return launch_s<32>(a, s);
+  if (S <= 1) return launch_s<1, SCORED>(a, s);
+  if (S <= 2) return launch_s<2, SCORED>(a, s);
+  if (S <= 4) return launch_s<4, SCORED>(a, s);
+  if (S <= 8) return launch_s<8, SCORED>(a, s);
+  if (S <= 16) return launch_s<16, SCORED>(a, s);
+  return launch_s<32, SCORED>(a, s);
+}
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) { return launch_all<false>(a, s); }
+cudaError_t launch_route_scored(const RouteArgs& a, cudaStream_t s) {
+  return launch_all<true>(a, s);
 }
 
 }  // namespace moeq4

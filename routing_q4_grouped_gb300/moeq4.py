@@ -29,6 +29,7 @@ MOE_DEVERR_BAD_PAGE = 64
 MOE_DEVERR_BAD_LENGTH = 128
 MOE_ERR_TOO_LARGE = -8
 MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_BASE, MOE_ROPE_BANDS = 0, 1, 2, 3
 
 _c_i32 = ctypes.c_int32
@@ -57,6 +58,22 @@ class RouteOutC(ctypes.Structure):
                 ("perm", _c_ptr), ("inv", _c_ptr), ("tiles", _c_ptr), ("n_tiles", _c_ptr),
                 ("err", _c_ptr), ("T", _c_i32), ("E", _c_i32), ("k", _c_i32),
                 ("block_m", _c_i32)]
+
+
+class RouteScoreC(ctypes.Structure):
+    _fields_ = [("bias", _c_ptr), ("score", _c_i32), ("groups", _c_i32), ("top_groups", _c_i32),
+                ("group_best", _c_i32), ("renorm", _c_i32), ("factor", _c_f32)]
+
+
+class NormC(ctypes.Structure):
+    _fields_ = [("x", _c_ptr), ("x_row", _c_i64), ("x_head", _c_i64),
+                ("add", _c_ptr), ("add_row", _c_i64), ("add_head", _c_i64),
+                ("sum", _c_ptr), ("sum_row", _c_i64), ("sum_head", _c_i64),
+                ("out", _c_ptr), ("out_row", _c_i64), ("out_head", _c_i64),
+                ("codes", _c_ptr), ("codes_row", _c_i64), ("codes_head", _c_i64),
+                ("scales", _c_ptr), ("weight", _c_ptr),
+                ("T", _c_i32), ("H", _c_i32), ("D", _c_i32), ("dtype", _c_i32),
+                ("eps", _c_f32), ("offset", _c_f32)]
 
 
 class RopeSpecC(ctypes.Structure):
@@ -99,6 +116,11 @@ _SIGS = {
     "moe_ffn_workspace_size": (_c_size, [_c_i32] * 7),
     "moe_layer_workspace_size": (_c_size, [_c_i32] * 7),
     "moe_route": (_c_i32, [_c_ptr, ctypes.POINTER(RouteOutC), _c_ptr, _c_size, _c_ptr]),
+    "moe_route_scored": (_c_i32, [_c_ptr, _c_ptr, ctypes.POINTER(RouteOutC), _c_ptr, _c_size,
+                                  _c_ptr]),
+    "moe_layer_scored": (_c_i32, [_c_ptr, _c_ptr, _c_i32, ctypes.POINTER(Q4PackedC), _c_ptr,
+                                  ctypes.POINTER(RouteOutC), _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "moe_rms_norm": (_c_i32, [_c_ptr, _c_ptr]),
     "moe_route_noalloc": (_c_i32, [_c_ptr, ctypes.POINTER(RouteOutC), _c_ptr]),
     "moe_q4_packed_size": (_c_size, [_c_i32] * 4),
     "moe_q4_prepack": (_c_i32, [ctypes.POINTER(Q4WeightsC), _c_ptr, _c_size, _c_ptr]),
@@ -185,6 +207,14 @@ try:   # the same handle without building a Stream object (saves about a microse
         return _cuda_getCurrentRawStream(_cuda_getDevice())
 except ImportError:
     pass
+
+
+def _here(fn, *tensors):
+    """A call runs on the current device: its tensors have to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn}: a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
 def _stream(stream) -> int:
@@ -320,6 +350,39 @@ def moe_route(logits: torch.Tensor, out: RouteBuffers, ws: torch.Tensor, stream=
                                         _stream(stream)))
 
 
+class RouteScore:
+    """How :func:`moe_route_scored` chooses (moe_route_score): softmax or sigmoid scores, an
+    fp32 ``bias`` [E] that takes part in the choice only, ``groups`` of experts of which the
+    ``top_groups`` with the largest sum of ``group_best`` keys stay, weights ``factor`` * score,
+    divided by the sum of the chosen scores if ``renorm``."""
+
+    def __init__(self, score=MOE_SCORE_SOFTMAX, bias: torch.Tensor = None, groups=1, top_groups=1,
+                 group_best=1, renorm=True, factor=1.0):
+        _need("RouteScore", bias, torch.float32, "bias", optional=True)
+        self.score, self.bias, self.groups, self.top_groups = score, bias, groups, top_groups
+        self.group_best, self.renorm, self.factor = group_best, renorm, factor
+        self._c = RouteScoreC(_ptr(bias), score, groups, top_groups, group_best, int(renorm), factor)
+        self._addr = ctypes.addressof(self._c)
+
+
+def _scored(fn, logits, score, out):
+    _need(fn, logits, torch.float32, "logits")
+    if logits.shape != (out.T, out.E):
+        raise ValueError(f"{fn}: logits must be [{out.T}][{out.E}], got {tuple(logits.shape)}")
+    if score.bias is not None and score.bias.numel() != out.E:
+        raise ValueError(f"{fn}: the bias must hold {out.E} values, got {score.bias.numel()}")
+    _here(fn, logits, score.bias, out.ids)
+
+
+def moe_route_scored(logits: torch.Tensor, score: RouteScore, out: RouteBuffers, ws: torch.Tensor,
+                     stream=None) -> None:
+    """Routing of fp32 logits [T, E] into ``out`` with the choice and weights of ``score``."""
+    _scored("moe_route_scored", logits, score, out)
+    c = out.cstruct()
+    _check("moe_route_scored", lib().moe_route_scored(_ptr(logits), score._addr, ctypes.byref(c),
+                                                      _ptr(ws), ws.numel(), _stream(stream)))
+
+
 def moe_route_noalloc(logits: torch.Tensor, out: RouteBuffers, stream=None) -> None:
     """moe_route with the library's fixed internal scratch (no workspace argument).
 
@@ -369,6 +432,22 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, W: DeviceWeights, r: RouteB
     wc, rc = W.cstruct(), r.cstruct()
     _check("moe_layer", lib().moe_layer(_ptr(x), _ptr(logits), T, ctypes.byref(wc), ctypes.byref(rc),
                                         _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_layer_scored(x: torch.Tensor, logits: torch.Tensor, W: DeviceWeights, score: RouteScore,
+                     r: RouteBuffers, y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """moe_route_scored then expert FFN on one stream, no host synchronisation."""
+    fn = "moe_layer_scored"
+    _need(fn, x, torch.bfloat16, "x")
+    _need(fn, y, torch.bfloat16, "y")
+    _scored(fn, logits, score, r)
+    if x.shape != (r.T, W.d) or y.shape != x.shape:
+        raise ValueError(f"{fn}: x and y must be [{r.T}][{W.d}], got {tuple(x.shape)} and "
+                         f"{tuple(y.shape)}")
+    wc, rc = W.cstruct(), r.cstruct()
+    _check(fn, lib().moe_layer_scored(_ptr(x), _ptr(logits), r.T, ctypes.byref(wc), score._addr,
+                                      ctypes.byref(rc), _ptr(y), _ptr(ws), ws.numel(),
+                                      _stream(stream)))
 
 
 def moe_router_topk(x: torch.Tensor, w_router: torch.Tensor, out: RouteBuffers,
@@ -505,6 +584,57 @@ def _ints(fn, t, n, name):
     got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"
     raise ValueError(f"{fn}: {name} must be a contiguous int32 CUDA tensor of at least {n} "
                      f"values, got {got}")
+
+
+_NORM = struct.Struct("@PqqPqqPqqPqqPqqPPiiiiff")
+_NORM_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+
+
+def _norm_rows(fn, t, name, shape, dtype):
+    """(pointer, row stride, head stride) of [T][D] or [T][H][D] rows with dense elements."""
+    if t is not None and t.is_cuda and t.dtype is dtype and t.shape == shape:
+        st = t.stride()
+        if st[-1] == 1 or shape[-1] == 1:
+            return t.data_ptr(), st[0], st[1] if len(st) == 3 else 0
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
+    raise ValueError(f"{fn}: {name} must be a {dtype} CUDA tensor {tuple(shape)} with dense "
+                     f"elements, got {got}")
+
+
+def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor = None, out: torch.Tensor = None,
+                 add: torch.Tensor = None, sum: torch.Tensor = None, codes: torch.Tensor = None,
+                 scales: torch.Tensor = None, eps=1e-6, offset=0.0, stream=None) -> None:
+    """h = x + add (kept in ``sum``), y = h / rms(h) * (weight + offset) of each row of x [T, D]
+    or [T, H, D] (bf16, fp16 or fp32, strided rows) into ``out``, or as e4m3 ``codes`` with one
+    fp32 scale per row in ``scales`` [T] or [T, H], or both. sum and out may be x or add."""
+    fn = "moe_rms_norm"
+    dtype = None if x is None else _NORM_DTYPES.get(x.dtype)
+    if dtype is None or x.dim() not in (2, 3):
+        raise ValueError(f"{fn}: x must be a bfloat16, float16 or float32 tensor [T][D] or "
+                         f"[T][H][D], got {None if x is None else (x.dtype, tuple(x.shape))}")
+    shape, td = x.shape, x.dtype
+    xa = _norm_rows(fn, x, "x", shape, td)
+    none = (0, 0, 0)
+    aa = none if add is None else _norm_rows(fn, add, "add", shape, td)
+    sa = none if sum is None else _norm_rows(fn, sum, "sum", shape, td)
+    oa = none if out is None else _norm_rows(fn, out, "out", shape, td)
+    ca, scale = none, 0
+    if codes is not None:
+        ca = _norm_rows(fn, codes, "codes", shape, torch.float8_e4m3fn)
+        _need(fn, scales, torch.float32, "scales")
+        if scales.shape != shape[:-1]:
+            raise ValueError(f"{fn}: scales must be {tuple(shape[:-1])}, got {tuple(scales.shape)}")
+        scale = scales.data_ptr()
+    if weight is not None:
+        _need(fn, weight, td, "weight")
+        if weight.numel() != shape[-1]:
+            raise ValueError(f"{fn}: weight must hold {shape[-1]} values, got {weight.numel()}")
+    _here(fn, x, add, sum, out, codes, scales, weight)
+    a = _NORM.pack(*xa, *aa, *sa, *oa, *ca, scale, 0 if weight is None else weight.data_ptr(),
+                   shape[0], 1 if len(shape) == 2 else shape[1], shape[-1], dtype, eps, offset)
+    st = lib().moe_rms_norm(a, _stream(stream))
+    if st:
+        _check(fn, st)
 
 
 _ROPE_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
