@@ -327,6 +327,7 @@ moe_status moe_l2_prefetch(const void* ptr, size_t bytes, void* stream);
 #define MOE_BF16 0
 #define MOE_F16  1
 #define MOE_F32  2
+#define MOE_E4M3 3   /* 8 bits: 4 of exponent, 3 of mantissa, largest value 448, no infinity */
 
 /* Residual addition and root-mean-square norm of T tokens of H rows of D elements (H = 1:
  * hidden rows; H heads: per head):
@@ -355,6 +356,37 @@ typedef struct moe_norm {
  * aligned pointers and strides (codes: 8 bytes, or 4 for MOE_F32) take the vector path,
  * anything else one element per load. T = 0 launches nothing. */
 moe_status moe_rms_norm(const moe_norm* a, void* stream);
+
+/* Dense projection of T tokens with its epilogue:
+ *   y = act(x w^T + bias) + add,   e4m3: act(x_scale[t] w_scale[n] (x w^T) + bias) + add
+ * fp32 accumulation on the tensor cores, everything after it in fp32, one rounding. */
+#define MOE_ACT_NONE      0
+#define MOE_ACT_RELU      1
+#define MOE_ACT_SILU      2  /* y / (1 + exp(-y)) */
+#define MOE_ACT_GELU      3  /* y/2 (1 + erf(y / sqrt 2)) */
+#define MOE_ACT_GELU_TANH 4  /* y/2 (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))) */
+
+typedef struct moe_linear_args {
+  const void* x;    int64_t x_row;       /* dtype [T][K], row t at t*x_row elements */
+  const void* w;    int64_t w_row;       /* dtype [N][K] */
+  const float* x_scale;                  /* [T], MOE_E4M3 only (the scales of moe_rms_norm) */
+  const float* w_scale;                  /* [N], MOE_E4M3 only */
+  const float* bias;                     /* [N], or NULL */
+  const void* add;  int64_t add_row;     /* out_dtype [T][N], or NULL */
+  void* out;        int64_t out_row;     /* out_dtype [T][N] */
+  int32_t* err;                          /* device error word */
+  int32_t T, N, K;
+  int32_t dtype;                         /* MOE_BF16, MOE_F16 or MOE_E4M3 */
+  int32_t out_dtype;                     /* dtype or MOE_F32; any 16- or 32-bit type from MOE_E4M3 */
+  int32_t act;
+} moe_linear_args;
+
+/* One launch. x and w: 16-byte aligned, rows that do not overlap, strides and K multiples of
+ * 16 bytes; out and add: aligned to their type, any stride. K <= 2^20. add may be out with
+ * the same stride; out overlaps nothing else. T = 0 launches nothing. A token's result does
+ * not depend on the other tokens' values (an infinity or NaN stays in its row), but a
+ * batch of another size may add a row's products in another order. */
+moe_status moe_linear(const moe_linear_args* a, void* stream);
 
 /* Rotary positions. The first `rot` elements of a head form rot/2 pairs
  * (a_i, b_i): elements (i, i + rot/2), or (2i, 2i + 1) when interleaved. At

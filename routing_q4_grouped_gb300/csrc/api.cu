@@ -411,9 +411,26 @@ std::atomic<int> g_nevents{0};
 
 }  // namespace
 
-int32_t check_device() {
+int32_t check_device(int* sms) {
   DevInfo di;
-  return device_info(&di);
+  const moe_status st = device_info(&di);
+  if (sms) *sms = di.sms;
+  return st;
+}
+
+bool map_rows(CUtensorMap* m, int32_t dtype, const void* base, uint64_t K, uint64_t rows,
+              uint64_t stride_bytes, uint32_t box_k, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {K, rows}, strides[1] = {stride_bytes};
+  const cuuint32_t box[2] = {box_k, box_rows}, estr[2] = {1, 1};
+  return fn(m,
+            dtype == MOE_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+            : dtype == MOE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                               : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+            2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 uint64_t wait_timeout_ns() { return timeout_ns(); }

@@ -83,8 +83,13 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// MOE_ERR_UNSUPPORTED unless the current device is sm_103.
-int32_t check_device();
+// MOE_ERR_UNSUPPORTED unless the current device is sm_103; its multiprocessors.
+int32_t check_device(int* sms = nullptr);
+
+// Tensor map of `rows` rows of K elements (MOE_BF16, MOE_F16 or MOE_E4M3), stride_bytes apart,
+// copied in boxes of box_k elements (128 bytes) and box_rows rows in the 128-byte swizzle.
+bool map_rows(CUtensorMap* m, int32_t dtype, const void* base, uint64_t K, uint64_t rows,
+              uint64_t stride_bytes, uint32_t box_k, uint32_t box_rows);
 
 // Allows `kernel` its dynamic shared memory, once per device (bit d of `done`).
 template <typename Kernel>

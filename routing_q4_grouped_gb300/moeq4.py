@@ -28,7 +28,8 @@ MOE_DEVERR_BAD_SLOT = 32
 MOE_DEVERR_BAD_PAGE = 64
 MOE_DEVERR_BAD_LENGTH = 128
 MOE_ERR_TOO_LARGE = -8
-MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+MOE_BF16, MOE_F16, MOE_F32, MOE_E4M3 = 0, 1, 2, 3
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = 0, 1, 2, 3, 4
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_BASE, MOE_ROPE_BANDS = 0, 1, 2, 3
 
@@ -76,6 +77,14 @@ class NormC(ctypes.Structure):
                 ("eps", _c_f32), ("offset", _c_f32)]
 
 
+class LinearC(ctypes.Structure):
+    _fields_ = [("x", _c_ptr), ("x_row", _c_i64), ("w", _c_ptr), ("w_row", _c_i64),
+                ("x_scale", _c_ptr), ("w_scale", _c_ptr), ("bias", _c_ptr),
+                ("add", _c_ptr), ("add_row", _c_i64), ("out", _c_ptr), ("out_row", _c_i64),
+                ("err", _c_ptr), ("T", _c_i32), ("N", _c_i32), ("K", _c_i32), ("dtype", _c_i32),
+                ("out_dtype", _c_i32), ("act", _c_i32)]
+
+
 class RopeSpecC(ctypes.Structure):
     _fields_ = [("phase", _c_ptr), ("rot", _c_i32), ("interleaved", _c_i32), ("mscale", _c_f32)]
 
@@ -121,6 +130,7 @@ _SIGS = {
     "moe_layer_scored": (_c_i32, [_c_ptr, _c_ptr, _c_i32, ctypes.POINTER(Q4PackedC), _c_ptr,
                                   ctypes.POINTER(RouteOutC), _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "moe_rms_norm": (_c_i32, [_c_ptr, _c_ptr]),
+    "moe_linear": (_c_i32, [_c_ptr, _c_ptr]),
     "moe_route_noalloc": (_c_i32, [_c_ptr, ctypes.POINTER(RouteOutC), _c_ptr]),
     "moe_q4_packed_size": (_c_size, [_c_i32] * 4),
     "moe_q4_prepack": (_c_i32, [ctypes.POINTER(Q4WeightsC), _c_ptr, _c_size, _c_ptr]),
@@ -155,6 +165,7 @@ _SIGS = {
     "moe_debug_tmem_layout": (_c_i32, [_c_ptr, _c_ptr]),
     "moe_debug_kv_page": (_c_i32, [_c_i32, _c_i32]),
     "moe_debug_kv_attention_rows": (_c_i32, [_c_i32] * 7),
+    "moe_debug_linear_plan": (_c_i32, [_c_i32] * 5 + [_c_ptr]),
     "moe_debug_noalloc_scratch": (_c_i32, [ctypes.POINTER(_c_ptr), ctypes.POINTER(_c_size)]),
 }
 
@@ -637,6 +648,79 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor = None, out: torch.Tensor
         _check(fn, st)
 
 
+_LINEAR = struct.Struct("@PqPqPPPPqPqPiiiiii")
+_LINEAR_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float8_e4m3fn: MOE_E4M3}
+
+
+def _matrix(fn, t, name, rows, columns, dtype):
+    """(pointer, row stride) of [rows][columns] with dense elements."""
+    if t is not None and t.is_cuda and t.dtype is dtype and t.shape == (rows, columns):
+        st = t.stride()
+        if st[1] == 1 or columns == 1:
+            return t.data_ptr(), st[0]
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
+    raise ValueError(f"{fn}: {name} must be a {dtype} CUDA tensor [{rows}][{columns}] with dense "
+                     f"elements, got {got}")
+
+
+class Linear:
+    """Weights of a dense projection: ``weight`` [N, K] in bf16, fp16 or e4m3 (strided rows),
+    fp32 ``bias`` [N], fp32 ``scale`` [N] of e4m3 weights; ``err`` is the device error word of
+    the calls with it."""
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor = None, scale: torch.Tensor = None,
+                 err: torch.Tensor = None):
+        fn = "Linear"
+        dtype = None if weight is None else _LINEAR_DTYPES.get(weight.dtype)
+        if dtype is None or weight.dim() != 2:
+            raise ValueError(f"{fn}: weight must be a bfloat16, float16 or float8_e4m3fn matrix, got "
+                             f"{None if weight is None else (weight.dtype, tuple(weight.shape))}")
+        self.N, self.K = weight.shape
+        _, self._row = _matrix(fn, weight, "weight", self.N, self.K, weight.dtype)
+        for name, t in (("bias", bias), ("scale", scale)):
+            _need(fn, t, torch.float32, name, optional=True)
+            if t is not None and t.numel() != self.N:
+                raise ValueError(f"{fn}: {name} must hold {self.N} values, got {t.numel()}")
+        if (scale is not None) != (dtype == MOE_E4M3):
+            raise ValueError(f"{fn}: scale goes with e4m3 weights, got {weight.dtype}")
+        self.weight, self.bias, self.scale, self.dtype = weight, bias, scale, dtype
+        self.err = torch.zeros(4, dtype=torch.int32, device=weight.device) if err is None else err
+        _need(fn, self.err, torch.int32, "err")
+
+
+def moe_linear(x: torch.Tensor, linear: Linear, out: torch.Tensor, act=MOE_ACT_NONE,
+               add: torch.Tensor = None, x_scale: torch.Tensor = None, stream=None) -> None:
+    """out [T, N] = act(x [T, K] weight^T + bias) + add; e4m3 x takes its fp32 scales ``x_scale``
+    [T]. out and add are of x's type or fp32 (bf16, fp16 or fp32 where x is e4m3); add may be
+    out."""
+    fn = "moe_linear"
+    w = linear.weight
+    T = 0 if x is None or x.dim() != 2 else x.shape[0]
+    xp, xr = _matrix(fn, x, "x", T, linear.K, w.dtype)
+    out_dtype = None if out is None else _NORM_DTYPES.get(out.dtype)
+    if out_dtype is None:
+        raise ValueError(f"{fn}: out must be bfloat16, float16 or float32, got "
+                         f"{None if out is None else out.dtype}")
+    op, orow = _matrix(fn, out, "out", T, linear.N, out.dtype)
+    ap, arow = (0, 0) if add is None else _matrix(fn, add, "add", T, linear.N, out.dtype)
+    sp = 0
+    if linear.scale is not None:
+        _need(fn, x_scale, torch.float32, "x_scale")
+        if x_scale.numel() != T:
+            raise ValueError(f"{fn}: x_scale must hold {T} values, got {x_scale.numel()}")
+        sp = x_scale.data_ptr()
+    elif x_scale is not None:
+        raise ValueError(f"{fn}: x_scale goes with e4m3 inputs, got {x.dtype}")
+    _here(fn, x, w, out, add, x_scale)
+    a = _LINEAR.pack(xp, xr, w.data_ptr(), linear._row, sp,
+                     0 if linear.scale is None else linear.scale.data_ptr(),
+                     0 if linear.bias is None else linear.bias.data_ptr(), ap, arow, op, orow,
+                     linear.err.data_ptr(), T, linear.N, linear.K, linear.dtype, out_dtype, act)
+    st = lib().moe_linear(a, _stream(stream))
+    if st:
+        _check(fn, st)
+
+
 _ROPE_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
 
 
@@ -739,9 +823,9 @@ def moe_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens:
         _check(fn, st)
 
 
-def moe_get_device_error(r: "RouteBuffers | KVCache", stream=None) -> int:
-    """Synchronises the stream and returns the device error word of a routing result or a
-    cache (0 = none)."""
+def moe_get_device_error(r: "RouteBuffers | KVCache | Linear", stream=None) -> int:
+    """Synchronises the stream and returns the device error word of a routing result, a
+    cache or a projection (0 = none)."""
     code = _c_i32(0)
     s = lib().moe_get_device_error(_ptr(r.err), ctypes.byref(code), _stream(stream))
     if s not in (MOE_OK, -5):
@@ -775,6 +859,13 @@ def moe_debug_kv_page(page_size: int, slot: int) -> int:
 def moe_debug_kv_attention_rows(B, nq, Hq, Hkv, D, max_len, prefix_len=0) -> int:
     """1: the prefix, 2: the requests' own tokens go to the kernel for many query rows. Host only."""
     return lib().moe_debug_kv_attention_rows(B, nq, Hq, Hkv, D, max_len, prefix_len)
+
+
+def moe_debug_linear_plan(T, N, K, dtype=MOE_BF16, sms=152) -> dict:
+    """How moe_linear would lay out a call. Host only."""
+    v = (_c_i32 * 6)()
+    _check("moe_debug_linear_plan", lib().moe_debug_linear_plan(T, N, K, dtype, sms, v))
+    return dict(zip(("cols", "splits", "stages", "acc", "tcols", "smem"), v))
 
 
 def moe_debug_noalloc_scratch() -> tuple[int, int]:
