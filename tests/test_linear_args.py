@@ -82,7 +82,9 @@ def test_layouts_fit_the_multiprocessor(L, dtype):
                 assert p["tcols"] >= (p["acc"] if p["splits"] > 1 else 2 * p["acc"])
                 assert p["splits"] in (1, 2, 4, 8) and p["splits"] <= chunks
                 assert p["cols"] % p["splits"] == 0 and 2 <= p["stages"] <= 12
-                stage = (128 + p["cols"]) * 128
+                assert (p["mode"] == 1) == (p["splits"] > 1)
+                assert p["mode"] != 2 or p["cols"] % 32 == 0
+                stage = (128 + p["cols"] // (2 if p["mode"] == 2 else 1)) * 128
                 assert p["smem"] >= p["stages"] * stage + 1024 + \
                     (p["cols"] * 512 if p["splits"] > 1 else 0)
                 assert p["smem"] <= 227 * 1024
