@@ -100,14 +100,32 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
                : "memory");
 }
 
-// TMA load into this block's shared memory, completing on a barrier of the pair's block 0.
-__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t bar,
-                                              int32_t c0, int32_t c1, uint64_t cache_hint) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(cache_hint)
-      : "memory");
+// One K-chunk's copies: `bytes` expected on `bar`, features from row `fn` and tokens from row
+// `ft` at element c0 of K, issued by one elected lane of a converged warp from one asm block
+// (warp-uniform operands stay in uniform registers; behind a test of the lane each copy took
+// about 250 cycles to issue). PAIR: both blocks' copies complete on block 0's barrier, at
+// cluster address `bar`, and block 0 alone expects them (`expect`).
+template <bool PAIR>
+__device__ __forceinline__ void load_chunk(uint32_t dst_w, uint32_t dst_x, const CUtensorMap* tm_w,
+                                           const CUtensorMap* tm_x, uint32_t bar, uint32_t own_bar,
+                                           uint32_t bytes, bool expect, int32_t c0, int32_t fn,
+                                           int32_t ft, uint64_t pol_w, uint64_t pol_x) {
+#define MOEQ4_LOAD(GROUP)                                                                        \
+  asm volatile(                                                                                  \
+      "{\n\t.reg .pred e, p;\n\tsetp.ne.b32 p, %7, 0;\n\t"                                       \
+      "elect.sync _|e, 0xffffffff;\n\tand.pred p, p, e;\n\t"                                     \
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"                            \
+      "@e cp.async.bulk.tensor.2d" GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::"  \
+      "bytes.L2::cache_hint [%0], [%2, {%8, %9}], [%4], %11;\n\t"                                \
+      "@e cp.async.bulk.tensor.2d" GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::"  \
+      "bytes.L2::cache_hint [%1], [%3, {%8, %10}], [%4], %12;\n\t}" ::"r"(dst_w),                \
+      "r"(dst_x), "l"(reinterpret_cast<uint64_t>(tm_w)), "l"(reinterpret_cast<uint64_t>(tm_x)),  \
+      "r"(bar), "r"(own_bar), "r"(bytes), "r"(static_cast<uint32_t>(expect)), "r"(c0), "r"(fn),  \
+      "r"(ft), "l"(pol_w), "l"(pol_x)                                                            \
+      : "memory")
+  if constexpr (PAIR) MOEQ4_LOAD(".cta_group::2");
+  else MOEQ4_LOAD("");
+#undef MOEQ4_LOAD
 }
 
 // One K-chunk (4 steps of 32 bytes of K) of D[features, tokens] += W X^T, issued by one
@@ -327,60 +345,58 @@ __global__ void __launch_bounds__(kThreads)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_last();
-      int it = 0;                            // chunks requested
-      for (int tile = first; tile < tiles && ok; tile += step) {
-        int fn, ft;
-        tile_at(a, tile, fn, ft);
-        const int tn = fn * fw + f0;
-        const int tt = ft * a.cols + (kIsPair ? static_cast<int>(rank) * (a.cols / 2) : 0);
-        for (int c = c_lo; c < c_hi; ++c, ++it) {
-          const int s = it % ns;
-          if (!mbar_wait(&ctl.empty[s], ((it / ns) & 1) ^ 1, abortp, lim)) {
-            ok = false;
-            break;
-          }
-          uint8_t* st = smem + static_cast<size_t>(s) * sb;
-          constexpr int kElems = E4M3 ? kChunk : kChunk / 2;
-          if constexpr (kIsPair) {
-            // both blocks' copies complete on block 0's barrier, which expects them all
-            if (rank == 0) mbar_arrive_expect_tx(&ctl.full[s], 2 * sb);
-            const uint32_t bar = peer_addr(smem_u32(&ctl.full[s]), 0);
-            tma_load_pair(st, &tm_w, bar, c * kElems, tn, pol);
-            tma_load_pair(st + kRows * kChunk, &tm_x, bar, c * kElems, tt, pol);
-          } else {
-            mbar_arrive_expect_tx(&ctl.full[s], sb);
-            tma_load_2d(st, &tm_w, &ctl.full[s], c * kElems, tn, pol);
-            tma_load_2d(st + kRows * kChunk, &tm_x, &ctl.full[s], c * kElems, tt, pol);
-          }
+    const uint64_t pol = policy_evict_last();
+    int st = 0, issued = 0;                  // stage, chunks requested
+    uint32_t ph = 1;                         // parity of the phase before the stage's next use
+    for (int tile = first; tile < tiles && ok; tile += step) {
+      int fn, ft;
+      tile_at(a, tile, fn, ft);
+      const int tn = fn * fw + f0;
+      const int tt = ft * a.cols + (kIsPair ? static_cast<int>(rank) * (a.cols / 2) : 0);
+      for (int c = c_lo; c < c_hi; ++c, ++issued) {
+        ok = __all_sync(kFull, mbar_wait(&ctl.empty[st], ph, abortp, lim));
+        if (!ok) break;
+        const uint32_t dst = smem_u32(smem) + st * sb, bar = smem_u32(&ctl.full[st]);
+        constexpr int kElems = E4M3 ? kChunk : kChunk / 2;
+        load_chunk<kIsPair>(dst, dst + kRows * kChunk, &tm_w, &tm_x,
+                            kIsPair ? peer_addr(bar, 0) : bar, bar, kIsPair ? 2 * sb : sb,
+                            !kIsPair || rank == 0, c * kElems, tn, tt, pol, pol);
+        if (++st == ns) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      if (!ok && atomicExch(&ctl.abort, 1) == 0) atomicOr(a.err, MOE_DEVERR_PIPE_TIMEOUT);
-      // Every copy has landed, and been multiplied, before the block's shared memory goes away.
-      for (int i = 1; i <= min(it, ns); ++i) {
-        const int c = it - i;
-        mbar_wait(&ctl.empty[c % ns], (c / ns) & 1, &ctl.zero, 20000000ull);
-      }
+    }
+    if (!ok && lane == 0 && atomicExch(&ctl.abort, 1) == 0)
+      atomicOr(a.err, MOE_DEVERR_PIPE_TIMEOUT);
+    // Every copy has landed, and been multiplied, before the block's shared memory goes away:
+    // the last use of each stage, oldest first.
+    for (int i = min(issued, ns); i > 0; --i) {
+      const int c = issued - i;
+      mbar_wait(&ctl.empty[c % ns], (c / ns) & 1, &ctl.zero, 20000000ull);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer
     if (rank == 0 || kIsSplit) {
-      int it = 0, i = 0;                     // chunks and tiles multiplied
+      int st = 0, i = 0;                     // stage, tiles multiplied
+      uint32_t ph = 0;
       for (int tile = first; tile < tiles && ok; tile += step, ++i) {
         const int b = i & 1;
         ok = __all_sync(kFull, mbar_wait(&ctl.acc_empty[b], ((i >> 1) & 1) ^ 1, abortp, lim));
         tc_fence_after();
-        for (int c = c_lo; c < c_hi && ok; ++c, ++it) {
-          const int s = it % ns;
-          ok = __all_sync(kFull, mbar_wait(&ctl.full[s], (it / ns) & 1, abortp, lim));
+        for (int c = c_lo; c < c_hi && ok; ++c) {
+          ok = __all_sync(kFull, mbar_wait(&ctl.full[st], ph, abortp, lim));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + static_cast<size_t>(s) * sb);
+          const uint32_t sa = smem_u32(smem) + st * sb;
           mma_chunk<E4M3, kIsPair>(tmem + b * a.acc, sdesc_k_sw128(sa),
                                    sdesc_k_sw128(sa + kRows * kChunk), a.idesc, c != c_lo);
-          commit<kIsPair>(&ctl.empty[s]);
+          commit<kIsPair>(&ctl.empty[st]);
+          if (++st == ns) {
+            st = 0;
+            ph ^= 1;
+          }
         }
         if (ok) commit<kIsPair>(&ctl.acc_full[b]);
       }
