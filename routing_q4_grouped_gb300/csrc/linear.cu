@@ -9,7 +9,7 @@
 //
 // A block keeps a ring of K-chunks (128 bytes of K of both operands, 128-byte swizzle)
 // that one thread fills by TMA and one warp feeds to the tensor cores; two accumulators in
-// tensor memory let eight warps finish a tile while the next one is multiplied. Three modes:
+// tensor memory let 16 warps finish a tile while the next one is multiplied. Three modes:
 //   kSingle  a block per tile, each block several tiles
 //   kSplit   too few tiles for the multiprocessors: a cluster of 2, 4 or 8 blocks splits K;
 //            each sends its partial sums to the block that finishes their tokens through
@@ -33,7 +33,10 @@ namespace moeq4 {
 namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
-constexpr int kEpiWarps = 8;               // two per tensor-memory lane quarter
+constexpr int kEpiWarps = 16;              // four per tensor-memory lane quarter: an epilogue is
+                                           // latency (8 warps: 4096 x 2048 -> 8192 with gelu
+                                           // 106 us, with a residual 100; 16: 92 and 86)
+constexpr int kParts = kEpiWarps / 4;      // warps that share a tile's tokens
 constexpr int kThreads = 64 + 32 * kEpiWarps;   // warp 0: producer, warp 1: MMA issuer
 constexpr int kRows = 128;                 // features per tile (MMA M)
 constexpr int kChunk = 128;                // bytes of K per stage and row
@@ -207,6 +210,17 @@ __device__ __forceinline__ __half to_out(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ float to_out(float v) { return v; }
 
+// erf(x) to 1.5e-7 (M. Abramowitz and I. A. Stegun, "Handbook of Mathematical Functions",
+// 1964, 7.1.26): a third of erff's instructions, next to results of 16 bits.
+__device__ __forceinline__ float erf_near(float x) {
+  const float z = fabsf(x), t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  return copysignf(fmaf(-p * t, __expf(-z * z), 1.f), x);
+}
+
 template <int M>
 __device__ __forceinline__ void activate(float (&v)[M], int act) {
   switch (act) {
@@ -215,18 +229,22 @@ __device__ __forceinline__ void activate(float (&v)[M], int act) {
       for (int j = 0; j < M; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];   // (NaN stays)
       break;
     case MOE_ACT_SILU:
+      // (a denominator above 2^126 gives 0, which the quotient has rounded to long before)
 #pragma unroll
-      for (int j = 0; j < M; ++j) v[j] = v[j] / (1.f + expf(-v[j]));
+      for (int j = 0; j < M; ++j) v[j] = __fdividef(v[j], 1.f + __expf(-v[j]));
       break;
     case MOE_ACT_GELU:
 #pragma unroll
-      for (int j = 0; j < M; ++j) v[j] = 0.5f * v[j] * (1.f + erff(v[j] * 0.70710678118654752f));
+      for (int j = 0; j < M; ++j)
+        v[j] = 0.5f * v[j] * (1.f + erf_near(v[j] * 0.70710678118654752f));
       break;
     case MOE_ACT_GELU_TANH:
+      // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
 #pragma unroll
-      for (int j = 0; j < M; ++j)
-        v[j] = 0.5f * v[j] *
-               (1.f + tanhf(0.79788456080286536f * fmaf(0.044715f * v[j] * v[j], v[j], v[j])));
+      for (int j = 0; j < M; ++j) {
+        const float u = 0.79788456080286536f * fmaf(0.044715f * v[j] * v[j], v[j], v[j]);
+        v[j] = __fdividef(v[j], 1.f + __expf(-2.f * u));
+      }
       break;
     default: break;
   }
@@ -234,42 +252,54 @@ __device__ __forceinline__ void activate(float (&v)[M], int act) {
 
 // M tokens t, t + step, ... of one feature n, of which the first `live` exist: what the
 // epilogue reads of them (all loads before any store), and the results from their sums.
+// Called by whole warps: a token's scale is held by one lane.
 template <bool E4M3, typename O, int M>
 struct Tokens {
   O add[M];
-  float xs[M];
+  float scale;               // of token t + lane * step
 
   __device__ __forceinline__ void load(const LinearArgs& a, int64_t t, int step, int live, int n,
                                        bool in) {
     if (E4M3) {
-#pragma unroll
-      for (int j = 0; j < M; ++j) xs[j] = j < live ? a.x_scale[t + j * step] : 0.f;
+      const int lane = static_cast<int>(threadIdx.x & 31);
+      scale = lane < min(live, M) ? a.x_scale[t + lane * step] : 0.f;
     }
     if (a.add && in) {
+      const int64_t row = step * a.add_row;
       const O* p = static_cast<const O*>(a.add) + t * a.add_row + n;
+      if (live >= M) {
 #pragma unroll
-      for (int j = 0; j < M; ++j)
-        if (j < live) add[j] = p[j * step * a.add_row];
+        for (int j = 0; j < M; ++j, p += row) add[j] = *p;
+      } else {
+#pragma unroll
+        for (int j = 0; j < M; ++j, p += row)
+          if (j < live) add[j] = *p;
+      }
     }
   }
   __device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[M], int64_t t, int step,
                                          int live, int n, bool in, float ws, float bias) {
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      if (E4M3) v[j] = v[j] * xs[j] * ws;
+      if (E4M3) v[j] = v[j] * __shfl_sync(kFull, scale, j) * ws;
       v[j] += bias;
     }
     activate(v, a.act);
     if (!in) return;
     if (a.add) {
 #pragma unroll
-      for (int j = 0; j < M; ++j)
-        if (j < live) v[j] += to_f(add[j]);
+      for (int j = 0; j < M; ++j) v[j] += to_f(add[j]);     // (not stored where j >= live)
     }
+    const int64_t row = step * a.out_row;
     O* o = static_cast<O*>(a.out) + t * a.out_row + n;
+    if (live >= M) {
 #pragma unroll
-    for (int j = 0; j < M; ++j)
-      if (j < live) o[j * step * a.out_row] = to_out<O>(v[j]);
+      for (int j = 0; j < M; ++j, o += row) *o = to_out<O>(v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < M; ++j, o += row)
+        if (j < live) *o = to_out<O>(v[j]);
+    }
   }
 };
 
@@ -410,8 +440,8 @@ __global__ void __launch_bounds__(kThreads)
   } else {
     // ---------------------------------------------------------------- epilogue
     // warp w reads tensor-memory lanes 32 (w % 4) .. (features n, one per lane) and every
-    // second batch of tokens
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    // kParts-th batch of tokens
+    const int q = warp & 3, part = (warp - 2) >> 2;
     int i = 0;
     for (int tile = first; tile < tiles && ok; tile += step, ++i) {
       const int b = i & 1;
@@ -426,7 +456,7 @@ __global__ void __launch_bounds__(kThreads)
       if constexpr (!kIsSplit) {
         bias = in && a.bias ? a.bias[n] : 0.f;
         ws = in && E4M3 ? a.w_scale[n] : 1.f;
-        next.load(a, t0 + half * kBatch, 1, live - half * kBatch, n, in);
+        next.load(a, t0 + part * kBatch, 1, live - part * kBatch, n, in);
       }
       ok = __all_sync(kFull, mbar_wait(&ctl.acc_full[b], (i >> 1) & 1, abortp, lim));
       if (!ok) break;
@@ -435,7 +465,7 @@ __global__ void __launch_bounds__(kThreads)
       if constexpr (kIsSplit) cluster_wait();   // every block of the cluster has started
       const int per = a.cols / static_cast<int>(group);
       const int inv = (65536 + per - 1) / per;  // x / per = x inv >> 16 for x < 128
-      for (int c = half * kBatch; c < live; c += 2 * kBatch) {
+      for (int c = part * kBatch; c < live; c += kParts * kBatch) {
         uint32_t v[kBatch];
         tmem_ld_32x32b_x16(taddr + c, v);
         if constexpr (kIsSplit) {
@@ -451,7 +481,7 @@ __global__ void __launch_bounds__(kThreads)
           }
         } else {
           Tokens<E4M3, O, kBatch> now = next;
-          next.load(a, t0 + c + 2 * kBatch, 1, live - c - 2 * kBatch, n, in);
+          next.load(a, t0 + c + kParts * kBatch, 1, live - c - kParts * kBatch, n, in);
           tmem_ld_wait();
           tmem_regs_ready(v);
           float y[kBatch];
@@ -479,34 +509,35 @@ __global__ void __launch_bounds__(kThreads)
       st_peer(peer_addr(smem_u32(&ctl.peer_ok[rank][warp - 2]), lane), ok ? 1u : 0u);
     __syncwarp();
     cluster_arrive();
-    constexpr int kM = 8;                    // tokens at once, every second one of the block's
+    constexpr int kM = 8;                    // tokens at once, every kParts-th of the block's
     const int per = a.cols / static_cast<int>(group);
-    const int half = (warp - 2) >> 2, f = (warp & 3) * 32 + lane, n = n0 + f;
+    const int part = (warp - 2) >> 2, f = (warp & 3) * 32 + lane, n = n0 + f;
     const int tb = t0 + static_cast<int>(rank) * per;      // this block's first token
     const int live = min(per, a.T - tb);
     const bool in = n < a.N;
+    const auto left = [&](int at) { return live > at ? (live - at + kParts - 1) / kParts : 0; };
     Tokens<E4M3, O, kM> now;
     float bias = 0.f, ws = 1.f;
     if (warp >= 2) {
       bias = in && a.bias ? a.bias[n] : 0.f;
       ws = in && E4M3 ? a.w_scale[n] : 1.f;
-      now.load(a, tb + half, 2, (live - half + 1) / 2, n, in);
+      now.load(a, tb + part, kParts, left(part), n, in);
     }
     cluster_wait();
     if (warp >= 2) {
-      bool all = true;
+      bool all = true;                       // partial sums of these features
       for (uint32_t r = 0; r < group; ++r)
-        all = all && ctl.peer_ok[r][warp - 2] != 0 && ctl.peer_ok[r][(warp - 2) ^ 4] != 0;
-      for (int at = half; at < live && all; at += 2 * kM) {
-        if (at != half) now.load(a, tb + at, 2, (live - at + 1) / 2, n, in);
+        for (int p = 0; p < kParts; ++p) all = all && ctl.peer_ok[r][((warp - 2) & 3) + 4 * p] != 0;
+      for (int at = part; at < live && all; at += kParts * kM) {
+        if (at != part) now.load(a, tb + at, kParts, left(at), n, in);
         float y[kM];
 #pragma unroll
         for (int j = 0; j < kM; ++j) {
           y[j] = 0.f;
-          if (at + 2 * j < live)
-            for (uint32_t r = 0; r < group; ++r) y[j] += parts[(r * per + at + 2 * j) * kRows + f];
+          if (at + kParts * j < live)
+            for (uint32_t r = 0; r < group; ++r) y[j] += parts[(r * per + at + kParts * j) * kRows + f];
         }
-        now.finish(a, y, tb + at, 2, (live - at + 1) / 2, n, in, ws, bias);
+        now.finish(a, y, tb + at, kParts, left(at), n, in, ws, bias);
       }
     }
   }
