@@ -12,8 +12,8 @@
 // tensor memory let 16 warps finish a tile while the next one is multiplied. Three modes:
 //   kSingle  a block per tile, each block several tiles
 //   kSplit   too few tiles for the multiprocessors: a cluster of 2, 4 or 8 blocks splits K;
-//            each sends its partial sums to the block that finishes their tokens through
-//            distributed shared memory, where they are added in the order of the blocks
+//            each finishes a share of the tokens, reading the others' partial sums from their
+//            shared memory, in the order of the blocks
 //   kPair    many tiles: two blocks on neighbouring multiprocessors multiply one tile of 256
 //            features (cta_group::2); each holds its 128 features and half of the tokens, so
 //            a chunk of 256 x 256 costs each of them 32 KB of copies instead of 48
@@ -56,6 +56,7 @@ struct LinearArgs {
   int tiles_n, tiles_t;
   int band;                  // feature tiles that are gone through together for every token tile
   int stages;
+  int sub;                   // K-chunks per stage
   int acc, tcols;            // tensor-memory columns per accumulator, and of all (powers of two)
   uint32_t idesc;
   const float *x_scale, *w_scale, *bias;
@@ -73,7 +74,6 @@ struct Ctl {
   uint64_t drained;
   uint32_t tmem;
   int abort, zero;
-  uint32_t peer_ok[kMaxSplit][kEpiWarps];    // [block][warp]: its partial sums were sent
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -86,8 +86,10 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(saddr), "r"(rank));
   return d;
 }
-__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ uint32_t ld_peer(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -103,28 +105,27 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
                : "memory");
 }
 
-// One K-chunk's copies: `bytes` expected on `bar`, features from row `fn` and tokens from row
-// `ft` at element c0 of K, issued by one elected lane of a converged warp from one asm block
-// (warp-uniform operands stay in uniform registers; behind a test of the lane each copy took
-// about 250 cycles to issue). PAIR: both blocks' copies complete on block 0's barrier, at
-// cluster address `bar`, and block 0 alone expects them (`expect`).
+// One K-chunk's copies: features from row `fn` and tokens from row `ft` at element c0 of K,
+// completing on `bar`, on which `bytes` are expected first (0: they have been), issued by one
+// elected lane of a converged warp from one asm block (warp-uniform operands stay in uniform
+// registers; behind a test of the lane a chunk took 261 ns to issue, so 127). PAIR: both blocks'
+// copies complete on block 0's barrier, at cluster address `bar`, and block 0 expects them all.
 template <bool PAIR>
 __device__ __forceinline__ void load_chunk(uint32_t dst_w, uint32_t dst_x, const CUtensorMap* tm_w,
                                            const CUtensorMap* tm_x, uint32_t bar, uint32_t own_bar,
-                                           uint32_t bytes, bool expect, int32_t c0, int32_t fn,
-                                           int32_t ft, uint64_t pol_w, uint64_t pol_x) {
+                                           uint32_t bytes, int32_t c0, int32_t fn, int32_t ft,
+                                           uint64_t pol) {
 #define MOEQ4_LOAD(GROUP)                                                                        \
   asm volatile(                                                                                  \
-      "{\n\t.reg .pred e, p;\n\tsetp.ne.b32 p, %7, 0;\n\t"                                       \
+      "{\n\t.reg .pred e, p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                       \
       "elect.sync _|e, 0xffffffff;\n\tand.pred p, p, e;\n\t"                                     \
       "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"                            \
       "@e cp.async.bulk.tensor.2d" GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::"  \
-      "bytes.L2::cache_hint [%0], [%2, {%8, %9}], [%4], %11;\n\t"                                \
+      "bytes.L2::cache_hint [%0], [%2, {%7, %8}], [%4], %10;\n\t"                                \
       "@e cp.async.bulk.tensor.2d" GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::"  \
-      "bytes.L2::cache_hint [%1], [%3, {%8, %10}], [%4], %12;\n\t}" ::"r"(dst_w),                \
+      "bytes.L2::cache_hint [%1], [%3, {%7, %9}], [%4], %10;\n\t}" ::"r"(dst_w),                 \
       "r"(dst_x), "l"(reinterpret_cast<uint64_t>(tm_w)), "l"(reinterpret_cast<uint64_t>(tm_x)),  \
-      "r"(bar), "r"(own_bar), "r"(bytes), "r"(static_cast<uint32_t>(expect)), "r"(c0), "r"(fn),  \
-      "r"(ft), "l"(pol_w), "l"(pol_x)                                                            \
+      "r"(bar), "r"(own_bar), "r"(bytes), "r"(c0), "r"(fn), "r"(ft), "l"(pol)                    \
       : "memory")
   if constexpr (PAIR) MOEQ4_LOAD(".cta_group::2");
   else MOEQ4_LOAD("");
@@ -303,8 +304,8 @@ struct Tokens {
   }
 };
 
-// Bytes of a ring stage: 128 features, and the tokens of a tile (kPair: half of them).
-__host__ __device__ inline int stage_bytes(int cols, int mode) {
+// Bytes of a K-chunk: 128 features, and the tokens of a tile (kPair: half of them).
+__host__ __device__ inline int chunk_bytes(int cols, int mode) {
   return (kRows + (mode == kPair ? cols / 2 : cols)) * kChunk;
 }
 
@@ -325,11 +326,8 @@ __global__ void __launch_bounds__(kThreads)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const int sb = stage_bytes(a.cols, MODE), ns = a.stages;
-  // behind the ring: partial sums [source block][token][feature] (kSplit), then control
-  float* parts = reinterpret_cast<float*>(smem + static_cast<size_t>(ns) * sb);
-  Ctl& ctl = *reinterpret_cast<Ctl*>(reinterpret_cast<uint8_t*>(parts) +
-                                     (kIsSplit ? static_cast<size_t>(a.cols) * kRows * 4 : 0));
+  const int cb = chunk_bytes(a.cols, MODE), sb = a.sub * cb, ns = a.stages;
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem + static_cast<size_t>(ns) * sb);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t group = 1, rank = 0;              // blocks that share a tile
   if constexpr (MODE != kSingle) {
@@ -356,10 +354,10 @@ __global__ void __launch_bounds__(kThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (MODE != kSingle) cluster_arrive();   // (this block's barriers and memory may be used)
-  if constexpr (kIsPair) cluster_wait();
-  griddep_wait();
-  griddep_launch_dependents();
+  if constexpr (kIsPair) {                   // the other block's barriers are set up
+    cluster_arrive();
+    cluster_wait();
+  }
   const uint32_t tmem = ctl.tmem;
   const volatile int* abortp = &ctl.abort;
   const uint64_t lim = a.timeout_ns;
@@ -370,27 +368,33 @@ __global__ void __launch_bounds__(kThreads)
   const int c_hi = kIsSplit ? static_cast<int>(static_cast<int64_t>(a.nch) * (rank + 1) / group) : a.nch;
   const int fw = kRows * (kIsPair ? 2 : 1);  // features of a tile
   const int f0 = kIsPair ? static_cast<int>(rank) * kRows : 0;   // this block's first one in it
+  constexpr int kElems = E4M3 ? kChunk : kChunk / 2;
+  griddep_wait();
+  griddep_launch_dependents();
   bool ok = true;
   int n0 = 0, t0 = 0;                        // of the tile that the epilogue holds at the end
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     const uint64_t pol = policy_evict_last();
-    int st = 0, issued = 0;                  // stage, chunks requested
+    int st = 0, issued = 0;                  // stage, stages filled
     uint32_t ph = 1;                         // parity of the phase before the stage's next use
     for (int tile = first; tile < tiles && ok; tile += step) {
       int fn, ft;
       tile_at(a, tile, fn, ft);
       const int tn = fn * fw + f0;
       const int tt = ft * a.cols + (kIsPair ? static_cast<int>(rank) * (a.cols / 2) : 0);
-      for (int c = c_lo; c < c_hi; ++c, ++issued) {
+      for (int c = c_lo; c < c_hi; c += a.sub, ++issued) {
         ok = __all_sync(kFull, mbar_wait(&ctl.empty[st], ph, abortp, lim));
         if (!ok) break;
-        const uint32_t dst = smem_u32(smem) + st * sb, bar = smem_u32(&ctl.full[st]);
-        constexpr int kElems = E4M3 ? kChunk : kChunk / 2;
-        load_chunk<kIsPair>(dst, dst + kRows * kChunk, &tm_w, &tm_x,
-                            kIsPair ? peer_addr(bar, 0) : bar, bar, kIsPair ? 2 * sb : sb,
-                            !kIsPair || rank == 0, c * kElems, tn, tt, pol, pol);
+        const uint32_t own_bar = smem_u32(&ctl.full[st]);
+        const uint32_t bar = kIsPair ? peer_addr(own_bar, 0) : own_bar;
+        const int n = min(a.sub, c_hi - c);
+        uint32_t dst = smem_u32(smem) + st * sb;
+        uint32_t bytes = !kIsPair ? n * cb : rank == 0 ? 2 * n * cb : 0;
+        for (int u = 0; u < n; ++u, dst += cb, bytes = 0)
+          load_chunk<kIsPair>(dst, dst + kRows * kChunk, &tm_w, &tm_x, bar, own_bar, bytes,
+                              (c + u) * kElems, tn, tt, pol);
         if (++st == ns) {
           st = 0;
           ph ^= 1;
@@ -415,13 +419,15 @@ __global__ void __launch_bounds__(kThreads)
         const int b = i & 1;
         ok = __all_sync(kFull, mbar_wait(&ctl.acc_empty[b], ((i >> 1) & 1) ^ 1, abortp, lim));
         tc_fence_after();
-        for (int c = c_lo; c < c_hi && ok; ++c) {
+        for (int c = c_lo; c < c_hi && ok; c += a.sub) {
           ok = __all_sync(kFull, mbar_wait(&ctl.full[st], ph, abortp, lim));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem) + st * sb;
-          mma_chunk<E4M3, kIsPair>(tmem + b * a.acc, sdesc_k_sw128(sa),
-                                   sdesc_k_sw128(sa + kRows * kChunk), a.idesc, c != c_lo);
+          const int n = min(a.sub, c_hi - c);
+          uint32_t sa = smem_u32(smem) + st * sb;
+          for (int u = 0; u < n; ++u, sa += cb)
+            mma_chunk<E4M3, kIsPair>(tmem + b * a.acc, sdesc_k_sw128(sa),
+                                     sdesc_k_sw128(sa + kRows * kChunk), a.idesc, c + u != c_lo);
           commit<kIsPair>(&ctl.empty[st]);
           if (++st == ns) {
             st = 0;
@@ -462,23 +468,16 @@ __global__ void __launch_bounds__(kThreads)
       if (!ok) break;
       tc_fence_after();
       const uint32_t taddr = tmem + b * a.acc + (static_cast<uint32_t>(q * 32) << 16);
-      if constexpr (kIsSplit) cluster_wait();   // every block of the cluster has started
-      const int per = a.cols / static_cast<int>(group);
-      const int inv = (65536 + per - 1) / per;  // x / per = x inv >> 16 for x < 128
       for (int c = part * kBatch; c < live; c += kParts * kBatch) {
         uint32_t v[kBatch];
         tmem_ld_32x32b_x16(taddr + c, v);
         if constexpr (kIsSplit) {
+          // partial sums [token][feature] over the ring, which nothing uses any more
           tmem_ld_wait();
           tmem_regs_ready(v);
-          // tokens [r per, r per + per) are finished by block r
+          uint32_t* part_sums = reinterpret_cast<uint32_t*>(smem) + c * kRows + q * 32 + lane;
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            if (c + j >= live) break;
-            const int owner = (c + j) * inv >> 16, at = c + j - owner * per;
-            st_peer(peer_addr(smem_u32(parts + (rank * per + at) * kRows + q * 32 + lane), owner),
-                    v[j]);
-          }
+          for (int j = 0; j < kBatch; ++j) part_sums[j * kRows] = v[j];
         } else {
           Tokens<E4M3, O, kBatch> now = next;
           next.load(a, t0 + c + kParts * kBatch, 1, live - c - kParts * kBatch, n, in);
@@ -502,44 +501,52 @@ __global__ void __launch_bounds__(kThreads)
       atomicOr(a.err, MOE_DEVERR_PIPE_TIMEOUT);
   }
   if constexpr (kIsSplit) {
-    // one tile per cluster. Each barrier is reached by every thread, whatever happened before
-    // it; the epilogue's warps passed the first one above unless they gave up.
-    if (warp < 2 || !ok) cluster_wait();
-    if (warp >= 2 && lane < group)
-      st_peer(peer_addr(smem_u32(&ctl.peer_ok[rank][warp - 2]), lane), ok ? 1u : 0u);
-    __syncwarp();
-    cluster_arrive();
-    constexpr int kM = 8;                    // tokens at once, every kParts-th of the block's
+    // One tile per cluster. Every thread reaches the barriers, whatever happened before them.
     const int per = a.cols / static_cast<int>(group);
     const int part = (warp - 2) >> 2, f = (warp & 3) * 32 + lane, n = n0 + f;
-    const int tb = t0 + static_cast<int>(rank) * per;      // this block's first token
-    const int live = min(per, a.T - tb);
+    const int at0 = static_cast<int>(rank) * per;          // this block's first token of the tile
+    const int live = min(per, a.T - t0 - at0);
     const bool in = n < a.N;
+    constexpr int kM = 2;                    // tokens at once (little code: it runs once or twice)
     const auto left = [&](int at) { return live > at ? (live - at + kParts - 1) / kParts : 0; };
     Tokens<E4M3, O, kM> now;
     float bias = 0.f, ws = 1.f;
     if (warp >= 2) {
       bias = in && a.bias ? a.bias[n] : 0.f;
       ws = in && E4M3 ? a.w_scale[n] : 1.f;
-      now.load(a, tb + part, kParts, left(part), n, in);
+      now.load(a, t0 + at0 + part, kParts, left(part), n, in);
     }
+    __syncwarp();
+    cluster_arrive();                        // the partial sums are written
     cluster_wait();
     if (warp >= 2) {
-      bool all = true;                       // partial sums of these features
-      for (uint32_t r = 0; r < group; ++r)
-        for (int p = 0; p < kParts; ++p) all = all && ctl.peer_ok[r][((warp - 2) & 3) + 4 * p] != 0;
+      // a block that gave up has no sums
+      bool all = true;
+      if (lane < group) all = ld_peer(peer_addr(smem_u32(&ctl.abort), lane)) == 0;
+      all = __all_sync(kFull, all);
       for (int at = part; at < live && all; at += kParts * kM) {
-        if (at != part) now.load(a, tb + at, kParts, left(at), n, in);
+        if (at != part) now.load(a, t0 + at0 + at, kParts, left(at), n, in);
         float y[kM];
 #pragma unroll
         for (int j = 0; j < kM; ++j) {
+          // (past the block's tokens: sums of another block's, or of no token, not written)
+          const uint32_t place =
+              smem_u32(smem) + (min(at0 + at + kParts * j, a.cols - 1) * kRows + f) * 4;
+          uint32_t p[kMaxSplit];
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r)
+            if (r < static_cast<int>(group)) p[r] = ld_peer(peer_addr(place, r));
           y[j] = 0.f;
-          if (at + kParts * j < live)
-            for (uint32_t r = 0; r < group; ++r) y[j] += parts[(r * per + at + kParts * j) * kRows + f];
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r)
+            if (r < static_cast<int>(group)) y[j] += __uint_as_float(p[r]);
         }
-        now.finish(a, y, tb + at, kParts, left(at), n, in, ws, bias);
+        now.finish(a, y, t0 + at0 + at, kParts, left(at), n, in, ws, bias);
       }
     }
+    __syncwarp();
+    cluster_arrive();                        // nothing of the others' memory is read any more
+    cluster_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -554,9 +561,121 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// -------------------------------------------------------------- few tokens
+//
+// Up to 16 tokens the weights' bytes are the work. A block takes 16 features, and its warps
+// share out K: each multiplies 128 bytes of K of the 16 rows at a time by mma.sync, with the
+// tokens as the 8-wide operand. A sum over K may be taken in any order, so a lane loads 16
+// consecutive bytes of a row and uses them as the k-slots of two products; the tokens' lanes
+// load the same places of x. No shared memory, barrier or copy engine stands between the loads
+// and the products; the warps' sums meet in shared memory once, in the order of the warps.
+
+constexpr int kFewWarps = 16;              // at most
+constexpr int kFewRows = 16;
+
+template <bool E4M3, bool HALF>
+__device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+#define MOEQ4_MMA_SYNC(OP)                                                                      \
+  asm(OP " {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                     \
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                          \
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+  if constexpr (E4M3) MOEQ4_MMA_SYNC("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32");
+  else if constexpr (HALF) MOEQ4_MMA_SYNC("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32");
+  else MOEQ4_MMA_SYNC("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32");
+#undef MOEQ4_MMA_SYNC
+}
+
+struct FewArgs {
+  const uint8_t *x, *w;
+  int64_t x_row, w_row;      // bytes
+  int k_bytes;               // of a row, a multiple of 16
+  int early;                 // blocks that prefetch
+  LinearArgs l;
+};
+
+// NT groups of 8 tokens.
+template <bool E4M3, bool HALF, typename O, int NT>
+__global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const FewArgs a) {
+  __shared__ float part[kFewWarps][NT * 8][kFewRows + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int n0 = blockIdx.x * kFewRows, warps = blockDim.x >> 5;
+  // The first blocks ask for the start of their weights while the previous kernel ends: reads of
+  // them wait for it, a prefetch into L2 does not (what that kernel writes reaches L2 all the
+  // same). One token, 2048 -> 2560: 4.96 -> 4.66 us; whole rows, or all blocks: slower.
+  if (blockIdx.x < a.early && tid < kFewRows && n0 + tid < a.l.N)
+    bulk_prefetch_l2(a.w + static_cast<int64_t>(n0 + tid) * a.w_row, min(a.k_bytes, 4096));
+  griddep_wait();
+  griddep_launch_dependents();
+  // rows past N repeat the last one, tokens past T the last token: nothing of them is written
+  const uint8_t* wa = a.w + static_cast<int64_t>(min(n0 + g, a.l.N - 1)) * a.w_row + c * 16;
+  const uint8_t* wb = a.w + static_cast<int64_t>(min(n0 + g + 8, a.l.N - 1)) * a.w_row + c * 16;
+  const uint8_t* xp[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+    xp[i] = a.x + static_cast<int64_t>(min(i * 8 + g, a.l.T - 1)) * a.x_row + c * 16;
+  float d[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
+  constexpr int kU = 4;                      // steps of 64 bytes whose loads go together
+  const int last = a.k_bytes - c * 16;       // bytes of K from this lane's first place on
+  for (int k0 = warp * 128; k0 < a.k_bytes; k0 += warps * 128 * (kU / 2)) {
+    uint4 p[kU], q[kU], x[kU][NT];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int k = k0 + (u >> 1) * (warps * 128) + (u & 1) * 64;
+      const bool in = k < last;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      p[u] = in ? __ldg(reinterpret_cast<const uint4*>(wa + k)) : zero;
+      q[u] = in ? __ldg(reinterpret_cast<const uint4*>(wb + k)) : zero;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        x[u][i] = in ? __ldg(reinterpret_cast<const uint4*>(xp[i] + k)) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        mma_16x8<E4M3, HALF>(d[i], p[u].x, q[u].x, p[u].y, q[u].y, x[u][i].x, x[u][i].y);
+        mma_16x8<E4M3, HALF>(d[i], p[u].z, q[u].z, p[u].w, q[u].w, x[u][i].z, x[u][i].w);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[warp][i * 8 + 2 * c + (j & 1)][g + (j >> 1) * 8] = d[i][j];
+  __syncthreads();
+  for (int v = tid; v < NT * 8 * kFewRows; v += warps * 32) {
+    const int t = v / kFewRows, r = v % kFewRows, n = n0 + r;
+    if (t >= a.l.T || n >= a.l.N) continue;
+    float y[1] = {0.f};
+    for (int w = 0; w < warps; ++w) y[0] += part[w][t][r];
+    if (E4M3) y[0] = y[0] * a.l.x_scale[t] * a.l.w_scale[n];
+    if (a.l.bias) y[0] += a.l.bias[n];
+    activate(y, a.l.act);
+    if (a.l.add) y[0] += to_f(static_cast<const O*>(a.l.add)[t * a.l.add_row + n]);
+    static_cast<O*>(a.l.out)[t * a.l.out_row + n] = to_out<O>(y[0]);
+  }
+}
+
+template <bool E4M3, bool HALF, typename O>
+cudaError_t launch_few(const FewArgs& a, cudaStream_t s) {
+  // 16 warps a block shorten each one's run through K, 8 leave room for more blocks. Measured,
+  // one token, 16 and 8 warps: 2048 -> 2560 4.33 and 5.1 us, 8192 -> 2048 9.7 and 16.2,
+  // 2048 -> 8192 in bf16 the same.
+  const int blocks = (a.l.N - 1) / kFewRows + 1;
+  const dim3 grid(blocks), block(32 * std::min(kFewWarps, std::max(1, (a.k_bytes + 127) / 128)));
+  const auto kernel = a.l.T <= 8 ? linear_few_kernel<E4M3, HALF, O, 1>
+                                 : linear_few_kernel<E4M3, HALF, O, 2>;
+  return launch_pdl(kernel, grid, block, 0, s, a);
+}
+
 // Sizes of one call.
 struct Plan {
-  int mode, cols, splits, stages, acc, tcols;
+  int mode, cols, splits, sub, stages, acc, tcols;
   size_t smem;
 };
 
@@ -574,11 +693,36 @@ size_t smem_for(int tcols, size_t need) {
   return std::max(need, least);
 }
 
-// Cycles of a call by mode and tokens per tile; the least is taken. A chunk costs its products
-// (2 cycles a column) or the copies that feed them.
+// Chunks per stage: a wait and a commit for several where their products are short. One token
+// tile of 16 columns, 8192 -> 2048: 1, 2 and 4 chunks a stage 13.8, 12.1 and 11.5 us.
+int chunks_per_stage(int cols, int chunks) {
+  return std::min(cols <= 16 ? 4 : cols <= 128 ? 2 : 1, chunks);
+}
+
+// Ring stages, tensor-memory columns and shared memory of a mode, tokens per tile and split.
+void lay_out(Plan& p, int nch) {
+  const int chunks = (nch + p.splits - 1) / p.splits, cb = chunk_bytes(p.cols, p.mode);
+  p.acc = next_pow2(p.cols);
+  p.tcols = std::max(32, p.mode == kSplit ? p.acc : 2 * p.acc);
+  const size_t fixed = 1024 + sizeof(Ctl);
+  p.sub = chunks_per_stage(p.cols, chunks);
+  const int sb = p.sub * cb;
+  const int room = static_cast<int>((kSmemMax - fixed) / sb);
+  p.stages = std::min({room, kMaxStages, std::max(2, (chunks + p.sub - 1) / p.sub)});
+  p.smem = smem_for(p.tcols, fixed + static_cast<size_t>(p.stages) * sb);
+}
+
+// The mode, tokens per tile and split of the least time in a model of it (us), fitted to
+// measurements: a K-chunk's time by columns, times the tiles that a multiprocessor takes in
+// turn, but no less than the weights' bytes take, and a start and an end; those of a cluster
+// grow with its size and their number. Model and measured, 2048 -> 2048: 64 tokens split by 4
+// at 32 columns 7.5 and 7.2, by 8 9.9 and 9.0, not split 9.1 and 8.9; 2048 -> 8192: 4096 tokens
+// in pairs 78 and 72, without 94 and 86; 8192 -> 8192: 16 tokens split by 2 25.6 and 24.1, not
+// split 27.9 and 27.8.
 Plan make_plan(int T, int N, int nch, int sms) {
   const int rows_n = (N + kRows - 1) / kRows;
   const int most = std::min(kMaxCols, (T + 15) / 16 * 16);
+  const double bytes = static_cast<double>(N) * nch * kChunk;
   double best = 1e300;
   Plan p{};
   const auto offer = [&](int mode, int cols, int splits, double cost) {
@@ -588,30 +732,41 @@ Plan make_plan(int T, int N, int nch, int sms) {
     p.cols = cols;
     p.splits = splits;
   };
+  // 0.085 TB/s for each block, 6.8 for all
+  const auto fetch = [&](double blocks) { return bytes / std::min(6.8e6, 0.085e6 * blocks); };
   for (int cols = 16; cols <= most; cols += 16) {
-    const int64_t tiles_t = (T + cols - 1) / cols;
-    const double chunk = std::max(2.0 * cols, stage_bytes(cols, kSingle) / 64.0);
-    for (int splits = 1; splits <= kMaxSplit && splits <= nch; splits *= 2) {
-      if (splits > 1 && cols > kMaxSplitCols) break;
-      const double turns = static_cast<double>((rows_n * tiles_t * splits + sms - 1) / sms);
-      offer(splits > 1 ? kSplit : kSingle, cols, splits,
-            turns * ((nch + splits - 1) / splits * chunk + 100.0) + 8.0 * cols +
-                (splits > 1 ? 1500.0 + 10.0 * cols : 0.0));
-    }
+    const int64_t tiles_t = (T + cols - 1) / cols, tiles = rows_n * tiles_t;
+    const double chunk = cols <= 16 ? 0.13 : std::max(0.175, 0.07 + 0.00125 * cols);
+    offer(kSingle, cols, 1,
+          std::max(static_cast<double>((tiles + sms - 1) / sms) * nch * chunk,
+                   fetch(static_cast<double>(tiles))) + 3.2 + 0.011 * cols);
     if (cols % 32 == 0 && sms >= 2) {
-      const double pair = std::max(2.0 * cols, stage_bytes(cols, kPair) / 64.0);
-      const double turns = static_cast<double>(((rows_n + 1) / 2 * tiles_t + sms / 2 - 1) / (sms / 2));
-      offer(kPair, cols, 1, turns * (nch * pair + 100.0) + 8.0 * cols + 500.0);
+      const int64_t pairs = (rows_n + 1) / 2 * tiles_t;
+      offer(kPair, cols, 1,
+            std::max(static_cast<double>((pairs + sms / 2 - 1) / (sms / 2)) * nch *
+                         (0.165 + 0.0006 * cols),
+                     fetch(2.0 * pairs)) + 4.2 + 0.011 * cols);
+    }
+    if (cols > kMaxSplitCols || tiles >= sms) continue;
+    for (int splits = 2; splits <= kMaxSplit && splits <= nch; splits *= 2) {
+      // Clusters side by side: all blocks of one find room within a group of multiprocessors
+      // (8 of 19 on this device: 76, 36 and 15 clusters of 2, 4 and 8 blocks that have a
+      // multiprocessor each, and a little more than twice that at half its shared memory).
+      Plan q{};
+      q.mode = kSplit;
+      q.cols = cols;
+      q.splits = splits;
+      lay_out(q, nch);
+      const int per_sm = static_cast<int>(kSmemMax + 1024) / static_cast<int>(q.smem + 1024);
+      const int64_t room = std::max(1, sms / 8 * per_sm / splits * 8 - (per_sm == 1 ? 1 : 0));
+      const double turns = static_cast<double>((tiles + room - 1) / room);
+      const double blocks = static_cast<double>(std::min(tiles, room)) * splits;
+      const double end = 1.9 + 0.13 * splits + 0.013 * blocks + 0.00015 * cols * cols;
+      offer(kSplit, cols, splits,
+            std::max(turns * ((nch + splits - 1) / splits) * chunk, fetch(blocks)) + turns * end + 2.0);
     }
   }
-  p.acc = next_pow2(p.cols);
-  p.tcols = std::max(32, p.mode == kSplit ? p.acc : 2 * p.acc);
-  const size_t fixed = 1024 + sizeof(Ctl) +
-                       (p.mode == kSplit ? static_cast<size_t>(p.cols) * kRows * sizeof(float) : 0);
-  const int sb = stage_bytes(p.cols, p.mode);
-  const int room = static_cast<int>((kSmemMax - fixed) / sb);
-  p.stages = std::min({room, kMaxStages, std::max(2, (nch + p.splits - 1) / p.splits)});
-  p.smem = smem_for(p.tcols, fixed + static_cast<size_t>(p.stages) * sb);
+  lay_out(p, nch);
   return p;
 }
 
@@ -649,6 +804,11 @@ cudaError_t launch_out(const CUtensorMap& tx, const CUtensorMap& tw, const Linea
          : p.mode == kSplit ? launch<E4M3, O, kSplit>(tx, tw, a, p, sms, s)
                             : launch<E4M3, O, kSingle>(tx, tw, a, p, sms, s);
 }
+
+// Measured, few-token kernel and the better of the others, us: 1 token 2048 -> 2560 4.3 and 7.3,
+// 8192 -> 8192 24.7 and 25.9, 2048 -> 16384 15.5 and 13.9; 16 tokens 2048 -> 2560 5.6 and 7.9,
+// 8192 -> 2048 12.4 and 12.6, 8192 -> 8192 29.7 and 26.9.
+bool take_few(int T, int N) { return (T <= 8 && N <= 8192) || (T <= 16 && N <= 4096); }
 
 bool bad_align(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
@@ -690,21 +850,6 @@ extern "C" moe_status moe_linear(const moe_linear_args* l, void* stream) {
   a.N = l->N;
   const int elems = kChunk / es;
   a.nch = (l->K + elems - 1) / elems;
-  const Plan p = make_plan(l->T, l->N, a.nch, sms);
-  a.cols = p.cols;
-  const int fw = p.mode == kPair ? 2 * kRows : kRows;
-  a.tiles_n = (l->N - 1) / fw + 1;
-  a.tiles_t = (l->T - 1) / p.cols + 1;
-  if (static_cast<int64_t>(a.tiles_n) * a.tiles_t * p.splits > 0x7FFFFFFF - 1024) return MOE_ERR_SHAPE;
-  a.stages = p.stages;
-  a.acc = p.acc;
-  a.tcols = p.tcols;
-  a.band = p.mode == kPair ? 8 : 12;         // about the square root of the tiles under way
-  // instruction descriptor: fp32 D, both operands K-major, M = features, N = cols; operand types
-  // fp16 (0) or bf16 (1), or e4m3 (0)
-  const uint32_t type = l->dtype == MOE_BF16 ? 1u : 0u;
-  a.idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(p.cols >> 3) << 17) |
-            (static_cast<uint32_t>(fw >> 4) << 24);
   a.x_scale = l->x_scale;
   a.w_scale = l->w_scale;
   a.bias = l->bias;
@@ -715,6 +860,45 @@ extern "C" moe_status moe_linear(const moe_linear_args* l, void* stream) {
   a.act = l->act;
   a.err = l->err;
   a.timeout_ns = wait_timeout_ns();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (take_few(l->T, l->N)) {
+    FewArgs f{};
+    f.x = static_cast<const uint8_t*>(l->x);
+    f.w = static_cast<const uint8_t*>(l->w);
+    f.x_row = l->T > 1 ? l->x_row * es : 0;
+    f.w_row = l->N > 1 ? l->w_row * es : 0;
+    f.k_bytes = l->K * es;
+    f.early = sms;
+    f.l = a;
+    cudaError_t e;
+    if (e4m3)
+      e = l->out_dtype == MOE_F32   ? launch_few<true, false, float>(f, s)
+          : l->out_dtype == MOE_F16 ? launch_few<true, false, __half>(f, s)
+                                    : launch_few<true, false, __nv_bfloat16>(f, s);
+    else if (l->dtype == MOE_F16)
+      e = l->out_dtype == MOE_F32 ? launch_few<false, true, float>(f, s)
+                                  : launch_few<false, true, __half>(f, s);
+    else
+      e = l->out_dtype == MOE_F32 ? launch_few<false, false, float>(f, s)
+                                  : launch_few<false, false, __nv_bfloat16>(f, s);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  const Plan p = make_plan(l->T, l->N, a.nch, sms);
+  a.cols = p.cols;
+  const int fw = p.mode == kPair ? 2 * kRows : kRows;
+  a.tiles_n = (l->N - 1) / fw + 1;
+  a.tiles_t = (l->T - 1) / p.cols + 1;
+  if (static_cast<int64_t>(a.tiles_n) * a.tiles_t * p.splits > 0x7FFFFFFF - 1024) return MOE_ERR_SHAPE;
+  a.stages = p.stages;
+  a.sub = p.sub;
+  a.acc = p.acc;
+  a.tcols = p.tcols;
+  a.band = p.mode == kPair ? 8 : 12;         // about the square root of the tiles under way
+  // instruction descriptor: fp32 D, both operands K-major, M = features, N = cols; operand types
+  // fp16 (0) or bf16 (1), or e4m3 (0)
+  const uint32_t type = l->dtype == MOE_BF16 ? 1u : 0u;
+  a.idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(p.cols >> 3) << 17) |
+            (static_cast<uint32_t>(fw >> 4) << 24);
   // a single row has no stride: any multiple of 16 bytes will do
   const uint64_t one = (static_cast<uint64_t>(l->K) * es + 15) / 16 * 16;
   CUtensorMap tx, tw;
@@ -722,7 +906,6 @@ extern "C" moe_status moe_linear(const moe_linear_args* l, void* stream) {
                 p.mode == kPair ? p.cols / 2 : p.cols) ||
       !map_rows(&tw, l->dtype, l->w, l->K, l->N, l->N > 1 ? l->w_row * es : one, elems, kRows))
     return MOE_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (e4m3)
     e = l->out_dtype == MOE_F32   ? launch_out<true, float>(tx, tw, a, p, sms, s)
@@ -741,8 +924,8 @@ extern "C" moe_status moe_debug_linear_plan(int32_t T, int32_t N, int32_t K, int
   if (T < 1 || N < 1 || K < 1 || sms < 1 || !plan) return MOE_ERR_ARG;
   const int elems = dtype == MOE_E4M3 ? kChunk : kChunk / 2, nch = (K + elems - 1) / elems;
   const Plan p = make_plan(T, N, nch, sms);
-  const int32_t v[7] = {p.cols, p.splits, p.stages, p.acc, p.tcols, static_cast<int32_t>(p.smem),
-                        p.mode};
-  for (int i = 0; i < 7; ++i) plan[i] = v[i];
+  const int32_t v[8] = {p.cols, p.splits, p.stages, p.acc, p.tcols, static_cast<int32_t>(p.smem),
+                        p.mode, p.sub};
+  for (int i = 0; i < 8; ++i) plan[i] = v[i];
   return MOE_OK;
 }

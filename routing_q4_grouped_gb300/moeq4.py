@@ -863,9 +863,9 @@ def moe_debug_kv_attention_rows(B, nq, Hq, Hkv, D, max_len, prefix_len=0) -> int
 
 def moe_debug_linear_plan(T, N, K, dtype=MOE_BF16, sms=152) -> dict:
     """How moe_linear would lay out a call. Host only."""
-    v = (_c_i32 * 7)()
+    v = (_c_i32 * 8)()
     _check("moe_debug_linear_plan", lib().moe_debug_linear_plan(T, N, K, dtype, sms, v))
-    return dict(zip(("cols", "splits", "stages", "acc", "tcols", "smem", "mode"), v))
+    return dict(zip(("cols", "splits", "stages", "acc", "tcols", "smem", "mode", "sub"), v))
 
 
 def moe_debug_noalloc_scratch() -> tuple[int, int]:

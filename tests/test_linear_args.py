@@ -85,7 +85,8 @@ def test_layouts_fit_the_multiprocessor(L, dtype):
                 assert (p["mode"] == 1) == (p["splits"] > 1)
                 assert p["mode"] != 2 or p["cols"] % 32 == 0
                 stage = (128 + p["cols"] // (2 if p["mode"] == 2 else 1)) * 128
-                assert p["smem"] >= p["stages"] * stage + 1024 + \
-                    (p["cols"] * 512 if p["splits"] > 1 else 0)
+                assert 1 <= p["sub"] <= 4 and p["smem"] >= p["stages"] * p["sub"] * stage + 1024
+                if p["splits"] > 1:           # the partial sums fit into the ring
+                    assert p["stages"] * p["sub"] * stage >= p["cols"] * 512
                 assert p["smem"] <= 227 * 1024
                 assert (p["smem"] + 1024) * 512 >= p["tcols"] * 228 * 1024
