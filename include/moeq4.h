@@ -204,8 +204,9 @@ typedef struct moe_route_score {
 } moe_route_score;
 
 /* moe_route with another choice: the same arrays, limits, scratch and launches. Keys are
- * compared as in 64-bit arithmetic; weights are fp32 within a few units in the last
- * place. A NaN or -inf logit counts as the least finite number, +inf as the largest, and
+ * compared in 64-bit arithmetic, and without a bias (and with group_best 1) as the exact
+ * scores, whose order is that of the logits; weights are fp32 within a few units in the
+ * last place. A NaN or -inf logit counts as the least finite number, +inf as the largest, and
  * either sets MOE_DEVERR_NONFINITE_LOGIT. */
 moe_status moe_route_scored(const float* logits, const moe_route_score* score,
                             const moe_route_out* out, void* ws, size_t ws_bytes, void* stream);

@@ -31,7 +31,13 @@ def choose(logits, k, sigmoid=False, bias=None, groups=1, top_groups=1, group_be
         score = [math.exp(v - top) for v in z]
         total = math.fsum(score)
         score = [s / total for s in score]
-    key = [s + (0.0 if bias is None else finite(float(bias[e]))) for e, s in enumerate(score)]
+    # scores grow with the logits: where scores alone are compared, the logits tell their order
+    # exactly, also where float64 rounds two scores to the same number
+    if bias is None and (groups == 1 or group_best == 1):
+        key = z
+    else:
+        key = [s + (0.0 if bias is None else finite(float(bias[e])))
+               for e, s in enumerate(score)]
     per = E // groups
     if groups > 1:
         rank = [sum(sorted(key[g * per:g * per + per], reverse=True)[:group_best])

@@ -596,7 +596,7 @@ struct FewArgs {
 
 // NT groups of 8 tokens.
 template <bool E4M3, bool HALF, typename O, int NT>
-__global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kFewWarps * 32, 2) linear_few_kernel(const FewArgs a) {
   __shared__ float part[kFewWarps][NT * 8][kFewRows + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const FewArg
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
-  constexpr int kU = 4;                      // steps of 64 bytes whose loads go together
+  constexpr int kU = NT == 1 ? 4 : 2;        // steps of 64 bytes whose loads go together
   const int last = a.k_bytes - c * 16;       // bytes of K from this lane's first place on
   for (int k0 = warp * 128; k0 < a.k_bytes; k0 += warps * 128 * (kU / 2)) {
     uint4 p[kU], q[kU], x[kU][NT];
@@ -663,11 +663,10 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const FewArg
 
 template <bool E4M3, bool HALF, typename O>
 cudaError_t launch_few(const FewArgs& a, cudaStream_t s) {
-  // 16 warps a block shorten each one's run through K, 8 leave room for more blocks. Measured,
-  // one token, 16 and 8 warps: 2048 -> 2560 4.33 and 5.1 us, 8192 -> 2048 9.7 and 16.2,
-  // 2048 -> 8192 in bf16 the same.
+  // A warp for 256 bytes of K, up to 16: measured for one token, 16 and 8 warps, 2048 -> 2560
+  // 4.3 and 5.1 us, 8192 -> 2048 9.7 and 16.2; 2048 -> 8192 in e4m3 (8 warps cover it) 7.5, 5.4.
   const int blocks = (a.l.N - 1) / kFewRows + 1;
-  const dim3 grid(blocks), block(32 * std::min(kFewWarps, std::max(1, (a.k_bytes + 127) / 128)));
+  const dim3 grid(blocks), block(32 * std::min(kFewWarps, std::max(1, (a.k_bytes + 255) / 256)));
   const auto kernel = a.l.T <= 8 ? linear_few_kernel<E4M3, HALF, O, 1>
                                  : linear_few_kernel<E4M3, HALF, O, 2>;
   return launch_pdl(kernel, grid, block, 0, s, a);

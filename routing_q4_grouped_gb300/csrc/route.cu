@@ -257,8 +257,7 @@ __device__ __forceinline__ void choose_and_rank(const RouteArgs& a, const RouteS
   for (int e = tid; e < route_ep(E); e += kRouteThreads) m.sCnt[e] = 0;
   if constexpr (SCORED) {
     bool bad = false;
-    for (int i = warp; i < nt; i += kRouteWarps)
-      select_scored<S>(a, t0 + i, lane, m.sE + i * k, m.sV + i * k, bad);
+    select_scored<S>(a, t0, warp, kRouteWarps, nt, lane, m.sE, m.sV, bad);
     if (__any_sync(kFull, bad) && lane == 0) atomicOr(a.err, MOE_DEVERR_NONFINITE_LOGIT);
   } else if (a.ids_given != 0) {
     // the fused router chose the experts (mode 1: with their weights in w;

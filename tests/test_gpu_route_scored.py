@@ -214,3 +214,33 @@ def test_binding_refusals():
         moeq4.moe_route_scored(torch.zeros((4, 64), device="cuda"), _spec(bias=np.zeros(32)), out, ws)
     with pytest.raises(moeq4.MoeError):
         moeq4.moe_route_scored(torch.zeros((4, 64), device="cuda"), _spec(groups=7), out, ws)
+
+
+@pytest.mark.parametrize("E,groups,best", [(256, 8, 2), (64, 8, 1), (128, 4, 2), (60, 12, 2)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_keys_near_the_rounding_of_fp32(E, groups, best, sigmoid):
+    # distances between keys from far below to above what fp32 scores resolve, within a lane's
+    # experts and across them, at the border of the choice and of the groups
+    rng = np.random.default_rng(E + best)
+    base = rng.standard_normal(E)
+    for step in (2.0 ** -24, 2.0 ** -22, 2.0 ** -20, 2.0 ** -18, 2.0 ** -16, 2.0 ** -12):
+        z = (rng.choice(base[:6], (60, E)) + step * rng.integers(-3, 4, (60, E)))
+        for bias in (None, 0.25 + step * rng.integers(-2, 3, E)):
+            _check(z, 6, sigmoid=sigmoid, bias=bias)
+            _check(z, 6, sigmoid=sigmoid, bias=bias, groups=groups, top_groups=groups // 2,
+                   group_best=best, renorm=False)
+            _check(z, 6, sigmoid=sigmoid, bias=bias, groups=groups, top_groups=groups,
+                   group_best=best)
+
+
+@pytest.mark.parametrize("top", [14.9, 16.0, 20.0, 30.0, 40.0])
+def test_saturated_scores(top):
+    # sigmoids that round to the same number in 64 bits although the logits differ
+    rng = np.random.default_rng(int(top))
+    z = top + 1e-5 * rng.integers(-2, 3, (80, 64)) - (rng.random((80, 64)) < 0.8) * rng.random((80, 64)) * 8
+    _check(z, 8, sigmoid=True)
+    _check(z, 8, sigmoid=True, groups=8, top_groups=4)
+    _check(z, 8)
+    tiny = rng.standard_normal((40, 64)) * 10.0 ** rng.integers(-44, -8, (40, 64)).astype(float)
+    _check(tiny, 8, sigmoid=True)
+    _check(tiny, 8)

@@ -49,7 +49,7 @@ def test_groups_by_brute_force(best):
 def test_values_out_of_range():
     inf = math.inf
     ids, w = scored.choose([math.nan, -inf, inf, 0.0], 4)
-    assert ids == [2, 0, 1, 3][:1] + [0, 1, 3] and w == [1.0, 0.0, 0.0, 0.0]
+    assert ids == [2, 3, 0, 1] and w == [1.0, 0.0, 0.0, 0.0]
     ids, w = scored.choose([-800.0] * 4, 2, sigmoid=True)
     assert ids == [0, 1] and w == [0.0, 0.0]
     ids, _ = scored.choose([3.0, 2.0, 1.0], 2, bias=[-inf, 0.0, math.nan])
