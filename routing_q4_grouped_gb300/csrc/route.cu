@@ -471,6 +471,23 @@ __global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const RouteA
   griddep_launch_dependents();
 }
 
+// The choice of moe_route_scored for a large batch, a launch of its own before the two others
+// (which then take ids and weights as given): it is instructions, and wants all multiprocessors
+// full, while the count rows want few blocks.
+constexpr int kChooseThreads = 128;
+constexpr int kChooseBlocks = 152 * 8;
+constexpr int kChooseTokens = 1024;        // from here on
+template <int S>
+__global__ void __launch_bounds__(kChooseThreads) route_choose_kernel(const RouteArgs a) {
+  const int lane = threadIdx.x & 31, warps = kChooseThreads / 32;
+  griddep_wait();
+  bool bad = false;
+  select_scored<S>(a, 0, blockIdx.x * warps + (threadIdx.x >> 5), gridDim.x * warps, a.T, lane,
+                   a.ids, a.w, bad);
+  if (__any_sync(kFull, bad) && lane == 0) atomicOr(a.err, MOE_DEVERR_NONFINITE_LOGIT);
+  griddep_launch_dependents();
+}
+
 // Second launch: block b reads back its rows' experts, ranks and logits, adds
 // the count rows of all blocks (expert totals) and of the blocks before b (its
 // base), computes its tokens' weights and places its rows. All loads of a
@@ -585,8 +602,17 @@ static cudaError_t launch_s(RouteArgs a, cudaStream_t s) {
     return launch_pdl(route_single_kernel<S, SCORED>, dim3(1), dim3(kRouteThreads),
                       route_smem_bytes(a.E, a.k, a.tpb), s, a);
   }
-  cudaError_t e =
-      launch_pdl(route_count_kernel<S, SCORED>, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
+  cudaError_t e;
+  if (SCORED && a.T >= kChooseTokens) {
+    const int warps = kChooseThreads / 32;
+    e = launch_pdl(route_choose_kernel<S>, dim3(min((a.T + warps - 1) / warps, kChooseBlocks)),
+                   dim3(kChooseThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
+    a.ids_given = 1;
+    e = launch_pdl(route_count_kernel<S, false>, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
+  } else {
+    e = launch_pdl(route_count_kernel<S, SCORED>, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
+  }
   if (e != cudaSuccess) return e;
   if (SCORED) a.ids_given = 1;   // the weights are in w
   return launch_pdl(route_place_kernel, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
