@@ -625,6 +625,7 @@ static cudaError_t launch_all(const RouteArgs& a, cudaStream_t s) {
   if (S <= 2) return launch_s<2, SCORED>(a, s);
   if (S <= 4) return launch_s<4, SCORED>(a, s);
   if (S <= 8) return launch_s<8, SCORED>(a, s);
+  if (SCORED && S <= 12) return launch_s<SCORED ? 12 : 16, SCORED>(a, s);
   if (S <= 16) return launch_s<16, SCORED>(a, s);
   return launch_s<32, SCORED>(a, s);
 }

@@ -248,7 +248,9 @@ template <int S>
 __device__ __forceinline__ bool select_scored_fast(const RouteArgs& a, const ScoreMode& m,
                                                    const float (&x)[S], const float (&bias)[S],
                                                    int t, int lane, int* sE, float* sV) {
-  constexpr int kLow = 32 * S - 1;                 // the expert's number, complemented
+  // the expert's number, complemented, and the size of the sorting network
+  constexpr int kLow = (S <= 1 ? 32 : S <= 2 ? 64 : S <= 4 ? 128 : S <= 8 ? 256 : S <= 16 ? 512 : 1024) - 1;
+  constexpr int P = S == 12 ? 16 : S;
   constexpr int kNone = INT_MIN;
   const int E = a.E, k = a.k;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
@@ -355,10 +357,10 @@ __device__ __forceinline__ bool select_scored_fast(const RouteArgs& a, const Sco
       open = sure | __ballot_sync(kFull, (near >> lane & 1u) && before_me < a.top_groups - __popc(sure));
     }
   }
-  int v[S];
+  int v[P];
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    v[s] = (signed_key(key[s]) & ~kLow) | ((31 - lane) * S + (S - 1 - s));
+  for (int s = 0; s < P; ++s)
+    v[s] = s < S ? (signed_key(key[s < S ? s : 0]) & ~kLow) | (kLow - s - lane * S) : kNone;
   if (m.lanes_alike) {
     const int e = lane * S;
     if (!(e < E && (!m.grouped || (open >> (e * m.inv_n >> 20) & 1u)))) {
@@ -373,11 +375,11 @@ __device__ __forceinline__ bool select_scored_fast(const RouteArgs& a, const Sco
     }
   }
 #pragma unroll
-  for (int size = 2; size <= S; size <<= 1)
+  for (int size = 2; size <= P; size <<= 1)
 #pragma unroll
     for (int stride = size >> 1; stride > 0; stride >>= 1)
 #pragma unroll
-      for (int i = 0; i < S; ++i) {
+      for (int i = 0; i < P; ++i) {
         const int j = i ^ stride;
         if (j > i) {
           const int hi = max(v[i], v[j]), lo = min(v[i], v[j]);
