@@ -61,6 +61,9 @@ class RouteOutC(ctypes.Structure):
                 ("block_m", _c_i32)]
 
 
+_ROUTE = struct.Struct("@9P4i")        # RouteOutC
+
+
 class RouteScoreC(ctypes.Structure):
     _fields_ = [("bias", _c_ptr), ("score", _c_i32), ("groups", _c_i32), ("top_groups", _c_i32),
                 ("group_best", _c_i32), ("renorm", _c_i32), ("factor", _c_f32)]
@@ -125,8 +128,7 @@ _SIGS = {
     "moe_ffn_workspace_size": (_c_size, [_c_i32] * 7),
     "moe_layer_workspace_size": (_c_size, [_c_i32] * 7),
     "moe_route": (_c_i32, [_c_ptr, ctypes.POINTER(RouteOutC), _c_ptr, _c_size, _c_ptr]),
-    "moe_route_scored": (_c_i32, [_c_ptr, _c_ptr, ctypes.POINTER(RouteOutC), _c_ptr, _c_size,
-                                  _c_ptr]),
+    "moe_route_scored": (_c_i32, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "moe_layer_scored": (_c_i32, [_c_ptr, _c_ptr, _c_i32, ctypes.POINTER(Q4PackedC), _c_ptr,
                                   ctypes.POINTER(RouteOutC), _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "moe_rms_norm": (_c_i32, [_c_ptr, _c_ptr]),
@@ -217,15 +219,7 @@ try:   # the same handle without building a Stream object (saves about a microse
     def _current_stream() -> int:                                          # noqa: F811
         return _cuda_getCurrentRawStream(_cuda_getDevice())
 except ImportError:
-    pass
-
-
-def _here(fn, *tensors):
-    """A call runs on the current device: its tensors have to be there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{fn}: a tensor is on {t.device}, the current device is cuda:{dev}")
+    _cuda_getDevice = torch.cuda.current_device
 
 
 def _stream(stream) -> int:
@@ -340,6 +334,13 @@ class RouteBuffers:
                    tiles=torch.empty((nmax, 3), **i32), n_tiles=torch.zeros(4, **i32),
                    err=torch.zeros(4, **i32))
 
+    def packed(self) -> bytes:
+        """cstruct as packed bytes: a fraction of the time that filling it takes."""
+        return _ROUTE.pack(self.ids.data_ptr(), self.w.data_ptr(), self.counts.data_ptr(),
+                           self.offsets.data_ptr(), self.perm.data_ptr(), self.inv.data_ptr(),
+                           self.tiles.data_ptr(), self.n_tiles.data_ptr(), self.err.data_ptr(),
+                           self.T, self.E, self.k, self.block_m)
+
     def cstruct(self) -> RouteOutC:
         return RouteOutC(_ptr(self.ids), _ptr(self.w), _ptr(self.counts), _ptr(self.offsets),
                          _ptr(self.perm), _ptr(self.inv), _ptr(self.tiles), _ptr(self.n_tiles),
@@ -376,22 +377,25 @@ class RouteScore:
         self._addr = ctypes.addressof(self._c)
 
 
-def _scored(fn, logits, score, out):
-    _need(fn, logits, torch.float32, "logits")
-    if logits.shape != (out.T, out.E):
-        raise ValueError(f"{fn}: logits must be [{out.T}][{out.E}], got {tuple(logits.shape)}")
+def _scored(fn, logits, score, out) -> int:
+    """Checks what both calls take; the logits' pointer."""
+    dev = None if logits is None or not logits.is_cuda else _device()
+    p = _vector(fn, logits, "logits", (out.T, out.E), torch.float32, dev)
     if score.bias is not None and score.bias.numel() != out.E:
         raise ValueError(f"{fn}: the bias must hold {out.E} values, got {score.bias.numel()}")
-    _here(fn, logits, score.bias, out.ids)
+    if out.ids.get_device() != dev or score.bias is not None and score.bias.get_device() != dev:
+        raise ValueError(f"{fn}: result or bias is not on the current device cuda:{dev}")
+    return p
 
 
 def moe_route_scored(logits: torch.Tensor, score: RouteScore, out: RouteBuffers, ws: torch.Tensor,
                      stream=None) -> None:
     """Routing of fp32 logits [T, E] into ``out`` with the choice and weights of ``score``."""
-    _scored("moe_route_scored", logits, score, out)
-    c = out.cstruct()
-    _check("moe_route_scored", lib().moe_route_scored(_ptr(logits), score._addr, ctypes.byref(c),
-                                                      _ptr(ws), ws.numel(), _stream(stream)))
+    p = _scored("moe_route_scored", logits, score, out)
+    st = lib().moe_route_scored(p, score._addr, out.packed(), ws.data_ptr(), ws.numel(),
+                                _stream(stream))
+    if st:
+        _check("moe_route_scored", st)
 
 
 def moe_route_noalloc(logits: torch.Tensor, out: RouteBuffers, stream=None) -> None:
@@ -451,12 +455,12 @@ def moe_layer_scored(x: torch.Tensor, logits: torch.Tensor, W: DeviceWeights, sc
     fn = "moe_layer_scored"
     _need(fn, x, torch.bfloat16, "x")
     _need(fn, y, torch.bfloat16, "y")
-    _scored(fn, logits, score, r)
+    p = _scored(fn, logits, score, r)
     if x.shape != (r.T, W.d) or y.shape != x.shape:
         raise ValueError(f"{fn}: x and y must be [{r.T}][{W.d}], got {tuple(x.shape)} and "
                          f"{tuple(y.shape)}")
     wc, rc = W.cstruct(), r.cstruct()
-    _check(fn, lib().moe_layer_scored(_ptr(x), _ptr(logits), r.T, ctypes.byref(wc), score._addr,
+    _check(fn, lib().moe_layer_scored(_ptr(x), p, r.T, ctypes.byref(wc), score._addr,
                                       ctypes.byref(rc), _ptr(y), _ptr(ws), ws.numel(),
                                       _stream(stream)))
 
@@ -601,15 +605,34 @@ _NORM = struct.Struct("@PqqPqqPqqPqqPqqPPiiiiff")
 _NORM_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
 
 
-def _norm_rows(fn, t, name, shape, dtype):
-    """(pointer, row stride, head stride) of [T][D] or [T][H][D] rows with dense elements."""
-    if t is not None and t.is_cuda and t.dtype is dtype and t.shape == shape:
+def _device() -> int:
+    """The current device (made ready by the call's first tensor)."""
+    return _cuda_getDevice()
+
+
+def _norm_rows(fn, t, name, shape, dtype, dev):
+    """(pointer, row stride, head stride) of [T][D] or [T][H][D] rows with dense elements on
+    device ``dev``."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
         st = t.stride()
         if st[-1] == 1 or shape[-1] == 1:
             return t.data_ptr(), st[0], st[1] if len(st) == 3 else 0
     got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
     raise ValueError(f"{fn}: {name} must be a {dtype} CUDA tensor {tuple(shape)} with dense "
-                     f"elements, got {got}")
+                     f"elements on the current device, got {got}")
+
+
+def _vector(fn, t, name, shape, dtype, dev):
+    """Pointer of a dense array on device ``dev``."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
+            t.is_contiguous():
+        return t.data_ptr()
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
+    raise ValueError(f"{fn}: {name} must be a contiguous {dtype} CUDA tensor {tuple(shape)} on the "
+                     f"current device, got {got}")
+
+
+_ROW0 = (0, 0, 0)
 
 
 def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor = None, out: torch.Tensor = None,
@@ -620,29 +643,27 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor = None, out: torch.Tensor
     fp32 scale per row in ``scales`` [T] or [T, H], or both. sum and out may be x or add."""
     fn = "moe_rms_norm"
     dtype = None if x is None else _NORM_DTYPES.get(x.dtype)
-    if dtype is None or x.dim() not in (2, 3):
+    shape = () if x is None else x.shape
+    n = len(shape)
+    if dtype is None or n != 2 and n != 3:
         raise ValueError(f"{fn}: x must be a bfloat16, float16 or float32 tensor [T][D] or "
                          f"[T][H][D], got {None if x is None else (x.dtype, tuple(x.shape))}")
-    shape, td = x.shape, x.dtype
-    xa = _norm_rows(fn, x, "x", shape, td)
-    none = (0, 0, 0)
-    aa = none if add is None else _norm_rows(fn, add, "add", shape, td)
-    sa = none if sum is None else _norm_rows(fn, sum, "sum", shape, td)
-    oa = none if out is None else _norm_rows(fn, out, "out", shape, td)
-    ca, scale = none, 0
+    td, dev = x.dtype, _device() if x.is_cuda else None
+    xa = _norm_rows(fn, x, "x", shape, td, dev)
+    aa = _ROW0 if add is None else _norm_rows(fn, add, "add", shape, td, dev)
+    sa = _ROW0 if sum is None else _norm_rows(fn, sum, "sum", shape, td, dev)
+    oa = _ROW0 if out is None else _norm_rows(fn, out, "out", shape, td, dev)
+    ca, scale, D = _ROW0, 0, shape[-1]
     if codes is not None:
-        ca = _norm_rows(fn, codes, "codes", shape, torch.float8_e4m3fn)
-        _need(fn, scales, torch.float32, "scales")
-        if scales.shape != shape[:-1]:
-            raise ValueError(f"{fn}: scales must be {tuple(shape[:-1])}, got {tuple(scales.shape)}")
-        scale = scales.data_ptr()
+        ca = _norm_rows(fn, codes, "codes", shape, torch.float8_e4m3fn, dev)
+        scale = _vector(fn, scales, "scales", shape[:-1], torch.float32, dev)
+    wp = 0
     if weight is not None:
-        _need(fn, weight, td, "weight")
-        if weight.numel() != shape[-1]:
-            raise ValueError(f"{fn}: weight must hold {shape[-1]} values, got {weight.numel()}")
-    _here(fn, x, add, sum, out, codes, scales, weight)
-    a = _NORM.pack(*xa, *aa, *sa, *oa, *ca, scale, 0 if weight is None else weight.data_ptr(),
-                   shape[0], 1 if len(shape) == 2 else shape[1], shape[-1], dtype, eps, offset)
+        if weight.numel() != D:
+            raise ValueError(f"{fn}: weight must hold {D} values, got {weight.numel()}")
+        wp = _vector(fn, weight, "weight", (D,), td, dev)
+    a = _NORM.pack(*xa, *aa, *sa, *oa, *ca, scale, wp, shape[0], 1 if n == 2 else shape[1], D, dtype,
+                   eps, offset)
     st = lib().moe_rms_norm(a, _stream(stream))
     if st:
         _check(fn, st)
@@ -652,15 +673,15 @@ _LINEAR = struct.Struct("@PqPqPPPPqPqPiiiiii")
 _LINEAR_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float8_e4m3fn: MOE_E4M3}
 
 
-def _matrix(fn, t, name, rows, columns, dtype):
-    """(pointer, row stride) of [rows][columns] with dense elements."""
-    if t is not None and t.is_cuda and t.dtype is dtype and t.shape == (rows, columns):
+def _matrix(fn, t, name, rows, columns, dtype, dev):
+    """(pointer, row stride) of [rows][columns] with dense elements on device ``dev``."""
+    if t is not None and t.dtype is dtype and t.shape == (rows, columns) and t.get_device() == dev:
         st = t.stride()
         if st[1] == 1 or columns == 1:
             return t.data_ptr(), st[0]
     got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
     raise ValueError(f"{fn}: {name} must be a {dtype} CUDA tensor [{rows}][{columns}] with dense "
-                     f"elements, got {got}")
+                     f"elements on the current device, got {got}")
 
 
 class Linear:
@@ -676,7 +697,10 @@ class Linear:
             raise ValueError(f"{fn}: weight must be a bfloat16, float16 or float8_e4m3fn matrix, got "
                              f"{None if weight is None else (weight.dtype, tuple(weight.shape))}")
         self.N, self.K = weight.shape
-        _, self._row = _matrix(fn, weight, "weight", self.N, self.K, weight.dtype)
+        if not weight.is_cuda:
+            raise ValueError(f"{fn}: weight must be a CUDA tensor, got one on {weight.device}")
+        _, self._row = _matrix(fn, weight, "weight", self.N, self.K, weight.dtype,
+                               weight.get_device())
         for name, t in (("bias", bias), ("scale", scale)):
             _need(fn, t, torch.float32, name, optional=True)
             if t is not None and t.numel() != self.N:
@@ -686,6 +710,9 @@ class Linear:
         self.weight, self.bias, self.scale, self.dtype = weight, bias, scale, dtype
         self.err = torch.zeros(4, dtype=torch.int32, device=weight.device) if err is None else err
         _need(fn, self.err, torch.int32, "err")
+        for name, t in (("bias", bias), ("scale", scale), ("err", self.err)):
+            if t is not None and t.device != weight.device:
+                raise ValueError(f"{fn}: {name} is on {t.device}, weight on {weight.device}")
 
 
 def moe_linear(x: torch.Tensor, linear: Linear, out: torch.Tensor, act=MOE_ACT_NONE,
@@ -694,28 +721,26 @@ def moe_linear(x: torch.Tensor, linear: Linear, out: torch.Tensor, act=MOE_ACT_N
     [T]. out and add are of x's type or fp32 (bf16, fp16 or fp32 where x is e4m3); add may be
     out."""
     fn = "moe_linear"
-    w = linear.weight
+    w, N, dev = linear.weight, linear.N, _device()
+    if w.get_device() != dev:
+        raise ValueError(f"{fn}: the weights are on {w.device}, the current device is cuda:{dev}")
     T = 0 if x is None or x.dim() != 2 else x.shape[0]
-    xp, xr = _matrix(fn, x, "x", T, linear.K, w.dtype)
-    out_dtype = None if out is None else _NORM_DTYPES.get(out.dtype)
+    xp, xr = _matrix(fn, x, "x", T, linear.K, w.dtype, dev)
+    td = None if out is None else out.dtype
+    out_dtype = _NORM_DTYPES.get(td)
     if out_dtype is None:
-        raise ValueError(f"{fn}: out must be bfloat16, float16 or float32, got "
-                         f"{None if out is None else out.dtype}")
-    op, orow = _matrix(fn, out, "out", T, linear.N, out.dtype)
-    ap, arow = (0, 0) if add is None else _matrix(fn, add, "add", T, linear.N, out.dtype)
+        raise ValueError(f"{fn}: out must be bfloat16, float16 or float32, got {td}")
+    op, orow = _matrix(fn, out, "out", T, N, td, dev)
+    ap, arow = (0, 0) if add is None else _matrix(fn, add, "add", T, N, td, dev)
     sp = 0
     if linear.scale is not None:
-        _need(fn, x_scale, torch.float32, "x_scale")
-        if x_scale.numel() != T:
-            raise ValueError(f"{fn}: x_scale must hold {T} values, got {x_scale.numel()}")
-        sp = x_scale.data_ptr()
+        sp = _vector(fn, x_scale, "x_scale", (T,), torch.float32, dev)
     elif x_scale is not None:
         raise ValueError(f"{fn}: x_scale goes with e4m3 inputs, got {x.dtype}")
-    _here(fn, x, w, out, add, x_scale)
     a = _LINEAR.pack(xp, xr, w.data_ptr(), linear._row, sp,
                      0 if linear.scale is None else linear.scale.data_ptr(),
                      0 if linear.bias is None else linear.bias.data_ptr(), ap, arow, op, orow,
-                     linear.err.data_ptr(), T, linear.N, linear.K, linear.dtype, out_dtype, act)
+                     linear.err.data_ptr(), T, N, linear.K, linear.dtype, out_dtype, act)
     st = lib().moe_linear(a, _stream(stream))
     if st:
         _check(fn, st)
