@@ -7,7 +7,12 @@
 // Each byte moves once and each element takes a few instructions, so many rows are
 // bound by memory bandwidth and few rows by launch latency. A row is held in registers
 // between its reductions (nothing is read twice): by 8, 16 or 32 lanes where it has up
-// to 128 vectors of 16 bytes, by a block of up to 512 threads where it has more.
+// to 64 vectors of 16 bytes, by a block of up to 512 threads where it has more. Two
+// vectors a thread: measured for 4096 rows of 2048 bf16 elements with a residual (67 MB)
+// 12.4 us, one vector 14.4, four 16.4. 40 registers for 1536 threads on a
+// multiprocessor: 8191 rows of 5120 into codes 61.5 us, with 64 registers 68.8.
+// Measured bandwidth, of a copy's 6.7 TB/s: 6.7 for 4096 fp32 rows of 4096, 6.0 for
+// 8191 bf16 rows of 5120, 4.8 into codes (two reductions, and a conversion behind them).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -48,6 +53,10 @@ template <int V>
 struct alignas(V) Bytes {
   uint8_t e[V];
 };
+// Two e4m3 codes, the first in the low byte.
+__device__ __forceinline__ uint32_t two_codes(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
@@ -61,45 +70,173 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ float from_f(float v) { return v; }
 
-// Sum, and unsigned maximum, over the lanes of a row: LANES neighbouring lanes of a warp
-// (LANES <= 32), or the whole block (LANES = 0; `sh` holds a word per warp; the order of
-// the additions is fixed).
-template <int LANES>
-__device__ __forceinline__ float row_sum(float v, float* sh) {
+// Sum and unsigned maximum over the lanes of a row: LANES neighbouring lanes of a warp
+// (LANES <= 32), or the whole block (LANES = 0; `sh` holds two words per warp and is used by one
+// call only; the order of the additions is fixed).
+template <int LANES, bool MAX>
+__device__ __forceinline__ void row_reduce(float& sum, uint32_t& most, float* sh) {
   constexpr int kFirst = (LANES == 0 ? 32 : LANES) / 2;
 #pragma unroll
-  for (int off = kFirst; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
-  if constexpr (LANES == 0) {
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) sh[warp] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int i = 0; i < warps; ++i) v += sh[i];
-    __syncthreads();
+  for (int off = kFirst; off > 0; off >>= 1) {
+    sum += __shfl_xor_sync(kFull, sum, off);
+    if (MAX) most = max(most, __shfl_xor_sync(kFull, most, off));
   }
-  return v;
-}
-template <int LANES>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, float* sh) {
-  constexpr int kFirst = (LANES == 0 ? 32 : LANES) / 2;
+  if constexpr (LANES == 0) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) {
+      sh[warp] = sum;
+      if (MAX) sh[16 + warp] = __uint_as_float(most);
+    }
+    __syncthreads();
+    sum = lane < warps ? sh[lane] : 0.f;             // (at most 16 warps)
+    if (MAX) most = lane < warps ? __float_as_uint(sh[16 + lane]) : 0u;
 #pragma unroll
-  for (int off = kFirst; off > 0; off >>= 1) v = max(v, __shfl_xor_sync(kFull, v, off));
-  if constexpr (LANES == 0) {
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) sh[warp] = __uint_as_float(v);
-    __syncthreads();
-    v = 0;
-    for (int i = 0; i < warps; ++i) v = max(v, __float_as_uint(sh[i]));
-    __syncthreads();
+    for (int off = 8; off > 0; off >>= 1) {
+      sum += __shfl_xor_sync(kFull, sum, off);
+      if (MAX) most = max(most, __shfl_xor_sync(kFull, most, off));
+    }
+    sum = __shfl_sync(kFull, sum, 0);                // (lanes 16.. added up zeros)
+    if (MAX) most = __shfl_sync(kFull, most, 0);
   }
-  return v;
 }
 
-// One row per LANES lanes (LANES = 0: per block), NV vectors of V elements per thread:
-// vector u of the row in thread u % lanes.
-template <typename E, int V, int NV, int LANES>
-__global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
-  __shared__ float sh[16];
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// What follows the loads: the sum's store, reductions, results. v holds h of row `row` (token t,
+// head `head`): vector u of the row in thread tid = u % lanes. CODES: with the 8-bit result, whose
+// largest magnitude is reduced together with the sum of squares, as that of h (weight + offset).
+template <typename E, int V, int NV, int LANES, bool CODES>
+__device__ __forceinline__ void finish_row(const NormArgs& a, float (&v)[NV][V], int64_t row,
+                                           uint32_t t, uint32_t head, bool live, int tid, int lanes,
+                                           float (*sh)[32]) {
+  using Vt = Vec<E, V>;
+  const auto at = [&](int64_t by_row, int64_t by_head) {
+    return static_cast<int64_t>(t) * by_row + static_cast<int64_t>(head) * by_head;
+  };
+  const Vt* weight = static_cast<const Vt*>(a.weight);
+  if (a.sum && live) {
+    Vt* o = reinterpret_cast<Vt*>(static_cast<E*>(a.sum) + at(a.sum_row, a.sum_head));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Vt w;
+#pragma unroll
+      for (int i = 0; i < V; ++i) w.e[i] = from_f<E>(v[j][i]);
+      if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
+    }
+  }
+  float ss = 0.f;
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    Vt w;
+    if (CODES && a.weight && tid + j * lanes < a.n) w = weight[tid + j * lanes];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      ss = fmaf(v[j][i], v[j][i], ss);
+      if (CODES && tid + j * lanes < a.n)
+        most = max(most, magnitude(v[j][i] *
+                                   ((a.weight ? to_f(w.e[i]) : 1.f) + a.offset)));
+    }
+  }
+  row_reduce<LANES, CODES>(ss, most, sh[0]);
+  float by = __frsqrt_rn(fmaf(ss, a.inv_d, a.eps));
+  // Squares that left fp32's range, above or (beside a small eps) below: again, on elements
+  // scaled by a power of two. All lanes of a warp, or of the block, take part.
+  const bool odd = !(ss < 1e37f) || ss < 1e-24f;
+  if (LANES == 0 ? odd : __any_sync(kFull, odd)) {
+    uint32_t m = 0;
+    float s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = max(m, magnitude(v[j][i]));
+    row_reduce<LANES, true>(s2, m, sh[1]);
+    const int e = m != 0 && m < 0x7F800000u ? ilogbf(__uint_as_float(m)) : 0;
+    const float f0 = __int_as_float((127 - e / 2) << 23);            // 2^-e in two factors
+    const float f1 = __int_as_float((127 - (e - e / 2)) << 23);
+    s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float z = v[j][i] * f0 * f1;
+        s2 = fmaf(z, z, s2);
+      }
+    row_reduce<LANES, false>(s2, m, sh[2]);
+    if (odd)
+      by = static_cast<float>(1.0 / sqrt(ldexp(static_cast<double>(s2) / a.D, 2 * e) +
+                                         static_cast<double>(a.eps)));
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int u = tid + j * lanes;
+    Vt w;
+    if (a.weight && u < a.n) w = weight[u];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float g = (a.weight && u < a.n ? to_f(w.e[i]) : 1.f) + a.offset;
+      v[j][i] = v[j][i] * by * g;
+    }
+  }
+  if (a.out && live) {
+    Vt* o = reinterpret_cast<Vt*>(static_cast<E*>(a.out) + at(a.out_row, a.out_head));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Vt w;
+#pragma unroll
+      for (int i = 0; i < V; ++i) w.e[i] = from_f<E>(v[j][i]);
+      if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
+    }
+  }
+  if constexpr (CODES) {
+    // (the largest product may have left fp32's range where the result does not: from the
+    // results then)
+    const float product = __uint_as_float(most);
+    const bool far = odd || most >= 0x7F800000u || (product < 1e-30f && most != 0);
+    uint32_t m = __float_as_uint(product * by);
+    if (LANES == 0 ? far : __any_sync(kFull, far)) {
+      uint32_t again = 0;
+      float none = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (tid + j * lanes < a.n) again = max(again, magnitude(v[j][i]));
+      row_reduce<LANES, true>(none, again, sh[3]);
+      if (far) m = again;
+    }
+    const float scale = m < 0x7F800000u
+                            ? fmaxf(__uint_as_float(m) * (1.f / kCodeMax), kScaleMin)
+                            : __uint_as_float(0x7FC00000u);
+    const float inv = __frcp_rn(scale);
+    if (live) {
+      if (tid == 0) a.scales[row] = scale;
+      Bytes<V>* o = reinterpret_cast<Bytes<V>*>(a.codes + at(a.c_row, a.c_head));
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        Bytes<V> w;
+        if constexpr (V % 4 == 0) {
+          uint32_t* words = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+          for (int i = 0; i < V; i += 4)
+            words[i / 4] = __byte_perm(two_codes(v[j][i] * inv, v[j][i + 1] * inv),
+                                       two_codes(v[j][i + 2] * inv, v[j][i + 3] * inv), 0x5410);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            w.e[i] = __nv_cvt_float_to_fp8(v[j][i] * inv, __NV_SATFINITE, __NV_E4M3);
+        }
+        if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
+      }
+    }
+  }
+}
+
+// A row per LANES lanes (LANES = 0: per block), NV vectors of V elements per thread.
+template <typename E, int V, int NV, int LANES, bool CODES>
+__global__ void __launch_bounds__(LANES == 0 ? 512 : 128, LANES == 0 && NV * V <= 16 ? 3 : 1)
+    norm_kernel(NormArgs a) {
+  __shared__ float sh[4][32];
   griddep_wait();
   griddep_launch_dependents();
   const int lanes = LANES == 0 ? static_cast<int>(blockDim.x) : LANES;
@@ -109,13 +246,14 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
                                  : static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) +
                                        threadIdx.x / lanes;
   const bool live = row < a.rows;        // (lanes of a dead row take part in the reductions)
-  const int64_t t = live ? row / a.H : 0, h = live ? row % a.H : 0;
+  const uint32_t some = static_cast<uint32_t>(live ? row : 0);
+  const uint32_t t = a.H == 1 ? some : some / static_cast<uint32_t>(a.H), h = some - t * a.H;
   using Vt = Vec<E, V>;
-  const Vt* x = reinterpret_cast<const Vt*>(static_cast<const E*>(a.x) + t * a.x_row + h * a.x_head);
-  const Vt* add =
-      reinterpret_cast<const Vt*>(static_cast<const E*>(a.add) + t * a.add_row + h * a.add_head);
   float v[NV][V];
   {
+    const Vt* x = reinterpret_cast<const Vt*>(static_cast<const E*>(a.x) + t * a.x_row + h * a.x_head);
+    const Vt* add =
+        reinterpret_cast<const Vt*>(static_cast<const E*>(a.add) + t * a.add_row + h * a.add_head);
     Vt p[NV], q[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -135,113 +273,15 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
       }
     }
   }
-  if (a.sum && live) {
-    Vt* o = reinterpret_cast<Vt*>(static_cast<E*>(a.sum) + t * a.sum_row + h * a.sum_head);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      Vt w;
-#pragma unroll
-      for (int i = 0; i < V; ++i) w.e[i] = from_f<E>(v[j][i]);
-      if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
-    }
-  }
-  float ss = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-  ss = row_sum<LANES>(ss, sh);
-  float r = __frsqrt_rn(fmaf(ss, a.inv_d, a.eps));
-  // Squares that left fp32's range, above or (beside a small eps) below: again, on elements
-  // scaled by a power of two. All lanes of a warp, or of the block, take part.
-  const bool odd = !(ss < 1e37f) || ss < 1e-24f;
-  if (LANES == 0 ? odd : __any_sync(kFull, odd)) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
-    m = row_max<LANES>(m, sh);
-    const float top = __uint_as_float(m);
-    const int e = m != 0 && m < 0x7F800000u ? ilogbf(top) : 0;
-    float s2 = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float z = ldexpf(v[j][i], -e);
-        s2 = fmaf(z, z, s2);
-      }
-    s2 = row_sum<LANES>(s2, sh);
-    if (odd)
-      r = static_cast<float>(
-          1.0 / sqrt(ldexp(static_cast<double>(s2) / a.D, 2 * e) + static_cast<double>(a.eps)));
-  }
-  const Vt* weight = static_cast<const Vt*>(a.weight);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int u = tid + j * lanes;
-    Vt w;
-    if (a.weight && u < a.n) w = weight[u];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float g = a.weight && u < a.n ? to_f(w.e[i]) + a.offset : 1.f + a.offset;
-      v[j][i] = v[j][i] * r * g;
-    }
-  }
-  if (a.out && live) {
-    Vt* o = reinterpret_cast<Vt*>(static_cast<E*>(a.out) + t * a.out_row + h * a.out_head);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      Vt w;
-#pragma unroll
-      for (int i = 0; i < V; ++i) w.e[i] = from_f<E>(v[j][i]);
-      if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
-    }
-  }
-  if (a.codes) {
-    // the largest magnitude by its bits, above which lie infinity and NaN
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (tid + j * lanes < a.n) m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
-    m = row_max<LANES>(m, sh);
-    const float scale = m < 0x7F800000u
-                            ? fmaxf(__fdiv_rn(__uint_as_float(m), kCodeMax), kScaleMin)
-                            : __uint_as_float(0x7FC00000u);
-    const float inv = __frcp_rn(scale);
-    if (live) {
-      if (tid == 0) a.scales[row] = scale;
-      Bytes<V>* o = reinterpret_cast<Bytes<V>*>(a.codes + t * a.c_row + h * a.c_head);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        Bytes<V> w;
-        if constexpr (V % 2 == 0) {
-#pragma unroll
-          for (int i = 0; i < V; i += 2) {
-            const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
-                make_float2(v[j][i] * inv, v[j][i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-            w.e[i] = static_cast<uint8_t>(two & 0xFF);
-            w.e[i + 1] = static_cast<uint8_t>(two >> 8);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            w.e[i] = __nv_cvt_float_to_fp8(v[j][i] * inv, __NV_SATFINITE, __NV_E4M3);
-        }
-        if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
-      }
-    }
-  }
+  finish_row<E, V, NV, LANES, CODES>(a, v, row, t, h, live, tid, lanes, sh);
 }
 
 template <typename E, int V, int NV, int LANES>
 cudaError_t launch_rows(const NormArgs& a, int threads, cudaStream_t s) {
-  const int per = LANES == 0 ? 1 : threads / LANES;
-  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.rows) + per - 1) / per);
-  return launch_pdl(norm_kernel<E, V, NV, LANES>, dim3(blocks), dim3(threads), 0, s, a);
+  const int64_t per = LANES == 0 ? 1 : threads / LANES;
+  const dim3 blocks(static_cast<unsigned>((a.rows + per - 1) / per)), block(threads);
+  return a.codes ? launch_pdl(norm_kernel<E, V, NV, LANES, true>, blocks, block, 0, s, a)
+                 : launch_pdl(norm_kernel<E, V, NV, LANES, false>, blocks, block, 0, s, a);
 }
 
 int round32(int n) { return (n + 31) / 32 * 32; }
@@ -251,22 +291,24 @@ cudaError_t launch_norm_v(NormArgs a, cudaStream_t s) {
   a.n = a.D / V;
   constexpr int kWarpRows = 128;         // threads of a block of several rows
   if (a.n <= 8) return launch_rows<E, V, 1, 8>(a, kWarpRows, s);
-  if (a.n <= 16) return launch_rows<E, V, 1, 16>(a, kWarpRows, s);
-  if (a.n <= 32) return launch_rows<E, V, 1, 32>(a, kWarpRows, s);
+  if (a.n <= 16) return launch_rows<E, V, 2, 8>(a, kWarpRows, s);
+  if (a.n <= 32) return launch_rows<E, V, 2, 16>(a, kWarpRows, s);
   if (a.n <= 64) return launch_rows<E, V, 2, 32>(a, kWarpRows, s);
-  if (a.n <= 128) return launch_rows<E, V, 4, 32>(a, kWarpRows, s);
   if (a.n <= 1024) return launch_rows<E, V, 2, 0>(a, round32((a.n + 1) / 2), s);
   if (a.n <= 2048) return launch_rows<E, V, 4, 0>(a, round32((a.n + 3) / 4), s);
   if constexpr (V * sizeof(E) < 16 || sizeof(E) == 4) {
     if (a.n <= 4096) return launch_rows<E, V, 8, 0>(a, round32((a.n + 7) / 8), s);
   }
+  if constexpr (V <= 2 && V * sizeof(E) <= 4) {
+    if (a.n <= 8192) return launch_rows<E, V, 16, 0>(a, round32((a.n + 15) / 16), s);
+  }
   if constexpr (V == 1) return launch_rows<E, V, 32, 0>(a, round32((a.n + 31) / 32), s);
   return cudaErrorInvalidValue;
 }
 
+// Vectors of 16 bytes, of two 16-bit elements, or single elements.
 template <typename E>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(E);
   const uint64_t strides =
       static_cast<uint64_t>(a.x_row | a.x_head | (a.add ? a.add_row | a.add_head : 0) |
                             (a.sum ? a.sum_row | a.sum_head : 0) |
@@ -275,9 +317,15 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.add) |
                       reinterpret_cast<uintptr_t>(a.sum) | reinterpret_cast<uintptr_t>(a.out) |
                       reinterpret_cast<uintptr_t>(a.weight);
-  if (a.D % V == 0 && strides % V == 0 && p % 16 == 0 &&
-      reinterpret_cast<uintptr_t>(a.codes) % V == 0)
-    return launch_norm_v<E, V>(a, s);
+  const auto fits = [&](unsigned v) {
+    return a.D % v == 0 && strides % v == 0 && p % (v * sizeof(E)) == 0 &&
+           reinterpret_cast<uintptr_t>(a.codes) % v == 0;
+  };
+  constexpr int kWide = 16 / sizeof(E);
+  if (fits(kWide)) return launch_norm_v<E, kWide>(a, s);
+  if constexpr (sizeof(E) == 2) {
+    if (fits(2)) return launch_norm_v<E, 2>(a, s);
+  }
   return launch_norm_v<E, 1>(a, s);
 }
 

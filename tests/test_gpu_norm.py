@@ -206,3 +206,42 @@ def test_binding_refusals():
         moeq4.moe_rms_norm(x, codes=x.to(torch.float8_e4m3fn), scales=torch.empty(3, device="cuda"))
     with pytest.raises(moeq4.MoeError):
         moeq4.moe_rms_norm(x)
+
+
+@pytest.mark.parametrize("dt,T,H,D", [(torch.bfloat16, 9001, 1, 2048), (torch.float16, 3001, 3, 1200),
+                                      (torch.float32, 7001, 1, 1024), (torch.bfloat16, 4100, 1, 8192)])
+def test_many_long_rows(dt, T, H, D):
+    # rows that a block goes through in turns; a row alone gives the same bits
+    x, add, weight = _inputs(T, H, D, dt, True, True, gap=1)
+    out, total = torch.empty_like(add), torch.empty_like(add)
+    codes = torch.empty(add.shape, dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.empty((T, H), device="cuda")
+    moeq4.moe_rms_norm(x, weight, out, add, total, codes, scales, eps=1e-5)
+    some = torch.tensor([0, 1, T // 2, T - 2, T - 1])
+    h, y = _ref(x[some], add[some], weight, 1e-5, 0.0)
+    _near(total[some], h, 2.0 ** -24)
+    _near(out[some], y, ARITH)
+    _check_codes(codes[some], scales[some], y)
+    for lo in range(0, T, 600):
+        part = slice(lo, min(T, lo + 600))
+        o, s2 = torch.empty_like(add[part]), torch.empty_like(add[part])
+        c, sc = torch.empty_like(codes[part]), torch.empty_like(scales[part])
+        moeq4.moe_rms_norm(x[part], weight, o, add[part], s2, c, sc, eps=1e-5)
+        assert torch.equal(o, out[part]) and torch.equal(s2, total[part])
+        assert torch.equal(c.view(torch.uint8), codes[part].view(torch.uint8))
+        assert torch.equal(sc, scales[part])
+    # in place: the norm over x's copy, the sum over add
+    x2 = x.contiguous()
+    moeq4.moe_rms_norm(x2, weight, x2, add, add, eps=1e-5)
+    assert torch.equal(x2, out) and torch.equal(add, total)
+
+
+def test_many_long_rows_without_summand():
+    x, _, _ = _inputs(6000, 1, 4096, torch.bfloat16, False, False)
+    x[5] = 0
+    x[4000, 0, 7] = math.nan
+    out = torch.empty_like(x)
+    moeq4.moe_rms_norm(x, out=out)
+    ok = [i for i in range(0, 6000, 37) if i != 4000]
+    _near(out[ok], _ref(x[ok], None, None, 1e-6, 0.0)[1], ARITH)
+    assert out[4000].isnan().all() and (out[5] == 0).all()
