@@ -360,7 +360,8 @@ moe_status moe_rms_norm(const moe_norm* a, void* stream);
 
 /* Dense projection of T tokens with its epilogue:
  *   y = act(x w^T + bias) + add,   e4m3: act(x_scale[t] w_scale[n] (x w^T) + bias) + add
- * fp32 accumulation on the tensor cores, everything after it in fp32, one rounding. */
+ * fp32 accumulation on the tensor cores (for fp32 results in pieces of 1024 bytes of K, which
+ * are added in fp32), everything after it in fp32, one rounding. */
 #define MOE_ACT_NONE      0
 #define MOE_ACT_RELU      1
 #define MOE_ACT_SILU      2  /* y / (1 + exp(-y)) */
@@ -383,7 +384,7 @@ typedef struct moe_linear_args {
 } moe_linear_args;
 
 /* One launch. x and w: 16-byte aligned, rows that do not overlap, strides and K multiples of
- * 16 bytes; out and add: aligned to their type, any stride. K <= 2^20. add may be out with
+ * 16 bytes; out and add: aligned to their type, any stride. K <= 65536. add may be out with
  * the same stride; out overlaps nothing else. T = 0 launches nothing. A token's result does
  * not depend on the other tokens' values (an infinity or NaN stays in its row), but a
  * batch of another size may add a row's products in another order. */

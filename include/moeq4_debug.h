@@ -74,8 +74,8 @@ int32_t moe_debug_kv_attention_rows(int32_t B, int32_t nq, int32_t Hq, int32_t H
  * plan[8] = tokens per tile, blocks that split K, ring stages, tensor-memory columns per
  * accumulator and in all, bytes of shared memory, mode (0: a block per tile, 1: K split, 2:
  * a pair of blocks per tile), K-chunks per stage. Calls with few tokens take another kernel. */
-moe_status moe_debug_linear_plan(int32_t T, int32_t N, int32_t K, int32_t dtype, int32_t sms,
-                                 int32_t* plan);
+moe_status moe_debug_linear_plan(int32_t T, int32_t N, int32_t K, int32_t dtype, int32_t out_dtype,
+                                 int32_t sms, int32_t* plan);
 
 #ifdef __cplusplus
 }

@@ -9,7 +9,11 @@
 //
 // A block keeps a ring of K-chunks (128 bytes of K of both operands, 128-byte swizzle)
 // that one thread fills by TMA and one warp feeds to the tensor cores; two accumulators in
-// tensor memory let 16 warps finish a tile while the next one is multiplied. Three modes:
+// tensor memory let 16 warps finish a tile while the next one is multiplied. The tensor
+// cores' fp32 sums are cut off, not rounded: a sum loses about 2^-26 of itself at each step of
+// 32 bytes of K, always towards zero. Next to results of 16 bits that is nothing (2^-16 at the
+// longest K); for fp32 results the sum is taken in pieces of 32 steps, which the finishing warps
+// add up in registers. Three modes:
 //   kSingle  a block per tile, each block several tiles
 //   kSplit   too few tiles for the multiprocessors: a cluster of 2, 4 or 8 blocks splits K;
 //            each finishes a share of the tokens, reading the others' partial sums from their
@@ -44,6 +48,8 @@ constexpr int kMaxCols = 256;              // tokens per tile at most (MMA N)
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplit = 8;
 constexpr int kMaxSplitCols = 128;         // tokens per tile at most where K is split
+constexpr int kPiece = 8;                  // K-chunks of a piece of an fp32 result's sum
+constexpr int kMaxK = 65536;
 constexpr int kBatch = 16;                 // tokens that an epilogue warp finishes at once
 constexpr size_t kSmemMax = 227 * 1024;
 
@@ -323,6 +329,7 @@ __global__ void __launch_bounds__(kThreads)
     linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                   const LinearArgs a) {
   constexpr bool kIsPair = MODE == kPair, kIsSplit = MODE == kSplit;
+  constexpr bool kPieces = sizeof(O) == 4;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -413,28 +420,32 @@ __global__ void __launch_bounds__(kThreads)
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer
     if (rank == 0 || kIsSplit) {
-      int st = 0, i = 0;                     // stage, tiles multiplied
+      int st = 0, i = 0;                     // stage, sums completed
       uint32_t ph = 0;
-      for (int tile = first; tile < tiles && ok; tile += step, ++i) {
-        const int b = i & 1;
-        ok = __all_sync(kFull, mbar_wait(&ctl.acc_empty[b], ((i >> 1) & 1) ^ 1, abortp, lim));
-        tc_fence_after();
-        for (int c = c_lo; c < c_hi && ok; c += a.sub) {
-          ok = __all_sync(kFull, mbar_wait(&ctl.full[st], ph, abortp, lim));
-          if (!ok) break;
+      for (int tile = first; tile < tiles && ok; tile += step) {
+        for (int lo = c_lo; lo < c_hi && ok; ++i) {
+          const int hi = kPieces ? min(c_hi, lo + kPiece) : c_hi;
+          const int b = i & 1;
+          ok = __all_sync(kFull, mbar_wait(&ctl.acc_empty[b], ((i >> 1) & 1) ^ 1, abortp, lim));
           tc_fence_after();
-          const int n = min(a.sub, c_hi - c);
-          uint32_t sa = smem_u32(smem) + st * sb;
-          for (int u = 0; u < n; ++u, sa += cb)
-            mma_chunk<E4M3, kIsPair>(tmem + b * a.acc, sdesc_k_sw128(sa),
-                                     sdesc_k_sw128(sa + kRows * kChunk), a.idesc, c + u != c_lo);
-          commit<kIsPair>(&ctl.empty[st]);
-          if (++st == ns) {
-            st = 0;
-            ph ^= 1;
+          for (int c = lo; c < hi && ok; c += a.sub) {
+            ok = __all_sync(kFull, mbar_wait(&ctl.full[st], ph, abortp, lim));
+            if (!ok) break;
+            tc_fence_after();
+            const int n = min(a.sub, c_hi - c);
+            uint32_t sa = smem_u32(smem) + st * sb;
+            for (int u = 0; u < n; ++u, sa += cb)
+              mma_chunk<E4M3, kIsPair>(tmem + b * a.acc, sdesc_k_sw128(sa),
+                                       sdesc_k_sw128(sa + kRows * kChunk), a.idesc, c + u != lo);
+            commit<kIsPair>(&ctl.empty[st]);
+            if (++st == ns) {
+              st = 0;
+              ph ^= 1;
+            }
           }
+          if (ok) commit<kIsPair>(&ctl.acc_full[b]);
+          lo = hi;
         }
-        if (ok) commit<kIsPair>(&ctl.acc_full[b]);
       }
       if (!ok && lane == 0 && atomicExch(&ctl.abort, 1) == 0)
         atomicOr(a.err, MOE_DEVERR_PIPE_TIMEOUT);
@@ -448,9 +459,16 @@ __global__ void __launch_bounds__(kThreads)
     // warp w reads tensor-memory lanes 32 (w % 4) .. (features n, one per lane) and every
     // kParts-th batch of tokens
     const int q = warp & 3, part = (warp - 2) >> 2;
-    int i = 0;
-    for (int tile = first; tile < tiles && ok; tile += step, ++i) {
-      const int b = i & 1;
+    int i = 0;                               // sums read
+    const auto give_back = [&](int b) {      // of an accumulator
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kIsPair) arrive_leader(&ctl.acc_empty[b]);
+        else mbar_arrive(&ctl.acc_empty[b]);
+      }
+    };
+    for (int tile = first; tile < tiles && ok; tile += step) {
       int fn, ft;
       tile_at(a, tile, fn, ft);
       n0 = fn * fw + f0;
@@ -462,39 +480,76 @@ __global__ void __launch_bounds__(kThreads)
       if constexpr (!kIsSplit) {
         bias = in && a.bias ? a.bias[n] : 0.f;
         ws = in && E4M3 ? a.w_scale[n] : 1.f;
-        next.load(a, t0 + part * kBatch, 1, live - part * kBatch, n, in);
+        if constexpr (!kPieces) next.load(a, t0 + part * kBatch, 1, live - part * kBatch, n, in);
       }
-      ok = __all_sync(kFull, mbar_wait(&ctl.acc_full[b], (i >> 1) & 1, abortp, lim));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem + b * a.acc + (static_cast<uint32_t>(q * 32) << 16);
-      for (int c = part * kBatch; c < live; c += kParts * kBatch) {
-        uint32_t v[kBatch];
-        tmem_ld_32x32b_x16(taddr + c, v);
+      // 16 tokens' sums: results (kSplit: partial sums [token][feature] over the ring, which
+      // nothing uses any more)
+      const auto put = [&](float (&y)[kBatch], int c, Tokens<E4M3, O, kBatch>& of) {
         if constexpr (kIsSplit) {
-          // partial sums [token][feature] over the ring, which nothing uses any more
-          tmem_ld_wait();
-          tmem_regs_ready(v);
-          uint32_t* part_sums = reinterpret_cast<uint32_t*>(smem) + c * kRows + q * 32 + lane;
+          float* part_sums = reinterpret_cast<float*>(smem) + c * kRows + q * 32 + lane;
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) part_sums[j * kRows] = v[j];
+          for (int j = 0; j < kBatch; ++j) part_sums[j * kRows] = y[j];
         } else {
+          of.finish(a, y, t0 + c, 1, live - c, n, in, ws, bias);
+        }
+        __syncwarp();
+      };
+      if constexpr (kPieces) {
+        constexpr int kMine = kMaxCols / (kParts * kBatch);   // batches of a warp at most
+        float sum[kMine][kBatch];
+#pragma unroll
+        for (int m = 0; m < kMine; ++m)
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) sum[m][j] = 0.f;
+        for (int lo = c_lo; lo < c_hi; lo += kPiece, ++i) {
+          const int b = i & 1;
+          ok = __all_sync(kFull, mbar_wait(&ctl.acc_full[b], (i >> 1) & 1, abortp, lim));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t taddr = tmem + b * a.acc + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+          for (int m = 0; m < kMine; ++m) {
+            const int c = (part + m * kParts) * kBatch;
+            if (c < live) {
+              uint32_t v[kBatch];
+              tmem_ld_32x32b_x16(taddr + c, v);
+              tmem_ld_wait();
+              tmem_regs_ready(v);
+#pragma unroll
+              for (int j = 0; j < kBatch; ++j) sum[m][j] += __uint_as_float(v[j]);
+            }
+          }
+          give_back(b);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+          const int c = (part + m * kParts) * kBatch;
+          if (c < live) {
+            if constexpr (!kIsSplit) next.load(a, t0 + c, 1, live - c, n, in);
+            put(sum[m], c, next);
+          }
+        }
+      } else {
+        const int b = i++ & 1;
+        ok = __all_sync(kFull, mbar_wait(&ctl.acc_full[b], ((i - 1) >> 1) & 1, abortp, lim));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem + b * a.acc + (static_cast<uint32_t>(q * 32) << 16);
+        for (int c = part * kBatch; c < live; c += kParts * kBatch) {
+          uint32_t v[kBatch];
+          tmem_ld_32x32b_x16(taddr + c, v);
           Tokens<E4M3, O, kBatch> now = next;
-          next.load(a, t0 + c + kParts * kBatch, 1, live - c - kParts * kBatch, n, in);
+          if constexpr (!kIsSplit)
+            next.load(a, t0 + c + kParts * kBatch, 1, live - c - kParts * kBatch, n, in);
           tmem_ld_wait();
           tmem_regs_ready(v);
           float y[kBatch];
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) y[j] = __uint_as_float(v[j]);
-          now.finish(a, y, t0 + c, 1, live - c, n, in, ws, bias);
+          put(y, c, now);
         }
-        __syncwarp();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kIsPair) arrive_leader(&ctl.acc_empty[b]);
-        else mbar_arrive(&ctl.acc_empty[b]);
+        give_back(b);
       }
     }
     if (!ok && lane == 0 && atomicExch(&ctl.abort, 1) == 0)
@@ -615,11 +670,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) linear_few_kernel(const Few
 #pragma unroll
   for (int i = 0; i < NT; ++i)
     xp[i] = a.x + static_cast<int64_t>(min(i * 8 + g, a.l.T - 1)) * a.x_row + c * 16;
-  float d[NT][4];
+  float sum[NT][4];          // of pieces of 2 kU steps: the products' own sums are cut off
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) sum[i][j] = 0.f;
   constexpr int kU = NT == 1 ? 4 : 2;        // steps of 64 bytes whose loads go together
   const int last = a.k_bytes - c * 16;       // bytes of K from this lane's first place on
   for (int k0 = warp * 128; k0 < a.k_bytes; k0 += warps * 128 * (kU / 2)) {
@@ -635,6 +690,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) linear_few_kernel(const Few
       for (int i = 0; i < NT; ++i)
         x[u][i] = in ? __ldg(reinterpret_cast<const uint4*>(xp[i] + k)) : zero;
     }
+    float d[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -642,11 +702,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) linear_few_kernel(const Few
         mma_16x8<E4M3, HALF>(d[i], p[u].x, q[u].x, p[u].y, q[u].y, x[u][i].x, x[u][i].y);
         mma_16x8<E4M3, HALF>(d[i], p[u].z, q[u].z, p[u].w, q[u].w, x[u][i].z, x[u][i].w);
       }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[i][j] += d[i][j];
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) part[warp][i * 8 + 2 * c + (j & 1)][g + (j >> 1) * 8] = d[i][j];
+    for (int j = 0; j < 4; ++j) part[warp][i * 8 + 2 * c + (j & 1)][g + (j >> 1) * 8] = sum[i][j];
   __syncthreads();
   for (int v = tid; v < NT * 8 * kFewRows; v += warps * 32) {
     const int t = v / kFewRows, r = v % kFewRows, n = n0 + r;
@@ -675,6 +739,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t s) {
 // Sizes of one call.
 struct Plan {
   int mode, cols, splits, sub, stages, acc, tcols;
+  bool pieces;
   size_t smem;
 };
 
@@ -702,7 +767,7 @@ int chunks_per_stage(int cols, int chunks) {
 void lay_out(Plan& p, int nch) {
   const int chunks = (nch + p.splits - 1) / p.splits, cb = chunk_bytes(p.cols, p.mode);
   p.acc = next_pow2(p.cols);
-  p.tcols = std::max(32, p.mode == kSplit ? p.acc : 2 * p.acc);
+  p.tcols = std::max(32, p.mode == kSplit && !p.pieces ? p.acc : 2 * p.acc);
   const size_t fixed = 1024 + sizeof(Ctl);
   p.sub = chunks_per_stage(p.cols, chunks);
   const int sb = p.sub * cb;
@@ -718,12 +783,13 @@ void lay_out(Plan& p, int nch) {
 // at 32 columns 7.5 and 7.2, by 8 9.9 and 9.0, not split 9.1 and 8.9; 2048 -> 8192: 4096 tokens
 // in pairs 78 and 72, without 94 and 86; 8192 -> 8192: 16 tokens split by 2 25.6 and 24.1, not
 // split 27.9 and 27.8.
-Plan make_plan(int T, int N, int nch, int sms) {
+Plan make_plan(int T, int N, int nch, bool pieces, int sms) {
   const int rows_n = (N + kRows - 1) / kRows;
   const int most = std::min(kMaxCols, (T + 15) / 16 * 16);
   const double bytes = static_cast<double>(N) * nch * kChunk;
   double best = 1e300;
   Plan p{};
+  p.pieces = pieces;
   const auto offer = [&](int mode, int cols, int splits, double cost) {
     if (cost >= best) return;
     best = cost;
@@ -755,6 +821,7 @@ Plan make_plan(int T, int N, int nch, int sms) {
       q.mode = kSplit;
       q.cols = cols;
       q.splits = splits;
+      q.pieces = pieces;
       lay_out(q, nch);
       const int per_sm = static_cast<int>(kSmemMax + 1024) / static_cast<int>(q.smem + 1024);
       const int64_t room = std::max(1, sms / 8 * per_sm / splits * 8 - (per_sm == 1 ? 1 : 0));
@@ -825,7 +892,7 @@ extern "C" moe_status moe_linear(const moe_linear_args* l, void* stream) {
       l->act < MOE_ACT_NONE || l->act > MOE_ACT_GELU_TANH)
     return MOE_ERR_ARG;
   const int es = e4m3 ? 1 : 2, os = l->out_dtype == MOE_F32 ? 4 : 2;
-  if (l->K % (16 / es) || l->K > (1 << 20)) return MOE_ERR_SHAPE;
+  if (l->K % (16 / es) || l->K > kMaxK) return MOE_ERR_SHAPE;
   if (!l->err || !l->w || (e4m3 && !l->w_scale) || (!e4m3 && (l->x_scale || l->w_scale)))
     return MOE_ERR_ARG;
   if (l->N > 1 && (l->w_row < l->K || l->w_row >= (1ll << 39) / es)) return MOE_ERR_SHAPE;
@@ -882,7 +949,7 @@ extern "C" moe_status moe_linear(const moe_linear_args* l, void* stream) {
                                   : launch_few<false, false, __nv_bfloat16>(f, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
-  const Plan p = make_plan(l->T, l->N, a.nch, sms);
+  const Plan p = make_plan(l->T, l->N, a.nch, l->out_dtype == MOE_F32, sms);
   a.cols = p.cols;
   const int fw = p.mode == kPair ? 2 * kRows : kRows;
   a.tiles_n = (l->N - 1) / fw + 1;
@@ -918,11 +985,11 @@ extern "C" moe_status moe_linear(const moe_linear_args* l, void* stream) {
 }
 
 extern "C" moe_status moe_debug_linear_plan(int32_t T, int32_t N, int32_t K, int32_t dtype,
-                                            int32_t sms, int32_t* plan) {
+                                            int32_t out_dtype, int32_t sms, int32_t* plan) {
   using namespace moeq4;
   if (T < 1 || N < 1 || K < 1 || sms < 1 || !plan) return MOE_ERR_ARG;
   const int elems = dtype == MOE_E4M3 ? kChunk : kChunk / 2, nch = (K + elems - 1) / elems;
-  const Plan p = make_plan(T, N, nch, sms);
+  const Plan p = make_plan(T, N, nch, out_dtype == MOE_F32, sms);
   const int32_t v[8] = {p.cols, p.splits, p.stages, p.acc, p.tcols, static_cast<int32_t>(p.smem),
                         p.mode, p.sub};
   for (int i = 0; i < 8; ++i) plan[i] = v[i];

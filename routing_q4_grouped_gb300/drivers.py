@@ -6,6 +6,10 @@ for profilers (ncu) and quick timings.
     python -m routing_q4_grouped_gb300.drivers attention B nq length prefix [bits] [D] [calls]
                                                                   # moe_kv_attention
     python -m routing_q4_grouped_gb300.drivers step B length [bits] [calls]   # one decoder step
+    python -m routing_q4_grouped_gb300.drivers block B length [bits] [calls]  # ... from hidden rows
+    python -m routing_q4_grouped_gb300.drivers linear T N K [e4m3] [calls]    # moe_linear
+    python -m routing_q4_grouped_gb300.drivers norm T D [codes] [calls]       # moe_rms_norm
+    python -m routing_q4_grouped_gb300.drivers scored T E groups [calls]      # moe_route_scored
 
 The full-width layer has d = 2048, 256 experts, top-8, f = f_s = 512 and the
 value recipe of the t512 workload; T tokens of its seeded x and logits. Each
@@ -19,7 +23,16 @@ tokens behind a shared prefix (0: none), 16 query and 2 key/value heads.
 layer uses them for a batch of B requests that decode one token each: the fused
 query/key/value projection, moe_kv_append (turn, quantise, write),
 moe_kv_attention, the output projection, then moe_layer on the sum. The two
-projections are plain matrix products of random bf16 weights.
+projections are moe_linear with random bf16 weights, the second with the residual
+in its epilogue.
+
+``block`` is the step from one hidden row per request to the next: moe_rms_norm
+with the residual, the projection, the norm of query and key heads, append,
+attention, the output projection, moe_rms_norm, the router's logits, and
+moe_layer_scored (sigmoid scores, a bias, 4 of 8 groups of experts).
+
+``linear``: e4m3 0 or 1. ``norm``: rows with a residual, into bf16 or (codes 1) e4m3
+codes. ``scored``: sigmoid scores with a bias, half of the groups, top 8.
 """
 from __future__ import annotations
 
@@ -81,39 +94,121 @@ def _attention(B: int, nq: int, length: int, prefix: int, bits: int, D: int, cal
                                           prefix_table=ptable, prefix_len=prefix), calls, cache)
 
 
+class _Attention:
+    """The attention side of one decoder layer for B requests that decode one token each."""
+
+    def __init__(self, cfg, B: int, length: int, bits: int):
+        self.B, self.length, self.D = B, length, cfg.d // HQ
+        D = self.D
+        heads = HQ + 2 * HKV
+        self.qkv = moeq4.Linear(_weights(heads * D, cfg.d))
+        self.out = moeq4.Linear(_weights(cfg.d, HQ * D))
+        pages, self.table, _ = _tables(B, length, 0)
+        self.cache = _cache(pages, bits, D)
+        self.rope = moeq4.RopeSpec(moeq4.moe_rope_phases(D, 1e6).cuda(), D)
+        self.lens = torch.full((B,), length, dtype=torch.int32, device="cuda")
+        self.pos = self.lens - 1                       # the new token is the context's last
+        last = (self.pos // self.cache.page_size).long()
+        self.slots = (self.table.gather(1, last[:, None])[:, 0] * self.cache.page_size
+                      + self.pos % self.cache.page_size).int()
+        self.heads = torch.empty((B, heads, D), dtype=torch.bfloat16, device="cuda")
+        self.att = torch.empty((B, HQ, D), dtype=torch.bfloat16, device="cuda")
+        self.ws = moeq4.alloc_workspace(
+            moeq4.moe_kv_attention_workspace_size(B, 1, HQ, HKV, D, length, 0))
+
+    def __call__(self, x, residual, h, norm=None):
+        """h = residual + the attention of x's rows."""
+        moeq4.moe_linear(x, self.qkv, self.heads.view(self.B, -1))
+        qk = self.heads[:, :HQ + HKV]
+        if norm is not None:
+            moeq4.moe_rms_norm(qk, norm, qk)
+        q = qk[:, :HQ]
+        moeq4.moe_kv_append(self.cache, qk[:, HQ:], self.heads[:, HQ + HKV:], self.slots, self.pos,
+                            self.rope, q, q)
+        moeq4.moe_kv_attention(q, self.cache, self.table, self.lens, self.length, self.att, self.ws)
+        moeq4.moe_linear(self.att.view(self.B, -1), self.out, h, add=residual)
+        return h
+
+
+def _weights(n: int, k: int) -> torch.Tensor:
+    return torch.randn((n, k), device="cuda").mul_(k ** -0.5).bfloat16()
+
+
 def _step(B: int, length: int, bits: int, calls: int) -> None:
     cfg = dataclasses.replace(synth.CONFIGS["t512"], T=B)
-    D = cfg.d // HQ
     W = moeq4.DeviceWeights.from_host(synth.gen_weights(cfg, 0))
     lay = moeq4.Layer(W, B, cfg.k, None)
     lg = torch.from_numpy(synth.gen_logits(cfg, 0, B)).cuda()
     x = torch.from_numpy(synth.gen_x(cfg, B).view(np.int16)).cuda().view(torch.bfloat16)
-    w_qkv = torch.randn((cfg.d, (HQ + 2 * HKV) * D), device="cuda").mul_(cfg.d ** -0.5).bfloat16()
-    w_out = torch.randn((HQ * D, cfg.d), device="cuda").mul_(cfg.d ** -0.5).bfloat16()
-    pages, table, _ = _tables(B, length, 0)
-    cache = _cache(pages, bits, D)
-    rope = moeq4.RopeSpec(moeq4.moe_rope_phases(D, 1e6).cuda(), D)
-    lens = torch.full((B,), length, dtype=torch.int32, device="cuda")
-    pos = lens - 1                                     # the new token is the context's last
-    last = (pos // cache.page_size).long()
-    slots = (table.gather(1, last[:, None])[:, 0] * cache.page_size + pos % cache.page_size).int()
-    att = torch.empty((B, HQ, D), dtype=torch.bfloat16, device="cuda")
-    ws = moeq4.alloc_workspace(moeq4.moe_kv_attention_workspace_size(B, 1, HQ, HKV, D, length, 0))
-
-    def step():
-        qkv = (x @ w_qkv).view(B, HQ + 2 * HKV, D)
-        q = qkv[:, :HQ]
-        moeq4.moe_kv_append(cache, qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:], slots, pos, rope, q, q)
-        moeq4.moe_kv_attention(q, cache, table, lens, length, att, ws)
-        h = x + att.view(B, -1) @ w_out
-        return lay(h, lg)
-
-    _timed(step, calls, cache)
-    if moeq4.moe_get_device_error(lay.route):
-        raise RuntimeError("device error word of the expert layer set")
+    attend, h = _Attention(cfg, B, length, bits), torch.empty_like(x)
+    _timed(lambda: lay(attend(x, x, h), lg), calls, attend.cache)
+    _clean(lay.route, attend.qkv, attend.out)
 
 
-def _timed(fn, calls: int, route) -> None:
+def _block(B: int, length: int, bits: int, calls: int) -> None:
+    cfg = dataclasses.replace(synth.CONFIGS["t512"], T=B)
+    W = moeq4.DeviceWeights.from_host(synth.gen_weights(cfg, 0))
+    route = moeq4.RouteBuffers.alloc(B, cfg.E, cfg.k, moeq4.default_block_m(B, cfg.E, cfg.k))
+    ws = moeq4.alloc_workspace(moeq4.moe_layer_workspace_size(B, cfg.E, cfg.k, W.d, W.f, W.f_s,
+                                                              route.block_m))
+    x = torch.from_numpy(synth.gen_x(cfg, B).view(np.int16)).cuda().view(torch.bfloat16)
+    ones = torch.ones(cfg.d, dtype=torch.bfloat16, device="cuda")
+    router = moeq4.Linear(_weights(cfg.E, cfg.d))
+    score = moeq4.RouteScore(moeq4.MOE_SCORE_SIGMOID, 0.1 * torch.randn(cfg.E, device="cuda"),
+                             groups=8, top_groups=4, group_best=2, factor=2.5)
+    attend = _Attention(cfg, B, length, bits)
+    h1, n1, h2, n2, y = (torch.zeros_like(x) for _ in range(5))
+    lg = torch.empty((B, cfg.E), dtype=torch.float32, device="cuda")
+
+    def block():
+        # y: the experts' output of the layer before (here: of the call before)
+        moeq4.moe_rms_norm(x, ones, n1, add=y, sum=h1)
+        attend(n1, h1, h2, ones[:attend.D])
+        moeq4.moe_rms_norm(h2, ones, n2)
+        moeq4.moe_linear(n2, router, lg)
+        moeq4.moe_layer_scored(n2, lg, W, score, route, y, ws)
+
+    _timed(block, calls, attend.cache)
+    _clean(route, attend.qkv, attend.out, router)
+
+
+def _clean(*owners) -> None:
+    if any(moeq4.moe_get_device_error(o) for o in owners):
+        raise RuntimeError("device error word set")
+
+
+def _linear(T: int, N: int, K: int, e4m3: int, calls: int) -> None:
+    x, w, scale = torch.randn((T, K), device="cuda"), torch.randn((N, K), device="cuda"), None
+    dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    if e4m3:
+        scale = torch.full((max(T, N),), K ** -0.25, device="cuda")
+    lin = moeq4.Linear(w.to(dtype), None, scale[:N].contiguous() if e4m3 else None)
+    x, xs = x.to(dtype), scale[:T].contiguous() if e4m3 else None
+    out = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    _timed(lambda: moeq4.moe_linear(x, lin, out, x_scale=xs), calls, lin)
+
+
+def _norm(T: int, D: int, codes: int, calls: int) -> None:
+    x, add = (torch.randn((T, D), device="cuda").bfloat16() for _ in range(2))
+    weight, total = torch.ones_like(x[0]), torch.empty_like(x)
+    if codes:
+        kw = dict(codes=torch.empty((T, D), dtype=torch.float8_e4m3fn, device="cuda"),
+                  scales=torch.empty(T, device="cuda"))
+    else:
+        kw = dict(out=torch.empty_like(x))
+    _timed(lambda: moeq4.moe_rms_norm(x, weight, add=add, sum=total, **kw), calls)
+
+
+def _scored(T: int, E: int, groups: int, calls: int) -> None:
+    lg = 1.5 * torch.randn((T, E), device="cuda")
+    score = moeq4.RouteScore(moeq4.MOE_SCORE_SIGMOID, 0.1 * torch.randn(E, device="cuda"), groups,
+                             max(1, groups // 2), 2 if groups > 1 else 1, factor=2.5)
+    out = moeq4.RouteBuffers.alloc(T, E, 8)
+    ws = moeq4.alloc_workspace(moeq4.moe_route_workspace_size(T, E, 8))
+    _timed(lambda: moeq4.moe_route_scored(lg, score, out, ws), calls, out)
+
+
+def _timed(fn, calls: int, owner=None) -> None:
     fn()
     torch.cuda.synchronize()
     e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -123,8 +218,8 @@ def _timed(fn, calls: int, route) -> None:
     e1.record()
     torch.cuda.synchronize()
     us = e0.elapsed_time(e1) / max(1, calls - 1) * 1e3
-    print(f"mean {us:.1f} us per call over {calls - 1} calls; device error word "
-          f"{moeq4.moe_get_device_error(route)}")
+    said = "" if owner is None else f"; device error word {moeq4.moe_get_device_error(owner)}"
+    print(f"mean {us:.1f} us per call over {calls - 1} calls{said}")
 
 
 def main(argv) -> None:
@@ -132,9 +227,15 @@ def main(argv) -> None:
     if what == "attention":
         B, nq, length, prefix, bits, D, calls = nums + [8, 128, 4][len(nums) - 4:]
         _attention(B, nq, length, prefix, bits, D, calls)
-    elif what == "step":
+    elif what in ("step", "block"):
         B, length, bits, calls = nums + [8, 4][len(nums) - 2:]
-        _step(B, length, bits, calls)
+        {"step": _step, "block": _block}[what](B, length, bits, calls)
+    elif what == "linear":
+        _linear(*(nums + [0, 4][len(nums) - 3:]))
+    elif what == "norm":
+        _norm(*(nums + [0, 4][len(nums) - 2:]))
+    elif what == "scored":
+        _scored(*(nums + [4][len(nums) - 3:]))
     else:
         {"layer": _layer, "router": _router}[what](nums[0], nums[1] if len(nums) > 1 else 4)
 

@@ -167,7 +167,7 @@ _SIGS = {
     "moe_debug_tmem_layout": (_c_i32, [_c_ptr, _c_ptr]),
     "moe_debug_kv_page": (_c_i32, [_c_i32, _c_i32]),
     "moe_debug_kv_attention_rows": (_c_i32, [_c_i32] * 7),
-    "moe_debug_linear_plan": (_c_i32, [_c_i32] * 5 + [_c_ptr]),
+    "moe_debug_linear_plan": (_c_i32, [_c_i32] * 6 + [_c_ptr]),
     "moe_debug_noalloc_scratch": (_c_i32, [ctypes.POINTER(_c_ptr), ctypes.POINTER(_c_size)]),
 }
 
@@ -886,10 +886,10 @@ def moe_debug_kv_attention_rows(B, nq, Hq, Hkv, D, max_len, prefix_len=0) -> int
     return lib().moe_debug_kv_attention_rows(B, nq, Hq, Hkv, D, max_len, prefix_len)
 
 
-def moe_debug_linear_plan(T, N, K, dtype=MOE_BF16, sms=152) -> dict:
+def moe_debug_linear_plan(T, N, K, dtype=MOE_BF16, out_dtype=MOE_BF16, sms=152) -> dict:
     """How moe_linear would lay out a call. Host only."""
     v = (_c_i32 * 8)()
-    _check("moe_debug_linear_plan", lib().moe_debug_linear_plan(T, N, K, dtype, sms, v))
+    _check("moe_debug_linear_plan", lib().moe_debug_linear_plan(T, N, K, dtype, out_dtype, sms, v))
     return dict(zip(("cols", "splits", "stages", "acc", "tcols", "smem", "mode", "sub"), v))
 
 

@@ -260,3 +260,22 @@ def test_binding_refusals():
         moeq4.Linear(w.to(E4M3))
     with pytest.raises(ValueError, match="bias must hold"):
         moeq4.Linear(w, torch.zeros(63, device="cuda"))
+
+
+@pytest.mark.parametrize("dt", [BF16, E4M3])
+@pytest.mark.parametrize("T,N,K", [(1, 256, 2048), (12, 128, 8192), (64, 512, 4096), (300, 256, 2048),
+                                   (2047, 256, 4096), (3000, 2048, 1024), (700, 384, 16384)])
+def test_fp32_results_of_long_sums(T, N, K, dt):
+    # sums whose terms have one sign: what each step cuts off adds up. A piece has 32 steps, each
+    # of which cuts off at most 2^-23 of the sum so far; the pieces' additions, at most 64 of them,
+    # round by 2^-24 of theirs: 32 / 2 * 2^-23 (a sum that grows) + 64 / 2 * 2^-24 = 2^-18, and the
+    # products within one step are added with a few more (4 of 2^-23).
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.rand((T, K), generator=g, device="cuda").to(dt)
+    w = torch.rand((N, K), generator=g, device="cuda").to(dt)
+    one = torch.ones(max(T, N), device="cuda")
+    lin = moeq4.Linear(w, None, one[:N].clone() if dt is E4M3 else None)
+    out = torch.empty((T, N), device="cuda")
+    moeq4.moe_linear(x, lin, out, x_scale=one[:T].clone() if dt is E4M3 else None)
+    want = _exact(x, w)
+    assert ((out.double() - want).abs() <= want * (2.0 ** -18 + 2.0 ** -21)).all()

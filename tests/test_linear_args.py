@@ -38,7 +38,7 @@ E4M3 = dict(dtype=3, x_scale=5 * FAKE, w_scale=6 * FAKE)
     (ARG, dict(w_scale=FAKE)), (ARG, dict(E4M3, x_scale=None)), (ARG, dict(E4M3, w_scale=None)),
     (ARG, dict(out=FAKE)), (ARG, dict(out=2 * FAKE)),
     (ARG, dict(add=3 * FAKE, add_row=128)),                  # in place, another stride
-    (SHAPE, dict(K=252)), (SHAPE, dict(E4M3, K=248)), (SHAPE, dict(K=(1 << 20) + 8)),
+    (SHAPE, dict(K=252)), (SHAPE, dict(E4M3, K=248)), (SHAPE, dict(K=65544, x_row=65544, w_row=65544)),
     (SHAPE, dict(x_row=248)), (SHAPE, dict(w_row=0)), (SHAPE, dict(out_row=63)),
     (SHAPE, dict(add=7 * FAKE, add_row=-64)), (SHAPE, dict(x_row=1 << 40)),
     (ALIGN, dict(x=FAKE + 8)), (ALIGN, dict(w=FAKE + 2)), (ALIGN, dict(x_row=260)),
@@ -66,20 +66,20 @@ def test_binding_refuses_what_does_not_fit(L):
     assert ctypes.sizeof(L.LinearC) == L._LINEAR.size
 
 
-@pytest.mark.parametrize("dtype", [0, 3])
-def test_layouts_fit_the_multiprocessor(L, dtype):
+@pytest.mark.parametrize("dtype,out", [(0, 0), (0, 2), (3, 0), (3, 2)])
+def test_layouts_fit_the_multiprocessor(L, dtype, out):
     # shared memory within the limit and in proportion to tensor memory (blocks that run side
     # by side never wait for columns), accumulators within it, K split no finer than its chunks
     sizes = sorted({1, 2, 15, 16, 17, 33, 64, 100, 128, 250, 256, 257, 300, 512, 1000, 2047, 4096, 8191})
     for T in sizes + [70000, 1 << 24]:
         for N in (1, 127, 128, 129, 256, 2048, 2560, 8192, 16384, 100000):
-            for K in (16, 64, 80, 128, 512, 2048, 8192, 1 << 20):
-                p = L.moe_debug_linear_plan(T, N, K, dtype)
+            for K in (16, 64, 80, 128, 512, 2048, 8192, 65536):
+                p = L.moe_debug_linear_plan(T, N, K, dtype, out)
                 chunks = -(-K // (128 if dtype == 3 else 64))
                 assert p["cols"] % 16 == 0 and 16 <= p["cols"] <= 256
                 assert p["acc"] >= p["cols"] and p["acc"] & (p["acc"] - 1) == 0
                 assert 32 <= p["tcols"] <= 512 and p["tcols"] & (p["tcols"] - 1) == 0
-                assert p["tcols"] >= (p["acc"] if p["splits"] > 1 else 2 * p["acc"])
+                assert p["tcols"] >= (p["acc"] if p["splits"] > 1 and out != 2 else 2 * p["acc"])
                 assert p["splits"] in (1, 2, 4, 8) and p["splits"] <= chunks
                 assert p["cols"] % p["splits"] == 0 and 2 <= p["stages"] <= 12
                 assert (p["mode"] == 1) == (p["splits"] > 1)
