@@ -384,7 +384,7 @@ typedef struct moe_linear_args {
 } moe_linear_args;
 
 /* One launch. x and w: 16-byte aligned, rows that do not overlap, strides and K multiples of
- * 16 bytes; out and add: aligned to their type, any stride. K <= 65536. add may be out with
+ * 16 bytes; out and add: aligned to their type, any stride. K <= 65536; T, N <= 2^30. add may be out with
  * the same stride; out overlaps nothing else. T = 0 launches nothing. A token's result does
  * not depend on the other tokens' values (an infinity or NaN stays in its row), but a
  * batch of another size may add a row's products in another order. */

@@ -50,6 +50,7 @@ constexpr int kMaxSplit = 8;
 constexpr int kMaxSplitCols = 128;         // tokens per tile at most where K is split
 constexpr int kPiece = 8;                  // K-chunks of a piece of an fp32 result's sum
 constexpr int kMaxK = 65536;
+constexpr int kMaxRows = 1 << 30;          // tokens, features
 constexpr int kBatch = 16;                 // tokens that an epilogue warp finishes at once
 constexpr size_t kSmemMax = 227 * 1024;
 
@@ -892,7 +893,7 @@ extern "C" moe_status moe_linear(const moe_linear_args* l, void* stream) {
       l->act < MOE_ACT_NONE || l->act > MOE_ACT_GELU_TANH)
     return MOE_ERR_ARG;
   const int es = e4m3 ? 1 : 2, os = l->out_dtype == MOE_F32 ? 4 : 2;
-  if (l->K % (16 / es) || l->K > kMaxK) return MOE_ERR_SHAPE;
+  if (l->K % (16 / es) || l->K > kMaxK || l->T > kMaxRows || l->N > kMaxRows) return MOE_ERR_SHAPE;
   if (!l->err || !l->w || (e4m3 && !l->w_scale) || (!e4m3 && (l->x_scale || l->w_scale)))
     return MOE_ERR_ARG;
   if (l->N > 1 && (l->w_row < l->K || l->w_row >= (1ll << 39) / es)) return MOE_ERR_SHAPE;

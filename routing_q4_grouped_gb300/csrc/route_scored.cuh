@@ -324,7 +324,8 @@ __device__ __forceinline__ bool select_scored_fast(const RouteArgs& a, const Sco
       }
     }
     const bool there = lane < a.groups;
-    const float rank = !there ? -INFINITY : a.group_best == 2 ? fmaxf(g0 + g1, -3.402823466e38f) : g0;
+    const float rank = !there ? -INFINITY : a.group_best == 2 ? fminf(fmaxf(g0 + g1, -3.402823466e38f), 3.402823466e38f)
+                                     : g0;
     int ahead = 0;
     for (int g = 0; g < a.groups; ++g) ahead += __shfl_sync(kFull, rank, g) > rank ? 1 : 0;
     const bool stays = there && ahead < a.top_groups;      // (equal ranks: perhaps too many)

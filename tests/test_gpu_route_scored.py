@@ -244,3 +244,29 @@ def test_saturated_scores(top):
     tiny = rng.standard_normal((40, 64)) * 10.0 ** rng.integers(-44, -8, (40, 64)).astype(float)
     _check(tiny, 8, sigmoid=True)
     _check(tiny, 8)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_experts_forced_in(sigmoid):
+    # several +inf biases in several groups: ranks beyond fp32, equal keys
+    rng = np.random.default_rng(12)
+    z = rng.standard_normal((40, 64))
+    for forced in ([3], [3, 5], [3, 5, 9, 11, 20], list(range(0, 64, 3)), list(range(64))):
+        bias = 0.1 * rng.standard_normal(64)
+        bias[forced] = math.inf
+        bias[60:] = -math.inf
+        for top, best in ((2, 2), (4, 2), (3, 1)):
+            _check(z, 8, sigmoid=sigmoid, bias=bias, groups=8, top_groups=top, group_best=best)
+
+
+@pytest.mark.parametrize("E,groups", [(300, 12), (384, 8), (384, 6), (512, 8), (640, 20), (257, 1)])
+def test_more_experts(E, groups):
+    rng = np.random.default_rng(E)
+    for T in (5, 1100):
+        z = 1.5 * rng.standard_normal((T, E))
+        bias = 0.1 * rng.standard_normal(E)
+        top = max(1, groups // 2)
+        if T > 1000:
+            z = z[rng.integers(0, 40, T)]          # (few different tokens: the oracle is slow)
+        _check(z, 10, sigmoid=True, bias=bias, groups=groups, top_groups=top, group_best=2)
+        _check(z, 10, renorm=False, groups=groups, top_groups=top)

@@ -39,6 +39,7 @@ E4M3 = dict(dtype=3, x_scale=5 * FAKE, w_scale=6 * FAKE)
     (ARG, dict(out=FAKE)), (ARG, dict(out=2 * FAKE)),
     (ARG, dict(add=3 * FAKE, add_row=128)),                  # in place, another stride
     (SHAPE, dict(K=252)), (SHAPE, dict(E4M3, K=248)), (SHAPE, dict(K=65544, x_row=65544, w_row=65544)),
+    (SHAPE, dict(T=(1 << 30) + 1)), (SHAPE, dict(N=(1 << 30) + 1, out_row=1 << 31)),
     (SHAPE, dict(x_row=248)), (SHAPE, dict(w_row=0)), (SHAPE, dict(out_row=63)),
     (SHAPE, dict(add=7 * FAKE, add_row=-64)), (SHAPE, dict(x_row=1 << 40)),
     (ALIGN, dict(x=FAKE + 8)), (ALIGN, dict(w=FAKE + 2)), (ALIGN, dict(x_row=260)),
