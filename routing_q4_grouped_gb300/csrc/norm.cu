@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -70,6 +71,48 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ float from_f(float v) { return v; }
 
+// The elements of a vector as floats, and back, two at a time where they have 16 bits.
+template <int V>
+__device__ __forceinline__ void unpack(const Vec<__nv_bfloat16, V>& p, float (&f)[V]) {
+  if constexpr (V % 2 == 0) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    f[0] = to_f(p.e[0]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void unpack(const Vec<__half, V>& p, float (&f)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = to_f(p.e[i]);
+}
+template <int V>
+__device__ __forceinline__ void unpack(const Vec<float, V>& p, float (&f)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = p.e[i];
+}
+template <typename E, int V>
+__device__ __forceinline__ Vec<E, V> pack(const float (&f)[V]) {
+  Vec<E, V> w;
+  if constexpr (V % 2 == 0 && sizeof(E) == 2) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      if constexpr (std::is_same_v<E, __nv_bfloat16>)
+        *reinterpret_cast<__nv_bfloat162*>(&w.e[i]) = __floats2bfloat162_rn(f[i], f[i + 1]);
+      else
+        *reinterpret_cast<__half2*>(&w.e[i]) = __floats2half2_rn(f[i], f[i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) w.e[i] = from_f<E>(f[i]);
+  }
+  return w;
+}
+
 // Sum and unsigned maximum over the lanes of a row: LANES neighbouring lanes of a warp
 // (LANES <= 32), or the whole block (LANES = 0; `sh` holds two words per warp and is used by one
 // call only; the order of the additions is fixed).
@@ -117,25 +160,34 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, float (&v)[NV][V],
   if (a.sum && live) {
     Vt* o = reinterpret_cast<Vt*>(static_cast<E*>(a.sum) + at(a.sum_row, a.sum_head));
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      Vt w;
-#pragma unroll
-      for (int i = 0; i < V; ++i) w.e[i] = from_f<E>(v[j][i]);
-      if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
-    }
+    for (int j = 0; j < NV; ++j)
+      if (tid + j * lanes < a.n) o[tid + j * lanes] = pack<E>(v[j]);
   }
+  // weight + offset of the thread's j-th vector (0 past the row, where v is 0 too)
+  const auto gains = [&](int j, float (&g)[V]) {
+    if (a.weight) {
+      Vt w{};
+      if (tid + j * lanes < a.n) w = weight[tid + j * lanes];
+      unpack(w, g);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] = 1.f;
+    }
+    if (a.offset != 0.f) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] += a.offset;
+    }
+  };
   float ss = 0.f;
   uint32_t most = 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    Vt w;
-    if (CODES && a.weight && tid + j * lanes < a.n) w = weight[tid + j * lanes];
+    float g[V];
+    if (CODES) gains(j, g);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       ss = fmaf(v[j][i], v[j][i], ss);
-      if (CODES && tid + j * lanes < a.n)
-        most = max(most, magnitude(v[j][i] *
-                                   ((a.weight ? to_f(w.e[i]) : 1.f) + a.offset)));
+      if (CODES) most = max(most, magnitude(v[j][i] * g[i]));
     }
   }
   row_reduce<LANES, CODES>(ss, most, sh[0]);
@@ -169,24 +221,16 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, float (&v)[NV][V],
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int u = tid + j * lanes;
-    Vt w;
-    if (a.weight && u < a.n) w = weight[u];
+    float g[V];
+    gains(j, g);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float g = (a.weight && u < a.n ? to_f(w.e[i]) : 1.f) + a.offset;
-      v[j][i] = v[j][i] * by * g;
-    }
+    for (int i = 0; i < V; ++i) v[j][i] = v[j][i] * by * g[i];
   }
   if (a.out && live) {
     Vt* o = reinterpret_cast<Vt*>(static_cast<E*>(a.out) + at(a.out_row, a.out_head));
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      Vt w;
-#pragma unroll
-      for (int i = 0; i < V; ++i) w.e[i] = from_f<E>(v[j][i]);
-      if (tid + j * lanes < a.n) o[tid + j * lanes] = w;
-    }
+    for (int j = 0; j < NV; ++j)
+      if (tid + j * lanes < a.n) o[tid + j * lanes] = pack<E>(v[j]);
   }
   if constexpr (CODES) {
     // (the largest product may have left fp32's range where the result does not: from the
@@ -258,18 +302,22 @@ __global__ void __launch_bounds__(LANES == 0 ? 512 : 128, LANES == 0 && NV * V <
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int u = tid + j * lanes;
+      p[j] = Vt{};
+      q[j] = Vt{};
       if (live && u < a.n) {
         p[j] = x[u];
         if (a.add) q[j] = add[u];
       }
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool in = live && tid + j * lanes < a.n;
+    for (int j = 0; j < NV; ++j) unpack(p[j], v[j]);
+    if (a.add) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        v[j][i] = in ? to_f(p[j].e[i]) : 0.f;
-        if (in && a.add) v[j][i] += to_f(q[j].e[i]);
+      for (int j = 0; j < NV; ++j) {
+        float b[V];
+        unpack(q[j], b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] += b[i];
       }
     }
   }
