@@ -326,12 +326,18 @@ __device__ __forceinline__ bool select_scored_fast(const RouteArgs& a, const Sco
     const bool there = lane < a.groups;
     const float rank = !there ? -INFINITY : a.group_best == 2 ? fminf(fmaxf(g0 + g1, -3.402823466e38f), 3.402823466e38f)
                                      : g0;
-    int ahead = 0;
-    for (int g = 0; g < a.groups; ++g) ahead += __shfl_sync(kFull, rank, g) > rank ? 1 : 0;
-    const bool stays = there && ahead < a.top_groups;      // (equal ranks: perhaps too many)
+    // the top_groups largest ranks, one after the other (equal ones together)
+    const int rank_key = there ? signed_key(rank) : INT_MIN;
+    int left_key = rank_key, low_key = INT_MIN;
+    for (int got = 0; got < a.top_groups;) {
+      low_key = __reduce_max_sync(kFull, left_key);
+      got += __popc(__ballot_sync(kFull, left_key == low_key));
+      if (left_key == low_key) left_key = INT_MIN;
+    }
+    const bool stays = there && rank_key >= low_key;       // (equal ranks: perhaps too many)
     // Groups whose rank is near the last that stays are compared in fp64; the others are sure.
     // Keys of experts out of use, or forced in, are beyond any rounding of the others.
-    const float low = signed_float(__reduce_min_sync(kFull, stays ? signed_key(rank) : INT_MAX));
+    const float low = signed_float(low_key);
     float size = there ? fabsf(g0) + fabsf(g1) : 0.f;
     if (!(size < 1e30f)) size = 0.f;
     size = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(size)));
@@ -451,7 +457,7 @@ __device__ __forceinline__ bool select_scored_fast(const RouteArgs& a, const Sco
   const bool mine = held && place < k;
   if (softmax && !m.sum) top = __shfl_sync(kFull, z, 0);   // only ratios matter
   float s = 0.f;
-  if (mine) s = softmax ? expf(z - top) * inv : 1.f / (1.f + expf(-z));
+  if (mine) s = softmax ? expf(z - top) * inv : __fdividef(1.f, 1.f + expf(-z));
   if (!__all_sync(kFull, !mine || (s > 1e-30f && s < 1e30f))) return false;
   float total = 1.f;
   if (a.renorm) {
@@ -461,7 +467,7 @@ __device__ __forceinline__ bool select_scored_fast(const RouteArgs& a, const Sco
   }
   if (mine) {
     sE[place] = chosen;
-    sV[place] = s / total * a.factor;
+    sV[place] = __fdividef(s, total) * a.factor;
   }
   return true;
 }
