@@ -419,17 +419,20 @@ int32_t check_device(int* sms) {
 }
 
 bool map_rows(CUtensorMap* m, int32_t dtype, const void* base, uint64_t K, uint64_t rows,
-              uint64_t stride_bytes, uint32_t box_k, uint32_t box_rows) {
+              uint64_t stride_bytes, uint32_t box_k, uint32_t box_rows, uint32_t depth) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {K, rows}, strides[1] = {stride_bytes};
-  const cuuint32_t box[2] = {box_k, box_rows}, estr[2] = {1, 1};
+  const bool cube = depth > 1;
+  const cuuint64_t dims[3] = {cube ? box_k : K, rows, cube ? K / box_k : 1};
+  const cuuint64_t strides[2] = {stride_bytes, 128};
+  const cuuint32_t box[3] = {box_k, box_rows, depth}, estr[3] = {1, 1, 1};
   return fn(m,
             dtype == MOE_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
             : dtype == MOE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                : CU_TENSOR_MAP_DATA_TYPE_UINT8,
-            2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            cube ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

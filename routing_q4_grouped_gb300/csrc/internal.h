@@ -87,9 +87,11 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 int32_t check_device(int* sms = nullptr);
 
 // Tensor map of `rows` rows of K elements (MOE_BF16, MOE_F16 or MOE_E4M3), stride_bytes apart,
-// copied in boxes of box_k elements (128 bytes) and box_rows rows in the 128-byte swizzle.
+// copied in boxes of box_k elements (128 bytes) and box_rows rows in the 128-byte swizzle; depth
+// above 1 (K a multiple of box_k): in `depth` such boxes, neighbours in K, one behind the other,
+// at coordinates (0, row, K-chunk).
 bool map_rows(CUtensorMap* m, int32_t dtype, const void* base, uint64_t K, uint64_t rows,
-              uint64_t stride_bytes, uint32_t box_k, uint32_t box_rows);
+              uint64_t stride_bytes, uint32_t box_k, uint32_t box_rows, uint32_t depth = 1);
 
 // Allows `kernel` its dynamic shared memory, once per device (bit d of `done`).
 template <typename Kernel>

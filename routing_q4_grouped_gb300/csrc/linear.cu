@@ -65,6 +65,7 @@ struct LinearArgs {
   int band;                  // feature tiles that are gone through together for every token tile
   int stages;
   int sub;                   // K-chunks per stage
+  int cube;                  // one copy of each operand per stage: K is whole chunks
   int acc, tcols;            // tensor-memory columns per accumulator, and of all (powers of two)
   uint32_t idesc;
   const float *x_scale, *w_scale, *bias;
@@ -113,30 +114,33 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
                : "memory");
 }
 
-// One K-chunk's copies: features from row `fn` and tokens from row `ft` at element c0 of K,
-// completing on `bar`, on which `bytes` are expected first (0: they have been), issued by one
-// elected lane of a converged warp from one asm block (warp-uniform operands stay in uniform
-// registers; behind a test of the lane a chunk took 261 ns to issue, so 127). PAIR: both blocks'
-// copies complete on block 0's barrier, at cluster address `bar`, and block 0 expects them all.
-template <bool PAIR>
+// A K-chunk's copies, or (CUBE) those of a whole stage's chunks: features from row `fn` and tokens
+// from row `ft` at element c0 of K (CUBE: at chunk c0), completing on `bar`, on which `bytes` are
+// expected first (0: they have been), issued by one elected lane of a converged warp from one asm
+// block (warp-uniform operands stay in uniform registers; behind a test of the lane a chunk took
+// 261 ns to issue, so 127). PAIR: both blocks' copies complete on block 0's barrier, at cluster
+// address `bar`, and block 0 expects them all.
+template <bool PAIR, bool CUBE>
 __device__ __forceinline__ void load_chunk(uint32_t dst_w, uint32_t dst_x, const CUtensorMap* tm_w,
                                            const CUtensorMap* tm_x, uint32_t bar, uint32_t own_bar,
                                            uint32_t bytes, int32_t c0, int32_t fn, int32_t ft,
                                            uint64_t pol) {
-#define MOEQ4_LOAD(GROUP)                                                                        \
+#define MOEQ4_LOAD(GROUP, DIM, AT_W, AT_X)                                                       \
   asm volatile(                                                                                  \
       "{\n\t.reg .pred e, p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                       \
       "elect.sync _|e, 0xffffffff;\n\tand.pred p, p, e;\n\t"                                     \
       "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"                            \
-      "@e cp.async.bulk.tensor.2d" GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::"  \
-      "bytes.L2::cache_hint [%0], [%2, {%7, %8}], [%4], %10;\n\t"                                \
-      "@e cp.async.bulk.tensor.2d" GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::"  \
-      "bytes.L2::cache_hint [%1], [%3, {%7, %9}], [%4], %10;\n\t}" ::"r"(dst_w),                 \
+      "@e cp.async.bulk.tensor." DIM GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::" \
+      "bytes.L2::cache_hint [%0], [%2, " AT_W "], [%4], %10;\n\t"                                \
+      "@e cp.async.bulk.tensor." DIM GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::" \
+      "bytes.L2::cache_hint [%1], [%3, " AT_X "], [%4], %10;\n\t}" ::"r"(dst_w),                 \
       "r"(dst_x), "l"(reinterpret_cast<uint64_t>(tm_w)), "l"(reinterpret_cast<uint64_t>(tm_x)),  \
-      "r"(bar), "r"(own_bar), "r"(bytes), "r"(c0), "r"(fn), "r"(ft), "l"(pol)                    \
+      "r"(bar), "r"(own_bar), "r"(bytes), "r"(c0), "r"(fn), "r"(ft), "l"(pol), "r"(0)            \
       : "memory")
-  if constexpr (PAIR) MOEQ4_LOAD(".cta_group::2");
-  else MOEQ4_LOAD("");
+  if constexpr (PAIR && CUBE) MOEQ4_LOAD(".cta_group::2", "3d", "{%11, %8, %7}", "{%11, %9, %7}");
+  else if constexpr (PAIR) MOEQ4_LOAD(".cta_group::2", "2d", "{%7, %8}", "{%7, %9}");
+  else if constexpr (CUBE) MOEQ4_LOAD("", "3d", "{%11, %8, %7}", "{%11, %9, %7}");
+  else MOEQ4_LOAD("", "2d", "{%7, %8}", "{%7, %9}");
 #undef MOEQ4_LOAD
 }
 
@@ -335,7 +339,8 @@ __global__ void __launch_bounds__(kThreads)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const int cb = chunk_bytes(a.cols, MODE), sb = a.sub * cb, ns = a.stages;
+  const int cb = chunk_bytes(a.cols, MODE), xb = cb - kRows * kChunk;   // of a chunk, its tokens
+  const int sb = a.sub * cb, ns = a.stages;
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + static_cast<size_t>(ns) * sb);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t group = 1, rank = 0;              // blocks that share a tile
@@ -403,14 +408,22 @@ __global__ void __launch_bounds__(kThreads)
           if (!ok) break;
           const uint32_t own_bar = smem_u32(&ctl.full[st]);
           const uint32_t bar = kIsPair ? peer_addr(own_bar, 0) : own_bar;
-          const uint32_t dst = smem_u32(smem) + st * sb;
-          const uint32_t all = (SUB == 1 ? cb : min(SUB, c_hi - c) * cb) * (kIsPair ? 2 : 1);
-          const uint32_t bytes = kIsPair && rank != 0 ? 0 : all;
+          // a stage: the weights of its chunks, then the tokens of its chunks
+          const uint32_t dst = smem_u32(smem) + st * sb, dst_x = dst + SUB * kRows * kChunk;
+          if (SUB > 1 && a.cube) {           // (chunks behind the last: zeros)
+            load_chunk<kIsPair, true>(dst, dst_x, &tm_w, &tm_x, bar, own_bar,
+                                      kIsPair && rank != 0 ? 0 : SUB * cb * (kIsPair ? 2 : 1), c,
+                                      tn, tt, pol);
+          } else {
+            const uint32_t all = (SUB == 1 ? cb : min(SUB, c_hi - c) * cb) * (kIsPair ? 2 : 1);
+            const uint32_t bytes = kIsPair && rank != 0 ? 0 : all;
 #pragma unroll
-          for (int u = 0; u < SUB; ++u)
-            if (u == 0 || c + u < c_hi)
-              load_chunk<kIsPair>(dst + u * cb, dst + u * cb + kRows * kChunk, &tm_w, &tm_x, bar,
-                                  own_bar, u == 0 ? bytes : 0, (c + u) * kElems, tn, tt, pol);
+            for (int u = 0; u < SUB; ++u)
+              if (u == 0 || c + u < c_hi)
+                load_chunk<kIsPair, false>(dst + u * kRows * kChunk, dst_x + u * xb, &tm_w, &tm_x,
+                                           bar, own_bar, u == 0 ? bytes : 0, (c + u) * kElems, tn,
+                                           tt, pol);
+          }
           if (++st == ns) {
             st = 0;
             ph ^= 1;
@@ -451,9 +464,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
               for (int u = 0; u < SUB; ++u)
                 if (u == 0 || c + u < hi)
-                  mma_chunk<E4M3, kIsPair>(tmem + b * a.acc, sdesc_k_sw128(sa + u * cb),
-                                           sdesc_k_sw128(sa + u * cb + kRows * kChunk), a.idesc,
-                                           u != 0 || c != lo);
+                  mma_chunk<E4M3, kIsPair>(
+                      tmem + b * a.acc, sdesc_k_sw128(sa + u * kRows * kChunk),
+                      sdesc_k_sw128(sa + SUB * kRows * kChunk + u * xb), a.idesc,
+                      u != 0 || c != lo);
               commit<kIsPair>(&ctl.empty[st]);
               if (++st == ns) {
                 st = 0;
@@ -989,10 +1003,13 @@ extern "C" moe_status moe_linear(const moe_linear_args* l, void* stream) {
             (static_cast<uint32_t>(fw >> 4) << 24);
   // a single row has no stride: any multiple of 16 bytes will do
   const uint64_t one = (static_cast<uint64_t>(l->K) * es + 15) / 16 * 16;
+  a.cube = l->K % elems == 0 && p.sub > 1;
+  const int depth = a.cube ? p.sub : 1;
   CUtensorMap tx, tw;
   if (!map_rows(&tx, l->dtype, l->x, l->K, l->T, l->T > 1 ? l->x_row * es : one, elems,
-                p.mode == kPair ? p.cols / 2 : p.cols) ||
-      !map_rows(&tw, l->dtype, l->w, l->K, l->N, l->N > 1 ? l->w_row * es : one, elems, kRows))
+                p.mode == kPair ? p.cols / 2 : p.cols, depth) ||
+      !map_rows(&tw, l->dtype, l->w, l->K, l->N, l->N > 1 ? l->w_row * es : one, elems, kRows,
+                depth))
     return MOE_ERR_CUDA;
   cudaError_t e;
   if (e4m3)
