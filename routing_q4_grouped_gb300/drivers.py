@@ -23,8 +23,7 @@ tokens behind a shared prefix (0: none), 16 query and 2 key/value heads.
 layer uses them for a batch of B requests that decode one token each: the fused
 query/key/value projection, moe_kv_append (turn, quantise, write),
 moe_kv_attention, the output projection, then moe_layer on the sum. The two
-projections are moe_linear with random bf16 weights, the second with the residual
-in its epilogue.
+projections are plain matrix products of random bf16 weights.
 
 ``block`` is the step from one hidden row per request to the next: moe_rms_norm
 with the residual, the projection, the norm of query and key heads, append,
@@ -100,9 +99,6 @@ class _Attention:
     def __init__(self, cfg, B: int, length: int, bits: int):
         self.B, self.length, self.D = B, length, cfg.d // HQ
         D = self.D
-        heads = HQ + 2 * HKV
-        self.qkv = moeq4.Linear(_weights(heads * D, cfg.d))
-        self.out = moeq4.Linear(_weights(cfg.d, HQ * D))
         pages, self.table, _ = _tables(B, length, 0)
         self.cache = _cache(pages, bits, D)
         self.rope = moeq4.RopeSpec(moeq4.moe_rope_phases(D, 1e6).cuda(), D)
@@ -111,23 +107,17 @@ class _Attention:
         last = (self.pos // self.cache.page_size).long()
         self.slots = (self.table.gather(1, last[:, None])[:, 0] * self.cache.page_size
                       + self.pos % self.cache.page_size).int()
-        self.heads = torch.empty((B, heads, D), dtype=torch.bfloat16, device="cuda")
         self.att = torch.empty((B, HQ, D), dtype=torch.bfloat16, device="cuda")
         self.ws = moeq4.alloc_workspace(
             moeq4.moe_kv_attention_workspace_size(B, 1, HQ, HKV, D, length, 0))
 
-    def __call__(self, x, residual, h, norm=None):
-        """h = residual + the attention of x's rows."""
-        moeq4.moe_linear(x, self.qkv, self.heads.view(self.B, -1))
-        qk = self.heads[:, :HQ + HKV]
-        if norm is not None:
-            moeq4.moe_rms_norm(qk, norm, qk)
-        q = qk[:, :HQ]
-        moeq4.moe_kv_append(self.cache, qk[:, HQ:], self.heads[:, HQ + HKV:], self.slots, self.pos,
+    def __call__(self, qkv):
+        """The attention [B, HQ * D] of the projected rows qkv [B, HQ + 2 HKV, D]."""
+        q = qkv[:, :HQ]
+        moeq4.moe_kv_append(self.cache, qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:], self.slots, self.pos,
                             self.rope, q, q)
         moeq4.moe_kv_attention(q, self.cache, self.table, self.lens, self.length, self.att, self.ws)
-        moeq4.moe_linear(self.att.view(self.B, -1), self.out, h, add=residual)
-        return h
+        return self.att.view(self.B, -1)
 
 
 def _weights(n: int, k: int) -> torch.Tensor:
@@ -140,9 +130,16 @@ def _step(B: int, length: int, bits: int, calls: int) -> None:
     lay = moeq4.Layer(W, B, cfg.k, None)
     lg = torch.from_numpy(synth.gen_logits(cfg, 0, B)).cuda()
     x = torch.from_numpy(synth.gen_x(cfg, B).view(np.int16)).cuda().view(torch.bfloat16)
-    attend, h = _Attention(cfg, B, length, bits), torch.empty_like(x)
-    _timed(lambda: lay(attend(x, x, h), lg), calls, attend.cache)
-    _clean(lay.route, attend.qkv, attend.out)
+    attend = _Attention(cfg, B, length, bits)
+    w_qkv = _weights((HQ + 2 * HKV) * attend.D, cfg.d).t().contiguous()
+    w_out = _weights(cfg.d, HQ * attend.D).t().contiguous()
+
+    def step():
+        qkv = (x @ w_qkv).view(B, HQ + 2 * HKV, attend.D)
+        return lay(x + attend(qkv) @ w_out, lg)
+
+    _timed(step, calls, attend.cache)
+    _clean(lay.route)
 
 
 def _block(B: int, length: int, bits: int, calls: int) -> None:
@@ -157,19 +154,24 @@ def _block(B: int, length: int, bits: int, calls: int) -> None:
     score = moeq4.RouteScore(moeq4.MOE_SCORE_SIGMOID, 0.1 * torch.randn(cfg.E, device="cuda"),
                              groups=8, top_groups=4, group_best=2, factor=2.5)
     attend = _Attention(cfg, B, length, bits)
+    heads, D = HQ + 2 * HKV, attend.D
+    qkv, out = moeq4.Linear(_weights(heads * D, cfg.d)), moeq4.Linear(_weights(cfg.d, HQ * D))
+    rows = torch.empty((B, heads, D), dtype=torch.bfloat16, device="cuda")
     h1, n1, h2, n2, y = (torch.zeros_like(x) for _ in range(5))
     lg = torch.empty((B, cfg.E), dtype=torch.float32, device="cuda")
 
     def block():
         # y: the experts' output of the layer before (here: of the call before)
         moeq4.moe_rms_norm(x, ones, n1, add=y, sum=h1)
-        attend(n1, h1, h2, ones[:attend.D])
+        moeq4.moe_linear(n1, qkv, rows.view(B, -1))
+        moeq4.moe_rms_norm(rows[:, :HQ + HKV], ones[:D], rows[:, :HQ + HKV])
+        moeq4.moe_linear(attend(rows), out, h2, add=h1)
         moeq4.moe_rms_norm(h2, ones, n2)
         moeq4.moe_linear(n2, router, lg)
         moeq4.moe_layer_scored(n2, lg, W, score, route, y, ws)
 
     _timed(block, calls, attend.cache)
-    _clean(route, attend.qkv, attend.out, router)
+    _clean(route, qkv, out, router)
 
 
 def _clean(*owners) -> None:
