@@ -8,12 +8,13 @@
 // feature's bias and scale are one register of its lane.
 //
 // A block keeps a ring of K-chunks (128 bytes of K of both operands, 128-byte swizzle)
-// that one thread fills by TMA and one warp feeds to the tensor cores; two accumulators in
+// that one warp fills by TMA and another feeds to the tensor cores; two accumulators in
 // tensor memory let 16 warps finish a tile while the next one is multiplied. The tensor
 // cores' fp32 sums are cut off, not rounded: a sum loses about 2^-26 of itself at each step of
-// 32 bytes of K, always towards zero. Next to results of 16 bits that is nothing (2^-16 at the
+// 32 bytes of K, always towards zero. Next to results of 16 bits that is little (2^-14 at the
 // longest K); for fp32 results the sum is taken in pieces of 32 steps, which the finishing warps
-// add up in registers. Three modes:
+// add up in registers (2047 tokens, 2048 -> 256: 10.1 us instead of 8.5). Three modes, and a
+// kernel of its own for few tokens (below):
 //   kSingle  a block per tile, each block several tiles
 //   kSplit   too few tiles for the multiprocessors: a cluster of 2, 4 or 8 blocks splits K;
 //            each finishes a share of the tokens, reading the others' partial sums from their
@@ -21,6 +22,10 @@
 //   kPair    many tiles: two blocks on neighbouring multiprocessors multiply one tile of 256
 //            features (cta_group::2); each holds its 128 features and half of the tokens, so
 //            a chunk of 256 x 256 costs each of them 32 KB of copies instead of 48
+// Measured (bursts): 8192^3 in bf16 541 us (2.03 PFLOP/s), in e4m3 313 us (3.5); 4096 tokens
+// 2048 -> 8192 72.5 us (1.90), with bias and gelu 79; both bound by the products, the first
+// copies and the last tile's epilogue. 64 tokens 2048 -> 2048 7.5 us: a small tile's chunk takes
+// 0.13 to 0.17 us to issue and wait for, whatever its bytes.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
