@@ -13,7 +13,7 @@
 // cores' fp32 sums are cut off, not rounded: a sum loses about 2^-26 of itself at each step of
 // 32 bytes of K, always towards zero. Next to results of 16 bits that is little (2^-14 at the
 // longest K); for fp32 results the sum is taken in pieces of 32 steps, which the finishing warps
-// add up in registers (2047 tokens, 2048 -> 256: 10.1 us instead of 8.5). Three modes, and a
+// add up in registers (2047 tokens, 2048 -> 256: 8.9 us instead of 8.3). Three modes, and a
 // kernel of its own for few tokens (below):
 //   kSingle  a block per tile, each block several tiles
 //   kSplit   too few tiles for the multiprocessors: a cluster of 2, 4 or 8 blocks splits K;

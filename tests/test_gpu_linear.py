@@ -279,3 +279,31 @@ def test_fp32_results_of_long_sums(T, N, K, dt):
     moeq4.moe_linear(x, lin, out, x_scale=one[:T].clone() if dt is E4M3 else None)
     want = _exact(x, w)
     assert ((out.double() - want).abs() <= want * (2.0 ** -18 + 2.0 ** -21)).all()
+
+
+@pytest.mark.parametrize("T,step", [(3, 1 << 31), (40, (1 << 27) + 64), (300, (1 << 24) + 8)])
+def test_far_rows(T, step):
+    # element offsets past 2^31 in x, the residual and the result
+    N, K = 200, 128
+    big = torch.empty(step * (T - 1) + 1024, dtype=BF16, device="cuda")
+    x, out = big.as_strided((T, K), (step, 1)), big.as_strided((T, N), (step, 1), 512)
+    add = big.as_strided((T, N), (step, 1), 768)
+    x0, w, g = _case(T, N, K, BF16)
+    x.copy_(x0)
+    add.copy_(_whole((T, N), 8, g, BF16))
+    want = (_exact(x0, w) + add.double()).to(BF16)
+    moeq4.moe_linear(x, moeq4.Linear(w), out, add=add)
+    assert torch.equal(out, want) and torch.equal(x, x0)
+
+
+def test_far_weights():
+    # weight rows 2^31 elements and more away from the first
+    N, K, step = 130, 256, (1 << 24) + 8
+    big = torch.empty(step * (N - 1) + K, dtype=BF16, device="cuda")
+    w = big.as_strided((N, K), (step, 1))
+    for T in (2, 60):
+        x, w0, _ = _case(T, N, K, BF16)
+        w.copy_(w0)
+        out = torch.empty((T, N), device="cuda")
+        moeq4.moe_linear(x, moeq4.Linear(w), out)
+        assert torch.equal(out, _exact(x, w0).float())

@@ -245,3 +245,18 @@ def test_many_long_rows_without_summand():
     ok = [i for i in range(0, 6000, 37) if i != 4000]
     _near(out[ok], _ref(x[ok], None, None, 1e-6, 0.0)[1], ARITH)
     assert out[4000].isnan().all() and (out[5] == 0).all()
+
+
+@pytest.mark.parametrize("D", [128, 130, 2048])
+def test_codes_inside_wider_rows(D):
+    # codes and results of heads inside rows of more heads; what lies between stays
+    x, add, weight = _inputs(50, 3, D, torch.bfloat16, True, True, gap=1)
+    rows = torch.full((50, 5, D), 2.0, device="cuda").to(torch.float8_e4m3fn)
+    out = torch.full((50, 5, D), 2.0, dtype=torch.bfloat16, device="cuda")
+    scales = torch.empty((50, 3), device="cuda")
+    moeq4.moe_rms_norm(x, weight, out[:, 1:4], add, codes=rows[:, 1:4], scales=scales)
+    y = _ref(x, add, weight, 1e-6, 0.0)[1]
+    _near(out[:, 1:4], y, ARITH)
+    _check_codes(rows[:, 1:4], scales, y)
+    for t in (rows.float(), out.float()):
+        assert (t[:, 0] == 2.0).all() and (t[:, 4] == 2.0).all()
