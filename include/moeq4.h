@@ -384,10 +384,11 @@ typedef struct moe_linear_args {
 } moe_linear_args;
 
 /* One launch. x and w: 16-byte aligned, rows that do not overlap, strides and K multiples of
- * 16 bytes; out and add: aligned to their type, any stride. K <= 65536; T, N <= 2^30. add may be out with
- * the same stride; out overlaps nothing else. T = 0 launches nothing. A token's result does
- * not depend on the other tokens' values (an infinity or NaN stays in its row), but a
- * batch of another size may add a row's products in another order. */
+ * 16 bytes; out and add: aligned to their type, any stride (out's rows may not overlap).
+ * K <= 65536; T, N <= 2^30. add may be out with the same stride; out overlaps nothing else.
+ * T = 0 launches nothing. A token's result does not depend on the other tokens' values (an
+ * infinity or NaN stays in its row), but a batch of another size may add a row's products in
+ * another order. */
 moe_status moe_linear(const moe_linear_args* a, void* stream);
 
 /* Rotary positions. The first `rot` elements of a head form rot/2 pairs
