@@ -664,6 +664,9 @@ __global__ void __launch_bounds__(kThreads)
 // consecutive bytes of a row and uses them as the k-slots of two products; the tokens' lanes
 // load the same places of x. No shared memory, barrier or copy engine stands between the loads
 // and the products; the warps' sums meet in shared memory once, in the order of the warps.
+// Plain loads: x, or fresh weights, may come from the kernel that still ended when this one
+// started, and a load for data that no one writes (ld.global.nc) has no place there. They are
+// also faster: one token, 8192 -> 2048 in bf16 7.4 us instead of 10.1, 8192 -> 8192 23.7, 27.0.
 
 constexpr int kFewWarps = 16;              // at most
 constexpr int kFewRows = 16;
@@ -724,11 +727,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) linear_few_kernel(const Few
       const int k = k0 + (u >> 1) * (warps * 128) + (u & 1) * 64;
       const bool in = k < last;
       const uint4 zero = make_uint4(0, 0, 0, 0);
-      p[u] = in ? __ldg(reinterpret_cast<const uint4*>(wa + k)) : zero;
-      q[u] = in ? __ldg(reinterpret_cast<const uint4*>(wb + k)) : zero;
+      p[u] = in ? *reinterpret_cast<const uint4*>(wa + k) : zero;
+      q[u] = in ? *reinterpret_cast<const uint4*>(wb + k) : zero;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        x[u][i] = in ? __ldg(reinterpret_cast<const uint4*>(xp[i] + k)) : zero;
+        x[u][i] = in ? *reinterpret_cast<const uint4*>(xp[i] + k) : zero;
     }
     float d[NT][4];
 #pragma unroll
@@ -912,9 +915,9 @@ cudaError_t launch_out(const CUtensorMap& tx, const CUtensorMap& tw, const Linea
                             : launch<E4M3, O, kSingle>(tx, tw, a, p, sms, s);
 }
 
-// Measured, few-token kernel and the better of the others, us: 1 token 2048 -> 2560 4.3 and 7.3,
-// 8192 -> 8192 24.7 and 25.9, 2048 -> 16384 15.5 and 13.9; 16 tokens 2048 -> 2560 5.6 and 7.9,
-// 8192 -> 2048 12.4 and 12.6, 8192 -> 8192 29.7 and 26.9.
+// Measured, few-token kernel and the better of the others, us: 1 token 2048 -> 2560 3.5 and 5.9,
+// 8192 -> 8192 23.8 and 24.0, 2048 -> 16384 15.8 and 13.6; 16 tokens 2048 -> 4096 5.1 and 6.7,
+// 2048 -> 8192 9.9 and 8.6, 8192 -> 2048 10.7 and 10.0, 8192 -> 8192 28.4 and 24.7.
 bool take_few(int T, int N) { return (T <= 8 && N <= 8192) || (T <= 16 && N <= 4096); }
 
 bool bad_align(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }

@@ -40,14 +40,14 @@ __device__ __noinline__ double score64(float x, bool softmax, float top, double 
   return (x < 0.f ? z : 1.0) / (1.0 + z);
 }
 __device__ __forceinline__ double bias64(const RouteArgs& a, int e) {
-  return a.bias ? static_cast<double>(finite_bias(__ldg(a.bias + e))) : 0.0;
+  return a.bias ? static_cast<double>(finite_bias(a.bias[e])) : 0.0;
 }
 // sum of exp(l - top) over token t's experts.
 __device__ __noinline__ double softmax_sum64(const RouteArgs& a, int t, int lane, float top) {
   const float* row = a.logits + static_cast<size_t>(t) * a.E;
   double sum = 0.0;
   for (int e = lane; e < a.E; e += 32)
-    sum += exp(static_cast<double>(__ldg(row + e)) - static_cast<double>(top));
+    sum += exp(static_cast<double>(row[e]) - static_cast<double>(top));
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
   return sum;
 }
@@ -59,7 +59,7 @@ __device__ __noinline__ double group_rank64(const RouteArgs& a, int t, int lane,
   double b0 = -INFINITY, b1 = -INFINITY;
   for (int i = lane; i < n; i += 32) {
     const int e = g * n + i;
-    const double key = score64(__ldg(row + e), a.score == MOE_SCORE_SOFTMAX, top, sum) + bias64(a, e);
+    const double key = score64(row[e], a.score == MOE_SCORE_SOFTMAX, top, sum) + bias64(a, e);
     b1 = fmax(b1, fmin(b0, key));
     b0 = fmax(b0, key);
   }
@@ -82,7 +82,7 @@ __device__ __noinline__ void select_scored_exact(const RouteArgs& a, int t, int 
   for (int s = 0; s < S; ++s) {
     const int e = lane + 32 * s;
     bool bad = false;                              // (reported by the caller)
-    x[s] = e < E ? finite_logit(__ldg(row + e), bad) : 0.f;
+    x[s] = e < E ? finite_logit(row[e], bad) : 0.f;
   }
   double score[S], key[S];
   double sum = 0.0;
@@ -428,14 +428,14 @@ __device__ __forceinline__ bool select_scored_fast(const RouteArgs& a, const Sco
       drawn == k && __all_sync(kFull, lane == 0 || lane >= k || clear_of(above, word));
   const int chosen = kLow - (word & kLow);
   const bool held = lane < drawn;
-  const float z = held ? __ldg(a.logits + static_cast<size_t>(t) * E + chosen) : 0.f;
+  const float z = held ? a.logits[static_cast<size_t>(t) * E + chosen] : 0.f;
   int place = lane;
   if (!sorted) {
     // by their fp32 keys (logits: exact), where these are clear of each other
     float mine = z;
     if (m.by_score) {
       mine = softmax ? __expf(z - top) * inv : __fdividef(1.f, 1.f + __expf(-z));
-      if (a.bias && held) mine += finite_bias(__ldg(a.bias + chosen));
+      if (a.bias && held) mine += finite_bias(a.bias[chosen]);
     }
     place = 0;
     bool near = false;
@@ -481,7 +481,7 @@ __device__ __forceinline__ void select_scored(const RouteArgs& a, int t0, int fi
 #pragma unroll
   for (int s = 0; s < S; ++s) {
     const int e = lane * S + s;
-    bias[s] = a.bias && e < a.E ? finite_bias(__ldg(a.bias + e)) : 0.f;
+    bias[s] = a.bias && e < a.E ? finite_bias(a.bias[e]) : 0.f;
   }
   const auto load = [&](int i, float (&x)[S]) {
     if (i >= nt) return;
@@ -490,7 +490,7 @@ __device__ __forceinline__ void select_scored(const RouteArgs& a, int t0, int fi
       if (m.vec) {
 #pragma unroll
         for (int s = 0; s < S; s += 4) {
-          const float4 q = lane * S < a.E ? __ldg(reinterpret_cast<const float4*>(row + s))
+          const float4 q = lane * S < a.E ? *reinterpret_cast<const float4*>(row + s)
                                           : make_float4(0.f, 0.f, 0.f, 0.f);
           x[s] = q.x;
           x[s + 1] = q.y;
@@ -501,7 +501,7 @@ __device__ __forceinline__ void select_scored(const RouteArgs& a, int t0, int fi
       }
     }
 #pragma unroll
-    for (int s = 0; s < S; ++s) x[s] = lane * S + s < a.E ? __ldg(row + s) : 0.f;
+    for (int s = 0; s < S; ++s) x[s] = lane * S + s < a.E ? row[s] : 0.f;
   };
   load(first, next);
   for (int i = first; i < nt; i += stride) {
