@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kThreads)
 // and the products; the warps' sums meet in shared memory once, in the order of the warps.
 // Plain loads: x, or fresh weights, may come from the kernel that still ended when this one
 // started, and a load for data that no one writes (ld.global.nc) has no place there. They are
-// also faster: one token, 8192 -> 2048 in bf16 7.4 us instead of 10.1, 8192 -> 8192 23.7, 27.0.
+// also faster: one token, 8192 -> 2048 in bf16 7.9 us instead of 10.1, 8192 -> 8192 23.7, 27.0.
 
 constexpr int kFewWarps = 16;              // at most
 constexpr int kFewRows = 16;
@@ -688,7 +688,7 @@ struct FewArgs {
   const uint8_t *x, *w;
   int64_t x_row, w_row;      // bytes
   int k_bytes;               // of a row, a multiple of 16
-  int early;                 // blocks that prefetch
+  int early;                 // blocks that prefetch: one per multiprocessor
   LinearArgs l;
 };
 
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) linear_few_kernel(const Few
   const int n0 = blockIdx.x * kFewRows, warps = blockDim.x >> 5;
   // The first blocks ask for the start of their weights while the previous kernel ends: reads of
   // them wait for it, a prefetch into L2 does not (what that kernel writes reaches L2 all the
-  // same). One token, 2048 -> 2560: 4.96 -> 4.66 us; whole rows, or all blocks: slower.
+  // same). One token, 8192 -> 8192 in e4m3: 15.4 -> 15.0 us; whole rows, or all blocks: slower.
   if (blockIdx.x < a.early && tid < kFewRows && n0 + tid < a.l.N)
     bulk_prefetch_l2(a.w + static_cast<int64_t>(n0 + tid) * a.w_row, min(a.k_bytes, 4096));
   griddep_wait();
@@ -770,10 +770,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) linear_few_kernel(const Few
 
 template <bool E4M3, bool HALF, typename O>
 cudaError_t launch_few(const FewArgs& a, cudaStream_t s) {
-  // A warp for 256 bytes of K, up to 16: measured for one token, 16 and 8 warps, 2048 -> 2560
-  // 4.3 and 5.1 us, 8192 -> 2048 9.7 and 16.2; 2048 -> 8192 in e4m3 (8 warps cover it) 7.5, 5.4.
+  // A warp for 256 elements of K, up to 16, or up to 8 where every multiprocessor has two blocks
+  // anyway. Measured for one token, 16 and 8 warps: 2048 -> 2560 in bf16 3.4 and 3.3 us, 8192 ->
+  // 2048 7.9 and 12.9, 2048 -> 8192 7.1 and 6.3; 8192 -> 8192 in e4m3 15.0 and 13.6. 2048 -> 2560
+  // in e4m3 with 8 and 4 warps 2.8 and 3.4.
   const int blocks = (a.l.N - 1) / kFewRows + 1;
-  const dim3 grid(blocks), block(32 * std::min(kFewWarps, std::max(1, (a.k_bytes + 255) / 256)));
+  const int most = blocks >= 2 * a.early ? kFewWarps / 2 : kFewWarps;
+  const int per = E4M3 ? 256 : 512;          // bytes
+  const dim3 grid(blocks), block(32 * std::min(most, (a.k_bytes + per - 1) / per));
   const auto kernel = a.l.T <= 8 ? linear_few_kernel<E4M3, HALF, O, 1>
                                  : linear_few_kernel<E4M3, HALF, O, 2>;
   return launch_pdl(kernel, grid, block, 0, s, a);
@@ -915,9 +919,9 @@ cudaError_t launch_out(const CUtensorMap& tx, const CUtensorMap& tw, const Linea
                             : launch<E4M3, O, kSingle>(tx, tw, a, p, sms, s);
 }
 
-// Measured, few-token kernel and the better of the others, us: 1 token 2048 -> 2560 3.5 and 5.9,
-// 8192 -> 8192 23.8 and 24.0, 2048 -> 16384 15.8 and 13.6; 16 tokens 2048 -> 4096 5.1 and 6.7,
-// 2048 -> 8192 9.9 and 8.6, 8192 -> 2048 10.7 and 10.0, 8192 -> 8192 28.4 and 24.7.
+// Measured, few-token kernel and the better of the others, us: 1 token 2048 -> 2560 3.3 and 5.9,
+// 8192 -> 8192 23.2 and 24.0, 2048 -> 16384 15.8 and 13.6; 16 tokens 2048 -> 4096 4.7 and 6.7,
+// 2048 -> 8192 9.9 and 8.6, 8192 -> 2048 10.9 and 10.0, 8192 -> 8192 28.4 and 24.7.
 bool take_few(int T, int N) { return (T <= 8 && N <= 8192) || (T <= 16 && N <= 4096); }
 
 bool bad_align(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
