@@ -277,7 +277,7 @@ __device__ __forceinline__ bool select_scored_fast(const RouteArgs& a, const Sco
   }
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    if (!m.by_score) key[s] = x[s];
+    if (!m.by_score) key[s] = x[s] + 0.f;          // (-0 is +0: words compare bits)
     else key[s] += bias[s];
   }
   // the errors of two fp32 keys add up to `fixed` and `per` of their magnitudes
