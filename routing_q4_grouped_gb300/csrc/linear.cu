@@ -261,7 +261,16 @@ __device__ __forceinline__ float gelu_tail(float y) {
   }
 }
 
-// WIDE: fp32 results.
+// y / (1 + exp(-w)) for a w of y's sign. The exponential is that of -|w|, so the denominator stays
+// between 1 and 2 and a negative tail keeps its value until fp32 ends.
+template <bool WIDE>
+__device__ __forceinline__ float times_sigmoid(float y, float w) {
+  const float e = WIDE ? expf(-fabsf(w)) : __expf(-fabsf(w));
+  const float n = w < 0.f ? y * e : y;
+  return WIDE ? __fdiv_rn(n, 1.f + e) : __fdividef(n, 1.f + e);
+}
+
+// WIDE: fp32 results, which take expf and rounded quotients.
 template <bool WIDE, int M>
 __device__ __forceinline__ void activate(float (&v)[M], int act) {
   switch (act) {
@@ -270,9 +279,8 @@ __device__ __forceinline__ void activate(float (&v)[M], int act) {
       for (int j = 0; j < M; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];   // (NaN stays)
       break;
     case MOE_ACT_SILU:
-      // (a denominator above 2^126 gives 0, which the quotient has rounded to long before)
 #pragma unroll
-      for (int j = 0; j < M; ++j) v[j] = __fdividef(v[j], 1.f + __expf(-v[j]));
+      for (int j = 0; j < M; ++j) v[j] = times_sigmoid<WIDE>(v[j], v[j]);
       break;
     case MOE_ACT_GELU:
 #pragma unroll
@@ -284,10 +292,9 @@ __device__ __forceinline__ void activate(float (&v)[M], int act) {
     case MOE_ACT_GELU_TANH:
       // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
 #pragma unroll
-      for (int j = 0; j < M; ++j) {
-        const float u = 0.79788456080286536f * fmaf(0.044715f * v[j] * v[j], v[j], v[j]);
-        v[j] = __fdividef(v[j], 1.f + __expf(-2.f * u));
-      }
+      for (int j = 0; j < M; ++j)
+        v[j] = times_sigmoid<WIDE>(
+            v[j], 1.5957691216057307f * fmaf(0.044715f * v[j] * v[j], v[j], v[j]));
       break;
     default: break;
   }

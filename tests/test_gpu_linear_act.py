@@ -82,7 +82,7 @@ def _run(y, T, dt, out_dt, act):
     return out
 
 
-@pytest.mark.parametrize("act", [GELU])
+@pytest.mark.parametrize("act", [SILU, GELU, TANH])
 @pytest.mark.parametrize("dt,out_dt", [(BF16, BF16), (BF16, F32), (F16, F16), (F16, F32), (E4M3, BF16),
                                        (E4M3, F16), (E4M3, F32)])
 @pytest.mark.parametrize("T", [1, 12, 40, 300, 3000])
@@ -98,7 +98,7 @@ def test_relative_to_the_value(T, dt, out_dt, act):
     assert not bad.any(), (y[bad][:5], out[0][bad][:5], want[bad][:5], int(bad.sum()))
 
 
-@pytest.mark.parametrize("act", [GELU])
+@pytest.mark.parametrize("act", [SILU, GELU, TANH])
 @pytest.mark.parametrize("out_dt", [BF16, F32])
 def test_ends(act, out_dt):
     # +inf stays, -inf is 0 times infinity, NaN stays, zeros keep their sign
