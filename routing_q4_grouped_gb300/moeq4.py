@@ -69,6 +69,9 @@ class RouteScoreC(ctypes.Structure):
                 ("group_best", _c_i32), ("renorm", _c_i32), ("factor", _c_f32)]
 
 
+_SCORE = struct.Struct("@P5if")        # RouteScoreC
+
+
 class NormC(ctypes.Structure):
     _fields_ = [("x", _c_ptr), ("x_row", _c_i64), ("x_head", _c_i64),
                 ("add", _c_ptr), ("add_row", _c_i64), ("add_head", _c_i64),
@@ -362,7 +365,20 @@ def moe_route(logits: torch.Tensor, out: RouteBuffers, ws: torch.Tensor, stream=
                                         _stream(stream)))
 
 
-class RouteScore:
+class _Handle:
+    """What a call takes besides its tensors, checked together when it is made: a later
+    replacement of one part would go unseen, or unchecked, and is refused. The values that its
+    tensors hold may change."""
+    _made = False
+
+    def __setattr__(self, name, value):
+        if self._made:
+            kind = type(self).__name__
+            raise AttributeError(f"{kind}: {name} cannot be replaced, make another {kind}")
+        object.__setattr__(self, name, value)
+
+
+class RouteScore(_Handle):
     """How :func:`moe_route_scored` chooses (moe_route_score): softmax or sigmoid scores, an
     fp32 ``bias`` [E] that takes part in the choice only, ``groups`` of experts of which the
     ``top_groups`` with the largest sum of ``group_best`` keys stay, weights ``factor`` * score,
@@ -373,17 +389,24 @@ class RouteScore:
         _need("RouteScore", bias, torch.float32, "bias", optional=True)
         self.score, self.bias, self.groups, self.top_groups = score, bias, groups, top_groups
         self.group_best, self.renorm, self.factor = group_best, renorm, factor
-        self._c = RouteScoreC(_ptr(bias), score, groups, top_groups, group_best, int(renorm), factor)
-        self._addr = ctypes.addressof(self._c)
+        self._rest = (score, groups, top_groups, group_best, int(renorm), factor)
+        self.packed()                      # (refuses what is not a number)
+        self._made = True
+
+    def packed(self) -> bytes:
+        """moe_route_score as it is now: the bias where its tensor holds it at this call."""
+        return _SCORE.pack(0 if self.bias is None else self.bias.data_ptr(), *self._rest)
 
 
 def _scored(fn, logits, score, out) -> int:
     """Checks what both calls take; the logits' pointer."""
     dev = None if logits is None or not logits.is_cuda else _device()
     p = _vector(fn, logits, "logits", (out.T, out.E), torch.float32, dev)
-    if score.bias is not None and score.bias.numel() != out.E:
-        raise ValueError(f"{fn}: the bias must hold {out.E} values, got {score.bias.numel()}")
-    if out.ids.get_device() != dev or score.bias is not None and score.bias.get_device() != dev:
+    b = score.bias
+    if b is not None and (b.numel() != out.E or not b.is_contiguous()):
+        raise ValueError(f"{fn}: the bias must hold {out.E} values, got {b.numel()}, "
+                         f"contiguous={b.is_contiguous()}")
+    if out.ids.get_device() != dev or b is not None and b.get_device() != dev:
         raise ValueError(f"{fn}: result or bias is not on the current device cuda:{dev}")
     return p
 
@@ -392,7 +415,7 @@ def moe_route_scored(logits: torch.Tensor, score: RouteScore, out: RouteBuffers,
                      stream=None) -> None:
     """Routing of fp32 logits [T, E] into ``out`` with the choice and weights of ``score``."""
     p = _scored("moe_route_scored", logits, score, out)
-    st = lib().moe_route_scored(p, score._addr, out.packed(), ws.data_ptr(), ws.numel(),
+    st = lib().moe_route_scored(p, score.packed(), out.packed(), ws.data_ptr(), ws.numel(),
                                 _stream(stream))
     if st:
         _check("moe_route_scored", st)
@@ -460,7 +483,7 @@ def moe_layer_scored(x: torch.Tensor, logits: torch.Tensor, W: DeviceWeights, sc
         raise ValueError(f"{fn}: x and y must be [{r.T}][{W.d}], got {tuple(x.shape)} and "
                          f"{tuple(y.shape)}")
     wc, rc = W.cstruct(), r.cstruct()
-    _check(fn, lib().moe_layer_scored(_ptr(x), p, r.T, ctypes.byref(wc), score._addr,
+    _check(fn, lib().moe_layer_scored(_ptr(x), p, r.T, ctypes.byref(wc), score.packed(),
                                       ctypes.byref(rc), _ptr(y), _ptr(ws), ws.numel(),
                                       _stream(stream)))
 
