@@ -707,7 +707,17 @@ def _matrix(fn, t, name, rows, columns, dtype, dev):
                      f"elements on the current device, got {got}")
 
 
-class Linear:
+def _held(fn, t, name, n) -> int:
+    """Pointer of a handle's n values (0: none), whose memory may have been exchanged."""
+    if t is None:
+        return 0
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must hold {n} values, got {t.numel()}, "
+                         f"contiguous={t.is_contiguous()}")
+    return t.data_ptr()
+
+
+class Linear(_Handle):
     """Weights of a dense projection: ``weight`` [N, K] in bf16, fp16 or e4m3 (strided rows),
     fp32 ``bias`` [N], fp32 ``scale`` [N] of e4m3 weights; ``err`` is the device error word of
     the calls with it."""
@@ -722,8 +732,7 @@ class Linear:
         self.N, self.K = weight.shape
         if not weight.is_cuda:
             raise ValueError(f"{fn}: weight must be a CUDA tensor, got one on {weight.device}")
-        _, self._row = _matrix(fn, weight, "weight", self.N, self.K, weight.dtype,
-                               weight.get_device())
+        _matrix(fn, weight, "weight", self.N, self.K, weight.dtype, weight.get_device())
         for name, t in (("bias", bias), ("scale", scale)):
             _need(fn, t, torch.float32, name, optional=True)
             if t is not None and t.numel() != self.N:
@@ -731,11 +740,13 @@ class Linear:
         if (scale is not None) != (dtype == MOE_E4M3):
             raise ValueError(f"{fn}: scale goes with e4m3 weights, got {weight.dtype}")
         self.weight, self.bias, self.scale, self.dtype = weight, bias, scale, dtype
+        self._type = weight.dtype
         self.err = torch.zeros(4, dtype=torch.int32, device=weight.device) if err is None else err
         _need(fn, self.err, torch.int32, "err")
         for name, t in (("bias", bias), ("scale", scale), ("err", self.err)):
             if t is not None and t.device != weight.device:
                 raise ValueError(f"{fn}: {name} is on {t.device}, weight on {weight.device}")
+        self._made = True
 
 
 def moe_linear(x: torch.Tensor, linear: Linear, out: torch.Tensor, act=MOE_ACT_NONE,
@@ -744,11 +755,10 @@ def moe_linear(x: torch.Tensor, linear: Linear, out: torch.Tensor, act=MOE_ACT_N
     [T]. out and add are of x's type or fp32 (bf16, fp16 or fp32 where x is e4m3); add may be
     out."""
     fn = "moe_linear"
-    w, N, dev = linear.weight, linear.N, _device()
-    if w.get_device() != dev:
-        raise ValueError(f"{fn}: the weights are on {w.device}, the current device is cuda:{dev}")
+    N, K, type_, dev = linear.N, linear.K, linear._type, _device()
+    wp, wr = _matrix(fn, linear.weight, "weight", N, K, type_, dev)
     T = 0 if x is None or x.dim() != 2 else x.shape[0]
-    xp, xr = _matrix(fn, x, "x", T, linear.K, w.dtype, dev)
+    xp, xr = _matrix(fn, x, "x", T, K, type_, dev)
     td = None if out is None else out.dtype
     out_dtype = _NORM_DTYPES.get(td)
     if out_dtype is None:
@@ -760,10 +770,9 @@ def moe_linear(x: torch.Tensor, linear: Linear, out: torch.Tensor, act=MOE_ACT_N
         sp = _vector(fn, x_scale, "x_scale", (T,), torch.float32, dev)
     elif x_scale is not None:
         raise ValueError(f"{fn}: x_scale goes with e4m3 inputs, got {x.dtype}")
-    a = _LINEAR.pack(xp, xr, w.data_ptr(), linear._row, sp,
-                     0 if linear.scale is None else linear.scale.data_ptr(),
-                     0 if linear.bias is None else linear.bias.data_ptr(), ap, arow, op, orow,
-                     linear.err.data_ptr(), T, N, linear.K, linear.dtype, out_dtype, act)
+    a = _LINEAR.pack(xp, xr, wp, wr, sp, _held(fn, linear.scale, "scale", N),
+                     _held(fn, linear.bias, "bias", N), ap, arow, op, orow, linear.err.data_ptr(),
+                     T, N, K, linear.dtype, out_dtype, act)
     st = lib().moe_linear(a, _stream(stream))
     if st:
         _check(fn, st)

@@ -70,3 +70,36 @@ def test_values_in_place_are_seen(L):
     score = L.RouteScore(L.MOE_SCORE_SIGMOID, bias)
     bias[7] = 10.0
     assert (_route(L, z, score)[:, 0] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["weight", "bias", "scale", "err", "N", "K", "dtype"])
+def test_a_projection_stays_as_it_was_made(L, name):
+    lin = L.Linear(torch.zeros((64, 128), dtype=torch.bfloat16, device="cuda"),
+                   torch.zeros(64, device="cuda"))
+    old = getattr(lin, name)
+    with pytest.raises(AttributeError, match=f"Linear: {name} cannot be replaced"):
+        setattr(lin, name, None)
+    assert getattr(lin, name) is old
+
+
+@pytest.mark.gpu
+def test_weights_moved_under_their_tensor(L):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").float()   # noqa: E731
+    w, bias, x = rnd(40, 64).bfloat16(), rnd(40), rnd(5, 64).bfloat16()
+    lin, out = L.Linear(w, bias), torch.empty((5, 40), device="cuda")
+    # other memory, another row stride, another bias
+    w.data = torch.cat((rnd(40, 64), rnd(40, 64)), 1).bfloat16()[:, 64:]
+    bias.data = rnd(40)
+    L.moe_linear(x, lin, out)
+    assert torch.equal(out, x.float() @ w.float().t() + bias)
+    for bad in (rnd(39, 64), rnd(40, 72), rnd(64, 40).t()):
+        w.data = bad.bfloat16() if bad.is_contiguous() else bad.bfloat16().t().contiguous().t()
+        with pytest.raises(ValueError, match="moe_linear: weight must be"):
+            L.moe_linear(x, lin, out)
+    w.data = rnd(40, 64).bfloat16()
+    bias.data = rnd(39)
+    with pytest.raises(ValueError, match="moe_linear: bias must hold 40"):
+        L.moe_linear(x, lin, out)
+    assert L.moe_get_device_error(lin) == 0
