@@ -69,8 +69,6 @@ class RouteScoreC(ctypes.Structure):
                 ("group_best", _c_i32), ("renorm", _c_i32), ("factor", _c_f32)]
 
 
-_SCORE = struct.Struct("@P5if")        # RouteScoreC
-
 
 class NormC(ctypes.Structure):
     _fields_ = [("x", _c_ptr), ("x_row", _c_i64), ("x_head", _c_i64),
@@ -337,6 +335,29 @@ class RouteBuffers:
                    tiles=torch.empty((nmax, 3), **i32), n_tiles=torch.zeros(4, **i32),
                    err=torch.zeros(4, **i32))
 
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__["_on"] = None        # the device that :meth:`check` has seen the arrays on
+
+    def check(self, fn, dev) -> None:
+        """Refuses arrays that do not hold a result of these sizes on device ``dev``; once, until
+        a field is replaced."""
+        if self._on == dev:
+            return
+        n, t = self.T * self.k, torch.int32
+        for name, least, dtype in (
+                ("ids", n, t), ("w", n, torch.float32), ("counts", self.E, t),
+                ("offsets", self.E + 1, t), ("perm", n, t), ("inv", n, t),
+                ("tiles", 3 * moe_route_max_tiles(self.T, self.E, self.k, self.block_m), t),
+                ("n_tiles", 1, t), ("err", 1, t)):
+            a = getattr(self, name)
+            if a is None or a.dtype is not dtype or a.get_device() != dev or a.numel() < least or \
+                    not a.is_contiguous():
+                got = "None" if a is None else f"{a.dtype} {tuple(a.shape)} on {a.device}"
+                raise ValueError(f"{fn}: {name} of the result must be a contiguous {dtype} CUDA tensor "
+                                 f"of at least {least} values on the current device, got {got}")
+        self.__dict__["_on"] = dev
+
     def packed(self) -> bytes:
         """cstruct as packed bytes: a fraction of the time that filling it takes."""
         return _ROUTE.pack(self.ids.data_ptr(), self.w.data_ptr(), self.counts.data_ptr(),
@@ -350,6 +371,18 @@ class RouteBuffers:
                          _ptr(self.err), self.T, self.E, self.k, self.block_m)
 
 
+_U8, _F32 = torch.uint8, torch.float32
+
+
+def _workspace(fn, ws, dev) -> int:
+    """Pointer of a workspace on device ``dev``; the library checks its size."""
+    if ws is not None and ws.dtype is _U8 and ws.get_device() == dev and ws.is_contiguous():
+        return ws.data_ptr()
+    got = "None" if ws is None else f"{ws.dtype} on {ws.device}, contiguous={ws.is_contiguous()}"
+    raise ValueError(f"{fn}: the workspace must be a contiguous uint8 CUDA tensor on the current "
+                     f"device, got {got}")
+
+
 def alloc_workspace(nbytes: int, device="cuda") -> torch.Tensor:
     """Zero-filled scratch (the FFN part's grid-barrier counter must start at zero)."""
     return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -357,11 +390,22 @@ def alloc_workspace(nbytes: int, device="cuda") -> torch.Tensor:
 
 # ---------------------------------------------------------------------- compute
 
+def _routed(fn, logits, out, ws) -> int:
+    """Checks what moe_route and moe_layer take; the workspace's pointer."""
+    _need(fn, logits, torch.float32, "logits")
+    dev = _device()
+    if logits.numel() < out.T * out.E or logits.get_device() != dev:
+        raise ValueError(f"{fn}: logits must hold {out.T} x {out.E} values on the current device, got "
+                         f"{tuple(logits.shape)} on {logits.device}")
+    out.check(fn, dev)
+    return _workspace(fn, ws, dev)
+
+
 def moe_route(logits: torch.Tensor, out: RouteBuffers, ws: torch.Tensor, stream=None) -> None:
     """Routing of fp32 logits [T, E] into ``out`` (asynchronous)."""
-    _need("moe_route", logits, torch.float32, "logits")
+    wp = _routed("moe_route", logits, out, ws)
     c = out.cstruct()
-    _check("moe_route", lib().moe_route(_ptr(logits), ctypes.byref(c), _ptr(ws), ws.numel(),
+    _check("moe_route", lib().moe_route(_ptr(logits), ctypes.byref(c), wp, ws.numel(),
                                         _stream(stream)))
 
 
@@ -389,34 +433,34 @@ class RouteScore(_Handle):
         _need("RouteScore", bias, torch.float32, "bias", optional=True)
         self.score, self.bias, self.groups, self.top_groups = score, bias, groups, top_groups
         self.group_best, self.renorm, self.factor = group_best, renorm, factor
-        self._rest = (score, groups, top_groups, group_best, int(renorm), factor)
-        self.packed()                      # (refuses what is not a number)
+        self._c = RouteScoreC(_ptr(bias), score, groups, top_groups, group_best, int(renorm), factor)
+        self._addr = ctypes.addressof(self._c)
         self._made = True
 
-    def packed(self) -> bytes:
-        """moe_route_score as it is now: the bias where its tensor holds it at this call."""
-        return _SCORE.pack(0 if self.bias is None else self.bias.data_ptr(), *self._rest)
 
-
-def _scored(fn, logits, score, out) -> int:
-    """Checks what both calls take; the logits' pointer."""
-    dev = None if logits is None or not logits.is_cuda else _device()
-    p = _vector(fn, logits, "logits", (out.T, out.E), torch.float32, dev)
+def _scored(fn, logits, score, out, ws):
+    """Checks what both calls take, and sets the bias's pointer (its memory may have been
+    exchanged); the pointers of logits and workspace."""
+    dev = -1 if logits is None else logits.get_device()
+    if dev < 0 or dev != _device():
+        dev = None                         # (refused below)
+    p = _vector(fn, logits, "logits", (out.T, out.E), _F32, dev)
     b = score.bias
-    if b is not None and (b.numel() != out.E or not b.is_contiguous()):
-        raise ValueError(f"{fn}: the bias must hold {out.E} values, got {b.numel()}, "
-                         f"contiguous={b.is_contiguous()}")
-    if out.ids.get_device() != dev or b is not None and b.get_device() != dev:
-        raise ValueError(f"{fn}: result or bias is not on the current device cuda:{dev}")
-    return p
+    if b is not None:
+        if b.numel() != out.E or b.get_device() != dev or not b.is_contiguous():
+            raise ValueError(f"{fn}: the bias must hold {out.E} values on the current device, got "
+                             f"{b.numel()} on {b.device}, contiguous={b.is_contiguous()}")
+        score._c.bias = b.data_ptr()
+    if out._on != dev:
+        out.check(fn, dev)
+    return p, _workspace(fn, ws, dev)
 
 
 def moe_route_scored(logits: torch.Tensor, score: RouteScore, out: RouteBuffers, ws: torch.Tensor,
                      stream=None) -> None:
     """Routing of fp32 logits [T, E] into ``out`` with the choice and weights of ``score``."""
-    p = _scored("moe_route_scored", logits, score, out)
-    st = lib().moe_route_scored(p, score.packed(), out.packed(), ws.data_ptr(), ws.numel(),
-                                _stream(stream))
+    p, wp = _scored("moe_route_scored", logits, score, out, ws)
+    st = lib().moe_route_scored(p, score._addr, out.packed(), wp, ws.numel(), _stream(stream))
     if st:
         _check("moe_route_scored", st)
 
@@ -464,12 +508,15 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, W: DeviceWeights, r: RouteB
               y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """Routing then expert FFN on one stream, no host synchronisation."""
     _need("moe_layer", x, torch.bfloat16, "x")
-    _need("moe_layer", logits, torch.float32, "logits")
     _need("moe_layer", y, torch.bfloat16, "y")
     T = x.shape[0]
+    wp = _routed("moe_layer", logits, r, ws)
+    if min(x.numel(), y.numel()) < T * W.d:
+        raise ValueError(f"moe_layer: x and y must hold {T} x {W.d} values, got {tuple(x.shape)} and "
+                         f"{tuple(y.shape)}")
     wc, rc = W.cstruct(), r.cstruct()
     _check("moe_layer", lib().moe_layer(_ptr(x), _ptr(logits), T, ctypes.byref(wc), ctypes.byref(rc),
-                                        _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
+                                        _ptr(y), wp, ws.numel(), _stream(stream)))
 
 
 def moe_layer_scored(x: torch.Tensor, logits: torch.Tensor, W: DeviceWeights, score: RouteScore,
@@ -478,14 +525,19 @@ def moe_layer_scored(x: torch.Tensor, logits: torch.Tensor, W: DeviceWeights, sc
     fn = "moe_layer_scored"
     _need(fn, x, torch.bfloat16, "x")
     _need(fn, y, torch.bfloat16, "y")
-    p = _scored(fn, logits, score, r)
+    p, wp = _scored(fn, logits, score, r, ws)
     if x.shape != (r.T, W.d) or y.shape != x.shape:
         raise ValueError(f"{fn}: x and y must be [{r.T}][{W.d}], got {tuple(x.shape)} and "
                          f"{tuple(y.shape)}")
+    dev = logits.get_device()
+    if W.packed is None or W.packed.numel() < moe_q4_packed_size(W.E, W.d, W.f, W.f_s):
+        raise ValueError(f"{fn}: the weights hold no packed copy of their sizes")
+    for name, t in (("x", x), ("y", y), ("the weights", W.packed)):
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} must be on the current device cuda:{dev}, got {t.device}")
     wc, rc = W.cstruct(), r.cstruct()
-    _check(fn, lib().moe_layer_scored(_ptr(x), p, r.T, ctypes.byref(wc), score.packed(),
-                                      ctypes.byref(rc), _ptr(y), _ptr(ws), ws.numel(),
-                                      _stream(stream)))
+    _check(fn, lib().moe_layer_scored(_ptr(x), p, r.T, ctypes.byref(wc), score._addr,
+                                      ctypes.byref(rc), _ptr(y), wp, ws.numel(), _stream(stream)))
 
 
 def moe_router_topk(x: torch.Tensor, w_router: torch.Tensor, out: RouteBuffers,
@@ -708,9 +760,7 @@ def _matrix(fn, t, name, rows, columns, dtype, dev):
 
 
 def _held(fn, t, name, n) -> int:
-    """Pointer of a handle's n values (0: none), whose memory may have been exchanged."""
-    if t is None:
-        return 0
+    """Pointer of a handle's n values, whose memory may have been exchanged."""
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must hold {n} values, got {t.numel()}, "
                          f"contiguous={t.is_contiguous()}")
@@ -757,8 +807,14 @@ def moe_linear(x: torch.Tensor, linear: Linear, out: torch.Tensor, act=MOE_ACT_N
     fn = "moe_linear"
     N, K, type_, dev = linear.N, linear.K, linear._type, _device()
     wp, wr = _matrix(fn, linear.weight, "weight", N, K, type_, dev)
-    T = 0 if x is None or x.dim() != 2 else x.shape[0]
-    xp, xr = _matrix(fn, x, "x", T, K, type_, dev)
+    st = shape = None
+    if x is not None and x.dtype is type_ and x.get_device() == dev:
+        shape, st = x.shape, x.stride()
+    if st is None or len(shape) != 2 or shape[1] != K or st[1] != 1 and K != 1:
+        got = "None" if x is None else f"{x.dtype} {tuple(x.shape)} on {x.device}, strides {x.stride()}"
+        raise ValueError(f"{fn}: x must be a {type_} CUDA tensor [T][{K}] with dense elements on the "
+                         f"current device, got {got}")
+    T = shape[0]
     td = None if out is None else out.dtype
     out_dtype = _NORM_DTYPES.get(td)
     if out_dtype is None:
@@ -770,9 +826,10 @@ def moe_linear(x: torch.Tensor, linear: Linear, out: torch.Tensor, act=MOE_ACT_N
         sp = _vector(fn, x_scale, "x_scale", (T,), torch.float32, dev)
     elif x_scale is not None:
         raise ValueError(f"{fn}: x_scale goes with e4m3 inputs, got {x.dtype}")
-    a = _LINEAR.pack(xp, xr, wp, wr, sp, _held(fn, linear.scale, "scale", N),
-                     _held(fn, linear.bias, "bias", N), ap, arow, op, orow, linear.err.data_ptr(),
-                     T, N, K, linear.dtype, out_dtype, act)
+    wsp = 0 if linear.scale is None else _held(fn, linear.scale, "scale", N)
+    bp = 0 if linear.bias is None else _held(fn, linear.bias, "bias", N)
+    a = _LINEAR.pack(x.data_ptr(), st[0], wp, wr, sp, wsp, bp, ap, arow, op, orow,
+                     linear.err.data_ptr(), T, N, K, linear.dtype, out_dtype, act)
     st = lib().moe_linear(a, _stream(stream))
     if st:
         _check(fn, st)

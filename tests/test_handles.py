@@ -1,6 +1,5 @@
 """Handles of calls: parts that were checked together cannot be replaced one by one, and a call
 takes its pointers from the tensors as they are when it is made."""
-import ctypes
 import os
 
 import pytest
@@ -20,18 +19,10 @@ def L():
                                         ("factor", 2.0)])
 def test_a_score_stays_as_it_was_made(L, name, value):
     s = L.RouteScore(L.MOE_SCORE_SIGMOID, groups=4, top_groups=2, factor=1.5)
-    old, packed = getattr(s, name), s.packed()
+    old = getattr(s, name)
     with pytest.raises(AttributeError, match=f"RouteScore: {name} cannot be replaced"):
         setattr(s, name, value)
-    assert getattr(s, name) is old and s.packed() == packed
-
-
-def test_packed_score_is_the_structure(L):
-    s = L.RouteScore(L.MOE_SCORE_SIGMOID, None, 8, 4, 2, False, 2.5)
-    assert ctypes.sizeof(L.RouteScoreC) == L._SCORE.size
-    c = L.RouteScoreC.from_buffer_copy(s.packed())
-    assert (c.bias, c.score, c.groups, c.top_groups, c.group_best, c.renorm, c.factor) == \
-        (None, 1, 8, 4, 2, 0, 2.5)
+    assert getattr(s, name) is old
 
 
 def _route(L, z, score):
@@ -103,3 +94,106 @@ def test_weights_moved_under_their_tensor(L):
     with pytest.raises(ValueError, match="moe_linear: bias must hold 40"):
         L.moe_linear(x, lin, out)
     assert L.moe_get_device_error(lin) == 0
+
+
+ARRAYS = ["ids", "w", "counts", "offsets", "perm", "inv", "tiles", "n_tiles", "err"]
+
+
+@pytest.mark.parametrize("name", ARRAYS)
+def test_results_on_the_host_are_refused(L, name):
+    out = L.RouteBuffers.alloc(4, 8, 2, device="cpu")
+    out.check("f", -1)                      # (-1: what tensors on the host say of their device)
+    with pytest.raises(ValueError, match="f: ids of the result must be"):
+        out.check("f", 0)
+    setattr(out, name, None)
+    with pytest.raises(ValueError, match=f"f: {name} of the result must be"):
+        out.check("f", -1)
+
+
+@pytest.mark.parametrize("name,value", [("T", 5), ("k", 3), ("E", 9), ("block_m", 1)])
+def test_results_of_other_sizes_are_refused(L, name, value):
+    out = L.RouteBuffers.alloc(4, 8, 2, 128, device="cpu")
+    out.check("f", -1)
+    setattr(out, name, value)
+    if name == "block_m":                   # tiles of 1 row: T k + min(E, T k) = 16 entries
+        assert out.tiles.shape[0] < 16
+    with pytest.raises(ValueError, match="of the result must be"):
+        out.check("f", -1)
+
+
+def test_workspaces_that_do_not_fit_are_refused(L):
+    for ws in (None, torch.zeros(256, dtype=torch.uint8), torch.zeros(256)):
+        with pytest.raises(ValueError, match="f: the workspace must be"):
+            L._workspace("f", ws, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scored", [False, True])
+def test_routing_refuses_what_it_cannot_write(L, scored):
+    T, E, k = 40, 64, 4
+    z = torch.randn((T, E), device="cuda")
+    size = L.moe_route_workspace_size(T, E, k)
+    ws = L.alloc_workspace(size)
+    score = L.RouteScore()
+    call = (lambda o, w: L.moe_route_scored(z, score, o, w)) if scored else \
+        (lambda o, w: L.moe_route(z, o, w))
+    out = L.RouteBuffers.alloc(T, E, k)
+    call(out, ws)
+    want = out.ids.clone()
+    for w in (None, ws.cpu(), ws.float(), ws.repeat(2)[::2]):
+        with pytest.raises(ValueError, match="the workspace must be"):
+            call(out, w)
+    with pytest.raises(L.MoeError):
+        call(out, ws[:16])
+    for name in ARRAYS:
+        a = getattr(out, name)
+        for bad in (None, a.cpu(), a.short(), a.flatten()[:0], torch.stack((a, a), -1)[..., 0]):
+            setattr(out, name, bad)
+            with pytest.raises(ValueError, match=f"{name} of the result must be"):
+                call(out, ws)
+        setattr(out, name, a)
+    for name, value in (("T", T + 1), ("k", k + 1), ("E", E + 1)):
+        old = getattr(out, name)
+        setattr(out, name, value)
+        with pytest.raises(ValueError):
+            call(out, ws)
+        setattr(out, name, old)
+    out.ids.zero_()
+    call(out, ws)
+    assert torch.equal(out.ids, want) and L.moe_get_device_error(out) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scored", [False, True])
+def test_layer_refuses_what_it_cannot_read_or_write(L, scored):
+    from routing_q4_grouped_gb300 import synth
+    cfg = synth.CONFIGS["tiny"]
+    T = 16
+    W = L.DeviceWeights.from_host(synth.gen_weights(cfg))
+    x, y = (torch.zeros((T, cfg.d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    z = torch.randn((T, cfg.E), device="cuda")
+    out = L.RouteBuffers.alloc(T, cfg.E, cfg.k)
+    ws = L.alloc_workspace(L.moe_layer_workspace_size(T, cfg.E, cfg.k, cfg.d, cfg.f, cfg.f_s))
+    score = L.RouteScore()
+
+    def call(x=x, z=z, y=y, ws=ws, out=out):
+        if scored:
+            L.moe_layer_scored(x, z, W, score, out, y, ws)
+        else:
+            L.moe_layer(x, z, W, out, y, ws)
+
+    call()
+    for kw in (dict(ws=ws.cpu()), dict(ws=None), dict(y=y[:-1].contiguous()),
+               dict(x=x[:, :64].contiguous()), dict(z=z[:-1].contiguous()), dict(z=z.cpu()),
+               dict(out=L.RouteBuffers.alloc(T, cfg.E, cfg.k, device="cpu"))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    call()
+    assert L.moe_get_device_error(out) == 0
+    if scored:
+        packed = W.packed
+        for bad in (None, packed[:-256].contiguous(), packed.cpu()):
+            W.packed = bad
+            with pytest.raises(ValueError, match="weights"):
+                call()
+        W.packed = packed
