@@ -46,6 +46,7 @@ __device__ __forceinline__ uint64_t cand_word(uint32_t key, int e) {
 // Sorts v descending (bitonic network; S a power of two, fixed at compile time).
 template <int S>
 __device__ __forceinline__ void sort_desc(uint64_t (&v)[S]) {
+  static_assert((S & (S - 1)) == 0, "the network pairs places i and i ^ stride");
 #pragma unroll
   for (int size = 2; size <= S; size <<= 1)
 #pragma unroll
@@ -247,8 +248,9 @@ __device__ __forceinline__ RouteSmem route_smem(int* smem, const RouteArgs& a) {
 }
 
 // The choice of each of the block's nt tokens (experts into sE, logits into
-// sV; SCORED: the final weights into sV), then the block's counts (sCnt) and each row's stable rank among the
-// block's rows of its expert (sRank, rows in ascending (t, j) order).
+// sV; SCORED: the final weights into sV; S = 0: always the choice that ids hold), then the
+// block's counts (sCnt) and each row's stable rank among the block's rows of its expert
+// (sRank, rows in ascending (t, j) order).
 template <int S, bool SCORED>
 __device__ __forceinline__ void choose_and_rank(const RouteArgs& a, const RouteSmem& m, int t0,
                                                 int nt) {
@@ -259,7 +261,7 @@ __device__ __forceinline__ void choose_and_rank(const RouteArgs& a, const RouteS
     bool bad = false;
     select_scored<S>(a, t0, warp, kRouteWarps, nt, lane, m.sE, m.sV, bad);
     if (__any_sync(kFull, bad) && lane == 0) atomicOr(a.err, MOE_DEVERR_NONFINITE_LOGIT);
-  } else if (a.ids_given != 0) {
+  } else if (S == 0 || a.ids_given != 0) {
     // the fused router chose the experts (mode 1: with their weights in w;
     // mode 2: with their logits in w, the weights are computed later). An id
     // out of range is reported and counted as expert 0 so that the permutation
@@ -274,7 +276,7 @@ __device__ __forceinline__ void choose_and_rank(const RouteArgs& a, const RouteS
       m.sE[i] = e;
       if (a.ids_given == 2) m.sV[i] = a.w[o];
     }
-  } else {
+  } else if constexpr (S > 0) {
     // warp w takes the block's tokens w, w + 8, w + 16, ..., up to four at a
     // time with their rank loops interleaved
     bool bad = false;
@@ -604,20 +606,25 @@ static cudaError_t launch_s(RouteArgs a, cudaStream_t s) {
     return launch_pdl(route_single_kernel<S, SCORED>, dim3(1), dim3(kRouteThreads),
                       route_smem_bytes(a.E, a.k, a.tpb), s, a);
   }
+  const dim3 grid(a.nblk), block(kRouteThreads);
   cudaError_t e;
-  if (SCORED && a.T >= kChooseTokens) {
-    const int warps = kChooseThreads / 32;
-    e = launch_pdl(route_choose_kernel<S>, dim3(min((a.T + warps - 1) / warps, kChooseBlocks)),
-                   dim3(kChooseThreads), 0, s, a);
-    if (e != cudaSuccess) return e;
-    a.ids_given = 1;
-    e = launch_pdl(route_count_kernel<S, false>, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
+  if constexpr (SCORED) {
+    if (a.T >= kChooseTokens) {
+      const int warps = kChooseThreads / 32;
+      e = launch_pdl(route_choose_kernel<S>, dim3(min((a.T + warps - 1) / warps, kChooseBlocks)),
+                     dim3(kChooseThreads), 0, s, a);
+      if (e != cudaSuccess) return e;
+      a.ids_given = 1;
+      e = launch_pdl(route_count_kernel<0, false>, grid, block, smem, s, a);
+    } else {
+      e = launch_pdl(route_count_kernel<S, true>, grid, block, smem, s, a);
+      a.ids_given = 1;           // the weights are in w
+    }
   } else {
-    e = launch_pdl(route_count_kernel<S, SCORED>, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
+    e = launch_pdl(route_count_kernel<S, false>, grid, block, smem, s, a);
   }
   if (e != cudaSuccess) return e;
-  if (SCORED) a.ids_given = 1;   // the weights are in w
-  return launch_pdl(route_place_kernel, dim3(a.nblk), dim3(kRouteThreads), smem, s, a);
+  return launch_pdl(route_place_kernel, grid, block, smem, s, a);
 }
 
 template <bool SCORED>
