@@ -100,7 +100,7 @@ __device__ __forceinline__ void select_rows(const RouteArgs& a, int t0, const in
             bad = true;
             if (isnan(f)) f = -INFINITY;
           }
-          kk = float_key(f);
+          kk = float_key(f + 0.f);                 // (-0 is +0)
         }
         v[g][s] = cand_word(kk, e);
       }

@@ -3,6 +3,9 @@ them goes to the lower expert."""
 import numpy as np
 import pytest
 
+import oracle as O
+from gpu_helpers import assert_route_equal, dev, route_gpu, route_np
+from routing_q4_grouped_gb300 import moeq4
 from test_gpu_route_scored import _check
 
 pytestmark = pytest.mark.gpu
@@ -45,7 +48,28 @@ def test_zeros_in_groups(T, E, groups, top, sigmoid):
 
 def test_zeros_beside_a_number_that_is_not_finite():
     # the row goes through the whole choice in 64 bits: the same experts
-    from routing_q4_grouped_gb300 import moeq4
     z = _zeros(50, 64, 5, 0.05)
     z[:, 63] = -np.inf
     _check(z, 6, err=moeq4.MOE_DEVERR_NONFINITE_LOGIT)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 4, 1), (7, 64, 6), (100, 33, 8), (40, 256, 8), (9, 384, 5),
+                                   (5, 1000, 32), (2100, 64, 4)])
+def test_plain_routing(T, E, k):
+    for others in (0.0, 0.1, 0.5):
+        z = _zeros(T, E, T + E, others)
+        out, err, _ = route_gpu(z, k, 128)
+        assert err == 0
+        assert_route_equal(route_np(out), O.route(z, k, 128))
+
+
+def test_router_of_rows_without_signal():
+    # products of zeros: logits of either sign of zero, all equal
+    rng = np.random.default_rng(9)
+    x = O.to_bf16(np.where(rng.random((200, 128)) < 0.5, np.float32(-0.0), np.float32(0.0)))
+    w = O.to_bf16(rng.standard_normal((64, 128)).astype(np.float32))
+    out = moeq4.RouteBuffers.alloc(200, 64, 8)
+    logits = dev(np.full((200, 64), 7.0, np.float32))
+    moeq4.moe_router_topk(dev(x), dev(w), out, logits)
+    assert moeq4.moe_get_device_error(out) == 0 and (logits == 0).all()
+    assert (out.ids.cpu().numpy() == np.arange(8)).all()
