@@ -602,7 +602,7 @@ def moe_rope_phases(rot, base, scaling=MOE_ROPE_PLAIN, factor=1.0, trained=0.0, 
     return phase
 
 
-class RopeSpec:
+class RopeSpec(_Handle):
     """Rotary positions of the first ``rot`` elements of a head (moe_rope_spec); ``phase`` is
     the device copy of :func:`moe_rope_phases`."""
 
@@ -613,6 +613,7 @@ class RopeSpec:
         self.phase, self.rot, self.interleaved, self.mscale = phase, rot, interleaved, mscale
         self._c = RopeSpecC(_ptr(phase), rot, int(interleaved), mscale)
         self._addr = ctypes.addressof(self._c)
+        self._made = True
 
 
 def moe_kv_cache_size(pages, page_size, Hkv, D, bits) -> int:
@@ -620,7 +621,7 @@ def moe_kv_cache_size(pages, page_size, Hkv, D, bits) -> int:
     return lib().moe_kv_cache_size(pages, page_size, Hkv, D, bits)
 
 
-class KVCache:
+class KVCache(_Handle):
     """A paged key/value cache in 64-element groups of 8- or 4-bit codes (moe_kv_cache).
 
     ``data`` is a dense uint8 CUDA tensor of whole pages (its layout is described in
@@ -639,6 +640,7 @@ class KVCache:
         _need("KVCache", self.err, torch.int32, "err")
         self._c = KVCacheC(_ptr(data), _ptr(self.err), self.pages, page_size, Hkv, D, bits)
         self._addr = ctypes.addressof(self._c)
+        self._made = True
 
     @classmethod
     def alloc(cls, pages, page_size, Hkv, D, bits, device="cuda"):

@@ -197,3 +197,23 @@ def test_layer_refuses_what_it_cannot_read_or_write(L, scored):
             with pytest.raises(ValueError, match="weights"):
                 call()
         W.packed = packed
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["data", "err", "pages", "page_size", "Hkv", "D", "bits"])
+def test_a_cache_stays_as_it_was_made(L, name):
+    cache = L.KVCache.alloc(4, 16, 2, 64, 8)
+    old = getattr(cache, name)
+    with pytest.raises(AttributeError, match=f"KVCache: {name} cannot be replaced"):
+        setattr(cache, name, None)
+    assert getattr(cache, name) is old
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["phase", "rot", "interleaved", "mscale"])
+def test_rotary_positions_stay_as_they_were_made(L, name):
+    rope = L.RopeSpec(L.moe_rope_phases(64, 10000.0).cuda(), 64)
+    old = getattr(rope, name)
+    with pytest.raises(AttributeError, match=f"RopeSpec: {name} cannot be replaced"):
+        setattr(rope, name, None)
+    assert getattr(rope, name) is old
