@@ -203,9 +203,10 @@ typedef struct moe_route_score {
   float   factor;
 } moe_route_score;
 
-/* moe_route with another choice: the same arrays, limits, scratch and launches. Keys are
- * compared in 64-bit arithmetic, and without a bias (and with group_best 1) as the exact
- * scores, whose order is that of the logits; weights are fp32 within a few units in the
+/* moe_route with another choice: the same arrays, limits and scratch; one launch, two, or from
+ * 2048 tokens on three. Keys are compared in 64-bit arithmetic, and without a bias (and with
+ * group_best 1) as the exact scores, whose order is that of the logits (+0.0 and -0.0 are
+ * equal); weights are fp32 within a few units in the
  * last place. A NaN or -inf logit counts as the least finite number, +inf as the largest, and
  * either sets MOE_DEVERR_NONFINITE_LOGIT. */
 moe_status moe_route_scored(const float* logits, const moe_route_score* score,
@@ -361,7 +362,9 @@ moe_status moe_rms_norm(const moe_norm* a, void* stream);
 /* Dense projection of T tokens with its epilogue:
  *   y = act(x w^T + bias) + add,   e4m3: act(x_scale[t] w_scale[n] (x w^T) + bias) + add
  * fp32 accumulation on the tensor cores (for fp32 results in pieces of 1024 bytes of K, which
- * are added in fp32), everything after it in fp32, one rounding. */
+ * are added in fp32), everything after it in fp32, one rounding. Activations keep their value in
+ * a negative tail: off by 2^-16 of it next to 16-bit results, by a few units in the last place
+ * next to fp32 results, and by as much as the rounding of an exponential's argument makes. */
 #define MOE_ACT_NONE      0
 #define MOE_ACT_RELU      1
 #define MOE_ACT_SILU      2  /* y / (1 + exp(-y)) */

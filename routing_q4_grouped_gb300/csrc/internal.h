@@ -60,7 +60,8 @@ RouteWs route_ws_layout(int T, int E, int k);
 // The whole routing step: one launch for a batch that one block covers, else
 // two (choose and count, then place), each with programmatic serialization.
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
-// The same with the choice and the weights of moe_route_scored (ids_given = 0).
+// The same with the choice and the weights of moe_route_scored (ids_given = 0); large batches
+// take three launches (choose, count, place).
 cudaError_t launch_route_scored(const RouteArgs& a, cudaStream_t s);
 constexpr int kRouteMaxGroups = 32;
 

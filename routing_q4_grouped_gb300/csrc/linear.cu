@@ -22,10 +22,12 @@
 //   kPair    many tiles: two blocks on neighbouring multiprocessors multiply one tile of 256
 //            features (cta_group::2); each holds its 128 features and half of the tokens, so
 //            a chunk of 256 x 256 costs each of them 32 KB of copies instead of 48
-// Measured (bursts): 8192^3 in bf16 541 us (2.03 PFLOP/s), in e4m3 313 us (3.5); 4096 tokens
-// 2048 -> 8192 72.5 us (1.90), with bias and gelu 79; both bound by the products, the first
-// copies and the last tile's epilogue. 64 tokens 2048 -> 2048 7.5 us: a small tile's chunk takes
-// 0.13 to 0.17 us to issue and wait for, whatever its bytes.
+// Measured in bursts of 12 calls in a graph, and in a long row of calls, whose power lowers the
+// clock: 8192^3 in bf16 541 to 557 and 625 us (2.0 and 1.76 PFLOP/s), in e4m3 with a residual 301
+// to 321 and 354 us (3.5 and 3.1); 4096 tokens 2048 -> 8192 73 us (1.88) and 92, with bias and gelu
+// 78 and 92; bound by the products, the first copies and the last tile's epilogue. 64 tokens
+// 2048 -> 2048 7.5 us: by the plan's model 1.4 for the chunks (0.13 to 0.17 us each to issue and
+// wait for, whatever their bytes), 2 for the start and 3.9 for the exchange of partial sums.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -9,10 +9,12 @@
 // between its reductions (nothing is read twice): by 8, 16 or 32 lanes where it has up
 // to 64 vectors of 16 bytes, by a block of up to 512 threads where it has more. Two
 // vectors a thread: measured for 4096 rows of 2048 bf16 elements with a residual (67 MB)
-// 12.4 us, one vector 14.4, four 16.4. 40 registers for 1536 threads on a
-// multiprocessor: 8191 rows of 5120 into codes 61.5 us, with 64 registers 68.8.
-// Measured bandwidth, of a copy's 6.7 TB/s: 6.7 for 4096 fp32 rows of 4096, 6.0 for
-// 8191 bf16 rows of 5120, 4.8 into codes (two reductions, and a conversion behind them).
+// 11.9 us, one vector 13.2, four 12.6. 40 registers for 1536 threads on a
+// multiprocessor: 8191 rows of 5120 into codes 50.4 us, with 64 registers 56.4.
+// Measured bandwidth, of a copy's 6.7 TB/s: 6.7 for 4096 fp32 rows of 4096, 6.8 for
+// 8191 bf16 rows of 5120, 5.8 into codes (33 instructions an element, issue slots 73 %
+// used). 4096 rows that vectors of 16 bytes do not fit: of 2050 elements, two a load,
+// 4.0; of 2047, one a load, 2.9.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
