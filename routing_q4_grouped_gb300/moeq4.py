@@ -69,7 +69,6 @@ class RouteScoreC(ctypes.Structure):
                 ("group_best", _c_i32), ("renorm", _c_i32), ("factor", _c_f32)]
 
 
-
 class NormC(ctypes.Structure):
     _fields_ = [("x", _c_ptr), ("x_row", _c_i64), ("x_head", _c_i64),
                 ("add", _c_ptr), ("add_row", _c_i64), ("add_head", _c_i64),
@@ -447,10 +446,7 @@ def _scored(fn, logits, score, out, ws):
     p = _vector(fn, logits, "logits", (out.T, out.E), _F32, dev)
     b = score.bias
     if b is not None:
-        if b.numel() != out.E or b.get_device() != dev or not b.is_contiguous():
-            raise ValueError(f"{fn}: the bias must hold {out.E} values on the current device, got "
-                             f"{b.numel()} on {b.device}, contiguous={b.is_contiguous()}")
-        score._c.bias = b.data_ptr()
+        score._c.bias = _held(fn, b, "the bias", out.E, dev)
     if out._on != dev:
         out.check(fn, dev)
     return p, _workspace(fn, ws, dev)
@@ -761,11 +757,11 @@ def _matrix(fn, t, name, rows, columns, dtype, dev):
                      f"elements on the current device, got {got}")
 
 
-def _held(fn, t, name, n) -> int:
+def _held(fn, t, name, n, dev) -> int:
     """Pointer of a handle's n values, whose memory may have been exchanged."""
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must hold {n} values, got {t.numel()}, "
-                         f"contiguous={t.is_contiguous()}")
+    if t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must hold {n} values on the current device, got "
+                         f"{t.numel()} on {t.device}, contiguous={t.is_contiguous()}")
     return t.data_ptr()
 
 
@@ -828,8 +824,8 @@ def moe_linear(x: torch.Tensor, linear: Linear, out: torch.Tensor, act=MOE_ACT_N
         sp = _vector(fn, x_scale, "x_scale", (T,), torch.float32, dev)
     elif x_scale is not None:
         raise ValueError(f"{fn}: x_scale goes with e4m3 inputs, got {x.dtype}")
-    wsp = 0 if linear.scale is None else _held(fn, linear.scale, "scale", N)
-    bp = 0 if linear.bias is None else _held(fn, linear.bias, "bias", N)
+    wsp = 0 if linear.scale is None else _held(fn, linear.scale, "scale", N, dev)
+    bp = 0 if linear.bias is None else _held(fn, linear.bias, "bias", N, dev)
     a = _LINEAR.pack(x.data_ptr(), st[0], wp, wr, sp, wsp, bp, ap, arow, op, orow,
                      linear.err.data_ptr(), T, N, K, linear.dtype, out_dtype, act)
     st = lib().moe_linear(a, _stream(stream))

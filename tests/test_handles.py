@@ -52,6 +52,9 @@ def test_a_bias_moved_under_its_tensor(L):
     bias.data = torch.zeros(128, device="cuda")[::2]
     with pytest.raises(ValueError, match="contiguous=False"):
         _route(L, z, score)
+    bias.data = torch.zeros(64)
+    with pytest.raises(ValueError, match="on cpu"):
+        _route(L, z, score)
 
 
 @pytest.mark.gpu
@@ -92,6 +95,12 @@ def test_weights_moved_under_their_tensor(L):
     w.data = rnd(40, 64).bfloat16()
     bias.data = rnd(39)
     with pytest.raises(ValueError, match="moe_linear: bias must hold 40"):
+        L.moe_linear(x, lin, out)
+    bias.data = torch.zeros(40)
+    with pytest.raises(ValueError, match="moe_linear: bias must hold 40 .* on cpu"):
+        L.moe_linear(x, lin, out)
+    w.data = torch.zeros((40, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="moe_linear: weight must be .* on cpu"):
         L.moe_linear(x, lin, out)
     assert L.moe_get_device_error(lin) == 0
 
