@@ -350,6 +350,8 @@ class RouteBuffers:
                 ("tiles", 3 * moe_route_max_tiles(self.T, self.E, self.k, self.block_m), t),
                 ("n_tiles", 1, t), ("err", 1, t)):
             a = getattr(self, name)
+            if a is None and least == 0:   # no tokens: ids, w, perm and inv may be missing
+                continue
             if a is None or a.dtype is not dtype or a.get_device() != dev or a.numel() < least or \
                     not a.is_contiguous():
                 got = "None" if a is None else f"{a.dtype} {tuple(a.shape)} on {a.device}"
@@ -359,6 +361,8 @@ class RouteBuffers:
 
     def packed(self) -> bytes:
         """cstruct as packed bytes: a fraction of the time that filling it takes."""
+        if self.T == 0:
+            return bytes(self.cstruct())
         return _ROUTE.pack(self.ids.data_ptr(), self.w.data_ptr(), self.counts.data_ptr(),
                            self.offsets.data_ptr(), self.perm.data_ptr(), self.inv.data_ptr(),
                            self.tiles.data_ptr(), self.n_tiles.data_ptr(), self.err.data_ptr(),

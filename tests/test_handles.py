@@ -226,3 +226,29 @@ def test_rotary_positions_stay_as_they_were_made(L, name):
     with pytest.raises(AttributeError, match=f"RopeSpec: {name} cannot be replaced"):
         setattr(rope, name, None)
     assert getattr(rope, name) is old
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scored", [False, True])
+def test_no_tokens_need_no_arrays(L, scored):
+    out = L.RouteBuffers.alloc(0, 16, 2)
+    ws = L.alloc_workspace(L.moe_route_workspace_size(0, 16, 2))
+    z = torch.empty((0, 16), device="cuda")
+    for name in ("ids", "w", "perm", "inv"):
+        setattr(out, name, None)
+    out.counts.fill_(5)
+    if scored:
+        L.moe_route_scored(z, L.RouteScore(), out, ws)
+    else:
+        L.moe_route(z, out, ws)
+    assert L.moe_get_device_error(out) == 0
+    assert (out.counts == 0).all() and (out.offsets == 0).all() and out.n_tiles[0] == 0
+    out.counts = None
+    with pytest.raises(ValueError, match="counts of the result must be"):
+        L.moe_route(z, out, ws)
+
+
+def test_packed_result_is_the_structure(L):
+    for T in (0, 4):
+        out = L.RouteBuffers.alloc(T, 8, 2, device="cpu")
+        assert out.packed() == bytes(out.cstruct())
