@@ -355,7 +355,7 @@ __device__ __forceinline__ void block_weights(const RouteArgs& a, const RouteSme
 // clamped, and every write is range-checked.
 __device__ __forceinline__ void place_rows(const RouteArgs& a, const RouteSmem& m, int b, int t0,
                                            int nt) {
-  __shared__ uint32_t s_ws[2][kRouteWarps];
+  __shared__ uint32_t s_ws[2][kRouteWarps];    // (kRouteSmemFixed)
   const int tid = threadIdx.x;
   const int E = a.E, k = a.k;
   const uint32_t n = static_cast<uint32_t>(a.T) * static_cast<uint32_t>(k);
@@ -583,6 +583,10 @@ RouteWs route_ws_layout(int T, int E, int k) {
   return w;
 }
 
+// Shared memory of a block: 48 KB at most, of which place_rows holds some outside the dynamic part.
+constexpr size_t kRouteSmemFixed = 2 * kRouteWarps * sizeof(uint32_t);
+constexpr size_t kRouteSmemMax = 48 * 1024 - kRouteSmemFixed;
+
 static size_t route_smem_bytes(int E, int k, int tpb) {
   return sizeof(int) * route_smem_words(E, k, tpb);
 }
@@ -594,11 +598,11 @@ static cudaError_t launch_s(RouteArgs a, cudaStream_t s) {
   // blocks spread the selection and the fp64 weights over more multiprocessors).
   int tpb = kRouteTokensMin;
   while (a.T > tpb * kRouteBlocksTarget) tpb += kRouteTokensMin;
-  // at most 48 KB of shared memory per block: larger batches take more blocks
-  while (tpb > kRouteTokensMin && route_smem_bytes(a.E, a.k, tpb) > 48 * 1024)
+  // larger batches take more blocks
+  while (tpb > kRouteTokensMin && route_smem_bytes(a.E, a.k, tpb) > kRouteSmemMax)
     tpb -= kRouteTokensMin;
   const size_t smem = route_smem_bytes(a.E, a.k, tpb);
-  if (smem > 48 * 1024) return cudaErrorInvalidValue;
+  if (smem > kRouteSmemMax) return cudaErrorInvalidValue;
   a.tpb = tpb;
   a.nblk = a.T > 0 ? (a.T + tpb - 1) / tpb : 1;
   if (a.nblk == 1) {
