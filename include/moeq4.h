@@ -206,7 +206,8 @@ typedef struct moe_route_score {
 /* moe_route with another choice: the same arrays, limits and scratch; one launch, two, or from
  * 2048 tokens on three. Keys are compared in 64-bit arithmetic, and without a bias (and with
  * group_best 1) as the exact scores, whose order is that of the logits (+0.0 and -0.0 are
- * equal); weights are fp32 within a few units in the
+ * equal). Sums that are equal on paper may differ there by a rounding (s(x) + s(-x) of two
+ * groups, say), and then go by it. Weights are fp32 within a few units in the
  * last place. A NaN or -inf logit counts as the least finite number, +inf as the largest, and
  * either sets MOE_DEVERR_NONFINITE_LOGIT. */
 moe_status moe_route_scored(const float* logits, const moe_route_score* score,
